@@ -17,6 +17,10 @@ and the steps around them: tensor_sf / grouped_tensor_sf (the NVFP4 tensor
 scales on the GPU), quantize_dynamic (tensor_sf read from device memory),
 grouped_quantize_dynamic (per-expert scales on the GPU, then the grouped
 quantize), gemm_quantize (a matmul with the quantize in its epilogue).
+
+Serving a decoder layer from block-scaled storage (serving.py): kv_append and
+kv_attention (an 8-bit paged key/value cache), moe_layer (a
+mixture-of-experts layer for a few tokens over packed weights).
 """
 from __future__ import annotations
 
@@ -31,7 +35,8 @@ __all__ = ["FORMATS", "GROUPED_KERNELS", "lib", "BsqError", "block_size", "packe
            "scales5d_bytes", "quantize", "quantize_dynamic", "tensor_sf", "grouped_tensor_sf",
            "grouped_quantize_dynamic",
            "grouped_quantize", "grouped_quantize_workspace_bytes", "scales_interleave", "block_scaled_dot", "gemm_quantize", "device_error",
-           "status_string"]
+           "status_string", "kv_append", "kv_attention", "kv_attention_workspace_bytes", "moe_layer",
+           "moe_layer_workspace_bytes"]
 
 FORMATS = {"nvfp4": 0, "mxfp4": 1, "mxfp8": 2}
 GROUPED_KERNELS = {"auto": 0, "stream": 1, "latency": 2, "token": 3}
@@ -70,6 +75,18 @@ _SIGNATURES = {
                                       _c_i64, _c_i64, _c_i64, _c_p, _c_p]),
     "bsq_gemm_quantize": (_c_i32, [_c_i32, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_f32,
                                    _c_p, _c_p, _c_p, _c_p]),
+}
+
+_SIGNATURES |= {
+    "bsq_kv_append": (_c_i32, [_c_i32, _c_p, _c_p, _c_i64, _c_i32, _c_i32, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64,
+                               _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i32, _c_p, _c_p, _c_i32, _c_p]),
+    "bsq_kv_attention_workspace_bytes": (_c_i64, [_c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32]),
+    "bsq_kv_attention": (_c_i32, [_c_i32, _c_p, _c_i64, _c_i32, _c_i32, _c_i32, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p,
+                                  _c_i64, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i32, _c_p, _c_p, _c_i32,
+                                  _c_i32, _c_f32, _c_i32, _c_i32, _c_p, _c_p, _c_p, _c_i64, _c_p]),
+    "bsq_moe_layer_workspace_bytes": (_c_i64, [_c_i32, _c_i32, _c_i64, _c_i64, _c_i32, _c_i32]),
+    "bsq_moe_layer": (_c_i32, [_c_i32, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
+                               _c_i64, _c_i32, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_p, _c_i64, _c_p]),
 }
 
 _lib = None
@@ -371,3 +388,7 @@ def device_error(device=None, stream=None) -> int:
         rc = lib().bsq_device_error(_stream(device, stream), ctypes.byref(code))
     _check(rc, "bsq_device_error")
     return code.value
+
+
+from .serving import (kv_append, kv_attention, kv_attention_workspace_bytes, moe_layer,  # noqa: E402
+                      moe_layer_workspace_bytes)

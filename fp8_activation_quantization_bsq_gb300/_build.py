@@ -12,8 +12,9 @@ INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_DIR = os.path.join(PKG_DIR, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libbsq.so")
 
-SOURCES = ["bsq.cu"]
-HEADERS = ["device_common.cuh", "box_quant.cuh", "dense_quant.cuh", "grouped_quant.cuh", "interleave.cuh",
+SOURCES = ["bsq.cu", "kv_cache.cu", "moe.cu"]
+HEADERS = ["host_common.h", "serving_common.cuh", "kv_append.cuh", "kv_attention.cuh", "moe_layer.cuh",
+           "device_common.cuh", "box_quant.cuh", "dense_quant.cuh", "grouped_quant.cuh", "interleave.cuh",
            "tensor_scale.cuh", "block_scaled_dot.cuh", "cluster.cuh", "gemm_quant.cuh", "grouped_token.cuh"]
 
 
@@ -42,16 +43,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc_path(), "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo",
-           "-std=c++17", "-Werror", "all-warnings", "-shared", "-cudart", "shared", "-Xcompiler", "-fPIC,-fvisibility=hidden",
-           "-Xlinker", "-rpath,/usr/local/cuda/lib64", "-I", INCLUDE, "-o", tmp]
-    cmd += [os.path.join(CSRC, s) for s in SOURCES]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if verbose or res.returncode != 0:
-        print(" ".join(cmd))
-        print(res.stdout + res.stderr)
-    if res.returncode != 0:
-        raise RuntimeError("libbsq build failed:\n" + res.stderr[-4000:])
+    base = [nvcc_path(), "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo",
+            "-std=c++17", "-Werror", "all-warnings", "-cudart", "shared", "-Xcompiler", "-fPIC,-fvisibility=hidden",
+            "-I", INCLUDE]
+    # one compiler process per translation unit, all at once, then the link
+    objects = [os.path.join(LIB_DIR, s + ".o") for s in SOURCES]
+    jobs = [base + ["-c", "-o", o, os.path.join(CSRC, s)] for s, o in zip(SOURCES, objects)]
+    running = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in jobs]
+    results = [(c, p.communicate()[0], p.returncode) for c, p in zip(jobs, running)]
+    if all(rc == 0 for _, _, rc in results):
+        link = base + ["-shared", "-Xlinker", "-rpath,/usr/local/cuda/lib64", "-o", tmp] + objects
+        res = subprocess.run(link, capture_output=True, text=True)
+        results.append((link, res.stdout + res.stderr, res.returncode))
+    for cmd, text, rc in results:
+        if verbose or rc != 0:
+            print(" ".join(cmd))
+            print(text)
+    failed = [text for _, text, rc in results if rc != 0]
+    if failed:
+        raise RuntimeError("libbsq build failed:\n" + "\n".join(failed)[-4000:])
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

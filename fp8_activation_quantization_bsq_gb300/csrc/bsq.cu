@@ -18,6 +18,7 @@
 #include "device_common.cuh"
 #include "grouped_quant.cuh"
 #include "grouped_token.cuh"
+#include "host_common.h"
 #include "interleave.cuh"
 #include "tensor_scale.cuh"
 
@@ -49,7 +50,9 @@ constexpr int kRowsPerWarp = 2;
 
 struct DeviceInfo {
   bool ready = false;
+  int index = 0;
   int sm_count = 0;
+  unsigned int* error_word = nullptr;  // device address of g_error_word
   int dense_ctas_per_sm[3] = {0, 0, 0};
   int tq_max_smem = 0;  // dynamic shared memory the token kernel may use
 };
@@ -58,32 +61,6 @@ std::mutex g_mu;
 DeviceInfo g_devices[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode_tiled = nullptr;
 bool g_encode_tried = false;
-
-inline bool fmt_ok(int32_t f) { return f == BSQ_NVFP4 || f == BSQ_MXFP4 || f == BSQ_MXFP8; }
-inline int sf_of(int32_t f) { return f == BSQ_NVFP4 ? 16 : 32; }
-inline int atom_cols_of(int32_t f) { return 4 * sf_of(f); }
-inline int64_t row_bytes_of(int32_t f, int64_t K) { return f == BSQ_MXFP8 ? K : K / 2; }
-inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Launch with programmatic stream serialization (programmatic dependent
-// launch): the kernel may start while the previous kernel in the stream
-// finishes; each kernel waits (griddepcontrol.wait) before touching memory.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                       cudaStream_t stream, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
 
 template <int FMT>
 void dense_kernel_setup(int fidx, DeviceInfo& d) {
@@ -104,6 +81,10 @@ bsq_status device_info(DeviceInfo** out) {
   if (!d.ready) {
     if (cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return BSQ_ERR_CUDA;
+    void* word = nullptr;
+    if (cudaGetSymbolAddress(&word, g_error_word) != cudaSuccess) return BSQ_ERR_CUDA;
+    d.index = dev;
+    d.error_word = static_cast<unsigned int*>(word);
     dense_kernel_setup<kNVFP4>(0, d);
     dense_kernel_setup<kMXFP4>(1, d);
     dense_kernel_setup<kMXFP8>(2, d);
@@ -123,6 +104,10 @@ bsq_status device_info(DeviceInfo** out) {
   return BSQ_OK;
 }
 
+}  // namespace
+
+namespace bsq {
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
   std::lock_guard<std::mutex> lock(g_mu);
   if (!g_encode_tried) {
@@ -136,6 +121,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
   }
   return g_encode_tiled;
 }
+
+bsq_status host_device(HostDevice* out) {
+  DeviceInfo* d = nullptr;
+  if (bsq_status s = device_info(&d); s != BSQ_OK) return s;
+  *out = HostDevice{d->index, d->sm_count, d->error_word};
+  return BSQ_OK;
+}
+
+}  // namespace bsq
+
+namespace {
 
 template <int FMT>
 bsq_status launch_dense(const void* in, int64_t M, int64_t K, int64_t ld_in, void* out,

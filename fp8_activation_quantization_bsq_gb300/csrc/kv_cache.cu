@@ -1,0 +1,162 @@
+// Host side of the 8-bit paged key/value cache: argument checks and launch
+// geometry of bsq_kv_append and bsq_kv_attention (include/bsq.h).
+#include <algorithm>
+#include <cmath>
+
+#include "host_common.h"
+#include "kv_append.cuh"
+#include "kv_attention.cuh"
+
+namespace {
+
+using namespace bsq;
+
+// What the cache calls check alike; BSQ_OK when the call may go on.
+bsq_status check_cache(int32_t dtype, int64_t total, int32_t kv_heads, int32_t dim, int64_t tok_stride, int64_t head_stride,
+                       const void* k_cache, const void* v_cache, const void* k_scales, const void* v_scales,
+                       int64_t num_pages, int32_t page, int64_t cs_page, int64_t cs_head, int64_t cs_tok,
+                       const int32_t* table, int64_t table_ld, int32_t table_width, const int32_t* offsets,
+                       const int32_t* lens, int32_t batch) {
+  if (dtype != BSQ_BF16 && dtype != BSQ_F16) return BSQ_ERR_VALUE;
+  if (total < 0 || total >= (int64_t(1) << 31) || batch < 0 || kv_heads < 1 || kv_heads > 1024 || (dim != 64 && dim != 128) ||
+      num_pages < 0 || num_pages >= (int64_t(1) << 31) || (page != 16 && page != 32 && page != 64 && page != 128) ||
+      table_width < 0 || (batch > 1 && table_ld < table_width) || cs_tok < dim || cs_page < 0 || cs_head < 0)
+    return BSQ_ERR_SHAPE;
+  if (total == 0 || batch == 0) return BSQ_OK;
+  if (!table || !offsets || !lens || (num_pages > 0 && (!k_cache || !v_cache || !k_scales || !v_scales))) return BSQ_ERR_NULL;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || cs_page % 16 != 0 || cs_head % 16 != 0 || cs_tok % 16 != 0 ||
+      tok_stride % 8 != 0 || head_stride % 8 != 0 || !aligned(table, 4) || !aligned(offsets, 4) || !aligned(lens, 4))
+    return BSQ_ERR_ALIGN;
+  return BSQ_OK;
+}
+
+template <int D, bool F16>
+cudaError_t launch_append(const KvAppendArgs& a, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(a.total / a.page + 2 * static_cast<int64_t>(a.batch)), 2u * a.kv_heads);
+  switch (a.page * (D / 8) / kKvAppendThreads) {
+    case 1: return launch_pdl(kv_append_kernel<D, 1, F16>, grid, dim3(kKvAppendThreads), 0, st, a);
+    case 2: return launch_pdl(kv_append_kernel<D, 2, F16>, grid, dim3(kKvAppendThreads), 0, st, a);
+    case 4: return launch_pdl(kv_append_kernel<D, 4, F16>, grid, dim3(kKvAppendThreads), 0, st, a);
+    case 8: return launch_pdl(kv_append_kernel<D, 8, F16>, grid, dim3(kKvAppendThreads), 0, st, a);
+    default: return launch_pdl(kv_append_kernel<D, 16, F16>, grid, dim3(kKvAppendThreads), 0, st, a);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t bsq_kv_append(int32_t dtype, const void* k, const void* v, int64_t total, int32_t kv_heads, int32_t dim,
+                      int64_t src_tok, int64_t src_head, void* k_cache, void* v_cache, void* k_scales, void* v_scales,
+                      int64_t num_pages, int32_t page, int64_t cs_page, int64_t cs_head, int64_t cs_tok,
+                      const int32_t* table, int64_t table_ld, int32_t table_width, const int32_t* offsets,
+                      const int32_t* lens, int32_t batch, void* stream) {
+  if (bsq_status s = check_cache(dtype, total, kv_heads, dim, src_tok, src_head, k_cache, v_cache, k_scales, v_scales,
+                                 num_pages, page, cs_page, cs_head, cs_tok, table, table_ld, table_width, offsets, lens, batch);
+      s != BSQ_OK)
+    return s;
+  if (total == 0 || batch == 0) return BSQ_OK;
+  if (!k || !v) return BSQ_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16)) return BSQ_ERR_ALIGN;
+  HostDevice d;
+  if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
+  KvAppendArgs a{};
+  a.src[0] = static_cast<const uint16_t*>(k);
+  a.src[1] = static_cast<const uint16_t*>(v);
+  a.src_tok = src_tok;
+  a.src_head = src_head;
+  a.cache[0] = static_cast<uint8_t*>(k_cache);
+  a.cache[1] = static_cast<uint8_t*>(v_cache);
+  a.cs_page = cs_page;
+  a.cs_head = cs_head;
+  a.cs_tok = cs_tok;
+  a.scales[0] = static_cast<uint8_t*>(k_scales);
+  a.scales[1] = static_cast<uint8_t*>(v_scales);
+  a.table = table;
+  a.table_ld = table_ld;
+  a.offsets = offsets;
+  a.lens = lens;
+  a.total = total;
+  a.num_pages = num_pages;
+  a.batch = batch;
+  a.kv_heads = kv_heads;
+  a.page = page;
+  a.table_width = table_width;
+  a.err = d.error_word;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dim == 64)
+    e = dtype == BSQ_F16 ? launch_append<64, true>(a, st) : launch_append<64, false>(a, st);
+  else
+    e = dtype == BSQ_F16 ? launch_append<128, true>(a, st) : launch_append<128, false>(a, st);
+  return e == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
+}
+
+int64_t bsq_kv_attention_workspace_bytes(int64_t total, int32_t heads, int32_t kv_heads, int32_t dim, int32_t batch,
+                                         int32_t max_q) {
+  if (total < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || (dim != 64 && dim != 128) || batch < 0 || max_q < 0)
+    return 0;
+  return 16;
+}
+
+int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t heads, int32_t kv_heads, int32_t dim,
+                         int64_t q_tok, int64_t q_head, const void* k_cache, const void* v_cache, const void* k_scales,
+                         const void* v_scales, int64_t num_pages, int32_t page, int64_t cs_page, int64_t cs_head,
+                         int64_t cs_tok, const int32_t* table, int64_t table_ld, int32_t table_width,
+                         const int32_t* offsets, const int32_t* lens, int32_t batch, int32_t max_q, float sm_scale,
+                         int32_t causal, int32_t window, void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                         void* stream) {
+  if (bsq_status s = check_cache(dtype, total, kv_heads, dim, q_tok, q_head, k_cache, v_cache, k_scales, v_scales, num_pages,
+                                 page, cs_page, cs_head, cs_tok, table, table_ld, table_width, offsets, lens, batch);
+      s != BSQ_OK)
+    return s;
+  if (heads < 1 || heads % kv_heads != 0 || heads / kv_heads > 64 || window < 0 || max_q < 0) return BSQ_ERR_SHAPE;
+  if (!std::isfinite(sm_scale)) return BSQ_ERR_VALUE;
+  if (total == 0 || batch == 0) return BSQ_OK;
+  if (max_q < 1) return BSQ_ERR_SHAPE;
+  if (!q || !out || !workspace) return BSQ_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16)) return BSQ_ERR_ALIGN;
+  if (workspace_bytes < bsq_kv_attention_workspace_bytes(total, heads, kv_heads, dim, batch, max_q)) return BSQ_ERR_SHAPE;
+  HostDevice d;
+  if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
+  KvAttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_tok = q_tok;
+  a.q_head = q_head;
+  a.cache[0] = static_cast<const uint8_t*>(k_cache);
+  a.cache[1] = static_cast<const uint8_t*>(v_cache);
+  a.cs_page = cs_page;
+  a.cs_head = cs_head;
+  a.cs_tok = cs_tok;
+  a.scales[0] = static_cast<const uint8_t*>(k_scales);
+  a.scales[1] = static_cast<const uint8_t*>(v_scales);
+  a.table = table;
+  a.table_ld = table_ld;
+  a.offsets = offsets;
+  a.lens = lens;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.total = total;
+  a.num_pages = num_pages;
+  a.batch = batch;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.page = page;
+  a.table_width = table_width;
+  a.causal = causal;
+  a.window = window;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.err = d.error_word;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dim3 grid(static_cast<unsigned>(ceil_div(total * heads, 4)));
+  cudaError_t e;
+  if (dim == 64)
+    e = dtype == BSQ_F16 ? launch_pdl(kv_attention_kernel<64, true>, grid, dim3(128), 0, st, a)
+                         : launch_pdl(kv_attention_kernel<64, false>, grid, dim3(128), 0, st, a);
+  else
+    e = dtype == BSQ_F16 ? launch_pdl(kv_attention_kernel<128, true>, grid, dim3(128), 0, st, a)
+                         : launch_pdl(kv_attention_kernel<128, false>, grid, dim3(128), 0, st, a);
+  return e == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -408,6 +408,131 @@ BSQ_API int32_t bsq_gemm_quantize(int32_t fmt, const void* a_dev, const void* b_
                                   int64_t K, int64_t lda, int64_t ldb, float tensor_sf, void* out_dev,
                                   void* scales5d_dev, void* c_bf16_dev, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Serving a decoder layer from block-scaled storage: an 8-bit paged
+ * key/value cache (append, attention) and a mixture-of-experts layer for a
+ * few tokens over packed weights.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { BSQ_BF16 = 0, BSQ_F16 = 1 } bsq_dtype;
+
+/*
+ * The cache.  Keys and values are held in pages of `page` tokens (16, 32, 64
+ * or 128) of each kv head: E4M3 codes, and one E8M0 scale byte e + 127 per
+ * (page, kv head); a code c stands for c * 2^e.  The code of page p, kv head
+ * h, token t of the page and dimension d lies at
+ * p*page_stride + h*head_stride + t*token_stride + d (bytes); scales are
+ * (num_pages, kv_heads), contiguous.  Keys and values have equal strides.
+ * Sequence b's token i lies in page block_table[b*table_stride + i/page].
+ *
+ * Arguments common to the cache calls:
+ *   dtype             bsq_dtype of the 16-bit tensors.
+ *   dim               head dimension, 64 or 128.
+ *   k_cache_dev, v_cache_dev   codes, 16-byte aligned; page_stride,
+ *                     head_stride and token_stride are multiples of 16,
+ *                     token_stride >= dim.
+ *   block_table_dev   int32, `batch` rows of table_width entries.
+ *   offsets_dev       int32[batch + 1], non-decreasing from 0: sequence b owns the
+ *                     rows [offsets[b], offsets[b+1]) of the 16-bit tensors.
+ *   seq_lens_dev      int32[batch]: cached tokens of the sequence, the rows
+ *                     of this call among them as its last ones.
+ * Device checks (error word BSQ_ERR_VALUE; what is affected is skipped): a
+ * page id outside [0, num_pages) where one is needed, a sequence longer than
+ * table_width pages, offsets outside the tensor, a length below the
+ * sequence's rows (append only: an attention row at a negative position has
+ * no allowed key).
+ */
+
+/*
+ * Write new keys and values into the cache.
+ *   k_dev, v_dev      (total, kv_heads, dim) with strides src_token_stride and
+ *                     src_head_stride in elements (multiples of 8), 16-byte aligned.
+ * Per page and kv head that new tokens reach, amax over its new tokens:
+ *   e = ceil(log2(fl32(amax / 448))), at least -32 (-32 for zeros); where the
+ *   page also holds earlier tokens, the larger of that and its present e,
+ *   and if that raises e the earlier codes c become E4M3(c * 2^(e_old - e)).
+ *   New codes are E4M3(x * 2^-e), nearest even, saturating.
+ * No two sequences may share a page that is written.  NaN or Inf inputs are
+ * outside the contract.
+ */
+BSQ_API int32_t bsq_kv_append(int32_t dtype, const void* k_dev, const void* v_dev, int64_t total, int32_t kv_heads,
+                              int32_t dim, int64_t src_token_stride, int64_t src_head_stride, void* k_cache_dev,
+                              void* v_cache_dev, void* k_scales_dev, void* v_scales_dev, int64_t num_pages, int32_t page,
+                              int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                              const int32_t* block_table_dev, int64_t table_stride, int32_t table_width,
+                              const int32_t* offsets_dev, const int32_t* seq_lens_dev, int32_t batch, void* stream);
+
+/*
+ * Attention of query rows over their sequences' cached keys and values.
+ *   q_dev             (total, heads, dim), strides in elements (multiples of
+ *                     8), 16-byte aligned; heads is a multiple of kv_heads, query head h
+ *                     reads kv head h / (heads / kv_heads); at most 64 query heads per kv head.
+ *   max_q             the most rows that any sequence has (1 for single tokens).
+ *   sm_scale          factor of the scores.
+ *   causal            row i of n rows of a sequence of length L sits at position
+ *                     L - n + i and sees keys at or before it (0: all L keys).
+ *   window            > 0: only keys less than `window` positions before the row; 0: all.
+ *   out_dev           (total, heads, dim) contiguous, of q's type.
+ *   lse_dev           NULL, or float (total, heads): natural logarithm of the sum
+ *                     of exp(score) over the allowed keys.
+ *   workspace_dev     bsq_kv_attention_workspace_bytes() bytes, 16-byte
+ *                     aligned, zeroed by the caller once before its first use; every call
+ *                     leaves its counters zeroed again.  Calls sharing it must not overlap.
+ * A row without an allowed key gets zeros and -inf.  What the cache holds
+ * beyond a sequence's length, or outside the allowed keys, does not matter.
+ * Rows of q that belong to no sequence are left as they are.  A softmax
+ * weight enters its product with the values as FP16; scores, sums and
+ * accumulators are FP32.
+ */
+BSQ_API int64_t bsq_kv_attention_workspace_bytes(int64_t total, int32_t heads, int32_t kv_heads, int32_t dim, int32_t batch,
+                                                 int32_t max_q);
+BSQ_API int32_t bsq_kv_attention(int32_t dtype, const void* q_dev, int64_t total, int32_t heads, int32_t kv_heads,
+                                 int32_t dim, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache_dev,
+                                 const void* v_cache_dev, const void* k_scales_dev, const void* v_scales_dev,
+                                 int64_t num_pages, int32_t page, int64_t page_stride, int64_t head_stride,
+                                 int64_t token_stride, const int32_t* block_table_dev, int64_t table_stride,
+                                 int32_t table_width, const int32_t* offsets_dev, const int32_t* seq_lens_dev, int32_t batch,
+                                 int32_t max_q, float sm_scale, int32_t causal, int32_t window, void* out_dev,
+                                 float* lse_dev, void* workspace_dev, int64_t workspace_bytes, void* stream);
+
+/*
+ * A mixture-of-experts layer for a few tokens.
+ *   fmt               bsq_format of the weights and of the quantized activations.
+ *   x_dev             BF16 (tokens, hidden), row stride ld_x (>= hidden, % 8 == 0), 16-byte aligned.
+ *   logits_dev        float (tokens, experts), row stride ld_logits: router logits.
+ *   w13_dev           packed (experts, 2*inter, hidden): rows [0, inter) the
+ *                     gate, [inter, 2*inter) the up projection; w13_scales_dev: per expert
+ *                     bsq_scales5d_bytes(fmt, 2*inter, hidden) bytes.
+ *   w2_dev            packed (experts, hidden, inter); w2_scales_dev: per
+ *                     expert bsq_scales5d_bytes(fmt, hidden, inter) bytes.
+ *   x_sf_dev, w13_sf_dev, h_sf_dev, w2_sf_dev   NVFP4: float[experts] tensor
+ *                     scales (> 0) of the layer's input, the weights and the inner
+ *                     activation; NULL for MX.
+ *   y_dev             BF16 (tokens, hidden), row stride ld_y (% 8 == 0), 16-byte aligned.
+ *   tokens            0 <= tokens <= 64 (0 = no-op); hidden % 32 == 0; inter % 128 == 0;
+ *                     1 <= top_k <= min(16, experts); experts <= 1024.
+ * Per token: the top_k largest logits (equal ones: the lowest expert first),
+ * weights p = their softmax over all experts, divided by their sum where
+ * renormalize != 0.  For each chosen expert e, with Q the quantization of
+ * bsq_quantize under the given tensor scale:
+ *   g, u = Q(x, x_sf[e]) . w13[e];  h = bf16(g / (1 + exp(-g)) * u);
+ *   y = bf16(sum over the choices of p * (Q(h, h_sf[e]) . w2[e])).
+ * Logits of -inf exclude an expert (its weight is 0); a row of nothing else
+ * gives zeros.  NaN logits count as -inf and record BSQ_ERR_VALUE.
+ *   workspace_dev     bsq_moe_layer_workspace_bytes() bytes, 1024-byte aligned,
+ *                     zeroed by the caller once before its first use; every call leaves
+ *                     its counters zeroed again (after a reported BSQ_ERR_TIMEOUT it has
+ *                     to be zeroed anew).  Calls sharing it must not overlap.
+ */
+BSQ_API int64_t bsq_moe_layer_workspace_bytes(int32_t fmt, int32_t tokens, int64_t hidden, int64_t inter, int32_t experts,
+                                              int32_t top_k);
+BSQ_API int32_t bsq_moe_layer(int32_t fmt, const void* x_dev, int64_t ld_x, const float* logits_dev, int64_t ld_logits,
+                              const void* w13_dev, const void* w13_scales_dev, const void* w2_dev,
+                              const void* w2_scales_dev, const float* x_sf_dev, const float* w13_sf_dev,
+                              const float* h_sf_dev, const float* w2_sf_dev, void* y_dev, int64_t ld_y, int32_t tokens,
+                              int64_t hidden, int64_t inter, int32_t experts, int32_t top_k, int32_t renormalize,
+                              void* workspace_dev, int64_t workspace_bytes, void* stream);
+
 /*
  * Self-test of the device-side failure path: enqueues a one-warp kernel that
  * waits, with the bounded wait every pipelined kernel here uses, on a
