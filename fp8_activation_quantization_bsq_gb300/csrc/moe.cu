@@ -1,5 +1,7 @@
-// Host side of the few-token mixture-of-experts layer (bsq_moe_layer).
+// Host side of the few-token mixture-of-experts layer (bsq_moe_layer):
+// argument checks, the workspace's layout, tensor maps and the cooperative launch.
 #include <algorithm>
+#include <mutex>
 
 #include "host_common.h"
 #include "moe_layer.cuh"
@@ -11,18 +13,100 @@ using namespace bsq;
 bool moe_sizes_ok(int32_t tokens, int64_t hidden, int64_t inter, int32_t experts, int32_t top_k) {
   return tokens >= 0 && tokens <= kMoeMaxTokens && hidden >= 32 && hidden % 32 == 0 && hidden <= (1 << 20) && inter >= 128 &&
          inter % 128 == 0 && inter <= (1 << 20) && experts >= 1 && experts <= kMoeMaxExperts && top_k >= 1 &&
-         top_k <= kMoeMaxTopK && top_k <= experts;
+         top_k <= kMoeMaxTopK && top_k <= experts && experts * std::max(2 * inter, hidden) < (int64_t(1) << 31);
+}
+
+// The workspace: counters (at the same place for all sizes), then the
+// tokens' operands and scales of both products, parts of split tiles, and
+// each choice's rows of y.
+struct MoeWorkspace {
+  int64_t xq, xq_s, hq, hq_s, part, yp, bytes;
+};
+MoeWorkspace moe_workspace(int32_t fmt, int32_t tokens, int64_t hidden, int64_t inter, int32_t experts, int32_t top_k) {
+  const int64_t pairs = static_cast<int64_t>(tokens) * top_k, active = std::min<int64_t>(experts, pairs);
+  const int64_t max_n = ceil_div(tokens, 16) * 16;
+  MoeWorkspace w;
+  int64_t at = kMoeCounterBytes;
+  auto take = [&at](int64_t bytes) {
+    const int64_t p = at;
+    at = ceil_div(at + bytes, 256) * 256;
+    return p;
+  };
+  w.xq = take(pairs * row_bytes_of(fmt, hidden));
+  w.xq_s = take(active * bsq_scales5d_bytes(fmt, 128, hidden));
+  w.hq = take(pairs * row_bytes_of(fmt, inter));
+  w.hq_s = take(active * bsq_scales5d_bytes(fmt, 128, inter));
+  w.part = take(int64_t(kMoeMaxBlocks) * 4 * 2 * max_n * 128 * 4);
+  w.yp = take(pairs * hidden * 4);
+  w.bytes = at;
+  return w;
+}
+
+// Rows of `row_bytes` bytes in boxes of 128 bytes x `box_rows` rows with the
+// 128-byte swizzle; what lies past the edges reads as zeros.
+bool moe_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t row_bytes, uint32_t box_rows) {
+  auto enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(row_bytes)};
+  const cuuint32_t box[2] = {128, box_rows}, ones[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dim, stride, box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct MoeDevice {
+  bool ready = false;
+  int max_smem = 0;
+};
+std::mutex g_moe_mu;
+MoeDevice g_moe_devices[64];
+
+bsq_status moe_device(int index, int* max_smem) {
+  std::lock_guard<std::mutex> lock(g_moe_mu);
+  MoeDevice& d = g_moe_devices[index];
+  if (!d.ready) {
+    int optin = 0;
+    cudaFuncAttributes fa;
+    if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, index) != cudaSuccess ||
+        cudaFuncGetAttributes(&fa, moe_layer_kernel<kNVFP4>) != cudaSuccess)
+      return BSQ_ERR_CUDA;
+    const int most = optin - static_cast<int>(fa.sharedSizeBytes);  // the kernels' static part is the same for all formats
+    if (cudaFuncSetAttribute(moe_layer_kernel<kNVFP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+        cudaFuncSetAttribute(moe_layer_kernel<kMXFP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+        cudaFuncSetAttribute(moe_layer_kernel<kMXFP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+      return BSQ_ERR_CUDA;
+    d.max_smem = most;
+    d.ready = true;
+  }
+  *max_smem = d.max_smem;
+  return BSQ_OK;
 }
 
 template <int FMT>
-cudaError_t launch_moe(const MoeArgs& a, cudaStream_t st) {
-  const unsigned rows = a.tokens * a.top_k;
-  launch_pdl(moe_route_kernel, dim3(a.tokens), dim3(32), 0, st, a);
-  launch_pdl(moe_quant_x_kernel<FMT>, dim3(a.hidden / 32, rows), dim3(32), 0, st, a);
-  launch_pdl(moe_up_kernel<FMT>, dim3(a.inter / 4, rows), dim3(128), 0, st, a);
-  launch_pdl(moe_quant_h_kernel<FMT>, dim3(a.inter / 32, rows), dim3(32), 0, st, a);
-  launch_pdl(moe_down_kernel<FMT>, dim3(a.hidden / 4, a.tokens), dim3(128), 0, st, a);
-  return cudaGetLastError();
+bsq_status launch_moe(MoeArgs& a, const void* w13, const void* w2, const HostDevice& d, int max_smem, cudaStream_t st) {
+  const int64_t pairs = static_cast<int64_t>(a.tokens) * a.top_k;
+  CUtensorMap m13, m2, mx, mh;
+  if (!moe_map(&m13, w13, static_cast<int64_t>(a.experts) * 2 * a.inter, row_bytes_of(FMT, a.hidden), 128) ||
+      !moe_map(&m2, w2, static_cast<int64_t>(a.experts) * a.hidden, row_bytes_of(FMT, a.inter), 128) ||
+      !moe_map(&mx, a.xq, pairs, row_bytes_of(FMT, a.hidden), 8) || !moe_map(&mh, a.hq, pairs, row_bytes_of(FMT, a.inter), 8))
+    return BSQ_ERR_CUDA;
+  a.max_n = static_cast<int>(ceil_div(a.tokens, 16) * 16);
+  a.stage_bytes = static_cast<int>(ceil_div(2 * kMoeHalfBytes + a.max_n * 128 + 3 * MoeFmt<FMT>::kAtoms * 512, 1024) * 1024);
+  const int tables = moe_table_bytes(a.experts, static_cast<int>(pairs));
+  a.stages = std::min(8, (max_smem - 1024 - tables) / a.stage_bytes);
+  if (a.stages < 2) return BSQ_ERR_SHAPE;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(std::min(d.sm_count, kMoeMaxBlocks));
+  cfg.blockDim = dim3(kMoeThreads);
+  cfg.dynamicSmemBytes = 1024 + a.stages * a.stage_bytes + tables;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;  // the blocks wait for one another
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, moe_layer_kernel<FMT>, m13, m2, mx, mh, a) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
 }
 
 }  // namespace
@@ -32,7 +116,7 @@ extern "C" {
 int64_t bsq_moe_layer_workspace_bytes(int32_t fmt, int32_t tokens, int64_t hidden, int64_t inter, int32_t experts,
                                       int32_t top_k) {
   if (!fmt_ok(fmt) || !moe_sizes_ok(tokens, hidden, inter, experts, top_k)) return 0;
-  return 1024 + static_cast<int64_t>(tokens) * top_k * (8 + 4 * (hidden + inter));
+  return moe_workspace(fmt, tokens, hidden, inter, experts, top_k).bytes;
 }
 
 int32_t bsq_moe_layer(int32_t fmt, const void* x, int64_t ld_x, const float* logits, int64_t ld_logits, const void* w13,
@@ -43,29 +127,27 @@ int32_t bsq_moe_layer(int32_t fmt, const void* x, int64_t ld_x, const float* log
   if (!fmt_ok(fmt)) return BSQ_ERR_VALUE;
   if (!moe_sizes_ok(tokens, hidden, inter, experts, top_k)) return BSQ_ERR_SHAPE;
   if (tokens == 0) return BSQ_OK;
-  if ((tokens > 1 && (ld_x < hidden || ld_y < hidden || ld_logits < experts))) return BSQ_ERR_SHAPE;
+  if (tokens > 1 && (ld_x < hidden || ld_y < hidden || ld_logits < experts)) return BSQ_ERR_SHAPE;
   if (!x || !logits || !w13 || !w13_s || !w2 || !w2_s || !y || !workspace) return BSQ_ERR_NULL;
   if (fmt == BSQ_NVFP4 && (!x_sf || !w13_sf || !h_sf || !w2_sf)) return BSQ_ERR_NULL;
   if (!aligned(x, 16) || !aligned(logits, 4) || !aligned(w13, 16) || !aligned(w13_s, 16) || !aligned(w2, 16) ||
       !aligned(w2_s, 16) || !aligned(y, 16) || !aligned(workspace, 256) || ld_x % 8 != 0 || ld_y % 8 != 0 ||
       !aligned(x_sf, 4) || !aligned(w13_sf, 4) || !aligned(h_sf, 4) || !aligned(w2_sf, 4))
     return BSQ_ERR_ALIGN;
-  if (workspace_bytes < bsq_moe_layer_workspace_bytes(fmt, tokens, hidden, inter, experts, top_k)) return BSQ_ERR_SHAPE;
+  const MoeWorkspace w = moe_workspace(fmt, tokens, hidden, inter, experts, top_k);
+  if (workspace_bytes < w.bytes) return BSQ_ERR_SHAPE;
   HostDevice d;
   if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
+  int max_smem = 0;
+  if (bsq_status s = moe_device(d.index, &max_smem); s != BSQ_OK) return s;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   MoeArgs a{};
   a.x = static_cast<const uint16_t*>(x);
   a.ld_x = ld_x;
   a.logits = logits;
   a.ld_logits = ld_logits;
-  a.w13 = static_cast<const uint8_t*>(w13);
   a.w13_s = static_cast<const uint8_t*>(w13_s);
-  a.w2 = static_cast<const uint8_t*>(w2);
   a.w2_s = static_cast<const uint8_t*>(w2_s);
-  a.w13_expert = 2 * inter * row_bytes_of(fmt, hidden);
-  a.w13_s_expert = bsq_scales5d_bytes(fmt, 2 * inter, hidden);
-  a.w2_expert = hidden * row_bytes_of(fmt, inter);
-  a.w2_s_expert = bsq_scales5d_bytes(fmt, hidden, inter);
   a.x_sf = x_sf;
   a.w13_sf = w13_sf;
   a.h_sf = h_sf;
@@ -78,21 +160,20 @@ int32_t bsq_moe_layer(int32_t fmt, const void* x, int64_t ld_x, const float* log
   a.experts = experts;
   a.top_k = top_k;
   a.renorm = renormalize;
-  uint8_t* ws = static_cast<uint8_t*>(workspace) + 1024;
-  const int64_t rows = static_cast<int64_t>(tokens) * top_k;
-  a.ids = reinterpret_cast<int*>(ws);
-  a.probs = reinterpret_cast<float*>(ws + 4 * rows);
-  a.xq = reinterpret_cast<float*>(ws + 8 * rows);
-  a.h = a.xq + rows * hidden;
+  a.counters = reinterpret_cast<uint32_t*>(ws);
+  a.xq = ws + w.xq;
+  a.xq_s = ws + w.xq_s;
+  a.hq = ws + w.hq;
+  a.hq_s = ws + w.hq_s;
+  a.part = reinterpret_cast<float*>(ws + w.part);
+  a.yp = reinterpret_cast<float*>(ws + w.yp);
   a.err = d.error_word;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
   switch (fmt) {
-    case BSQ_NVFP4: e = launch_moe<kNVFP4>(a, st); break;
-    case BSQ_MXFP4: e = launch_moe<kMXFP4>(a, st); break;
-    default: e = launch_moe<kMXFP8>(a, st);
+    case BSQ_NVFP4: return launch_moe<kNVFP4>(a, w13, w2, d, max_smem, st);
+    case BSQ_MXFP4: return launch_moe<kMXFP4>(a, w13, w2, d, max_smem, st);
+    default: return launch_moe<kMXFP8>(a, w13, w2, d, max_smem, st);
   }
-  return e == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
 }
 
 }  // extern "C"

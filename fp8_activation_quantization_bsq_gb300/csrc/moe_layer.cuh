@@ -1,157 +1,683 @@
-// A mixture-of-experts layer for a few tokens over packed weights.
-//   ids, p = top-k of softmax(logits); xq = Q(x, x_sf[e]); g, u = W13[e] xq;
-//   h = bf16(silu(g) u); hq = Q(h, h_sf[e]); y = sum_k p_k W2[e] hq.
-// Simple form: one warp per output value.
+// A mixture-of-experts layer for a few tokens (at most 64) over packed
+// weights, in one kernel:
+//   ids, p = top-k of softmax(logits);  xq = Q(x, x_sf[e]);
+//   g, u = W13[e] xq;  h = bf16(silu(g) u);  hq = Q(h, h_sf[e]);
+//   y = sum over the choices of p W2[e] hq.
+//
+// What bounds it: every chosen expert's weights are read once, 3 I H values
+// per expert for a handful of operations per byte, so the kernel is a stream
+// of weights from DRAM, and everything else has to hide behind it.
+//
+// Form.  The weights' codes and 5D scales are exactly what the block-scaled
+// tensor-core product takes, so nothing is decoded: with the weights as the
+// 128-row operand and an expert's tokens as the narrow one (N = 16..64), a stage
+// of 2 x 128 rows x 128 bytes costs its loads and 8 products.  One persistent block per
+// SM; blocks wait for one another, so the launch is cooperative.
+//  * Every block routes all tokens itself (a warp per token), which saves a
+//    grid-wide wait before the first weight can be requested.
+//  * A phase's work is cut into units of one stage, numbered expert by
+//    expert, tile by tile along K, and every block takes an equal run of them
+//    whatever the tiles are.  A tile (pair of 128-row halves: gate and up rows, or
+//    256 rows of W2) that several blocks share is joined by the last of them
+//    to finish, which adds the parts in block order (no atomics on values: the result
+//    does not depend on timing).
+//  * warp 0 streams weights through a ring of shared-memory stages.  They do
+//    not depend on the activations, so at the start (while the tokens
+//    are quantized) and between the two phases (while h is finished) the ring
+//    fills ahead; warp 2 adds the tokens' operand to each stage once it is there.
+//  * warp 1 copies the stage's scales to tensor memory and issues the products;
+//    warps 4-7 drain finished accumulators: silu, the quantization of h along a
+//    warp's 32 rows, or the weighted rows of y.
+//  * After a last grid-wide wait every block sums its share of y over the choices, in their order.
+// All waits are bounded (about a second): an expired one records
+// BSQ_ERR_TIMEOUT, stops the block's roles, waits for the copies and products in
+// flight, frees the tensor memory and returns.
 #pragma once
 
-#include "serving_common.cuh"
+#include "tcgen05.cuh"
 
 namespace bsq {
 
 constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 1024;
+constexpr int kMoeThreads = 256;
+constexpr int kMoeHalfBytes = 128 * 128;  // a stage's 128 rows x 128 bytes of one tile half
+constexpr int kMoeMaxBlocks = 512;
+// counters at the start of the workspace, zero between calls
+constexpr int kMoeBarQuant = 0, kMoeBarDone = 1, kMoeBarExit = 2, kMoeSplit = 16, kMoeExpertDone = kMoeSplit + 2 * kMoeMaxBlocks;
+constexpr int kMoeCounterBytes = 4 * (kMoeExpertDone + 1024);
+
+// Columns of a stage and its scale atoms per 128 rows.
+template <int FMT> struct MoeFmt {
+  static constexpr int kElems = FMT == kMXFP8 ? 128 : 256;
+  static constexpr int kAtoms = kElems / Fmt<FMT>::ATOM_COLS;
+};
 
 struct MoeArgs {
   const uint16_t* x;
   int64_t ld_x;
   const float* logits;
   int64_t ld_logits;
-  const uint8_t *w13, *w13_s, *w2, *w2_s;
-  int64_t w13_expert, w13_s_expert, w2_expert, w2_s_expert;  // bytes per expert
-  const float *x_sf, *w13_sf, *h_sf, *w2_sf;                 // NVFP4
+  const uint8_t *w13_s, *w2_s;
+  const float *x_sf, *w13_sf, *h_sf, *w2_sf;  // NVFP4
   uint16_t* y;
   int64_t ld_y;
   int tokens, hidden, inter, experts, top_k, renorm;
-  int* ids;      // tokens * top_k
-  float* probs;
-  float* xq;     // rows x hidden values
-  float* h;      // rows x inter
+  uint32_t* counters;
+  uint8_t *xq, *xq_s, *hq, *hq_s;  // tokens' operands by row (expert by expert), scales by active expert
+  float* part;                     // [block][phase][part][2 halves][max_n][128]
+  float* yp;                       // [token * top_k + choice][hidden]
+  int max_n;                       // tokens rounded up to 16
+  int stages, stage_bytes;
   unsigned int* err;
 };
 
-__global__ void __launch_bounds__(32) moe_route_kernel(const MoeArgs a) {
-  pdl_wait();
-  const int t = blockIdx.x, lane = threadIdx.x;
+// Shared memory before the stages: routing tables (16-byte aligned parts).
+struct MoeTables {
+  uint64_t* mask;    // [experts] tokens that chose the expert
+  int* active;       // [active] expert of active index
+  int* row0;         // [active + 1] first row
+  int* index_of;     // [experts] active index
+  int* pair_of;      // [rows] token * top_k + choice
+  int* id;           // [pairs] expert
+  float* prob;       // [pairs]
+};
+__host__ __device__ inline int moe_align16(int n) { return (n + 15) & ~15; }
+__host__ __device__ inline int moe_table_bytes(int experts, int pairs) {
+  const int act = (experts < pairs ? experts : pairs) + 1;
+  return moe_align16(8 * experts) + 2 * moe_align16(4 * act) + moe_align16(4 * experts) + 3 * moe_align16(4 * pairs);
+}
+
+// A phase's units, cut into `parts` runs of equal length, none empty: block b
+// takes run b.
+struct MoePhase {
+  int64_t units;
+  int tiles;   // per expert
+  int chunks;  // stages per tile
+  int parts;
+};
+struct MoeRun {
+  int64_t begin, end;
+};
+__device__ __forceinline__ MoeRun moe_run(const MoePhase& p, int block) {
+  if (block >= p.parts) return {0, 0};
+  return {p.units * block / p.parts, p.units * (block + 1) / p.parts};
+}
+// The block whose run holds unit u.
+__device__ __forceinline__ int moe_owner(const MoePhase& p, int64_t u) {
+  return static_cast<int>(((u + 1) * p.parts - 1) / p.units);
+}
+
+template <int FMT>
+__device__ __forceinline__ MoePhase moe_phase(const MoeArgs& a, int phase, int active, int blocks) {
+  MoePhase p;
+  const int cols = phase == 0 ? a.hidden : a.inter;
+  p.tiles = phase == 0 ? a.inter / 128 : (a.hidden + 255) / 256;
+  p.chunks = (cols + MoeFmt<FMT>::kElems - 1) / MoeFmt<FMT>::kElems;
+  p.units = static_cast<int64_t>(active) * p.tiles * p.chunks;
+  p.parts = static_cast<int>(min(p.units, static_cast<int64_t>(blocks)));
+  return p;
+}
+
+// Order-preserving key of a logit: larger logits have larger keys, NaN and -inf the least.
+__device__ __forceinline__ uint32_t moe_key(float z) {
+  const uint32_t u = __float_as_uint(z == z ? z + 0.0f : -INFINITY);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float moe_unkey(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
+// Route token t with one warp: its choices and weights into the tables.
+__device__ __forceinline__ void moe_route(const MoeArgs& a, const MoeTables& tb, int t, int lane) {
   const float* z = a.logits + t * a.ld_logits;
-  float top = -INFINITY;
-  for (int e = lane; e < a.experts; e += 32) top = fmaxf(top, z[e]);
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+  uint32_t best = 0;
+  int at = 0x7FFFFFFF;
+  bool nan = false;
+  for (int e = lane; e < a.experts; e += 32) {
+    const float v = z[e];
+    nan |= v != v;
+    const uint32_t k = moe_key(v);
+    if (at == 0x7FFFFFFF || k > best) { best = k; at = e; }
+  }
+  if (__any_sync(~0u, nan) && lane == 0 && blockIdx.x == 0) record_error_at(a.err, kErrValue);
+  const float top = moe_unkey(__reduce_max_sync(~0u, best));
   float sum = 0.f;
-  for (int e = lane; e < a.experts; e += 32) sum += expf(z[e] - top);
+  for (int e = lane; e < a.experts; e += 32) sum += expf(moe_unkey(moe_key(z[e])) - top);
+#pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-  float last = INFINITY, chosen = 0.f;
-  int last_id = -1;
+  float chosen = 0.f, mine = 0.f;
   for (int k = 0; k < a.top_k; ++k) {
-    float best = -INFINITY;
-    int id = 0x7FFFFFFF;
-    for (int e = lane; e < a.experts; e += 32)
-      if ((z[e] < last || (z[e] == last && e > last_id)) && (z[e] > best || id == 0x7FFFFFFF)) { best = z[e]; id = e; }
-    for (int d = 16; d > 0; d >>= 1) {
-      const float ob = __shfl_xor_sync(~0u, best, d);
-      const int oi = __shfl_xor_sync(~0u, id, d);
-      if (ob > best || (ob == best && oi < id)) { best = ob; id = oi; }
-    }
-    if (id == 0x7FFFFFFF) id = 0;  // nothing left to compare (NaN)
-    last = best; last_id = id;
-    const float p = expf(best - top);
+    const uint32_t m = __reduce_max_sync(~0u, at == 0x7FFFFFFF ? 0u : best);
+    const int id = static_cast<int>(__reduce_min_sync(~0u, at != 0x7FFFFFFF && best == m ? static_cast<uint32_t>(at) : 0x7FFFFFFFu));
+    const float p = top == -INFINITY ? 0.f : expf(moe_unkey(m) - top);
     chosen += p;
-    if (lane == 0) { a.ids[t * a.top_k + k] = id; a.probs[t * a.top_k + k] = p; }
-  }
-  __syncwarp();
-  const float by = 1.f / (a.renorm ? chosen : sum);
-  for (int k = lane; k < a.top_k; k += 32) a.probs[t * a.top_k + k] *= by;
-}
-
-// Values that a warp's block of 32 (or two of 16) elements stands for once quantized.
-template <int FMT>
-__device__ __forceinline__ float moe_quant(float v, float tsf) {
-  constexpr int SF = Fmt<FMT>::SF;
-  float amax = fabsf(v);
-  for (int d = SF / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, d));
-  if constexpr (FMT == kNVFP4) {
-    const float ds = e4m3_to_f32(f32_to_e4m3(__fmul_rn(__fdiv_rn(amax, 6.f), tsf)));
-    const float f = ds == 0.f ? 0.f : __fdiv_rn(tsf, ds);
-    uint32_t h;
-    const float s = v * f;
-    asm("{.reg .b8 q, r;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %2, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, q;}" : "=r"(h) : "f"(s), "f"(0.f));
-    return f16x2_to_f32x2(h).x * ds / tsf;
-  } else {
-    const MxScale sc = mx_scale<FMT == kMXFP4 ? 6 : 448>(amax);
-    const int e = static_cast<int>(sc.byte) - 127;
-    const float s = v * pow2f(-e > 127 ? 127 : -e);
-    uint32_t h;
-    if constexpr (FMT == kMXFP4)
-      asm("{.reg .b8 q, r;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %2, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, q;}" : "=r"(h) : "f"(s), "f"(0.f));
-    else
-      h = e4m3x2_to_f16x2(f32x2_to_e4m3x2(s, 0.f));
-    return f16x2_to_f32x2(h).x * exp2f(static_cast<float>(e));
-  }
-}
-
-template <int FMT>
-__global__ void __launch_bounds__(32) moe_quant_x_kernel(const MoeArgs a) {
-  pdl_wait();
-  const int row = blockIdx.y, c = blockIdx.x * 32 + threadIdx.x;
-  const int e = a.ids[row];
-  const float v = __uint_as_float(static_cast<uint32_t>(a.x[(row / a.top_k) * a.ld_x + c]) << 16);
-  a.xq[static_cast<int64_t>(row) * a.hidden + c] = moe_quant<FMT>(v, FMT == kNVFP4 ? a.x_sf[e] : 1.f);
-}
-
-// Dot product of a packed weight row with FP32 values, per warp.
-template <int FMT>
-__device__ __forceinline__ float moe_dot(const uint8_t* w, const uint8_t* s5, int row, int K, const float* x) {
-  constexpr int SF = Fmt<FMT>::SF;
-  const int lane = threadIdx.x & 31, kt = (K / SF + 3) / 4;
-  float acc = 0.f;
-  const int64_t row_bytes = FMT == kMXFP8 ? K : K / 2;
-  for (int k = 2 * lane; k < K; k += 64) {
-    uint32_t h;
-    if constexpr (FMT == kMXFP8)
-      h = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(w + row * row_bytes + k));
-    else {
-      const uint32_t byte = w[row * row_bytes + k / 2];
-      asm("{.reg .b8 q, a, b, c;\n\tmov.b32 {q, a, b, c}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, q;}" : "=r"(h) : "r"(byte));
+    if (lane == k) mine = p;
+    if (lane == 0) {
+      tb.id[t * a.top_k + k] = id;
+      atomicOr(reinterpret_cast<unsigned long long*>(&tb.mask[id]), 1ull << t);
     }
-    const int sc = k / SF;
-    const uint32_t byte = s5[(static_cast<int64_t>(row / 128) * kt + sc / 4) * 512 + (row % 32) * 16 + (row % 128) / 32 * 4 + sc % 4];
-    const float f = FMT == kNVFP4 ? e4m3_to_f32(byte) : exp2f(static_cast<float>(byte) - 127.f);
-    const float2 v = f16x2_to_f32x2(h);
-    acc += (v.x * x[k] + v.y * x[k + 1]) * f;
+    if (at == id) {  // the owner's next best: after (m, id) in the order (larger key, lower expert)
+      at = 0x7FFFFFFF;
+      uint32_t nb = 0;
+      for (int e = lane; e < a.experts; e += 32) {
+        const uint32_t key = moe_key(z[e]);
+        if ((key < m || (key == m && e > id)) && (at == 0x7FFFFFFF || key > nb)) { nb = key; at = e; }
+      }
+      best = nb;
+    }
   }
-  for (int d = 16; d > 0; d >>= 1) acc += __shfl_xor_sync(~0u, acc, d);
-  return acc;
+  const float by = a.renorm ? chosen : sum;
+  if (lane < a.top_k) tb.prob[t * a.top_k + lane] = top == -INFINITY ? 0.f : mine / by;
 }
 
+// Quantize 32 consecutive BF16 values (16 words): packed bytes and scale bytes.
 template <int FMT>
-__global__ void __launch_bounds__(128) moe_up_kernel(const MoeArgs a) {
-  pdl_wait();
-  const int row = blockIdx.y, i = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int64_t e = a.ids[row];
-  const float* x = a.xq + static_cast<int64_t>(row) * a.hidden;
-  const float sf = FMT == kNVFP4 ? a.w13_sf[e] : 1.f;
-  const float g = moe_dot<FMT>(a.w13 + e * a.w13_expert, a.w13_s + e * a.w13_s_expert, i, a.hidden, x) / sf;
-  const float u = moe_dot<FMT>(a.w13 + e * a.w13_expert, a.w13_s + e * a.w13_s_expert, a.inter + i, a.hidden, x) / sf;
-  if ((threadIdx.x & 31) == 0) a.h[static_cast<int64_t>(row) * a.inter + i] = __bfloat162float(__float2bfloat16_rn(g / (1.f + expf(-g)) * u));
-}
-
-template <int FMT>
-__global__ void __launch_bounds__(32) moe_quant_h_kernel(const MoeArgs a) {
-  pdl_wait();
-  const int row = blockIdx.y, c = blockIdx.x * 32 + threadIdx.x;
-  float* p = a.h + static_cast<int64_t>(row) * a.inter + c;
-  *p = moe_quant<FMT>(*p, FMT == kNVFP4 ? a.h_sf[a.ids[row]] : 1.f);
-}
-
-template <int FMT>
-__global__ void __launch_bounds__(128) moe_down_kernel(const MoeArgs a) {
-  pdl_wait();
-  const int t = blockIdx.y, c = blockIdx.x * 4 + (threadIdx.x >> 5);
-  float y = 0.f;
-  for (int k = 0; k < a.top_k; ++k) {
-    const int64_t e = a.ids[t * a.top_k + k];
-    y += a.probs[t * a.top_k + k] / (FMT == kNVFP4 ? a.w2_sf[e] : 1.f) *
-         moe_dot<FMT>(a.w2 + e * a.w2_expert, a.w2_s + e * a.w2_s_expert, c, a.inter, a.h + static_cast<int64_t>(t * a.top_k + k) * a.inter);
+__device__ __forceinline__ void moe_quant_block(const uint4 (&v)[4], float tsf, uint8_t* dst, uint8_t* scale_word) {
+  if constexpr (FMT == kNVFP4) {
+    uint32_t sb[2], q[4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 2 * b; i < 2 * b + 2; ++i) m = absmax2(absmax2(absmax2(absmax2(m, v[i].x), v[i].y), v[i].z), v[i].w);
+      sb[b] = f32_to_e4m3(__fmul_rn(__fdiv_rn(absmax_final(m), 6.0f), tsf));
+      const float ds = e4m3_to_f32(sb[b]);
+      const float f = ds == 0.0f ? 0.0f : __fdiv_rn(tsf, ds);
+      q[2 * b] = quant8_e2m1(v[2 * b], f);
+      q[2 * b + 1] = quant8_e2m1(v[2 * b + 1], f);
+    }
+    *reinterpret_cast<uint4*>(dst) = make_uint4(q[0], q[1], q[2], q[3]);
+    *reinterpret_cast<uint16_t*>(scale_word) = static_cast<uint16_t>(sb[0] | (sb[1] << 8));
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = absmax2(absmax2(absmax2(absmax2(m, v[i].x), v[i].y), v[i].z), v[i].w);
+    const MxScale s = mx_scale<FMT == kMXFP4 ? 6 : 448>(absmax_final(m));
+    if constexpr (FMT == kMXFP4) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(quant8_e2m1_pow2(v[0], s.pow2), quant8_e2m1_pow2(v[1], s.pow2),
+                                                  quant8_e2m1_pow2(v[2], s.pow2), quant8_e2m1_pow2(v[3], s.pow2));
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint2 lo = quant8_e4m3_pow2(v[2 * h], s.pow2), hi = quant8_e4m3_pow2(v[2 * h + 1], s.pow2);
+        *reinterpret_cast<uint4*>(dst + 16 * h) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      }
+    }
+    *scale_word = static_cast<uint8_t>(s.byte);
   }
-  if ((threadIdx.x & 31) == 0) a.y[t * a.ld_y + c] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+}
+
+// This thread's h (row i of a warp's 32, one token) quantized with its
+// neighbours': blocks run along the lanes.  Every lane calls.
+template <int FMT>
+__device__ __forceinline__ void moe_quant_lane(float h, float tsf, int lane, uint8_t* row_bytes, uint8_t* scale_word) {
+  const uint32_t mag = __float_as_uint(fabsf(h));
+  if constexpr (FMT == kNVFP4) {
+    uint32_t m = mag;
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(~0u, m, d));
+    const uint32_t sb = f32_to_e4m3(__fmul_rn(__fdiv_rn(__uint_as_float(m), 6.0f), tsf));
+    const float ds = e4m3_to_f32(sb);
+    const float v = __fmul_rn(h, ds == 0.0f ? 0.0f : __fdiv_rn(tsf, ds));
+    const float next = __shfl_down_sync(~0u, v, 1);
+    if ((lane & 1) == 0) row_bytes[lane >> 1] = f32x2_to_e2m1x2(v, next);
+    if ((lane & 15) == 0) scale_word[lane >> 4] = static_cast<uint8_t>(sb);
+  } else {
+    const MxScale s = mx_scale<FMT == kMXFP4 ? 6 : 448>(__uint_as_float(__reduce_max_sync(~0u, mag)));
+    const float v = __fmul_rn(h, __uint_as_float(static_cast<uint32_t>(s.pow2) << 16));
+    if constexpr (FMT == kMXFP4) {
+      const float next = __shfl_down_sync(~0u, v, 1);
+      if ((lane & 1) == 0) row_bytes[lane >> 1] = f32x2_to_e2m1x2(v, next);
+    } else {
+      row_bytes[lane] = static_cast<uint8_t>(f32x2_to_e4m3x2(v, 0.f));
+    }
+    if (lane == 0) *scale_word = static_cast<uint8_t>(s.byte);
+  }
+}
+
+// Wait until a counter in global memory reaches `value`, for about a second.
+__device__ __forceinline__ bool moe_wait_count(const uint32_t* p, uint32_t value, const volatile uint32_t* abort_flag) {
+  if (ld_acquire(p) >= value) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (ld_acquire(p) < value) {
+    if (*abort_flag != 0u || globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    __nanosleep(40);
+  }
+  return true;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kMoeThreads, 1)
+    moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_constant__ CUtensorMap map_w2,
+                     const __grid_constant__ CUtensorMap map_xq, const __grid_constant__ CUtensorMap map_hq, const MoeArgs a) {
+  constexpr int kElems = MoeFmt<FMT>::kElems, kAtoms = MoeFmt<FMT>::kAtoms, kSF = Fmt<FMT>::SF;
+  constexpr int kAtomElems = Fmt<FMT>::ATOM_COLS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  __shared__ uint64_t full_bar[8], empty_bar[8], acc_full[2], acc_empty[2], drain_bar;
+  __shared__ uint32_t tmem_slot, last_flag;
+  __shared__ volatile uint32_t abort_flag, fills_a, fills_b, consumed;
+  __shared__ int active_count;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int blocks = gridDim.x, block = blockIdx.x, pairs = a.tokens * a.top_k;
+  const int stages = a.stages;
+
+  MoeTables tb;
+  {
+    const int act = (a.experts < pairs ? a.experts : pairs) + 1;
+    uint8_t* p = smem + stages * a.stage_bytes;
+    tb.mask = reinterpret_cast<uint64_t*>(p);
+    p += moe_align16(8 * a.experts);
+    tb.active = reinterpret_cast<int*>(p);
+    p += moe_align16(4 * act);
+    tb.row0 = reinterpret_cast<int*>(p);
+    p += moe_align16(4 * act);
+    tb.index_of = reinterpret_cast<int*>(p);
+    p += moe_align16(4 * a.experts);
+    tb.pair_of = reinterpret_cast<int*>(p);
+    p += moe_align16(4 * pairs);
+    tb.id = reinterpret_cast<int*>(p);
+    p += moe_align16(4 * pairs);
+    tb.prob = reinterpret_cast<float*>(p);
+  }
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full_bar[s], 2);  // weights, tokens
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 1);
+    }
+    mbar_init(&drain_bar, 1);
+    abort_flag = 0u;
+    fills_a = fills_b = consumed = 0u;
+    fence_mbar_init();
+    prefetch_tensormap(&map_w13);
+    prefetch_tensormap(&map_w2);
+    prefetch_tensormap(&map_xq);
+    prefetch_tensormap(&map_hq);
+  }
+  if (warp == 1) t5_alloc(&tmem_slot, 512);
+  for (int e = tid; e < a.experts; e += kMoeThreads) tb.mask[e] = 0;
+  __syncthreads();
+  for (int t = warp; t < a.tokens; t += kMoeThreads / 32) moe_route(a, tb, t, lane);
+  __syncthreads();
+  if (warp == 0) {  // active experts in increasing order, and their first rows
+    int n = 0, rows = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 32) {
+      const uint64_t m = e0 + lane < a.experts ? tb.mask[e0 + lane] : 0;
+      const uint32_t some = __ballot_sync(~0u, m != 0);
+      const int c = __popcll(m);
+      int before = c;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(~0u, before, d);
+        if (lane >= d) before += o;
+      }
+      if (m != 0) {
+        const int i = n + __popc(some & ((1u << lane) - 1u));
+        tb.active[i] = e0 + lane;
+        tb.row0[i] = rows + before - c;
+        tb.index_of[e0 + lane] = i;
+      }
+      n += __popc(some);
+      rows += __shfl_sync(~0u, before, 31);
+    }
+    if (lane == 0) {
+      tb.row0[n] = rows;
+      active_count = n;
+    }
+  }
+  t5_fence_before();
+  __syncthreads();
+  t5_fence_after();
+  for (int p = tid; p < pairs; p += kMoeThreads) {  // rows of an expert in token order
+    const int t = p / a.top_k, e = tb.id[p];
+    tb.pair_of[tb.row0[tb.index_of[e]] + __popcll(tb.mask[e] & ((1ull << t) - 1ull))] = p;
+  }
+  __syncthreads();
+  const uint32_t tmem = tmem_slot;
+  const int active = active_count;
+  const int part_floats = 2 * a.max_n * 128;
+
+  if (warp == 0) {
+    // ---- weights
+    if (lane == 0) {
+      uint32_t stage = 0, phase_bit = 0, fills = 0;
+      for (int phase = 0; phase < 2 && abort_flag == 0u; ++phase) {
+        const MoePhase p = moe_phase<FMT>(a, phase, active, blocks);
+        const MoeRun run = moe_run(p, block);
+        const int cols = phase == 0 ? a.hidden : a.inter, rows = phase == 0 ? 2 * a.inter : a.hidden;
+        const int kt = (cols / kSF + 3) / 4;
+        const int64_t scale_bytes = static_cast<int64_t>((rows + 127) / 128) * kt * 512;
+        const uint8_t* scales = phase == 0 ? a.w13_s : a.w2_s;
+        const CUtensorMap* map = phase == 0 ? &map_w13 : &map_w2;
+        int kc = static_cast<int>(run.begin % p.chunks);
+        int64_t item = run.begin / p.chunks;
+        for (int64_t u = run.begin; u < run.end; ++u) {
+          const int expert = tb.active[item / p.tiles], tile = static_cast<int>(item % p.tiles);
+          const int r0 = phase == 0 ? 128 * tile : 256 * tile, r1 = phase == 0 ? a.inter + r0 : r0 + 128;
+          const bool two = r1 < rows;
+          const int atoms = min(kAtoms, kt - kc * kAtoms);
+          if (!mbar_wait_bounded(&empty_bar[stage], phase_bit ^ 1u)) {
+            if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
+            abort_flag = 1u;
+            break;
+          }
+          if (abort_flag != 0u) break;
+          uint8_t* st = smem + stage * a.stage_bytes;
+          uint8_t* sc = st + 2 * kMoeHalfBytes + a.max_n * 128;
+          uint64_t* bar = &full_bar[stage];
+          mbar_arrive_expect_tx(bar, (two ? 2 : 1) * (kMoeHalfBytes + atoms * 512));
+          const int y = static_cast<int>(static_cast<int64_t>(expert) * rows);
+          const uint8_t* src = scales + expert * scale_bytes + static_cast<int64_t>(kc) * kAtoms * 512;
+          tma_load_2d(st, map, kc * 128, y + r0, bar);
+          bulk_load(sc, src + static_cast<int64_t>(r0 / 128) * kt * 512, atoms * 512, bar);
+          if (two) {
+            tma_load_2d(st + kMoeHalfBytes, map, kc * 128, y + r1, bar);
+            bulk_load(sc + kAtoms * 512, src + static_cast<int64_t>(r1 / 128) * kt * 512, atoms * 512, bar);
+          }
+          fills_a = ++fills;
+          if (++stage == stages) { stage = 0; phase_bit ^= 1u; }
+          if (++kc == p.chunks) { kc = 0; ++item; }
+        }
+      }
+    }
+  } else if (warp == 2) {
+    // ---- tokens
+    if (lane == 0) {
+      uint32_t stage = 0, phase_bit = 0, fills = 0;
+      bool ok = true;
+      for (int phase = 0; phase < 2 && ok; ++phase) {
+        const MoePhase p = moe_phase<FMT>(a, phase, active, blocks);
+        const MoeRun run = moe_run(p, block);
+        const int cols = phase == 0 ? a.hidden : a.inter, kt = (cols / kSF + 3) / 4;
+        const CUtensorMap* map = phase == 0 ? &map_xq : &map_hq;
+        const uint8_t* scales = phase == 0 ? a.xq_s : a.hq_s;
+        int kc = static_cast<int>(run.begin % p.chunks), ready = -1;
+        int64_t item = run.begin / p.chunks;
+        if (phase == 0 && run.begin < run.end) {
+          ok = moe_wait_count(a.counters + kMoeBarQuant, blocks, &abort_flag);
+          fence_async();
+        }
+        for (int64_t u = run.begin; u < run.end && ok; ++u) {
+          const int i = static_cast<int>(item / p.tiles);
+          if (phase == 1 && ready != i) {  // every tile of this expert's h is there
+            ok = moe_wait_count(a.counters + kMoeExpertDone + i, a.inter / 128, &abort_flag);
+            fence_async();
+            ready = i;
+          }
+          if (ok) ok = mbar_wait_bounded(&empty_bar[stage], phase_bit ^ 1u) && abort_flag == 0u;
+          if (!ok) break;
+          const int row = tb.row0[i], n8 = (tb.row0[i + 1] - row + 7) >> 3;
+          const int atoms = min(kAtoms, kt - kc * kAtoms);
+          uint8_t* st = smem + stage * a.stage_bytes + 2 * kMoeHalfBytes;
+          uint64_t* bar = &full_bar[stage];
+          mbar_arrive_expect_tx(bar, n8 * 1024 + atoms * 512);
+          for (int b = 0; b < n8; ++b) tma_load_2d(st + b * 1024, map, kc * 128, row + 8 * b, bar);
+          bulk_load(st + a.max_n * 128 + 2 * kAtoms * 512, scales + (static_cast<int64_t>(i) * kt + kc * kAtoms) * 512,
+                    atoms * 512, bar);
+          fills_b = ++fills;
+          if (++stage == stages) { stage = 0; phase_bit ^= 1u; }
+          if (++kc == p.chunks) { kc = 0; ++item; }
+        }
+      }
+      if (!ok) {
+        if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
+        abort_flag = 1u;
+      }
+    }
+  } else if (warp == 1) {
+    // ---- products
+    if (lane == 0) {
+      uint32_t stage = 0, phase_bit = 0, done = 0, seg = 0;
+      bool ok = true;
+      for (int phase = 0; phase < 2 && ok; ++phase) {
+        const MoePhase p = moe_phase<FMT>(a, phase, active, blocks);
+        const MoeRun run = moe_run(p, block);
+        const int cols = phase == 0 ? a.hidden : a.inter, rows = phase == 0 ? 2 * a.inter : a.hidden;
+        for (int64_t u = run.begin; u < run.end && ok; ++seg) {
+          const int64_t item = u / p.chunks, stop = min(run.end, (item + 1) * p.chunks);
+          const int i = static_cast<int>(item / p.tiles), tile = static_cast<int>(item % p.tiles);
+          const bool two = phase == 0 || 256 * tile + 128 < rows;
+          const uint32_t n = (tb.row0[i + 1] - tb.row0[i] + 15) & ~15u;
+          const uint32_t buf = seg & 1u, d = tmem + buf * 128u;
+          if (!mbar_wait_bounded(&acc_empty[buf], ((seg >> 1) & 1u) ^ 1u) || abort_flag != 0u) { ok = false; break; }
+          t5_fence_after();
+          for (uint32_t fresh = 0; u < stop; ++u) {
+            const int kc = static_cast<int>(u % p.chunks);
+            if (!mbar_wait_bounded(&full_bar[stage], phase_bit) || abort_flag != 0u) { ok = false; break; }
+            t5_fence_after();
+            const uint32_t st = smem_addr(smem + stage * a.stage_bytes);
+            const uint32_t tok = st + 2 * kMoeHalfBytes, sc = tok + a.max_n * 128;
+            const uint32_t sf = tmem + 256u + (done & 1u) * 64u;
+            const int left = cols - kc * kElems, atoms = min(kAtoms, (left + kAtomElems - 1) / kAtomElems);
+            for (int q = 0; q < atoms; ++q) {
+              t5_copy_atom(sf + 4 * q, t5_desc_atom(sc + 512 * q));
+              if (two) t5_copy_atom(sf + 16 + 4 * q, t5_desc_atom(sc + 512 * (kAtoms + q)));
+              t5_copy_atom(sf + 32 + 4 * q, t5_desc_atom(sc + 512 * (2 * kAtoms + q)));
+            }
+            constexpr int kMmaElems = kElems / 4;
+            const int slices = min(4, (left + kMmaElems - 1) / kMmaElems);
+            for (int m = 0; m < slices; ++m) {
+              const uint32_t atom = FMT == kNVFP4 ? m : FMT == kMXFP4 ? m >> 1 : 0;
+              const uint32_t id = FMT == kNVFP4 ? 0 : FMT == kMXFP4 ? 2 * (m & 1) : m;
+              const uint32_t idesc = t5_idesc_scaled<FMT>(n, id);
+              const uint64_t b = t5_desc_sw128(tok + 32 * m);
+              t5_mma_scaled<FMT>(d, t5_desc_sw128(st + 32 * m), b, idesc, sf + 4 * atom, sf + 32 + 4 * atom, fresh | m);
+              if (two)
+                t5_mma_scaled<FMT>(d + 64, t5_desc_sw128(st + kMoeHalfBytes + 32 * m), b, idesc, sf + 16 + 4 * atom,
+                                   sf + 32 + 4 * atom, fresh | m);
+            }
+            fresh = 4;
+            t5_commit(&empty_bar[stage]);
+            consumed = ++done;
+            if (++stage == stages) { stage = 0; phase_bit ^= 1u; }
+          }
+          if (ok) t5_commit(&acc_full[buf]);
+        }
+      }
+      if (!ok) {
+        if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
+        abort_flag = 1u;
+      }
+      t5_commit(&drain_bar);
+      if (!mbar_wait_bounded(&drain_bar, 0)) record_error_at(a.err, kErrTimeout);
+    }
+  } else if (warp >= 4) {
+    // ---- quantize the tokens' rows, a block of 32 columns per thread at a time
+    const int et = tid - 128, quarter = warp & 3;
+    {
+      const int per_row = a.hidden / 32, kt = (a.hidden / kSF + 3) / 4;
+      const int row_bytes = FMT == kMXFP8 ? a.hidden : a.hidden / 2;
+      for (int64_t w = static_cast<int64_t>(block) * 128 + et; w < static_cast<int64_t>(pairs) * per_row; w += blocks * 128) {
+        const int row = static_cast<int>(w / per_row), c = static_cast<int>(w % per_row);
+        const int pair = tb.pair_of[row], e = tb.id[pair], i = tb.index_of[e], r = row - tb.row0[i];
+        const uint16_t* src = a.x + (pair / a.top_k) * a.ld_x + 32 * c;
+        uint4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = ld_global_nc_v4(src + 8 * q);
+        const int s0 = 32 * c / kSF;  // first scale column
+        uint8_t* word = a.xq_s + (static_cast<int64_t>(i) * kt + s0 / 4) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (s0 & 3);
+        moe_quant_block<FMT>(v, FMT == kNVFP4 ? a.x_sf[e] : 1.f, a.xq + static_cast<int64_t>(row) * row_bytes + 32 * c / (FMT == kMXFP8 ? 1 : 2),
+                             word);
+        if (c == per_row - 1)  // the last atom's columns past the row: zero
+          for (int s = s0 + 32 / kSF; s < 4 * kt; ++s) word[s - s0] = 0;
+      }
+      fence_async();
+      __threadfence();
+      named_sync(1, 128);
+      if (et == 0) atomicAdd(a.counters + kMoeBarQuant, 1u);
+    }
+    // ---- finished accumulators
+    uint32_t seg = 0;
+    bool ok = true;
+    for (int phase = 0; phase < 2 && ok; ++phase) {
+      const MoePhase p = moe_phase<FMT>(a, phase, active, blocks);
+      const MoeRun run = moe_run(p, block);
+      for (int64_t u = run.begin; u < run.end; ++seg) {
+        const int64_t item = u / p.chunks, first = item * p.chunks, stop = min(run.end, first + p.chunks);
+        const int i = static_cast<int>(item / p.tiles), tile = static_cast<int>(item % p.tiles), expert = tb.active[i];
+        const int row0 = tb.row0[i], n = tb.row0[i + 1] - row0;
+        const bool whole = u == first && stop == first + p.chunks;
+        const uint32_t buf = seg & 1u;
+        if (et == 0) last_flag = mbar_wait_bounded(&acc_full[buf], (seg >> 1) & 1u) && abort_flag == 0u ? 1u : 0u;
+        named_sync(1, 128);
+        ok = last_flag != 0u;
+        if (!ok) break;  // uniform
+        t5_fence_after();
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + buf * 128u;
+        const int r = 32 * quarter + lane;
+        // a block's run begins inside at most one tile of a phase (part 0) and ends inside one (part 1)
+        float* mine = a.part + ((static_cast<int64_t>(block) * 2 + phase) * 2 + (u == first ? 1 : 0)) * part_floats;
+        const int owner0 = whole ? block : moe_owner(p, first);
+        const int owner1 = whole ? block : moe_owner(p, first + p.chunks - 1);
+        bool finish = whole;
+        if (!whole) {
+          for (int c = 0; c < n; c += 16) {
+            float x[16], z[16];
+            t5_ld16_pair(lanes + c, lanes + 64 + c, x, z);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < n) {
+                mine[(c + j) * 128 + r] = x[j];
+                mine[(a.max_n + c + j) * 128 + r] = z[j];
+              }
+          }
+          __threadfence();
+          t5_fence_before();
+          named_sync(1, 128);
+          if (et == 0) {
+            mbar_arrive(&acc_empty[buf]);
+            uint32_t* count = a.counters + kMoeSplit + 2 * owner0 + phase;
+            const uint32_t now = atomicAdd(count, static_cast<uint32_t>(stop - u)) + static_cast<uint32_t>(stop - u);
+            last_flag = now == static_cast<uint32_t>(p.chunks) ? 1u : 0u;
+            if (last_flag != 0u) *count = 0u;
+            __threadfence();
+          }
+          named_sync(1, 128);
+          finish = last_flag != 0u;
+          named_sync(1, 128);  // last_flag is written again below
+        }
+        if (finish) {
+          for (int c = 0; c < n; c += 16) {
+            float x[16], z[16];
+            if (whole) {
+              t5_ld16_pair(lanes + c, lanes + 64 + c, x, z);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j] = z[j] = 0.f;
+              for (int o = owner0; o <= owner1; ++o) {
+                const float* part = a.part + ((static_cast<int64_t>(o) * 2 + phase) * 2 + (o == owner0 ? 1 : 0)) * part_floats;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  if (c + j < n) {
+                    x[j] += __ldcg(part + (c + j) * 128 + r);
+                    z[j] += __ldcg(part + (a.max_n + c + j) * 128 + r);
+                  }
+              }
+            }
+            if (phase == 0) {
+              const float by = FMT == kNVFP4 ? 1.f / (a.x_sf[expert] * a.w13_sf[expert]) : 1.f;
+              const float hsf = FMT == kNVFP4 ? a.h_sf[expert] : 1.f;
+              const int i0 = 128 * tile + 32 * quarter;  // first of this warp's rows
+              const int kt = a.inter / kAtomElems, s0 = i0 / kSF;
+              const int64_t row_bytes = FMT == kMXFP8 ? a.inter : a.inter / 2;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (c + j >= n) break;  // uniform
+                const float g = x[j] * by, up = z[j] * by;
+                const float h = __bfloat162float(__float2bfloat16_rn(g / (1.f + expf(-g)) * up));
+                const int tok = c + j;
+                uint8_t* word = a.hq_s + (static_cast<int64_t>(i) * kt + s0 / 4) * 512 + (tok & 31) * 16 + (tok >> 5) * 4 + (s0 & 3);
+                moe_quant_lane<FMT>(h, hsf, lane, a.hq + (row0 + tok) * row_bytes + (FMT == kMXFP8 ? i0 : i0 / 2), word);
+              }
+            } else {
+              const float by = FMT == kNVFP4 ? 1.f / (a.h_sf[expert] * a.w2_sf[expert]) : 1.f;
+              const int col = 256 * tile + r;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (c + j >= n) break;
+                const int pair = tb.pair_of[row0 + c + j];
+                const float f = tb.prob[pair] * by;
+                float* dst = a.yp + static_cast<int64_t>(pair) * a.hidden + col;
+                if (col < a.hidden) __stcg(dst, x[j] * f);
+                if (col + 128 < a.hidden) __stcg(dst + 128, z[j] * f);
+              }
+            }
+          }
+          fence_async();
+          __threadfence();
+          t5_fence_before();
+          named_sync(1, 128);
+          if (et == 0) {
+            if (whole) mbar_arrive(&acc_empty[buf]);
+            if (phase == 0) atomicAdd(a.counters + kMoeExpertDone + i, 1u);
+          }
+        }
+        u = stop;
+      }
+    }
+    // ---- y, once every block is done
+    named_sync(1, 128);
+    if (et == 0) {
+      bool all = ok && abort_flag == 0u;
+      if (all) {
+        atomicAdd(a.counters + kMoeBarDone, 1u);
+        all = moe_wait_count(a.counters + kMoeBarDone, blocks, &abort_flag);
+      }
+      if (!all) {
+        if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
+        abort_flag = 1u;
+      }
+      last_flag = all ? 1u : 0u;
+    }
+    named_sync(1, 128);
+    if (last_flag != 0u) {
+      const int quads = a.hidden / 4;
+      for (int64_t w = static_cast<int64_t>(block) * 128 + et; w < static_cast<int64_t>(a.tokens) * quads; w += blocks * 128) {
+        const int t = static_cast<int>(w / quads), c = static_cast<int>(w % quads) * 4;
+        const float* src = a.yp + static_cast<int64_t>(t) * a.top_k * a.hidden + c;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < a.top_k; ++k) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(k) * a.hidden));
+          s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
+        *reinterpret_cast<uint2*>(a.y + t * a.ld_y + c) = make_uint2(f32x2_to_elem2<false>(s.x, s.y), f32x2_to_elem2<false>(s.z, s.w));
+      }
+      // every block has passed every other wait: clear the counters
+      for (int i = block * 128 + et; i < active; i += blocks * 128) a.counters[kMoeExpertDone + i] = 0u;
+      if (et == 0) {
+        __threadfence();
+        if (atomicAdd(a.counters + kMoeBarExit, 1u) == static_cast<uint32_t>(blocks) - 1u) {
+          a.counters[kMoeBarQuant] = 0u;
+          a.counters[kMoeBarDone] = 0u;
+          a.counters[kMoeBarExit] = 0u;
+        }
+      }
+    }
+  }
+
+  __syncthreads();
+  // after an expired wait: loads that nothing consumed land before the block ends
+  if (tid == 0) {
+    const uint32_t most = max(fills_a, fills_b);
+    for (uint32_t f = consumed; f < most; ++f) {
+      uint64_t* bar = &full_bar[f % stages];
+      if (f >= fills_a) mbar_arrive(bar);
+      if (f >= fills_b) mbar_arrive(bar);
+      if (!mbar_wait_bounded(bar, (f / stages) & 1u)) record_error_at(a.err, kErrTimeout);
+    }
+  }
+  t5_fence_before();
+  __syncthreads();
+  t5_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    t5_dealloc(tmem, 512);
+  }
 }
 
 }  // namespace bsq

@@ -26,6 +26,13 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Two FP32 -> a byte of two E2M1 codes, `lo` in the low nibble.
+__device__ __forceinline__ uint8_t f32x2_to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 q;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %2, %1;\n\tmov.b32 %0, {q, q, q, q};\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
+  return static_cast<uint8_t>(r);
+}
+
 __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }

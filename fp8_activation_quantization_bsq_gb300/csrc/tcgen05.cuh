@@ -1,0 +1,118 @@
+// tcgen05 (5th-generation tensor core) and TMA wrappers shared by the
+// serving kernels, as inline PTX: tensor-memory allocation, shared-memory and
+// instruction descriptors, block-scaled and FP16 matrix products, copies of
+// scale factors into tensor memory, and bulk copies.
+#pragma once
+
+#include "serving_common.cuh"
+
+namespace bsq {
+
+__device__ __forceinline__ void t5_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void t5_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+// Whole warp.
+__device__ __forceinline__ void t5_alloc(uint32_t* slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void t5_dealloc(uint32_t taddr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+
+// Arrive on `bar` when every tcgen05 operation this thread has issued is done.
+__device__ __forceinline__ void t5_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// K-major operand tile with the 128-byte swizzle: rows of 128 bytes, groups of 8
+// rows 1024 bytes apart.  Fields: address >> 4, leading offset (unused, 1),
+// stride offset >> 4 at 32, 0b001 at 46, swizzle mode 2 at 61.
+__device__ __forceinline__ uint64_t t5_desc_sw128(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(1) << 16) | (static_cast<uint64_t>(64) << 32) |
+         (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+// A 512-byte scale atom (32 rows of 16 bytes, no swizzle): groups of 8 rows 128 bytes apart.
+__device__ __forceinline__ uint64_t t5_desc_atom(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(8) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+// One scale atom into 4 columns of tensor memory: column c, lane i of every
+// quarter gets the 4 bytes of the atom's row 32 c + i.
+__device__ __forceinline__ void t5_copy_atom(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// D (128 x N, FP32) (+)= A B^T with block scales, K = 32 bytes of each row.
+template <int FMT>
+__device__ __forceinline__ void t5_mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                              uint32_t accumulate) {
+  if constexpr (FMT == kNVFP4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else if constexpr (FMT == kMXFP4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a),
+        "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of the block-scaled products, M = 128: scale id of B
+// at 4-5, operand formats at 7 and 10 (E2M1 1, E4M3 0), N >> 3 at 17, scale type at 23
+// (E4M3 0, E8M0 1), M >> 4 at 24, scale id of A at 29-30.  The id picks the
+// byte of a scale word that a K slice uses.
+template <int FMT>
+__device__ __forceinline__ uint32_t t5_idesc_scaled(uint32_t n, uint32_t sf_id) {
+  constexpr uint32_t fmt = FMT == kMXFP8 ? 0u : 1u;
+  return (sf_id << 4) | (fmt << 7) | (fmt << 10) | ((n >> 3) << 17) | ((FMT == kNVFP4 ? 0u : 1u) << 23) | (8u << 24) | (sf_id << 29);
+}
+
+// 16 consecutive columns of this thread's tensor-memory lane at two addresses,
+// waited for in the same statement, so that no register is read early.
+__device__ __forceinline__ void t5_ld16_pair(uint32_t ta, uint32_t tb, float (&x)[16], float (&y)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+      "[%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]),
+        "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15]), "=f"(y[0]), "=f"(y[1]), "=f"(y[2]),
+        "=f"(y[3]), "=f"(y[4]), "=f"(y[5]), "=f"(y[6]), "=f"(y[7]), "=f"(y[8]), "=f"(y[9]), "=f"(y[10]), "=f"(y[11]),
+        "=f"(y[12]), "=f"(y[13]), "=f"(y[14]), "=f"(y[15])
+      : "r"(ta), "r"(tb)
+      : "memory");
+}
+
+// Contiguous copy of `bytes` (a multiple of 16) into shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)),
+               "l"(src), "r"(bytes), "r"(smem_addr(bar))
+               : "memory");
+}
+
+// Order generic-proxy accesses before and after it with the async proxy's (TMA).
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Barrier of `threads` threads of the block (id 1..15).
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+}  // namespace bsq

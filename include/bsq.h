@@ -519,7 +519,7 @@ BSQ_API int32_t bsq_kv_attention(int32_t dtype, const void* q_dev, int64_t total
  *   y = bf16(sum over the choices of p * (Q(h, h_sf[e]) . w2[e])).
  * Logits of -inf exclude an expert (its weight is 0); a row of nothing else
  * gives zeros.  NaN logits count as -inf and record BSQ_ERR_VALUE.
- *   workspace_dev     bsq_moe_layer_workspace_bytes() bytes, 1024-byte aligned,
+ *   workspace_dev     bsq_moe_layer_workspace_bytes() bytes, 256-byte aligned,
  *                     zeroed by the caller once before its first use; every call leaves
  *                     its counters zeroed again (after a reported BSQ_ERR_TIMEOUT it has
  *                     to be zeroed anew).  Calls sharing it must not overlap.
