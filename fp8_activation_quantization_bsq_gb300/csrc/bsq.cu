@@ -11,6 +11,7 @@
 #include <mutex>
 #include <algorithm>
 #include <utility>
+#include <vector>
 
 #include "block_scaled_dot.cuh"
 #include "dense_quant.cuh"
@@ -120,6 +121,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
       g_encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
   return g_encode_tiled;
+}
+
+bsq_status allow_smem(const void* kernel, int bytes, int index) {
+  static std::vector<std::pair<const void*, int>> done;  // under g_mu
+  std::lock_guard<std::mutex> lock(g_mu);
+  for (const auto& [k, i] : done)
+    if (k == kernel && i == index) return BSQ_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return BSQ_ERR_CUDA;
+  try {
+    done.emplace_back(kernel, index);
+  } catch (...) {  // not remembered: set again next time
+  }
+  return BSQ_OK;
 }
 
 bsq_status host_device(HostDevice* out) {

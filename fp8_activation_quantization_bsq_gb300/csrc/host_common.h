@@ -47,6 +47,9 @@ struct HostDevice {
 };
 bsq_status host_device(HostDevice* out);
 
+// Allow `kernel` `bytes` of dynamic shared memory on device `index` (once per kernel and device).
+bsq_status allow_smem(const void* kernel, int bytes, int index);
+
 // cuTensorMapEncodeTiled, or NULL when the driver does not have it.
 PFN_cuTensorMapEncodeTiled_v12000 encode_tiled();
 

@@ -1,20 +1,44 @@
-// Attention over the 8-bit paged cache.
+// Attention over the 8-bit paged cache, for few query rows per kv head
+// (single tokens, guessed tokens).
 //
 // Per query row of a head, over the allowed keys j of its sequence:
-//   s_j = sm_scale q.k_j,  out = sum_j exp(s_j) v_j / sum_j exp(s_j).
-// One warp per (query token, head), a key at a time, with the running
-// maximum and sum of the softmax.
+//   s_j = sm_scale log2(e) q.k_j,  out = sum_j 2^s_j v_j / sum_j 2^s_j.
+// A page holds codes under power-of-two scales, k = c 2^ek and v = c 2^ev.  The
+// value scale goes into the exponent: with t_j = s_j + ev_j and m at or above
+// most t_j (it follows the running maximum once that is 8 above it),
+//   out = sum_j 2^(t_j - m) c_j / sum_j 2^(t_j - m) 2^-ev_j,
+// so the weights of the codes stay within FP16 whatever the pages' scales are, and
+// nothing is multiplied into the values.  The key scale is one factor of a tile's
+// scores.  E4M3 codes and scaled query rows (a power of two per row) are exact in FP16;
+// weights are rounded to FP16 (a relative 2^-11 each, against 2^-9 of a BF16
+// output), and all sums are FP32.
+//
+// What bounds it: the cache is read once, about 2 x heads-per-kv-head operations
+// per byte, so DRAM.  Persistent blocks (two per SM) of four consumer warps and a
+// producer; the units, tiles of 64 keys of one (sequence, kv head, row tile), are cut
+// into equal runs, so that ragged lengths and long contexts spread evenly.  The
+// producer streams tiles by TMA through a ring.  Each consumer warp takes 16 of a tile's
+// keys for all 16 rows and keeps its own maximum, sum and accumulators, so warps meet
+// only at the end of an item.  mma.sync products: with 16 rows at most, a 128-row
+// tensor-memory product would be mostly padding.  Fragments come straight from the codes with wide
+// shared loads: the order of the dimension in q.k and of the output columns is free, so a thread takes
+// 16 consecutive bytes of a key, and pairs of keys are interleaved bytewise before conversion.
+// An item cut by the runs is joined by the last block that finishes (in two levels of at most 16
+// parts when there are many), always in block order.
 #pragma once
 
-#include "serving_common.cuh"
+#include "tcgen05.cuh"
 
 namespace bsq {
+
+constexpr int kKvTile = 64;       // keys per unit
+constexpr int kKvMaxBlocks = 1024;
+constexpr int kKvJoin = 16;       // parts joined at a time
+constexpr int kKvCounterBytes = 4 * 2 * kKvMaxBlocks;
 
 struct KvAttnArgs {
   const uint16_t* q;              // (total, heads, D)
   int64_t q_tok, q_head;          // strides in elements
-  const uint8_t* cache[2];
-  int64_t cs_page, cs_head, cs_tok;
   const uint8_t* scales[2];       // (num_pages, kv_heads) E8M0 bytes
   const int32_t* table;
   int64_t table_ld;
@@ -23,69 +47,617 @@ struct KvAttnArgs {
   uint16_t* out;                  // (total, heads, D) contiguous
   float* lse;                     // (total, heads) or NULL
   int64_t total, num_pages;
-  int batch, heads, kv_heads, page, table_width, causal, window;
+  int batch, heads, kv_heads, group, page, page_shift, table_width, causal, window;
   float scale_log2;               // sm_scale * log2(e)
+  uint32_t* counters;             // [2][kKvMaxBlocks], zero between calls
+  float* part;                    // [block][2][rows * D + 2 * rows]
   unsigned int* err;
 };
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(128) kv_attention_kernel(const KvAttnArgs a) {
+// A sequence's rows and, per row tile, its keys.
+struct KvSeq {
+  int t0, n, len, row_tiles;
+};
+template <int RT>
+__device__ __forceinline__ KvSeq kv_seq(const KvAttnArgs& a, int b, bool report) {
+  KvSeq s;
+  const int64_t t0 = a.offsets[b], t1 = a.offsets[b + 1];
+  s.len = a.lens[b];
+  bool ok = t0 >= 0 && t1 <= a.total;
+  if (s.len < 0 || s.len > static_cast<int64_t>(a.table_width) * a.page) {
+    ok = false;
+    s.len = 0;
+  }
+  if (!ok && report) record_error_at(a.err, kErrValue);
+  s.t0 = static_cast<int>(t0);
+  s.n = t0 >= 0 && t1 <= a.total && t1 > t0 ? static_cast<int>(t1 - t0) : 0;
+  s.row_tiles = (s.n * a.group + RT - 1) / RT;
+  return s;
+}
+// Keys [lo, hi) that any row of tile rt may see (lo = hi: none).
+template <int RT>
+__device__ __forceinline__ void kv_keys(const KvAttnArgs& a, const KvSeq& s, int rt, int& lo, int& hi) {
+  const int rows = s.n * a.group;
+  const int i0 = rt * RT / a.group, i1 = (min(rows, (rt + 1) * RT) - 1) / a.group;
+  hi = a.causal ? min(s.len, s.len - s.n + i1 + 1) : s.len;
+  lo = a.window > 0 ? max(0, s.len - s.n + i0 - a.window + 1) : 0;
+  if (hi <= lo) lo = hi = 0;
+}
+// Units of an item: tiles of kKvTile keys, one for an item without keys (its rows are still written).
+__device__ __forceinline__ int kv_units(int lo, int hi) { return max(1, (hi + kKvTile - 1) / kKvTile - lo / kKvTile); }
+
+template <int RT>
+__device__ __forceinline__ int64_t kv_seq_units(const KvAttnArgs& a, const KvSeq& s) {
+  int64_t u = 0;
+  for (int rt = 0; rt < s.row_tiles; ++rt) {
+    int lo, hi;
+    kv_keys<RT>(a, s, rt, lo, hi);
+    u += kv_units(lo, hi);
+  }
+  return u;  // per kv head
+}
+
+// Where a block's run begins.
+struct KvStart {
+  int64_t total;    // units in all
+  int64_t before;   // units of the sequences before `seq`
+  int seq;
+};
+
+// One item's share of a block's run.
+struct KvSegment {
+  KvSeq s;
+  int b, head, rt, lo, hi;  // kv head, row tile, keys
+  int tile0, tile1;         // of this share, in tiles of the sequence
+  int64_t first, count;     // the item's units
+};
+
+// Walks the units [u, end) item by item.
+template <int RT>
+struct KvWalk {
+  int64_t u, end, before, per_head;
+  int b;
+  KvSeq s;
+  __device__ __forceinline__ void load(const KvAttnArgs& a) {
+    s = kv_seq<RT>(a, b, false);
+    per_head = kv_seq_units<RT>(a, s);
+  }
+  __device__ __forceinline__ bool next(const KvAttnArgs& a, KvSegment& g) {
+    if (u >= end) return false;
+    while (u >= before + per_head * a.kv_heads) {
+      before += per_head * a.kv_heads;
+      ++b;
+      load(a);
+    }
+    const int64_t rel = u - before;
+    g.head = static_cast<int>(rel / per_head);
+    int64_t at = before + g.head * per_head;
+    int rt = 0;
+    while (true) {
+      kv_keys<RT>(a, s, rt, g.lo, g.hi);
+      const int c = kv_units(g.lo, g.hi);
+      if (u < at + c) {
+        g.first = at;
+        g.count = c;
+        break;
+      }
+      at += c;
+      ++rt;
+    }
+    g.rt = rt;
+    g.b = b;
+    g.s = s;
+    const int64_t stop = min(end, g.first + g.count);
+    g.tile0 = g.lo / kKvTile + static_cast<int>(u - g.first);
+    g.tile1 = g.hi > g.lo ? g.tile0 + static_cast<int>(stop - u) : g.tile0;
+    u = stop;
+    return true;
+  }
+};
+
+__device__ __forceinline__ void kv_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// 4D TMA tile (dimension, token, head, page).
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Per page of a stage: factor of the scores, exponent of the values, and its reciprocal power.
+struct KvPageScale {
+  float kfac, ev, inv;
+};
+
+template <int D, int ROWG>
+struct KvShape {
+  static constexpr int kWarps = 4 * ROWG;                  // consumers
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kRows = 16 * ROWG;
+  static constexpr int kTileBytes = kKvTile * D;           // of keys, and of values
+  static constexpr int kStages = ROWG == 1 ? 4 : 6;
+  static constexpr int kMergeBytes = ROWG * 4 * 16 * D * 4;
+  static constexpr int kSmem = 1024 + kStages * 2 * kTileBytes + kMergeBytes;
+  static constexpr int kPartFloats = kRows * D + 2 * kRows;
+};
+
+// The codes of 4 consecutive dimensions of two keys -> for each dimension
+// the pair (key 0, key 1) in FP16.
+__device__ __forceinline__ void kv_pairs(uint32_t w0, uint32_t w1, uint32_t (&o)[4]) {
+  const uint32_t lo = __byte_perm(w0, w1, 0x5140), hi = __byte_perm(w0, w1, 0x7362);
+  o[0] = e4m3x2_to_f16x2(lo & 0xFFFFu);
+  o[1] = e4m3x2_to_f16x2(lo >> 16);
+  o[2] = e4m3x2_to_f16x2(hi & 0xFFFFu);
+  o[3] = e4m3x2_to_f16x2(hi >> 16);
+}
+
+// Byte offset of 16-byte chunk `c` of row `r` in a tile that TMA wrote with
+// the 128-byte (D = 128) or 64-byte (D = 64) swizzle.
+template <int D>
+__device__ __forceinline__ uint32_t kv_chunk(int r, int c) {
+  if constexpr (D == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+  return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Join `parts` parts whose slots follow from `slot`, in order, with the
+// block's consumer threads: each thread keeps its share of the sum in `acc`
+// (float4 q of the tile at index q * threads + tid); row sums and maxima in shared memory.
+template <int D, int ROWG, class SlotFn>
+__device__ __forceinline__ void kv_join(int parts, SlotFn slot, int tid, float (*weight)[16 * ROWG], float (*sums)[16 * ROWG],
+                                        float* row_m, float* row_l, float4 (&acc)[D / 32]) {
+  using S = KvShape<D, ROWG>;
+  constexpr int kT = 32 * S::kWarps;
+  for (int i = tid; i < parts * S::kRows; i += kT) {
+    const float* s = slot(i / S::kRows) + S::kRows * D + i % S::kRows;
+    weight[i / S::kRows][i % S::kRows] = __ldcg(s);
+    sums[i / S::kRows][i % S::kRows] = __ldcg(s + S::kRows);
+  }
+  named_sync(1, kT);
+  if (tid < S::kRows) {
+    float m = -INFINITY, l = 0.f;
+    for (int p = 0; p < parts; ++p) m = fmaxf(m, weight[p][tid]);
+    for (int p = 0; p < parts; ++p) {
+      const float w = m == -INFINITY ? 0.f : fast_exp2(weight[p][tid] - m);
+      weight[p][tid] = w;
+      l += w * sums[p][tid];
+    }
+    row_m[tid] = m;
+    row_l[tid] = l;
+  }
+  named_sync(1, kT);
+#pragma unroll
+  for (int q = 0; q < D / 32; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const float4* s = reinterpret_cast<const float4*>(slot(p));
+#pragma unroll
+    for (int q = 0; q < D / 32; ++q) {
+      const float4 v = __ldcg(s + q * kT + tid);
+      const float w = weight[p][(q * kT + tid) / (D / 4)];
+      acc[q].x += w * v.x; acc[q].y += w * v.y; acc[q].z += w * v.z; acc[q].w += w * v.w;
+    }
+  }
+}
+
+template <int D, int ROWG, bool F16>
+__global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
+    kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const KvAttnArgs a) {
+  using S = KvShape<D, ROWG>;
+  constexpr int RT = S::kRows, kT = 32 * S::kWarps;
+  constexpr int kQuads = D / 64;  // 16-byte loads of a key per thread
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  float* merge = reinterpret_cast<float*>(smem + S::kStages * 2 * S::kTileBytes);
+  __shared__ uint64_t full_bar[S::kStages], empty_bar[S::kStages];
+  __shared__ KvPageScale page_scale[S::kStages][4];
+  __shared__ int64_t prefix[S::kThreads + 1];
+  __shared__ KvStart start;
+  __shared__ float warp_m[S::kWarps][16], warp_l[S::kWarps][16];
+  __shared__ float weight[kKvMaxBlocks / kKvJoin][RT], sums[kKvMaxBlocks / kKvJoin][RT], row_m[RT], row_l[RT];
+  __shared__ volatile uint32_t abort_flag, fills, last_flag, go_on;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], S::kWarps);
+    }
+    abort_flag = 0u;
+    fills = 0u;
+    fence_mbar_init();
+    prefetch_tensormap(&map_k);
+    prefetch_tensormap(&map_v);
+  }
   pdl_wait();
-  constexpr int N = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (unit >= a.total * a.heads) return;
-  const int64_t t = unit / a.heads;
-  const int h = static_cast<int>(unit % a.heads), kvh = h / (a.heads / a.kv_heads);
-  int lo = 0, hi = a.batch;  // the last b with offsets[b] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.offsets[mid] <= t) lo = mid; else hi = mid;
-  }
-  const int b = lo;
-  if (t < a.offsets[b] || t >= a.offsets[b + 1]) return;
-  const int64_t n = a.offsets[b + 1] - a.offsets[b];
-  int64_t len = a.lens[b];
-  if (len < 0 || len > static_cast<int64_t>(a.table_width) * a.page) {
-    if (lane == 0) record_error_at(a.err, kErrValue);
-    len = 0;
-  }
-  const int64_t pos = len - n + (t - a.offsets[b]);
-  const int64_t last = a.causal ? min(len, pos + 1) : len;
-  const int64_t first = a.window > 0 ? max(int64_t{0}, pos - a.window + 1) : 0;
-  float q[N], o[N], m = -INFINITY, l = 0.f;
-  for (int i = 0; i < N; i += 2) {
-    const float2 x = elem2_to_f32x2<F16>(*reinterpret_cast<const uint32_t*>(a.q + t * a.q_tok + h * a.q_head + lane * N + i));
-    q[i] = x.x * a.scale_log2; q[i + 1] = x.y * a.scale_log2; o[i] = o[i + 1] = 0.f;
-  }
-  for (int64_t j = first; j < last; ++j) {
-    const int64_t pid = a.table[b * a.table_ld + j / a.page];
-    if (pid < 0 || pid >= a.num_pages) {
-      if (lane == 0) record_error_at(a.err, kErrValue);
-      continue;
+
+  // ---- every sequence's units, and this block's run
+  {
+    const int per = (a.batch + S::kThreads - 1) / S::kThreads;
+    const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += kv_seq_units<RT>(a, kv_seq<RT>(a, b, blockIdx.x == 0)) * a.kv_heads;
+    prefix[tid + 1] = mine;
+    if (tid == 0) prefix[0] = 0;
+    __syncthreads();
+    if (warp == 0) {  // inclusive sums, 32 at a time
+      int64_t carry = 0;
+      for (int i = 0; i < S::kThreads; i += 32) {
+        int64_t v = prefix[1 + i + lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int64_t o = __shfl_up_sync(~0u, v, d);
+          if (lane >= d) v += o;
+        }
+        prefix[1 + i + lane] = carry + v;
+        carry += __shfl_sync(~0u, v, 31);
+      }
     }
-    const int64_t at = pid * a.cs_page + kvh * a.cs_head + (j % a.page) * a.cs_tok + lane * N;
-    const float ks = pow2f(a.scales[0][pid * a.kv_heads + kvh] - 127), vs = pow2f(a.scales[1][pid * a.kv_heads + kvh] - 127);
-    float s = 0.f;
-    for (int i = 0; i < N; i += 2) {
-      const float2 k = f16x2_to_f32x2(e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(a.cache[0] + at + i)));
-      s += q[i] * k.x + q[i + 1] * k.y;
+    __syncthreads();
+    const int64_t total = prefix[S::kThreads], parts = min(total, static_cast<int64_t>(gridDim.x));
+    if (blockIdx.x >= parts) return;  // the whole block
+    const int64_t begin = total * blockIdx.x / parts;
+    if (prefix[tid] <= begin && begin < prefix[tid + 1]) {
+      int64_t before = prefix[tid];
+      int b = b0;
+      while (true) {
+        const int64_t c = kv_seq_units<RT>(a, kv_seq<RT>(a, b, false)) * a.kv_heads;
+        if (begin < before + c) break;
+        before += c;
+        ++b;
+      }
+      start = {total, before, b};
     }
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    s *= ks;
-    const float m2 = fmaxf(m, s), c = exp2f(m - m2), p = exp2f(s - m2);
-    m = m2;
-    l = l * c + p;
-    for (int i = 0; i < N; i += 2) {
-      const float2 v = f16x2_to_f32x2(e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(a.cache[1] + at + i)));
-      o[i] = o[i] * c + p * vs * v.x;
-      o[i + 1] = o[i + 1] * c + p * vs * v.y;
-    }
+    __syncthreads();
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  for (int i = 0; i < N; i += 2)
-    *reinterpret_cast<uint32_t*>(a.out + (t * a.heads + h) * D + lane * N + i) = f32x2_to_elem2<F16>(o[i] * inv, o[i + 1] * inv);
-  if (lane == 0 && a.lse) a.lse[t * a.heads + h] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  const int64_t total = start.total, parts = min(total, static_cast<int64_t>(gridDim.x));
+  KvWalk<RT> walk;
+  walk.u = total * blockIdx.x / parts;
+  walk.end = total * (blockIdx.x + 1) / parts;
+  walk.before = start.before;
+  walk.b = start.seq;
+  walk.load(a);
+  KvSegment g;
+
+  if (warp == S::kWarps) {
+    // ---- producer
+    uint32_t stage = 0, phase = 0, n = 0;
+    const int box = min(a.page, kKvTile), boxes = kKvTile / box;
+    bool ok = true;
+    while (ok && walk.next(a, g)) {
+      const int32_t* table = a.table + static_cast<int64_t>(g.b) * a.table_ld;
+      const int pages = (g.hi + a.page - 1) >> a.page_shift;  // beyond these no entry is read
+      int batch0 = -1, pid = -1;
+      KvPageScale sc{};
+      for (int t = g.tile0; t < g.tile1; ++t) {
+        const int pg0 = (t * kKvTile) >> a.page_shift;
+        if (batch0 < 0 || pg0 + boxes > batch0 + 32) {  // the next 32 pages' ids and scales, one per lane
+          batch0 = pg0;
+          const int pg = pg0 + lane;
+          pid = pg < pages ? table[pg] : -1;
+          const bool valid = pid >= 0 && pid < a.num_pages;
+          // pages before the first allowed key are masked anyway and need no entry
+          if (pg < pages && !valid && (pg + 1) << a.page_shift > g.lo) record_error_at(a.err, kErrValue);
+          sc = {0.f, -INFINITY, 0.f};
+          if (valid) {
+            const int64_t at = static_cast<int64_t>(pid) * a.kv_heads + g.head;
+            const int ek = a.scales[0][at], ev = a.scales[1][at];
+            sc.kfac = pow2f(min(max(ek - 127, -126), 127));
+            sc.ev = static_cast<float>(ev - 127);
+            sc.inv = pow2f(min(max(127 - ev, -126), 127));
+          } else {
+            pid = -1;
+          }
+        }
+        if (lane == 0) ok = mbar_wait_bounded(&empty_bar[stage], phase ^ 1u) && abort_flag == 0u;
+        ok = __shfl_sync(~0u, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        const int first = pg0 - batch0;
+        if (lane >= first && lane < first + boxes) page_scale[stage][lane - first] = sc;
+        const uint32_t got = __ballot_sync(~0u, pid >= 0) >> first & ((1u << boxes) - 1u);
+        __syncwarp();
+        uint8_t* kd = smem + stage * 2 * S::kTileBytes;
+        if (lane == 0) mbar_arrive_expect_tx(&full_bar[stage], 2u * __popc(got) * box * D);
+        for (int i = 0; i < boxes; ++i) {
+          const int id = __shfl_sync(~0u, pid, first + i);
+          if (lane == 0 && id >= 0) {
+            const int y = (t * kKvTile + i * box) & (a.page - 1);
+            tma_load_4d(kd + i * box * D, &map_k, 0, y, g.head, id, &full_bar[stage]);
+            tma_load_4d(kd + S::kTileBytes + i * box * D, &map_v, 0, y, g.head, id, &full_bar[stage]);
+          }
+        }
+        ++n;
+        if (lane == 0) fills = n;
+        if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
+      }
+    }
+    if (!ok && lane == 0) {
+      if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
+      abort_flag = 1u;
+    }
+  } else {
+    // ---- consumers: warp w takes keys 16 (w % 4) .. + 15 of each tile for rows 16 (w / 4) .. + 15
+    const int gq = lane >> 2, c = lane & 3, kw = warp & 3, rg = warp >> 2;
+    uint32_t stage = 0, phase = 0, used = 0;
+    bool ok = true;
+    while (ok && walk.next(a, g)) {
+      const int rows = g.s.n * a.group, pos0 = g.s.len - g.s.n;
+      int pos[2];       // positions of this thread's two rows
+      float rowfac[2];  // sm_scale log2(e) 2^eq
+      uint32_t q[2][D / 8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = g.rt * RT + rg * 16 + gq + 8 * h;
+        pos[h] = pos0 + r / a.group;
+        float amax = 0.f;
+        uint4 v[D / 32];
+        const uint16_t* src = a.q + (g.s.t0 + r / a.group) * a.q_tok + (g.head * a.group + r % a.group) * a.q_head + c * (D / 4);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          v[i] = r < rows ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+          uint32_t m = 0;
+          m = elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(m, v[i].x), v[i].y), v[i].z), v[i].w);
+          amax = fmaxf(amax, elem_absmax_final<F16>(m));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
+        // the row times 2^-eq has its largest magnitude in [2^12, 2^13)
+        const int eq = amax > 0.f ? static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 12 : 0;
+        const float f = pow2f(min(max(-eq, -126), 127));
+        rowfac[h] = a.scale_log2 * pow2f(min(max(eq, -126), 127));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = elem2_to_f32x2<F16>(w[j]);
+            q[h][4 * i + j] = f32x2_to_elem2<true>(x.x * f, x.y * f);
+          }
+        }
+      }
+      float o[D / 8][4];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+      for (int t = g.tile0; t < g.tile1; ++t) {
+        ok = __all_sync(~0u, mbar_wait_bounded(&full_bar[stage], phase) && abort_flag == 0u);
+        if (!ok) break;
+        const uint8_t* kd = smem + stage * 2 * S::kTileBytes;
+        const uint8_t* vd = kd + S::kTileBytes;
+        const KvPageScale ps = page_scale[stage][(16 * kw) >> min(a.page_shift, 6)];
+        float s[2][4];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+          s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+          const int r = 16 * kw + 8 * nb + gq;
+#pragma unroll
+          for (int j = 0; j < kQuads; ++j) {
+            const uint4 w = *reinterpret_cast<const uint4*>(kd + kv_chunk<D>(r, kQuads * c + j));
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int k = 4 * j + i;  // K slice: dimensions c D/4 + 4 k .. + 3
+              kv_mma(s[nb], q[0][2 * k], q[1][2 * k], q[0][2 * k + 1], q[1][2 * k + 1], e4m3x2_to_f16x2(x[i] & 0xFFFFu),
+                     e4m3x2_to_f16x2(x[i] >> 16));
+            }
+          }
+        }
+        const int key0 = t * kKvTile + 16 * kw;
+        // keys that not all rows see, or none: only tiles at the range's ends
+        const bool edge = ps.inv == 0.f || key0 < g.lo || key0 + 16 > g.hi || (a.causal && key0 + 15 > pos0 + g.rt * RT / a.group) ||
+                          (a.window > 0 && key0 <= pos0 + (min(rows, (g.rt + 1) * RT) - 1) / a.group - a.window);
+        float top[2] = {-INFINITY, -INFINITY};
+        const float f0 = rowfac[0] * ps.kfac, f1 = rowfac[1] * ps.kfac;
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int h = i >> 1;
+            float x = s[nb][i] * (h ? f1 : f0) + ps.ev;
+            if (edge) {
+              const int key = key0 + 8 * nb + 2 * c + (i & 1);
+              const bool see = ps.inv != 0.f && key >= g.lo && key < g.hi && (!a.causal || key <= pos[h]) && (a.window <= 0 || key > pos[h] - a.window);
+              x = see ? x : -INFINITY;
+            }
+            s[nb][i] = x;
+            top[h] = fmaxf(top[h], x);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 1));
+          top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 2));
+        }
+        if (__any_sync(~0u, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float mn = fmaxf(m[h], top[h]);
+            const float f = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - mn);
+            m[h] = mn;
+            l[h] *= f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              o[i][2 * h] *= f;
+              o[i][2 * h + 1] *= f;
+            }
+          }
+        }
+        const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
+        uint32_t p[2][2];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+          const float a0 = fast_exp2(s[nb][0] - m0), a1 = fast_exp2(s[nb][1] - m0);
+          const float b0 = fast_exp2(s[nb][2] - m1), b1 = fast_exp2(s[nb][3] - m1);
+          l[0] += (a0 + a1) * ps.inv;
+          l[1] += (b0 + b1) * ps.inv;
+          p[nb][0] = f32x2_to_elem2<true>(a0, a1);
+          p[nb][1] = f32x2_to_elem2<true>(b0, b1);
+        }
+        // values: keys 2c, 2c + 1 and 8 + 2c, 9 + 2c; this thread's dimensions D/8 gq ..
+        uint32_t vw[4][D / 32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = 16 * kw + 8 * (k >> 1) + 2 * c + (k & 1);
+          if constexpr (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4*>(vd + kv_chunk<D>(r, gq));
+            vw[k][0] = w.x; vw[k][1] = w.y; vw[k][2] = w.z; vw[k][3] = w.w;
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(vd + kv_chunk<D>(r, gq >> 1) + 8 * (gq & 1));
+            vw[k][0] = w.x; vw[k][1] = w.y;
+          }
+          if (edge) {  // whatever lies outside the allowed keys (NaN codes too) counts as zero
+            const int key = t * kKvTile + r;
+            if (key < g.lo || key >= g.hi || ps.inv == 0.f) {
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i) vw[k][i] = 0u;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t lo[4], hi[4];
+          kv_pairs(vw[0][i], vw[1][i], lo);
+          kv_pairs(vw[2][i], vw[3][i], hi);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) kv_mma(o[4 * i + j], p[0][0], p[0][1], p[1][0], p[1][1], lo[j], hi[j]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty_bar[stage]);
+        ++used;
+        if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok && lane == 0) {
+        if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
+        abort_flag = 1u;
+      }
+      // ---- the item's share: the four key quarters of each row group meet
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(~0u, l[h], 1);
+        l[h] += __shfl_xor_sync(~0u, l[h], 2);
+        if (c == 0) {
+          warp_m[warp][gq + 8 * h] = m[h];
+          warp_l[warp][gq + 8 * h] = l[h];
+        }
+      }
+      named_sync(1, kT);
+      if (tid == 0) go_on = abort_flag == 0u ? 1u : 0u;  // one answer for all warps
+      float* mw = merge + warp * 16 * D;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = gq + 8 * h;
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mm = fmaxf(mm, warp_m[4 * rg + w][r]);
+        const float f = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - mm);
+        // columns 2c (first half) and 2c + 1 (second) of every product: D/4 consecutive dimensions
+#pragma unroll
+        for (int i = 0; i < D / 8; i += 4) {
+          float4* dst = reinterpret_cast<float4*>(mw + r * D + c * (D / 4) + i);
+          dst[0] = make_float4(o[i][2 * h] * f, o[i + 1][2 * h] * f, o[i + 2][2 * h] * f, o[i + 3][2 * h] * f);
+          dst[D / 32] = make_float4(o[i][2 * h + 1] * f, o[i + 1][2 * h + 1] * f, o[i + 2][2 * h + 1] * f, o[i + 3][2 * h + 1] * f);
+        }
+        if (kw == 0 && c == 0) {
+          float ll = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float wm = warp_m[4 * rg + w][r];
+            ll += warp_l[4 * rg + w][r] * (wm == -INFINITY ? 0.f : fast_exp2(wm - mm));
+          }
+          row_m[rg * 16 + r] = mm;
+          row_l[rg * 16 + r] = ll;
+        }
+      }
+      named_sync(1, kT);
+      ok = go_on != 0u;
+      float4 acc[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int at = i * kT + tid, r = at / (D / 4), d4 = at % (D / 4);
+        const float4* src = reinterpret_cast<const float4*>(merge + (r >> 4) * 64 * D + (r & 15) * D) + d4;
+        const float4 x = src[0], y = src[4 * D], z = src[8 * D], w = src[12 * D];  // 16 D floats apart
+        acc[i] = make_float4((x.x + y.x) + (z.x + w.x), (x.y + y.y) + (z.y + w.y), (x.z + y.z) + (z.z + w.z), (x.w + y.w) + (z.w + w.w));
+      }
+      const int64_t u0 = g.first, u1 = g.first + g.count - 1;
+      const int own0 = static_cast<int>(((u0 + 1) * parts - 1) / total), own1 = static_cast<int>(((u1 + 1) * parts - 1) / total);
+      bool write = own0 == own1 && ok;
+      if (own0 != own1) {
+        const int count = own1 - own0 + 1, groups = (count + kKvJoin - 1) / kKvJoin, me = static_cast<int>(blockIdx.x) - own0;
+        // a run begins inside at most one item (slot 0) and ends inside one (slot 1)
+        auto slot = [&](int p) { return a.part + (static_cast<int64_t>(own0 + p) * 2 + (p == 0 ? 1 : 0)) * S::kPartFloats; };
+        auto put = [&](int p) {
+          float* dst = slot(p);
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) __stcg(reinterpret_cast<float4*>(dst) + i * kT + tid, acc[i]);
+          if (tid < RT) {
+            __stcg(dst + RT * D + tid, row_m[tid]);
+            __stcg(dst + RT * D + RT + tid, row_l[tid]);
+          }
+          __threadfence();
+          named_sync(1, kT);
+        };
+        auto arrive = [&](uint32_t* counter, int of) {  // true for the last of `of`
+          if (tid == 0) {
+            const bool last = ok && atomicAdd(counter, 1u) == static_cast<uint32_t>(of) - 1u;
+            if (last) *counter = 0u;
+            __threadfence();
+            last_flag = last ? 1u : 0u;
+          }
+          named_sync(1, kT);
+          const bool last = last_flag != 0u;
+          named_sync(1, kT);
+          return last;
+        };
+        put(me);
+        const int gi = me / kKvJoin, gsize = min(kKvJoin, count - gi * kKvJoin);
+        if (arrive(a.counters + own0 + gi * kKvJoin, gsize)) {
+          kv_join<D, ROWG>(gsize, [&](int p) { return slot(gi * kKvJoin + p); }, tid, weight, sums, row_m, row_l, acc);
+          write = true;
+          if (groups > 1) {
+            put(gi * kKvJoin);  // each thread overwrites what it alone has read
+            write = arrive(a.counters + kKvMaxBlocks + own0, groups);
+            if (write) kv_join<D, ROWG>(groups, [&](int p) { return slot(p * kKvJoin); }, tid, weight, sums, row_m, row_l, acc);
+          }
+        }
+      }
+      if (write) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const int at = i * kT + tid, r = at / (D / 4), d = at % (D / 4) * 4, rr = g.rt * RT + r;
+          if (rr < rows) {
+            const float lr = row_l[r], f = lr > 0.f ? 1.f / lr : 0.f;
+            uint16_t* dst = a.out + (static_cast<int64_t>(g.s.t0 + rr / a.group) * a.heads + g.head * a.group + rr % a.group) * D + d;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(f32x2_to_elem2<F16>(acc[i].x * f, acc[i].y * f), f32x2_to_elem2<F16>(acc[i].z * f, acc[i].w * f));
+          }
+        }
+        if (a.lse != nullptr && tid < RT && g.rt * RT + tid < rows) {
+          const int rr = g.rt * RT + tid;
+          a.lse[static_cast<int64_t>(g.s.t0 + rr / a.group) * a.heads + g.head * a.group + rr % a.group] =
+              row_l[tid] > 0.f ? (row_m[tid] + log2f(row_l[tid])) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+      named_sync(1, kT);  // row_m, row_l and merge are written again
+    }
+    if (tid == 0) last_flag = used;
+  }
+  __syncthreads();
+  // after an expired wait: loads that nothing consumed land before the block ends
+  if (tid == 0)
+    for (uint32_t f = last_flag; f < fills; ++f)
+      if (!mbar_wait_bounded(&full_bar[f % S::kStages], (f / S::kStages) & 1u)) record_error_at(a.err, kErrTimeout);
 }
 
 }  // namespace bsq

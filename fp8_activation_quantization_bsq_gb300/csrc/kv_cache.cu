@@ -19,11 +19,12 @@ bsq_status check_cache(int32_t dtype, int64_t total, int32_t kv_heads, int32_t d
                        const int32_t* lens, int32_t batch) {
   if (dtype != BSQ_BF16 && dtype != BSQ_F16) return BSQ_ERR_VALUE;
   if (total < 0 || total >= (int64_t(1) << 31) || batch < 0 || kv_heads < 1 || kv_heads > 1024 || (dim != 64 && dim != 128) ||
-      num_pages < 0 || num_pages >= (int64_t(1) << 31) || (page != 16 && page != 32 && page != 64 && page != 128) ||
-      table_width < 0 || (batch > 1 && table_ld < table_width) || cs_tok < dim || cs_page < 0 || cs_head < 0)
+      num_pages < 1 || num_pages >= (int64_t(1) << 31) || (page != 16 && page != 32 && page != 64 && page != 128) ||
+      table_width < 0 || (batch > 1 && table_ld < table_width) || cs_tok < dim || cs_page < 0 || cs_head < 0 ||
+      cs_tok >= (int64_t(1) << 32) || cs_head >= (int64_t(1) << 38) || cs_page >= (int64_t(1) << 38))
     return BSQ_ERR_SHAPE;
   if (total == 0 || batch == 0) return BSQ_OK;
-  if (!table || !offsets || !lens || (num_pages > 0 && (!k_cache || !v_cache || !k_scales || !v_scales))) return BSQ_ERR_NULL;
+  if (!table || !offsets || !lens || !k_cache || !v_cache || !k_scales || !v_scales) return BSQ_ERR_NULL;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || cs_page % 16 != 0 || cs_head % 16 != 0 || cs_tok % 16 != 0 ||
       tok_stride % 8 != 0 || head_stride % 8 != 0 || !aligned(table, 4) || !aligned(offsets, 4) || !aligned(lens, 4))
     return BSQ_ERR_ALIGN;
@@ -40,6 +41,41 @@ cudaError_t launch_append(const KvAppendArgs& a, cudaStream_t st) {
     case 8: return launch_pdl(kv_append_kernel<D, 8, F16>, grid, dim3(kKvAppendThreads), 0, st, a);
     default: return launch_pdl(kv_append_kernel<D, 16, F16>, grid, dim3(kKvAppendThreads), 0, st, a);
   }
+}
+
+// The cache as a 4D tensor of bytes (dimension, token, head, page), in boxes
+// of a head's tokens, at most a tile of them.
+bool cache_map(CUtensorMap* map, const void* ptr, int dim, int page, int heads, int64_t pages, int64_t cs_tok, int64_t cs_head,
+               int64_t cs_page) {
+  auto enc = encode_tiled();
+  if (!enc) return false;
+  // the stride of an extent of one is never used, but has to be valid
+  if (heads == 1) cs_head = cs_tok * page;
+  if (pages == 1) cs_page = cs_tok * page;
+  const cuuint64_t size[4] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(pages)};
+  const cuuint64_t stride[3] = {static_cast<cuuint64_t>(cs_tok), static_cast<cuuint64_t>(cs_head), static_cast<cuuint64_t>(cs_page)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(dim), static_cast<cuuint32_t>(std::min(page, kKvTile)), 1, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), size, stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int ROWG, bool F16>
+bsq_status launch_attention(const KvAttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, const HostDevice& d,
+                            cudaStream_t st) {
+  using S = KvShape<D, ROWG>;
+  auto kernel = kv_attention_kernel<D, ROWG, F16>;
+  if (bsq_status s = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem, d.index); s != BSQ_OK) return s;
+  const int grid = ROWG == 1 ? std::min(2 * d.sm_count, kKvMaxBlocks) : std::min(d.sm_count, kKvMaxBlocks / 2);
+  return launch_pdl(kernel, dim3(grid), dim3(S::kThreads), S::kSmem, st, mk, mv, a) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
+}
+
+template <int D, bool F16>
+bsq_status launch_attention_rows(const KvAttnArgs& a, int64_t max_rows, const CUtensorMap& mk, const CUtensorMap& mv,
+                                 const HostDevice& d, cudaStream_t st) {
+  return max_rows <= 16 ? launch_attention<D, 1, F16>(a, mk, mv, d, st) : launch_attention<D, 2, F16>(a, mk, mv, d, st);
 }
 
 }  // namespace
@@ -96,7 +132,8 @@ int64_t bsq_kv_attention_workspace_bytes(int64_t total, int32_t heads, int32_t k
                                          int32_t max_q) {
   if (total < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || (dim != 64 && dim != 128) || batch < 0 || max_q < 0)
     return 0;
-  return 16;
+  // a slot of 16 or 32 rows for each end of every block's run, whichever kernel runs
+  return kKvCounterBytes + int64_t(kKvMaxBlocks) * 2 * KvShape<128, 1>::kPartFloats * 4;
 }
 
 int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t heads, int32_t kv_heads, int32_t dim,
@@ -123,11 +160,6 @@ int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t he
   a.q = static_cast<const uint16_t*>(q);
   a.q_tok = q_tok;
   a.q_head = q_head;
-  a.cache[0] = static_cast<const uint8_t*>(k_cache);
-  a.cache[1] = static_cast<const uint8_t*>(v_cache);
-  a.cs_page = cs_page;
-  a.cs_head = cs_head;
-  a.cs_tok = cs_tok;
   a.scales[0] = static_cast<const uint8_t*>(k_scales);
   a.scales[1] = static_cast<const uint8_t*>(v_scales);
   a.table = table;
@@ -141,22 +173,27 @@ int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t he
   a.batch = batch;
   a.heads = heads;
   a.kv_heads = kv_heads;
+  a.group = heads / kv_heads;
   a.page = page;
+  a.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
   a.table_width = table_width;
   a.causal = causal;
   a.window = window;
   a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.counters = static_cast<uint32_t*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKvCounterBytes);
   a.err = d.error_word;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(ceil_div(total * heads, 4)));
-  cudaError_t e;
+  CUtensorMap mk, mv;
+  if (!cache_map(&mk, k_cache, dim, page, kv_heads, num_pages, cs_tok, cs_head, cs_page) ||
+      !cache_map(&mv, v_cache, dim, page, kv_heads, num_pages, cs_tok, cs_head, cs_page))
+    return BSQ_ERR_CUDA;
+  const int64_t max_rows = static_cast<int64_t>(max_q) * a.group;
   if (dim == 64)
-    e = dtype == BSQ_F16 ? launch_pdl(kv_attention_kernel<64, true>, grid, dim3(128), 0, st, a)
-                         : launch_pdl(kv_attention_kernel<64, false>, grid, dim3(128), 0, st, a);
-  else
-    e = dtype == BSQ_F16 ? launch_pdl(kv_attention_kernel<128, true>, grid, dim3(128), 0, st, a)
-                         : launch_pdl(kv_attention_kernel<128, false>, grid, dim3(128), 0, st, a);
-  return e == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
+    return dtype == BSQ_F16 ? launch_attention_rows<64, true>(a, max_rows, mk, mv, d, st)
+                            : launch_attention_rows<64, false>(a, max_rows, mk, mv, d, st);
+  return dtype == BSQ_F16 ? launch_attention_rows<128, true>(a, max_rows, mk, mv, d, st)
+                          : launch_attention_rows<128, false>(a, max_rows, mk, mv, d, st);
 }
 
 }  // extern "C"

@@ -1,7 +1,6 @@
 // Host side of the few-token mixture-of-experts layer (bsq_moe_layer):
 // argument checks, the workspace's layout, tensor maps and the cooperative launch.
 #include <algorithm>
-#include <mutex>
 
 #include "host_common.h"
 #include "moe_layer.cuh"
@@ -55,36 +54,13 @@ bool moe_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t row_bytes,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct MoeDevice {
-  bool ready = false;
-  int max_smem = 0;
-};
-std::mutex g_moe_mu;
-MoeDevice g_moe_devices[64];
-
-bsq_status moe_device(int index, int* max_smem) {
-  std::lock_guard<std::mutex> lock(g_moe_mu);
-  MoeDevice& d = g_moe_devices[index];
-  if (!d.ready) {
-    int optin = 0;
-    cudaFuncAttributes fa;
-    if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, index) != cudaSuccess ||
-        cudaFuncGetAttributes(&fa, moe_layer_kernel<kNVFP4>) != cudaSuccess)
-      return BSQ_ERR_CUDA;
-    const int most = optin - static_cast<int>(fa.sharedSizeBytes);  // the kernels' static part is the same for all formats
-    if (cudaFuncSetAttribute(moe_layer_kernel<kNVFP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-        cudaFuncSetAttribute(moe_layer_kernel<kMXFP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-        cudaFuncSetAttribute(moe_layer_kernel<kMXFP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
-      return BSQ_ERR_CUDA;
-    d.max_smem = most;
-    d.ready = true;
-  }
-  *max_smem = d.max_smem;
-  return BSQ_OK;
-}
+// Dynamic shared memory of the layer's block: what the SM allows less the kernel's static tables.
+constexpr int kMoeDynamicSmem = 227 * 1024 - 1024;
 
 template <int FMT>
-bsq_status launch_moe(MoeArgs& a, const void* w13, const void* w2, const HostDevice& d, int max_smem, cudaStream_t st) {
+bsq_status launch_moe(MoeArgs& a, const void* w13, const void* w2, const HostDevice& d, cudaStream_t st) {
+  if (bsq_status s = allow_smem(reinterpret_cast<const void*>(moe_layer_kernel<FMT>), kMoeDynamicSmem, d.index); s != BSQ_OK)
+    return s;
   const int64_t pairs = static_cast<int64_t>(a.tokens) * a.top_k;
   CUtensorMap m13, m2, mx, mh;
   if (!moe_map(&m13, w13, static_cast<int64_t>(a.experts) * 2 * a.inter, row_bytes_of(FMT, a.hidden), 128) ||
@@ -94,7 +70,7 @@ bsq_status launch_moe(MoeArgs& a, const void* w13, const void* w2, const HostDev
   a.max_n = static_cast<int>(ceil_div(a.tokens, 16) * 16);
   a.stage_bytes = static_cast<int>(ceil_div(2 * kMoeHalfBytes + a.max_n * 128 + 3 * MoeFmt<FMT>::kAtoms * 512, 1024) * 1024);
   const int tables = moe_table_bytes(a.experts, static_cast<int>(pairs));
-  a.stages = std::min(8, (max_smem - 1024 - tables) / a.stage_bytes);
+  a.stages = std::min(8, (kMoeDynamicSmem - 1024 - tables) / a.stage_bytes);
   if (a.stages < 2) return BSQ_ERR_SHAPE;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(std::min(d.sm_count, kMoeMaxBlocks));
@@ -138,8 +114,6 @@ int32_t bsq_moe_layer(int32_t fmt, const void* x, int64_t ld_x, const float* log
   if (workspace_bytes < w.bytes) return BSQ_ERR_SHAPE;
   HostDevice d;
   if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
-  int max_smem = 0;
-  if (bsq_status s = moe_device(d.index, &max_smem); s != BSQ_OK) return s;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   MoeArgs a{};
   a.x = static_cast<const uint16_t*>(x);
@@ -170,9 +144,9 @@ int32_t bsq_moe_layer(int32_t fmt, const void* x, int64_t ld_x, const float* log
   a.err = d.error_word;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (fmt) {
-    case BSQ_NVFP4: return launch_moe<kNVFP4>(a, w13, w2, d, max_smem, st);
-    case BSQ_MXFP4: return launch_moe<kMXFP4>(a, w13, w2, d, max_smem, st);
-    default: return launch_moe<kMXFP8>(a, w13, w2, d, max_smem, st);
+    case BSQ_NVFP4: return launch_moe<kNVFP4>(a, w13, w2, d, st);
+    case BSQ_MXFP4: return launch_moe<kMXFP4>(a, w13, w2, d, st);
+    default: return launch_moe<kMXFP8>(a, w13, w2, d, st);
   }
 }
 
