@@ -10,8 +10,8 @@ namespace {
 using namespace bsq;
 
 bool moe_sizes_ok(int32_t tokens, int64_t hidden, int64_t inter, int32_t experts, int32_t top_k) {
-  return tokens >= 0 && tokens <= kMoeMaxTokens && hidden >= 32 && hidden % 32 == 0 && hidden <= (1 << 20) && inter >= 128 &&
-         inter % 128 == 0 && inter <= (1 << 20) && experts >= 1 && experts <= kMoeMaxExperts && top_k >= 1 &&
+  return tokens >= 0 && tokens <= kMoeMaxTokens && hidden >= 32 && hidden % 32 == 0 && hidden <= (1 << 16) && inter >= 128 &&
+         inter % 128 == 0 && inter <= (1 << 16) && experts >= 1 && experts <= kMoeMaxExperts && top_k >= 1 &&
          top_k <= kMoeMaxTopK && top_k <= experts && experts * std::max(2 * inter, hidden) < (int64_t(1) << 31);
 }
 

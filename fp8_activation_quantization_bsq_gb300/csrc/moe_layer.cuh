@@ -88,33 +88,32 @@ __host__ __device__ inline int moe_table_bytes(int experts, int pairs) {
 }
 
 // A phase's units, cut into `parts` runs of equal length, none empty: block b
-// takes run b.
+// takes run b.  The host's size limits keep units below 2^31.
 struct MoePhase {
-  int64_t units;
+  int units;
   int tiles;   // per expert
   int chunks;  // stages per tile
   int parts;
+  int begin, end;  // this block's run
+  __device__ __forceinline__ int start_of(int part) const {
+    return static_cast<int>(static_cast<uint64_t>(units) * static_cast<uint32_t>(part) / static_cast<uint32_t>(parts));
+  }
+  // The block whose run holds unit u.
+  __device__ __forceinline__ int owner(int u) const {
+    return static_cast<int>((static_cast<uint64_t>(u + 1) * static_cast<uint32_t>(parts) - 1) / static_cast<uint32_t>(units));
+  }
 };
-struct MoeRun {
-  int64_t begin, end;
-};
-__device__ __forceinline__ MoeRun moe_run(const MoePhase& p, int block) {
-  if (block >= p.parts) return {0, 0};
-  return {p.units * block / p.parts, p.units * (block + 1) / p.parts};
-}
-// The block whose run holds unit u.
-__device__ __forceinline__ int moe_owner(const MoePhase& p, int64_t u) {
-  return static_cast<int>(((u + 1) * p.parts - 1) / p.units);
-}
 
 template <int FMT>
-__device__ __forceinline__ MoePhase moe_phase(const MoeArgs& a, int phase, int active, int blocks) {
+__device__ __forceinline__ MoePhase moe_phase(const MoeArgs& a, int phase, int active) {
   MoePhase p;
-  const int cols = phase == 0 ? a.hidden : a.inter;
+  const int cols = phase == 0 ? a.hidden : a.inter, block = blockIdx.x;
   p.tiles = phase == 0 ? a.inter / 128 : (a.hidden + 255) / 256;
   p.chunks = (cols + MoeFmt<FMT>::kElems - 1) / MoeFmt<FMT>::kElems;
-  p.units = static_cast<int64_t>(active) * p.tiles * p.chunks;
-  p.parts = static_cast<int>(min(p.units, static_cast<int64_t>(blocks)));
+  p.units = active * p.tiles * p.chunks;
+  p.parts = min(p.units, static_cast<int>(gridDim.x));
+  p.begin = block < p.parts ? p.start_of(block) : 0;
+  p.end = block < p.parts ? p.start_of(block + 1) : 0;
   return p;
 }
 
@@ -127,47 +126,61 @@ __device__ __forceinline__ float moe_unkey(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
-// Route token t with one warp: its choices and weights into the tables.
+// Route token t with one warp, its logits in registers (expert 32 i + lane
+// in key[i]): choices and weights into the tables.
+template <int NL>
 __device__ __forceinline__ void moe_route(const MoeArgs& a, const MoeTables& tb, int t, int lane) {
   const float* z = a.logits + t * a.ld_logits;
-  uint32_t best = 0;
-  int at = 0x7FFFFFFF;
+  uint32_t key[NL];
   bool nan = false;
-  for (int e = lane; e < a.experts; e += 32) {
-    const float v = z[e];
-    nan |= v != v;
-    const uint32_t k = moe_key(v);
-    if (at == 0x7FFFFFFF || k > best) { best = k; at = e; }
-  }
-  if (__any_sync(~0u, nan) && lane == 0 && blockIdx.x == 0) record_error_at(a.err, kErrValue);
-  const float top = moe_unkey(__reduce_max_sync(~0u, best));
-  float sum = 0.f;
-  for (int e = lane; e < a.experts; e += 32) sum += expf(moe_unkey(moe_key(z[e])) - top);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-  float chosen = 0.f, mine = 0.f;
+  for (int i = 0; i < NL; ++i) {
+    const int e = 32 * i + lane;
+    const float v = e < a.experts ? __ldg(z + e) : 0.f;
+    nan |= v != v;
+    key[i] = e < a.experts ? moe_key(v) : 0u;  // 0: none (every key of a logit is larger)
+  }
+  uint32_t best = 0;
+#pragma unroll
+  for (int i = 0; i < NL; ++i) best = max(best, key[i]);
+  uint32_t m = __reduce_max_sync(~0u, best);
+  const float top = moe_unkey(m);
+  if (__any_sync(~0u, nan) && lane == 0 && blockIdx.x == 0) record_error_at(a.err, kErrValue);
+  float sum = 0.f;
+  if (!a.renorm) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      if (key[i] != 0u) sum += expf(moe_unkey(key[i]) - top);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+  }
+  uint32_t mine = 0;  // key of choice `lane`
   for (int k = 0; k < a.top_k; ++k) {
-    const uint32_t m = __reduce_max_sync(~0u, at == 0x7FFFFFFF ? 0u : best);
-    const int id = static_cast<int>(__reduce_min_sync(~0u, at != 0x7FFFFFFF && best == m ? static_cast<uint32_t>(at) : 0x7FFFFFFFu));
-    const float p = top == -INFINITY ? 0.f : expf(moe_unkey(m) - top);
-    chosen += p;
-    if (lane == k) mine = p;
+    int at = 0x7FFFFFFF;
+#pragma unroll
+    for (int i = NL - 1; i >= 0; --i)
+      if (key[i] == m) at = 32 * i + lane;
+    const int id = static_cast<int>(__reduce_min_sync(~0u, static_cast<uint32_t>(at)));  // equal ones: the lowest expert
+    if (lane == k) mine = m;
     if (lane == 0) {
       tb.id[t * a.top_k + k] = id;
       atomicOr(reinterpret_cast<unsigned long long*>(&tb.mask[id]), 1ull << t);
     }
-    if (at == id) {  // the owner's next best: after (m, id) in the order (larger key, lower expert)
-      at = 0x7FFFFFFF;
-      uint32_t nb = 0;
-      for (int e = lane; e < a.experts; e += 32) {
-        const uint32_t key = moe_key(z[e]);
-        if ((key < m || (key == m && e > id)) && (at == 0x7FFFFFFF || key > nb)) { nb = key; at = e; }
-      }
-      best = nb;
+    best = 0;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      if (32 * i + lane == id) key[i] = 0u;
+      best = max(best, key[i]);
     }
+    m = __reduce_max_sync(~0u, best);
   }
-  const float by = a.renorm ? chosen : sum;
-  if (lane < a.top_k) tb.prob[t * a.top_k + lane] = top == -INFINITY ? 0.f : mine / by;
+  const float p = lane < a.top_k && top > -INFINITY ? expf(moe_unkey(mine) - top) : 0.f;
+  if (a.renorm) {
+    sum = p;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+  }
+  if (lane < a.top_k) tb.prob[t * a.top_k + lane] = top > -INFINITY ? p / sum : 0.f;
 }
 
 // Quantize 32 consecutive BF16 values (16 words): packed bytes and scale bytes.
@@ -207,6 +220,15 @@ __device__ __forceinline__ void moe_quant_block(const uint4 (&v)[4], float tsf, 
   }
 }
 
+// Block `w` of 32 columns of the (token, choice) pairs' rows of x.
+__device__ __forceinline__ void moe_load_x(const MoeArgs& a, int w, int total, int per_row, uint4 (&v)[4]) {
+  if (w >= total) return;
+  const int pair = w / per_row, c = w - pair * per_row;
+  const uint16_t* src = a.x + (pair / a.top_k) * a.ld_x + 32 * c;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = ld_global_nc_v4(src + 8 * q);
+}
+
 // This thread's h (row i of a warp's 32, one token) quantized with its
 // neighbours': blocks run along the lanes.  Every lane calls.
 template <int FMT>
@@ -235,13 +257,22 @@ __device__ __forceinline__ void moe_quant_lane(float h, float tsf, int lane, uin
   }
 }
 
+// Rows g and u of one token and this thread's row of the tile: h, quantized
+// with the warp's other rows.  Not inlined: one copy of it per format keeps
+// the epilogue small in the instruction cache, which a short call starts cold.
+template <int FMT>
+__device__ __noinline__ void moe_finish_h(float g, float u, float hsf, int lane, uint8_t* row_bytes, uint8_t* scale_word) {
+  const float h = __bfloat162float(__float2bfloat16_rn(g / (1.f + expf(-g)) * u));
+  moe_quant_lane<FMT>(h, hsf, lane, row_bytes, scale_word);
+}
+
 // Wait until a counter in global memory reaches `value`, for about a second.
 __device__ __forceinline__ bool moe_wait_count(const uint32_t* p, uint32_t value, const volatile uint32_t* abort_flag) {
   if (ld_acquire(p) >= value) return true;
   const uint64_t t0 = globaltimer_ns();
   while (ld_acquire(p) < value) {
     if (*abort_flag != 0u || globaltimer_ns() - t0 > kWaitLimitNs) return false;
-    __nanosleep(40);
+    __nanosleep(20);
   }
   return true;
 }
@@ -302,7 +333,16 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   if (warp == 1) t5_alloc(&tmem_slot, 512);
   for (int e = tid; e < a.experts; e += kMoeThreads) tb.mask[e] = 0;
   __syncthreads();
-  for (int t = warp; t < a.tokens; t += kMoeThreads / 32) moe_route(a, tb, t, lane);
+  // the first block of x that this thread will quantize is on its way while the tokens are routed
+  const int per_row = a.hidden / 32, quant_total = pairs * per_row, quant_step = blocks * 128;
+  int quant_at = block + blocks * (tid - 128);
+  uint4 xv[4];
+  if (warp >= 4) moe_load_x(a, quant_at, quant_total, per_row, xv);
+  if (a.experts <= 256) {
+    for (int t = warp; t < a.tokens; t += kMoeThreads / 32) moe_route<8>(a, tb, t, lane);
+  } else {
+    for (int t = warp; t < a.tokens; t += kMoeThreads / 32) moe_route<32>(a, tb, t, lane);
+  }
   __syncthreads();
   if (warp == 0) {  // active experts in increasing order, and their first rows
     int n = 0, rows = 0;
@@ -347,41 +387,40 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     if (lane == 0) {
       uint32_t stage = 0, phase_bit = 0, fills = 0;
       for (int phase = 0; phase < 2 && abort_flag == 0u; ++phase) {
-        const MoePhase p = moe_phase<FMT>(a, phase, active, blocks);
-        const MoeRun run = moe_run(p, block);
+        const MoePhase p = moe_phase<FMT>(a, phase, active);
         const int cols = phase == 0 ? a.hidden : a.inter, rows = phase == 0 ? 2 * a.inter : a.hidden;
         const int kt = (cols / kSF + 3) / 4;
         const int64_t scale_bytes = static_cast<int64_t>((rows + 127) / 128) * kt * 512;
         const uint8_t* scales = phase == 0 ? a.w13_s : a.w2_s;
         const CUtensorMap* map = phase == 0 ? &map_w13 : &map_w2;
-        int kc = static_cast<int>(run.begin % p.chunks);
-        int64_t item = run.begin / p.chunks;
-        for (int64_t u = run.begin; u < run.end; ++u) {
-          const int expert = tb.active[item / p.tiles], tile = static_cast<int>(item % p.tiles);
+        for (int u = p.begin; u < p.end && abort_flag == 0u;) {
+          const int item = u / p.chunks, stop = min(p.end, (item + 1) * p.chunks);
+          const int expert = tb.active[item / p.tiles], tile = item % p.tiles;
           const int r0 = phase == 0 ? 128 * tile : 256 * tile, r1 = phase == 0 ? a.inter + r0 : r0 + 128;
           const bool two = r1 < rows;
-          const int atoms = min(kAtoms, kt - kc * kAtoms);
-          if (!mbar_wait_bounded(&empty_bar[stage], phase_bit ^ 1u)) {
-            if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
-            abort_flag = 1u;
-            break;
+          const int y = expert * rows;
+          const uint8_t* s0 = scales + expert * scale_bytes + static_cast<int64_t>(r0 / 128) * kt * 512;
+          const uint8_t* s1 = scales + expert * scale_bytes + static_cast<int64_t>(r1 / 128) * kt * 512;
+          for (int kc = u - item * p.chunks; u < stop; ++u, ++kc) {
+            const int atoms = min(kAtoms, kt - kc * kAtoms);
+            if (!mbar_wait_bounded(&empty_bar[stage], phase_bit ^ 1u)) {
+              if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
+              abort_flag = 1u;
+            }
+            if (abort_flag != 0u) break;
+            uint8_t* st = smem + stage * a.stage_bytes;
+            uint8_t* sc = st + 2 * kMoeHalfBytes + a.max_n * 128;
+            uint64_t* bar = &full_bar[stage];
+            mbar_arrive_expect_tx(bar, (two ? 2 : 1) * (kMoeHalfBytes + atoms * 512));
+            tma_load_2d(st, map, kc * 128, y + r0, bar);
+            bulk_load(sc, s0 + kc * kAtoms * 512, atoms * 512, bar);
+            if (two) {
+              tma_load_2d(st + kMoeHalfBytes, map, kc * 128, y + r1, bar);
+              bulk_load(sc + kAtoms * 512, s1 + kc * kAtoms * 512, atoms * 512, bar);
+            }
+            fills_a = ++fills;
+            if (++stage == stages) { stage = 0; phase_bit ^= 1u; }
           }
-          if (abort_flag != 0u) break;
-          uint8_t* st = smem + stage * a.stage_bytes;
-          uint8_t* sc = st + 2 * kMoeHalfBytes + a.max_n * 128;
-          uint64_t* bar = &full_bar[stage];
-          mbar_arrive_expect_tx(bar, (two ? 2 : 1) * (kMoeHalfBytes + atoms * 512));
-          const int y = static_cast<int>(static_cast<int64_t>(expert) * rows);
-          const uint8_t* src = scales + expert * scale_bytes + static_cast<int64_t>(kc) * kAtoms * 512;
-          tma_load_2d(st, map, kc * 128, y + r0, bar);
-          bulk_load(sc, src + static_cast<int64_t>(r0 / 128) * kt * 512, atoms * 512, bar);
-          if (two) {
-            tma_load_2d(st + kMoeHalfBytes, map, kc * 128, y + r1, bar);
-            bulk_load(sc + kAtoms * 512, src + static_cast<int64_t>(r1 / 128) * kt * 512, atoms * 512, bar);
-          }
-          fills_a = ++fills;
-          if (++stage == stages) { stage = 0; phase_bit ^= 1u; }
-          if (++kc == p.chunks) { kc = 0; ++item; }
         }
       }
     }
@@ -391,37 +430,36 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       uint32_t stage = 0, phase_bit = 0, fills = 0;
       bool ok = true;
       for (int phase = 0; phase < 2 && ok; ++phase) {
-        const MoePhase p = moe_phase<FMT>(a, phase, active, blocks);
-        const MoeRun run = moe_run(p, block);
+        const MoePhase p = moe_phase<FMT>(a, phase, active);
         const int cols = phase == 0 ? a.hidden : a.inter, kt = (cols / kSF + 3) / 4;
         const CUtensorMap* map = phase == 0 ? &map_xq : &map_hq;
         const uint8_t* scales = phase == 0 ? a.xq_s : a.hq_s;
-        int kc = static_cast<int>(run.begin % p.chunks), ready = -1;
-        int64_t item = run.begin / p.chunks;
-        if (phase == 0 && run.begin < run.end) {
+        int ready = -1;
+        if (phase == 0 && p.begin < p.end) {
           ok = moe_wait_count(a.counters + kMoeBarQuant, blocks, &abort_flag);
           fence_async();
         }
-        for (int64_t u = run.begin; u < run.end && ok; ++u) {
-          const int i = static_cast<int>(item / p.tiles);
+        for (int u = p.begin; u < p.end && ok;) {
+          const int item = u / p.chunks, stop = min(p.end, (item + 1) * p.chunks), i = item / p.tiles;
           if (phase == 1 && ready != i) {  // every tile of this expert's h is there
             ok = moe_wait_count(a.counters + kMoeExpertDone + i, a.inter / 128, &abort_flag);
             fence_async();
             ready = i;
           }
-          if (ok) ok = mbar_wait_bounded(&empty_bar[stage], phase_bit ^ 1u) && abort_flag == 0u;
-          if (!ok) break;
           const int row = tb.row0[i], n8 = (tb.row0[i + 1] - row + 7) >> 3;
-          const int atoms = min(kAtoms, kt - kc * kAtoms);
-          uint8_t* st = smem + stage * a.stage_bytes + 2 * kMoeHalfBytes;
-          uint64_t* bar = &full_bar[stage];
-          mbar_arrive_expect_tx(bar, n8 * 1024 + atoms * 512);
-          for (int b = 0; b < n8; ++b) tma_load_2d(st + b * 1024, map, kc * 128, row + 8 * b, bar);
-          bulk_load(st + a.max_n * 128 + 2 * kAtoms * 512, scales + (static_cast<int64_t>(i) * kt + kc * kAtoms) * 512,
-                    atoms * 512, bar);
-          fills_b = ++fills;
-          if (++stage == stages) { stage = 0; phase_bit ^= 1u; }
-          if (++kc == p.chunks) { kc = 0; ++item; }
+          const uint8_t* s0 = scales + static_cast<int64_t>(i) * kt * 512;
+          for (int kc = u - item * p.chunks; u < stop && ok; ++u, ++kc) {
+            ok = mbar_wait_bounded(&empty_bar[stage], phase_bit ^ 1u) && abort_flag == 0u;
+            if (!ok) break;
+            const int atoms = min(kAtoms, kt - kc * kAtoms);
+            uint8_t* st = smem + stage * a.stage_bytes + 2 * kMoeHalfBytes;
+            uint64_t* bar = &full_bar[stage];
+            mbar_arrive_expect_tx(bar, n8 * 1024 + atoms * 512);
+            for (int b = 0; b < n8; ++b) tma_load_2d(st + b * 1024, map, kc * 128, row + 8 * b, bar);
+            bulk_load(st + a.max_n * 128 + 2 * kAtoms * 512, s0 + kc * kAtoms * 512, atoms * 512, bar);
+            fills_b = ++fills;
+            if (++stage == stages) { stage = 0; phase_bit ^= 1u; }
+          }
         }
       }
       if (!ok) {
@@ -435,19 +473,18 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       uint32_t stage = 0, phase_bit = 0, done = 0, seg = 0;
       bool ok = true;
       for (int phase = 0; phase < 2 && ok; ++phase) {
-        const MoePhase p = moe_phase<FMT>(a, phase, active, blocks);
-        const MoeRun run = moe_run(p, block);
+        const MoePhase p = moe_phase<FMT>(a, phase, active);
         const int cols = phase == 0 ? a.hidden : a.inter, rows = phase == 0 ? 2 * a.inter : a.hidden;
-        for (int64_t u = run.begin; u < run.end && ok; ++seg) {
-          const int64_t item = u / p.chunks, stop = min(run.end, (item + 1) * p.chunks);
-          const int i = static_cast<int>(item / p.tiles), tile = static_cast<int>(item % p.tiles);
+        for (int u = p.begin; u < p.end && ok; ++seg) {
+          const int item = u / p.chunks, stop = min(p.end, (item + 1) * p.chunks);
+          const int i = item / p.tiles, tile = item % p.tiles;
           const bool two = phase == 0 || 256 * tile + 128 < rows;
           const uint32_t n = (tb.row0[i + 1] - tb.row0[i] + 15) & ~15u;
           const uint32_t buf = seg & 1u, d = tmem + buf * 128u;
           if (!mbar_wait_bounded(&acc_empty[buf], ((seg >> 1) & 1u) ^ 1u) || abort_flag != 0u) { ok = false; break; }
           t5_fence_after();
-          for (uint32_t fresh = 0; u < stop; ++u) {
-            const int kc = static_cast<int>(u % p.chunks);
+          int kc = u - item * p.chunks;
+          for (uint32_t fresh = 0; u < stop; ++u, ++kc) {
             if (!mbar_wait_bounded(&full_bar[stage], phase_bit) || abort_flag != 0u) { ok = false; break; }
             t5_fence_after();
             const uint32_t st = smem_addr(smem + stage * a.stage_bytes);
@@ -490,39 +527,41 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     // ---- quantize the tokens' rows, a block of 32 columns per thread at a time
     const int et = tid - 128, quarter = warp & 3;
     {
-      const int per_row = a.hidden / 32, kt = (a.hidden / kSF + 3) / 4;
-      const int row_bytes = FMT == kMXFP8 ? a.hidden : a.hidden / 2;
-      for (int64_t w = static_cast<int64_t>(block) * 128 + et; w < static_cast<int64_t>(pairs) * per_row; w += blocks * 128) {
-        const int row = static_cast<int>(w / per_row), c = static_cast<int>(w % per_row);
-        const int pair = tb.pair_of[row], e = tb.id[pair], i = tb.index_of[e], r = row - tb.row0[i];
-        const uint16_t* src = a.x + (pair / a.top_k) * a.ld_x + 32 * c;
-        uint4 v[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = ld_global_nc_v4(src + 8 * q);
+      const int kt = (a.hidden / kSF + 3) / 4, row_bytes = FMT == kMXFP8 ? a.hidden : a.hidden / 2;
+      while (quant_at < quant_total) {
+        uint4 next[4];
+        moe_load_x(a, quant_at + quant_step, quant_total, per_row, next);
+        const int pair = quant_at / per_row, c = quant_at - pair * per_row, t = pair / a.top_k;
+        const int e = tb.id[pair], i = tb.index_of[e], r = __popcll(tb.mask[e] & ((1ull << t) - 1ull));
         const int s0 = 32 * c / kSF;  // first scale column
         uint8_t* word = a.xq_s + (static_cast<int64_t>(i) * kt + s0 / 4) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (s0 & 3);
-        moe_quant_block<FMT>(v, FMT == kNVFP4 ? a.x_sf[e] : 1.f, a.xq + static_cast<int64_t>(row) * row_bytes + 32 * c / (FMT == kMXFP8 ? 1 : 2),
-                             word);
+        moe_quant_block<FMT>(xv, FMT == kNVFP4 ? __ldg(a.x_sf + e) : 1.f,
+                             a.xq + static_cast<int64_t>(tb.row0[i] + r) * row_bytes + (FMT == kMXFP8 ? 32 * c : 16 * c), word);
         if (c == per_row - 1)  // the last atom's columns past the row: zero
           for (int s = s0 + 32 / kSF; s < 4 * kt; ++s) word[s - s0] = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) xv[q] = next[q];
+        quant_at += quant_step;
       }
-      fence_async();
-      __threadfence();
       named_sync(1, 128);
-      if (et == 0) atomicAdd(a.counters + kMoeBarQuant, 1u);
+      if (et == 0) atomic_add_acq_rel(a.counters + kMoeBarQuant, 1u);
     }
     // ---- finished accumulators
     uint32_t seg = 0;
     bool ok = true;
     for (int phase = 0; phase < 2 && ok; ++phase) {
-      const MoePhase p = moe_phase<FMT>(a, phase, active, blocks);
-      const MoeRun run = moe_run(p, block);
-      for (int64_t u = run.begin; u < run.end; ++seg) {
-        const int64_t item = u / p.chunks, first = item * p.chunks, stop = min(run.end, first + p.chunks);
-        const int i = static_cast<int>(item / p.tiles), tile = static_cast<int>(item % p.tiles), expert = tb.active[i];
+      const MoePhase p = moe_phase<FMT>(a, phase, active);
+      for (int u = p.begin; u < p.end; ++seg) {
+        const int item = u / p.chunks, first = item * p.chunks, stop = min(p.end, first + p.chunks);
+        const int i = item / p.tiles, tile = item % p.tiles, expert = tb.active[i];
         const int row0 = tb.row0[i], n = tb.row0[i + 1] - row0;
         const bool whole = u == first && stop == first + p.chunks;
         const uint32_t buf = seg & 1u;
+        float by = 1.f, hsf = 1.f;
+        if constexpr (FMT == kNVFP4) {
+          hsf = __ldg(a.h_sf + expert);
+          by = phase == 0 ? 1.f / (__ldg(a.x_sf + expert) * __ldg(a.w13_sf + expert)) : 1.f / (hsf * __ldg(a.w2_sf + expert));
+        }
         if (et == 0) last_flag = mbar_wait_bounded(&acc_full[buf], (seg >> 1) & 1u) && abort_flag == 0u ? 1u : 0u;
         named_sync(1, 128);
         ok = last_flag != 0u;
@@ -532,47 +571,45 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         const int r = 32 * quarter + lane;
         // a block's run begins inside at most one tile of a phase (part 0) and ends inside one (part 1)
         float* mine = a.part + ((static_cast<int64_t>(block) * 2 + phase) * 2 + (u == first ? 1 : 0)) * part_floats;
-        const int owner0 = whole ? block : moe_owner(p, first);
-        const int owner1 = whole ? block : moe_owner(p, first + p.chunks - 1);
+        const int owner0 = whole ? block : p.owner(first), owner1 = whole ? block : p.owner(first + p.chunks - 1);
         bool finish = whole;
         if (!whole) {
-          for (int c = 0; c < n; c += 16) {
-            float x[16], z[16];
-            t5_ld16_pair(lanes + c, lanes + 64 + c, x, z);
+          for (int c = 0; c < n; c += 8) {
+            float x[8], z[8];
+            t5_ld8_pair(lanes + c, lanes + 64 + c, x, z);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
+            for (int j = 0; j < 8; ++j)
               if (c + j < n) {
-                mine[(c + j) * 128 + r] = x[j];
-                mine[(a.max_n + c + j) * 128 + r] = z[j];
+                __stcg(mine + (c + j) * 128 + r, x[j]);
+                __stcg(mine + (a.max_n + c + j) * 128 + r, z[j]);
               }
           }
-          __threadfence();
           t5_fence_before();
           named_sync(1, 128);
           if (et == 0) {
             mbar_arrive(&acc_empty[buf]);
             uint32_t* count = a.counters + kMoeSplit + 2 * owner0 + phase;
-            const uint32_t now = atomicAdd(count, static_cast<uint32_t>(stop - u)) + static_cast<uint32_t>(stop - u);
-            last_flag = now == static_cast<uint32_t>(p.chunks) ? 1u : 0u;
-            if (last_flag != 0u) *count = 0u;
-            __threadfence();
+            const uint32_t add = static_cast<uint32_t>(stop - u);
+            const bool last = atomic_add_acq_rel(count, add) + add == static_cast<uint32_t>(p.chunks);
+            last_flag = last ? 1u : 0u;
+            if (last) *count = 0u;
           }
           named_sync(1, 128);
           finish = last_flag != 0u;
           named_sync(1, 128);  // last_flag is written again below
         }
         if (finish) {
-          for (int c = 0; c < n; c += 16) {
-            float x[16], z[16];
+          for (int c = 0; c < n; c += 8) {
+            float x[8], z[8];
             if (whole) {
-              t5_ld16_pair(lanes + c, lanes + 64 + c, x, z);
+              t5_ld8_pair(lanes + c, lanes + 64 + c, x, z);
             } else {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) x[j] = z[j] = 0.f;
+              for (int j = 0; j < 8; ++j) x[j] = z[j] = 0.f;
               for (int o = owner0; o <= owner1; ++o) {
                 const float* part = a.part + ((static_cast<int64_t>(o) * 2 + phase) * 2 + (o == owner0 ? 1 : 0)) * part_floats;
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
+                for (int j = 0; j < 8; ++j)
                   if (c + j < n) {
                     x[j] += __ldcg(part + (c + j) * 128 + r);
                     z[j] += __ldcg(part + (a.max_n + c + j) * 128 + r);
@@ -580,25 +617,21 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
               }
             }
             if (phase == 0) {
-              const float by = FMT == kNVFP4 ? 1.f / (a.x_sf[expert] * a.w13_sf[expert]) : 1.f;
-              const float hsf = FMT == kNVFP4 ? a.h_sf[expert] : 1.f;
               const int i0 = 128 * tile + 32 * quarter;  // first of this warp's rows
               const int kt = a.inter / kAtomElems, s0 = i0 / kSF;
               const int64_t row_bytes = FMT == kMXFP8 ? a.inter : a.inter / 2;
+              uint8_t* word = a.hq_s + (static_cast<int64_t>(i) * kt + s0 / 4) * 512 + (s0 & 3);
+              uint8_t* dst = a.hq + row0 * row_bytes + (FMT == kMXFP8 ? i0 : i0 / 2);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                if (c + j >= n) break;  // uniform
-                const float g = x[j] * by, up = z[j] * by;
-                const float h = __bfloat162float(__float2bfloat16_rn(g / (1.f + expf(-g)) * up));
+              for (int j = 0; j < 8; ++j) {
                 const int tok = c + j;
-                uint8_t* word = a.hq_s + (static_cast<int64_t>(i) * kt + s0 / 4) * 512 + (tok & 31) * 16 + (tok >> 5) * 4 + (s0 & 3);
-                moe_quant_lane<FMT>(h, hsf, lane, a.hq + (row0 + tok) * row_bytes + (FMT == kMXFP8 ? i0 : i0 / 2), word);
+                if (tok >= n) break;  // uniform
+                moe_finish_h<FMT>(x[j] * by, z[j] * by, hsf, lane, dst + tok * row_bytes, word + (tok & 31) * 16 + (tok >> 5) * 4);
               }
             } else {
-              const float by = FMT == kNVFP4 ? 1.f / (a.h_sf[expert] * a.w2_sf[expert]) : 1.f;
               const int col = 256 * tile + r;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
+              for (int j = 0; j < 8; ++j) {
                 if (c + j >= n) break;
                 const int pair = tb.pair_of[row0 + c + j];
                 const float f = tb.prob[pair] * by;
@@ -608,13 +641,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
               }
             }
           }
-          fence_async();
-          __threadfence();
           t5_fence_before();
           named_sync(1, 128);
           if (et == 0) {
             if (whole) mbar_arrive(&acc_empty[buf]);
-            if (phase == 0) atomicAdd(a.counters + kMoeExpertDone + i, 1u);
+            if (phase == 0) atomic_add_acq_rel(a.counters + kMoeExpertDone + i, 1u);
           }
         }
         u = stop;
@@ -625,7 +656,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     if (et == 0) {
       bool all = ok && abort_flag == 0u;
       if (all) {
-        atomicAdd(a.counters + kMoeBarDone, 1u);
+        atomic_add_acq_rel(a.counters + kMoeBarDone, 1u);
         all = moe_wait_count(a.counters + kMoeBarDone, blocks, &abort_flag);
       }
       if (!all) {
@@ -637,8 +668,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     named_sync(1, 128);
     if (last_flag != 0u) {
       const int quads = a.hidden / 4;
-      for (int64_t w = static_cast<int64_t>(block) * 128 + et; w < static_cast<int64_t>(a.tokens) * quads; w += blocks * 128) {
-        const int t = static_cast<int>(w / quads), c = static_cast<int>(w % quads) * 4;
+      for (int w = block * 128 + et; w < a.tokens * quads; w += blocks * 128) {
+        const int t = w / quads, c = (w - t * quads) * 4;
         const float* src = a.yp + static_cast<int64_t>(t) * a.top_k * a.hidden + c;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < a.top_k; ++k) {
@@ -650,8 +681,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       // every block has passed every other wait: clear the counters
       for (int i = block * 128 + et; i < active; i += blocks * 128) a.counters[kMoeExpertDone + i] = 0u;
       if (et == 0) {
-        __threadfence();
-        if (atomicAdd(a.counters + kMoeBarExit, 1u) == static_cast<uint32_t>(blocks) - 1u) {
+        if (atomic_add_acq_rel(a.counters + kMoeBarExit, 1u) == static_cast<uint32_t>(blocks) - 1u) {
           a.counters[kMoeBarQuant] = 0u;
           a.counters[kMoeBarDone] = 0u;
           a.counters[kMoeBarExit] = 0u;

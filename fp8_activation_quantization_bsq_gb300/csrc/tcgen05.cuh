@@ -78,18 +78,15 @@ __device__ __forceinline__ uint32_t t5_idesc_scaled(uint32_t n, uint32_t sf_id) 
   return (sf_id << 4) | (fmt << 7) | (fmt << 10) | ((n >> 3) << 17) | ((FMT == kNVFP4 ? 0u : 1u) << 23) | (8u << 24) | (sf_id << 29);
 }
 
-// 16 consecutive columns of this thread's tensor-memory lane at two addresses,
+// 8 consecutive columns of this thread's tensor-memory lane at two addresses,
 // waited for in the same statement, so that no register is read early.
-__device__ __forceinline__ void t5_ld16_pair(uint32_t ta, uint32_t tb, float (&x)[16], float (&y)[16]) {
+__device__ __forceinline__ void t5_ld8_pair(uint32_t ta, uint32_t tb, float (&x)[8], float (&y)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
-      "[%33];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]),
-        "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15]), "=f"(y[0]), "=f"(y[1]), "=f"(y[2]),
-        "=f"(y[3]), "=f"(y[4]), "=f"(y[5]), "=f"(y[6]), "=f"(y[7]), "=f"(y[8]), "=f"(y[9]), "=f"(y[10]), "=f"(y[11]),
-        "=f"(y[12]), "=f"(y[13]), "=f"(y[14]), "=f"(y[15])
+      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(y[0]), "=f"(y[1]),
+        "=f"(y[2]), "=f"(y[3]), "=f"(y[4]), "=f"(y[5]), "=f"(y[6]), "=f"(y[7])
       : "r"(ta), "r"(tb)
       : "memory");
 }
@@ -108,6 +105,14 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
   uint32_t v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
+}
+
+// Adds and returns the old value; orders this thread's accesses, and those
+// it has seen through a barrier, before and after it (GPU scope).
+__device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
 }
 
 // Barrier of `threads` threads of the block (id 1..15).
