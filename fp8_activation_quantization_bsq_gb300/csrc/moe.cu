@@ -35,7 +35,7 @@ MoeWorkspace moe_workspace(int32_t fmt, int32_t tokens, int64_t hidden, int64_t 
   w.xq_s = take(active * bsq_scales5d_bytes(fmt, 128, hidden));
   w.hq = take(pairs * row_bytes_of(fmt, inter));
   w.hq_s = take(active * bsq_scales5d_bytes(fmt, 128, inter));
-  w.part = take(int64_t(kMoeMaxBlocks) * 4 * 2 * max_n * 128 * 4);
+  w.part = take(int64_t(kMoeMaxBlocks) * 2 * 2 * max_n * 128 * 4);
   w.yp = take(pairs * hidden * 4);
   w.bytes = at;
   return w;

@@ -18,9 +18,9 @@
 //  * A phase's work is cut into units of one stage, numbered expert by
 //    expert, tile by tile along K, and every block takes an equal run of them
 //    whatever the tiles are.  A tile (pair of 128-row halves: gate and up rows, or
-//    256 rows of W2) that several blocks share is joined by the last of them
-//    to finish, which adds the parts in block order (no atomics on values: the result
-//    does not depend on timing).
+//    256 rows of W2) that several blocks share is finished by the block that began it, which
+//    adds the others' parts in block order (no atomics on values: the result does not
+//    depend on timing).
 //  * warp 0 streams weights through a ring of shared-memory stages.  They do
 //    not depend on the activations, so at the start (while the tokens
 //    are quantized) and between the two phases (while h is finished) the ring
@@ -39,11 +39,13 @@
 namespace bsq {
 
 constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 1024;
-constexpr int kMoeThreads = 256;
+constexpr int kMoeThreads = 384;          // weights, products, tokens, (idle), 4 epilogue and 4 helper warps
+constexpr int kMoeQuantThreads = 256;      // warps 4-11 quantize the tokens and sum y
 constexpr int kMoeHalfBytes = 128 * 128;  // a stage's 128 rows x 128 bytes of one tile half
 constexpr int kMoeMaxBlocks = 512;
 // counters at the start of the workspace, zero between calls
-constexpr int kMoeBarQuant = 0, kMoeBarDone = 1, kMoeBarExit = 2, kMoeSplit = 16, kMoeExpertDone = kMoeSplit + 2 * kMoeMaxBlocks;
+constexpr int kMoeBarQuant = 0, kMoeBarDone = 32, kMoeBarExit = 64, kMoePartReady = 96,
+              kMoeExpertDone = kMoePartReady + 2 * kMoeMaxBlocks;
 constexpr int kMoeCounterBytes = 4 * (kMoeExpertDone + 1024);
 
 // Columns of a stage and its scale atoms per 128 rows.
@@ -64,7 +66,7 @@ struct MoeArgs {
   int tokens, hidden, inter, experts, top_k, renorm;
   uint32_t* counters;
   uint8_t *xq, *xq_s, *hq, *hq_s;  // tokens' operands by row (expert by expert), scales by active expert
-  float* part;                     // [block][phase][part][2 halves][max_n][128]
+  float* part;                     // [block][phase][2 halves][max_n][128]
   float* yp;                       // [token * top_k + choice][hidden]
   int max_n;                       // tokens rounded up to 16
   int stages, stage_bytes;
@@ -73,7 +75,7 @@ struct MoeArgs {
 
 // Shared memory before the stages: routing tables (16-byte aligned parts).
 struct MoeTables {
-  uint64_t* mask;    // [experts] tokens that chose the expert
+  uint32_t* mask;    // [experts][2] tokens that chose the expert, a bit each
   int* active;       // [active] expert of active index
   int* row0;         // [active + 1] first row
   int* index_of;     // [experts] active index
@@ -154,17 +156,17 @@ __device__ __forceinline__ void moe_route(const MoeArgs& a, const MoeTables& tb,
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
   }
-  uint32_t mine = 0;  // key of choice `lane`
+  uint32_t mine = 0;  // key and expert of choice `lane`
+  int my_id = 0;
   for (int k = 0; k < a.top_k; ++k) {
     int at = 0x7FFFFFFF;
 #pragma unroll
     for (int i = NL - 1; i >= 0; --i)
       if (key[i] == m) at = 32 * i + lane;
     const int id = static_cast<int>(__reduce_min_sync(~0u, static_cast<uint32_t>(at)));  // equal ones: the lowest expert
-    if (lane == k) mine = m;
-    if (lane == 0) {
-      tb.id[t * a.top_k + k] = id;
-      atomicOr(reinterpret_cast<unsigned long long*>(&tb.mask[id]), 1ull << t);
+    if (lane == k) {
+      mine = m;
+      my_id = id;
     }
     best = 0;
 #pragma unroll
@@ -180,8 +182,19 @@ __device__ __forceinline__ void moe_route(const MoeArgs& a, const MoeTables& tb,
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
   }
-  if (lane < a.top_k) tb.prob[t * a.top_k + lane] = top > -INFINITY ? p / sum : 0.f;
+  if (lane < a.top_k) {
+    tb.prob[t * a.top_k + lane] = top > -INFINITY ? p / sum : 0.f;
+    tb.id[t * a.top_k + lane] = my_id;
+    atomicOr(&tb.mask[2 * my_id + (t >> 5)], 1u << (t & 31));
+  }
 }
+
+// Rank of token t among the tokens of an expert, and their number.
+__device__ __forceinline__ int moe_rank(const MoeTables& tb, int e, int t) {
+  const uint32_t lo = tb.mask[2 * e], hi = tb.mask[2 * e + 1], below = (1u << (t & 31)) - 1u;
+  return t < 32 ? __popc(lo & below) : __popc(lo) + __popc(hi & below);
+}
+__device__ __forceinline__ int moe_count(const MoeTables& tb, int e) { return __popc(tb.mask[2 * e]) + __popc(tb.mask[2 * e + 1]); }
 
 // Quantize 32 consecutive BF16 values (16 words): packed bytes and scale bytes.
 template <int FMT>
@@ -266,6 +279,40 @@ __device__ __noinline__ void moe_finish_h(float g, float u, float hsf, int lane,
   moe_quant_lane<FMT>(h, hsf, lane, row_bytes, scale_word);
 }
 
+// One stage's products into accumulators d and d + 64 (the tile's halves).
+// da, db, ds: descriptors of the stage's weights, tokens and scales.  FULL: a
+// whole stage of two halves, without a branch; else `slices` products of 32
+// bytes of each row, `atoms` scale atoms.  Scale addresses in tensor memory
+// are multiples of 4 columns.
+template <int FMT, bool FULL>
+__device__ __forceinline__ void moe_products(uint32_t d, uint64_t da, uint64_t db, uint64_t ds, uint32_t n, uint32_t sf,
+                                             uint32_t fresh, int slices, int atoms, bool two, uint32_t lead) {
+  constexpr int kAtoms = MoeFmt<FMT>::kAtoms;
+#pragma unroll
+  for (int q = 0; q < kAtoms; ++q) {
+    if (FULL || q < atoms) {
+      t5_copy_atom(sf + 4 * q, ds + 32 * q, lead);
+      if (FULL || two) t5_copy_atom(sf + 16 + 4 * q, ds + 32 * (kAtoms + q), lead);
+      t5_copy_atom(sf + 32 + 4 * q, ds + 32 * (2 * kAtoms + q), lead);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    if (FULL || m < slices) {
+      constexpr uint32_t kPer = 4 / kAtoms;  // slices per atom
+      const uint32_t atom = m / kPer, id = (m % kPer) * (4 / kPer);
+      const uint32_t idesc = t5_idesc_scaled<FMT>(n, id);
+      const uint32_t sfb = sf + 32 + 4 * atom;
+      t5_mma_scaled<FMT>(d, da + 2 * m, db + 2 * m, idesc, sf + 4 * atom, sfb, fresh | m, lead);
+      if (FULL || two) t5_mma_scaled<FMT>(d + 64, da + kMoeHalfBytes / 16 + 2 * m, db + 2 * m, idesc, sf + 16 + 4 * atom, sfb, fresh | m, lead);
+    }
+  }
+}
+
+// Byte of the scale of an expert's token r, scale column s, in the tokens'
+// scales: the 5D layout of one row tile.
+__device__ __forceinline__ int moe_token_scale(int r, int s) { return (s >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (s & 3); }
+
 // Wait until a counter in global memory reaches `value`, for about a second.
 __device__ __forceinline__ bool moe_wait_count(const uint32_t* p, uint32_t value, const volatile uint32_t* abort_flag) {
   if (ld_acquire(p) >= value) return true;
@@ -289,6 +336,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   __shared__ uint32_t tmem_slot, last_flag;
   __shared__ volatile uint32_t abort_flag, fills_a, fills_b, consumed;
   __shared__ int active_count;
+  __shared__ uint32_t warp_sum[kMoeThreads / 32];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int blocks = gridDim.x, block = blockIdx.x, pairs = a.tokens * a.top_k;
@@ -298,7 +346,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   {
     const int act = (a.experts < pairs ? a.experts : pairs) + 1;
     uint8_t* p = smem + stages * a.stage_bytes;
-    tb.mask = reinterpret_cast<uint64_t*>(p);
+    tb.mask = reinterpret_cast<uint32_t*>(p);
     p += moe_align16(8 * a.experts);
     tb.active = reinterpret_cast<int*>(p);
     p += moe_align16(4 * act);
@@ -331,10 +379,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     prefetch_tensormap(&map_hq);
   }
   if (warp == 1) t5_alloc(&tmem_slot, 512);
-  for (int e = tid; e < a.experts; e += kMoeThreads) tb.mask[e] = 0;
+  for (int e = tid; e < 2 * a.experts; e += kMoeThreads) tb.mask[e] = 0u;
   __syncthreads();
   // the first block of x that this thread will quantize is on its way while the tokens are routed
-  const int per_row = a.hidden / 32, quant_total = pairs * per_row, quant_step = blocks * 128;
+  const int per_row = a.hidden / 32, quant_total = pairs * per_row, quant_step = blocks * kMoeQuantThreads;
   int quant_at = block + blocks * (tid - 128);
   uint4 xv[4];
   if (warp >= 4) moe_load_x(a, quant_at, quant_total, per_row, xv);
@@ -344,30 +392,40 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     for (int t = warp; t < a.tokens; t += kMoeThreads / 32) moe_route<32>(a, tb, t, lane);
   }
   __syncthreads();
-  if (warp == 0) {  // active experts in increasing order, and their first rows
-    int n = 0, rows = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 32) {
-      const uint64_t m = e0 + lane < a.experts ? tb.mask[e0 + lane] : 0;
-      const uint32_t some = __ballot_sync(~0u, m != 0);
-      const int c = __popcll(m);
-      int before = c;
+  // active experts in increasing order and their first rows: a thread per expert, (rows << 16 | 1) summed
+  {
+    uint32_t base = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += kMoeThreads) {
+      const int e = e0 + tid;
+      const int c = e < a.experts ? moe_count(tb, e) : 0;
+      const uint32_t v = c > 0 ? static_cast<uint32_t>(c) << 16 | 1u : 0u;
+      uint32_t sum = v;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(~0u, before, d);
-        if (lane >= d) before += o;
+        const uint32_t o = __shfl_up_sync(~0u, sum, d);
+        if (lane >= d) sum += o;
       }
-      if (m != 0) {
-        const int i = n + __popc(some & ((1u << lane) - 1u));
-        tb.active[i] = e0 + lane;
-        tb.row0[i] = rows + before - c;
-        tb.index_of[e0 + lane] = i;
+      if (lane == 31) warp_sum[warp] = sum;
+      __syncthreads();
+      uint32_t before = base, all = base;
+#pragma unroll
+      for (int w = 0; w < kMoeThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        all += warp_sum[w];
       }
-      n += __popc(some);
-      rows += __shfl_sync(~0u, before, 31);
+      before += sum - v;
+      if (c > 0) {
+        const int i = before & 0xFFFF;
+        tb.active[i] = e;
+        tb.row0[i] = before >> 16;
+        tb.index_of[e] = i;
+      }
+      base = all;
+      __syncthreads();
     }
-    if (lane == 0) {
-      tb.row0[n] = rows;
-      active_count = n;
+    if (tid == 0) {
+      active_count = base & 0xFFFF;
+      tb.row0[base & 0xFFFF] = base >> 16;
     }
   }
   t5_fence_before();
@@ -375,10 +433,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   t5_fence_after();
   for (int p = tid; p < pairs; p += kMoeThreads) {  // rows of an expert in token order
     const int t = p / a.top_k, e = tb.id[p];
-    tb.pair_of[tb.row0[tb.index_of[e]] + __popcll(tb.mask[e] & ((1ull << t) - 1ull))] = p;
+    tb.pair_of[tb.row0[tb.index_of[e]] + moe_rank(tb, e, t)] = p;
   }
   __syncthreads();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = tmem_slot, smem_base = smem_addr(smem);
   const int active = active_count;
   const int part_floats = 2 * a.max_n * 128;
 
@@ -468,61 +526,52 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ---- products
-    if (lane == 0) {
-      uint32_t stage = 0, phase_bit = 0, done = 0, seg = 0;
-      bool ok = true;
-      for (int phase = 0; phase < 2 && ok; ++phase) {
-        const MoePhase p = moe_phase<FMT>(a, phase, active);
-        const int cols = phase == 0 ? a.hidden : a.inter, rows = phase == 0 ? 2 * a.inter : a.hidden;
-        for (int u = p.begin; u < p.end && ok; ++seg) {
-          const int item = u / p.chunks, stop = min(p.end, (item + 1) * p.chunks);
-          const int i = item / p.tiles, tile = item % p.tiles;
-          const bool two = phase == 0 || 256 * tile + 128 < rows;
-          const uint32_t n = (tb.row0[i + 1] - tb.row0[i] + 15) & ~15u;
-          const uint32_t buf = seg & 1u, d = tmem + buf * 128u;
-          if (!mbar_wait_bounded(&acc_empty[buf], ((seg >> 1) & 1u) ^ 1u) || abort_flag != 0u) { ok = false; break; }
+    // ---- products: the whole warp in step, one lane issuing
+    const uint32_t lead = t5_elect();
+    uint32_t stage = 0, phase_bit = 0, done = 0, seg = 0;
+    bool ok = true;
+    for (int phase = 0; phase < 2 && ok; ++phase) {
+      const MoePhase p = moe_phase<FMT>(a, phase, active);
+      const int cols = phase == 0 ? a.hidden : a.inter, rows = phase == 0 ? 2 * a.inter : a.hidden;
+      for (int u = p.begin; u < p.end && ok; ++seg) {
+        const int item = u / p.chunks, stop = min(p.end, (item + 1) * p.chunks);
+        const int i = item / p.tiles, tile = item % p.tiles;
+        const bool two = phase == 0 || 256 * tile + 128 < rows;
+        const uint32_t n = (tb.row0[i + 1] - tb.row0[i] + 15) & ~15u;
+        const uint32_t buf = seg & 1u, d = tmem + buf * 128u;
+        ok = __all_sync(~0u, mbar_wait_bounded(&acc_empty[buf], ((seg >> 1) & 1u) ^ 1u) && abort_flag == 0u);
+        if (!ok) break;
+        t5_fence_after();
+        int kc = u - item * p.chunks;
+        for (uint32_t fresh = 0; u < stop; ++u, ++kc) {
+          ok = __all_sync(~0u, mbar_wait_bounded(&full_bar[stage], phase_bit) && abort_flag == 0u);
+          if (!ok) break;
           t5_fence_after();
-          int kc = u - item * p.chunks;
-          for (uint32_t fresh = 0; u < stop; ++u, ++kc) {
-            if (!mbar_wait_bounded(&full_bar[stage], phase_bit) || abort_flag != 0u) { ok = false; break; }
-            t5_fence_after();
-            const uint32_t st = smem_addr(smem + stage * a.stage_bytes);
-            const uint32_t tok = st + 2 * kMoeHalfBytes, sc = tok + a.max_n * 128;
-            const uint32_t sf = tmem + 256u + (done & 1u) * 64u;
-            const int left = cols - kc * kElems, atoms = min(kAtoms, (left + kAtomElems - 1) / kAtomElems);
-            for (int q = 0; q < atoms; ++q) {
-              t5_copy_atom(sf + 4 * q, t5_desc_atom(sc + 512 * q));
-              if (two) t5_copy_atom(sf + 16 + 4 * q, t5_desc_atom(sc + 512 * (kAtoms + q)));
-              t5_copy_atom(sf + 32 + 4 * q, t5_desc_atom(sc + 512 * (2 * kAtoms + q)));
-            }
-            constexpr int kMmaElems = kElems / 4;
-            const int slices = min(4, (left + kMmaElems - 1) / kMmaElems);
-            for (int m = 0; m < slices; ++m) {
-              const uint32_t atom = FMT == kNVFP4 ? m : FMT == kMXFP4 ? m >> 1 : 0;
-              const uint32_t id = FMT == kNVFP4 ? 0 : FMT == kMXFP4 ? 2 * (m & 1) : m;
-              const uint32_t idesc = t5_idesc_scaled<FMT>(n, id);
-              const uint64_t b = t5_desc_sw128(tok + 32 * m);
-              t5_mma_scaled<FMT>(d, t5_desc_sw128(st + 32 * m), b, idesc, sf + 4 * atom, sf + 32 + 4 * atom, fresh | m);
-              if (two)
-                t5_mma_scaled<FMT>(d + 64, t5_desc_sw128(st + kMoeHalfBytes + 32 * m), b, idesc, sf + 16 + 4 * atom,
-                                   sf + 32 + 4 * atom, fresh | m);
-            }
-            fresh = 4;
-            t5_commit(&empty_bar[stage]);
-            consumed = ++done;
-            if (++stage == stages) { stage = 0; phase_bit ^= 1u; }
-          }
-          if (ok) t5_commit(&acc_full[buf]);
+          const uint32_t st = smem_base + stage * a.stage_bytes;
+          const uint32_t tok = st + 2 * kMoeHalfBytes, sc = tok + a.max_n * 128;
+          const uint32_t sf = tmem + 256u + (done & 1u) * 64u;
+          const uint64_t da = t5_desc_sw128(st), db = t5_desc_sw128(tok), ds = t5_desc_atom(sc);
+          const int left = cols - kc * kElems;
+          if (left >= kElems && two)
+            moe_products<FMT, true>(d, da, db, ds, n, sf, fresh, 4, kAtoms, true, lead);
+          else
+            moe_products<FMT, false>(d, da, db, ds, n, sf, fresh, min(4, (left + kElems / 4 - 1) / (kElems / 4)),
+                                     min(kAtoms, (left + kAtomElems - 1) / kAtomElems), two, lead);
+          fresh = 1;
+          t5_commit(smem_addr(&empty_bar[stage]), lead);
+          ++done;
+          if (lane == 0) consumed = done;
+          if (++stage == stages) { stage = 0; phase_bit ^= 1u; }
         }
+        if (ok) t5_commit(smem_addr(&acc_full[buf]), lead);
       }
-      if (!ok) {
-        if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
-        abort_flag = 1u;
-      }
-      t5_commit(&drain_bar);
-      if (!mbar_wait_bounded(&drain_bar, 0)) record_error_at(a.err, kErrTimeout);
     }
+    if (!ok && lane == 0) {
+      if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
+      abort_flag = 1u;
+    }
+    t5_commit(smem_addr(&drain_bar), lead);
+    if (!mbar_wait_bounded(&drain_bar, 0) && lane == 0) record_error_at(a.err, kErrTimeout);
   } else if (warp >= 4) {
     // ---- quantize the tokens' rows, a block of 32 columns per thread at a time
     const int et = tid - 128, quarter = warp & 3;
@@ -532,23 +581,25 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         uint4 next[4];
         moe_load_x(a, quant_at + quant_step, quant_total, per_row, next);
         const int pair = quant_at / per_row, c = quant_at - pair * per_row, t = pair / a.top_k;
-        const int e = tb.id[pair], i = tb.index_of[e], r = __popcll(tb.mask[e] & ((1ull << t) - 1ull));
+        const int e = tb.id[pair], i = tb.index_of[e], r = moe_rank(tb, e, t);
         const int s0 = 32 * c / kSF;  // first scale column
-        uint8_t* word = a.xq_s + (static_cast<int64_t>(i) * kt + s0 / 4) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (s0 & 3);
+        uint8_t* sc = a.xq_s + static_cast<int64_t>(i) * kt * 512;
+        uint8_t* word = sc + moe_token_scale(r, s0);
         moe_quant_block<FMT>(xv, FMT == kNVFP4 ? __ldg(a.x_sf + e) : 1.f,
                              a.xq + static_cast<int64_t>(tb.row0[i] + r) * row_bytes + (FMT == kMXFP8 ? 32 * c : 16 * c), word);
         if (c == per_row - 1)  // the last atom's columns past the row: zero
-          for (int s = s0 + 32 / kSF; s < 4 * kt; ++s) word[s - s0] = 0;
+          for (int s = s0 + 32 / kSF; s < 4 * kt; ++s) sc[moe_token_scale(r, s)] = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) xv[q] = next[q];
         quant_at += quant_step;
       }
-      named_sync(1, 128);
+      named_sync(2, kMoeQuantThreads);
       if (et == 0) atomic_add_acq_rel(a.counters + kMoeBarQuant, 1u);
     }
+    bool ok = true;
+    if (warp < 8) {
     // ---- finished accumulators
     uint32_t seg = 0;
-    bool ok = true;
     for (int phase = 0; phase < 2 && ok; ++phase) {
       const MoePhase p = moe_phase<FMT>(a, phase, active);
       for (int u = p.begin; u < p.end; ++seg) {
@@ -562,18 +613,28 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           hsf = __ldg(a.h_sf + expert);
           by = phase == 0 ? 1.f / (__ldg(a.x_sf + expert) * __ldg(a.w13_sf + expert)) : 1.f / (hsf * __ldg(a.w2_sf + expert));
         }
-        if (et == 0) last_flag = mbar_wait_bounded(&acc_full[buf], (seg >> 1) & 1u) && abort_flag == 0u ? 1u : 0u;
+        // The block that began a tile finishes it: it gets there at the end
+        // of its run, when the blocks that began theirs inside the tile have
+        // long stored their parts.  Parts are added in block order.
+        const int more = u == first && !whole ? p.owner(first + p.chunks - 1) - block : 0;  // blocks after this one in the tile
+        if (et == 0) {
+          bool go = true;
+          for (int o = block + 1; o <= block + more && go; ++o) {
+            uint32_t* flag = a.counters + kMoePartReady + 2 * o + phase;
+            go = moe_wait_count(flag, 1u, &abort_flag);
+            *flag = 0u;
+          }
+          go = go && mbar_wait_bounded(&acc_full[buf], (seg >> 1) & 1u) && abort_flag == 0u;
+          last_flag = go ? 1u : 0u;
+        }
         named_sync(1, 128);
         ok = last_flag != 0u;
         if (!ok) break;  // uniform
         t5_fence_after();
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + buf * 128u;
         const int r = 32 * quarter + lane;
-        // a block's run begins inside at most one tile of a phase (part 0) and ends inside one (part 1)
-        float* mine = a.part + ((static_cast<int64_t>(block) * 2 + phase) * 2 + (u == first ? 1 : 0)) * part_floats;
-        const int owner0 = whole ? block : p.owner(first), owner1 = whole ? block : p.owner(first + p.chunks - 1);
-        bool finish = whole;
-        if (!whole) {
+        if (u != first) {
+          float* mine = a.part + (static_cast<int64_t>(block) * 2 + phase) * part_floats;
           for (int c = 0; c < n; c += 8) {
             float x[8], z[8];
             t5_ld8_pair(lanes + c, lanes + 64 + c, x, z);
@@ -588,45 +649,32 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           named_sync(1, 128);
           if (et == 0) {
             mbar_arrive(&acc_empty[buf]);
-            uint32_t* count = a.counters + kMoeSplit + 2 * owner0 + phase;
-            const uint32_t add = static_cast<uint32_t>(stop - u);
-            const bool last = atomic_add_acq_rel(count, add) + add == static_cast<uint32_t>(p.chunks);
-            last_flag = last ? 1u : 0u;
-            if (last) *count = 0u;
+            st_release(a.counters + kMoePartReady + 2 * block + phase, 1u);
           }
-          named_sync(1, 128);
-          finish = last_flag != 0u;
-          named_sync(1, 128);  // last_flag is written again below
-        }
-        if (finish) {
+        } else {
           for (int c = 0; c < n; c += 8) {
             float x[8], z[8];
-            if (whole) {
-              t5_ld8_pair(lanes + c, lanes + 64 + c, x, z);
-            } else {
+            t5_ld8_pair(lanes + c, lanes + 64 + c, x, z);
+            for (int o = block + 1; o <= block + more; ++o) {
+              const float* part = a.part + (static_cast<int64_t>(o) * 2 + phase) * part_floats;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) x[j] = z[j] = 0.f;
-              for (int o = owner0; o <= owner1; ++o) {
-                const float* part = a.part + ((static_cast<int64_t>(o) * 2 + phase) * 2 + (o == owner0 ? 1 : 0)) * part_floats;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  if (c + j < n) {
-                    x[j] += __ldcg(part + (c + j) * 128 + r);
-                    z[j] += __ldcg(part + (a.max_n + c + j) * 128 + r);
-                  }
-              }
+              for (int j = 0; j < 8; ++j)
+                if (c + j < n) {
+                  x[j] += __ldcg(part + (c + j) * 128 + r);
+                  z[j] += __ldcg(part + (a.max_n + c + j) * 128 + r);
+                }
             }
             if (phase == 0) {
               const int i0 = 128 * tile + 32 * quarter;  // first of this warp's rows
               const int kt = a.inter / kAtomElems, s0 = i0 / kSF;
               const int64_t row_bytes = FMT == kMXFP8 ? a.inter : a.inter / 2;
-              uint8_t* word = a.hq_s + (static_cast<int64_t>(i) * kt + s0 / 4) * 512 + (s0 & 3);
+              uint8_t* sc = a.hq_s + static_cast<int64_t>(i) * kt * 512;
               uint8_t* dst = a.hq + row0 * row_bytes + (FMT == kMXFP8 ? i0 : i0 / 2);
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 const int tok = c + j;
                 if (tok >= n) break;  // uniform
-                moe_finish_h<FMT>(x[j] * by, z[j] * by, hsf, lane, dst + tok * row_bytes, word + (tok & 31) * 16 + (tok >> 5) * 4);
+                moe_finish_h<FMT>(x[j] * by, z[j] * by, hsf, lane, dst + tok * row_bytes, sc + moe_token_scale(tok, s0));
               }
             } else {
               const int col = 256 * tile + r;
@@ -644,15 +692,16 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           t5_fence_before();
           named_sync(1, 128);
           if (et == 0) {
-            if (whole) mbar_arrive(&acc_empty[buf]);
+            mbar_arrive(&acc_empty[buf]);
             if (phase == 0) atomic_add_acq_rel(a.counters + kMoeExpertDone + i, 1u);
           }
         }
         u = stop;
       }
     }
+    }
     // ---- y, once every block is done
-    named_sync(1, 128);
+    named_sync(2, kMoeQuantThreads);
     if (et == 0) {
       bool all = ok && abort_flag == 0u;
       if (all) {
@@ -665,21 +714,28 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       }
       last_flag = all ? 1u : 0u;
     }
-    named_sync(1, 128);
+    named_sync(2, kMoeQuantThreads);
     if (last_flag != 0u) {
       const int quads = a.hidden / 4;
-      for (int w = block * 128 + et; w < a.tokens * quads; w += blocks * 128) {
+      for (int w = block * kMoeQuantThreads + et; w < a.tokens * quads; w += blocks * kMoeQuantThreads) {
         const int t = w / quads, c = (w - t * quads) * 4;
         const float* src = a.yp + static_cast<int64_t>(t) * a.top_k * a.hidden + c;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < a.top_k; ++k) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(k) * a.hidden));
-          s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        for (int k0 = 0; k0 < a.top_k; k0 += 8) {  // eight choices' loads in flight, added in their order
+          float4 v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k0 + k < a.top_k) v[k] = __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(k0 + k) * a.hidden));
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k0 + k < a.top_k) {
+              s.x += v[k].x; s.y += v[k].y; s.z += v[k].z; s.w += v[k].w;
+            }
         }
         *reinterpret_cast<uint2*>(a.y + t * a.ld_y + c) = make_uint2(f32x2_to_elem2<false>(s.x, s.y), f32x2_to_elem2<false>(s.z, s.w));
       }
       // every block has passed every other wait: clear the counters
-      for (int i = block * 128 + et; i < active; i += blocks * 128) a.counters[kMoeExpertDone + i] = 0u;
+      for (int i = block * kMoeQuantThreads + et; i < active; i += blocks * kMoeQuantThreads) a.counters[kMoeExpertDone + i] = 0u;
       if (et == 0) {
         if (atomic_add_acq_rel(a.counters + kMoeBarExit, 1u) == static_cast<uint32_t>(blocks) - 1u) {
           a.counters[kMoeBarQuant] = 0u;

@@ -20,9 +20,24 @@ __device__ __forceinline__ void t5_dealloc(uint32_t taddr, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
 }
 
-// Arrive on `bar` when every tcgen05 operation this thread has issued is done.
-__device__ __forceinline__ void t5_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+// The products, scale copies and commits below are issued by a whole warp in
+// uniform control flow and executed by its one lane with `lead` set: their
+// operands live in uniform registers, and inside a branch of one lane every one of them would be
+// moved there by itself, one after the other (about 90 cycles per product).
+
+// Whether this lane is the warp's leader.
+__device__ __forceinline__ uint32_t t5_elect() {
+  uint32_t lead;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(lead));
+  return lead;
+}
+
+// Arrive on `bar` when every tcgen05 operation the leader has issued is done.
+__device__ __forceinline__ void t5_commit(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead)
+      : "memory");
 }
 
 // K-major operand tile with the 128-byte swizzle: rows of 128 bytes, groups of 8
@@ -40,33 +55,31 @@ __device__ __forceinline__ uint64_t t5_desc_atom(uint32_t saddr) {
 
 // One scale atom into 4 columns of tensor memory: column c, lane i of every
 // quarter gets the 4 bytes of the atom's row 32 c + i.
-__device__ __forceinline__ void t5_copy_atom(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+__device__ __forceinline__ void t5_copy_atom(uint32_t taddr, uint64_t desc, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+      "l"(desc), "r"(lead)
+      : "memory");
 }
 
 // D (128 x N, FP32) (+)= A B^T with block scales, K = 32 bytes of each row.
+#define BSQ_T5_MMA_SCALED(KIND)                                                                                        \
+  asm volatile(                                                                                                        \
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"                                      \
+      "@q tcgen05.mma.cta_group::1.kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a), "l"(b),     \
+      "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)                                                       \
+      : "memory")
 template <int FMT>
 __device__ __forceinline__ void t5_mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                              uint32_t accumulate) {
+                                              uint32_t accumulate, uint32_t lead) {
   if constexpr (FMT == kNVFP4)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    BSQ_T5_MMA_SCALED("mxf4nvf4.block_scale.scale_vec::4X");
   else if constexpr (FMT == kMXFP4)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a),
-        "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    BSQ_T5_MMA_SCALED("mxf4.block_scale.scale_vec::2X");
   else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    BSQ_T5_MMA_SCALED("mxf8f6f4.block_scale.scale_vec::1X");
 }
+#undef BSQ_T5_MMA_SCALED
 
 // Instruction descriptor of the block-scaled products, M = 128: scale id of B
 // at 4-5, operand formats at 7 and 10 (E2M1 1, E4M3 0), N >> 3 at 17, scale type at 23
@@ -105,6 +118,10 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
   uint32_t v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
+}
+
+__device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
 // Adds and returns the old value; orders this thread's accesses, and those
