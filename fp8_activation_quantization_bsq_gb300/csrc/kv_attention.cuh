@@ -23,9 +23,12 @@
 // tensor-memory product would be mostly padding.  Fragments come straight from the codes with wide
 // shared loads: the order of the dimension in q.k and of the output columns is free, so a thread takes
 // 16 consecutive bytes of a key, and pairs of keys are interleaved bytewise before conversion.
-// An item cut by the runs is joined by the last block that finishes (in two levels of at most 16
-// parts when there are many), always in block order.
+// An item cut by the runs is finished by the block that began it, which adds the other blocks' parts
+// in block order (first in groups of 16 where there are many): those blocks hold them at the start of
+// their runs, it at the end of its own.
 #pragma once
+
+#include <type_traits>
 
 #include "tcgen05.cuh"
 
@@ -34,7 +37,7 @@ namespace bsq {
 constexpr int kKvTile = 64;       // keys per unit
 constexpr int kKvMaxBlocks = 1024;
 constexpr int kKvJoin = 16;       // parts joined at a time
-constexpr int kKvCounterBytes = 4 * 2 * kKvMaxBlocks;
+constexpr int kKvCounterBytes = 4 * kKvMaxBlocks;
 
 struct KvAttnArgs {
   const uint16_t* q;              // (total, heads, D)
@@ -49,8 +52,8 @@ struct KvAttnArgs {
   int64_t total, num_pages;
   int batch, heads, kv_heads, group, page, page_shift, table_width, causal, window;
   float scale_log2;               // sm_scale * log2(e)
-  uint32_t* counters;             // [2][kKvMaxBlocks], zero between calls
-  float* part;                    // [block][2][rows * D + 2 * rows]
+  uint32_t* ready;                // [block] part stored, zero between calls
+  float* part;                    // [block][rows * D + 2 * rows]: sums, maxima, weights' sums
   unsigned int* err;
 };
 
@@ -189,7 +192,10 @@ struct KvShape {
   static constexpr int kRows = 16 * ROWG;
   static constexpr int kTileBytes = kKvTile * D;           // of keys, and of values
   static constexpr int kStages = ROWG == 1 ? 4 : 6;
-  static constexpr int kMergeBytes = ROWG * 4 * 16 * D * 4;
+  // merge buffer: a row's quarters of D / 4 floats lie 4 floats further apart, so that the 8 rows x 4 quarters
+  // of a warp's float4 stores fall into different banks
+  static constexpr int kQuarter = D / 4 + 4, kRow = 4 * kQuarter;
+  static constexpr int kMergeBytes = kWarps * 16 * kRow * 4;
   static constexpr int kSmem = 1024 + kStages * 2 * kTileBytes + kMergeBytes;
   static constexpr int kPartFloats = kRows * D + 2 * kRows;
 };
@@ -212,44 +218,13 @@ __device__ __forceinline__ uint32_t kv_chunk(int r, int c) {
   return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Join `parts` parts whose slots follow from `slot`, in order, with the
-// block's consumer threads: each thread keeps its share of the sum in `acc`
-// (float4 q of the tile at index q * threads + tid); row sums and maxima in shared memory.
-template <int D, int ROWG, class SlotFn>
-__device__ __forceinline__ void kv_join(int parts, SlotFn slot, int tid, float (*weight)[16 * ROWG], float (*sums)[16 * ROWG],
-                                        float* row_m, float* row_l, float4 (&acc)[D / 32]) {
-  using S = KvShape<D, ROWG>;
-  constexpr int kT = 32 * S::kWarps;
-  for (int i = tid; i < parts * S::kRows; i += kT) {
-    const float* s = slot(i / S::kRows) + S::kRows * D + i % S::kRows;
-    weight[i / S::kRows][i % S::kRows] = __ldcg(s);
-    sums[i / S::kRows][i % S::kRows] = __ldcg(s + S::kRows);
-  }
-  named_sync(1, kT);
-  if (tid < S::kRows) {
-    float m = -INFINITY, l = 0.f;
-    for (int p = 0; p < parts; ++p) m = fmaxf(m, weight[p][tid]);
-    for (int p = 0; p < parts; ++p) {
-      const float w = m == -INFINITY ? 0.f : fast_exp2(weight[p][tid] - m);
-      weight[p][tid] = w;
-      l += w * sums[p][tid];
-    }
-    row_m[tid] = m;
-    row_l[tid] = l;
-  }
-  named_sync(1, kT);
-#pragma unroll
-  for (int q = 0; q < D / 32; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int p = 0; p < parts; ++p) {
-    const float4* s = reinterpret_cast<const float4*>(slot(p));
-#pragma unroll
-    for (int q = 0; q < D / 32; ++q) {
-      const float4 v = __ldcg(s + q * kT + tid);
-      const float w = weight[p][(q * kT + tid) / (D / 4)];
-      acc[q].x += w * v.x; acc[q].y += w * v.y; acc[q].z += w * v.z; acc[q].w += w * v.w;
-    }
-  }
+// Wait for a block's part, for about a second, and take the flag down.
+__device__ __forceinline__ bool kv_take_part(uint32_t* flag, const volatile uint32_t* abort_flag) {
+  const long long t0 = clock64();
+  while (ld_acquire(flag) == 0u)
+    if (*abort_flag != 0u || clock64() - t0 > kWaitLimitCycles) return false;
+  *flag = 0u;
+  return true;
 }
 
 template <int D, int ROWG, bool F16>
@@ -265,9 +240,8 @@ __global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
   __shared__ KvPageScale page_scale[S::kStages][4];
   __shared__ int64_t prefix[S::kThreads + 1];
   __shared__ KvStart start;
-  __shared__ float warp_m[S::kWarps][16], warp_l[S::kWarps][16];
-  __shared__ float weight[kKvMaxBlocks / kKvJoin][RT], sums[kKvMaxBlocks / kKvJoin][RT], row_m[RT], row_l[RT];
-  __shared__ volatile uint32_t abort_flag, fills, last_flag, go_on;
+  __shared__ float warp_m2[2][S::kWarps][16], warp_l2[2][S::kWarps][16];  // by parity of the item
+  __shared__ volatile uint32_t abort_flag, fills, used_tiles, go_on, joined;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -323,6 +297,8 @@ __global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
     __syncthreads();
   }
   const int64_t total = start.total, parts = min(total, static_cast<int64_t>(gridDim.x));
+  // the block whose run holds unit u
+  const auto owner = [&](int64_t u) { return static_cast<int>(((u + 1) * parts - 1) / total); };
   KvWalk<RT> walk;
   walk.u = total * blockIdx.x / parts;
   walk.end = total * (blockIdx.x + 1) / parts;
@@ -361,7 +337,7 @@ __global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
             pid = -1;
           }
         }
-        if (lane == 0) ok = mbar_wait_bounded(&empty_bar[stage], phase ^ 1u) && abort_flag == 0u;
+        if (lane == 0) ok = mbar_wait_clocked(&empty_bar[stage], phase ^ 1u) && abort_flag == 0u;
         ok = __shfl_sync(~0u, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
         const int first = pg0 - batch0;
@@ -392,7 +368,9 @@ __global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
     const int gq = lane >> 2, c = lane & 3, kw = warp & 3, rg = warp >> 2;
     uint32_t stage = 0, phase = 0, used = 0;
     bool ok = true;
-    while (ok && walk.next(a, g)) {
+    for (int item = 0; ok && walk.next(a, g); ++item) {
+      float(*warp_m)[16] = warp_m2[item & 1];
+      float(*warp_l)[16] = warp_l2[item & 1];
       const int rows = g.s.n * a.group, pos0 = g.s.len - g.s.n;
       int pos[2];       // positions of this thread's two rows
       float rowfac[2];  // sm_scale log2(e) 2^eq
@@ -433,7 +411,7 @@ __global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
       for (int t = g.tile0; t < g.tile1; ++t) {
-        ok = __all_sync(~0u, mbar_wait_bounded(&full_bar[stage], phase) && abort_flag == 0u);
+        ok = __all_sync(~0u, mbar_wait_clocked(&full_bar[stage], phase) && abort_flag == 0u);
         if (!ok) break;
         const uint8_t* kd = smem + stage * 2 * S::kTileBytes;
         const uint8_t* vd = kd + S::kTileBytes;
@@ -457,83 +435,87 @@ __global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
         }
         const int key0 = t * kKvTile + 16 * kw;
         // keys that not all rows see, or none: only tiles at the range's ends
-        const bool edge = ps.inv == 0.f || key0 < g.lo || key0 + 16 > g.hi || (a.causal && key0 + 15 > pos0 + g.rt * RT / a.group) ||
+        const bool masked = ps.inv == 0.f || key0 < g.lo || key0 + 16 > g.hi || (a.causal && key0 + 15 > pos0 + g.rt * RT / a.group) ||
                           (a.window > 0 && key0 <= pos0 + (min(rows, (g.rt + 1) * RT) - 1) / a.group - a.window);
-        float top[2] = {-INFINITY, -INFINITY};
-        const float f0 = rowfac[0] * ps.kfac, f1 = rowfac[1] * ps.kfac;
+        // two copies of the rest, so that the tiles in between carry no masks
+        const auto rest = [&](auto edge) {
+          float top[2] = {-INFINITY, -INFINITY};
+          const float f0 = rowfac[0] * ps.kfac, f1 = rowfac[1] * ps.kfac;
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
+          for (int nb = 0; nb < 2; ++nb) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int h = i >> 1;
-            float x = s[nb][i] * (h ? f1 : f0) + ps.ev;
-            if (edge) {
-              const int key = key0 + 8 * nb + 2 * c + (i & 1);
-              const bool see = ps.inv != 0.f && key >= g.lo && key < g.hi && (!a.causal || key <= pos[h]) && (a.window <= 0 || key > pos[h] - a.window);
-              x = see ? x : -INFINITY;
+            for (int i = 0; i < 4; ++i) {
+              const int h = i >> 1;
+              float x = s[nb][i] * (h ? f1 : f0) + ps.ev;
+              if constexpr (decltype(edge)::value) {
+                const int key = key0 + 8 * nb + 2 * c + (i & 1);
+                const bool see = ps.inv != 0.f && key >= g.lo && key < g.hi && (!a.causal || key <= pos[h]) && (a.window <= 0 || key > pos[h] - a.window);
+                x = see ? x : -INFINITY;
+              }
+              s[nb][i] = x;
+              top[h] = fmaxf(top[h], x);
             }
-            s[nb][i] = x;
-            top[h] = fmaxf(top[h], x);
           }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 1));
-          top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 2));
-        }
-        if (__any_sync(~0u, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float mn = fmaxf(m[h], top[h]);
-            const float f = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - mn);
-            m[h] = mn;
-            l[h] *= f;
+            top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 1));
+            top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 2));
+          }
+          if (__any_sync(~0u, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              o[i][2 * h] *= f;
-              o[i][2 * h + 1] *= f;
+            for (int h = 0; h < 2; ++h) {
+              const float mn = fmaxf(m[h], top[h]);
+              const float f = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - mn);
+              m[h] = mn;
+              l[h] *= f;
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i) {
+                o[i][2 * h] *= f;
+                o[i][2 * h + 1] *= f;
+              }
             }
           }
-        }
-        const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
-        uint32_t p[2][2];
+          const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
+          uint32_t p[2][2];
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
-          const float a0 = fast_exp2(s[nb][0] - m0), a1 = fast_exp2(s[nb][1] - m0);
-          const float b0 = fast_exp2(s[nb][2] - m1), b1 = fast_exp2(s[nb][3] - m1);
-          l[0] += (a0 + a1) * ps.inv;
-          l[1] += (b0 + b1) * ps.inv;
-          p[nb][0] = f32x2_to_elem2<true>(a0, a1);
-          p[nb][1] = f32x2_to_elem2<true>(b0, b1);
-        }
-        // values: keys 2c, 2c + 1 and 8 + 2c, 9 + 2c; this thread's dimensions D/8 gq ..
-        uint32_t vw[4][D / 32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = 16 * kw + 8 * (k >> 1) + 2 * c + (k & 1);
-          if constexpr (D == 128) {
-            const uint4 w = *reinterpret_cast<const uint4*>(vd + kv_chunk<D>(r, gq));
-            vw[k][0] = w.x; vw[k][1] = w.y; vw[k][2] = w.z; vw[k][3] = w.w;
-          } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(vd + kv_chunk<D>(r, gq >> 1) + 8 * (gq & 1));
-            vw[k][0] = w.x; vw[k][1] = w.y;
+          for (int nb = 0; nb < 2; ++nb) {
+            const float a0 = fast_exp2(s[nb][0] - m0), a1 = fast_exp2(s[nb][1] - m0);
+            const float b0 = fast_exp2(s[nb][2] - m1), b1 = fast_exp2(s[nb][3] - m1);
+            l[0] += (a0 + a1) * ps.inv;
+            l[1] += (b0 + b1) * ps.inv;
+            p[nb][0] = f32x2_to_elem2<true>(a0, a1);
+            p[nb][1] = f32x2_to_elem2<true>(b0, b1);
           }
-          if (edge) {  // whatever lies outside the allowed keys (NaN codes too) counts as zero
-            const int key = t * kKvTile + r;
-            if (key < g.lo || key >= g.hi || ps.inv == 0.f) {
+          // values: keys 2c, 2c + 1 and 8 + 2c, 9 + 2c; this thread's dimensions D/8 gq ..
+          uint32_t vw[4][D / 32];
 #pragma unroll
-              for (int i = 0; i < D / 32; ++i) vw[k][i] = 0u;
+          for (int k = 0; k < 4; ++k) {
+            const int r = 16 * kw + 8 * (k >> 1) + 2 * c + (k & 1);
+            if constexpr (D == 128) {
+              const uint4 w = *reinterpret_cast<const uint4*>(vd + kv_chunk<D>(r, gq));
+              vw[k][0] = w.x; vw[k][1] = w.y; vw[k][2] = w.z; vw[k][3] = w.w;
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2*>(vd + kv_chunk<D>(r, gq >> 1) + 8 * (gq & 1));
+              vw[k][0] = w.x; vw[k][1] = w.y;
+            }
+            if constexpr (decltype(edge)::value) {  // whatever lies outside the allowed keys (NaN codes too) counts as zero
+              const int key = t * kKvTile + r;
+              if (key < g.lo || key >= g.hi || ps.inv == 0.f) {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) vw[k][i] = 0u;
+              }
             }
           }
-        }
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          uint32_t lo[4], hi[4];
-          kv_pairs(vw[0][i], vw[1][i], lo);
-          kv_pairs(vw[2][i], vw[3][i], hi);
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t lo[4], hi[4];
+            kv_pairs(vw[0][i], vw[1][i], lo);
+            kv_pairs(vw[2][i], vw[3][i], hi);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) kv_mma(o[4 * i + j], p[0][0], p[0][1], p[1][0], p[1][1], lo[j], hi[j]);
-        }
+            for (int j = 0; j < 4; ++j) kv_mma(o[4 * i + j], p[0][0], p[0][1], p[1][0], p[1][1], lo[j], hi[j]);
+          }
+        };
+        if (masked) rest(std::true_type{}); else rest(std::false_type{});
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty_bar[stage]);
         ++used;
@@ -555,7 +537,7 @@ __global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
       }
       named_sync(1, kT);
       if (tid == 0) go_on = abort_flag == 0u ? 1u : 0u;  // one answer for all warps
-      float* mw = merge + warp * 16 * D;
+      float* mw = merge + warp * 16 * S::kRow;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = gq + 8 * h;
@@ -566,98 +548,104 @@ __global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
         // columns 2c (first half) and 2c + 1 (second) of every product: D/4 consecutive dimensions
 #pragma unroll
         for (int i = 0; i < D / 8; i += 4) {
-          float4* dst = reinterpret_cast<float4*>(mw + r * D + c * (D / 4) + i);
+          float4* dst = reinterpret_cast<float4*>(mw + r * S::kRow + c * S::kQuarter + i);
           dst[0] = make_float4(o[i][2 * h] * f, o[i + 1][2 * h] * f, o[i + 2][2 * h] * f, o[i + 3][2 * h] * f);
           dst[D / 32] = make_float4(o[i][2 * h + 1] * f, o[i + 1][2 * h + 1] * f, o[i + 2][2 * h + 1] * f, o[i + 3][2 * h + 1] * f);
-        }
-        if (kw == 0 && c == 0) {
-          float ll = 0.f;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const float wm = warp_m[4 * rg + w][r];
-            ll += warp_l[4 * rg + w][r] * (wm == -INFINITY ? 0.f : fast_exp2(wm - mm));
-          }
-          row_m[rg * 16 + r] = mm;
-          row_l[rg * 16 + r] = ll;
         }
       }
       named_sync(1, kT);
       ok = go_on != 0u;
+      const int live = min(RT, rows - g.rt * RT);  // rows of the tile
+      // eight threads per row, float4s 8 q + tid % 8 of it
+      const int r = tid >> 3, wr = 4 * (r >> 4), r16 = r & 15;
       float4 acc[D / 32];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const int at = i * kT + tid, r = at / (D / 4), d4 = at % (D / 4);
-        const float4* src = reinterpret_cast<const float4*>(merge + (r >> 4) * 64 * D + (r & 15) * D) + d4;
-        const float4 x = src[0], y = src[4 * D], z = src[8 * D], w = src[12 * D];  // 16 D floats apart
+        const int d4 = 8 * i + (tid & 7);
+        const float* src = merge + (wr * 16 + r16) * S::kRow + d4 / (D / 16) * S::kQuarter + d4 % (D / 16) * 4;
+        const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 16 * S::kRow);
+        const float4 z = *reinterpret_cast<const float4*>(src + 32 * S::kRow), w = *reinterpret_cast<const float4*>(src + 48 * S::kRow);
         acc[i] = make_float4((x.x + y.x) + (z.x + w.x), (x.y + y.y) + (z.y + w.y), (x.z + y.z) + (z.z + w.z), (x.w + y.w) + (z.w + w.w));
       }
-      const int64_t u0 = g.first, u1 = g.first + g.count - 1;
-      const int own0 = static_cast<int>(((u0 + 1) * parts - 1) / total), own1 = static_cast<int>(((u1 + 1) * parts - 1) / total);
-      bool write = own0 == own1 && ok;
-      if (own0 != own1) {
-        const int count = own1 - own0 + 1, groups = (count + kKvJoin - 1) / kKvJoin, me = static_cast<int>(blockIdx.x) - own0;
-        // a run begins inside at most one item (slot 0) and ends inside one (slot 1)
-        auto slot = [&](int p) { return a.part + (static_cast<int64_t>(own0 + p) * 2 + (p == 0 ? 1 : 0)) * S::kPartFloats; };
-        auto put = [&](int p) {
-          float* dst = slot(p);
+      float am = -INFINITY, al = 0.f;
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) __stcg(reinterpret_cast<float4*>(dst) + i * kT + tid, acc[i]);
-          if (tid < RT) {
-            __stcg(dst + RT * D + tid, row_m[tid]);
-            __stcg(dst + RT * D + RT + tid, row_l[tid]);
+      for (int k = 0; k < 4; ++k) am = fmaxf(am, warp_m[wr + k][r16]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float wm = warp_m[wr + k][r16];
+        al += wm == -INFINITY ? 0.f : warp_l[wr + k][r16] * fast_exp2(wm - am);
+      }
+      const int own0 = owner(g.first), own1 = owner(g.first + g.count - 1);
+      const int me = static_cast<int>(blockIdx.x) - own0, count = own1 - own0 + 1;
+      if (ok && me % kKvJoin == 0 && count > 1) {
+        // parts of the group's other blocks, then (the item's first block) of the other groups' first blocks
+        const int near = min(kKvJoin, count - me) - 1, far = me == 0 ? (count - 1) / kKvJoin : 0;
+        if (warp == 0) {
+          bool got = true;
+          for (int p = lane; p < near + far && got; p += 32)
+            got = kv_take_part(a.ready + blockIdx.x + (p < near ? 1 + p : kKvJoin * (p - near + 1)), &abort_flag);
+          got = __all_sync(~0u, got);
+          if (lane == 0) {
+            if (!got) {
+              if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
+              abort_flag = 1u;
+            }
+            joined = got ? 1u : 0u;
           }
-          __threadfence();
-          named_sync(1, kT);
-        };
-        auto arrive = [&](uint32_t* counter, int of) {  // true for the last of `of`
-          if (tid == 0) {
-            const bool last = ok && atomicAdd(counter, 1u) == static_cast<uint32_t>(of) - 1u;
-            if (last) *counter = 0u;
-            __threadfence();
-            last_flag = last ? 1u : 0u;
-          }
-          named_sync(1, kT);
-          const bool last = last_flag != 0u;
-          named_sync(1, kT);
-          return last;
-        };
-        put(me);
-        const int gi = me / kKvJoin, gsize = min(kKvJoin, count - gi * kKvJoin);
-        if (arrive(a.counters + own0 + gi * kKvJoin, gsize)) {
-          kv_join<D, ROWG>(gsize, [&](int p) { return slot(gi * kKvJoin + p); }, tid, weight, sums, row_m, row_l, acc);
-          write = true;
-          if (groups > 1) {
-            put(gi * kKvJoin);  // each thread overwrites what it alone has read
-            write = arrive(a.counters + kKvMaxBlocks + own0, groups);
-            if (write) kv_join<D, ROWG>(groups, [&](int p) { return slot(p * kKvJoin); }, tid, weight, sums, row_m, row_l, acc);
+        }
+        named_sync(1, kT);
+        ok = joined != 0u;
+        if (ok && r < live) {
+#pragma unroll 4
+          for (int p = 0; p < near + far; ++p) {
+            const float* part = a.part + static_cast<int64_t>(blockIdx.x + (p < near ? 1 + p : kKvJoin * (p - near + 1))) * S::kPartFloats;
+            float4 v[D / 32];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(part + r * D) + 8 * i + (tid & 7));
+            const float pm = __ldcg(part + RT * D + r), pl = __ldcg(part + RT * D + RT + r);
+            const float mm = fmaxf(am, pm);
+            const float f0 = am == -INFINITY ? 0.f : fast_exp2(am - mm), f1 = pm == -INFINITY ? 0.f : fast_exp2(pm - mm);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+              acc[i] = make_float4(acc[i].x * f0 + v[i].x * f1, acc[i].y * f0 + v[i].y * f1, acc[i].z * f0 + v[i].z * f1,
+                                   acc[i].w * f0 + v[i].w * f1);
+            al = al * f0 + pl * f1;
+            am = mm;
           }
         }
       }
-      if (write) {
+      if (ok && me != 0) {
+        float* part = a.part + static_cast<int64_t>(blockIdx.x) * S::kPartFloats;
+        if (r < live) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const int at = i * kT + tid, r = at / (D / 4), d = at % (D / 4) * 4, rr = g.rt * RT + r;
-          if (rr < rows) {
-            const float lr = row_l[r], f = lr > 0.f ? 1.f / lr : 0.f;
-            uint16_t* dst = a.out + (static_cast<int64_t>(g.s.t0 + rr / a.group) * a.heads + g.head * a.group + rr % a.group) * D + d;
-            *reinterpret_cast<uint2*>(dst) = make_uint2(f32x2_to_elem2<F16>(acc[i].x * f, acc[i].y * f), f32x2_to_elem2<F16>(acc[i].z * f, acc[i].w * f));
+          for (int i = 0; i < D / 32; ++i) __stcg(reinterpret_cast<float4*>(part + r * D) + 8 * i + (tid & 7), acc[i]);
+          if ((tid & 7) == 0) {
+            __stcg(part + RT * D + r, am);
+            __stcg(part + RT * D + RT + r, al);
           }
         }
-        if (a.lse != nullptr && tid < RT && g.rt * RT + tid < rows) {
-          const int rr = g.rt * RT + tid;
-          a.lse[static_cast<int64_t>(g.s.t0 + rr / a.group) * a.heads + g.head * a.group + rr % a.group] =
-              row_l[tid] > 0.f ? (row_m[tid] + log2f(row_l[tid])) * 0.6931471805599453f : -INFINITY;
-        }
+        named_sync(1, kT);
+        if (tid == 0) st_release(a.ready + blockIdx.x, 1u);
+      } else if (ok && r < live) {
+        const int rr = g.rt * RT + r;
+        const int64_t row = static_cast<int64_t>(g.s.t0 + rr / a.group) * a.heads + g.head * a.group + rr % a.group;
+        const float f = al > 0.f ? 1.f / al : 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          *reinterpret_cast<uint2*>(a.out + row * D + 32 * i + 4 * (tid & 7)) =
+              make_uint2(f32x2_to_elem2<F16>(acc[i].x * f, acc[i].y * f), f32x2_to_elem2<F16>(acc[i].z * f, acc[i].w * f));
+        if ((tid & 7) == 0 && a.lse != nullptr) a.lse[row] = al > 0.f ? (am + log2f(al)) * 0.6931471805599453f : -INFINITY;
       }
-      named_sync(1, kT);  // row_m, row_l and merge are written again
+      // the merge buffer and the flags are written again only after the first
+      // barrier of the next item's end, which all threads reach after this
     }
-    if (tid == 0) last_flag = used;
+    if (tid == 0) used_tiles = used;
   }
   __syncthreads();
   // after an expired wait: loads that nothing consumed land before the block ends
   if (tid == 0)
-    for (uint32_t f = last_flag; f < fills; ++f)
-      if (!mbar_wait_bounded(&full_bar[f % S::kStages], (f / S::kStages) & 1u)) record_error_at(a.err, kErrTimeout);
+    for (uint32_t f = used_tiles; f < fills; ++f)
+      if (!mbar_wait_clocked(&full_bar[f % S::kStages], (f / S::kStages) & 1u)) record_error_at(a.err, kErrTimeout);
 }
 
 }  // namespace bsq

@@ -132,8 +132,8 @@ int64_t bsq_kv_attention_workspace_bytes(int64_t total, int32_t heads, int32_t k
                                          int32_t max_q) {
   if (total < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || (dim != 64 && dim != 128) || batch < 0 || max_q < 0)
     return 0;
-  // a slot of 16 or 32 rows for each end of every block's run, whichever kernel runs
-  return kKvCounterBytes + int64_t(kKvMaxBlocks) * 2 * KvShape<128, 1>::kPartFloats * 4;
+  // a part of 16 rows for each of the blocks, or of 32 for half as many
+  return kKvCounterBytes + int64_t(kKvMaxBlocks) * KvShape<128, 1>::kPartFloats * 4;
 }
 
 int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t heads, int32_t kv_heads, int32_t dim,
@@ -180,7 +180,7 @@ int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t he
   a.causal = causal;
   a.window = window;
   a.scale_log2 = sm_scale * 1.4426950408889634f;
-  a.counters = static_cast<uint32_t*>(workspace);
+  a.ready = static_cast<uint32_t*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKvCounterBytes);
   a.err = d.error_word;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -316,11 +316,9 @@ __device__ __forceinline__ int moe_token_scale(int r, int s) { return (s >> 2) *
 // Wait until a counter in global memory reaches `value`, for about a second.
 __device__ __forceinline__ bool moe_wait_count(const uint32_t* p, uint32_t value, const volatile uint32_t* abort_flag) {
   if (ld_acquire(p) >= value) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (ld_acquire(p) < value) {
-    if (*abort_flag != 0u || globaltimer_ns() - t0 > kWaitLimitNs) return false;
-    __nanosleep(20);
-  }
+  const long long t0 = clock64();
+  while (ld_acquire(p) < value)
+    if (*abort_flag != 0u || clock64() - t0 > kWaitLimitCycles) return false;
   return true;
 }
 
@@ -461,7 +459,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           const uint8_t* s1 = scales + expert * scale_bytes + static_cast<int64_t>(r1 / 128) * kt * 512;
           for (int kc = u - item * p.chunks; u < stop; ++u, ++kc) {
             const int atoms = min(kAtoms, kt - kc * kAtoms);
-            if (!mbar_wait_bounded(&empty_bar[stage], phase_bit ^ 1u)) {
+            if (!mbar_wait_clocked(&empty_bar[stage], phase_bit ^ 1u)) {
               if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
               abort_flag = 1u;
             }
@@ -507,7 +505,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           const int row = tb.row0[i], n8 = (tb.row0[i + 1] - row + 7) >> 3;
           const uint8_t* s0 = scales + static_cast<int64_t>(i) * kt * 512;
           for (int kc = u - item * p.chunks; u < stop && ok; ++u, ++kc) {
-            ok = mbar_wait_bounded(&empty_bar[stage], phase_bit ^ 1u) && abort_flag == 0u;
+            ok = mbar_wait_clocked(&empty_bar[stage], phase_bit ^ 1u) && abort_flag == 0u;
             if (!ok) break;
             const int atoms = min(kAtoms, kt - kc * kAtoms);
             uint8_t* st = smem + stage * a.stage_bytes + 2 * kMoeHalfBytes;
@@ -539,12 +537,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         const bool two = phase == 0 || 256 * tile + 128 < rows;
         const uint32_t n = (tb.row0[i + 1] - tb.row0[i] + 15) & ~15u;
         const uint32_t buf = seg & 1u, d = tmem + buf * 128u;
-        ok = __all_sync(~0u, mbar_wait_bounded(&acc_empty[buf], ((seg >> 1) & 1u) ^ 1u) && abort_flag == 0u);
+        ok = __all_sync(~0u, mbar_wait_clocked(&acc_empty[buf], ((seg >> 1) & 1u) ^ 1u) && abort_flag == 0u);
         if (!ok) break;
         t5_fence_after();
         int kc = u - item * p.chunks;
         for (uint32_t fresh = 0; u < stop; ++u, ++kc) {
-          ok = __all_sync(~0u, mbar_wait_bounded(&full_bar[stage], phase_bit) && abort_flag == 0u);
+          ok = __all_sync(~0u, mbar_wait_clocked(&full_bar[stage], phase_bit) && abort_flag == 0u);
           if (!ok) break;
           t5_fence_after();
           const uint32_t st = smem_base + stage * a.stage_bytes;
@@ -571,7 +569,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       abort_flag = 1u;
     }
     t5_commit(smem_addr(&drain_bar), lead);
-    if (!mbar_wait_bounded(&drain_bar, 0) && lane == 0) record_error_at(a.err, kErrTimeout);
+    if (!mbar_wait_clocked(&drain_bar, 0) && lane == 0) record_error_at(a.err, kErrTimeout);
   } else if (warp >= 4) {
     // ---- quantize the tokens' rows, a block of 32 columns per thread at a time
     const int et = tid - 128, quarter = warp & 3;
@@ -624,7 +622,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             go = moe_wait_count(flag, 1u, &abort_flag);
             *flag = 0u;
           }
-          go = go && mbar_wait_bounded(&acc_full[buf], (seg >> 1) & 1u) && abort_flag == 0u;
+          go = go && mbar_wait_clocked(&acc_full[buf], (seg >> 1) & 1u) && abort_flag == 0u;
           last_flag = go ? 1u : 0u;
         }
         named_sync(1, 128);
@@ -754,7 +752,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       uint64_t* bar = &full_bar[f % stages];
       if (f >= fills_a) mbar_arrive(bar);
       if (f >= fills_b) mbar_arrive(bar);
-      if (!mbar_wait_bounded(bar, (f / stages) & 1u)) record_error_at(a.err, kErrTimeout);
+      if (!mbar_wait_clocked(bar, (f / stages) & 1u)) record_error_at(a.err, kErrTimeout);
     }
   }
   t5_fence_before();

@@ -8,6 +8,19 @@
 
 namespace bsq {
 
+// Waits are bounded by the SM's clock, about a second (the global timer that
+// mbar_wait_bounded reads costs about a microsecond when a wait is not over at once).
+constexpr long long kWaitLimitCycles = 2000000000ll;
+
+// Wait until the phase with the given parity has completed; false when the limit expired.
+__device__ __forceinline__ bool mbar_wait_clocked(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > kWaitLimitCycles) return false;
+  return true;
+}
+
 __device__ __forceinline__ void t5_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void t5_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
