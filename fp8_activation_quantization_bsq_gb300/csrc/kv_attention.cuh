@@ -14,15 +14,17 @@
 // output), and all sums are FP32.
 //
 // What bounds it: the cache is read once, about 2 x heads-per-kv-head operations
-// per byte, so DRAM.  Persistent blocks (two per SM) of four consumer warps and a
+// per byte, so DRAM.  Persistent blocks (one to three per SM) of four consumer warps and a
 // producer; the units, tiles of 64 keys of one (sequence, kv head, row tile), are cut
 // into equal runs, so that ragged lengths and long contexts spread evenly.  The
 // producer streams tiles by TMA through a ring.  Each consumer warp takes 16 of a tile's
-// keys for all 16 rows and keeps its own maximum, sum and accumulators, so warps meet
-// only at the end of an item.  mma.sync products: with 16 rows at most, a 128-row
-// tensor-memory product would be mostly padding.  Fragments come straight from the codes with wide
-// shared loads: the order of the dimension in q.k and of the output columns is free, so a thread takes
-// 16 consecutive bytes of a key, and pairs of keys are interleaved bytewise before conversion.
+// keys for all rows and keeps its own maximum, sums and accumulators, so warps meet
+// only at the end of an item.  mma.sync products: with 32 rows at most, a 128-row
+// tensor-memory product would be mostly padding.  The products are transposed, keys
+// (S^T = K Q^T) and dimensions (O^T = V^T P^T) as the 16-row side, so that 8 query rows (NT = 1) are no
+// padding either.  Fragments come straight from the codes with wide shared loads: the order of the
+// dimension in q.k and of the output rows is free, so a thread takes 16 consecutive bytes of a
+// key, and pairs of keys are interleaved bytewise before conversion.
 // An item cut by the runs is finished by the block that began it, which adds the other blocks' parts
 // in block order (first in groups of 16 where there are many): those blocks hold them at the start of
 // their runs, it at the end of its own.
@@ -185,18 +187,23 @@ struct KvPageScale {
   float kfac, ev, inv;
 };
 
-template <int D, int ROWG>
+// NT: tiles of 8 query rows.
+template <int D, int NT>
 struct KvShape {
-  static constexpr int kWarps = 4 * ROWG;                  // consumers
+  static constexpr int kWarps = 4;                         // consumers
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kRows = 16 * ROWG;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kPassRows = NT == 1 ? 8 : 16;       // rows merged at a time
+  // registers allow 15 warps per SM at 128, 10 at 168, 5 at 255 (five warps spread unevenly over four schedulers)
+  static constexpr int kBlocksPerSm = NT == 1 ? 3 : NT == 2 ? 2 : 1;
   static constexpr int kTileBytes = kKvTile * D;           // of keys, and of values
-  static constexpr int kStages = ROWG == 1 ? 4 : 6;
-  // merge buffer: a row's quarters of D / 4 floats lie 4 floats further apart, so that the 8 rows x 4 quarters
-  // of a warp's float4 stores fall into different banks
-  static constexpr int kQuarter = D / 4 + 4, kRow = 4 * kQuarter;
-  static constexpr int kMergeBytes = kWarps * 16 * kRow * 4;
-  static constexpr int kSmem = 1024 + kStages * 2 * kTileBytes + kMergeBytes;
+  static constexpr int kStages = NT == 1 ? 3 : NT == 2 ? 4 : 6;
+  // merge buffer: a row's eighths lie 4 floats further apart and rows 4 modulo
+  // 16, so that the rows and eighths of a warp's float4 stores fall into different banks
+  static constexpr int kEighth = D / 8 + 4, kRow = 8 * kEighth + 4;
+  static constexpr int kMergeBytes = kWarps * kPassRows * kRow * 4;
+  static constexpr int kQueryBytes = NT == 4 ? kRows * D * 2 : 0;
+  static constexpr int kSmem = 1024 + kStages * 2 * kTileBytes + kMergeBytes + kQueryBytes;
   static constexpr int kPartFloats = kRows * D + 2 * kRows;
 };
 
@@ -227,20 +234,28 @@ __device__ __forceinline__ bool kv_take_part(uint32_t* flag, const volatile uint
   return true;
 }
 
-template <int D, int ROWG, bool F16>
-__global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
+// An 8 x 8 matrix of 16-bit elements over the warp, transposed.
+__device__ __forceinline__ uint32_t kv_transpose(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+template <int D, int NT, bool F16>
+__global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlocksPerSm)
     kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const KvAttnArgs a) {
-  using S = KvShape<D, ROWG>;
+  using S = KvShape<D, NT>;
   constexpr int RT = S::kRows, kT = 32 * S::kWarps;
   constexpr int kQuads = D / 64;  // 16-byte loads of a key per thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   float* merge = reinterpret_cast<float*>(smem + S::kStages * 2 * S::kTileBytes);
+  [[maybe_unused]] uint4* query = reinterpret_cast<uint4*>(smem + S::kStages * 2 * S::kTileBytes + S::kMergeBytes);
   __shared__ uint64_t full_bar[S::kStages], empty_bar[S::kStages];
   __shared__ KvPageScale page_scale[S::kStages][4];
   __shared__ int64_t prefix[S::kThreads + 1];
   __shared__ KvStart start;
-  __shared__ float warp_m2[2][S::kWarps][16], warp_l2[2][S::kWarps][16];  // by parity of the item
+  __shared__ float warp_m2[2][S::kWarps][RT], warp_l2[2][S::kWarps][RT];  // by parity of the item
   __shared__ volatile uint32_t abort_flag, fills, used_tiles, go_on, joined;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -364,133 +379,178 @@ __global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
       abort_flag = 1u;
     }
   } else {
-    // ---- consumers: warp w takes keys 16 (w % 4) .. + 15 of each tile for rows 16 (w / 4) .. + 15
-    const int gq = lane >> 2, c = lane & 3, kw = warp & 3, rg = warp >> 2;
+    // ---- consumers: warp w takes keys 16 w .. + 15 of each tile, for all rows
+    const int gq = lane >> 2, c = lane & 3;
     uint32_t stage = 0, phase = 0, used = 0;
     bool ok = true;
     for (int item = 0; ok && walk.next(a, g); ++item) {
-      float(*warp_m)[16] = warp_m2[item & 1];
-      float(*warp_l)[16] = warp_l2[item & 1];
+      float(*warp_m)[RT] = warp_m2[item & 1];
+      float(*warp_l)[RT] = warp_l2[item & 1];
       const int rows = g.s.n * a.group, pos0 = g.s.len - g.s.n;
-      int pos[2];       // positions of this thread's two rows
-      float rowfac[2];  // sm_scale log2(e) 2^eq
-      uint32_t q[2][D / 8];
+      // Query rows 8 t + gq, dimensions D/4 c .. + D/4 - 1: the second operand
+      // of K Q^T.  For NT = 4 they stay in shared memory, which all warps read.
+      uint32_t q[NT == 4 ? 1 : NT][D / 8];
+      int pos[NT][2];       // positions of rows 8 t + 2 c, + 1: those of this thread's scores
+      float rowfac[NT][2];  // sm_scale log2(e) 2^eq
+      float m[NT][2], l[NT][2];
+      if (NT == 4) named_sync(1, kT);  // the last item's rows have been read
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = g.rt * RT + rg * 16 + gq + 8 * h;
-        pos[h] = pos0 + r / a.group;
+      for (int t = 0; t < NT; ++t) {
+        const int r = g.rt * RT + 8 * t + gq;
         float amax = 0.f;
         uint4 v[D / 32];
-        const uint16_t* src = a.q + (g.s.t0 + r / a.group) * a.q_tok + (g.head * a.group + r % a.group) * a.q_head + c * (D / 4);
+        const uint16_t* src = a.q + static_cast<int64_t>(g.s.t0 + r / a.group) * a.q_tok + (g.head * a.group + r % a.group) * a.q_head + c * (D / 4);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           v[i] = r < rows ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
-          uint32_t m = 0;
-          m = elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(m, v[i].x), v[i].y), v[i].z), v[i].w);
-          amax = fmaxf(amax, elem_absmax_final<F16>(m));
+          uint32_t x = 0;
+          x = elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(x, v[i].x), v[i].y), v[i].z), v[i].w);
+          amax = fmaxf(amax, elem_absmax_final<F16>(x));
         }
         amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
         // the row times 2^-eq has its largest magnitude in [2^12, 2^13)
         const int eq = amax > 0.f ? static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 12 : 0;
-        const float f = pow2f(min(max(-eq, -126), 127));
-        rowfac[h] = a.scale_log2 * pow2f(min(max(eq, -126), 127));
+        const float f = pow2f(min(max(-eq, -126), 127)), rf = a.scale_log2 * pow2f(min(max(eq, -126), 127));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t x[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 x = elem2_to_f32x2<F16>(w[j]);
-            q[h][4 * i + j] = f32x2_to_elem2<true>(x.x * f, x.y * f);
+            const float2 y = elem2_to_f32x2<F16>(w[j]);
+            x[j] = f32x2_to_elem2<true>(y.x * f, y.y * f);
+            if constexpr (NT != 4) q[t][4 * i + j] = x[j];
           }
+          if constexpr (NT == 4)  // every warp stores the same values' quarter
+            if (warp == t) query[(t * (D / 32) + i) * 32 + lane] = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          rowfac[t][h] = __shfl_sync(~0u, rf, 4 * (2 * c + h));
+          pos[t][h] = pos0 + (g.rt * RT + 8 * t + 2 * c + h) / a.group;
+          m[t][h] = -INFINITY;
+          l[t][h] = 0.f;
         }
       }
-      float o[D / 8][4];
+      if (NT == 4) named_sync(1, kT);
+      // O^T: dimensions D/8 gq + 2 i (elements 0, 1) and + 1 (2, 3), rows 8 t + 2 c (0, 2) and + 1 (1, 3)
+      float o[NT][D / 16][4];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
 
-      for (int t = g.tile0; t < g.tile1; ++t) {
+      for (int tile = g.tile0; tile < g.tile1; ++tile) {
         ok = __all_sync(~0u, mbar_wait_clocked(&full_bar[stage], phase) && abort_flag == 0u);
         if (!ok) break;
         const uint8_t* kd = smem + stage * 2 * S::kTileBytes;
         const uint8_t* vd = kd + S::kTileBytes;
-        const KvPageScale ps = page_scale[stage][(16 * kw) >> min(a.page_shift, 6)];
-        float s[2][4];
+        const KvPageScale ps = page_scale[stage][(16 * warp) >> min(a.page_shift, 6)];
+        // S^T: keys gq (elements 0, 1) and gq + 8 (2, 3), rows 2 c (0, 2) and + 1 (1, 3); two chains of products
+        float s[NT][4], s2[NT][4];
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
-          s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
-          const int r = 16 * kw + 8 * nb + gq;
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int j = 0; j < kQuads; ++j) {
-            const uint4 w = *reinterpret_cast<const uint4*>(kd + kv_chunk<D>(r, kQuads * c + j));
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+          for (int i = 0; i < 4; ++i) s[t][i] = s2[t][i] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int k = 4 * j + i;  // K slice: dimensions c D/4 + 4 k .. + 3
-              kv_mma(s[nb], q[0][2 * k], q[1][2 * k], q[0][2 * k + 1], q[1][2 * k + 1], e4m3x2_to_f16x2(x[i] & 0xFFFFu),
-                     e4m3x2_to_f16x2(x[i] >> 16));
+        for (int j = 0; j < kQuads; ++j) {
+          const uint4 u = *reinterpret_cast<const uint4*>(kd + kv_chunk<D>(16 * warp + gq, kQuads * c + j));
+          const uint4 w = *reinterpret_cast<const uint4*>(kd + kv_chunk<D>(16 * warp + 8 + gq, kQuads * c + j));
+          const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {w.x, w.y, w.z, w.w};
+          uint4 qv[NT == 4 ? NT : 1][2];
+          if constexpr (NT == 4) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) qv[t][i] = query[(t * (D / 32) + 2 * j + i) * 32 + lane];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // K slice: dimensions D/4 c + 16 j + 4 i .. + 3
+            const uint32_t a0 = e4m3x2_to_f16x2(x[i] & 0xFFFFu), a1 = e4m3x2_to_f16x2(y[i] & 0xFFFFu);
+            const uint32_t a2 = e4m3x2_to_f16x2(x[i] >> 16), a3 = e4m3x2_to_f16x2(y[i] >> 16);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              uint32_t b0, b1;
+              if constexpr (NT == 4) {
+                const uint4 z = qv[t][i >> 1];
+                b0 = i & 1 ? z.z : z.x;
+                b1 = i & 1 ? z.w : z.y;
+              } else {
+                b0 = q[t][8 * j + 2 * i];
+                b1 = q[t][8 * j + 2 * i + 1];
+              }
+              if (i & 1) kv_mma(s2[t], a0, a1, a2, a3, b0, b1);
+              else kv_mma(s[t], a0, a1, a2, a3, b0, b1);
             }
           }
         }
-        const int key0 = t * kKvTile + 16 * kw;
+        const int key0 = tile * kKvTile + 16 * warp;
         // keys that not all rows see, or none: only tiles at the range's ends
         const bool masked = ps.inv == 0.f || key0 < g.lo || key0 + 16 > g.hi || (a.causal && key0 + 15 > pos0 + g.rt * RT / a.group) ||
-                          (a.window > 0 && key0 <= pos0 + (min(rows, (g.rt + 1) * RT) - 1) / a.group - a.window);
+                            (a.window > 0 && key0 <= pos0 + (min(rows, (g.rt + 1) * RT) - 1) / a.group - a.window);
         // two copies of the rest, so that the tiles in between carry no masks
         const auto rest = [&](auto edge) {
-          float top[2] = {-INFINITY, -INFINITY};
-          const float f0 = rowfac[0] * ps.kfac, f1 = rowfac[1] * ps.kfac;
+          float top[NT][2];
+          bool raise = false;
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb) {
+          for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int h = i >> 1;
-              float x = s[nb][i] * (h ? f1 : f0) + ps.ev;
+              const int h = i & 1;
+              float x = (s[t][i] + s2[t][i]) * (rowfac[t][h] * ps.kfac) + ps.ev;
               if constexpr (decltype(edge)::value) {
-                const int key = key0 + 8 * nb + 2 * c + (i & 1);
-                const bool see = ps.inv != 0.f && key >= g.lo && key < g.hi && (!a.causal || key <= pos[h]) && (a.window <= 0 || key > pos[h] - a.window);
+                const int key = key0 + gq + 8 * (i >> 1);
+                const bool see = ps.inv != 0.f && key >= g.lo && key < g.hi && (!a.causal || key <= pos[t][h]) &&
+                                 (a.window <= 0 || key > pos[t][h] - a.window);
                 x = see ? x : -INFINITY;
               }
-              s[nb][i] = x;
-              top[h] = fmaxf(top[h], x);
+              s[t][i] = x;
             }
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 1));
-            top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 2));
-          }
-          if (__any_sync(~0u, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float mn = fmaxf(m[h], top[h]);
-              const float f = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - mn);
-              m[h] = mn;
-              l[h] *= f;
+              float x = fmaxf(s[t][h], s[t][2 + h]);
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+              top[t][h] = x;
+              raise |= x > m[t][h] + 8.f;
+            }
+          }
+          if (__any_sync(~0u, raise)) {
 #pragma unroll
-              for (int i = 0; i < D / 8; ++i) {
-                o[i][2 * h] *= f;
-                o[i][2 * h + 1] *= f;
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float mn = fmaxf(m[t][h], top[t][h]);
+                const float f = m[t][h] == -INFINITY ? 0.f : fast_exp2(m[t][h] - mn);
+                m[t][h] = mn;
+                l[t][h] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                  o[t][i][h] *= f;
+                  o[t][i][2 + h] *= f;
+                }
               }
             }
           }
-          const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
-          uint32_t p[2][2];
+          // P^T as the second operand: pairs of rows to pairs of keys
+          uint32_t p[NT][2];
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb) {
-            const float a0 = fast_exp2(s[nb][0] - m0), a1 = fast_exp2(s[nb][1] - m0);
-            const float b0 = fast_exp2(s[nb][2] - m1), b1 = fast_exp2(s[nb][3] - m1);
-            l[0] += (a0 + a1) * ps.inv;
-            l[1] += (b0 + b1) * ps.inv;
-            p[nb][0] = f32x2_to_elem2<true>(a0, a1);
-            p[nb][1] = f32x2_to_elem2<true>(b0, b1);
+          for (int t = 0; t < NT; ++t) {
+            const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+            const float x0 = fast_exp2(s[t][0] - m0), x1 = fast_exp2(s[t][1] - m1);
+            const float x2 = fast_exp2(s[t][2] - m0), x3 = fast_exp2(s[t][3] - m1);
+            l[t][0] += (x0 + x2) * ps.inv;
+            l[t][1] += (x1 + x3) * ps.inv;
+            p[t][0] = kv_transpose(f32x2_to_elem2<true>(x0, x1));
+            p[t][1] = kv_transpose(f32x2_to_elem2<true>(x2, x3));
           }
           // values: keys 2c, 2c + 1 and 8 + 2c, 9 + 2c; this thread's dimensions D/8 gq ..
           uint32_t vw[4][D / 32];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int r = 16 * kw + 8 * (k >> 1) + 2 * c + (k & 1);
+            const int r = 16 * warp + 8 * (k >> 1) + 2 * c + (k & 1);
             if constexpr (D == 128) {
               const uint4 w = *reinterpret_cast<const uint4*>(vd + kv_chunk<D>(r, gq));
               vw[k][0] = w.x; vw[k][1] = w.y; vw[k][2] = w.z; vw[k][3] = w.w;
@@ -499,7 +559,7 @@ __global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
               vw[k][0] = w.x; vw[k][1] = w.y;
             }
             if constexpr (decltype(edge)::value) {  // whatever lies outside the allowed keys (NaN codes too) counts as zero
-              const int key = t * kKvTile + r;
+              const int key = tile * kKvTile + r;
               if (key < g.lo || key >= g.hi || ps.inv == 0.f) {
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) vw[k][i] = 0u;
@@ -512,7 +572,10 @@ __global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
             kv_pairs(vw[0][i], vw[1][i], lo);
             kv_pairs(vw[2][i], vw[3][i], hi);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) kv_mma(o[4 * i + j], p[0][0], p[0][1], p[1][0], p[1][1], lo[j], hi[j]);
+            for (int t = 0; t < NT; ++t) {
+              kv_mma(o[t][2 * i], lo[0], lo[1], hi[0], hi[1], p[t][0], p[t][1]);
+              kv_mma(o[t][2 * i + 1], lo[2], lo[3], hi[2], hi[3], p[t][0], p[t][1]);
+            }
           }
         };
         if (masked) rest(std::true_type{}); else rest(std::false_type{});
@@ -525,80 +588,92 @@ __global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
         if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
         abort_flag = 1u;
       }
-      // ---- the item's share: the four key quarters of each row group meet
+      // ---- the item's share: the four warps' keys meet
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l[h] += __shfl_xor_sync(~0u, l[h], 1);
-        l[h] += __shfl_xor_sync(~0u, l[h], 2);
-        if (c == 0) {
-          warp_m[warp][gq + 8 * h] = m[h];
-          warp_l[warp][gq + 8 * h] = l[h];
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) l[t][h] += __shfl_xor_sync(~0u, l[t][h], d);
+          if (gq == 0) {
+            warp_m[warp][8 * t + 2 * c + h] = m[t][h];
+            warp_l[warp][8 * t + 2 * c + h] = l[t][h];
+          }
         }
       }
       named_sync(1, kT);
       if (tid == 0) go_on = abort_flag == 0u ? 1u : 0u;  // one answer for all warps
-      float* mw = merge + warp * 16 * S::kRow;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = gq + 8 * h;
-        float mm = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) mm = fmaxf(mm, warp_m[4 * rg + w][r]);
-        const float f = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - mm);
-        // columns 2c (first half) and 2c + 1 (second) of every product: D/4 consecutive dimensions
-#pragma unroll
-        for (int i = 0; i < D / 8; i += 4) {
-          float4* dst = reinterpret_cast<float4*>(mw + r * S::kRow + c * S::kQuarter + i);
-          dst[0] = make_float4(o[i][2 * h] * f, o[i + 1][2 * h] * f, o[i + 2][2 * h] * f, o[i + 3][2 * h] * f);
-          dst[D / 32] = make_float4(o[i][2 * h + 1] * f, o[i + 1][2 * h + 1] * f, o[i + 2][2 * h + 1] * f, o[i + 3][2 * h + 1] * f);
-        }
-      }
-      named_sync(1, kT);
-      ok = go_on != 0u;
       const int live = min(RT, rows - g.rt * RT);  // rows of the tile
-      // eight threads per row, float4s 8 q + tid % 8 of it
-      const int r = tid >> 3, wr = 4 * (r >> 4), r16 = r & 15;
-      float4 acc[D / 32];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const int d4 = 8 * i + (tid & 7);
-        const float* src = merge + (wr * 16 + r16) * S::kRow + d4 / (D / 16) * S::kQuarter + d4 % (D / 16) * 4;
-        const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 16 * S::kRow);
-        const float4 z = *reinterpret_cast<const float4*>(src + 32 * S::kRow), w = *reinterpret_cast<const float4*>(src + 48 * S::kRow);
-        acc[i] = make_float4((x.x + y.x) + (z.x + w.x), (x.y + y.y) + (z.y + w.y), (x.z + y.z) + (z.z + w.z), (x.w + y.w) + (z.w + w.w));
-      }
-      float am = -INFINITY, al = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) am = fmaxf(am, warp_m[wr + k][r16]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float wm = warp_m[wr + k][r16];
-        al += wm == -INFINITY ? 0.f : warp_l[wr + k][r16] * fast_exp2(wm - am);
-      }
       const int own0 = owner(g.first), own1 = owner(g.first + g.count - 1);
       const int me = static_cast<int>(blockIdx.x) - own0, count = own1 - own0 + 1;
-      if (ok && me % kKvJoin == 0 && count > 1) {
-        // parts of the group's other blocks, then (the item's first block) of the other groups' first blocks
-        const int near = min(kKvJoin, count - me) - 1, far = me == 0 ? (count - 1) / kKvJoin : 0;
-        if (warp == 0) {
-          bool got = true;
-          for (int p = lane; p < near + far && got; p += 32)
-            got = kv_take_part(a.ready + blockIdx.x + (p < near ? 1 + p : kKvJoin * (p - near + 1)), &abort_flag);
-          got = __all_sync(~0u, got);
-          if (lane == 0) {
-            if (!got) {
-              if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
-              abort_flag = 1u;
-            }
-            joined = got ? 1u : 0u;
+      // parts of the group's other blocks, then (the item's first block) of the other groups' first blocks
+      const int near = me % kKvJoin == 0 ? min(kKvJoin, count - me) - 1 : 0, far = me == 0 ? (count - 1) / kKvJoin : 0;
+      float* mine = a.part + static_cast<int64_t>(blockIdx.x) * S::kPartFloats;
+#pragma unroll
+      for (int pass = 0; pass < RT / S::kPassRows; ++pass) {
+        if (pass > 0) named_sync(1, kT);  // the buffer has been read
+        float* mw = merge + warp * S::kPassRows * S::kRow;
+#pragma unroll
+        for (int tt = 0; tt < S::kPassRows / 8; ++tt) {
+          const int t = pass * (S::kPassRows / 8) + tt;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = 8 * t + 2 * c + h;
+            float mm = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mm = fmaxf(mm, warp_m[w][row]);
+            const float f = m[t][h] == -INFINITY ? 0.f : fast_exp2(m[t][h] - mm);
+            float* dst = mw + (8 * tt + 2 * c + h) * S::kRow + gq * S::kEighth;
+#pragma unroll
+            for (int i = 0; i < D / 16; i += 2)
+              *reinterpret_cast<float4*>(dst + 2 * i) =
+                  make_float4(o[t][i][h] * f, o[t][i][2 + h] * f, o[t][i + 1][h] * f, o[t][i + 1][2 + h] * f);
           }
         }
         named_sync(1, kT);
-        ok = joined != 0u;
-        if (ok && r < live) {
+        ok = go_on != 0u;
+        if (ok && pass == 0 && near + far > 0) {
+          if (warp == 0) {
+            bool got = true;
+            for (int p = lane; p < near + far && got; p += 32)
+              got = kv_take_part(a.ready + blockIdx.x + (p < near ? 1 + p : kKvJoin * (p - near + 1)), &abort_flag);
+            got = __all_sync(~0u, got);
+            if (lane == 0) {
+              if (!got) {
+                if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
+                abort_flag = 1u;
+              }
+              joined = got ? 1u : 0u;
+            }
+          }
+          named_sync(1, kT);
+          if (joined == 0u) go_on = 0u;  // every thread, the same
+          ok = joined != 0u;
+        }
+        // eight threads per row, float4s 8 i + tid % 8 of it
+        const int rl = tid >> 3, r = pass * S::kPassRows + rl;
+        if (ok && rl < S::kPassRows && r < live) {
+          float4 acc[D / 32];
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const int d = 4 * (8 * i + (tid & 7));
+            const float* src = merge + rl * S::kRow + d / (D / 8) * S::kEighth + d % (D / 8);
+            constexpr int kWarpStride = S::kPassRows * S::kRow;
+            const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + kWarpStride);
+            const float4 z = *reinterpret_cast<const float4*>(src + 2 * kWarpStride), w = *reinterpret_cast<const float4*>(src + 3 * kWarpStride);
+            acc[i] = make_float4((x.x + y.x) + (z.x + w.x), (x.y + y.y) + (z.y + w.y), (x.z + y.z) + (z.z + w.z), (x.w + y.w) + (z.w + w.w));
+          }
+          float am = -INFINITY, al = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) am = fmaxf(am, warp_m[k][r]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float wm = warp_m[k][r];
+            al += wm == -INFINITY ? 0.f : warp_l[k][r] * fast_exp2(wm - am);
+          }
 #pragma unroll 4
           for (int p = 0; p < near + far; ++p) {
-            const float* part = a.part + static_cast<int64_t>(blockIdx.x + (p < near ? 1 + p : kKvJoin * (p - near + 1))) * S::kPartFloats;
+            const float* part = mine + static_cast<int64_t>(p < near ? 1 + p : kKvJoin * (p - near + 1)) * S::kPartFloats;
             float4 v[D / 32];
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(part + r * D) + 8 * i + (tid & 7));
@@ -612,29 +687,28 @@ __global__ void __launch_bounds__(KvShape<D, ROWG>::kThreads, ROWG == 1 ? 2 : 1)
             al = al * f0 + pl * f1;
             am = mm;
           }
+          if (me != 0) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) __stcg(reinterpret_cast<float4*>(mine + r * D) + 8 * i + (tid & 7), acc[i]);
+            if ((tid & 7) == 0) {
+              __stcg(mine + RT * D + r, am);
+              __stcg(mine + RT * D + RT + r, al);
+            }
+          } else {
+            const int rr = g.rt * RT + r;
+            const int64_t row = static_cast<int64_t>(g.s.t0 + rr / a.group) * a.heads + g.head * a.group + rr % a.group;
+            const float f = al > 0.f ? 1.f / al : 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+              *reinterpret_cast<uint2*>(a.out + row * D + 32 * i + 4 * (tid & 7)) =
+                  make_uint2(f32x2_to_elem2<F16>(acc[i].x * f, acc[i].y * f), f32x2_to_elem2<F16>(acc[i].z * f, acc[i].w * f));
+            if ((tid & 7) == 0 && a.lse != nullptr) a.lse[row] = al > 0.f ? (am + log2f(al)) * 0.6931471805599453f : -INFINITY;
+          }
         }
       }
       if (ok && me != 0) {
-        float* part = a.part + static_cast<int64_t>(blockIdx.x) * S::kPartFloats;
-        if (r < live) {
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) __stcg(reinterpret_cast<float4*>(part + r * D) + 8 * i + (tid & 7), acc[i]);
-          if ((tid & 7) == 0) {
-            __stcg(part + RT * D + r, am);
-            __stcg(part + RT * D + RT + r, al);
-          }
-        }
         named_sync(1, kT);
         if (tid == 0) st_release(a.ready + blockIdx.x, 1u);
-      } else if (ok && r < live) {
-        const int rr = g.rt * RT + r;
-        const int64_t row = static_cast<int64_t>(g.s.t0 + rr / a.group) * a.heads + g.head * a.group + rr % a.group;
-        const float f = al > 0.f ? 1.f / al : 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          *reinterpret_cast<uint2*>(a.out + row * D + 32 * i + 4 * (tid & 7)) =
-              make_uint2(f32x2_to_elem2<F16>(acc[i].x * f, acc[i].y * f), f32x2_to_elem2<F16>(acc[i].z * f, acc[i].w * f));
-        if ((tid & 7) == 0 && a.lse != nullptr) a.lse[row] = al > 0.f ? (am + log2f(al)) * 0.6931471805599453f : -INFINITY;
       }
       // the merge buffer and the flags are written again only after the first
       // barrier of the next item's end, which all threads reach after this

@@ -62,20 +62,22 @@ bool cache_map(CUtensorMap* map, const void* ptr, int dim, int page, int heads, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int ROWG, bool F16>
+template <int D, int NT, bool F16>
 bsq_status launch_attention(const KvAttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, const HostDevice& d,
                             cudaStream_t st) {
-  using S = KvShape<D, ROWG>;
-  auto kernel = kv_attention_kernel<D, ROWG, F16>;
+  using S = KvShape<D, NT>;
+  auto kernel = kv_attention_kernel<D, NT, F16>;
   if (bsq_status s = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem, d.index); s != BSQ_OK) return s;
-  const int grid = ROWG == 1 ? std::min(2 * d.sm_count, kKvMaxBlocks) : std::min(d.sm_count, kKvMaxBlocks / 2);
+  const int grid = std::min(d.sm_count * S::kBlocksPerSm, NT == 4 ? kKvMaxBlocks / 2 : kKvMaxBlocks);
   return launch_pdl(kernel, dim3(grid), dim3(S::kThreads), S::kSmem, st, mk, mv, a) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
 }
 
 template <int D, bool F16>
 bsq_status launch_attention_rows(const KvAttnArgs& a, int64_t max_rows, const CUtensorMap& mk, const CUtensorMap& mv,
                                  const HostDevice& d, cudaStream_t st) {
-  return max_rows <= 16 ? launch_attention<D, 1, F16>(a, mk, mv, d, st) : launch_attention<D, 2, F16>(a, mk, mv, d, st);
+  if (max_rows <= 8) return launch_attention<D, 1, F16>(a, mk, mv, d, st);
+  if (max_rows <= 16) return launch_attention<D, 2, F16>(a, mk, mv, d, st);
+  return launch_attention<D, 4, F16>(a, mk, mv, d, st);
 }
 
 }  // namespace
@@ -133,7 +135,7 @@ int64_t bsq_kv_attention_workspace_bytes(int64_t total, int32_t heads, int32_t k
   if (total < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || (dim != 64 && dim != 128) || batch < 0 || max_q < 0)
     return 0;
   // a part of 16 rows for each of the blocks, or of 32 for half as many
-  return kKvCounterBytes + int64_t(kKvMaxBlocks) * KvShape<128, 1>::kPartFloats * 4;
+  return kKvCounterBytes + int64_t(kKvMaxBlocks) * KvShape<128, 2>::kPartFloats * 4;
 }
 
 int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t heads, int32_t kv_heads, int32_t dim,
