@@ -13,7 +13,7 @@ LIB_DIR = os.path.join(PKG_DIR, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libbsq.so")
 
 SOURCES = ["bsq.cu", "kv_cache.cu", "moe.cu"]
-HEADERS = ["host_common.h", "tcgen05.cuh", "serving_common.cuh", "kv_append.cuh", "kv_attention.cuh", "moe_layer.cuh",
+HEADERS = ["host_common.h", "tcgen05.cuh", "serving_common.cuh", "kv_append.cuh", "kv_attention.cuh", "kv_prompt.cuh", "moe_layer.cuh",
            "device_common.cuh", "box_quant.cuh", "dense_quant.cuh", "grouped_quant.cuh", "interleave.cuh",
            "tensor_scale.cuh", "block_scaled_dot.cuh", "cluster.cuh", "gemm_quant.cuh", "grouped_token.cuh"]
 

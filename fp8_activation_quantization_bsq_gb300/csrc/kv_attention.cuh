@@ -88,16 +88,17 @@ __device__ __forceinline__ void kv_keys(const KvAttnArgs& a, const KvSeq& s, int
   lo = a.window > 0 ? max(0, s.len - s.n + i0 - a.window + 1) : 0;
   if (hi <= lo) lo = hi = 0;
 }
-// Units of an item: tiles of kKvTile keys, one for an item without keys (its rows are still written).
-__device__ __forceinline__ int kv_units(int lo, int hi) { return max(1, (hi + kKvTile - 1) / kKvTile - lo / kKvTile); }
+// Units of an item: tiles of TILE keys, one for an item without keys (its rows are still written).
+template <int TILE>
+__device__ __forceinline__ int kv_units(int lo, int hi) { return max(1, (hi + TILE - 1) / TILE - lo / TILE); }
 
-template <int RT>
+template <int RT, int TILE>
 __device__ __forceinline__ int64_t kv_seq_units(const KvAttnArgs& a, const KvSeq& s) {
   int64_t u = 0;
   for (int rt = 0; rt < s.row_tiles; ++rt) {
     int lo, hi;
     kv_keys<RT>(a, s, rt, lo, hi);
-    u += kv_units(lo, hi);
+    u += kv_units<TILE>(lo, hi);
   }
   return u;  // per kv head
 }
@@ -118,14 +119,14 @@ struct KvSegment {
 };
 
 // Walks the units [u, end) item by item.
-template <int RT>
+template <int RT, int TILE>
 struct KvWalk {
   int64_t u, end, before, per_head;
   int b;
   KvSeq s;
   __device__ __forceinline__ void load(const KvAttnArgs& a) {
     s = kv_seq<RT>(a, b, false);
-    per_head = kv_seq_units<RT>(a, s);
+    per_head = kv_seq_units<RT, TILE>(a, s);
   }
   __device__ __forceinline__ bool next(const KvAttnArgs& a, KvSegment& g) {
     if (u >= end) return false;
@@ -140,7 +141,7 @@ struct KvWalk {
     int rt = 0;
     while (true) {
       kv_keys<RT>(a, s, rt, g.lo, g.hi);
-      const int c = kv_units(g.lo, g.hi);
+      const int c = kv_units<TILE>(g.lo, g.hi);
       if (u < at + c) {
         g.first = at;
         g.count = c;
@@ -153,7 +154,7 @@ struct KvWalk {
     g.b = b;
     g.s = s;
     const int64_t stop = min(end, g.first + g.count);
-    g.tile0 = g.lo / kKvTile + static_cast<int>(u - g.first);
+    g.tile0 = g.lo / TILE + static_cast<int>(u - g.first);
     g.tile1 = g.hi > g.lo ? g.tile0 + static_cast<int>(stop - u) : g.tile0;
     u = stop;
     return true;
@@ -180,6 +181,50 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
           smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
       : "memory");
+}
+
+// Sum every sequence's units and find this block's run (by all THREADS of the
+// block; prefix: THREADS + 1 entries of shared memory); false for a block without one.
+template <int RT, int TILE, int THREADS>
+__device__ __forceinline__ bool kv_start(const KvAttnArgs& a, int64_t* prefix, KvStart* start) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int per = (a.batch + THREADS - 1) / THREADS;
+  const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += kv_seq_units<RT, TILE>(a, kv_seq<RT>(a, b, blockIdx.x == 0)) * a.kv_heads;
+  prefix[tid + 1] = mine;
+  if (tid == 0) prefix[0] = 0;
+  __syncthreads();
+  if (tid < 32) {  // inclusive sums, 32 at a time
+    int64_t carry = 0;
+    for (int i = 0; i < THREADS; i += 32) {
+      int64_t v = prefix[1 + i + lane];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(~0u, v, d);
+        if (lane >= d) v += o;
+      }
+      prefix[1 + i + lane] = carry + v;
+      carry += __shfl_sync(~0u, v, 31);
+    }
+  }
+  __syncthreads();
+  const int64_t total = prefix[THREADS], parts = min(total, static_cast<int64_t>(gridDim.x));
+  if (blockIdx.x >= parts) return false;
+  const int64_t begin = total * blockIdx.x / parts;
+  if (prefix[tid] <= begin && begin < prefix[tid + 1]) {
+    int64_t before = prefix[tid];
+    int b = b0;
+    while (true) {
+      const int64_t c = kv_seq_units<RT, TILE>(a, kv_seq<RT>(a, b, false)) * a.kv_heads;
+      if (begin < before + c) break;
+      before += c;
+      ++b;
+    }
+    *start = {total, before, b};
+  }
+  __syncthreads();
+  return true;
 }
 
 // Per page of a stage: factor of the scores, exponent of the values, and its reciprocal power.
@@ -272,49 +317,11 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
   }
   pdl_wait();
 
-  // ---- every sequence's units, and this block's run
-  {
-    const int per = (a.batch + S::kThreads - 1) / S::kThreads;
-    const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += kv_seq_units<RT>(a, kv_seq<RT>(a, b, blockIdx.x == 0)) * a.kv_heads;
-    prefix[tid + 1] = mine;
-    if (tid == 0) prefix[0] = 0;
-    __syncthreads();
-    if (warp == 0) {  // inclusive sums, 32 at a time
-      int64_t carry = 0;
-      for (int i = 0; i < S::kThreads; i += 32) {
-        int64_t v = prefix[1 + i + lane];
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int64_t o = __shfl_up_sync(~0u, v, d);
-          if (lane >= d) v += o;
-        }
-        prefix[1 + i + lane] = carry + v;
-        carry += __shfl_sync(~0u, v, 31);
-      }
-    }
-    __syncthreads();
-    const int64_t total = prefix[S::kThreads], parts = min(total, static_cast<int64_t>(gridDim.x));
-    if (blockIdx.x >= parts) return;  // the whole block
-    const int64_t begin = total * blockIdx.x / parts;
-    if (prefix[tid] <= begin && begin < prefix[tid + 1]) {
-      int64_t before = prefix[tid];
-      int b = b0;
-      while (true) {
-        const int64_t c = kv_seq_units<RT>(a, kv_seq<RT>(a, b, false)) * a.kv_heads;
-        if (begin < before + c) break;
-        before += c;
-        ++b;
-      }
-      start = {total, before, b};
-    }
-    __syncthreads();
-  }
+  if (!kv_start<RT, kKvTile, S::kThreads>(a, prefix, &start)) return;  // the whole block
   const int64_t total = start.total, parts = min(total, static_cast<int64_t>(gridDim.x));
   // the block whose run holds unit u
   const auto owner = [&](int64_t u) { return static_cast<int>(((u + 1) * parts - 1) / total); };
-  KvWalk<RT> walk;
+  KvWalk<RT, kKvTile> walk;
   walk.u = total * blockIdx.x / parts;
   walk.end = total * (blockIdx.x + 1) / parts;
   walk.before = start.before;

@@ -6,6 +6,7 @@
 #include "host_common.h"
 #include "kv_append.cuh"
 #include "kv_attention.cuh"
+#include "kv_prompt.cuh"
 
 namespace {
 
@@ -43,10 +44,13 @@ cudaError_t launch_append(const KvAppendArgs& a, cudaStream_t st) {
   }
 }
 
+// Rows (query tokens x heads of a kv head) up to which the kernel for few rows runs.
+constexpr int kKvFewRows = 32;
+
 // The cache as a 4D tensor of bytes (dimension, token, head, page), in boxes
-// of a head's tokens, at most a tile of them.
+// of a head's tokens, at most `tile` of them.
 bool cache_map(CUtensorMap* map, const void* ptr, int dim, int page, int heads, int64_t pages, int64_t cs_tok, int64_t cs_head,
-               int64_t cs_page) {
+               int64_t cs_page, int tile, CUtensorMapSwizzle swizzle) {
   auto enc = encode_tiled();
   if (!enc) return false;
   // the stride of an extent of one is never used, but has to be valid
@@ -55,10 +59,10 @@ bool cache_map(CUtensorMap* map, const void* ptr, int dim, int page, int heads, 
   const cuuint64_t size[4] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(pages)};
   const cuuint64_t stride[3] = {static_cast<cuuint64_t>(cs_tok), static_cast<cuuint64_t>(cs_head), static_cast<cuuint64_t>(cs_page)};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(dim), static_cast<cuuint32_t>(std::min(page, kKvTile)), 1, 1};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(dim), static_cast<cuuint32_t>(std::min(page, tile)), 1, 1};
   const cuuint32_t ones[4] = {1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), size, stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -77,7 +81,12 @@ bsq_status launch_attention_rows(const KvAttnArgs& a, int64_t max_rows, const CU
                                  const HostDevice& d, cudaStream_t st) {
   if (max_rows <= 8) return launch_attention<D, 1, F16>(a, mk, mv, d, st);
   if (max_rows <= 16) return launch_attention<D, 2, F16>(a, mk, mv, d, st);
-  return launch_attention<D, 4, F16>(a, mk, mv, d, st);
+  if (max_rows <= kKvFewRows) return launch_attention<D, 4, F16>(a, mk, mv, d, st);
+  auto kernel = kv_prompt_kernel<D, F16>;
+  if (bsq_status s = allow_smem(reinterpret_cast<const void*>(kernel), KpShape<D>::kSmem, d.index); s != BSQ_OK) return s;
+  return launch_pdl(kernel, dim3(std::min(d.sm_count, kKpMaxBlocks)), dim3(kKpThreads), KpShape<D>::kSmem, st, mk, mv, a) == cudaSuccess
+             ? BSQ_OK
+             : BSQ_ERR_CUDA;
 }
 
 }  // namespace
@@ -134,6 +143,8 @@ int64_t bsq_kv_attention_workspace_bytes(int64_t total, int32_t heads, int32_t k
                                          int32_t max_q) {
   if (total < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || (dim != 64 && dim != 128) || batch < 0 || max_q < 0)
     return 0;
+  if (static_cast<int64_t>(max_q) * (heads / kv_heads) > kKvFewRows)
+    return kKvCounterBytes + int64_t(kKpMaxBlocks) * (dim == 64 ? KpShape<64>::kPartFloats : KpShape<128>::kPartFloats) * 4;
   // a part of 16 rows for each of the blocks, or of 32 for half as many
   return kKvCounterBytes + int64_t(kKvMaxBlocks) * KvShape<128, 2>::kPartFloats * 4;
 }
@@ -187,10 +198,13 @@ int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t he
   a.err = d.error_word;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap mk, mv;
-  if (!cache_map(&mk, k_cache, dim, page, kv_heads, num_pages, cs_tok, cs_head, cs_page) ||
-      !cache_map(&mv, v_cache, dim, page, kv_heads, num_pages, cs_tok, cs_head, cs_page))
-    return BSQ_ERR_CUDA;
   const int64_t max_rows = static_cast<int64_t>(max_q) * a.group;
+  const bool few = max_rows <= kKvFewRows;
+  const int tile = few ? kKvTile : kKpKeys;
+  const CUtensorMapSwizzle swizzle = !few ? CU_TENSOR_MAP_SWIZZLE_NONE : dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  if (!cache_map(&mk, k_cache, dim, page, kv_heads, num_pages, cs_tok, cs_head, cs_page, tile, swizzle) ||
+      !cache_map(&mv, v_cache, dim, page, kv_heads, num_pages, cs_tok, cs_head, cs_page, tile, swizzle))
+    return BSQ_ERR_CUDA;
   if (dim == 64)
     return dtype == BSQ_F16 ? launch_attention_rows<64, true>(a, max_rows, mk, mv, d, st)
                             : launch_attention_rows<64, false>(a, max_rows, mk, mv, d, st);

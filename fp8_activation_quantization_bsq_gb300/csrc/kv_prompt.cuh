@@ -1,0 +1,521 @@
+// Attention over the 8-bit paged cache, for many query rows per kv head
+// (prompts and chunks of them).  The mathematics, the folding of the page
+// scales and the equal runs are those of kv_attention.cuh; here the rows fill
+// 128-row products of the tcgen05 tensor cores.
+//
+// A unit is 128 keys of a tile of 256 rows (query tokens x heads of a kv head), as two halves of
+// 128.  Per unit and half: S = Q K^T into tensor memory, the softmax weights P
+// (FP16) over S in place, O += P V with P as the tensor-memory operand.  With both halves in
+// flight the tensor cores compute one half's products while the other's softmax runs.
+// What bounds it: 4 x 256 x 128 x D operations a unit against 256 x 128
+// exponentials and the conversions below; the softmax warps' issue slots come first.
+//  * warps 0-3 and 4-7: the halves' softmax, a thread per row: the row's
+//    maximum in a first pass over S, weights and their sum in a second (S is read from
+//    tensor memory twice, which keeps it out of registers).  O is rescaled only where a row's
+//    maximum grew by more than 2^8.  They also bring the query rows (a power of two per row, so
+//    that they are exact in FP16) and write the output.
+//  * warps 8-11: E4M3 tiles to FP16 in the 128-byte-swizzled layout that both
+//    products read (K as rows of the dimension, V as rows of keys, the same bytes); keys outside the
+//    item's range become zeros.
+//  * warp 12: TMA of the codes, page by page; warp 13: the products.
+#pragma once
+
+#include "kv_attention.cuh"
+
+namespace bsq {
+
+constexpr int kKpKeys = 128, kKpRows = 256, kKpThreads = 512;
+constexpr int kKpRaw = 4, kKpWide = 3;  // rings of E4M3 and FP16 tiles: K, V, K, V, ...
+constexpr int kKpSlots = 8;             // units whose page scales are kept
+constexpr int kKpMaxBlocks = 256;
+
+template <int D>
+struct KpShape {
+  static constexpr int kRawBytes = kKpKeys * D, kWideBytes = 2 * kRawBytes;
+  static constexpr int kHalfBytes = 128 * D * 2;  // query rows of a half
+  static constexpr int kSmem = 1024 + 2 * kHalfBytes + kKpWide * kWideBytes + kKpRaw * kRawBytes;
+  static constexpr int kPartFloats = kKpRows * D + 2 * kKpRows;  // [d][row], maxima, sums
+};
+
+// Page scales of a unit (up to 8 pages of 16 tokens); bad: some page is missing.
+struct KpSlot {
+  KvPageScale sc[8];
+  int bad;
+};
+
+// A half's softmax state of one row.
+struct KpRow {
+  float m, l, fac;
+  int pos;
+  bool live;
+};
+
+// Scores of 16 keys, scaled and masked: x = s f + ev, -inf where the row does not see the key.
+template <bool EDGE>
+__device__ __forceinline__ float kp_score(const KvAttnArgs& a, const KpRow& row, float s, float f, const KvPageScale& ps, int key,
+                                          int lo, int hi) {
+  const float x = fmaf(s, f, ps.ev);
+  if constexpr (!EDGE) return x;
+  const bool see = ps.inv != 0.f && key >= lo && key < hi && (!a.causal || key <= row.pos) && (a.window <= 0 || key > row.pos - a.window);
+  return see ? x : -INFINITY;
+}
+
+template <bool EDGE>
+__device__ __forceinline__ float kp_top(const KvAttnArgs& a, const KpRow& row, uint32_t taddr, const KpSlot& slot, int shift, int key0,
+                                        int lo, int hi) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < kKpKeys; c += 32) {
+    float x[32];
+    t5_ld32(taddr + c, x);
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      const KvPageScale ps = slot.sc[(c + h) >> shift];
+      const float f = row.fac * ps.kfac;
+      if constexpr (EDGE) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, kp_score<true>(a, row, x[h + i], f, ps, key0 + c + h + i, lo, hi));
+      } else {
+        float m = x[h];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) m = fmaxf(m, x[h + i]);
+        top = fmaxf(top, fmaf(m, f, ps.ev));  // f >= 0
+      }
+    }
+  }
+  return top;
+}
+
+// Weights of the unit over its scores; returns their sum (of 2^(t - m) 2^-ev).
+template <bool EDGE>
+__device__ __forceinline__ float kp_weights(const KvAttnArgs& a, const KpRow& row, uint32_t taddr, const KpSlot& slot, int shift,
+                                            int key0, int lo, int hi, float m) {
+  float sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < kKpKeys; c += 32) {
+    float x[32];
+    t5_ld32(taddr + c, x);
+    uint32_t p[16];
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      KvPageScale ps = slot.sc[(c + h) >> shift];
+      const float f = row.fac * ps.kfac;
+      float part = 0.f;
+      if constexpr (!EDGE) ps.ev -= m;
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        float w0, w1;
+        if constexpr (EDGE) {
+          w0 = fast_exp2(kp_score<true>(a, row, x[h + i], f, ps, key0 + c + h + i, lo, hi) - m);
+          w1 = fast_exp2(kp_score<true>(a, row, x[h + i + 1], f, ps, key0 + c + h + i + 1, lo, hi) - m);
+        } else {
+          w0 = fast_exp2(fmaf(x[h + i], f, ps.ev));
+          w1 = fast_exp2(fmaf(x[h + i + 1], f, ps.ev));
+        }
+        part += w0 + w1;
+        p[(h + i) / 2] = f32x2_to_elem2<true>(w0, w1);
+      }
+      sum = fmaf(part, ps.inv, sum);
+    }
+    t5_st16(taddr + c / 2, p);  // over scores that have been read
+  }
+  return sum;
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kKpThreads, 1)
+    kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const KvAttnArgs a) {
+  using S = KpShape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint8_t* wide = smem + 2 * S::kHalfBytes;
+  uint8_t* raw = wide + kKpWide * S::kWideBytes;
+  __shared__ uint64_t raw_full[kKpRaw], raw_empty[kKpRaw], wide_full[kKpWide], wide_empty[kKpWide];
+  __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drain_bar;
+  __shared__ KpSlot slots[kKpSlots];
+  __shared__ KvStart start;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t abort_flag, fills, used_tiles, go_on, joined;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kKpRaw; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
+    for (int i = 0; i < kKpWide; ++i) {
+      mbar_init(&wide_full[i], 4);
+      mbar_init(&wide_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(&drain_bar, 1);
+    abort_flag = 0u;
+    fills = used_tiles = 0u;
+    fence_mbar_init();
+    prefetch_tensormap(&map_k);
+    prefetch_tensormap(&map_v);
+  }
+  pdl_wait();
+  int64_t* prefix = reinterpret_cast<int64_t*>(raw);  // before the ring is in use
+  if (!kv_start<kKpRows, kKpKeys, kKpThreads>(a, prefix, &start)) return;  // the whole block
+  fence_async();  // the ring's next writes are TMA's
+  if (warp == 13) t5_alloc(&tmem_slot, 512);
+  t5_fence_before();
+  __syncthreads();
+  t5_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int64_t total = start.total, parts = min(total, static_cast<int64_t>(gridDim.x));
+  const auto owner = [&](int64_t u) { return static_cast<int>(((u + 1) * parts - 1) / total); };
+  KvWalk<kKpRows, kKpKeys> walk;
+  walk.u = total * blockIdx.x / parts;
+  walk.end = total * (blockIdx.x + 1) / parts;
+  walk.before = start.before;
+  walk.b = start.seq;
+  walk.load(a);
+  KvSegment g;
+  const auto fail = [&]() {
+    if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
+    abort_flag = 1u;
+  };
+
+  if (warp == 12) {
+    // ---- codes
+    uint32_t n = 0, unit = 0;
+    const int box = min(a.page, kKpKeys), boxes = kKpKeys / box;
+    bool ok = true;
+    while (ok && walk.next(a, g)) {
+      const int32_t* table = a.table + static_cast<int64_t>(g.b) * a.table_ld;
+      const int pages = (g.hi + a.page - 1) >> a.page_shift;  // beyond these no entry is read
+      int batch0 = -1, pid = -1;
+      KvPageScale sc{};
+      for (int t = g.tile0; t < g.tile1 && ok; ++t, ++unit) {
+        const int pg0 = (t * kKpKeys) >> a.page_shift;
+        if (batch0 < 0 || pg0 + boxes > batch0 + 32) {
+          batch0 = pg0;
+          const int pg = pg0 + lane;
+          pid = pg < pages ? table[pg] : -1;
+          const bool valid = pid >= 0 && pid < a.num_pages;
+          if (pg < pages && !valid && (pg + 1) << a.page_shift > g.lo) record_error_at(a.err, kErrValue);
+          sc = {0.f, -INFINITY, 0.f};
+          if (valid) {
+            const int64_t at = static_cast<int64_t>(pid) * a.kv_heads + g.head;
+            const int ek = a.scales[0][at], ev = a.scales[1][at];
+            sc.kfac = pow2f(min(max(ek - 127, -126), 127));
+            sc.ev = static_cast<float>(ev - 127);
+            sc.inv = pow2f(min(max(127 - ev, -126), 127));
+          } else {
+            pid = -1;
+          }
+        }
+        const int first = pg0 - batch0;
+        const uint32_t got = __ballot_sync(~0u, pid >= 0) >> first & ((1u << boxes) - 1u);
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t slot = n % kKpRaw;
+          ok = __all_sync(~0u, mbar_wait_clocked(&raw_empty[slot], (n / kKpRaw & 1u) ^ 1u) && abort_flag == 0u);
+          if (!ok) break;
+          if (kv == 0) {  // the softmax reads these after the unit's scores, long before 8 units on
+            if (lane >= first && lane < first + boxes) slots[unit % kKpSlots].sc[lane - first] = sc;
+            if (lane == 0) slots[unit % kKpSlots].bad = got != (1u << boxes) - 1u;
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], __popc(got) * box * D);
+          for (int i = 0; i < boxes; ++i) {
+            const int id = __shfl_sync(~0u, pid, first + i);
+            if (lane == 0 && id >= 0)
+              tma_load_4d(raw + slot * S::kRawBytes + i * box * D, kv == 0 ? &map_k : &map_v, 0, (t * kKpKeys + i * box) & (a.page - 1),
+                          g.head, id, &raw_full[slot]);
+          }
+          ++n;
+          if (lane == 0) fills = n;
+        }
+      }
+    }
+    if (!ok && lane == 0) fail();
+  } else if (warp >= 8 && warp < 12) {
+    // ---- E4M3 to FP16
+    const int ct = tid - 256;
+    constexpr int kRowThreads = D / 16, kRowsPerIter = 128 / kRowThreads;
+    uint32_t n = 0, unit = 0;
+    bool ok = true;
+    while (ok && walk.next(a, g)) {
+      for (int t = g.tile0; t < g.tile1 && ok; ++t, ++unit) {
+        const bool ends = t * kKpKeys < g.lo || (t + 1) * kKpKeys > g.hi;
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++n) {
+          const uint32_t r = n % kKpRaw, w = n % kKpWide;
+          ok = __all_sync(~0u, mbar_wait_clocked(&raw_full[r], n / kKpRaw & 1u) &&
+                                   mbar_wait_clocked(&wide_empty[w], (n / kKpWide & 1u) ^ 1u) && abort_flag == 0u);
+          if (!ok) break;
+          const uint8_t* src = raw + r * S::kRawBytes;
+          uint8_t* dst = wide + w * S::kWideBytes;
+          const KpSlot& slot = slots[unit % kKpSlots];
+          const bool some = ends || slot.bad != 0;
+          const int c = ct % kRowThreads;       // 16 dimensions
+          const int block = c >> 2, odd = block;  // 64 dimensions; the second block's lanes store their halves the other way round
+#pragma unroll 4
+          for (int i = 0; i < 128 / kRowsPerIter; ++i) {
+            const int key = i * kRowsPerIter + ct / kRowThreads;
+            uint4 v = *reinterpret_cast<const uint4*>(src + key * D + 16 * c);
+            if (some) {
+              const int k = t * kKpKeys + key;
+              if (k < g.lo || k >= g.hi || slot.sc[key >> a.page_shift].inv == 0.f) v = make_uint4(0, 0, 0, 0);
+            }
+            const uint4 lo = make_uint4(e4m3x2_to_f16x2(v.x & 0xFFFFu), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y & 0xFFFFu),
+                                        e4m3x2_to_f16x2(v.y >> 16));
+            const uint4 hi = make_uint4(e4m3x2_to_f16x2(v.z & 0xFFFFu), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w & 0xFFFFu),
+                                        e4m3x2_to_f16x2(v.w >> 16));
+            uint8_t* row = dst + block * (kKpKeys * 128) + key * 128;
+            const int ch = 2 * (c & 3);
+            *reinterpret_cast<uint4*>(row + (((ch + odd) ^ (key & 7)) << 4)) = odd ? hi : lo;
+            *reinterpret_cast<uint4*>(row + (((ch + 1 - odd) ^ (key & 7)) << 4)) = odd ? lo : hi;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&wide_full[w]);
+            mbar_arrive(&raw_empty[r]);
+          }
+          if (ct == 0) used_tiles = n + 1;
+        }
+      }
+    }
+    if (!ok && lane == 0) fail();
+  } else if (warp == 13) {
+    // ---- products
+    const uint32_t lead = t5_elect();
+    const uint32_t q_addr = smem_addr(smem), wide_addr = smem_addr(wide);
+    constexpr uint32_t kIdS = t5_idesc_f16(kKpKeys, false), kIdO = t5_idesc_f16(D, true);
+    uint32_t n = 0, queries[2] = {0u, 0u}, k[2] = {0u, 0u};
+    bool ok = true;
+    const auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(~0u, mbar_wait_clocked(bar, parity) && abort_flag == 0u); };
+    const auto scores = [&](int h, uint32_t w) {  // S of half h: tensor memory columns 128 h ..
+      const uint32_t qa = q_addr + h * S::kHalfBytes, ka = wide_addr + w * S::kWideBytes;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+        t5_mma_f16(tmem + 128 * h, t5_desc_sw128(qa + (i >> 2) * 16384 + 32 * (i & 3)), t5_desc_sw128(ka + (i >> 2) * 16384 + 32 * (i & 3)),
+                   kIdS, i, lead);
+      t5_commit(smem_addr(&s_full[h]), lead);
+    };
+    const auto values = [&](int h, uint32_t w, uint32_t accumulate) {  // O of half h: columns 256 + 128 h ..
+      const uint32_t va = wide_addr + w * S::kWideBytes;
+#pragma unroll
+      for (int i = 0; i < kKpKeys / 16; ++i)
+        t5_mma_f16_ta(tmem + 256 + 128 * h, tmem + 128 * h + 8 * i, t5_desc_sw128_n(va + 2048 * i, 16384), kIdO, accumulate | i, lead);
+      t5_commit(smem_addr(&pv_done[h]), lead);
+    };
+    while (ok && walk.next(a, g)) {
+      const int units = g.tile1 - g.tile0;
+      const bool two = g.s.n * a.group - g.rt * kKpRows > 128;
+      if (units > 0) {
+        ok = wait(&q_full[0], queries[0]++ & 1u) && (!two || wait(&q_full[1], queries[1]++ & 1u)) &&
+             wait(&wide_full[n % kKpWide], n / kKpWide & 1u);
+        if (!ok) break;
+        t5_fence_after();
+        scores(0, n % kKpWide);
+        if (two) scores(1, n % kKpWide);
+        t5_commit(smem_addr(&wide_empty[n % kKpWide]), lead);
+        ++n;
+      }
+      for (int u = 0; u < units && ok; ++u) {
+        const uint32_t v = n, nk = n + 1;  // this unit's values, the next one's keys
+        const bool more = u + 1 < units;
+        ok = wait(&wide_full[v % kKpWide], v / kKpWide & 1u) && (!more || wait(&wide_full[nk % kKpWide], nk / kKpWide & 1u));
+        for (int h = 0; h < (two ? 2 : 1) && ok; ++h) {
+          ok = wait(&p_full[h], k[h] & 1u);
+          if (!ok) break;
+          ++k[h];
+          t5_fence_after();
+          values(h, v % kKpWide, u);
+          if (h == (two ? 1 : 0)) t5_commit(smem_addr(&wide_empty[v % kKpWide]), lead);
+          if (more) scores(h, nk % kKpWide);
+        }
+        if (ok && more) t5_commit(smem_addr(&wide_empty[nk % kKpWide]), lead);
+        n += more ? 2 : 1;
+      }
+    }
+    if (!ok && lane == 0) fail();
+    t5_commit(smem_addr(&drain_bar), lead);
+    if (!mbar_wait_clocked(&drain_bar, 0) && lane == 0) record_error_at(a.err, kErrTimeout);
+  } else if (warp < 8) {
+    // ---- softmax of half `half`, a thread per row
+    const int half = warp >> 2, quarter = warp & 3, r_half = 32 * quarter + lane, r_tile = 128 * half + r_half;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+    const uint32_t ts = lanes + 128 * half, to = lanes + 256 + 128 * half;
+    const int shift = min(a.page_shift, 7);
+    uint32_t unit = 0, k = 0;
+    bool ok = true;
+    while (ok && walk.next(a, g)) {
+      const int rows = g.s.n * a.group, r = g.rt * kKpRows + r_tile, pos0 = g.s.len - g.s.n;
+      const int half_rows = min(128, rows - g.rt * kKpRows - 128 * half);  // <= 0: the half is empty
+      const bool busy = half_rows > 0 && g.tile1 > g.tile0;
+      const int64_t out_row = static_cast<int64_t>(g.s.t0 + r / a.group) * a.heads + g.head * a.group + r % a.group;
+      KpRow row{-INFINITY, 0.f, 0.f, pos0 + r / a.group, r < rows};
+      if (busy) {
+        // the query row in FP16, 2^-eq of it, largest magnitude in [2^12, 2^13)
+        const uint16_t* src = a.q + static_cast<int64_t>(g.s.t0 + r / a.group) * a.q_tok + (g.head * a.group + r % a.group) * a.q_head;
+        float amax = 0.f;
+        if (row.live) {
+          uint32_t x = 0;
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
+            x = elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(x, v.x), v.y), v.z), v.w);
+          }
+          amax = elem_absmax_final<F16>(x);
+        }
+        const int eq = amax > 0.f ? static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 12 : 0;
+        const float f = copysignf(pow2f(min(max(-eq, -126), 127)), a.scale_log2);  // scores times a factor >= 0
+        row.fac = fabsf(a.scale_log2) * pow2f(min(max(eq, -126), 127));
+        uint8_t* dst = smem + half * S::kHalfBytes + r_half * 128;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 v = row.live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+          const float2 x = elem2_to_f32x2<F16>(v.x), y = elem2_to_f32x2<F16>(v.y), z = elem2_to_f32x2<F16>(v.z), w = elem2_to_f32x2<F16>(v.w);
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * 16384 + (((i & 7) ^ (r_half & 7)) << 4)) =
+              make_uint4(f32x2_to_elem2<true>(x.x * f, x.y * f), f32x2_to_elem2<true>(y.x * f, y.y * f),
+                         f32x2_to_elem2<true>(z.x * f, z.y * f), f32x2_to_elem2<true>(w.x * f, w.y * f));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[half]);
+      }
+      const int last_row = min(rows, g.rt * kKpRows + 128 * (half + 1)) - 1, first_row = g.rt * kKpRows + 128 * half;
+      for (int t = g.tile0; t < g.tile1; ++t, ++unit) {
+        if (!busy) continue;
+        ok = __all_sync(~0u, mbar_wait_clocked(&s_full[half], k & 1u) && abort_flag == 0u);
+        if (!ok) break;
+        t5_fence_after();
+        const KpSlot& slot = slots[unit % kKpSlots];
+        const int key0 = t * kKpKeys;
+        const bool masked = slot.bad != 0 || key0 < g.lo || key0 + kKpKeys > g.hi ||
+                            (a.causal && key0 + kKpKeys - 1 > pos0 + first_row / a.group) ||
+                            (a.window > 0 && key0 <= pos0 + last_row / a.group - a.window);
+        const float top = masked ? kp_top<true>(a, row, ts, slot, shift, key0, g.lo, g.hi)
+                                 : kp_top<false>(a, row, ts, slot, shift, key0, g.lo, g.hi);
+        if (__any_sync(~0u, top > row.m + 8.f)) {
+          const float mn = fmaxf(row.m, top), f = row.m == -INFINITY ? 0.f : fast_exp2(row.m - mn);
+          row.m = mn;
+          row.l *= f;
+          if (t > g.tile0) {  // O holds the units before: wait for the last of them
+            ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u) && abort_flag == 0u);
+            if (!ok) break;
+            t5_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float x[32];
+              t5_ld32(to + c, x);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] *= f;
+              t5_st32(to + c, x);
+            }
+          }
+        }
+        const float m = row.m == -INFINITY ? 0.f : row.m;
+        row.l += masked ? kp_weights<true>(a, row, ts, slot, shift, key0, g.lo, g.hi, m)
+                        : kp_weights<false>(a, row, ts, slot, shift, key0, g.lo, g.hi, m);
+        t5_st_wait();
+        t5_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[half]);
+        ++k;
+      }
+      if (ok && busy) {
+        ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u) && abort_flag == 0u);
+        t5_fence_after();
+      }
+      if (!ok && lane == 0) fail();
+      // ---- the item's share
+      const int own0 = owner(g.first), own1 = owner(g.first + g.count - 1);
+      const int me = static_cast<int>(blockIdx.x) - own0, count = own1 - own0 + 1;
+      const int near = me % kKvJoin == 0 ? min(kKvJoin, count - me) - 1 : 0, far = me == 0 ? (count - 1) / kKvJoin : 0;
+      named_sync(1, 256);
+      if (warp == 0) {
+        bool got = abort_flag == 0u;
+        got = __shfl_sync(~0u, got ? 1 : 0, 0) != 0;
+        for (int p = lane; p < near + far && got; p += 32)
+          got = kv_take_part(a.ready + blockIdx.x + (p < near ? 1 + p : kKvJoin * (p - near + 1)), &abort_flag);
+        got = __all_sync(~0u, got);
+        if (lane == 0) {
+          if (!got) fail();
+          joined = got ? 1u : 0u;
+        }
+      }
+      named_sync(1, 256);
+      ok = joined != 0u;  // one answer for all warps
+      float* mine = a.part + static_cast<int64_t>(blockIdx.x) * S::kPartFloats;
+      if (ok && half_rows > 0) {  // uniform per warp
+        const auto part_of = [&](int p) { return mine + static_cast<int64_t>(p < near ? 1 + p : kKvJoin * (p - near + 1)) * S::kPartFloats; };
+        float am = row.m, al = row.l;
+        for (int p = 0; p < near + far; ++p) {
+          const float pm = row.live ? __ldcg(part_of(p) + kKpRows * D + r_tile) : -INFINITY;
+          const float pl = row.live ? __ldcg(part_of(p) + kKpRows * D + kKpRows + r_tile) : 0.f;
+          const float mm = fmaxf(am, pm);
+          al = al * (am == -INFINITY ? 0.f : fast_exp2(am - mm)) + pl * (pm == -INFINITY ? 0.f : fast_exp2(pm - mm));
+          am = mm;
+        }
+        const float f0 = row.m == -INFINITY ? 0.f : fast_exp2(row.m - am);
+        const float inv = me != 0 ? 1.f : al > 0.f ? 1.f / al : 0.f;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float x[32];
+          if (busy) t5_ld32(to + c, x);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = busy ? x[i] * f0 : 0.f;
+          for (int p = 0; p < near + far; ++p) {
+            const float pm = row.live ? __ldcg(part_of(p) + kKpRows * D + r_tile) : -INFINITY;
+            const float f1 = pm == -INFINITY ? 0.f : fast_exp2(pm - am);
+            if (row.live) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = fmaf(f1, __ldcg(part_of(p) + (c + i) * kKpRows + r_tile), x[i]);
+            }
+          }
+          if (row.live) {
+            if (me != 0) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) __stcg(mine + (c + i) * kKpRows + r_tile, x[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4*>(a.out + out_row * D + c + i) =
+                    make_uint4(f32x2_to_elem2<F16>(x[i] * inv, x[i + 1] * inv), f32x2_to_elem2<F16>(x[i + 2] * inv, x[i + 3] * inv),
+                               f32x2_to_elem2<F16>(x[i + 4] * inv, x[i + 5] * inv), f32x2_to_elem2<F16>(x[i + 6] * inv, x[i + 7] * inv));
+            }
+          }
+        }
+        if (row.live) {
+          if (me != 0) {
+            __stcg(mine + kKpRows * D + r_tile, am);
+            __stcg(mine + kKpRows * D + kKpRows + r_tile, al);
+          } else if (a.lse != nullptr) {
+            a.lse[out_row] = al > 0.f ? (am + log2f(al)) * 0.6931471805599453f : -INFINITY;
+          }
+        }
+        t5_fence_before();
+      }
+      if (ok && me != 0) {
+        named_sync(1, 256);
+        if (tid == 0) st_release(a.ready + blockIdx.x, 1u);
+      }
+    }
+  }
+  __syncthreads();
+  // after an expired wait: loads that nothing consumed land before the block ends
+  if (tid == 0)
+    for (uint32_t f = used_tiles; f < fills; ++f)
+      if (!mbar_wait_clocked(&raw_full[f % kKpRaw], f / kKpRaw & 1u)) record_error_at(a.err, kErrTimeout);
+  t5_fence_before();
+  __syncthreads();
+  t5_fence_after();
+  if (warp == 13) {
+    __syncwarp();
+    t5_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace bsq
