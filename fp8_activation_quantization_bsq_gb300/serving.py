@@ -11,54 +11,59 @@ import torch
 
 from . import FORMATS, _check, _fmt, lib
 
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_MXFP8, _NVFP4 = FORMATS["mxfp8"], FORMATS["nvfp4"]
+
+# A call of these costs the host about as much as the GPU for a single token,
+# so each attribute of a tensor is read once and the checks are plain expressions.
 
 
-def _on(device, stream):
-    """The raw stream of a call on `device`, which has to be current where no stream is given."""
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-
-
-def _call(name, device, args):
+def _call(name, index, stream, args):
+    """Call the library on device `index` and the given or current stream."""
     fn = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args)
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args)
-    _check(rc, name)
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
+    if rc != 0:
+        _check(rc, name)
 
 
-def _check_rows(x, what):
-    """A (tokens, heads, dim) 16-bit CUDA tensor with unit inner stride: its dtype code."""
-    code = _DTYPES.get(x.dtype)
-    if code is None or x.dim() != 3 or not x.is_cuda or x.stride(2) != 1:
+def _rows(x, what):
+    """(dtype code, shape, strides, device index) of a (tokens, heads, dim) 16-bit CUDA tensor."""
+    code, shape = _DTYPES.get(x.dtype), x.shape
+    if code is None or len(shape) != 3 or not x.is_cuda or (stride := x.stride())[2] != 1:
         raise ValueError(f"{what} must be a (tokens, heads, dim) bfloat16 or float16 CUDA tensor with unit inner stride")
-    return code
+    return code, shape, stride, x.get_device()
 
 
-def _cache_args(rows, k_cache, v_cache, k_scales, v_scales, block_table, offsets, seq_lens):
-    """Checks the cache tensors of a call for `rows`; (kv_heads, dim, page, batch)."""
-    if k_cache.dtype != torch.uint8 or k_cache.dim() != 4 or k_cache.stride(3) != 1 or v_cache.dtype != torch.uint8 or \
-            k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+def _cache(dim, index, k_cache, v_cache, k_scales, v_scales, block_table, offsets, seq_lens):
+    """Checks the cache tensors of a call; the library's arguments from the cache to the batch."""
+    shape, cs = k_cache.shape, k_cache.stride()
+    if k_cache.dtype is not _U8 or v_cache.dtype is not _U8 or len(shape) != 4 or v_cache.shape != shape or \
+            v_cache.stride() != cs or cs[3] != 1:
         raise ValueError("k_cache and v_cache must be uint8 (pages, kv_heads, page, dim) tensors of equal strides, unit inner stride")
-    pages, heads, page, dim = k_cache.shape
-    for s in (k_scales, v_scales):
-        if s.dtype != torch.uint8 or s.dim() != 2 or s.shape[0] != pages or s.shape[1] != heads or not s.is_contiguous():
-            raise ValueError("k_scales and v_scales must be contiguous uint8 (pages, kv_heads) tensors")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    pages, heads, page, cache_dim = shape
+    if k_scales.dtype is not _U8 or v_scales.dtype is not _U8 or k_scales.shape != (pages, heads) or \
+            v_scales.shape != (pages, heads) or not k_scales.is_contiguous() or not v_scales.is_contiguous():
+        raise ValueError("k_scales and v_scales must be contiguous uint8 (pages, kv_heads) tensors")
+    tshape = block_table.shape
+    if block_table.dtype is not _I32 or len(tshape) != 2 or ((ts := block_table.stride())[1] != 1 and tshape[1] > 1):
         raise ValueError("block_table must be an int32 (batch, pages per sequence) tensor with unit inner stride")
-    batch = block_table.shape[0]
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != batch + 1 or not offsets.is_contiguous() or \
-            seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.shape[0] != batch or not seq_lens.is_contiguous():
+    batch, width = tshape
+    if offsets.dtype is not _I32 or offsets.shape != (batch + 1,) or not offsets.is_contiguous() or \
+            seq_lens.dtype is not _I32 or seq_lens.shape != (batch,) or not seq_lens.is_contiguous():
         raise ValueError("offsets and seq_lens must be contiguous int32 tensors of batch + 1 and batch entries")
-    device = rows.device
-    for t in (k_cache, v_cache, k_scales, v_scales, block_table, offsets, seq_lens):
-        if t.device != device:
-            raise ValueError("all tensors of a cache call must be on one CUDA device")
-    if rows.shape[2] != dim:
+    if not (k_cache.get_device() == v_cache.get_device() == k_scales.get_device() == v_scales.get_device() ==
+            block_table.get_device() == offsets.get_device() == seq_lens.get_device() == index):
+        raise ValueError("all tensors of a cache call must be on one CUDA device")
+    if dim != cache_dim:
         raise ValueError("the rows' dim must be the cache's")
-    return heads, dim, page, batch
+    return heads, (k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), pages, page, cs[0], cs[1], cs[2],
+                   block_table.data_ptr(), ts[0], width, offsets.data_ptr(), seq_lens.data_ptr(), batch)
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
@@ -75,18 +80,14 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     pages per sequence); ``seq_lens``: int32 (batch), each sequence's length
     with the new tokens.  A page that earlier tokens share keeps the larger
     of its scale and the new tokens', and its codes are rewritten when it grows."""
-    dt = _check_rows(k, "k")
-    if v.dtype != k.dtype or v.shape != k.shape or v.stride() != k.stride() or v.device != k.device:
+    dt, shape, stride, index = _rows(k, "k")
+    if v.dtype != k.dtype or v.shape != shape or v.stride() != stride or v.get_device() != index:
         raise ValueError("k and v must have equal shapes, types and strides")
-    heads, dim, page, batch = _cache_args(k, k_cache, v_cache, k_scales, v_scales, block_table, offsets, seq_lens)
-    if k.shape[1] != heads:
+    heads, cache = _cache(shape[2], index, k_cache, v_cache, k_scales, v_scales, block_table, offsets, seq_lens)
+    if shape[1] != heads:
         raise ValueError("k must have the cache's kv_heads")
-    cs = k_cache.stride()
-    _call("bsq_kv_append", k.device,
-          (dt, k.data_ptr(), v.data_ptr(), k.shape[0], heads, dim, k.stride(0), k.stride(1), k_cache.data_ptr(),
-           v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), k_cache.shape[0], page, cs[0], cs[1], cs[2],
-           block_table.data_ptr(), block_table.stride(0), block_table.shape[1], offsets.data_ptr(), seq_lens.data_ptr(), batch,
-           _on(k.device, stream)))
+    _call("bsq_kv_append", index, stream,
+          (dt, k.data_ptr(), v.data_ptr(), shape[0], heads, shape[2], stride[0], stride[1], *cache))
 
 
 def kv_attention_workspace_bytes(total: int, heads: int, kv_heads: int, dim: int, batch: int, max_q: int) -> int:
@@ -108,28 +109,26 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     ``workspace``: uint8, zeroed once (``torch.zeros``), left ready for the
     next call; allocated when None.  Returns ``out`` (contiguous, q's type),
     or (out, float32 lse (tokens, heads)) with ``return_lse``."""
-    dt = _check_rows(q, "q")
-    kv_heads, dim, page, batch = _cache_args(q, k_cache, v_cache, k_scales, v_scales, block_table, offsets, seq_lens)
-    total, heads = q.shape[0], q.shape[1]
+    dt, shape, stride, index = _rows(q, "q")
+    total, heads, dim = shape
+    kv_heads, cache = _cache(dim, index, k_cache, v_cache, k_scales, v_scales, block_table, offsets, seq_lens)
     if out is None:
-        out = torch.empty((total, heads, dim), dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != q.device:
+        out = q.new_empty(shape)
+    elif out.dtype != q.dtype or out.shape != shape or not out.is_contiguous() or out.get_device() != index:
         raise ValueError("out must be a contiguous tensor of q's shape, type and device")
-    if return_lse and lse is None:
-        lse = torch.empty((total, heads), dtype=torch.float32, device=q.device)
-    elif lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (total, heads) or not lse.is_contiguous() or
-                              lse.device != q.device):
+    if lse is None:
+        if return_lse:
+            lse = q.new_empty((total, heads), dtype=_F32)
+    elif lse.dtype is not _F32 or lse.shape != (total, heads) or not lse.is_contiguous() or lse.get_device() != index:
         raise ValueError("lse must be a contiguous float32 (tokens, heads) tensor on q's device")
     if workspace is None:
-        workspace = torch.zeros(kv_attention_workspace_bytes(total, heads, kv_heads, dim, batch, max_q), dtype=torch.uint8,
-                                device=q.device)
-    cs = k_cache.stride()
-    _call("bsq_kv_attention", q.device,
-          (dt, q.data_ptr(), total, heads, kv_heads, dim, q.stride(0), q.stride(1), k_cache.data_ptr(), v_cache.data_ptr(),
-           k_scales.data_ptr(), v_scales.data_ptr(), k_cache.shape[0], page, cs[0], cs[1], cs[2], block_table.data_ptr(),
-           block_table.stride(0), block_table.shape[1], offsets.data_ptr(), seq_lens.data_ptr(), batch, max_q,
+        workspace = torch.zeros(kv_attention_workspace_bytes(total, heads, kv_heads, dim, cache[-1], max_q), dtype=_U8, device=q.device)
+    elif workspace.dtype is not _U8 or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    _call("bsq_kv_attention", index, stream,
+          (dt, q.data_ptr(), total, heads, kv_heads, dim, stride[0], stride[1], *cache, max_q,
            1.0 / math.sqrt(dim) if sm_scale is None else sm_scale, 1 if causal else 0, window, out.data_ptr(),
-           None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _on(q.device, stream)))
+           None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel()))
     return (out, lse) if return_lse else out
 
 
@@ -153,45 +152,49 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w13_scal
     ``renormalize``).  Activations are quantized to ``fmt`` as by
     :func:`quantize`, x before the first product and bf16(silu(g) * u) before the second.
     ``workspace``: uint8, zeroed once, left ready for the next call; allocated when None."""
-    if x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_cuda or x.stride(1) != 1:
+    shape = x.shape
+    if x.dtype is not _BF16 or len(shape) != 2 or not x.is_cuda or (xs := x.stride())[1] != 1:
         raise ValueError("x must be a 2-D bfloat16 CUDA tensor with unit inner stride")
-    tokens, hidden = x.shape
-    if logits.dtype != torch.float32 or logits.dim() != 2 or logits.shape[0] != tokens or logits.stride(1) != 1:
+    tokens, hidden = shape
+    index = x.get_device()
+    lshape = logits.shape
+    if logits.dtype is not _F32 or len(lshape) != 2 or lshape[0] != tokens or (ls := logits.stride())[1] != 1:
         raise ValueError("logits must be a float32 (tokens, experts) tensor with unit inner stride")
-    experts = logits.shape[1]
+    experts = lshape[1]
     f = _fmt(fmt)
-    bits = 8 if f == FORMATS["mxfp8"] else 4
-    if w13.dtype != torch.uint8 or w13.dim() != 3 or w2.dtype != torch.uint8 or w2.dim() != 3 or not w13.is_contiguous() or \
+    s13, s2 = w13.shape, w2.shape
+    if w13.dtype is not _U8 or len(s13) != 3 or w2.dtype is not _U8 or len(s2) != 3 or not w13.is_contiguous() or \
             not w2.is_contiguous():
         raise ValueError("w13 and w2 must be contiguous uint8 (experts, rows, row bytes) tensors")
-    inter = w13.shape[1] // 2
-    if w13.shape[0] != experts or w13.shape[1] % 2 or w13.shape[2] * 8 != hidden * bits or w2.shape[0] != experts or \
-            w2.shape[1] != hidden or w2.shape[2] * 8 != inter * bits:
+    inter = s13[1] // 2
+    per = 1 if f == _MXFP8 else 2  # values per byte
+    if s13 != (experts, 2 * inter, hidden // per) or s2 != (experts, hidden, inter // per) or hidden % per or inter % per:
         raise ValueError("w13 must be (experts, 2*inter, row bytes of hidden) and w2 (experts, hidden, row bytes of inter)")
-    for s, rows, cols in ((w13_scales, 2 * inter, hidden), (w2_scales, hidden, inter)):
-        if s.dtype != torch.uint8 or not s.is_contiguous() or s.numel() != experts * lib().bsq_scales5d_bytes(f, rows, cols):
-            raise ValueError("w13_scales and w2_scales must be contiguous uint8 tensors of each expert's 5D scales")
-    sfs = (x_sf, w13_sf, h_sf, w2_sf)
-    if f == FORMATS["nvfp4"]:
-        for s in sfs:
-            if s is None or s.dtype != torch.float32 or s.numel() != experts or not s.is_contiguous():
-                raise ValueError("nvfp4 needs contiguous float32 (experts) tensors x_sf, w13_sf, h_sf and w2_sf")
+    sf = 16 if f == _NVFP4 else 32
+    n13 = experts * -(-2 * inter // 128) * -(-hidden // (4 * sf)) * 512
+    n2 = experts * -(-hidden // 128) * -(-inter // (4 * sf)) * 512
+    if w13_scales.dtype is not _U8 or w13_scales.numel() != n13 or not w13_scales.is_contiguous() or \
+            w2_scales.dtype is not _U8 or w2_scales.numel() != n2 or not w2_scales.is_contiguous():
+        raise ValueError("w13_scales and w2_scales must be contiguous uint8 tensors of each expert's 5D scales")
+    if not (logits.get_device() == w13.get_device() == w2.get_device() == w13_scales.get_device() == w2_scales.get_device() == index):
+        raise ValueError("all tensors must be on one CUDA device")
+    if f == _NVFP4:
+        for t in (x_sf, w13_sf, h_sf, w2_sf):
+            if t is None or t.dtype is not _F32 or t.numel() != experts or not t.is_contiguous() or t.get_device() != index:
+                raise ValueError("nvfp4 needs contiguous float32 (experts) tensors x_sf, w13_sf, h_sf and w2_sf on x's device")
+        sfs = (x_sf.data_ptr(), w13_sf.data_ptr(), h_sf.data_ptr(), w2_sf.data_ptr())
     else:
-        sfs = (None,) * 4
-    device = x.device
-    for t in (logits, w13, w13_scales, w2, w2_scales, *sfs):
-        if t is not None and t.device != device:
-            raise ValueError("all tensors must be on one CUDA device")
+        sfs = (None, None, None, None)
     if out is None:
-        out = torch.empty((tokens, hidden), dtype=torch.bfloat16, device=device)
-    elif out.dtype != torch.bfloat16 or out.shape != x.shape or out.stride(1) != 1 or out.device != device:
+        out = x.new_empty(shape)
+    elif out.dtype is not _BF16 or out.shape != shape or out.stride(1) != 1 or out.get_device() != index:
         raise ValueError("out must be a (tokens, hidden) bfloat16 tensor with unit inner stride on x's device")
     if workspace is None:
-        workspace = torch.zeros(lib().bsq_moe_layer_workspace_bytes(f, tokens, hidden, inter, experts, top_k),
-                                dtype=torch.uint8, device=device)
-    _call("bsq_moe_layer", device,
-          (f, x.data_ptr(), x.stride(0), logits.data_ptr(), logits.stride(0), w13.data_ptr(), w13_scales.data_ptr(),
-           w2.data_ptr(), w2_scales.data_ptr(), *(None if s is None else s.data_ptr() for s in sfs), out.data_ptr(),
-           out.stride(0), tokens, hidden, inter, experts, top_k, 1 if renormalize else 0, workspace.data_ptr(),
-           workspace.numel(), _on(device, stream)))
+        workspace = torch.zeros(moe_layer_workspace_bytes(f, tokens, hidden, inter, experts, top_k), dtype=_U8, device=x.device)
+    elif workspace.dtype is not _U8 or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on x's device")
+    _call("bsq_moe_layer", index, stream,
+          (f, x.data_ptr(), xs[0], logits.data_ptr(), ls[0], w13.data_ptr(), w13_scales.data_ptr(), w2.data_ptr(),
+           w2_scales.data_ptr(), *sfs, out.data_ptr(), out.stride(0), tokens, hidden, inter, experts, top_k,
+           1 if renormalize else 0, workspace.data_ptr(), workspace.numel()))
     return out
