@@ -26,7 +26,7 @@
 // dimension in q.k and of the output rows is free, so a thread takes 16 consecutive bytes of a
 // key, and pairs of keys are interleaved bytewise before conversion.
 // An item cut by the runs is finished by the block that began it, which adds the other blocks' parts
-// in block order (first in groups of 16 where there are many): those blocks hold them at the start of
+// in block order (first in groups where there are many): those blocks hold them at the start of
 // their runs, it at the end of its own.
 #pragma once
 
@@ -38,7 +38,10 @@ namespace bsq {
 
 constexpr int kKvTile = 64;       // keys per unit
 constexpr int kKvMaxBlocks = 1024;
-constexpr int kKvJoin = 16;       // parts joined at a time
+constexpr int kKvMinRun = 3;      // units of a run, at least, once every SM has one
+// Parts of an item that one block joins by itself, and the size of the groups
+// that are joined first where there are more: about their number's square root.
+__device__ __forceinline__ int kv_join_group(int parts) { return parts <= 20 ? parts : parts <= 72 ? 8 : 16; }
 constexpr int kKvCounterBytes = 4 * kKvMaxBlocks;
 
 struct KvAttnArgs {
@@ -83,7 +86,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnArgs& a, int b, bool report)
 template <int RT>
 __device__ __forceinline__ void kv_keys(const KvAttnArgs& a, const KvSeq& s, int rt, int& lo, int& hi) {
   const int rows = s.n * a.group;
-  const int i0 = rt * RT / a.group, i1 = (min(rows, (rt + 1) * RT) - 1) / a.group;
+  const int i0 = rt == 0 ? 0 : rt * RT / a.group, i1 = rows <= (rt + 1) * RT ? s.n - 1 : ((rt + 1) * RT - 1) / a.group;
   hi = a.causal ? min(s.len, s.len - s.n + i1 + 1) : s.len;
   lo = a.window > 0 ? max(0, s.len - s.n + i0 - a.window + 1) : 0;
   if (hi <= lo) lo = hi = 0;
@@ -103,11 +106,22 @@ __device__ __forceinline__ int64_t kv_seq_units(const KvAttnArgs& a, const KvSeq
   return u;  // per kv head
 }
 
-// Where a block's run begins.
+// A block's run of units, and the sequence it begins in.
 struct KvStart {
-  int64_t total;    // units in all
-  int64_t before;   // units of the sequences before `seq`
-  int seq;
+  int64_t total;       // units in all
+  int64_t before;      // units of the sequences before `seq`
+  int seq, parts;      // parts: runs, none of them empty
+  int64_t begin, end;  // this block's
+  // total * i / parts and the run that holds a unit, in 32 bits where they suffice
+  __device__ __forceinline__ int64_t start_of(int i) const {
+    if (total < (1 << 21)) return static_cast<uint32_t>(total) * static_cast<uint32_t>(i) / static_cast<uint32_t>(parts);
+    return total * i / parts;
+  }
+  __device__ __forceinline__ int owner(int64_t u) const {
+    if (total < (1 << 21))
+      return static_cast<int>(((static_cast<uint32_t>(u) + 1u) * static_cast<uint32_t>(parts) - 1u) / static_cast<uint32_t>(total));
+    return static_cast<int>(((u + 1) * parts - 1) / total);
+  }
 };
 
 // One item's share of a block's run.
@@ -118,12 +132,33 @@ struct KvSegment {
   int64_t first, count;     // the item's units
 };
 
-// Walks the units [u, end) item by item.
+// Walks the units [u, end) item by item.  Each warp has its own in shared
+// memory, which its first lane moves on: kept in registers it would cost the
+// loop over the keys some fifty of them.
 template <int RT, int TILE>
 struct KvWalk {
   int64_t u, end, before, per_head;
   int b;
   KvSeq s;
+  KvSegment seg;
+  // Whole warp; true while there is an item, described by seg.
+  __device__ __forceinline__ bool step(const KvAttnArgs& a) {
+    __syncwarp();
+    bool more = false;
+    if ((threadIdx.x & 31) == 0) more = next(a, seg);
+    __syncwarp();
+    return __shfl_sync(~0u, more ? 1 : 0, 0) != 0;
+  }
+  __device__ __forceinline__ void begin(const KvAttnArgs& a, const KvStart& start) {
+    if ((threadIdx.x & 31) == 0) {
+      u = start.begin;
+      end = start.end;
+      before = start.before;
+      b = start.seq;
+      load(a);
+    }
+    __syncwarp();
+  }
   __device__ __forceinline__ void load(const KvAttnArgs& a) {
     s = kv_seq<RT>(a, b, false);
     per_head = kv_seq_units<RT, TILE>(a, s);
@@ -184,44 +219,40 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
 }
 
 // Sum every sequence's units and find this block's run (by all THREADS of the
-// block; prefix: THREADS + 1 entries of shared memory); false for a block without one.
+// block, a thread taking consecutive sequences); false for a block without one.
 template <int RT, int TILE, int THREADS>
-__device__ __forceinline__ bool kv_start(const KvAttnArgs& a, int64_t* prefix, KvStart* start) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int per = (a.batch + THREADS - 1) / THREADS;
-  const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
+__device__ __forceinline__ bool kv_start(const KvAttnArgs& a, int blocks_per_sm, int64_t* warp_sum, KvStart* start) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.batch + THREADS - 1) / THREADS, b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) mine += kv_seq_units<RT, TILE>(a, kv_seq<RT>(a, b, blockIdx.x == 0)) * a.kv_heads;
-  prefix[tid + 1] = mine;
-  if (tid == 0) prefix[0] = 0;
-  __syncthreads();
-  if (tid < 32) {  // inclusive sums, 32 at a time
-    int64_t carry = 0;
-    for (int i = 0; i < THREADS; i += 32) {
-      int64_t v = prefix[1 + i + lane];
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(~0u, v, d);
-        if (lane >= d) v += o;
-      }
-      prefix[1 + i + lane] = carry + v;
-      carry += __shfl_sync(~0u, v, 31);
-    }
+  int64_t sum = mine;
+#pragma unroll 1
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(~0u, sum, d);
+    if (lane >= d) sum += o;
   }
+  if (lane == 31) warp_sum[warp] = sum;
   __syncthreads();
-  const int64_t total = prefix[THREADS], parts = min(total, static_cast<int64_t>(gridDim.x));
-  if (blockIdx.x >= parts) return false;
-  const int64_t begin = total * blockIdx.x / parts;
-  if (prefix[tid] <= begin && begin < prefix[tid + 1]) {
-    int64_t before = prefix[tid];
-    int b = b0;
-    while (true) {
-      const int64_t c = kv_seq_units<RT, TILE>(a, kv_seq<RT>(a, b, false)) * a.kv_heads;
-      if (begin < before + c) break;
-      before += c;
-      ++b;
-    }
-    *start = {total, before, b};
+  KvStart s;
+  s.total = 0;
+#pragma unroll 1
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w == warp) sum += s.total;
+    s.total += warp_sum[w];
+  }
+  // Joining a part costs about as much as a few units: at most one run per SM
+  // until they have kKvMinRun units (contexts of 777 / 3000 tokens, 8 kv heads: 10.1 / 13.1 us,
+  // 10.1 / 16.8 with a run for every unit, 12.4 / 13.8 with at least four)
+  s.parts = static_cast<int>(min(static_cast<int64_t>(gridDim.x),
+                                 max(s.total / kKvMinRun, min(s.total, static_cast<int64_t>(gridDim.x / blocks_per_sm)))));
+  if (static_cast<int>(blockIdx.x) >= s.parts) return false;
+  s.begin = s.start_of(blockIdx.x);
+  s.end = s.start_of(blockIdx.x + 1);
+  if (sum - mine <= s.begin && s.begin < sum) {  // one thread
+    s.before = sum - mine;
+    s.seq = b0;  // KvWalk goes on to the sequence itself
+    *start = s;
   }
   __syncthreads();
   return true;
@@ -233,6 +264,12 @@ struct KvPageScale {
 };
 
 // NT: tiles of 8 query rows.
+// From the scale bytes; -1: no such page.
+__device__ __forceinline__ KvPageScale kv_page_scale(int ek, int ev) {
+  if (ek < 0) return {0.f, -INFINITY, 0.f};
+  return {pow2f(min(max(ek - 127, -126), 127)), static_cast<float>(ev - 127), pow2f(min(max(127 - ev, -126), 127))};
+}
+
 template <int D, int NT>
 struct KvShape {
   static constexpr int kWarps = 4;                         // consumers
@@ -288,7 +325,8 @@ __device__ __forceinline__ uint32_t kv_transpose(uint32_t x) {
 
 template <int D, int NT, bool F16>
 __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlocksPerSm)
-    kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const KvAttnArgs a) {
+    kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                        const __grid_constant__ KvAttnArgs a) {
   using S = KvShape<D, NT>;
   constexpr int RT = S::kRows, kT = 32 * S::kWarps;
   constexpr int kQuads = D / 64;  // 16-byte loads of a key per thread
@@ -298,15 +336,16 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
   [[maybe_unused]] uint4* query = reinterpret_cast<uint4*>(smem + S::kStages * 2 * S::kTileBytes + S::kMergeBytes);
   __shared__ uint64_t full_bar[S::kStages], empty_bar[S::kStages];
   __shared__ KvPageScale page_scale[S::kStages][4];
-  __shared__ int64_t prefix[S::kThreads + 1];
-  __shared__ KvStart start;
   __shared__ float warp_m2[2][S::kWarps][RT], warp_l2[2][S::kWarps][RT];  // by parity of the item
+  __shared__ KvWalk<RT, kKvTile> walks[S::kWarps + 1];
+  __shared__ KvStart start;
+  __shared__ int64_t warp_sum[S::kWarps + 1];
   __shared__ volatile uint32_t abort_flag, fills, used_tiles, go_on, joined;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(&full_bar[s], 1);
+      mbar_init(&full_bar[s], 2);  // codes, scales
       mbar_init(&empty_bar[s], S::kWarps);
     }
     abort_flag = 0u;
@@ -315,30 +354,23 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
     prefetch_tensormap(&map_k);
     prefetch_tensormap(&map_v);
   }
+  __syncthreads();
   pdl_wait();
-
-  if (!kv_start<RT, kKvTile, S::kThreads>(a, prefix, &start)) return;  // the whole block
-  const int64_t total = start.total, parts = min(total, static_cast<int64_t>(gridDim.x));
-  // the block whose run holds unit u
-  const auto owner = [&](int64_t u) { return static_cast<int>(((u + 1) * parts - 1) / total); };
-  KvWalk<RT, kKvTile> walk;
-  walk.u = total * blockIdx.x / parts;
-  walk.end = total * (blockIdx.x + 1) / parts;
-  walk.before = start.before;
-  walk.b = start.seq;
-  walk.load(a);
-  KvSegment g;
+  KvWalk<RT, kKvTile>& walk = walks[warp];
+  const KvSegment& g = walk.seg;
+  if (!kv_start<RT, kKvTile, S::kThreads>(a, S::kBlocksPerSm, warp_sum, &start)) return;  // the whole block
+  walk.begin(a, start);
 
   if (warp == S::kWarps) {
     // ---- producer
     uint32_t stage = 0, phase = 0, n = 0;
     const int box = min(a.page, kKvTile), boxes = kKvTile / box;
     bool ok = true;
-    while (ok && walk.next(a, g)) {
+    while (ok && walk.step(a)) {
       const int32_t* table = a.table + static_cast<int64_t>(g.b) * a.table_ld;
       const int pages = (g.hi + a.page - 1) >> a.page_shift;  // beyond these no entry is read
       int batch0 = -1, pid = -1;
-      KvPageScale sc{};
+      int ek = -1, ev = -1;
       for (int t = g.tile0; t < g.tile1; ++t) {
         const int pg0 = (t * kKvTile) >> a.page_shift;
         if (batch0 < 0 || pg0 + boxes > batch0 + 32) {  // the next 32 pages' ids and scales, one per lane
@@ -348,24 +380,19 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
           const bool valid = pid >= 0 && pid < a.num_pages;
           // pages before the first allowed key are masked anyway and need no entry
           if (pg < pages && !valid && (pg + 1) << a.page_shift > g.lo) record_error_at(a.err, kErrValue);
-          sc = {0.f, -INFINITY, 0.f};
-          if (valid) {
+          if (!valid) pid = -1;
+          ek = ev = -1;
+          if (valid) {  // used only after the codes have been requested
             const int64_t at = static_cast<int64_t>(pid) * a.kv_heads + g.head;
-            const int ek = a.scales[0][at], ev = a.scales[1][at];
-            sc.kfac = pow2f(min(max(ek - 127, -126), 127));
-            sc.ev = static_cast<float>(ev - 127);
-            sc.inv = pow2f(min(max(127 - ev, -126), 127));
-          } else {
-            pid = -1;
+            ek = a.scales[0][at];
+            ev = a.scales[1][at];
           }
         }
         if (lane == 0) ok = mbar_wait_clocked(&empty_bar[stage], phase ^ 1u) && abort_flag == 0u;
         ok = __shfl_sync(~0u, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
         const int first = pg0 - batch0;
-        if (lane >= first && lane < first + boxes) page_scale[stage][lane - first] = sc;
         const uint32_t got = __ballot_sync(~0u, pid >= 0) >> first & ((1u << boxes) - 1u);
-        __syncwarp();
         uint8_t* kd = smem + stage * 2 * S::kTileBytes;
         if (lane == 0) mbar_arrive_expect_tx(&full_bar[stage], 2u * __popc(got) * box * D);
         for (int i = 0; i < boxes; ++i) {
@@ -376,6 +403,9 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
             tma_load_4d(kd + S::kTileBytes + i * box * D, &map_v, 0, y, g.head, id, &full_bar[stage]);
           }
         }
+        if (lane >= first && lane < first + boxes) page_scale[stage][lane - first] = kv_page_scale(ek, ev);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full_bar[stage]);
         ++n;
         if (lane == 0) fills = n;
         if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
@@ -390,10 +420,13 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
     const int gq = lane >> 2, c = lane & 3;
     uint32_t stage = 0, phase = 0, used = 0;
     bool ok = true;
-    for (int item = 0; ok && walk.next(a, g); ++item) {
+    for (int item = 0; ok && walk.step(a); ++item) {
       float(*warp_m)[RT] = warp_m2[item & 1];
       float(*warp_l)[RT] = warp_l2[item & 1];
       const int rows = g.s.n * a.group, pos0 = g.s.len - g.s.n;
+      const int lo = g.lo, hi = g.hi, tile1 = g.tile1;
+      // positions of the tile's first and last row
+      const int pos_first = pos0 + g.rt * RT / a.group, pos_last = pos0 + (min(rows, (g.rt + 1) * RT) - 1) / a.group;
       // Query rows 8 t + gq, dimensions D/4 c .. + D/4 - 1: the second operand
       // of K Q^T.  For NT = 4 they stay in shared memory, which all warps read.
       uint32_t q[NT == 4 ? 1 : NT][D / 8];
@@ -448,7 +481,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
 
-      for (int tile = g.tile0; tile < g.tile1; ++tile) {
+      for (int tile = g.tile0; tile < tile1; ++tile) {
         ok = __all_sync(~0u, mbar_wait_clocked(&full_bar[stage], phase) && abort_flag == 0u);
         if (!ok) break;
         const uint8_t* kd = smem + stage * 2 * S::kTileBytes;
@@ -494,8 +527,8 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
         }
         const int key0 = tile * kKvTile + 16 * warp;
         // keys that not all rows see, or none: only tiles at the range's ends
-        const bool masked = ps.inv == 0.f || key0 < g.lo || key0 + 16 > g.hi || (a.causal && key0 + 15 > pos0 + g.rt * RT / a.group) ||
-                            (a.window > 0 && key0 <= pos0 + (min(rows, (g.rt + 1) * RT) - 1) / a.group - a.window);
+        const bool masked = ps.inv == 0.f || key0 < lo || key0 + 16 > hi || (a.causal && key0 + 15 > pos_first) ||
+                            (a.window > 0 && key0 <= pos_last - a.window);
         // two copies of the rest, so that the tiles in between carry no masks
         const auto rest = [&](auto edge) {
           float top[NT][2];
@@ -508,7 +541,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
               float x = (s[t][i] + s2[t][i]) * (rowfac[t][h] * ps.kfac) + ps.ev;
               if constexpr (decltype(edge)::value) {
                 const int key = key0 + gq + 8 * (i >> 1);
-                const bool see = ps.inv != 0.f && key >= g.lo && key < g.hi && (!a.causal || key <= pos[t][h]) &&
+                const bool see = ps.inv != 0.f && key >= lo && key < hi && (!a.causal || key <= pos[t][h]) &&
                                  (a.window <= 0 || key > pos[t][h] - a.window);
                 x = see ? x : -INFINITY;
               }
@@ -567,7 +600,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
             }
             if constexpr (decltype(edge)::value) {  // whatever lies outside the allowed keys (NaN codes too) counts as zero
               const int key = tile * kKvTile + r;
-              if (key < g.lo || key >= g.hi || ps.inv == 0.f) {
+              if (key < lo || key >= hi || ps.inv == 0.f) {
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) vw[k][i] = 0u;
               }
@@ -611,10 +644,11 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
       named_sync(1, kT);
       if (tid == 0) go_on = abort_flag == 0u ? 1u : 0u;  // one answer for all warps
       const int live = min(RT, rows - g.rt * RT);  // rows of the tile
-      const int own0 = owner(g.first), own1 = owner(g.first + g.count - 1);
+      const int own0 = start.owner(g.first), own1 = start.owner(g.first + g.count - 1);
       const int me = static_cast<int>(blockIdx.x) - own0, count = own1 - own0 + 1;
       // parts of the group's other blocks, then (the item's first block) of the other groups' first blocks
-      const int near = me % kKvJoin == 0 ? min(kKvJoin, count - me) - 1 : 0, far = me == 0 ? (count - 1) / kKvJoin : 0;
+      const int join = kv_join_group(count);
+      const int near = me % join == 0 ? min(join, count - me) - 1 : 0, far = me == 0 ? (count - 1) / join : 0;
       float* mine = a.part + static_cast<int64_t>(blockIdx.x) * S::kPartFloats;
 #pragma unroll
       for (int pass = 0; pass < RT / S::kPassRows; ++pass) {
@@ -643,7 +677,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
           if (warp == 0) {
             bool got = true;
             for (int p = lane; p < near + far && got; p += 32)
-              got = kv_take_part(a.ready + blockIdx.x + (p < near ? 1 + p : kKvJoin * (p - near + 1)), &abort_flag);
+              got = kv_take_part(a.ready + blockIdx.x + (p < near ? 1 + p : join * (p - near + 1)), &abort_flag);
             got = __all_sync(~0u, got);
             if (lane == 0) {
               if (!got) {
@@ -657,13 +691,14 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
           if (joined == 0u) go_on = 0u;  // every thread, the same
           ok = joined != 0u;
         }
-        // eight threads per row, float4s 8 i + tid % 8 of it
-        const int rl = tid >> 3, r = pass * S::kPassRows + rl;
-        if (ok && rl < S::kPassRows && r < live) {
-          float4 acc[D / 32];
+        // kTpr threads per row, float4s kTpr i + tid % kTpr of it
+        constexpr int kTpr = kT / S::kPassRows, kOwn = D / 4 / kTpr;
+        const int rl = tid / kTpr, r = pass * S::kPassRows + rl, d4 = tid % kTpr;
+        if (ok && r < live) {
+          float4 acc[kOwn];
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const int d = 4 * (8 * i + (tid & 7));
+          for (int i = 0; i < kOwn; ++i) {
+            const int d = 4 * (kTpr * i + d4);
             const float* src = merge + rl * S::kRow + d / (D / 8) * S::kEighth + d % (D / 8);
             constexpr int kWarpStride = S::kPassRows * S::kRow;
             const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + kWarpStride);
@@ -678,17 +713,17 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
             const float wm = warp_m[k][r];
             al += wm == -INFINITY ? 0.f : warp_l[k][r] * fast_exp2(wm - am);
           }
-#pragma unroll 4
+#pragma unroll(16 / kOwn)
           for (int p = 0; p < near + far; ++p) {
-            const float* part = mine + static_cast<int64_t>(p < near ? 1 + p : kKvJoin * (p - near + 1)) * S::kPartFloats;
-            float4 v[D / 32];
+            const float* part = mine + static_cast<int64_t>(p < near ? 1 + p : join * (p - near + 1)) * S::kPartFloats;
+            float4 v[kOwn];
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(part + r * D) + 8 * i + (tid & 7));
+            for (int i = 0; i < kOwn; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(part + r * D) + kTpr * i + d4);
             const float pm = __ldcg(part + RT * D + r), pl = __ldcg(part + RT * D + RT + r);
             const float mm = fmaxf(am, pm);
             const float f0 = am == -INFINITY ? 0.f : fast_exp2(am - mm), f1 = pm == -INFINITY ? 0.f : fast_exp2(pm - mm);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
+            for (int i = 0; i < kOwn; ++i)
               acc[i] = make_float4(acc[i].x * f0 + v[i].x * f1, acc[i].y * f0 + v[i].y * f1, acc[i].z * f0 + v[i].z * f1,
                                    acc[i].w * f0 + v[i].w * f1);
             al = al * f0 + pl * f1;
@@ -696,8 +731,8 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
           }
           if (me != 0) {
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) __stcg(reinterpret_cast<float4*>(mine + r * D) + 8 * i + (tid & 7), acc[i]);
-            if ((tid & 7) == 0) {
+            for (int i = 0; i < kOwn; ++i) __stcg(reinterpret_cast<float4*>(mine + r * D) + kTpr * i + d4, acc[i]);
+            if (d4 == 0) {
               __stcg(mine + RT * D + r, am);
               __stcg(mine + RT * D + RT + r, al);
             }
@@ -706,10 +741,10 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
             const int64_t row = static_cast<int64_t>(g.s.t0 + rr / a.group) * a.heads + g.head * a.group + rr % a.group;
             const float f = al > 0.f ? 1.f / al : 0.f;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              *reinterpret_cast<uint2*>(a.out + row * D + 32 * i + 4 * (tid & 7)) =
+            for (int i = 0; i < kOwn; ++i)
+              *reinterpret_cast<uint2*>(a.out + row * D + 4 * (kTpr * i + d4)) =
                   make_uint2(f32x2_to_elem2<F16>(acc[i].x * f, acc[i].y * f), f32x2_to_elem2<F16>(acc[i].z * f, acc[i].w * f));
-            if ((tid & 7) == 0 && a.lse != nullptr) a.lse[row] = al > 0.f ? (am + log2f(al)) * 0.6931471805599453f : -INFINITY;
+            if (d4 == 0 && a.lse != nullptr) a.lse[row] = al > 0.f ? (am + log2f(al)) * 0.6931471805599453f : -INFINITY;
           }
         }
       }

@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
   __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drain_bar;
   __shared__ KpSlot slots[kKpSlots];
   __shared__ KvStart start;
+  __shared__ int64_t warp_sum[kKpThreads / 32];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag, fills, used_tiles, go_on, joined;
 
@@ -161,19 +162,15 @@ __global__ void __launch_bounds__(kKpThreads, 1)
     prefetch_tensormap(&map_v);
   }
   pdl_wait();
-  int64_t* prefix = reinterpret_cast<int64_t*>(raw);  // before the ring is in use
-  if (!kv_start<kKpRows, kKpKeys, kKpThreads>(a, prefix, &start)) return;  // the whole block
-  fence_async();  // the ring's next writes are TMA's
+  if (!kv_start<kKpRows, kKpKeys, kKpThreads>(a, 1, warp_sum, &start)) return;  // the whole block
   if (warp == 13) t5_alloc(&tmem_slot, 512);
   t5_fence_before();
   __syncthreads();
   t5_fence_after();
   const uint32_t tmem = tmem_slot;
-  const int64_t total = start.total, parts = min(total, static_cast<int64_t>(gridDim.x));
-  const auto owner = [&](int64_t u) { return static_cast<int>(((u + 1) * parts - 1) / total); };
   KvWalk<kKpRows, kKpKeys> walk;
-  walk.u = total * blockIdx.x / parts;
-  walk.end = total * (blockIdx.x + 1) / parts;
+  walk.u = start.begin;
+  walk.end = start.end;
   walk.before = start.before;
   walk.b = start.seq;
   walk.load(a);
@@ -201,16 +198,9 @@ __global__ void __launch_bounds__(kKpThreads, 1)
           pid = pg < pages ? table[pg] : -1;
           const bool valid = pid >= 0 && pid < a.num_pages;
           if (pg < pages && !valid && (pg + 1) << a.page_shift > g.lo) record_error_at(a.err, kErrValue);
-          sc = {0.f, -INFINITY, 0.f};
-          if (valid) {
-            const int64_t at = static_cast<int64_t>(pid) * a.kv_heads + g.head;
-            const int ek = a.scales[0][at], ev = a.scales[1][at];
-            sc.kfac = pow2f(min(max(ek - 127, -126), 127));
-            sc.ev = static_cast<float>(ev - 127);
-            sc.inv = pow2f(min(max(127 - ev, -126), 127));
-          } else {
-            pid = -1;
-          }
+          const int64_t at = static_cast<int64_t>(pid) * a.kv_heads + g.head;
+          sc = kv_page_scale(valid ? a.scales[0][at] : -1, valid ? a.scales[1][at] : -1);
+          if (!valid) pid = -1;
         }
         const int first = pg0 - batch0;
         const uint32_t got = __ballot_sync(~0u, pid >= 0) >> first & ((1u << boxes) - 1u);
@@ -431,15 +421,16 @@ __global__ void __launch_bounds__(kKpThreads, 1)
       }
       if (!ok && lane == 0) fail();
       // ---- the item's share
-      const int own0 = owner(g.first), own1 = owner(g.first + g.count - 1);
+      const int own0 = start.owner(g.first), own1 = start.owner(g.first + g.count - 1);
       const int me = static_cast<int>(blockIdx.x) - own0, count = own1 - own0 + 1;
-      const int near = me % kKvJoin == 0 ? min(kKvJoin, count - me) - 1 : 0, far = me == 0 ? (count - 1) / kKvJoin : 0;
+      const int join = kv_join_group(count);
+      const int near = me % join == 0 ? min(join, count - me) - 1 : 0, far = me == 0 ? (count - 1) / join : 0;
       named_sync(1, 256);
       if (warp == 0) {
         bool got = abort_flag == 0u;
         got = __shfl_sync(~0u, got ? 1 : 0, 0) != 0;
         for (int p = lane; p < near + far && got; p += 32)
-          got = kv_take_part(a.ready + blockIdx.x + (p < near ? 1 + p : kKvJoin * (p - near + 1)), &abort_flag);
+          got = kv_take_part(a.ready + blockIdx.x + (p < near ? 1 + p : join * (p - near + 1)), &abort_flag);
         got = __all_sync(~0u, got);
         if (lane == 0) {
           if (!got) fail();
@@ -450,7 +441,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
       ok = joined != 0u;  // one answer for all warps
       float* mine = a.part + static_cast<int64_t>(blockIdx.x) * S::kPartFloats;
       if (ok && half_rows > 0) {  // uniform per warp
-        const auto part_of = [&](int p) { return mine + static_cast<int64_t>(p < near ? 1 + p : kKvJoin * (p - near + 1)) * S::kPartFloats; };
+        const auto part_of = [&](int p) { return mine + static_cast<int64_t>(p < near ? 1 + p : join * (p - near + 1)) * S::kPartFloats; };
         float am = row.m, al = row.l;
         for (int p = 0; p < near + far; ++p) {
           const float pm = row.live ? __ldcg(part_of(p) + kKpRows * D + r_tile) : -INFINITY;
