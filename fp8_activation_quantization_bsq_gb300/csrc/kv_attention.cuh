@@ -149,8 +149,17 @@ struct KvWalk {
     __syncwarp();
     return __shfl_sync(~0u, more ? 1 : 0, 0) != 0;
   }
-  __device__ __forceinline__ void begin(const KvAttnArgs& a, const KvStart& start) {
-    if ((threadIdx.x & 31) == 0) {
+  // The same for warps that share one: `threads` threads meet at barrier `id`;
+  // none goes on once one of them has given up.
+  __device__ __forceinline__ bool step_together(const KvAttnArgs& a, int id, int threads, bool first, volatile uint32_t* more,
+                                                const volatile uint32_t* abort_flag) {
+    named_sync(id, threads);
+    if (first) *more = *abort_flag == 0u && next(a, seg) ? 1u : 0u;
+    named_sync(id, threads);
+    return *more != 0u;
+  }
+  __device__ __forceinline__ void begin(const KvAttnArgs& a, const KvStart& start, bool mine) {
+    if (mine) {
       u = start.begin;
       end = start.end;
       before = start.before;
@@ -342,7 +351,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
   __shared__ int64_t warp_sum[S::kWarps + 1];
   __shared__ volatile uint32_t abort_flag, fills, used_tiles, go_on, joined;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&full_bar[s], 2);  // codes, scales
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
   KvWalk<RT, kKvTile>& walk = walks[warp];
   const KvSegment& g = walk.seg;
   if (!kv_start<RT, kKvTile, S::kThreads>(a, S::kBlocksPerSm, warp_sum, &start)) return;  // the whole block
-  walk.begin(a, start);
+  walk.begin(a, start, lane == 0);
 
   if (warp == S::kWarps) {
     // ---- producer
@@ -388,7 +397,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
             ev = a.scales[1][at];
           }
         }
-        if (lane == 0) ok = mbar_wait_clocked(&empty_bar[stage], phase ^ 1u) && abort_flag == 0u;
+        if (lane == 0) ok = mbar_wait_clocked(&empty_bar[stage], phase ^ 1u, &abort_flag);
         ok = __shfl_sync(~0u, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
         const int first = pg0 - batch0;
@@ -482,7 +491,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
         for (int i = 0; i < D / 16; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
 
       for (int tile = g.tile0; tile < tile1; ++tile) {
-        ok = __all_sync(~0u, mbar_wait_clocked(&full_bar[stage], phase) && abort_flag == 0u);
+        ok = __all_sync(~0u, mbar_wait_clocked(&full_bar[stage], phase, &abort_flag));
         if (!ok) break;
         const uint8_t* kd = smem + stage * 2 * S::kTileBytes;
         const uint8_t* vd = kd + S::kTileBytes;

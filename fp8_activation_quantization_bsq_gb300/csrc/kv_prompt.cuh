@@ -64,10 +64,13 @@ template <bool EDGE>
 __device__ __forceinline__ float kp_top(const KvAttnArgs& a, const KpRow& row, uint32_t taddr, const KpSlot& slot, int shift, int key0,
                                         int lo, int hi) {
   float top = -INFINITY;
+  float buf[2][32];  // the next 32 scores are on their way while these are looked at
+  t5_ld32_async(taddr, buf[0]);
 #pragma unroll
   for (int c = 0; c < kKpKeys; c += 32) {
-    float x[32];
-    t5_ld32(taddr + c, x);
+    float(&x)[32] = buf[c / 32 & 1];
+    t5_ld32_wait(x);
+    if (c + 32 < kKpKeys) t5_ld32_async(taddr + c + 32, buf[(c / 32 + 1) & 1]);
 #pragma unroll
     for (int h = 0; h < 32; h += 16) {
       const KvPageScale ps = slot.sc[(c + h) >> shift];
@@ -76,10 +79,13 @@ __device__ __forceinline__ float kp_top(const KvAttnArgs& a, const KpRow& row, u
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, kp_score<true>(a, row, x[h + i], f, ps, key0 + c + h + i, lo, hi));
       } else {
-        float m = x[h];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) m = fmaxf(m, x[h + i]);
-        top = fmaxf(top, fmaf(m, f, ps.ev));  // f >= 0
+        float m0 = fmaxf(fmaxf(x[h], x[h + 1]), x[h + 2]), m1 = fmaxf(fmaxf(x[h + 3], x[h + 4]), x[h + 5]);
+        m0 = fmaxf(fmaxf(m0, x[h + 6]), x[h + 7]);
+        m1 = fmaxf(fmaxf(m1, x[h + 8]), x[h + 9]);
+        m0 = fmaxf(fmaxf(m0, x[h + 10]), x[h + 11]);
+        m1 = fmaxf(fmaxf(m1, x[h + 12]), x[h + 13]);
+        m0 = fmaxf(fmaxf(m0, x[h + 14]), x[h + 15]);
+        top = fmaxf(top, fmaf(fmaxf(m0, m1), f, ps.ev));  // f >= 0
       }
     }
   }
@@ -91,33 +97,35 @@ template <bool EDGE>
 __device__ __forceinline__ float kp_weights(const KvAttnArgs& a, const KpRow& row, uint32_t taddr, const KpSlot& slot, int shift,
                                             int key0, int lo, int hi, float m) {
   float sum = 0.f;
+  float buf[2][32];
+  t5_ld32_async(taddr, buf[0]);
 #pragma unroll
   for (int c = 0; c < kKpKeys; c += 32) {
-    float x[32];
-    t5_ld32(taddr + c, x);
+    float(&x)[32] = buf[c / 32 & 1];
+    t5_ld32_wait(x);
+    if (c + 32 < kKpKeys) t5_ld32_async(taddr + c + 32, buf[(c / 32 + 1) & 1]);
     uint32_t p[16];
 #pragma unroll
     for (int h = 0; h < 32; h += 16) {
-      KvPageScale ps = slot.sc[(c + h) >> shift];
-      const float f = row.fac * ps.kfac;
-      float part = 0.f;
-      if constexpr (!EDGE) ps.ev -= m;
+      const KvPageScale ps = slot.sc[(c + h) >> shift];
+      const float f = row.fac * ps.kfac, e = ps.ev - m;
+      float2 part = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
-        float w0, w1;
+        float2 w;
         if constexpr (EDGE) {
-          w0 = fast_exp2(kp_score<true>(a, row, x[h + i], f, ps, key0 + c + h + i, lo, hi) - m);
-          w1 = fast_exp2(kp_score<true>(a, row, x[h + i + 1], f, ps, key0 + c + h + i + 1, lo, hi) - m);
+          w = make_float2(kp_score<true>(a, row, x[h + i], f, ps, key0 + c + h + i, lo, hi) - m,
+                          kp_score<true>(a, row, x[h + i + 1], f, ps, key0 + c + h + i + 1, lo, hi) - m);
         } else {
-          w0 = fast_exp2(fmaf(x[h + i], f, ps.ev));
-          w1 = fast_exp2(fmaf(x[h + i + 1], f, ps.ev));
+          w = fma_f32x2(make_float2(x[h + i], x[h + i + 1]), make_float2(f, f), make_float2(e, e));
         }
-        part += w0 + w1;
-        p[(h + i) / 2] = f32x2_to_elem2<true>(w0, w1);
+        w = make_float2(fast_exp2(w.x), fast_exp2(w.y));
+        part = add_f32x2(part, w);
+        p[(h + i) / 2] = f32x2_to_elem2<true>(w.x, w.y);
       }
-      sum = fmaf(part, ps.inv, sum);
+      sum = fmaf(part.x + part.y, ps.inv, sum);
     }
-    t5_st16(taddr + c / 2, p);  // over scores that have been read
+    t5_st16(taddr + c / 2, p);  // over scores that have been read: the 32 in flight lie further on
   }
   return sum;
 }
@@ -134,11 +142,13 @@ __global__ void __launch_bounds__(kKpThreads, 1)
   __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drain_bar;
   __shared__ KpSlot slots[kKpSlots];
   __shared__ KvStart start;
+  __shared__ KvWalk<kKpRows, kKpKeys> walks[4];
+  __shared__ volatile uint32_t more[2];
   __shared__ int64_t warp_sum[kKpThreads / 32];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag, fills, used_tiles, go_on, joined;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kKpRaw; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -167,14 +177,11 @@ __global__ void __launch_bounds__(kKpThreads, 1)
   t5_fence_before();
   __syncthreads();
   t5_fence_after();
-  const uint32_t tmem = tmem_slot;
-  KvWalk<kKpRows, kKpKeys> walk;
-  walk.u = start.begin;
-  walk.end = start.end;
-  walk.before = start.before;
-  walk.b = start.seq;
-  walk.load(a);
-  KvSegment g;
+  const uint32_t tmem = warp_uniform(static_cast<int>(tmem_slot));
+  // one walk for the eight softmax warps, one for the converters, one each for codes and products
+  KvWalk<kKpRows, kKpKeys>& walk = walks[warp < 8 ? 0 : warp < 12 ? 1 : warp == 12 ? 2 : 3];
+  const KvSegment& g = walk.seg;
+  walk.begin(a, start, lane == 0 && (warp == 0 || warp == 8 || warp == 12 || warp == 13));
   const auto fail = [&]() {
     if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
     abort_flag = 1u;
@@ -185,7 +192,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
     uint32_t n = 0, unit = 0;
     const int box = min(a.page, kKpKeys), boxes = kKpKeys / box;
     bool ok = true;
-    while (ok && walk.next(a, g)) {
+    while (ok && walk.step(a)) {
       const int32_t* table = a.table + static_cast<int64_t>(g.b) * a.table_ld;
       const int pages = (g.hi + a.page - 1) >> a.page_shift;  // beyond these no entry is read
       int batch0 = -1, pid = -1;
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           const uint32_t slot = n % kKpRaw;
-          ok = __all_sync(~0u, mbar_wait_clocked(&raw_empty[slot], (n / kKpRaw & 1u) ^ 1u) && abort_flag == 0u);
+          ok = __all_sync(~0u, mbar_wait_clocked(&raw_empty[slot], (n / kKpRaw & 1u) ^ 1u, &abort_flag));
           if (!ok) break;
           if (kv == 0) {  // the softmax reads these after the unit's scores, long before 8 units on
             if (lane >= first && lane < first + boxes) slots[unit % kKpSlots].sc[lane - first] = sc;
@@ -233,14 +240,14 @@ __global__ void __launch_bounds__(kKpThreads, 1)
     constexpr int kRowThreads = D / 16, kRowsPerIter = 128 / kRowThreads;
     uint32_t n = 0, unit = 0;
     bool ok = true;
-    while (ok && walk.next(a, g)) {
+    while (walk.step_together(a, 2, 128, ct == 0, &more[1], &abort_flag)) {
       for (int t = g.tile0; t < g.tile1 && ok; ++t, ++unit) {
         const bool ends = t * kKpKeys < g.lo || (t + 1) * kKpKeys > g.hi;
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++n) {
           const uint32_t r = n % kKpRaw, w = n % kKpWide;
-          ok = __all_sync(~0u, mbar_wait_clocked(&raw_full[r], n / kKpRaw & 1u) &&
-                                   mbar_wait_clocked(&wide_empty[w], (n / kKpWide & 1u) ^ 1u) && abort_flag == 0u);
+          ok = __all_sync(~0u, mbar_wait_clocked(&raw_full[r], n / kKpRaw & 1u, &abort_flag) &&
+                                   mbar_wait_clocked(&wide_empty[w], (n / kKpWide & 1u) ^ 1u, &abort_flag));
           if (!ok) break;
           const uint8_t* src = raw + r * S::kRawBytes;
           uint8_t* dst = wide + w * S::kWideBytes;
@@ -274,8 +281,8 @@ __global__ void __launch_bounds__(kKpThreads, 1)
           if (ct == 0) used_tiles = n + 1;
         }
       }
+      if (!ok && lane == 0) fail();
     }
-    if (!ok && lane == 0) fail();
   } else if (warp == 13) {
     // ---- products
     const uint32_t lead = t5_elect();
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
     constexpr uint32_t kIdS = t5_idesc_f16(kKpKeys, false), kIdO = t5_idesc_f16(D, true);
     uint32_t n = 0, queries[2] = {0u, 0u}, k[2] = {0u, 0u};
     bool ok = true;
-    const auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(~0u, mbar_wait_clocked(bar, parity) && abort_flag == 0u); };
+    const auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(~0u, mbar_wait_clocked(bar, parity, &abort_flag)); };
     const auto scores = [&](int h, uint32_t w) {  // S of half h: tensor memory columns 128 h ..
       const uint32_t qa = q_addr + h * S::kHalfBytes, ka = wide_addr + w * S::kWideBytes;
 #pragma unroll
@@ -299,9 +306,9 @@ __global__ void __launch_bounds__(kKpThreads, 1)
         t5_mma_f16_ta(tmem + 256 + 128 * h, tmem + 128 * h + 8 * i, t5_desc_sw128_n(va + 2048 * i, 16384), kIdO, accumulate | i, lead);
       t5_commit(smem_addr(&pv_done[h]), lead);
     };
-    while (ok && walk.next(a, g)) {
-      const int units = g.tile1 - g.tile0;
-      const bool two = g.s.n * a.group - g.rt * kKpRows > 128;
+    while (ok && walk.step(a)) {
+      const int units = warp_uniform(g.tile1 - g.tile0);
+      const bool two = warp_uniform(g.s.n * a.group - g.rt * kKpRows) > 128;
       if (units > 0) {
         ok = wait(&q_full[0], queries[0]++ & 1u) && (!two || wait(&q_full[1], queries[1]++ & 1u)) &&
              wait(&wide_full[n % kKpWide], n / kKpWide & 1u);
@@ -315,7 +322,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
       for (int u = 0; u < units && ok; ++u) {
         const uint32_t v = n, nk = n + 1;  // this unit's values, the next one's keys
         const bool more = u + 1 < units;
-        ok = wait(&wide_full[v % kKpWide], v / kKpWide & 1u) && (!more || wait(&wide_full[nk % kKpWide], nk / kKpWide & 1u));
+        ok = wait(&wide_full[v % kKpWide], v / kKpWide & 1u);
         for (int h = 0; h < (two ? 2 : 1) && ok; ++h) {
           ok = wait(&p_full[h], k[h] & 1u);
           if (!ok) break;
@@ -323,7 +330,14 @@ __global__ void __launch_bounds__(kKpThreads, 1)
           t5_fence_after();
           values(h, v % kKpWide, u);
           if (h == (two ? 1 : 0)) t5_commit(smem_addr(&wide_empty[v % kKpWide]), lead);
-          if (more) scores(h, nk % kKpWide);
+          if (more) {
+            if (h == 0) {
+              ok = wait(&wide_full[nk % kKpWide], nk / kKpWide & 1u);
+              if (!ok) break;
+              t5_fence_after();
+            }
+            scores(h, nk % kKpWide);
+          }
         }
         if (ok && more) t5_commit(smem_addr(&wide_empty[nk % kKpWide]), lead);
         n += more ? 2 : 1;
@@ -340,7 +354,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
     const int shift = min(a.page_shift, 7);
     uint32_t unit = 0, k = 0;
     bool ok = true;
-    while (ok && walk.next(a, g)) {
+    while (walk.step_together(a, 1, 256, tid == 0, &more[0], &abort_flag)) {
       const int rows = g.s.n * a.group, r = g.rt * kKpRows + r_tile, pos0 = g.s.len - g.s.n;
       const int half_rows = min(128, rows - g.rt * kKpRows - 128 * half);  // <= 0: the half is empty
       const bool busy = half_rows > 0 && g.tile1 > g.tile0;
@@ -378,7 +392,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
       const int last_row = min(rows, g.rt * kKpRows + 128 * (half + 1)) - 1, first_row = g.rt * kKpRows + 128 * half;
       for (int t = g.tile0; t < g.tile1; ++t, ++unit) {
         if (!busy) continue;
-        ok = __all_sync(~0u, mbar_wait_clocked(&s_full[half], k & 1u) && abort_flag == 0u);
+        ok = __all_sync(~0u, mbar_wait_clocked(&s_full[half], k & 1u, &abort_flag));
         if (!ok) break;
         t5_fence_after();
         const KpSlot& slot = slots[unit % kKpSlots];
@@ -393,7 +407,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
           row.m = mn;
           row.l *= f;
           if (t > g.tile0) {  // O holds the units before: wait for the last of them
-            ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u) && abort_flag == 0u);
+            ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u, &abort_flag));
             if (!ok) break;
             t5_fence_after();
 #pragma unroll 1
@@ -416,7 +430,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
         ++k;
       }
       if (ok && busy) {
-        ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u) && abort_flag == 0u);
+        ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u, &abort_flag));
         t5_fence_after();
       }
       if (!ok && lane == 0) fail();

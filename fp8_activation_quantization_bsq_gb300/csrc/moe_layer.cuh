@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   __shared__ int active_count;
   __shared__ uint32_t warp_sum[kMoeThreads / 32];
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int blocks = gridDim.x, block = blockIdx.x, pairs = a.tokens * a.top_k;
   const int stages = a.stages;
 
@@ -434,8 +434,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     tb.pair_of[tb.row0[tb.index_of[e]] + moe_rank(tb, e, t)] = p;
   }
   __syncthreads();
-  const uint32_t tmem = tmem_slot, smem_base = smem_addr(smem);
-  const int active = active_count;
+  const uint32_t tmem = warp_uniform(static_cast<int>(tmem_slot)), smem_base = smem_addr(smem);
+  const int active = warp_uniform(active_count);
   const int part_floats = 2 * a.max_n * 128;
 
   if (warp == 0) {
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           const uint8_t* s1 = scales + expert * scale_bytes + static_cast<int64_t>(r1 / 128) * kt * 512;
           for (int kc = u - item * p.chunks; u < stop; ++u, ++kc) {
             const int atoms = min(kAtoms, kt - kc * kAtoms);
-            if (!mbar_wait_clocked(&empty_bar[stage], phase_bit ^ 1u)) {
+            if (!mbar_wait_clocked(&empty_bar[stage], phase_bit ^ 1u, &abort_flag)) {
               if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
               abort_flag = 1u;
             }
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           const int row = tb.row0[i], n8 = (tb.row0[i + 1] - row + 7) >> 3;
           const uint8_t* s0 = scales + static_cast<int64_t>(i) * kt * 512;
           for (int kc = u - item * p.chunks; u < stop && ok; ++u, ++kc) {
-            ok = mbar_wait_clocked(&empty_bar[stage], phase_bit ^ 1u) && abort_flag == 0u;
+            ok = mbar_wait_clocked(&empty_bar[stage], phase_bit ^ 1u, &abort_flag) && abort_flag == 0u;
             if (!ok) break;
             const int atoms = min(kAtoms, kt - kc * kAtoms);
             uint8_t* st = smem + stage * a.stage_bytes + 2 * kMoeHalfBytes;
@@ -535,14 +535,14 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         const int item = u / p.chunks, stop = min(p.end, (item + 1) * p.chunks);
         const int i = item / p.tiles, tile = item % p.tiles;
         const bool two = phase == 0 || 256 * tile + 128 < rows;
-        const uint32_t n = (tb.row0[i + 1] - tb.row0[i] + 15) & ~15u;
+        const uint32_t n = warp_uniform((tb.row0[i + 1] - tb.row0[i] + 15) & ~15);
         const uint32_t buf = seg & 1u, d = tmem + buf * 128u;
-        ok = __all_sync(~0u, mbar_wait_clocked(&acc_empty[buf], ((seg >> 1) & 1u) ^ 1u) && abort_flag == 0u);
+        ok = __all_sync(~0u, mbar_wait_clocked(&acc_empty[buf], ((seg >> 1) & 1u) ^ 1u, &abort_flag));
         if (!ok) break;
         t5_fence_after();
         int kc = u - item * p.chunks;
         for (uint32_t fresh = 0; u < stop; ++u, ++kc) {
-          ok = __all_sync(~0u, mbar_wait_clocked(&full_bar[stage], phase_bit) && abort_flag == 0u);
+          ok = __all_sync(~0u, mbar_wait_clocked(&full_bar[stage], phase_bit, &abort_flag));
           if (!ok) break;
           t5_fence_after();
           const uint32_t st = smem_base + stage * a.stage_bytes;
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             go = moe_wait_count(flag, 1u, &abort_flag);
             *flag = 0u;
           }
-          go = go && mbar_wait_clocked(&acc_full[buf], (seg >> 1) & 1u) && abort_flag == 0u;
+          go = go && mbar_wait_clocked(&acc_full[buf], (seg >> 1) & 1u, &abort_flag) && abort_flag == 0u;
           last_flag = go ? 1u : 0u;
         }
         named_sync(1, 128);
