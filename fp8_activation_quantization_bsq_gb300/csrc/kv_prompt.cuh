@@ -4,16 +4,15 @@
 // 128-row products of the tcgen05 tensor cores.
 //
 // A unit is 128 keys of a tile of 256 rows (query tokens x heads of a kv head), as two halves of
-// 128.  Per unit and half: S = Q K^T into tensor memory, the softmax weights P
-// (FP16) over S in place, O += P V with P as the tensor-memory operand.  With both halves in
-// flight the tensor cores compute one half's products while the other's softmax runs.
-// What bounds it: 4 x 256 x 128 x D operations a unit against 256 x 128
-// exponentials and the conversions below; the softmax warps' issue slots come first.
-//  * warps 0-3 and 4-7: the halves' softmax, a thread per row: the row's
-//    maximum in a first pass over S, weights and their sum in a second (S is read from
-//    tensor memory twice, which keeps it out of registers).  O is rescaled only where a row's
-//    maximum grew by more than 2^8.  They also bring the query rows (a power of two per row, so
-//    that they are exact in FP16) and write the output.
+// 128 rows.  Per half and 64 keys: S = Q K^T into tensor memory, the softmax weights P
+// (FP16) over S in place, O += P V with P as the tensor-memory operand.  A half's two S tiles take
+// turns, so that the next 64 keys' scores are there when its softmax comes to them; with two halves the
+// tensor cores have products of the other while either softmax runs.  (512 columns: 4 x 64 of S, 2 x 128 of O.)
+// What bounds it: 4 x 256 x 128 x D operations a unit (2048 cycles at D = 128) against the issue
+// slots of 256 x 128 exponentials and of the conversions below.
+//  * warps 0-3 and 4-7: the halves' softmax, a thread per row, 64 scores in registers.
+//    O is rescaled only where a row's maximum grew by more than 2^8.  They also bring the
+//    query rows (a power of two per row, so that they are exact in FP16) and write the output.
 //  * warps 8-11: E4M3 tiles to FP16 in the 128-byte-swizzled layout that both
 //    products read (K as rows of the dimension, V as rows of keys, the same bytes); keys outside the
 //    item's range become zeros.
@@ -24,7 +23,8 @@
 
 namespace bsq {
 
-constexpr int kKpKeys = 128, kKpRows = 256, kKpThreads = 512;
+constexpr int kKpKeys = 128, kKpRows = 256, kKpThreads = 448;
+constexpr int kKpSub = 64;              // keys of an S tile
 constexpr int kKpRaw = 4, kKpWide = 3;  // rings of E4M3 and FP16 tiles: K, V, K, V, ...
 constexpr int kKpSlots = 8;             // units whose page scales are kept
 constexpr int kKpMaxBlocks = 256;
@@ -60,72 +60,65 @@ __device__ __forceinline__ float kp_score(const KvAttnArgs& a, const KpRow& row,
   return see ? x : -INFINITY;
 }
 
+// The row's scores of kKpSub keys into registers, scaled and with the values'
+// exponent added; their maximum.
 template <bool EDGE>
-__device__ __forceinline__ float kp_top(const KvAttnArgs& a, const KpRow& row, uint32_t taddr, const KpSlot& slot, int shift, int key0,
-                                        int lo, int hi) {
+__device__ __forceinline__ float kp_scores(const KvAttnArgs& a, const KpRow& row, uint32_t taddr, const KpSlot& slot, int shift,
+                                           int first, int key0, int lo, int hi, float (&x)[kKpSub]) {
+  float(&x0)[32] = reinterpret_cast<float(&)[32]>(x[0]);
+  float(&x1)[32] = reinterpret_cast<float(&)[32]>(x[32]);
+  t5_ld32_async(taddr, x0);
+  t5_ld32_async(taddr + 32, x1);
+  t5_ld32_wait(x0);
+  t5_ld32_wait(x1);
   float top = -INFINITY;
-  float buf[2][32];  // the next 32 scores are on their way while these are looked at
-  t5_ld32_async(taddr, buf[0]);
 #pragma unroll
-  for (int c = 0; c < kKpKeys; c += 32) {
-    float(&x)[32] = buf[c / 32 & 1];
-    t5_ld32_wait(x);
-    if (c + 32 < kKpKeys) t5_ld32_async(taddr + c + 32, buf[(c / 32 + 1) & 1]);
+  for (int h = 0; h < kKpSub; h += 16) {
+    const KvPageScale ps = slot.sc[(first + h) >> shift];
+    const float f = row.fac * ps.kfac;
+    if constexpr (EDGE) {
 #pragma unroll
-    for (int h = 0; h < 32; h += 16) {
-      const KvPageScale ps = slot.sc[(c + h) >> shift];
-      const float f = row.fac * ps.kfac;
-      if constexpr (EDGE) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, kp_score<true>(a, row, x[h + i], f, ps, key0 + c + h + i, lo, hi));
-      } else {
-        float m0 = fmaxf(fmaxf(x[h], x[h + 1]), x[h + 2]), m1 = fmaxf(fmaxf(x[h + 3], x[h + 4]), x[h + 5]);
-        m0 = fmaxf(fmaxf(m0, x[h + 6]), x[h + 7]);
-        m1 = fmaxf(fmaxf(m1, x[h + 8]), x[h + 9]);
-        m0 = fmaxf(fmaxf(m0, x[h + 10]), x[h + 11]);
-        m1 = fmaxf(fmaxf(m1, x[h + 12]), x[h + 13]);
-        m0 = fmaxf(fmaxf(m0, x[h + 14]), x[h + 15]);
-        top = fmaxf(top, fmaf(fmaxf(m0, m1), f, ps.ev));  // f >= 0
+      for (int i = 0; i < 16; ++i) {
+        x[h + i] = kp_score<true>(a, row, x[h + i], f, ps, key0 + first + h + i, lo, hi);
+        top = fmaxf(top, x[h + i]);
       }
+    } else {
+      float m0 = fmaxf(fmaxf(x[h], x[h + 1]), x[h + 2]), m1 = fmaxf(fmaxf(x[h + 3], x[h + 4]), x[h + 5]);
+      m0 = fmaxf(fmaxf(m0, x[h + 6]), x[h + 7]);
+      m1 = fmaxf(fmaxf(m1, x[h + 8]), x[h + 9]);
+      m0 = fmaxf(fmaxf(m0, x[h + 10]), x[h + 11]);
+      m1 = fmaxf(fmaxf(m1, x[h + 12]), x[h + 13]);
+      m0 = fmaxf(fmaxf(m0, x[h + 14]), x[h + 15]);
+      top = fmaxf(top, fmaf(fmaxf(m0, m1), f, ps.ev));  // f >= 0
     }
   }
   return top;
 }
 
-// Weights of the unit over its scores; returns their sum (of 2^(t - m) 2^-ev).
+// Weights over the scores' place; returns their sum (of 2^(t - m) 2^-ev).
 template <bool EDGE>
-__device__ __forceinline__ float kp_weights(const KvAttnArgs& a, const KpRow& row, uint32_t taddr, const KpSlot& slot, int shift,
-                                            int key0, int lo, int hi, float m) {
+__device__ __forceinline__ float kp_weights(const KpRow& row, uint32_t taddr, const KpSlot& slot, int shift, int first, float m,
+                                            const float (&x)[kKpSub]) {
   float sum = 0.f;
-  float buf[2][32];
-  t5_ld32_async(taddr, buf[0]);
 #pragma unroll
-  for (int c = 0; c < kKpKeys; c += 32) {
-    float(&x)[32] = buf[c / 32 & 1];
-    t5_ld32_wait(x);
-    if (c + 32 < kKpKeys) t5_ld32_async(taddr + c + 32, buf[(c / 32 + 1) & 1]);
+  for (int c = 0; c < kKpSub; c += 32) {
     uint32_t p[16];
 #pragma unroll
     for (int h = 0; h < 32; h += 16) {
-      const KvPageScale ps = slot.sc[(c + h) >> shift];
+      const KvPageScale ps = slot.sc[(first + c + h) >> shift];
       const float f = row.fac * ps.kfac, e = ps.ev - m;
       float2 part = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
-        float2 w;
-        if constexpr (EDGE) {
-          w = make_float2(kp_score<true>(a, row, x[h + i], f, ps, key0 + c + h + i, lo, hi) - m,
-                          kp_score<true>(a, row, x[h + i + 1], f, ps, key0 + c + h + i + 1, lo, hi) - m);
-        } else {
-          w = fma_f32x2(make_float2(x[h + i], x[h + i + 1]), make_float2(f, f), make_float2(e, e));
-        }
+        const float x0 = x[c + h + i], x1 = x[c + h + i + 1];
+        float2 w = EDGE ? make_float2(x0 - m, x1 - m) : fma_f32x2(make_float2(x0, x1), make_float2(f, f), make_float2(e, e));
         w = make_float2(fast_exp2(w.x), fast_exp2(w.y));
         part = add_f32x2(part, w);
         p[(h + i) / 2] = f32x2_to_elem2<true>(w.x, w.y);
       }
       sum = fmaf(part.x + part.y, ps.inv, sum);
     }
-    t5_st16(taddr + c / 2, p);  // over scores that have been read: the 32 in flight lie further on
+    t5_st16(taddr + c / 2, p);
   }
   return sum;
 }
@@ -139,7 +132,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
   uint8_t* wide = smem + 2 * S::kHalfBytes;
   uint8_t* raw = wide + kKpWide * S::kWideBytes;
   __shared__ uint64_t raw_full[kKpRaw], raw_empty[kKpRaw], wide_full[kKpWide], wide_empty[kKpWide];
-  __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drain_bar;
+  __shared__ uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], drain_bar;  // [half][S tile]
   __shared__ KpSlot slots[kKpSlots];
   __shared__ KvStart start;
   __shared__ KvWalk<kKpRows, kKpKeys> walks[4];
@@ -160,8 +153,10 @@ __global__ void __launch_bounds__(kKpThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 4);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(&s_full[i][t], 1);
+        mbar_init(&p_full[i][t], 4);
+      }
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(&drain_bar, 1);
@@ -253,24 +248,35 @@ __global__ void __launch_bounds__(kKpThreads, 1)
           uint8_t* dst = wide + w * S::kWideBytes;
           const KpSlot& slot = slots[unit % kKpSlots];
           const bool some = ends || slot.bad != 0;
-          const int c = ct % kRowThreads;       // 16 dimensions
-          const int block = c >> 2, odd = block;  // 64 dimensions; the second block's lanes store their halves the other way round
-#pragma unroll 4
-          for (int i = 0; i < 128 / kRowsPerIter; ++i) {
-            const int key = i * kRowsPerIter + ct / kRowThreads;
-            uint4 v = *reinterpret_cast<const uint4*>(src + key * D + 16 * c);
+          // 16 dimensions of keys key0, key0 + kRowsPerIter, ...; the second 64 dimensions' lanes
+          // store their halves the other way round, so that a row's stores fall into different banks
+          const int c = ct % kRowThreads, key0 = ct / kRowThreads, block = c >> 2, ch = 2 * (c & 3), sw = key0 & 7;
+          const uint8_t* from = src + key0 * D + 16 * c;
+          uint8_t* to = dst + block * (kKpKeys * 128) + key0 * 128;
+          const int at0 = ((ch + block) ^ sw) << 4, at1 = ((ch + 1 - block) ^ sw) << 4;
+          constexpr int kIters = 128 / kRowsPerIter, kBatch = 8 < kIters ? 8 : kIters;
+#pragma unroll 1
+          for (int i0 = 0; i0 < kIters; i0 += kBatch) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) v[i] = *reinterpret_cast<const uint4*>(from + (i0 + i) * kRowsPerIter * D);
             if (some) {
-              const int k = t * kKpKeys + key;
-              if (k < g.lo || k >= g.hi || slot.sc[key >> a.page_shift].inv == 0.f) v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) {
+                const int key = key0 + (i0 + i) * kRowsPerIter, k = t * kKpKeys + key;
+                if (k < g.lo || k >= g.hi || slot.sc[key >> a.page_shift].inv == 0.f) v[i] = make_uint4(0, 0, 0, 0);
+              }
             }
-            const uint4 lo = make_uint4(e4m3x2_to_f16x2(v.x & 0xFFFFu), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y & 0xFFFFu),
-                                        e4m3x2_to_f16x2(v.y >> 16));
-            const uint4 hi = make_uint4(e4m3x2_to_f16x2(v.z & 0xFFFFu), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w & 0xFFFFu),
-                                        e4m3x2_to_f16x2(v.w >> 16));
-            uint8_t* row = dst + block * (kKpKeys * 128) + key * 128;
-            const int ch = 2 * (c & 3);
-            *reinterpret_cast<uint4*>(row + (((ch + odd) ^ (key & 7)) << 4)) = odd ? hi : lo;
-            *reinterpret_cast<uint4*>(row + (((ch + 1 - odd) ^ (key & 7)) << 4)) = odd ? lo : hi;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const uint4 x = make_uint4(e4m3x2_to_f16x2(v[i].x & 0xFFFFu), e4m3x2_to_f16x2(v[i].x >> 16),
+                                         e4m3x2_to_f16x2(v[i].y & 0xFFFFu), e4m3x2_to_f16x2(v[i].y >> 16));
+              const uint4 y = make_uint4(e4m3x2_to_f16x2(v[i].z & 0xFFFFu), e4m3x2_to_f16x2(v[i].z >> 16),
+                                         e4m3x2_to_f16x2(v[i].w & 0xFFFFu), e4m3x2_to_f16x2(v[i].w >> 16));
+              uint8_t* row = to + (i0 + i) * kRowsPerIter * 128;
+              *reinterpret_cast<uint4*>(row + at0) = block ? y : x;
+              *reinterpret_cast<uint4*>(row + at1) = block ? x : y;
+            }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
@@ -287,60 +293,67 @@ __global__ void __launch_bounds__(kKpThreads, 1)
     // ---- products
     const uint32_t lead = t5_elect();
     const uint32_t q_addr = smem_addr(smem), wide_addr = smem_addr(wide);
-    constexpr uint32_t kIdS = t5_idesc_f16(kKpKeys, false), kIdO = t5_idesc_f16(D, true);
+    constexpr uint32_t kIdS = t5_idesc_f16(kKpSub, false), kIdO = t5_idesc_f16(D, true);
     uint32_t n = 0, queries[2] = {0u, 0u}, k[2] = {0u, 0u};
     bool ok = true;
     const auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(~0u, mbar_wait_clocked(bar, parity, &abort_flag)); };
-    const auto scores = [&](int h, uint32_t w) {  // S of half h: tensor memory columns 128 h ..
-      const uint32_t qa = q_addr + h * S::kHalfBytes, ka = wide_addr + w * S::kWideBytes;
+    const auto scores = [&](int h, int sub, uint32_t w) {  // S tile: tensor memory columns 128 h + 64 sub ..
+      const uint32_t qa = q_addr + h * S::kHalfBytes, ka = wide_addr + w * S::kWideBytes + sub * (kKpSub * 128);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
-        t5_mma_f16(tmem + 128 * h, t5_desc_sw128(qa + (i >> 2) * 16384 + 32 * (i & 3)), t5_desc_sw128(ka + (i >> 2) * 16384 + 32 * (i & 3)),
-                   kIdS, i, lead);
-      t5_commit(smem_addr(&s_full[h]), lead);
+        t5_mma_f16(tmem + 128 * h + kKpSub * sub, t5_desc_sw128(qa + (i >> 2) * 16384 + 32 * (i & 3)),
+                   t5_desc_sw128(ka + (i >> 2) * 16384 + 32 * (i & 3)), kIdS, i, lead);
+      t5_commit(smem_addr(&s_full[h][sub]), lead);
     };
-    const auto values = [&](int h, uint32_t w, uint32_t accumulate) {  // O of half h: columns 256 + 128 h ..
-      const uint32_t va = wide_addr + w * S::kWideBytes;
+    const auto values = [&](int h, int sub, uint32_t w, uint32_t accumulate) {  // O of half h: columns 256 + 128 h ..
+      const uint32_t va = wide_addr + w * S::kWideBytes + sub * (kKpSub * 128);
 #pragma unroll
-      for (int i = 0; i < kKpKeys / 16; ++i)
-        t5_mma_f16_ta(tmem + 256 + 128 * h, tmem + 128 * h + 8 * i, t5_desc_sw128_n(va + 2048 * i, 16384), kIdO, accumulate | i, lead);
+      for (int i = 0; i < kKpSub / 16; ++i)
+        t5_mma_f16_ta(tmem + 256 + 128 * h, tmem + 128 * h + kKpSub * sub + 8 * i, t5_desc_sw128_n(va + 2048 * i, 16384), kIdO,
+                      accumulate | i, lead);
       t5_commit(smem_addr(&pv_done[h]), lead);
     };
     while (ok && walk.step(a)) {
       const int units = warp_uniform(g.tile1 - g.tile0);
-      const bool two = warp_uniform(g.s.n * a.group - g.rt * kKpRows) > 128;
+      const int halves = warp_uniform(g.s.n * a.group - g.rt * kKpRows) > 128 ? 2 : 1;
       if (units > 0) {
-        ok = wait(&q_full[0], queries[0]++ & 1u) && (!two || wait(&q_full[1], queries[1]++ & 1u)) &&
-             wait(&wide_full[n % kKpWide], n / kKpWide & 1u);
+        for (int h = 0; h < halves && ok; ++h) ok = wait(&q_full[h], queries[h]++ & 1u);
+        ok = ok && wait(&wide_full[n % kKpWide], n / kKpWide & 1u);
         if (!ok) break;
         t5_fence_after();
-        scores(0, n % kKpWide);
-        if (two) scores(1, n % kKpWide);
+        for (int sub = 0; sub < 2; ++sub)
+          for (int h = 0; h < halves; ++h) scores(h, sub, n % kKpWide);
         t5_commit(smem_addr(&wide_empty[n % kKpWide]), lead);
         ++n;
       }
       for (int u = 0; u < units && ok; ++u) {
-        const uint32_t v = n, nk = n + 1;  // this unit's values, the next one's keys
-        const bool more = u + 1 < units;
-        ok = wait(&wide_full[v % kKpWide], v / kKpWide & 1u);
-        for (int h = 0; h < (two ? 2 : 1) && ok; ++h) {
-          ok = wait(&p_full[h], k[h] & 1u);
-          if (!ok) break;
-          ++k[h];
-          t5_fence_after();
-          values(h, v % kKpWide, u);
-          if (h == (two ? 1 : 0)) t5_commit(smem_addr(&wide_empty[v % kKpWide]), lead);
-          if (more) {
-            if (h == 0) {
-              ok = wait(&wide_full[nk % kKpWide], nk / kKpWide & 1u);
-              if (!ok) break;
-              t5_fence_after();
+        const uint32_t v = n % kKpWide, nk = (n + 1) % kKpWide;  // this unit's values, the next one's keys
+        const bool next = u + 1 < units;
+        ok = wait(&wide_full[v], n / kKpWide & 1u);
+#pragma unroll 1
+        for (int sub = 0; sub < 2 && ok; ++sub) {
+#pragma unroll 1
+          for (int h = 0; h < halves && ok; ++h) {
+            ok = wait(&p_full[h][sub], k[h] & 1u);
+            if (!ok) break;
+            t5_fence_after();
+            values(h, sub, v, u | sub);
+            if (sub == 1) {
+              ++k[h];
+              if (h == halves - 1) t5_commit(smem_addr(&wide_empty[v]), lead);
             }
-            scores(h, nk % kKpWide);
+            if (next) {
+              if (sub == 0 && h == 0) {
+                ok = wait(&wide_full[nk], (n + 1) / kKpWide & 1u);
+                if (!ok) break;
+                t5_fence_after();
+              }
+              scores(h, sub, nk);
+            }
           }
         }
-        if (ok && more) t5_commit(smem_addr(&wide_empty[nk % kKpWide]), lead);
-        n += more ? 2 : 1;
+        if (ok && next) t5_commit(smem_addr(&wide_empty[nk]), lead);
+        n += next ? 2 : 1;
       }
     }
     if (!ok && lane == 0) fail();
@@ -390,44 +403,53 @@ __global__ void __launch_bounds__(kKpThreads, 1)
         if (lane == 0) mbar_arrive(&q_full[half]);
       }
       const int last_row = min(rows, g.rt * kKpRows + 128 * (half + 1)) - 1, first_row = g.rt * kKpRows + 128 * half;
-      for (int t = g.tile0; t < g.tile1; ++t, ++unit) {
+      const int tile0 = g.tile0, tile1 = g.tile1, lo = g.lo, hi = g.hi;
+      // positions of the half's first and last row
+      const int pos_first = pos0 + first_row / a.group, pos_last = pos0 + last_row / a.group;
+      for (int t = tile0; t < tile1 && ok; ++t, ++unit) {
         if (!busy) continue;
-        ok = __all_sync(~0u, mbar_wait_clocked(&s_full[half], k & 1u, &abort_flag));
-        if (!ok) break;
-        t5_fence_after();
         const KpSlot& slot = slots[unit % kKpSlots];
         const int key0 = t * kKpKeys;
-        const bool masked = slot.bad != 0 || key0 < g.lo || key0 + kKpKeys > g.hi ||
-                            (a.causal && key0 + kKpKeys - 1 > pos0 + first_row / a.group) ||
-                            (a.window > 0 && key0 <= pos0 + last_row / a.group - a.window);
-        const float top = masked ? kp_top<true>(a, row, ts, slot, shift, key0, g.lo, g.hi)
-                                 : kp_top<false>(a, row, ts, slot, shift, key0, g.lo, g.hi);
-        if (__any_sync(~0u, top > row.m + 8.f)) {
-          const float mn = fmaxf(row.m, top), f = row.m == -INFINITY ? 0.f : fast_exp2(row.m - mn);
-          row.m = mn;
-          row.l *= f;
-          if (t > g.tile0) {  // O holds the units before: wait for the last of them
-            ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u, &abort_flag));
-            if (!ok) break;
-            t5_fence_after();
+        bool masked = false;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float x[32];
-              t5_ld32(to + c, x);
+        for (int sub = 0; sub < 2; ++sub) {
+          ok = __all_sync(~0u, mbar_wait_clocked(&s_full[half][sub], k >> 1 & 1u, &abort_flag));
+          if (!ok) break;
+          t5_fence_after();
+          if (sub == 0)
+            masked = slot.bad != 0 || key0 < lo || key0 + kKpKeys > hi || (a.causal && key0 + kKpKeys - 1 > pos_first) ||
+                     (a.window > 0 && key0 <= pos_last - a.window);
+          const uint32_t tile = ts + kKpSub * sub;
+          const int first = kKpSub * sub;
+          float x[kKpSub];
+          const float top = masked ? kp_scores<true>(a, row, tile, slot, shift, first, key0, lo, hi, x)
+                                   : kp_scores<false>(a, row, tile, slot, shift, first, key0, lo, hi, x);
+          if (__any_sync(~0u, top > row.m + 8.f)) {
+            const float mn = fmaxf(row.m, top), f = row.m == -INFINITY ? 0.f : fast_exp2(row.m - mn);
+            row.m = mn;
+            row.l *= f;
+            if (t > tile0 || sub > 0) {  // O holds the keys before: wait for the last product
+              ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u, &abort_flag));
+              if (!ok) break;
+              t5_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                float y[16];
+                t5_ld16(to + c, y);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] *= f;
-              t5_st32(to + c, x);
+                for (int i = 0; i < 16; ++i) y[i] *= f;
+                t5_st16f(to + c, y);
+              }
             }
           }
+          const float m = row.m == -INFINITY ? 0.f : row.m;
+          row.l += masked ? kp_weights<true>(row, tile, slot, shift, first, m, x) : kp_weights<false>(row, tile, slot, shift, first, m, x);
+          t5_st_wait();
+          t5_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[half][sub]);
+          ++k;
         }
-        const float m = row.m == -INFINITY ? 0.f : row.m;
-        row.l += masked ? kp_weights<true>(a, row, ts, slot, shift, key0, g.lo, g.hi, m)
-                        : kp_weights<false>(a, row, ts, slot, shift, key0, g.lo, g.hi, m);
-        t5_st_wait();
-        t5_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[half]);
-        ++k;
       }
       if (ok && busy) {
         ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u, &abort_flag));

@@ -173,6 +173,24 @@ __device__ __forceinline__ void t5_ld32(uint32_t taddr, float (&x)[32]) {
       : "r"(taddr)
       : "memory");
 }
+// 16 columns, waited for, and back.
+__device__ __forceinline__ void t5_ld16(uint32_t taddr, float (&x)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]),
+        "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void t5_st16f(uint32_t taddr, const float (&x)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+          taddr),
+      "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "f"(x[8]), "f"(x[9]), "f"(x[10]),
+      "f"(x[11]), "f"(x[12]), "f"(x[13]), "f"(x[14]), "f"(x[15])
+      : "memory");
+}
 // The same without the wait; t5_ld32_wait on the same registers (once no other
 // load matters) comes before their first use.
 __device__ __forceinline__ void t5_ld32_async(uint32_t taddr, float (&x)[32]) {
@@ -195,16 +213,6 @@ __device__ __forceinline__ void t5_ld32_wait(float (&x)[32]) {
                :
                : "memory");
   asm volatile("" : "+f"(x[30]), "+f"(x[31]));
-}
-__device__ __forceinline__ void t5_st32(uint32_t taddr, const float (&x)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
-      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "f"(x[8]), "f"(x[9]), "f"(x[10]),
-      "f"(x[11]), "f"(x[12]), "f"(x[13]), "f"(x[14]), "f"(x[15]), "f"(x[16]), "f"(x[17]), "f"(x[18]), "f"(x[19]), "f"(x[20]),
-      "f"(x[21]), "f"(x[22]), "f"(x[23]), "f"(x[24]), "f"(x[25]), "f"(x[26]), "f"(x[27]), "f"(x[28]), "f"(x[29]), "f"(x[30]),
-      "f"(x[31])
-      : "memory");
 }
 __device__ __forceinline__ void t5_st16(uint32_t taddr, const uint32_t (&x)[16]) {
   asm volatile(
