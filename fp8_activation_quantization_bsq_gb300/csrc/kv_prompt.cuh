@@ -299,18 +299,12 @@ __global__ void __launch_bounds__(kKpThreads, 1)
     const auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(~0u, mbar_wait_clocked(bar, parity, &abort_flag)); };
     const auto scores = [&](int h, int sub, uint32_t w) {  // S tile: tensor memory columns 128 h + 64 sub ..
       const uint32_t qa = q_addr + h * S::kHalfBytes, ka = wide_addr + w * S::kWideBytes + sub * (kKpSub * 128);
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-        t5_mma_f16(tmem + 128 * h + kKpSub * sub, t5_desc_sw128(qa + (i >> 2) * 16384 + 32 * (i & 3)),
-                   t5_desc_sw128(ka + (i >> 2) * 16384 + 32 * (i & 3)), kIdS, i, lead);
+      t5_mma_f16_ss<D / 64>(tmem + 128 * h + kKpSub * sub, t5_desc_sw128(qa), t5_desc_sw128(ka), kIdS, lead);
       t5_commit(smem_addr(&s_full[h][sub]), lead);
     };
     const auto values = [&](int h, int sub, uint32_t w, uint32_t accumulate) {  // O of half h: columns 256 + 128 h ..
       const uint32_t va = wide_addr + w * S::kWideBytes + sub * (kKpSub * 128);
-#pragma unroll
-      for (int i = 0; i < kKpSub / 16; ++i)
-        t5_mma_f16_ta(tmem + 256 + 128 * h, tmem + 128 * h + kKpSub * sub + 8 * i, t5_desc_sw128_n(va + 2048 * i, 16384), kIdO,
-                      accumulate | i, lead);
+      t5_mma_f16_ts(tmem + 256 + 128 * h, tmem + 128 * h + kKpSub * sub, t5_desc_sw128_n(va, 16384), kIdO, accumulate, lead);
       t5_commit(smem_addr(&pv_done[h]), lead);
     };
     while (ok && walk.step(a)) {

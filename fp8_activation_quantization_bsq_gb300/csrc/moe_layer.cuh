@@ -279,33 +279,26 @@ __device__ __noinline__ void moe_finish_h(float g, float u, float hsf, int lane,
   moe_quant_lane<FMT>(h, hsf, lane, row_bytes, scale_word);
 }
 
-// One stage's products into accumulators d and d + 64 (the tile's halves).
-// da, db, ds: descriptors of the stage's weights, tokens and scales.  FULL: a
-// whole stage of two halves, without a branch; else `slices` products of 32
-// bytes of each row, `atoms` scale atoms.  Scale addresses in tensor memory
-// are multiples of 4 columns.
-template <int FMT, bool FULL>
+// One stage's products into accumulators d and d + 64 (the tile's halves) where
+// the stage is not whole (t5_stage_scaled): `slices` products of 32 bytes of each row, `atoms`
+// scale atoms, one half or two.  da, db, ds: descriptors of the stage's weights, tokens and scales.
+template <int FMT>
 __device__ __forceinline__ void moe_products(uint32_t d, uint64_t da, uint64_t db, uint64_t ds, uint32_t n, uint32_t sf,
                                              uint32_t fresh, int slices, int atoms, bool two, uint32_t lead) {
   constexpr int kAtoms = MoeFmt<FMT>::kAtoms;
-#pragma unroll
-  for (int q = 0; q < kAtoms; ++q) {
-    if (FULL || q < atoms) {
-      t5_copy_atom(sf + 4 * q, ds + 32 * q, lead);
-      if (FULL || two) t5_copy_atom(sf + 16 + 4 * q, ds + 32 * (kAtoms + q), lead);
-      t5_copy_atom(sf + 32 + 4 * q, ds + 32 * (2 * kAtoms + q), lead);
-    }
+#pragma unroll 1
+  for (int q = 0; q < atoms; ++q) {
+    t5_copy_atom(sf + 4 * q, ds + 32 * q, lead);
+    if (two) t5_copy_atom(sf + 16 + 4 * q, ds + 32 * (kAtoms + q), lead);
+    t5_copy_atom(sf + 32 + 4 * q, ds + 32 * (2 * kAtoms + q), lead);
   }
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    if (FULL || m < slices) {
-      constexpr uint32_t kPer = 4 / kAtoms;  // slices per atom
-      const uint32_t atom = m / kPer, id = (m % kPer) * (4 / kPer);
-      const uint32_t idesc = t5_idesc_scaled<FMT>(n, id);
-      const uint32_t sfb = sf + 32 + 4 * atom;
-      t5_mma_scaled<FMT>(d, da + 2 * m, db + 2 * m, idesc, sf + 4 * atom, sfb, fresh | m, lead);
-      if (FULL || two) t5_mma_scaled<FMT>(d + 64, da + kMoeHalfBytes / 16 + 2 * m, db + 2 * m, idesc, sf + 16 + 4 * atom, sfb, fresh | m, lead);
-    }
+#pragma unroll 1
+  for (int m = 0; m < slices; ++m) {
+    constexpr uint32_t kPer = 4 / kAtoms;  // slices per atom
+    const uint32_t atom = m / kPer, id = (m % kPer) * (4 / kPer), sfb = sf + 32 + 4 * atom;
+    const uint32_t idesc = t5_idesc_scaled<FMT>(n, id);
+    t5_mma_scaled<FMT>(d, da + 2 * m, db + 2 * m, idesc, sf + 4 * atom, sfb, fresh | m, lead);
+    if (two) t5_mma_scaled<FMT>(d + 64, da + kMoeHalfBytes / 16 + 2 * m, db + 2 * m, idesc, sf + 16 + 4 * atom, sfb, fresh | m, lead);
   }
 }
 
@@ -551,9 +544,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           const uint64_t da = t5_desc_sw128(st), db = t5_desc_sw128(tok), ds = t5_desc_atom(sc);
           const int left = cols - kc * kElems;
           if (left >= kElems && two)
-            moe_products<FMT, true>(d, da, db, ds, n, sf, fresh, 4, kAtoms, true, lead);
+            t5_stage_scaled<FMT>(d, da, db, ds, t5_idesc_scaled<FMT>(n, 0), sf, fresh, lead);
           else
-            moe_products<FMT, false>(d, da, db, ds, n, sf, fresh, min(4, (left + kElems / 4 - 1) / (kElems / 4)),
+            moe_products<FMT>(d, da, db, ds, n, sf, fresh, min(4, (left + kElems / 4 - 1) / (kElems / 4)),
                                      min(kAtoms, (left + kAtomElems - 1) / kAtomElems), two, lead);
           fresh = 1;
           t5_commit(smem_addr(&empty_bar[stage]), lead);

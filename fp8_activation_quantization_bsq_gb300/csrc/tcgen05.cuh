@@ -89,6 +89,52 @@ __device__ __forceinline__ void t5_copy_atom(uint32_t taddr, uint64_t desc, uint
       : "memory");
 }
 
+// A whole stage of the block-scaled products of two 128-row tiles (accumulators d
+// and d + 64, operand a and 16 KB on) with the same second operand b: the scale
+// atoms ds.. of both tiles and of b (ATOMS each) to tensor memory at sf, sf + 16 and sf + 32, then four
+// slices of 32 bytes of each row.  One statement, as for FP16 below.
+#define BSQ_T5_CP(TOFF, DOFF)                                      \
+  "add.u32 t, %6, " #TOFF ";\n\tadd.u64 e, %5, " #DOFF ";\n\t"     \
+  "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [t], e;\n\t"
+#define BSQ_T5_BS(KIND, OFF, OFF2, SA, SA2, SB, ID, ACC)                                                            \
+  "add.u64 x, %2, " #OFF ";\n\tadd.u64 y, %3, " #OFF ";\n\tadd.u32 t, %6, " #SA ";\n\tadd.u32 u, %6, " #SB ";\n\t"       \
+  "add.u32 i, %4, " #ID ";\n\t@q tcgen05.mma.cta_group::1.kind::" KIND " [%0], x, y, i, [t], [u], " ACC ";\n\t"          \
+  "add.u64 x, %2, " #OFF2 ";\n\tadd.u32 t, %6, " #SA2 ";\n\t@q tcgen05.mma.cta_group::1.kind::" KIND                  \
+  " [%1], x, y, i, [t], [u], " ACC ";\n\t"
+#define BSQ_T5_OPEN                                                                                                 \
+  "{\n\t.reg .pred p, o, q;\n\t.reg .b32 t, u, i;\n\t.reg .b64 e, x, y;\n\tsetp.ne.b32 p, %7, 0;\n\t"                 \
+  "setp.ne.b32 q, %8, 0;\n\tsetp.eq.b32 o, 0, 0;\n\t"
+#define BSQ_T5_ARGS                                                                                                 \
+  ::"r"(d), "r"(d + 64), "l"(a), "l"(b), "r"(idesc), "l"(ds), "r"(sf), "r"(accumulate), "r"(lead) : "memory"
+template <int FMT>
+__device__ __forceinline__ void t5_stage_scaled(uint32_t d, uint64_t a, uint64_t b, uint64_t ds, uint32_t idesc, uint32_t sf,
+                                                uint32_t accumulate, uint32_t lead) {
+  // the scale ids of a slice (bits 4 and 29 of idesc): 2 -> 0x40000020, 1 -> 0x20000010, 3 -> 0x60000030
+  if constexpr (FMT == kNVFP4)
+    asm volatile(BSQ_T5_OPEN BSQ_T5_CP(0, 0) BSQ_T5_CP(16, 128) BSQ_T5_CP(32, 256) BSQ_T5_CP(4, 32) BSQ_T5_CP(20, 160) BSQ_T5_CP(36, 288)
+                 BSQ_T5_CP(8, 64) BSQ_T5_CP(24, 192) BSQ_T5_CP(40, 320) BSQ_T5_CP(12, 96) BSQ_T5_CP(28, 224) BSQ_T5_CP(44, 352)
+                 BSQ_T5_BS("mxf4nvf4.block_scale.scale_vec::4X", 0, 1024, 0, 16, 32, 0, "p")
+                 BSQ_T5_BS("mxf4nvf4.block_scale.scale_vec::4X", 2, 1026, 4, 20, 36, 0, "o")
+                 BSQ_T5_BS("mxf4nvf4.block_scale.scale_vec::4X", 4, 1028, 8, 24, 40, 0, "o")
+                 BSQ_T5_BS("mxf4nvf4.block_scale.scale_vec::4X", 6, 1030, 12, 28, 44, 0, "o") "}" BSQ_T5_ARGS);
+  else if constexpr (FMT == kMXFP4)
+    asm volatile(BSQ_T5_OPEN BSQ_T5_CP(0, 0) BSQ_T5_CP(16, 64) BSQ_T5_CP(32, 128) BSQ_T5_CP(4, 32) BSQ_T5_CP(20, 96) BSQ_T5_CP(36, 160)
+                 BSQ_T5_BS("mxf4.block_scale.scale_vec::2X", 0, 1024, 0, 16, 32, 0, "p")
+                 BSQ_T5_BS("mxf4.block_scale.scale_vec::2X", 2, 1026, 0, 16, 32, 0x40000020, "o")
+                 BSQ_T5_BS("mxf4.block_scale.scale_vec::2X", 4, 1028, 4, 20, 36, 0, "o")
+                 BSQ_T5_BS("mxf4.block_scale.scale_vec::2X", 6, 1030, 4, 20, 36, 0x40000020, "o") "}" BSQ_T5_ARGS);
+  else
+    asm volatile(BSQ_T5_OPEN BSQ_T5_CP(0, 0) BSQ_T5_CP(16, 32) BSQ_T5_CP(32, 64)
+                 BSQ_T5_BS("mxf8f6f4.block_scale.scale_vec::1X", 0, 1024, 0, 16, 32, 0, "p")
+                 BSQ_T5_BS("mxf8f6f4.block_scale.scale_vec::1X", 2, 1026, 0, 16, 32, 0x20000010, "o")
+                 BSQ_T5_BS("mxf8f6f4.block_scale.scale_vec::1X", 4, 1028, 0, 16, 32, 0x40000020, "o")
+                 BSQ_T5_BS("mxf8f6f4.block_scale.scale_vec::1X", 6, 1030, 0, 16, 32, 0x60000030, "o") "}" BSQ_T5_ARGS);
+}
+#undef BSQ_T5_CP
+#undef BSQ_T5_BS
+#undef BSQ_T5_OPEN
+#undef BSQ_T5_ARGS
+
 // D (128 x N, FP32) (+)= A B^T with block scales, K = 32 bytes of each row.
 #define BSQ_T5_MMA_SCALED(KIND)                                                                                        \
   asm volatile(                                                                                                        \
@@ -131,22 +177,38 @@ __device__ __forceinline__ void t5_ld8_pair(uint32_t ta, uint32_t tb, float (&x)
       : "memory");
 }
 
-// D (128 x N, FP32) (+)= A B^T of FP16 operands, K = 16: A from shared memory or
-// (packed pairs, 8 columns) from tensor memory.
-__device__ __forceinline__ void t5_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
+// FP16 products in batches: one statement of straight code, so that an operand
+// costs one addition on its base.  (A product at a time came to about 60 cycles of a
+// single warp's issue, as long as the product itself.)
+#define BSQ_T5_F16_SS(OFF, ACC)                              \
+  "add.u64 a, %1, " #OFF ";\n\tadd.u64 b, %2, " #OFF ";\n\t" \
+  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, " ACC ";\n\t"
+// D (128 x N, FP32) = A B^T, K = 64 KBLOCKS: operand blocks of 64 columns 16384 bytes apart, both in
+// shared memory with the 128-byte swizzle.
+template <int KBLOCKS>
+__device__ __forceinline__ void t5_mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t lead) {
+  if constexpr (KBLOCKS == 1)
+    asm volatile("{\n\t.reg .pred z, o, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.ne.b32 z, 0, 0;\n\tsetp.eq.b32 o, 0, 0;\n\t"
+                 BSQ_T5_F16_SS(0, "z") BSQ_T5_F16_SS(2, "o") BSQ_T5_F16_SS(4, "o") BSQ_T5_F16_SS(6, "o") "}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(lead) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred z, o, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.ne.b32 z, 0, 0;\n\tsetp.eq.b32 o, 0, 0;\n\t"
+                 BSQ_T5_F16_SS(0, "z") BSQ_T5_F16_SS(2, "o") BSQ_T5_F16_SS(4, "o") BSQ_T5_F16_SS(6, "o")
+                 BSQ_T5_F16_SS(1024, "o") BSQ_T5_F16_SS(1026, "o") BSQ_T5_F16_SS(1028, "o") BSQ_T5_F16_SS(1030, "o") "}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(lead) : "memory");
 }
-__device__ __forceinline__ void t5_mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
+#undef BSQ_T5_F16_SS
+#define BSQ_T5_F16_TS(AOFF, BOFF, ACC)                        \
+  "add.u32 a, %1, " #AOFF ";\n\tadd.u64 b, %2, " #BOFF ";\n\t" \
+  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, " ACC ";\n\t"
+// D (128 x N, FP32) (+)= A B, K = 64: A from tensor memory (packed pairs, 8 columns per 16), B rows of
+// K 128 bytes apart.
+__device__ __forceinline__ void t5_mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t lead) {
+  asm volatile("{\n\t.reg .pred p, o, q;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.eq.b32 o, 0, 0;\n\t"
+               BSQ_T5_F16_TS(0, 0, "p") BSQ_T5_F16_TS(8, 128, "o") BSQ_T5_F16_TS(16, 256, "o") BSQ_T5_F16_TS(24, 384, "o") "}"
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
 }
+#undef BSQ_T5_F16_TS
 // Its instruction descriptor, M = 128: FP32 sums (4), FP16 operands (0 at 7
 // and 10), the second operand N-major (16), N >> 3 at 17, M >> 4 at 24.
 __host__ __device__ constexpr uint32_t t5_idesc_f16(uint32_t n, bool b_n_major) {
