@@ -123,6 +123,21 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
   return g_encode_tiled;
 }
 
+PFN_cuTensorMapReplaceAddress_v12000 replace_address() {
+  std::lock_guard<std::mutex> lock(g_mu);
+  static bool tried = false;
+  static PFN_cuTensorMapReplaceAddress_v12000 found = nullptr;
+  if (!tried) {
+    tried = true;
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapReplaceAddress", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      found = reinterpret_cast<PFN_cuTensorMapReplaceAddress_v12000>(fn);
+  }
+  return found;
+}
+
 bsq_status allow_smem(const void* kernel, int bytes, int index) {
   static std::vector<std::pair<const void*, int>> done;  // under g_mu
   std::lock_guard<std::mutex> lock(g_mu);

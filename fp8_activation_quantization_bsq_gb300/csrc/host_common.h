@@ -50,7 +50,8 @@ bsq_status host_device(HostDevice* out);
 // Allow `kernel` `bytes` of dynamic shared memory on device `index` (once per kernel and device).
 bsq_status allow_smem(const void* kernel, int bytes, int index);
 
-// cuTensorMapEncodeTiled, or NULL when the driver does not have it.
+// cuTensorMapEncodeTiled and cuTensorMapReplaceAddress, or NULL when the driver does not have them.
 PFN_cuTensorMapEncodeTiled_v12000 encode_tiled();
+PFN_cuTensorMapReplaceAddress_v12000 replace_address();
 
 }  // namespace bsq

@@ -202,8 +202,10 @@ int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t he
   const bool few = max_rows <= kKvFewRows;
   const int tile = few ? kKvTile : kKpKeys;
   const CUtensorMapSwizzle swizzle = !few ? CU_TENSOR_MAP_SWIZZLE_NONE : dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  if (!cache_map(&mk, k_cache, dim, page, kv_heads, num_pages, cs_tok, cs_head, cs_page, tile, swizzle) ||
-      !cache_map(&mv, v_cache, dim, page, kv_heads, num_pages, cs_tok, cs_head, cs_page, tile, swizzle))
+  auto at = replace_address();
+  if (!at || !cache_map(&mk, k_cache, dim, page, kv_heads, num_pages, cs_tok, cs_head, cs_page, tile, swizzle)) return BSQ_ERR_CUDA;
+  mv = mk;  // the values' map differs in its address alone
+  if (at(&mv, const_cast<void*>(v_cache)) != CUDA_SUCCESS)
     return BSQ_ERR_CUDA;
   if (dim == 64)
     return dtype == BSQ_F16 ? launch_attention_rows<64, true>(a, max_rows, mk, mv, d, st)

@@ -113,12 +113,12 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     total, heads, dim = shape
     kv_heads, cache = _cache(dim, index, k_cache, v_cache, k_scales, v_scales, block_table, offsets, seq_lens)
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.dtype != q.dtype or out.shape != shape or not out.is_contiguous() or out.get_device() != index:
         raise ValueError("out must be a contiguous tensor of q's shape, type and device")
     if lse is None:
         if return_lse:
-            lse = q.new_empty((total, heads), dtype=_F32)
+            lse = torch.empty((total, heads), dtype=_F32, device=q.device)
     elif lse.dtype is not _F32 or lse.shape != (total, heads) or not lse.is_contiguous() or lse.get_device() != index:
         raise ValueError("lse must be a contiguous float32 (tokens, heads) tensor on q's device")
     if workspace is None:
@@ -186,7 +186,7 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w13_scal
     else:
         sfs = (None, None, None, None)
     if out is None:
-        out = x.new_empty(shape)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out.dtype is not _BF16 or out.shape != shape or out.stride(1) != 1 or out.get_device() != index:
         raise ValueError("out must be a (tokens, hidden) bfloat16 tensor with unit inner stride on x's device")
     if workspace is None:
