@@ -446,7 +446,10 @@ __global__ void __launch_bounds__(kKpThreads, 1)
         }
       }
       if (ok && busy) {
-        ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u, &abort_flag));
+        // the last two products, in order: a wait for the last alone would
+        // also pass while the one before it is still open
+        ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], k & 1u, &abort_flag)) &&
+             __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u, &abort_flag));
         t5_fence_after();
       }
       if (!ok && lane == 0) fail();

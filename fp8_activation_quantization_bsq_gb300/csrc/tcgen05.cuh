@@ -331,6 +331,7 @@ __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v) 
 
 // Barrier of `threads` threads of the block (id 1..15).
 __device__ __forceinline__ void named_sync(int id, int threads) {
+  __syncwarp();  // the barrier wants whole warps
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
