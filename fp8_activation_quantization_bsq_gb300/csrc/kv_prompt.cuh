@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
   uint8_t* wide = smem + 2 * S::kHalfBytes;
   uint8_t* raw = wide + kKpWide * S::kWideBytes;
   __shared__ uint64_t raw_full[kKpRaw], raw_empty[kKpRaw], wide_full[kKpWide], wide_empty[kKpWide];
-  __shared__ uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], drain_bar;  // [half][S tile]
+  __shared__ uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2], drain_bar;  // [half][S tile]
   __shared__ KpSlot slots[kKpSlots];
   __shared__ KvStart start;
   __shared__ KvWalk<kKpRows, kKpKeys> walks[4];
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
         mbar_init(&p_full[i][t], 4);
       }
       mbar_init(&pv_done[i], 1);
+      mbar_init(&o_full[i], 1);
     }
     mbar_init(&drain_bar, 1);
     abort_flag = 0u;
@@ -333,6 +334,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
             t5_fence_after();
             values(h, sub, v, u | sub);
             if (sub == 1) {
+              if (!next) t5_commit(smem_addr(&o_full[h]), lead);
               ++k[h];
               if (h == halves - 1) t5_commit(smem_addr(&wide_empty[v]), lead);
             }
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const uint32_t ts = lanes + 128 * half, to = lanes + 256 + 128 * half;
     const int shift = min(a.page_shift, 7);
-    uint32_t unit = 0, k = 0;
+    uint32_t unit = 0, k = 0, finished = 0;
     bool ok = true;
     while (walk.step_together(a, 1, 256, tid == 0, &more[0], &abort_flag)) {
       const int rows = g.s.n * a.group, r = g.rt * kKpRows + r_tile, pos0 = g.s.len - g.s.n;
@@ -422,7 +424,9 @@ __global__ void __launch_bounds__(kKpThreads, 1)
             const float mn = fmaxf(row.m, top), f = row.m == -INFINITY ? 0.f : fast_exp2(row.m - mn);
             row.m = mn;
             row.l *= f;
-            if (t > tile0 || sub > 0) {  // O holds the keys before: wait for the last product
+            // O holds the keys before: wait for the last product (the one before it is done: these
+            // scores came after it)
+            if (t > tile0 || sub > 0) {
               ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u, &abort_flag));
               if (!ok) break;
               t5_fence_after();
@@ -446,10 +450,8 @@ __global__ void __launch_bounds__(kKpThreads, 1)
         }
       }
       if (ok && busy) {
-        // the last two products, in order: a wait for the last alone would
-        // also pass while the one before it is still open
-        ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], k & 1u, &abort_flag)) &&
-             __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u, &abort_flag));
+        // of its own, once an item: pv_done may be two phases behind here, which its parity could not tell
+        ok = __all_sync(~0u, mbar_wait_clocked(&o_full[half], finished++ & 1u, &abort_flag));
         t5_fence_after();
       }
       if (!ok && lane == 0) fail();
