@@ -57,10 +57,16 @@ struct KvAttnArgs {
   int64_t total, num_pages;
   int batch, heads, kv_heads, group, page, page_shift, table_width, causal, window;
   float scale_log2;               // sm_scale * log2(e)
+  uint64_t group_inv;             // ceil(2^64 / group), for kv_token
   uint32_t* ready;                // [block] part stored, zero between calls
   float* part;                    // [block][rows * D + 2 * rows]: sums, maxima, weights' sums
   unsigned int* err;
 };
+
+// The token of row r of a sequence, r / group (exact for r < 2^32; a division is some forty instructions).
+__device__ __forceinline__ int kv_token(const KvAttnArgs& a, int r) {
+  return a.group == 1 ? r : static_cast<int>(__umul64hi(static_cast<uint64_t>(r), a.group_inv));
+}
 
 // A sequence's rows and, per row tile, its keys.
 struct KvSeq {
@@ -86,7 +92,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnArgs& a, int b, bool report)
 template <int RT>
 __device__ __forceinline__ void kv_keys(const KvAttnArgs& a, const KvSeq& s, int rt, int& lo, int& hi) {
   const int rows = s.n * a.group;
-  const int i0 = rt == 0 ? 0 : rt * RT / a.group, i1 = rows <= (rt + 1) * RT ? s.n - 1 : ((rt + 1) * RT - 1) / a.group;
+  const int i0 = kv_token(a, rt * RT), i1 = rows <= (rt + 1) * RT ? s.n - 1 : kv_token(a, (rt + 1) * RT - 1);
   hi = a.causal ? min(s.len, s.len - s.n + i1 + 1) : s.len;
   lo = a.window > 0 ? max(0, s.len - s.n + i0 - a.window + 1) : 0;
   if (hi <= lo) lo = hi = 0;
@@ -137,8 +143,9 @@ struct KvSegment {
 // loop over the keys some fifty of them.
 template <int RT, int TILE>
 struct KvWalk {
-  int64_t u, end, before, per_head;
-  int b;
+  int64_t u, end, at;       // the next unit, the run's end, the first unit of item (b, head, rt)
+  int count, b, head, rt;   // the item's units
+  int lo, hi;
   KvSeq s;
   KvSegment seg;
   // Whole warp; true while there is an item, described by seg.
@@ -162,44 +169,56 @@ struct KvWalk {
     if (mine) {
       u = start.begin;
       end = start.end;
-      before = start.before;
       b = start.seq;
       load(a);
+      at = start.before;
+      head = rt = 0;
+      int64_t per_head = kv_seq_units<RT, TILE>(a, s);
+      while (u >= at + per_head * a.kv_heads) {  // kv_start names a sequence at or before the first unit's
+        at += per_head * a.kv_heads;
+        ++b;
+        load(a);
+        per_head = kv_seq_units<RT, TILE>(a, s);
+      }
+      head = static_cast<int>((u - at) / per_head);
+      at += head * per_head;
+      keys(a);
     }
     __syncwarp();
   }
-  __device__ __forceinline__ void load(const KvAttnArgs& a) {
-    s = kv_seq<RT>(a, b, false);
-    per_head = kv_seq_units<RT, TILE>(a, s);
+  __device__ __forceinline__ void load(const KvAttnArgs& a) { s = kv_seq<RT>(a, b, false); }
+  __device__ __forceinline__ void keys(const KvAttnArgs& a) {
+    lo = hi = count = 0;
+    if (s.row_tiles == 0) return;  // a sequence without rows
+    kv_keys<RT>(a, s, rt, lo, hi);
+    count = kv_units<TILE>(lo, hi);
   }
+  // The item that holds unit u, from the one before it.
   __device__ __forceinline__ bool next(const KvAttnArgs& a, KvSegment& g) {
     if (u >= end) return false;
-    while (u >= before + per_head * a.kv_heads) {
-      before += per_head * a.kv_heads;
-      ++b;
-      load(a);
-    }
-    const int64_t rel = u - before;
-    g.head = static_cast<int>(rel / per_head);
-    int64_t at = before + g.head * per_head;
-    int rt = 0;
-    while (true) {
-      kv_keys<RT>(a, s, rt, g.lo, g.hi);
-      const int c = kv_units<TILE>(g.lo, g.hi);
-      if (u < at + c) {
-        g.first = at;
-        g.count = c;
-        break;
+    while (u >= at + count) {
+      at += count;
+      if (++rt >= s.row_tiles) {
+        rt = 0;
+        if (++head >= a.kv_heads || s.row_tiles == 0) {
+          head = 0;
+          ++b;
+          load(a);
+        }
       }
-      at += c;
-      ++rt;
+      keys(a);
     }
+    g.first = at;
+    g.count = count;
+    g.lo = lo;
+    g.hi = hi;
+    g.head = head;
     g.rt = rt;
     g.b = b;
     g.s = s;
-    const int64_t stop = min(end, g.first + g.count);
-    g.tile0 = g.lo / TILE + static_cast<int>(u - g.first);
-    g.tile1 = g.hi > g.lo ? g.tile0 + static_cast<int>(stop - u) : g.tile0;
+    const int64_t stop = min(end, at + count);
+    g.tile0 = lo / TILE + static_cast<int>(u - at);
+    g.tile1 = hi > lo ? g.tile0 + static_cast<int>(stop - u) : g.tile0;
     u = stop;
     return true;
   }
@@ -435,7 +454,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
       const int rows = g.s.n * a.group, pos0 = g.s.len - g.s.n;
       const int lo = g.lo, hi = g.hi, tile1 = g.tile1;
       // positions of the tile's first and last row
-      const int pos_first = pos0 + g.rt * RT / a.group, pos_last = pos0 + (min(rows, (g.rt + 1) * RT) - 1) / a.group;
+      const int pos_first = pos0 + kv_token(a, g.rt * RT), pos_last = pos0 + kv_token(a, min(rows, (g.rt + 1) * RT) - 1);
       // Query rows 8 t + gq, dimensions D/4 c .. + D/4 - 1: the second operand
       // of K Q^T.  For NT = 4 they stay in shared memory, which all warps read.
       uint32_t q[NT == 4 ? 1 : NT][D / 8];
@@ -445,10 +464,10 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
       if (NT == 4) named_sync(1, kT);  // the last item's rows have been read
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int r = g.rt * RT + 8 * t + gq;
+        const int r = g.rt * RT + 8 * t + gq, tok = kv_token(a, r);
         float amax = 0.f;
         uint4 v[D / 32];
-        const uint16_t* src = a.q + static_cast<int64_t>(g.s.t0 + r / a.group) * a.q_tok + (g.head * a.group + r % a.group) * a.q_head + c * (D / 4);
+        const uint16_t* src = a.q + static_cast<int64_t>(g.s.t0 + tok) * a.q_tok + (g.head * a.group + r - tok * a.group) * a.q_head + c * (D / 4);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           v[i] = r < rows ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
@@ -477,7 +496,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           rowfac[t][h] = __shfl_sync(~0u, rf, 4 * (2 * c + h));
-          pos[t][h] = pos0 + (g.rt * RT + 8 * t + 2 * c + h) / a.group;
+          pos[t][h] = pos0 + kv_token(a, g.rt * RT + 8 * t + 2 * c + h);
           m[t][h] = -INFINITY;
           l[t][h] = 0.f;
         }
@@ -747,7 +766,8 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
             }
           } else {
             const int rr = g.rt * RT + r;
-            const int64_t row = static_cast<int64_t>(g.s.t0 + rr / a.group) * a.heads + g.head * a.group + rr % a.group;
+            const int tok = kv_token(a, rr);
+            const int64_t row = static_cast<int64_t>(g.s.t0 + tok) * a.heads + g.head * a.group + rr - tok * a.group;
             const float f = al > 0.f ? 1.f / al : 0.f;
 #pragma unroll
             for (int i = 0; i < kOwn; ++i)

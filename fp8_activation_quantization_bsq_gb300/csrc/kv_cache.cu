@@ -160,7 +160,9 @@ int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t he
                                  page, cs_page, cs_head, cs_tok, table, table_ld, table_width, offsets, lens, batch);
       s != BSQ_OK)
     return s;
-  if (heads < 1 || heads % kv_heads != 0 || heads / kv_heads > 64 || window < 0 || max_q < 0) return BSQ_ERR_SHAPE;
+  if (heads < 1 || heads % kv_heads != 0 || heads / kv_heads > 64 || total * (heads / kv_heads) >= (int64_t(1) << 31) || window < 0 ||
+      max_q < 0)
+    return BSQ_ERR_SHAPE;
   if (!std::isfinite(sm_scale)) return BSQ_ERR_VALUE;
   if (total == 0 || batch == 0) return BSQ_OK;
   if (max_q < 1) return BSQ_ERR_SHAPE;
@@ -187,6 +189,7 @@ int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t he
   a.heads = heads;
   a.kv_heads = kv_heads;
   a.group = heads / kv_heads;
+  a.group_inv = a.group > 1 ? ~uint64_t{0} / static_cast<uint64_t>(a.group) + 1 : 0;
   a.page = page;
   a.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
   a.table_width = table_width;

@@ -367,29 +367,27 @@ __global__ void __launch_bounds__(kKpThreads, 1)
       const int rows = g.s.n * a.group, r = g.rt * kKpRows + r_tile, pos0 = g.s.len - g.s.n;
       const int half_rows = min(128, rows - g.rt * kKpRows - 128 * half);  // <= 0: the half is empty
       const bool busy = half_rows > 0 && g.tile1 > g.tile0;
-      const int64_t out_row = static_cast<int64_t>(g.s.t0 + r / a.group) * a.heads + g.head * a.group + r % a.group;
-      KpRow row{-INFINITY, 0.f, 0.f, pos0 + r / a.group, r < rows};
+      const int tok = kv_token(a, r);
+      const int64_t out_row = static_cast<int64_t>(g.s.t0 + tok) * a.heads + g.head * a.group + r - tok * a.group;
+      KpRow row{-INFINITY, 0.f, 0.f, pos0 + tok, r < rows};
       if (busy) {
         // the query row in FP16, 2^-eq of it, largest magnitude in [2^12, 2^13)
-        const uint16_t* src = a.q + static_cast<int64_t>(g.s.t0 + r / a.group) * a.q_tok + (g.head * a.group + r % a.group) * a.q_head;
-        float amax = 0.f;
-        if (row.live) {
-          uint32_t x = 0;
-#pragma unroll 4
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
-            x = elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(x, v.x), v.y), v.z), v.w);
-          }
-          amax = elem_absmax_final<F16>(x);
-        }
+        const uint16_t* src = a.q + static_cast<int64_t>(g.s.t0 + tok) * a.q_tok + (g.head * a.group + r - tok * a.group) * a.q_head;
+        uint4 v[D / 8];
+        uint32_t mag = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) v[i] = row.live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          mag = elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(mag, v[i].x), v[i].y), v[i].z), v[i].w);
+        const float amax = elem_absmax_final<F16>(mag);
         const int eq = amax > 0.f ? static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 12 : 0;
         const float f = copysignf(pow2f(min(max(-eq, -126), 127)), a.scale_log2);  // scores times a factor >= 0
         row.fac = fabsf(a.scale_log2) * pow2f(min(max(eq, -126), 127));
         uint8_t* dst = smem + half * S::kHalfBytes + r_half * 128;
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < D / 8; ++i) {
-          const uint4 v = row.live ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
-          const float2 x = elem2_to_f32x2<F16>(v.x), y = elem2_to_f32x2<F16>(v.y), z = elem2_to_f32x2<F16>(v.z), w = elem2_to_f32x2<F16>(v.w);
+          const float2 x = elem2_to_f32x2<F16>(v[i].x), y = elem2_to_f32x2<F16>(v[i].y), z = elem2_to_f32x2<F16>(v[i].z), w = elem2_to_f32x2<F16>(v[i].w);
           *reinterpret_cast<uint4*>(dst + (i >> 3) * 16384 + (((i & 7) ^ (r_half & 7)) << 4)) =
               make_uint4(f32x2_to_elem2<true>(x.x * f, x.y * f), f32x2_to_elem2<true>(y.x * f, y.y * f),
                          f32x2_to_elem2<true>(z.x * f, z.y * f), f32x2_to_elem2<true>(w.x * f, w.y * f));
@@ -401,7 +399,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
       const int last_row = min(rows, g.rt * kKpRows + 128 * (half + 1)) - 1, first_row = g.rt * kKpRows + 128 * half;
       const int tile0 = g.tile0, tile1 = g.tile1, lo = g.lo, hi = g.hi;
       // positions of the half's first and last row
-      const int pos_first = pos0 + first_row / a.group, pos_last = pos0 + last_row / a.group;
+      const int pos_first = pos0 + kv_token(a, first_row), pos_last = pos0 + kv_token(a, last_row);
       for (int t = tile0; t < tile1 && ok; ++t, ++unit) {
         if (!busy) continue;
         const KpSlot& slot = slots[unit % kKpSlots];
