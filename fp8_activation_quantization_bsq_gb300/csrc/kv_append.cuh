@@ -63,8 +63,9 @@ __global__ void __launch_bounds__(kKvAppendThreads) kv_append_kernel(const KvApp
   const int kv = blockIdx.y & 1, head = blockIdx.y >> 1;
   const int64_t t0 = a.offsets[b], n = a.offsets[b + 1] - t0, len = a.lens[b], start = len - n;
   if (n <= 0) return;
-  const int64_t pg = start / a.page + (slot - kv_first_slot(a, b));
-  if (t0 < 0 || t0 + n > a.total || start < 0 || len > static_cast<int64_t>(a.table_width) * a.page) {
+  const int64_t nth = slot - kv_first_slot(a, b);  // page of the new tokens; negative only under falling offsets
+  const int64_t pg = start / a.page + nth;
+  if (nth < 0 || t0 < 0 || t0 + n > a.total || start < 0 || len > static_cast<int64_t>(a.table_width) * a.page) {
     if (tid == 0) record_error_at(a.err, kErrValue);
     return;
   }

@@ -12,6 +12,9 @@ namespace {
 
 using namespace bsq;
 
+// Positions, and rows of a kv head, that leave 32-bit sums of two of them, a window and a tile's end in range.
+constexpr int64_t kKvMaxLen = int64_t(1) << 30;
+
 // What the cache calls check alike; BSQ_OK when the call may go on.
 bsq_status check_cache(int32_t dtype, int64_t total, int32_t kv_heads, int32_t dim, int64_t tok_stride, int64_t head_stride,
                        const void* k_cache, const void* v_cache, const void* k_scales, const void* v_scales,
@@ -21,7 +24,7 @@ bsq_status check_cache(int32_t dtype, int64_t total, int32_t kv_heads, int32_t d
   if (dtype != BSQ_BF16 && dtype != BSQ_F16) return BSQ_ERR_VALUE;
   if (total < 0 || total >= (int64_t(1) << 31) || batch < 0 || kv_heads < 1 || kv_heads > 1024 || (dim != 64 && dim != 128) ||
       num_pages < 1 || num_pages >= (int64_t(1) << 31) || (page != 16 && page != 32 && page != 64 && page != 128) ||
-      table_width < 0 || (batch > 1 && table_ld < table_width) || cs_tok < dim || cs_page < 0 || cs_head < 0 ||
+      table_width < 0 || static_cast<int64_t>(table_width) * page > kKvMaxLen || (batch > 1 && table_ld < table_width) || cs_tok < dim || cs_page < 0 || cs_head < 0 ||
       cs_tok >= (int64_t(1) << 32) || cs_head >= (int64_t(1) << 38) || cs_page >= (int64_t(1) << 38))
     return BSQ_ERR_SHAPE;
   if (total == 0 || batch == 0) return BSQ_OK;
@@ -160,7 +163,7 @@ int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t he
                                  page, cs_page, cs_head, cs_tok, table, table_ld, table_width, offsets, lens, batch);
       s != BSQ_OK)
     return s;
-  if (heads < 1 || heads % kv_heads != 0 || heads / kv_heads > 64 || total * (heads / kv_heads) >= (int64_t(1) << 31) || window < 0 ||
+  if (heads < 1 || heads % kv_heads != 0 || heads / kv_heads > 64 || total * (heads / kv_heads) > kKvMaxLen || window < 0 ||
       max_q < 0)
     return BSQ_ERR_SHAPE;
   if (!std::isfinite(sm_scale)) return BSQ_ERR_VALUE;
@@ -194,7 +197,7 @@ int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t he
   a.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
   a.table_width = table_width;
   a.causal = causal;
-  a.window = window;
+  a.window = window < kKvMaxLen ? window : 0;  // no two positions are that far apart
   a.scale_log2 = sm_scale * 1.4426950408889634f;
   a.ready = static_cast<uint32_t*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKvCounterBytes);

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
   __shared__ volatile uint32_t more[2];
   __shared__ int64_t warp_sum[kKpThreads / 32];
   __shared__ uint32_t tmem_slot;
-  __shared__ volatile uint32_t abort_flag, fills, used_tiles, go_on, joined;
+  __shared__ volatile uint32_t abort_flag, fills, used_tiles, joined;
 
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   if (tid == 0) {

@@ -673,10 +673,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
               for (int j = 0; j < 8; ++j) {
                 if (c + j >= n) break;
                 const int pair = tb.pair_of[row0 + c + j];
-                const float f = tb.prob[pair] * by;
+                const float p = tb.prob[pair], f = p * by;  // p = 0: excluded, whatever its product is
                 float* dst = a.yp + static_cast<int64_t>(pair) * a.hidden + col;
-                if (col < a.hidden) __stcg(dst, x[j] * f);
-                if (col + 128 < a.hidden) __stcg(dst + 128, z[j] * f);
+                if (col < a.hidden) __stcg(dst, p == 0.f ? 0.f : x[j] * f);
+                if (col + 128 < a.hidden) __stcg(dst + 128, p == 0.f ? 0.f : z[j] * f);
               }
             }
           }

@@ -2,7 +2,8 @@
 (``bsq_kv_append``, ``bsq_kv_attention``) and the few-token expert layer
 (``bsq_moe_layer``).  As in the package's other calls, work is enqueued on the
 current stream (or ``stream``), outputs are allocated with torch when not
-passed in, and a refused argument raises ValueError or BsqError."""
+passed in (under the given stream, so that their memory is free in its order),
+and a refused argument raises ValueError or BsqError."""
 from __future__ import annotations
 
 import math
@@ -30,6 +31,14 @@ def _call(name, index, stream, args):
             rc = fn(*args, raw)
     if rc != 0:
         _check(rc, name)
+
+
+def _new(stream, make, shape, dtype, device):
+    """make(shape) on the stream that the call runs on."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
 
 
 def _rows(x, what):
@@ -113,16 +122,16 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     total, heads, dim = shape
     kv_heads, cache = _cache(dim, index, k_cache, v_cache, k_scales, v_scales, block_table, offsets, seq_lens)
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _new(stream, torch.empty, shape, q.dtype, q.device)
     elif out.dtype != q.dtype or out.shape != shape or not out.is_contiguous() or out.get_device() != index:
         raise ValueError("out must be a contiguous tensor of q's shape, type and device")
     if lse is None:
         if return_lse:
-            lse = torch.empty((total, heads), dtype=_F32, device=q.device)
+            lse = _new(stream, torch.empty, (total, heads), _F32, q.device)
     elif lse.dtype is not _F32 or lse.shape != (total, heads) or not lse.is_contiguous() or lse.get_device() != index:
         raise ValueError("lse must be a contiguous float32 (tokens, heads) tensor on q's device")
     if workspace is None:
-        workspace = torch.zeros(kv_attention_workspace_bytes(total, heads, kv_heads, dim, cache[-1], max_q), dtype=_U8, device=q.device)
+        workspace = _new(stream, torch.zeros, kv_attention_workspace_bytes(total, heads, kv_heads, dim, cache[-1], max_q), _U8, q.device)
     elif workspace.dtype is not _U8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
     _call("bsq_kv_attention", index, stream,
@@ -186,11 +195,11 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w13_scal
     else:
         sfs = (None, None, None, None)
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        out = _new(stream, torch.empty, shape, _BF16, x.device)
     elif out.dtype is not _BF16 or out.shape != shape or out.stride(1) != 1 or out.get_device() != index:
         raise ValueError("out must be a (tokens, hidden) bfloat16 tensor with unit inner stride on x's device")
     if workspace is None:
-        workspace = torch.zeros(moe_layer_workspace_bytes(f, tokens, hidden, inter, experts, top_k), dtype=_U8, device=x.device)
+        workspace = _new(stream, torch.zeros, moe_layer_workspace_bytes(f, tokens, hidden, inter, experts, top_k), _U8, x.device)
     elif workspace.dtype is not _U8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on x's device")
     _call("bsq_moe_layer", index, stream,

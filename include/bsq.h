@@ -423,6 +423,8 @@ typedef enum { BSQ_BF16 = 0, BSQ_F16 = 1 } bsq_dtype;
  * h, token t of the page and dimension d lies at
  * p*page_stride + h*head_stride + t*token_stride + d (bytes); scales are
  * (num_pages, kv_heads), contiguous.  Keys and values have equal strides.
+ * Scale bytes are 1 to 254; a sequence's own tokens hold no NaN codes (0x7F,
+ * 0xFF: bsq_kv_append writes none for finite inputs).
  * Sequence b's token i lies in page block_table[b*table_stride + i/page].
  *
  * Arguments common to the cache calls:
@@ -431,7 +433,7 @@ typedef enum { BSQ_BF16 = 0, BSQ_F16 = 1 } bsq_dtype;
  *   k_cache_dev, v_cache_dev   codes, 16-byte aligned; page_stride,
  *                     head_stride and token_stride are multiples of 16,
  *                     token_stride >= dim.
- *   block_table_dev   int32, `batch` rows of table_width entries.
+ *   block_table_dev   int32, `batch` rows of table_width entries, table_width * page <= 2^30.
  *   offsets_dev       int32[batch + 1], non-decreasing from 0: sequence b owns the
  *                     rows [offsets[b], offsets[b+1]) of the 16-bit tensors.
  *   seq_lens_dev      int32[batch]: cached tokens of the sequence, the rows
@@ -477,7 +479,9 @@ BSQ_API int32_t bsq_kv_append(int32_t dtype, const void* k_dev, const void* v_de
  *                     of exp(score) over the allowed keys.
  *   workspace_dev     bsq_kv_attention_workspace_bytes() bytes, 16-byte
  *                     aligned, zeroed by the caller once before its first use; every call
- *                     leaves its counters zeroed again.  Calls sharing it must not overlap.
+ *                     leaves its counters zeroed again (after a reported BSQ_ERR_TIMEOUT
+ *                     it has to be zeroed anew).  Calls sharing it must not overlap.
+ *   total             total * heads / kv_heads <= 2^30.
  * A row without an allowed key gets zeros and -inf.  What the cache holds
  * beyond a sequence's length, or outside the allowed keys, does not matter.
  * Rows of q that belong to no sequence are left as they are.  A softmax
@@ -517,7 +521,7 @@ BSQ_API int32_t bsq_kv_attention(int32_t dtype, const void* q_dev, int64_t total
  * bsq_quantize under the given tensor scale:
  *   g, u = Q(x, x_sf[e]) . w13[e];  h = bf16(g / (1 + exp(-g)) * u);
  *   y = bf16(sum over the choices of p * (Q(h, h_sf[e]) . w2[e])).
- * Logits of -inf exclude an expert (its weight is 0); a row of nothing else
+ * Logits of -inf exclude an expert (a choice of weight 0 adds nothing); a row of nothing else
  * gives zeros.  NaN logits count as -inf and record BSQ_ERR_VALUE.
  *   workspace_dev     bsq_moe_layer_workspace_bytes() bytes, 256-byte aligned,
  *                     zeroed by the caller once before its first use; every call leaves

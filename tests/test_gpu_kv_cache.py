@@ -284,6 +284,52 @@ def test_bad_metadata_is_reported_and_skipped(bsq):
     assert not out[0].any() and torch.equal(out[1:], before[1:])
 
 
+def test_falling_offsets_reach_nothing_else(bsq):
+    case = Case([200] * 3, [100] * 3, 1, 64, 16, seed=13)
+    k, _ = case.rows(1)
+    q, _ = case.rows(2)
+    for offsets in ([0, 200, 100, 300], [0, 300, 300, 100], [200, 0, 100, 300], [-20, 0, 100, 200], [0, 100, 200, 1 << 30],
+                    [160, 176, 0, 300]):
+        args = list(case.device())
+        args[5] = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        used = set(case.table.ravel().tolist())
+        others = [i for i in range(case.pages) if i not in used]
+        kept = args[0].clone()
+        bsq.kv_append(k, k, *args)
+        assert torch.equal(args[0][others], kept[others])  # nothing outside the sequences' pages
+        bsq.device_error()
+        out = bsq.kv_attention(q, *case.device()[:5], args[5], args[6], 100)
+        assert out.shape == q.shape
+        bsq.device_error()
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_widest_window_is_none(bsq, new):
+    case = Case([300, 20], [new, min(new, 20)], 1, 64, 16, seed=14)
+    q, _ = case.rows(2)
+    args = case.device()
+    for causal in (True, False):
+        expect = bsq.kv_attention(q, *args, new, causal=causal)
+        for window in (1 << 20, (1 << 30) - 1, 1 << 30, (1 << 31) - 1):
+            assert torch.equal(bsq.kv_attention(q, *args, new, causal=causal, window=window), expect)
+
+
+def test_own_workspace_on_another_stream(bsq):
+    """What the call allocates belongs to the stream it runs on: the current one is busy, and its free memory is not zero."""
+    case = Case([3000], [1], 1, 128, 64, seed=15)
+    q, _ = case.rows(8)
+    args = case.device()
+    expect = bsq.kv_attention(q, *args, 1)
+    stale = torch.full((bsq.kv_attention_workspace_bytes(1, 8, 1, 128, 1, 1),), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del stale
+    stream = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)
+    got, lse = bsq.kv_attention(q, *args, 1, return_lse=True, stream=stream)
+    stream.synchronize()
+    assert torch.equal(got.cpu(), expect.cpu()) and bsq.device_error() == 0
+
+
 def test_no_rows_is_a_no_op(bsq):
     case = Case([5], [1], 1, 64, 16, seed=12)
     args = case.device()

@@ -109,6 +109,20 @@ def test_ties_and_excluded_experts(bsq):
         assert not y[3].any()
 
 
+def test_weights_of_an_excluded_expert_do_not_matter(bsq):
+    layer = Layer(bsq, "mxfp8", 64, 128, 4, seed=8)
+    x, _, z = layer.inputs(2, 4)
+    z[:] = -np.inf
+    z[0, :2] = [0.5, 1.0]
+    z[1, 1] = 0.0
+    zl = torch.from_numpy(z).cuda()
+    expect = bsq.moe_layer(x, zl, *layer.args, "mxfp8", 4)
+    bad = [t.clone() for t in layer.args]
+    for t in bad:
+        t[2:] = 0x7F                                 # NaN codes (weights), 2^0 (scales)
+    assert torch.isfinite(expect).all() and torch.equal(bsq.moe_layer(x, zl, *bad, "mxfp8", 4), expect)
+
+
 def test_nan_logits_are_reported(bsq):
     layer = Layer(bsq, "mxfp4", 64, 128, 8, seed=4)
     x, _, z = layer.inputs(3, 5)

@@ -22,7 +22,7 @@ ATTN = dict(dtype=0, q=P, total=4, heads=4, kv_heads=2, dim=64, q_tok=256, q_hea
             causal=1, window=0, out=P, lse=None, ws=P, ws_bytes=1 << 40, stream=None)
 CACHE_BAD = [(dict(dtype=2), VALUE), (dict(dtype=-1), VALUE), (dict(total=-1), SHAPE), (dict(batch=-1), SHAPE), (dict(kv_heads=0), SHAPE),
              (dict(dim=96), SHAPE), (dict(dim=256), SHAPE), (dict(page=8), SHAPE), (dict(page=256), SHAPE), (dict(pages=0), SHAPE),
-             (dict(width=-1), SHAPE), (dict(table_ld=3), SHAPE), (dict(cs_tok=48), SHAPE), (dict(cs_page=-16), SHAPE),
+             (dict(width=-1), SHAPE), (dict(width=(1 << 26) + 1, table_ld=1 << 27), SHAPE), (dict(table_ld=3), SHAPE), (dict(cs_tok=48), SHAPE), (dict(cs_page=-16), SHAPE),
              (dict(kc=None), NULL), (dict(vs=None), NULL), (dict(table=None), NULL), (dict(offsets=None), NULL), (dict(lens=None), NULL),
              (dict(kc=P + 8), ALIGN), (dict(cs_page=2056), ALIGN), (dict(cs_head=1032), ALIGN), (dict(cs_tok=72), ALIGN),
              (dict(table=P + 2), ALIGN), (dict(total=0), OK), (dict(batch=0), OK)]
@@ -38,7 +38,7 @@ def test_append_refusals(bsq, change, code):
     (dict(heads=3), SHAPE), (dict(heads=0), SHAPE), (dict(heads=130, kv_heads=2), SHAPE), (dict(window=-1), SHAPE), (dict(max_q=0), SHAPE),
     (dict(sm_scale=float("inf")), VALUE), (dict(sm_scale=float("nan")), VALUE), (dict(q=None), NULL), (dict(out=None), NULL),
     (dict(ws=None), NULL), (dict(ws_bytes=64), SHAPE), (dict(out=P + 4), ALIGN), (dict(lse=P + 2), ALIGN), (dict(q_tok=252), ALIGN),
-    (dict(ws=P + 8), ALIGN)])
+    (dict(ws=P + 8), ALIGN), (dict(total=(1 << 29) + 1), SHAPE)])
 def test_attention_refusals(bsq, change, code):
     assert bsq.lib().bsq_kv_attention(*{**ATTN, **change}.values()) == code
 
