@@ -10,7 +10,11 @@
 // One block of 128 threads per (page that new tokens reach, kv head, key or
 // value): the page's new rows are read once, stay in registers over the
 // maximum and are written as codes.  Bound by DRAM for prompts (2 bytes read
-// and 1 written per element), by latency for single tokens.
+// and 1 written per element), by latency for single tokens.  A block holds a whole page's
+// rows, so that no maximum crosses blocks and nothing is read twice; ITERS follows from the page's size.
+// Measured (8 kv heads of 128, pages of 64): six prompts of up to 4500 tokens 24 us,
+// 5.4 TB/s or 80 % of a plain copy; a token for each of 64 sequences 5.9 us, most of it the
+// chain offsets, table, row, maximum, earlier codes.
 #pragma once
 
 #include "serving_common.cuh"

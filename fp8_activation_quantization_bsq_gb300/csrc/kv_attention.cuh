@@ -9,7 +9,8 @@
 //   out = sum_j 2^(t_j - m) c_j / sum_j 2^(t_j - m) 2^-ev_j,
 // so the weights of the codes stay within FP16 whatever the pages' scales are, and
 // nothing is multiplied into the values.  The key scale is one factor of a tile's
-// scores.  E4M3 codes and scaled query rows (a power of two per row) are exact in FP16;
+// scores.  E4M3 codes and scaled query rows (a power of two per row) are exact in FP16
+// (elements below 2^-28 of a row's largest: to 2^-37 of that);
 // weights are rounded to FP16 (a relative 2^-11 each, against 2^-9 of a BF16
 // output), and all sums are FP32.
 //
@@ -25,6 +26,10 @@
 // padding either.  Fragments come straight from the codes with wide shared loads: the order of the
 // dimension in q.k and of the output rows is free, so a thread takes 16 consecutive bytes of a
 // key, and pairs of keys are interleaved bytewise before conversion.
+// Measured (64 contexts of 1000 to 8192 tokens, 64 heads of 128 over 8, a graph of calls): 8 rows
+// per kv head 100 us, 6.1 TB/s or 90 % of a plain copy; 16 rows 125 us and 32 rows 237 us, where
+// the conversions and mma.sync products bound it.  One context of 777: 10.3 us, a chain of
+// latencies (lengths, table, codes, the join); two of 131072, 4 kv heads: 53 us.
 // An item cut by the runs is finished by the block that began it, which adds the other blocks' parts
 // in block order (first in groups where there are many): those blocks hold them at the start of
 // their runs, it at the end of its own.
@@ -40,7 +45,9 @@ constexpr int kKvTile = 64;       // keys per unit
 constexpr int kKvMaxBlocks = 1024;
 constexpr int kKvMinRun = 3;      // units of a run, at least, once every SM has one
 // Parts of an item that one block joins by itself, and the size of the groups
-// that are joined first where there are more: about their number's square root.
+// that are joined first where there are more: about their number's square root.  (104 parts, one
+// context of 20000 with one kv head: 16.3 us, 25.6 when one block joins them all; 57 parts of
+// contexts of 131072: 53.3 / 53.9, and 53.2 to 54.7 for groups of 5 to 20.)
 __device__ __forceinline__ int kv_join_group(int parts) { return parts <= 20 ? parts : parts <= 72 ? 8 : 16; }
 constexpr int kKvCounterBytes = 4 * kKvMaxBlocks;
 
@@ -270,8 +277,9 @@ __device__ __forceinline__ bool kv_start(const KvAttnArgs& a, int blocks_per_sm,
     s.total += warp_sum[w];
   }
   // Joining a part costs about as much as a few units: at most one run per SM
-  // until they have kKvMinRun units (contexts of 777 / 3000 tokens, 8 kv heads: 10.1 / 13.1 us,
-  // 10.1 / 16.8 with a run for every unit, 12.4 / 13.8 with at least four)
+  // until they have kKvMinRun units (contexts of 777 / 3000 tokens with 8 kv heads and 20000 with one:
+  // 10.3 / 12.5 / 16.3 us, and 10.3 / 16.5 / 18.1 with a run for every unit; with at least four
+  // 12.4 / 13.8 where three took 10.1 / 13.1)
   s.parts = static_cast<int>(min(static_cast<int64_t>(gridDim.x),
                                  max(s.total / kKvMinRun, min(s.total, static_cast<int64_t>(gridDim.x / blocks_per_sm)))));
   if (static_cast<int>(blockIdx.x) >= s.parts) return false;
@@ -291,20 +299,21 @@ struct KvPageScale {
   float kfac, ev, inv;
 };
 
-// NT: tiles of 8 query rows.
 // From the scale bytes; -1: no such page.
 __device__ __forceinline__ KvPageScale kv_page_scale(int ek, int ev) {
   if (ek < 0) return {0.f, -INFINITY, 0.f};
   return {pow2f(min(max(ek - 127, -126), 127)), static_cast<float>(ev - 127), pow2f(min(max(127 - ev, -126), 127))};
 }
 
+// NT: tiles of 8 query rows.
 template <int D, int NT>
 struct KvShape {
   static constexpr int kWarps = 4;                         // consumers
   static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kRows = 8 * NT;
   static constexpr int kPassRows = NT == 1 ? 8 : 16;       // rows merged at a time
-  // registers allow 15 warps per SM at 128, 10 at 168, 5 at 255 (five warps spread unevenly over four schedulers)
+  // registers allow 15 warps per SM at 128, 10 at 168, 5 at 255 (five warps spread unevenly over four
+  // schedulers); 64 contexts to 8192 with 8 rows: 101 us with three blocks, 106 to 108 with two of longer rings
   static constexpr int kBlocksPerSm = NT == 1 ? 3 : NT == 2 ? 2 : 1;
   static constexpr int kTileBytes = kKvTile * D;           // of keys, and of values
   static constexpr int kStages = NT == 1 ? 3 : NT == 2 ? 4 : 6;

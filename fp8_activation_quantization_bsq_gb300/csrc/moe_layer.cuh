@@ -29,6 +29,10 @@
 //    warps 4-7 drain finished accumulators: silu, the quantization of h along a
 //    warp's 32 rows, or the weighted rows of y.
 //  * After a last grid-wide wait every block sums its share of y over the choices, in their order.
+// Measured (graphs of calls; hidden 7168, inter 2048, NVFP4, top 8 of 256 experts): 64 tokens that reach 156 experts
+// 649 us, 6.0 TB/s or 88 % of a plain copy; one token 51 us (3.9 TB/s: 27 us stream the first product's weights
+// and x, the rest is the wait for h, the second product's ramp, the last wait and y).  16 tokens, hidden 4096, MXFP8,
+// 34 of 64 experts: 152 us, 5.8 TB/s.  7 tokens, 17 experts of 3 MB each: 30 us, most of it those waits.
 // All waits are bounded (about a second): an expired one records
 // BSQ_ERR_TIMEOUT, stops the block's roles, waits for the copies and products in
 // flight, frees the tensor memory and returns.
@@ -377,6 +381,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   int quant_at = block + blocks * (tid - 128);
   uint4 xv[4];
   if (warp >= 4) moe_load_x(a, quant_at, quant_total, per_row, xv);
+  // as many logits a lane as the experts need, in two sizes (256 experts: 649 / 668 us for 64 tokens and 51 / 52
+  // for one with the smaller / larger form)
   if (a.experts <= 256) {
     for (int t = warp; t < a.tokens; t += kMoeThreads / 32) moe_route<8>(a, tb, t, lane);
   } else {
