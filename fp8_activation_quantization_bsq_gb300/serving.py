@@ -33,20 +33,12 @@ def _call(name, index, stream, args):
         _check(rc, name)
 
 
-def _like(stream, x):
-    """An uninitialized contiguous tensor like x, on the stream that the call runs on."""
+def _new(stream, make, shape, dtype, device):
+    """make(shape) on the stream that the call runs on."""
     if stream is None:
-        return torch.empty_like(x, memory_format=torch.contiguous_format)
+        return make(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty_like(x, memory_format=torch.contiguous_format)
-
-
-def _zeros(stream, nbytes, device):
-    """A workspace, on the stream that the call runs on."""
-    if stream is None:
-        return torch.zeros(nbytes, dtype=_U8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.zeros(nbytes, dtype=_U8, device=device)
+        return make(shape, dtype=dtype, device=device)
 
 
 def _rows(x, what):
@@ -130,20 +122,16 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     total, heads, dim = shape
     kv_heads, cache = _cache(dim, index, k_cache, v_cache, k_scales, v_scales, block_table, offsets, seq_lens)
     if out is None:
-        out = _like(stream, q)
+        out = _new(stream, torch.empty, shape, q.dtype, q.device)
     elif out.dtype != q.dtype or out.shape != shape or not out.is_contiguous() or out.get_device() != index:
         raise ValueError("out must be a contiguous tensor of q's shape, type and device")
     if lse is None:
         if return_lse:
-            if stream is None:
-                lse = q.new_empty((total, heads), dtype=_F32)
-            else:
-                with torch.cuda.stream(stream):
-                    lse = q.new_empty((total, heads), dtype=_F32)
+            lse = _new(stream, torch.empty, (total, heads), _F32, q.device)
     elif lse.dtype is not _F32 or lse.shape != (total, heads) or not lse.is_contiguous() or lse.get_device() != index:
         raise ValueError("lse must be a contiguous float32 (tokens, heads) tensor on q's device")
     if workspace is None:
-        workspace = _zeros(stream, kv_attention_workspace_bytes(total, heads, kv_heads, dim, cache[-1], max_q), q.device)
+        workspace = _new(stream, torch.zeros, kv_attention_workspace_bytes(total, heads, kv_heads, dim, cache[-1], max_q), _U8, q.device)
     elif workspace.dtype is not _U8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
     _call("bsq_kv_attention", index, stream,
@@ -207,11 +195,11 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w13_scal
     else:
         sfs = (None, None, None, None)
     if out is None:
-        out = _like(stream, x)
+        out = _new(stream, torch.empty, shape, _BF16, x.device)
     elif out.dtype is not _BF16 or out.shape != shape or out.stride(1) != 1 or out.get_device() != index:
         raise ValueError("out must be a (tokens, hidden) bfloat16 tensor with unit inner stride on x's device")
     if workspace is None:
-        workspace = _zeros(stream, moe_layer_workspace_bytes(f, tokens, hidden, inter, experts, top_k), x.device)
+        workspace = _new(stream, torch.zeros, moe_layer_workspace_bytes(f, tokens, hidden, inter, experts, top_k), _U8, x.device)
     elif workspace.dtype is not _U8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on x's device")
     _call("bsq_moe_layer", index, stream,
