@@ -27,7 +27,7 @@
 // dimension in q.k and of the output rows is free, so a thread takes 16 consecutive bytes of a
 // key, and pairs of keys are interleaved bytewise before conversion.
 // Measured (64 contexts of 1000 to 8192 tokens, 64 heads of 128 over 8, a graph of calls): 8 rows
-// per kv head 100 us, 6.1 TB/s or 90 % of a plain copy; 16 rows 125 us and 32 rows 237 us, where
+// per kv head 100 us, 6.1 TB/s or 90 % of a plain copy; 16 rows 116 us and 32 rows 237 us, where
 // the conversions and mma.sync products bound it.  One context of 777: 10.3 us, a chain of
 // latencies (lengths, table, codes, the join); two of 131072, 4 kv heads: 53 us.
 // An item cut by the runs is finished by the block that began it, which adds the other blocks' parts
@@ -321,8 +321,11 @@ struct KvShape {
   // 16, so that the rows and eighths of a warp's float4 stores fall into different banks
   static constexpr int kEighth = D / 8 + 4, kRow = 8 * kEighth + 4;
   static constexpr int kMergeBytes = kWarps * kPassRows * kRow * 4;
-  static constexpr int kQueryBytes = NT == 4 ? kRows * D * 2 : 0;
-  static constexpr int kSmem = 1024 + kStages * 2 * kTileBytes + kMergeBytes + kQueryBytes;
+  // query rows in shared memory, in the merge buffer that an item uses after them, where registers are short: with
+  // 16 rows of 128 (64 contexts to 8192 / 16 to 800) 116 / 14.8 us against 125 / 15.1 in registers, with 16 of 64
+  // (guessed tokens) 26.7 against 24.6.  Three blocks per SM for 16 rows: 111, but 17.3 for the short contexts
+  static constexpr bool kSharedQuery = NT == 4 || (NT == 2 && D == 128);
+  static constexpr int kSmem = 1024 + kStages * 2 * kTileBytes + kMergeBytes;
   static constexpr int kPartFloats = kRows * D + 2 * kRows;
 };
 
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   float* merge = reinterpret_cast<float*>(smem + S::kStages * 2 * S::kTileBytes);
-  [[maybe_unused]] uint4* query = reinterpret_cast<uint4*>(smem + S::kStages * 2 * S::kTileBytes + S::kMergeBytes);
+  [[maybe_unused]] uint4* query = reinterpret_cast<uint4*>(merge);
   __shared__ uint64_t full_bar[S::kStages], empty_bar[S::kStages];
   __shared__ KvPageScale page_scale[S::kStages][4];
   __shared__ float warp_m2[2][S::kWarps][RT], warp_l2[2][S::kWarps][RT];  // by parity of the item
@@ -465,12 +468,12 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
       // positions of the tile's first and last row
       const int pos_first = pos0 + kv_token(a, g.rt * RT), pos_last = pos0 + kv_token(a, min(rows, (g.rt + 1) * RT) - 1);
       // Query rows 8 t + gq, dimensions D/4 c .. + D/4 - 1: the second operand
-      // of K Q^T.  For NT = 4 they stay in shared memory, which all warps read.
-      uint32_t q[NT == 4 ? 1 : NT][D / 8];
+      // of K Q^T.  In shared memory all warps read one copy.
+      uint32_t q[S::kSharedQuery ? 1 : NT][D / 8];
       int pos[NT][2];       // positions of rows 8 t + 2 c, + 1: those of this thread's scores
       float rowfac[NT][2];  // sm_scale log2(e) 2^eq
       float m[NT][2], l[NT][2];
-      if (NT == 4) named_sync(1, kT);  // the last item's rows have been read
+      if (S::kSharedQuery) named_sync(1, kT);  // the last item's sums have been read
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int r = g.rt * RT + 8 * t + gq, tok = kv_token(a, r);
@@ -497,9 +500,9 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
           for (int j = 0; j < 4; ++j) {
             const float2 y = elem2_to_f32x2<F16>(w[j]);
             x[j] = f32x2_to_elem2<true>(y.x * f, y.y * f);
-            if constexpr (NT != 4) q[t][4 * i + j] = x[j];
+            if constexpr (!S::kSharedQuery) q[t][4 * i + j] = x[j];
           }
-          if constexpr (NT == 4)  // every warp stores the same values' quarter
+          if constexpr (S::kSharedQuery)  // every warp stores the same values' quarter
             if (warp == t) query[(t * (D / 32) + i) * 32 + lane] = make_uint4(x[0], x[1], x[2], x[3]);
         }
 #pragma unroll
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
           l[t][h] = 0.f;
         }
       }
-      if (NT == 4) named_sync(1, kT);
+      if (S::kSharedQuery) named_sync(1, kT);
       // O^T: dimensions D/8 gq + 2 i (elements 0, 1) and + 1 (2, 3), rows 8 t + 2 c (0, 2) and + 1 (1, 3)
       float o[NT][D / 16][4];
 #pragma unroll
@@ -535,8 +538,8 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
           const uint4 u = *reinterpret_cast<const uint4*>(kd + kv_chunk<D>(16 * warp + gq, kQuads * c + j));
           const uint4 w = *reinterpret_cast<const uint4*>(kd + kv_chunk<D>(16 * warp + 8 + gq, kQuads * c + j));
           const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {w.x, w.y, w.z, w.w};
-          uint4 qv[NT == 4 ? NT : 1][2];
-          if constexpr (NT == 4) {
+          uint4 qv[S::kSharedQuery ? NT : 1][2];
+          if constexpr (S::kSharedQuery) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               uint32_t b0, b1;
-              if constexpr (NT == 4) {
+              if constexpr (S::kSharedQuery) {
                 const uint4 z = qv[t][i >> 1];
                 b0 = i & 1 ? z.z : z.x;
                 b1 = i & 1 ? z.w : z.y;

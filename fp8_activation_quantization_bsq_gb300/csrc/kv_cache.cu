@@ -85,7 +85,7 @@ template <int D, bool F16>
 bsq_status launch_attention_rows(const KvAttnArgs& a, int64_t max_rows, const CUtensorMap& mk, const CUtensorMap& mv,
                                  const HostDevice& d, cudaStream_t st) {
   // the narrowest tile that holds all rows (those 64 contexts: 8 rows 100 / 119 / 225 us in tiles of 8 / 16 / 32,
-  // 16 rows 125 / 228 in tiles of 16 / 32): unused rows are products, registers and warps per SM lost
+  // 16 rows 116 / 228 in tiles of 16 / 32): unused rows are products, registers and warps per SM lost
   if (max_rows <= 8) return launch_attention<D, 1, F16>(a, mk, mv, d, st);
   if (max_rows <= 16) return launch_attention<D, 2, F16>(a, mk, mv, d, st);
   if (max_rows <= kKvFewRows) return launch_attention<D, 4, F16>(a, mk, mv, d, st);
