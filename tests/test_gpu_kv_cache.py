@@ -202,6 +202,14 @@ def test_attention_many_sequences(bsq, group, new):
     check_attention(bsq, Case(lens, [min(new, n) for n in lens], 1, 64, 16, seed=2), group)
 
 
+@pytest.mark.parametrize("group,new", [(4, 4), (3, 5), (8, 4), (5, 5)])
+def test_attention_many_items_share_query_memory(bsq, group, new):
+    """Rows in shared memory that the items of a block use one after the other."""
+    rng = np.random.default_rng(5)
+    lens = [int(n) for n in rng.integers(0, 300, 500)]
+    check_attention(bsq, Case(lens, [min(new, n) for n in lens], 2, 128, 16, seed=6), 2 * group)
+
+
 @pytest.mark.parametrize("group,new", [(4, 1), (8, 3), (4, 33)])
 def test_attention_scales_and_sharpness(bsq, group, new):
     """Page scales far apart, and one key that takes all of the weight."""
