@@ -32,7 +32,10 @@
 // latencies (lengths, table, codes, the join); two of 131072, 4 kv heads: 53 us.
 // An item cut by the runs is finished by the block that began it, which adds the other blocks' parts
 // in block order (first in groups where there are many): those blocks hold them at the start of
-// their runs, it at the end of its own.
+// their runs, it at the end of its own.  A block waits only for blocks after it, and for the first
+// thing they do: of those on the GPU at most the last one, its group's first and its item's first
+// wait for one that is not there yet, and all others leave and make room.  So the launch needs
+// not be cooperative (the grid fits an idle GPU at once; other work on it only delays).
 #pragma once
 
 #include <type_traits>
