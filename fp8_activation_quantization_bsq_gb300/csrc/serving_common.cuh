@@ -69,7 +69,7 @@ __device__ __forceinline__ float elem_absmax_final(uint32_t acc) {
   return fmaxf(v.x, v.y);
 }
 
-// 2^e for -126 <= e <= 127.
-__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// 2^e for -127 <= e <= 127 (2^-127 is subnormal).
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(e > -127 ? static_cast<uint32_t>(e + 127) << 23 : 0x00400000u); }
 
 }  // namespace bsq
