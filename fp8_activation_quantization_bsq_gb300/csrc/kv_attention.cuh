@@ -66,7 +66,9 @@ struct KvAttnArgs {
   float* lse;                     // (total, heads) or NULL
   int64_t total, num_pages;
   int batch, heads, kv_heads, group, page, page_shift, table_width, causal, window;
-  float scale_log2;               // sm_scale * log2(e)
+  // sm_scale log2(e) as its power of two, with the sign, and its significand in [1, 2) (or 0): a row's power of two
+  // takes the one, a page's the other, so that neither product loses bits below FP32's normal numbers
+  float scale_pow, scale_sig;
   uint64_t group_inv;             // ceil(2^64 / group), for kv_token
   uint32_t* ready;                // [block] part stored, zero between calls
   float* part;                    // [block][rows * D + 2 * rows]: sums, maxima, weights' sums
@@ -297,15 +299,16 @@ __device__ __forceinline__ bool kv_start(const KvAttnArgs& a, int blocks_per_sm,
   return true;
 }
 
-// Per page of a stage: factor of the scores, exponent of the values, and its reciprocal power.
+// Per page of a stage: factor of the scores (with the significand of sm_scale log2(e)), exponent of the values, and its
+// reciprocal power.
 struct KvPageScale {
   float kfac, ev, inv;
 };
 
 // From the scale bytes; -1: no such page.
-__device__ __forceinline__ KvPageScale kv_page_scale(int ek, int ev) {
+__device__ __forceinline__ KvPageScale kv_page_scale(const KvAttnArgs& a, int ek, int ev) {
   if (ek < 0) return {0.f, -INFINITY, 0.f};
-  return {pow2f(min(max(ek - 127, -126), 127)), static_cast<float>(ev - 127), pow2f(min(max(127 - ev, -126), 127))};
+  return {a.scale_sig * pow2f(min(max(ek - 127, -126), 127)), static_cast<float>(ev - 127), pow2f(min(max(127 - ev, -126), 127))};
 }
 
 // NT: tiles of 8 query rows.
@@ -331,6 +334,13 @@ struct KvShape {
   static constexpr int kSmem = 1024 + kStages * 2 * kTileBytes + kMergeBytes;
   static constexpr int kPartFloats = kRows * D + 2 * kRows;
 };
+
+// A query row enters its products as 2^-eq of itself, with its largest magnitude in
+// [2^12, 2^13).  Rows below 2^-114 stay smaller: there 2^-eq would pass FP32, and their
+// elements, multiples of 2^-133 at least, are exact in FP16 at 2^126 as well.
+__device__ __forceinline__ int kv_query_exp(float amax) {
+  return amax > 0.f ? max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 12, -126) : 0;
+}
 
 // The codes of 4 consecutive dimensions of two keys -> for each dimension
 // the pair (key 0, key 1) in FP16.
@@ -446,7 +456,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
             tma_load_4d(kd + S::kTileBytes + i * box * D, &map_v, 0, y, g.head, id, &full_bar[stage]);
           }
         }
-        if (lane >= first && lane < first + boxes) page_scale[stage][lane - first] = kv_page_scale(ek, ev);
+        if (lane >= first && lane < first + boxes) page_scale[stage][lane - first] = kv_page_scale(a, ek, ev);
         __syncwarp();
         if (lane == 0) mbar_arrive(&full_bar[stage]);
         ++n;
@@ -474,7 +484,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
       // of K Q^T.  In shared memory all warps read one copy.
       uint32_t q[S::kSharedQuery ? 1 : NT][D / 8];
       int pos[NT][2];       // positions of rows 8 t + 2 c, + 1: those of this thread's scores
-      float rowfac[NT][2];  // sm_scale log2(e) 2^eq
+      float rowfac[NT][2];  // 2^eq and the power of two of sm_scale log2(e)
       float m[NT][2], l[NT][2];
       if (S::kSharedQuery) named_sync(1, kT);  // the last item's sums have been read
 #pragma unroll
@@ -492,9 +502,8 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
         }
         amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
-        // the row times 2^-eq has its largest magnitude in [2^12, 2^13)
-        const int eq = amax > 0.f ? static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 12 : 0;
-        const float f = pow2f(min(max(-eq, -126), 127)), rf = a.scale_log2 * pow2f(min(max(eq, -126), 127));
+        const int eq = kv_query_exp(amax);
+        const float f = pow2f(-eq), rf = a.scale_pow * pow2f(eq);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};

@@ -202,7 +202,10 @@ int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t he
   a.table_width = table_width;
   a.causal = causal;
   a.window = window < kKvMaxLen ? window : 0;  // no two positions are that far apart
-  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  int exponent;
+  const float significand = std::frexp(sm_scale * 1.4426950408889634f, &exponent);  // 0, or in [1/2, 1)
+  a.scale_sig = 2.f * std::fabs(significand);
+  a.scale_pow = std::copysign(std::ldexp(1.f, exponent - 1), sm_scale);
   a.ready = static_cast<uint32_t*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKvCounterBytes);
   a.err = d.error_word;

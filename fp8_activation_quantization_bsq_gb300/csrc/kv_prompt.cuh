@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
           const bool valid = pid >= 0 && pid < a.num_pages;
           if (pg < pages && !valid && (pg + 1) << a.page_shift > g.lo) record_error_at(a.err, kErrValue);
           const int64_t at = static_cast<int64_t>(pid) * a.kv_heads + g.head;
-          sc = kv_page_scale(valid ? a.scales[0][at] : -1, valid ? a.scales[1][at] : -1);
+          sc = kv_page_scale(a, valid ? a.scales[0][at] : -1, valid ? a.scales[1][at] : -1);
           if (!valid) pid = -1;
         }
         const int first = pg0 - batch0;
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
       const int64_t out_row = static_cast<int64_t>(g.s.t0 + tok) * a.heads + g.head * a.group + r - tok * a.group;
       KpRow row{-INFINITY, 0.f, 0.f, pos0 + tok, r < rows};
       if (busy) {
-        // the query row in FP16, 2^-eq of it, largest magnitude in [2^12, 2^13)
+        // the query row in FP16, 2^-eq of it
         const uint16_t* src = a.q + static_cast<int64_t>(g.s.t0 + tok) * a.q_tok + (g.head * a.group + r - tok * a.group) * a.q_head;
         uint4 v[D / 8];
         uint32_t mag = 0;
@@ -386,9 +386,9 @@ __global__ void __launch_bounds__(kKpThreads, 1)
         for (int i = 0; i < D / 8; ++i)
           mag = elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(elem_absmax2<F16>(mag, v[i].x), v[i].y), v[i].z), v[i].w);
         const float amax = elem_absmax_final<F16>(mag);
-        const int eq = amax > 0.f ? static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 12 : 0;
-        const float f = copysignf(pow2f(min(max(-eq, -126), 127)), a.scale_log2);  // scores times a factor >= 0
-        row.fac = fabsf(a.scale_log2) * pow2f(min(max(eq, -126), 127));
+        const int eq = kv_query_exp(amax);
+        const float f = copysignf(pow2f(-eq), a.scale_pow);  // scores times a factor >= 0
+        row.fac = fabsf(a.scale_pow) * pow2f(eq);
         uint8_t* dst = smem + half * S::kHalfBytes + r_half * 128;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {

@@ -1,13 +1,18 @@
 """kv_append and kv_attention at the ends of what include/bsq.h allows: scale
 bytes 1 to 254, query rows of any finite size, softmax weights far below a
 row's largest, NaN queries."""
+import numpy as np
 import pytest
 
-from test_gpu_kv_cache import Case, check_append
+import serving_reference as ref
+from test_gpu_kv_cache import HALF_ULP, SUBNORMAL, Case, check_append
 
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
+
+# query heads per kv head, rows: 4, 16, 32 and 160 rows of a kv head, each in a kernel of its own
+ROWS = [(4, 1), (8, 2), (8, 4), (4, 40)]
 
 
 @pytest.fixture(scope="module")
@@ -21,9 +26,40 @@ def bsq():
     assert m.device_error() == 0
 
 
+def close(case, got, got_lse, out, lse, mag, size, low, weight=2.0 ** -25):
+    """As test_gpu_kv_cache.compare, without a floor for the smallest outputs.
+    A score and the value scale's exponent meet in one FP32 number, and references of both are subtracted
+    from such numbers: four roundings of up to 2^-24 of the exponent each.  `weight`: error of the smallest weights, of the largest."""
+    ev = max(abs(int(b) - 127) for b in case.scales[1].ravel())
+    score = (case.dim + 4) * 2.0 ** -24 * size + 2.0 ** -22 * ev
+    tol = HALF_ULP[case.dtype] * np.abs(out) + (2.0 ** -11 + 2 * score + 2.0 ** -19)[..., None] * mag + weight * low + SUBNORMAL[case.dtype]
+    err = np.abs(got.double().cpu().numpy() - out)
+    assert np.isfinite(err).all()
+    assert (err <= tol).all(), f"{(err / tol).max():.3f} of the tolerance"
+    g = got_lse.double().cpu().numpy()
+    some = np.isfinite(lse)
+    np.testing.assert_array_equal(np.isneginf(g), ~some)
+    assert (np.abs(g[some] - lse[some]) <= 2 * score[some] + 2.0 ** -20 * (1 + np.abs(lse[some]))).all()
+
+
+def attend(bsq, case, heads, q_scale=1.0, **kw):
+    q, qn = case.rows(heads, q_scale)
+    got = bsq.kv_attention(q, *case.device(), int(np.max(np.diff(case.offsets))), return_lse=True)
+    close(case, *got, *ref.attention(qn, *case.cache, *case.scales, case.table, case.offsets, case.lens, case.dim ** -0.5, True, 0), **kw)
+
+
 def test_append_under_the_largest_scale(bsq):
     """New tokens in a page whose earlier tokens brought it to byte 254."""
     case = Case([20, 40, 7], [3, 1, 7], 2, 64, 32, seed=5)
     for s in case.scales:
         s[:] = 254
     check_append(bsq, case, 2.0 ** 126, 2.0 ** 125)
+
+
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("q_exp,key_byte", [(-113, 233), (-116, 236), (-122, 242), (-129, 249)])
+def test_smallest_query_rows(bsq, group, new, q_exp, key_byte):
+    """Rows below 2^-114, down to subnormal numbers, against keys large enough for scores of about 1."""
+    case = Case([300, 77], [new, new], 2, 128, 16, seed=new)
+    case.scales[0][:] = key_byte
+    attend(bsq, case, 2 * group, 2.0 ** q_exp)
