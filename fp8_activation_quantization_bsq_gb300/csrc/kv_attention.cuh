@@ -342,6 +342,12 @@ __device__ __forceinline__ int kv_query_exp(float amax) {
   return amax > 0.f ? max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 12, -126) : 0;
 }
 
+// The factor of a row's scores of a page.  Where the two together pass FP32 it is FP32's largest number, so that
+// a score of 0 stays 0.
+__device__ __forceinline__ float kv_score_factor(float row, float page) {
+  return fminf(fmaxf(row * page, -3.402823466e38f), 3.402823466e38f);
+}
+
 // The codes of 4 consecutive dimensions of two keys -> for each dimension
 // the pair (key 0, key 1) in FP16.
 __device__ __forceinline__ void kv_pairs(uint32_t w0, uint32_t w1, uint32_t (&o)[4]) {
@@ -590,7 +596,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int h = i & 1;
-              float x = (s[t][i] + s2[t][i]) * (rowfac[t][h] * ps.kfac) + ps.ev;
+              float x = (s[t][i] + s2[t][i]) * kv_score_factor(rowfac[t][h], ps.kfac) + ps.ev;
               if constexpr (decltype(edge)::value) {
                 const int key = key0 + gq + 8 * (i >> 1);
                 const bool see = ps.inv != 0.f && key >= lo && key < hi && (!a.causal || key <= pos[t][h]) &&

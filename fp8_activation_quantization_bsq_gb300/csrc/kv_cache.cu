@@ -1,6 +1,7 @@
 // Host side of the 8-bit paged key/value cache: argument checks and launch
 // geometry of bsq_kv_append and bsq_kv_attention (include/bsq.h).
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "host_common.h"
@@ -203,8 +204,9 @@ int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t he
   a.causal = causal;
   a.window = window < kKvMaxLen ? window : 0;  // no two positions are that far apart
   int exponent;
-  const float significand = std::frexp(sm_scale * 1.4426950408889634f, &exponent);  // 0, or in [1/2, 1)
-  a.scale_sig = 2.f * std::fabs(significand);
+  const float scale = std::fmin(std::fabs(sm_scale * 1.4426950408889634f), FLT_MAX);
+  const float significand = std::frexp(scale, &exponent);  // 0, or in [1/2, 1)
+  a.scale_sig = 2.f * significand;
   a.scale_pow = std::copysign(std::ldexp(1.f, exponent - 1), sm_scale);
   a.ready = static_cast<uint32_t*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKvCounterBytes);

@@ -80,7 +80,7 @@ __device__ __forceinline__ float kp_scores(const KvAttnArgs& a, const KpRow& row
 #pragma unroll
   for (int h = 0; h < kKpSub; h += 16) {
     const KvPageScale ps = slot.sc[(first + h) >> shift];
-    const float f = row.fac * ps.kfac;
+    const float f = fminf(row.fac * ps.kfac, 3.402823466e38f);
     if constexpr (EDGE) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -111,7 +111,7 @@ __device__ __forceinline__ float kp_weights(const KpRow& row, uint32_t taddr, co
 #pragma unroll
     for (int h = 0; h < 32; h += 16) {
       const KvPageScale ps = slot.sc[(first + c + h) >> shift];
-      const float f = row.fac * ps.kfac, e = ps.ev - m;
+      const float f = fminf(row.fac * ps.kfac, 3.402823466e38f), e = ps.ev - m;
       float2 part = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {

@@ -63,3 +63,12 @@ def test_smallest_query_rows(bsq, group, new, q_exp, key_byte):
     case = Case([300, 77], [new, new], 2, 128, 16, seed=new)
     case.scales[0][:] = key_byte
     attend(bsq, case, 2 * group, 2.0 ** q_exp)
+
+
+@pytest.mark.parametrize("group,new", ROWS)
+def test_zero_keys_under_any_scale(bsq, group, new):
+    """Scores of 0, where the factors of the row and of the page together pass FP32."""
+    case = Case([300, 77], [new, new], 2, 64, 16, seed=new)
+    case.cache[0][:] = case.rng.choice(np.array([0x00, 0x80], np.uint8), case.cache[0].shape)
+    case.scales[0][:] = 254
+    attend(bsq, case, 2 * group, 2.0 ** 100)
