@@ -4,12 +4,15 @@
 // Per query row of a head, over the allowed keys j of its sequence:
 //   s_j = sm_scale log2(e) q.k_j,  out = sum_j 2^s_j v_j / sum_j 2^s_j.
 // A page holds codes under power-of-two scales, k = c 2^ek and v = c 2^ev.  The
-// value scale goes into the exponent: with t_j = s_j + ev_j and m at or above
-// most t_j (it follows the running maximum once that is 8 above it),
-//   out = sum_j 2^(t_j - m) c_j / sum_j 2^(t_j - m) 2^-ev_j,
+// value scale goes into the exponent: with t_j = s_j + ev_j, and m at or above
+// most t_j (it follows the running maximum once that is 8 above it) and a reference z of the scores,
+//   out = 2^(m - z) sum_j 2^(t_j - m) c_j / sum_j 2^(s_j - z),
 // so the weights of the codes stay within FP16 whatever the pages' scales are, and
-// nothing is multiplied into the values.  The key scale is one factor of a tile's
-// scores.  E4M3 codes and scaled query rows (a power of two per row) are exact in FP16
+// nothing is multiplied into the values.  While the pages' |ev| are at most kKvTameExp, z is m and the sum below
+// takes 2^(t_j - m) 2^-ev, an exponential per key for both: it stays below 2^(48 + 30), and what 2^(t_j - m) loses
+// below 2^-126 is less than 2^-46 of the largest.  From the first page past that on, an item's share
+// has a z of its own, the scores' running maximum, and exponentials of its own for the sum.
+// The key scale is one factor of a tile's scores.  E4M3 codes and scaled query rows (a power of two per row) are exact in FP16
 // (elements below 2^-28 of a row's largest: to 2^-37 of that);
 // weights are rounded to FP16 (a relative 2^-11 each, against 2^-9 of a BF16
 // output), and all sums are FP32.
@@ -71,7 +74,7 @@ struct KvAttnArgs {
   float scale_pow, scale_sig;
   uint64_t group_inv;             // ceil(2^64 / group), for kv_token
   uint32_t* ready;                // [block] part stored, zero between calls
-  float* part;                    // [block][rows * D + 2 * rows]: sums, maxima, weights' sums
+  float* part;                    // [block][rows * D + 3 * rows]: sums, m, sums below, z
   unsigned int* err;
 };
 
@@ -300,15 +303,22 @@ __device__ __forceinline__ bool kv_start(const KvAttnArgs& a, int blocks_per_sm,
 }
 
 // Per page of a stage: factor of the scores (with the significand of sm_scale log2(e)), exponent of the values, and its
-// reciprocal power.
+// reciprocal power (0: no such page).
 struct KvPageScale {
   float kfac, ev, inv;
 };
+constexpr float kKvTameExp = 40.f;
+// No such page, or |ev| above kKvTameExp, as one comparison of 2^-ev.
+__device__ __forceinline__ bool kv_special(const KvPageScale& ps) {
+  constexpr uint32_t kLeast = static_cast<uint32_t>(127 - static_cast<int>(kKvTameExp)) << 23;
+  return __float_as_uint(ps.inv) - kLeast > static_cast<uint32_t>(2 * static_cast<int>(kKvTameExp)) << 23;
+}
+constexpr float kKvMaxFloat = 3.402823466e38f;
 
 // From the scale bytes; -1: no such page.
 __device__ __forceinline__ KvPageScale kv_page_scale(const KvAttnArgs& a, int ek, int ev) {
-  if (ek < 0) return {0.f, -INFINITY, 0.f};
-  return {a.scale_sig * pow2f(min(max(ek - 127, -126), 127)), static_cast<float>(ev - 127), pow2f(min(max(127 - ev, -126), 127))};
+  if (ek < 0) return {0.f, 0.f, 0.f};
+  return {a.scale_sig * pow2f(min(max(ek - 127, -126), 127)), static_cast<float>(ev - 127), pow2f(min(127 - ev, 127))};
 }
 
 // NT: tiles of 8 query rows.
@@ -332,7 +342,7 @@ struct KvShape {
   // (guessed tokens) 26.7 against 24.6.  Three blocks per SM for 16 rows: 111, but 17.3 for the short contexts
   static constexpr bool kSharedQuery = NT == 4 || (NT == 2 && D == 128);
   static constexpr int kSmem = 1024 + kStages * 2 * kTileBytes + kMergeBytes;
-  static constexpr int kPartFloats = kRows * D + 2 * kRows;
+  static constexpr int kPartFloats = kRows * D + 3 * kRows;
 };
 
 // A query row enters its products as 2^-eq of itself, with its largest magnitude in
@@ -345,8 +355,25 @@ __device__ __forceinline__ int kv_query_exp(float amax) {
 // The factor of a row's scores of a page.  Where the two together pass FP32 it is FP32's largest number, so that
 // a score of 0 stays 0.
 __device__ __forceinline__ float kv_score_factor(float row, float page) {
-  return fminf(fmaxf(row * page, -3.402823466e38f), 3.402823466e38f);
+  return fminf(fmaxf(row * page, -kKvMaxFloat), kKvMaxFloat);
 }
+
+// A row's sum below, relative to 2^m, or to 2^z where some page made it wild.  In memory a wild sum is negative,
+// and only then does its z count.
+struct KvSum {
+  float l = 0.f, z = -INFINITY;
+  bool wild = false;
+  // Adds another (as in memory, with its m and, if it is wild, z) where one of the two is wild.
+  __device__ __forceinline__ void add_wild(float pm, float pl, float pz) {
+    if (!(pl < 0.f)) pz = pm;
+    const float zz = fmaxf(z, pz);
+    l = l * (z == -INFINITY ? 0.f : fast_exp2(z - zz)) + fabsf(pl) * (pz == -INFINITY ? 0.f : fast_exp2(pz - zz));
+    z = zz;
+    wild = true;
+  }
+  __device__ __forceinline__ float stored() const { return wild ? -l : l; }
+  __device__ __forceinline__ float lse(float m) const { return l > 0.f ? ((wild ? z : m) + log2f(l)) * 0.6931471805599453f : -INFINITY; }
+};
 
 // The codes of 4 consecutive dimensions of two keys -> for each dimension
 // the pair (key 0, key 1) in FP16.
@@ -395,7 +422,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
   [[maybe_unused]] uint4* query = reinterpret_cast<uint4*>(merge);
   __shared__ uint64_t full_bar[S::kStages], empty_bar[S::kStages];
   __shared__ KvPageScale page_scale[S::kStages][4];
-  __shared__ float warp_m2[2][S::kWarps][RT], warp_l2[2][S::kWarps][RT];  // by parity of the item
+  __shared__ float warp_m2[2][S::kWarps][RT], warp_z2[2][S::kWarps][RT], warp_l2[2][S::kWarps][RT];  // by parity of the item
   __shared__ KvWalk<RT, kKvTile> walks[S::kWarps + 1];
   __shared__ KvStart start;
   __shared__ int64_t warp_sum[S::kWarps + 1];
@@ -481,6 +508,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
     bool ok = true;
     for (int item = 0; ok && walk.step(a); ++item) {
       float(*warp_m)[RT] = warp_m2[item & 1];
+      float(*warp_z)[RT] = warp_z2[item & 1];
       float(*warp_l)[RT] = warp_l2[item & 1];
       const int rows = g.s.n * a.group, pos0 = g.s.len - g.s.n;
       const int lo = g.lo, hi = g.hi, tile1 = g.tile1;
@@ -539,148 +567,188 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
 
-      for (int tile = g.tile0; tile < tile1; ++tile) {
-        ok = __all_sync(~0u, mbar_wait_clocked(&full_bar[stage], phase, &abort_flag));
-        if (!ok) break;
-        const uint8_t* kd = smem + stage * 2 * S::kTileBytes;
-        const uint8_t* vd = kd + S::kTileBytes;
-        const KvPageScale ps = page_scale[stage][(16 * warp) >> min(a.page_shift, 6)];
-        // S^T: keys gq (elements 0, 1) and gq + 8 (2, 3), rows 2 c (0, 2) and + 1 (1, 3); two chains of products
-        float s[NT][4], s2[NT][4];
+      int tile = g.tile0;
+      // The tiles from `tile` on; without kWild up to the first page that wants z to be the scores' own (in warp_z).
+      // A loop of its own: in one with them the other tiles took 3 to 14 % longer (64 contexts to 8192, 16 and 32 rows).
+      const auto walk_tiles = [&](auto wild_tag) {
+        constexpr bool kWild = decltype(wild_tag)::value;
+        for (; tile < tile1; ++tile) {
+          ok = __all_sync(~0u, mbar_wait_clocked(&full_bar[stage], phase, &abort_flag));
+          if (!ok) break;
+          const uint8_t* kd = smem + stage * 2 * S::kTileBytes;
+          const uint8_t* vd = kd + S::kTileBytes;
+          const KvPageScale ps = page_scale[stage][(16 * warp) >> min(a.page_shift, 6)];
+          // S^T: keys gq (elements 0, 1) and gq + 8 (2, 3), rows 2 c (0, 2) and + 1 (1, 3); two chains of products
+          float s[NT][4], s2[NT][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[t][i] = s2[t][i] = 0.f;
+            for (int i = 0; i < 4; ++i) s[t][i] = s2[t][i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kQuads; ++j) {
-          const uint4 u = *reinterpret_cast<const uint4*>(kd + kv_chunk<D>(16 * warp + gq, kQuads * c + j));
-          const uint4 w = *reinterpret_cast<const uint4*>(kd + kv_chunk<D>(16 * warp + 8 + gq, kQuads * c + j));
-          const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {w.x, w.y, w.z, w.w};
-          uint4 qv[S::kSharedQuery ? NT : 1][2];
-          if constexpr (S::kSharedQuery) {
+          for (int j = 0; j < kQuads; ++j) {
+            const uint4 u = *reinterpret_cast<const uint4*>(kd + kv_chunk<D>(16 * warp + gq, kQuads * c + j));
+            const uint4 w = *reinterpret_cast<const uint4*>(kd + kv_chunk<D>(16 * warp + 8 + gq, kQuads * c + j));
+            const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {w.x, w.y, w.z, w.w};
+            [[maybe_unused]] uint4 qv[S::kSharedQuery ? NT : 1][2];
+            if constexpr (S::kSharedQuery) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+              for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) qv[t][i] = query[(t * (D / 32) + 2 * j + i) * 32 + lane];
+                for (int i = 0; i < 2; ++i) qv[t][i] = query[(t * (D / 32) + 2 * j + i) * 32 + lane];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // K slice: dimensions D/4 c + 16 j + 4 i .. + 3
+              const uint32_t a0 = e4m3x2_to_f16x2(x[i] & 0xFFFFu), a1 = e4m3x2_to_f16x2(y[i] & 0xFFFFu);
+              const uint32_t a2 = e4m3x2_to_f16x2(x[i] >> 16), a3 = e4m3x2_to_f16x2(y[i] >> 16);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                uint32_t b0, b1;
+                if constexpr (S::kSharedQuery) {
+                  const uint4 z = qv[t][i >> 1];
+                  b0 = i & 1 ? z.z : z.x;
+                  b1 = i & 1 ? z.w : z.y;
+                } else {
+                  b0 = q[t][8 * j + 2 * i];
+                  b1 = q[t][8 * j + 2 * i + 1];
+                }
+                if (i & 1) kv_mma(s2[t], a0, a1, a2, a3, b0, b1);
+                else kv_mma(s[t], a0, a1, a2, a3, b0, b1);
+              }
+            }
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {  // K slice: dimensions D/4 c + 16 j + 4 i .. + 3
-            const uint32_t a0 = e4m3x2_to_f16x2(x[i] & 0xFFFFu), a1 = e4m3x2_to_f16x2(y[i] & 0xFFFFu);
-            const uint32_t a2 = e4m3x2_to_f16x2(x[i] >> 16), a3 = e4m3x2_to_f16x2(y[i] >> 16);
+          const int key0 = tile * kKvTile + 16 * warp;
+          // keys that not all rows see, or none: only tiles at the range's ends
+          const bool masked = kv_special(ps) || key0 < lo || key0 + 16 > hi || (a.causal && key0 + 15 > pos_first) ||
+                              (a.window > 0 && key0 <= pos_last - a.window);
+          // two copies of the rest, so that the tiles in between carry no masks
+          const auto rest = [&](auto edge) {
+            float top[NT][2];
+            bool raise = false;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-              uint32_t b0, b1;
-              if constexpr (S::kSharedQuery) {
-                const uint4 z = qv[t][i >> 1];
-                b0 = i & 1 ? z.z : z.x;
-                b1 = i & 1 ? z.w : z.y;
-              } else {
-                b0 = q[t][8 * j + 2 * i];
-                b1 = q[t][8 * j + 2 * i + 1];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int h = i & 1;
+                float x = (s[t][i] + s2[t][i]) * kv_score_factor(rowfac[t][h], ps.kfac) + ps.ev;
+                if constexpr (decltype(edge)::value) {
+                  const int key = key0 + gq + 8 * (i >> 1);
+                  const bool see = ps.inv != 0.f && key >= lo && key < hi && (!a.causal || key <= pos[t][h]) &&
+                                   (a.window <= 0 || key > pos[t][h] - a.window);
+                  x = see ? x : -INFINITY;
+                }
+                s[t][i] = x;
               }
-              if (i & 1) kv_mma(s2[t], a0, a1, a2, a3, b0, b1);
-              else kv_mma(s[t], a0, a1, a2, a3, b0, b1);
-            }
-          }
-        }
-        const int key0 = tile * kKvTile + 16 * warp;
-        // keys that not all rows see, or none: only tiles at the range's ends
-        const bool masked = ps.inv == 0.f || key0 < lo || key0 + 16 > hi || (a.causal && key0 + 15 > pos_first) ||
-                            (a.window > 0 && key0 <= pos_last - a.window);
-        // two copies of the rest, so that the tiles in between carry no masks
-        const auto rest = [&](auto edge) {
-          float top[NT][2];
-          bool raise = false;
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int h = i & 1;
-              float x = (s[t][i] + s2[t][i]) * kv_score_factor(rowfac[t][h], ps.kfac) + ps.ev;
-              if constexpr (decltype(edge)::value) {
-                const int key = key0 + gq + 8 * (i >> 1);
-                const bool see = ps.inv != 0.f && key >= lo && key < hi && (!a.causal || key <= pos[t][h]) &&
-                                 (a.window <= 0 || key > pos[t][h] - a.window);
-                x = see ? x : -INFINITY;
-              }
-              s[t][i] = x;
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float x = fmaxf(s[t][h], s[t][2 + h]);
-              x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-              top[t][h] = x;
-              raise |= x > m[t][h] + 8.f;
-            }
-          }
-          if (__any_sync(~0u, raise)) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float mn = fmaxf(m[t][h], top[t][h]);
-                const float f = m[t][h] == -INFINITY ? 0.f : fast_exp2(m[t][h] - mn);
-                m[t][h] = mn;
-                l[t][h] *= f;
+                float x = fmaxf(s[t][h], s[t][2 + h]);
+                x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+                top[t][h] = x;
+                raise |= x > m[t][h] + 8.f;
+              }
+            }
+            if constexpr (kWild) {
+              __syncwarp();
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                  o[t][i][h] *= f;
-                  o[t][i][2 + h] *= f;
+              for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float z = warp_z[warp][8 * t + 2 * c + h], zn = fmaxf(z, top[t][h] - ps.ev), z0 = zn == -INFINITY ? 0.f : zn;
+                  l[t][h] = l[t][h] * fast_exp2(z - z0) + fast_exp2(s[t][h] - ps.ev - z0) + fast_exp2(s[t][2 + h] - ps.ev - z0);
+                  __syncwarp();
+                  if (gq == 0) warp_z[warp][8 * t + 2 * c + h] = zn;
                 }
               }
             }
-          }
-          // P^T as the second operand: pairs of rows to pairs of keys
-          uint32_t p[NT][2];
+            if (__any_sync(~0u, raise)) {
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
-            const float x0 = fast_exp2(s[t][0] - m0), x1 = fast_exp2(s[t][1] - m1);
-            const float x2 = fast_exp2(s[t][2] - m0), x3 = fast_exp2(s[t][3] - m1);
-            l[t][0] += (x0 + x2) * ps.inv;
-            l[t][1] += (x1 + x3) * ps.inv;
-            p[t][0] = kv_transpose(f32x2_to_elem2<true>(x0, x1));
-            p[t][1] = kv_transpose(f32x2_to_elem2<true>(x2, x3));
-          }
-          // values: keys 2c, 2c + 1 and 8 + 2c, 9 + 2c; this thread's dimensions D/8 gq ..
-          uint32_t vw[4][D / 32];
+              for (int t = 0; t < NT; ++t) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = 16 * warp + 8 * (k >> 1) + 2 * c + (k & 1);
-            if constexpr (D == 128) {
-              const uint4 w = *reinterpret_cast<const uint4*>(vd + kv_chunk<D>(r, gq));
-              vw[k][0] = w.x; vw[k][1] = w.y; vw[k][2] = w.z; vw[k][3] = w.w;
-            } else {
-              const uint2 w = *reinterpret_cast<const uint2*>(vd + kv_chunk<D>(r, gq >> 1) + 8 * (gq & 1));
-              vw[k][0] = w.x; vw[k][1] = w.y;
-            }
-            if constexpr (decltype(edge)::value) {  // whatever lies outside the allowed keys (NaN codes too) counts as zero
-              const int key = tile * kKvTile + r;
-              if (key < lo || key >= hi || ps.inv == 0.f) {
+                for (int h = 0; h < 2; ++h) {
+                  const float mn = fmaxf(m[t][h], top[t][h]);
+                  const float f = m[t][h] == -INFINITY ? 0.f : fast_exp2(m[t][h] - mn);
+                  m[t][h] = mn;
+                  if constexpr (!kWild) l[t][h] *= f;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) vw[k][i] = 0u;
+                  for (int i = 0; i < D / 16; ++i) {
+                    o[t][i][h] *= f;
+                    o[t][i][2 + h] *= f;
+                  }
+                }
               }
             }
-          }
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t lo[4], hi[4];
-            kv_pairs(vw[0][i], vw[1][i], lo);
-            kv_pairs(vw[2][i], vw[3][i], hi);
+            // P^T as the second operand: pairs of rows to pairs of keys
+            uint32_t p[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-              kv_mma(o[t][2 * i], lo[0], lo[1], hi[0], hi[1], p[t][0], p[t][1]);
-              kv_mma(o[t][2 * i + 1], lo[2], lo[3], hi[2], hi[3], p[t][0], p[t][1]);
+              const float m0 = m[t][0] == -INFINITY ? 0.f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+              const float x0 = fast_exp2(s[t][0] - m0), x1 = fast_exp2(s[t][1] - m1);
+              const float x2 = fast_exp2(s[t][2] - m0), x3 = fast_exp2(s[t][3] - m1);
+              if constexpr (!kWild) {
+                l[t][0] += (x0 + x2) * ps.inv;
+                l[t][1] += (x1 + x3) * ps.inv;
+              }
+              p[t][0] = kv_transpose(f32x2_to_elem2<true>(x0, x1));
+              p[t][1] = kv_transpose(f32x2_to_elem2<true>(x2, x3));
+            }
+            // values: keys 2c, 2c + 1 and 8 + 2c, 9 + 2c; this thread's dimensions D/8 gq ..
+            uint32_t vw[4][D / 32];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = 16 * warp + 8 * (k >> 1) + 2 * c + (k & 1);
+              if constexpr (D == 128) {
+                const uint4 w = *reinterpret_cast<const uint4*>(vd + kv_chunk<D>(r, gq));
+                vw[k][0] = w.x; vw[k][1] = w.y; vw[k][2] = w.z; vw[k][3] = w.w;
+              } else {
+                const uint2 w = *reinterpret_cast<const uint2*>(vd + kv_chunk<D>(r, gq >> 1) + 8 * (gq & 1));
+                vw[k][0] = w.x; vw[k][1] = w.y;
+              }
+              if constexpr (decltype(edge)::value) {  // whatever lies outside the allowed keys (NaN codes too) counts as zero
+                const int key = tile * kKvTile + r;
+                if (key < lo || key >= hi || ps.inv == 0.f) {
+#pragma unroll
+                  for (int i = 0; i < D / 32; ++i) vw[k][i] = 0u;
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t lo[4], hi[4];
+              kv_pairs(vw[0][i], vw[1][i], lo);
+              kv_pairs(vw[2][i], vw[3][i], hi);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                kv_mma(o[t][2 * i], lo[0], lo[1], hi[0], hi[1], p[t][0], p[t][1]);
+                kv_mma(o[t][2 * i + 1], lo[2], lo[3], hi[2], hi[3], p[t][0], p[t][1]);
+              }
+            }
+          };
+          if constexpr (kWild) {
+            rest(std::true_type{});
+          } else {
+            if (masked) {
+              if (fabsf(ps.ev) > kKvTameExp) break;
+              rest(std::true_type{});
+            } else {
+              rest(std::false_type{});
             }
           }
-        };
-        if (masked) rest(std::true_type{}); else rest(std::false_type{});
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty_bar[stage]);
-        ++used;
-        if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty_bar[stage]);
+          ++used;
+          if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
+        }
+      };
+      walk_tiles(std::false_type{});
+      const bool wild = ok && tile < tile1;
+      if (wild) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (gq == 0) warp_z[warp][8 * t + 2 * c + h] = m[t][h];
+        walk_tiles(std::true_type{});
       }
       if (!ok && lane == 0) {
         if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
@@ -695,7 +763,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
           for (int d = 4; d < 32; d <<= 1) l[t][h] += __shfl_xor_sync(~0u, l[t][h], d);
           if (gq == 0) {
             warp_m[warp][8 * t + 2 * c + h] = m[t][h];
-            warp_l[warp][8 * t + 2 * c + h] = l[t][h];
+            warp_l[warp][8 * t + 2 * c + h] = wild ? -l[t][h] : l[t][h];
           }
         }
       }
@@ -763,13 +831,15 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
             const float4 z = *reinterpret_cast<const float4*>(src + 2 * kWarpStride), w = *reinterpret_cast<const float4*>(src + 3 * kWarpStride);
             acc[i] = make_float4((x.x + y.x) + (z.x + w.x), (x.y + y.y) + (z.y + w.y), (x.z + y.z) + (z.z + w.z), (x.w + y.w) + (z.w + w.w));
           }
-          float am = -INFINITY, al = 0.f;
+          KvSum below;
+          float am = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 4; ++k) am = fmaxf(am, warp_m[k][r]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float wm = warp_m[k][r];
-            al += wm == -INFINITY ? 0.f : warp_l[k][r] * fast_exp2(wm - am);
+            const float wm = warp_m[k][r], wl = warp_l[k][r];
+            below.wild |= wl < 0.f;
+            below.l += wm == -INFINITY ? 0.f : wl * fast_exp2(wm - am);
           }
 #pragma unroll(16 / kOwn)
           for (int p = 0; p < near + far; ++p) {
@@ -784,26 +854,44 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
             for (int i = 0; i < kOwn; ++i)
               acc[i] = make_float4(acc[i].x * f0 + v[i].x * f1, acc[i].y * f0 + v[i].y * f1, acc[i].z * f0 + v[i].z * f1,
                                    acc[i].w * f0 + v[i].w * f1);
-            al = al * f0 + pl * f1;
+            below.wild |= pl < 0.f;
+            below.l = below.l * f0 + pl * f1;
             am = mm;
+          }
+          if (below.wild) {  // the sum again, with every z
+            below = KvSum{};
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) below.add_wild(warp_m[k][r], warp_l[k][r], warp_z[k][r]);
+#pragma unroll 1
+            for (int p = 0; p < near + far; ++p) {
+              const float* part = mine + static_cast<int64_t>(p < near ? 1 + p : join * (p - near + 1)) * S::kPartFloats + RT * D + r;
+              below.add_wild(__ldcg(part), __ldcg(part + RT), __ldcg(part + 2 * RT));
+            }
           }
           if (me != 0) {
 #pragma unroll
             for (int i = 0; i < kOwn; ++i) __stcg(reinterpret_cast<float4*>(mine + r * D) + kTpr * i + d4, acc[i]);
             if (d4 == 0) {
               __stcg(mine + RT * D + r, am);
-              __stcg(mine + RT * D + RT + r, al);
+              __stcg(mine + RT * D + RT + r, below.stored());
+              if (below.wild) __stcg(mine + RT * D + 2 * RT + r, below.z);
             }
           } else {
             const int rr = g.rt * RT + r;
             const int tok = kv_token(a, rr);
             const int64_t row = static_cast<int64_t>(g.s.t0 + tok) * a.heads + g.head * a.group + rr - tok * a.group;
-            const float f = al > 0.f ? 1.f / al : 0.f;
+            float f = below.l > 0.f ? 1.f / below.l : 0.f;
+            if (below.wild) {  // 2^(m - z) in two steps: the whole may pass FP32 where the output does not
+              const float half = fast_exp2(0.5f * (am - below.z));
+              f *= half;
+#pragma unroll
+              for (int i = 0; i < kOwn; ++i) acc[i] = make_float4(acc[i].x * half, acc[i].y * half, acc[i].z * half, acc[i].w * half);
+            }
 #pragma unroll
             for (int i = 0; i < kOwn; ++i)
               *reinterpret_cast<uint2*>(a.out + row * D + 4 * (kTpr * i + d4)) =
                   make_uint2(f32x2_to_elem2<F16>(acc[i].x * f, acc[i].y * f), f32x2_to_elem2<F16>(acc[i].z * f, acc[i].w * f));
-            if (d4 == 0 && a.lse != nullptr) a.lse[row] = al > 0.f ? (am + log2f(al)) * 0.6931471805599453f : -INFINITY;
+            if (d4 == 0 && a.lse != nullptr) a.lse[row] = below.lse(am);
           }
         }
       }

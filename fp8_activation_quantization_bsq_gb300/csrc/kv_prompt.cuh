@@ -39,13 +39,13 @@ struct KpShape {
   static constexpr int kRawBytes = kKpKeys * D, kWideBytes = 2 * kRawBytes;
   static constexpr int kHalfBytes = 128 * D * 2;  // query rows of a half
   static constexpr int kSmem = 1024 + 2 * kHalfBytes + kKpWide * kWideBytes + kKpRaw * kRawBytes;
-  static constexpr int kPartFloats = kKpRows * D + 2 * kKpRows;  // [d][row], maxima, sums
+  static constexpr int kPartFloats = kKpRows * D + 4 * kKpRows;  // [d][row], m, sums below, z; the block's own: z of the rows at work
 };
 
-// Page scales of a unit (up to 8 pages of 16 tokens); bad: some page is missing.
+// Page scales of a unit (up to 8 pages of 16 tokens).
 struct KpSlot {
   KvPageScale sc[8];
-  int bad;
+  uint32_t special;  // 1: some page is missing, 2: some |ev| is above kKvTameExp
 };
 
 // A half's softmax state of one row.
@@ -80,7 +80,7 @@ __device__ __forceinline__ float kp_scores(const KvAttnArgs& a, const KpRow& row
 #pragma unroll
   for (int h = 0; h < kKpSub; h += 16) {
     const KvPageScale ps = slot.sc[(first + h) >> shift];
-    const float f = fminf(row.fac * ps.kfac, 3.402823466e38f);
+    const float f = fminf(row.fac * ps.kfac, kKvMaxFloat);
     if constexpr (EDGE) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -100,6 +100,29 @@ __device__ __forceinline__ float kp_scores(const KvAttnArgs& a, const KpRow& row
   return top;
 }
 
+// The scores of kKpSub keys (from their t) into a sum below with a z of its own, which lies in memory.
+__device__ __forceinline__ float kp_wild_sum(float l, float* z, const KpSlot& slot, int shift, int first, const float (&x)[kKpSub]) {
+  const float before = *z;
+  float zn = before;
+#pragma unroll
+  for (int h = 0; h < kKpSub; h += 16) {
+    float top = x[h];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, x[h + i]);
+    zn = fmaxf(zn, top - slot.sc[(first + h) >> shift].ev);
+  }
+  const float z0 = zn == -INFINITY ? 0.f : zn;
+  l *= fast_exp2(before - z0);
+#pragma unroll
+  for (int h = 0; h < kKpSub; h += 16) {
+    const float e = slot.sc[(first + h) >> shift].ev + z0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) l += fast_exp2(x[h + i] - e);
+  }
+  *z = zn;
+  return l;
+}
+
 // Weights over the scores' place; returns their sum (of 2^(t - m) 2^-ev).
 template <bool EDGE>
 __device__ __forceinline__ float kp_weights(const KpRow& row, uint32_t taddr, const KpSlot& slot, int shift, int first, float m,
@@ -111,7 +134,7 @@ __device__ __forceinline__ float kp_weights(const KpRow& row, uint32_t taddr, co
 #pragma unroll
     for (int h = 0; h < 32; h += 16) {
       const KvPageScale ps = slot.sc[(first + c + h) >> shift];
-      const float f = fminf(row.fac * ps.kfac, 3.402823466e38f), e = ps.ev - m;
+      const float f = fminf(row.fac * ps.kfac, kKvMaxFloat), e = ps.ev - m;
       float2 part = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
@@ -219,7 +242,8 @@ __global__ void __launch_bounds__(kKpThreads, 1)
           if (!ok) break;
           if (kv == 0) {  // the softmax reads these after the unit's scores, long before 8 units on
             if (lane >= first && lane < first + boxes) slots[unit % kKpSlots].sc[lane - first] = sc;
-            if (lane == 0) slots[unit % kKpSlots].bad = got != (1u << boxes) - 1u;
+            const uint32_t wild = __ballot_sync(~0u, fabsf(sc.ev) > kKvTameExp) >> first & ((1u << boxes) - 1u);
+            if (lane == 0) slots[unit % kKpSlots].special = (got != (1u << boxes) - 1u ? 1u : 0u) | (wild != 0u ? 2u : 0u);
             __syncwarp();
           }
           if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], __popc(got) * box * D);
@@ -253,7 +277,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
           const uint8_t* src = raw + r * S::kRawBytes;
           uint8_t* dst = wide + w * S::kWideBytes;
           const KpSlot& slot = slots[unit % kKpSlots];
-          const bool some = ends || slot.bad != 0;
+          const bool some = ends || (slot.special & 1u) != 0u;
           // 16 dimensions of keys key0, key0 + kRowsPerIter, ...; the second 64 dimensions' lanes
           // store their halves the other way round, so that a row's stores fall into different banks
           const int c = ct % kRowThreads, key0 = ct / kRowThreads, block = c >> 2, ch = 2 * (c & 3), sw = key0 & 7;
@@ -366,6 +390,8 @@ __global__ void __launch_bounds__(kKpThreads, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const uint32_t ts = lanes + 128 * half, to = lanes + 256 + 128 * half;
     const int shift = min(a.page_shift, 7);
+    float* const mine = a.part + static_cast<int64_t>(blockIdx.x) * S::kPartFloats;
+    float* const row_z = mine + kKpRows * D + 3 * kKpRows + r_tile;
     uint32_t unit = 0, k = 0, finished = 0;
     bool ok = true;
     while (walk.step_together(a, 1, 256, tid == 0, &more[0], &abort_flag)) {
@@ -405,52 +431,71 @@ __global__ void __launch_bounds__(kKpThreads, 1)
       const int tile0 = g.tile0, tile1 = g.tile1, lo = g.lo, hi = g.hi;
       // positions of the half's first and last row
       const int pos_first = pos0 + kv_token(a, first_row), pos_last = pos0 + kv_token(a, last_row);
-      for (int t = tile0; t < tile1 && ok; ++t, ++unit) {
-        if (!busy) continue;
-        const KpSlot& slot = slots[unit % kKpSlots];
-        const int key0 = t * kKpKeys;
-        bool masked = false;
+      int t = tile0;
+      // The units from t on; without kWild up to the first page that wants z to be the scores' own (in *row_z).
+      const auto walk_units = [&](auto wild_tag) {
+        constexpr bool kWild = decltype(wild_tag)::value;
+        bool leave = false;
+        for (; t < tile1 && ok; ++t, ++unit) {
+          if (!busy) continue;
+          const KpSlot& slot = slots[unit % kKpSlots];
+          const int key0 = t * kKpKeys;
+          bool masked = false;
 #pragma unroll 1
-        for (int sub = 0; sub < 2; ++sub) {
-          ok = __all_sync(~0u, mbar_wait_clocked(&s_full[half][sub], k >> 1 & 1u, &abort_flag));
-          if (!ok) break;
-          t5_fence_after();
-          if (sub == 0)
-            masked = slot.bad != 0 || key0 < lo || key0 + kKpKeys > hi || (a.causal && key0 + kKpKeys - 1 > pos_first) ||
-                     (a.window > 0 && key0 <= pos_last - a.window);
-          const uint32_t tile = ts + kKpSub * sub;
-          const int first = kKpSub * sub;
-          float x[kKpSub];
-          const float top = masked ? kp_scores<true>(a, row, tile, slot, shift, first, key0, lo, hi, x)
-                                   : kp_scores<false>(a, row, tile, slot, shift, first, key0, lo, hi, x);
-          if (__any_sync(~0u, top > row.m + 8.f)) {
-            const float mn = fmaxf(row.m, top), f = row.m == -INFINITY ? 0.f : fast_exp2(row.m - mn);
-            row.m = mn;
-            row.l *= f;
-            // O holds the keys before: wait for the last product (the one before it is done: these
-            // scores came after it)
-            if (t > tile0 || sub > 0) {
-              ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u, &abort_flag));
-              if (!ok) break;
-              t5_fence_after();
+          for (int sub = 0; sub < 2; ++sub) {
+            ok = __all_sync(~0u, mbar_wait_clocked(&s_full[half][sub], k >> 1 & 1u, &abort_flag));
+            if (!ok) break;
+            t5_fence_after();
+            if (sub == 0)
+              masked = kWild || slot.special != 0u || key0 < lo || key0 + kKpKeys > hi || (a.causal && key0 + kKpKeys - 1 > pos_first) ||
+                       (a.window > 0 && key0 <= pos_last - a.window);
+            if (!kWild && masked && (slot.special & 2u) != 0u) {  // while sub is 0
+              leave = true;
+              break;
+            }
+            const uint32_t tile = ts + kKpSub * sub;
+            const int first = kKpSub * sub;
+            float x[kKpSub];
+            const float top = masked ? kp_scores<true>(a, row, tile, slot, shift, first, key0, lo, hi, x)
+                                     : kp_scores<false>(a, row, tile, slot, shift, first, key0, lo, hi, x);
+            if constexpr (kWild) row.l = kp_wild_sum(row.l, row_z, slot, shift, first, x);
+            if (__any_sync(~0u, top > row.m + 8.f)) {
+              const float mn = fmaxf(row.m, top), f = row.m == -INFINITY ? 0.f : fast_exp2(row.m - mn);
+              row.m = mn;
+              if constexpr (!kWild) row.l *= f;
+              // O holds the keys before: wait for the last product (the one before it is done: these
+              // scores came after it)
+              if (t > tile0 || sub > 0) {
+                ok = __all_sync(~0u, mbar_wait_clocked(&pv_done[half], (k - 1u) & 1u, &abort_flag));
+                if (!ok) break;
+                t5_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                float y[16];
-                t5_ld16(to + c, y);
+                for (int c = 0; c < D; c += 16) {
+                  float y[16];
+                  t5_ld16(to + c, y);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] *= f;
-                t5_st16f(to + c, y);
+                  for (int i = 0; i < 16; ++i) y[i] *= f;
+                  t5_st16f(to + c, y);
+                }
               }
             }
+            const float m = row.m == -INFINITY ? 0.f : row.m;
+            const float sum = masked ? kp_weights<true>(row, tile, slot, shift, first, m, x) : kp_weights<false>(row, tile, slot, shift, first, m, x);
+            if constexpr (!kWild) row.l += sum;
+            t5_st_wait();
+            t5_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[half][sub]);
+            ++k;
           }
-          const float m = row.m == -INFINITY ? 0.f : row.m;
-          row.l += masked ? kp_weights<true>(row, tile, slot, shift, first, m, x) : kp_weights<false>(row, tile, slot, shift, first, m, x);
-          t5_st_wait();
-          t5_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[half][sub]);
-          ++k;
+          if (leave) break;
         }
+      };
+      walk_units(std::false_type{});
+      if (ok && t < tile1) {
+        *row_z = row.m;
+        walk_units(std::true_type{});
+        row.l = -row.l;  // as in memory (KvSum)
       }
       if (ok && busy) {
         // of its own, once an item: pv_done may be two phases behind here, which its parity could not tell
@@ -477,19 +522,25 @@ __global__ void __launch_bounds__(kKpThreads, 1)
       }
       named_sync(1, 256);
       ok = joined != 0u;  // one answer for all warps
-      float* mine = a.part + static_cast<int64_t>(blockIdx.x) * S::kPartFloats;
       if (ok && half_rows > 0) {  // uniform per warp
         const auto part_of = [&](int p) { return mine + static_cast<int64_t>(p < near ? 1 + p : join * (p - near + 1)) * S::kPartFloats; };
-        float am = row.m, al = row.l;
+        KvSum below{fabsf(row.l), row.l < 0.f ? *row_z : row.m, row.l < 0.f};
+        float am = row.m;
         for (int p = 0; p < near + far; ++p) {
           const float pm = row.live ? __ldcg(part_of(p) + kKpRows * D + r_tile) : -INFINITY;
           const float pl = row.live ? __ldcg(part_of(p) + kKpRows * D + kKpRows + r_tile) : 0.f;
           const float mm = fmaxf(am, pm);
-          al = al * (am == -INFINITY ? 0.f : fast_exp2(am - mm)) + pl * (pm == -INFINITY ? 0.f : fast_exp2(pm - mm));
+          if (below.wild || pl < 0.f) {
+            if (!below.wild) below.z = am;
+            below.add_wild(pm, pl, __ldcg(part_of(p) + kKpRows * D + 2 * kKpRows + r_tile));
+          } else {
+            below.l = below.l * (am == -INFINITY ? 0.f : fast_exp2(am - mm)) + pl * (pm == -INFINITY ? 0.f : fast_exp2(pm - mm));
+          }
           am = mm;
         }
         const float f0 = row.m == -INFINITY ? 0.f : fast_exp2(row.m - am);
-        const float inv = me != 0 ? 1.f : al > 0.f ? 1.f / al : 0.f;
+        // a wild sum's 2^(m - z) in two steps: the whole may pass FP32 where the output does not
+        const float half = below.wild ? fast_exp2(0.5f * (am - below.z)) : 1.f, inv = below.l > 0.f ? half / below.l : 0.f;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float x[32];
@@ -512,17 +563,20 @@ __global__ void __launch_bounds__(kKpThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; i += 8)
                 *reinterpret_cast<uint4*>(a.out + out_row * D + c + i) =
-                    make_uint4(f32x2_to_elem2<F16>(x[i] * inv, x[i + 1] * inv), f32x2_to_elem2<F16>(x[i + 2] * inv, x[i + 3] * inv),
-                               f32x2_to_elem2<F16>(x[i + 4] * inv, x[i + 5] * inv), f32x2_to_elem2<F16>(x[i + 6] * inv, x[i + 7] * inv));
+                    make_uint4(f32x2_to_elem2<F16>(x[i] * inv * half, x[i + 1] * inv * half),
+                               f32x2_to_elem2<F16>(x[i + 2] * inv * half, x[i + 3] * inv * half),
+                               f32x2_to_elem2<F16>(x[i + 4] * inv * half, x[i + 5] * inv * half),
+                               f32x2_to_elem2<F16>(x[i + 6] * inv * half, x[i + 7] * inv * half));
             }
           }
         }
         if (row.live) {
           if (me != 0) {
             __stcg(mine + kKpRows * D + r_tile, am);
-            __stcg(mine + kKpRows * D + kKpRows + r_tile, al);
+            __stcg(mine + kKpRows * D + kKpRows + r_tile, below.stored());
+            if (below.wild) __stcg(mine + kKpRows * D + 2 * kKpRows + r_tile, below.z);
           } else if (a.lse != nullptr) {
-            a.lse[out_row] = al > 0.f ? (am + log2f(al)) * 0.6931471805599453f : -INFINITY;
+            a.lse[out_row] = below.lse(am);
           }
         }
         t5_fence_before();

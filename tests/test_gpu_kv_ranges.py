@@ -26,6 +26,14 @@ def bsq():
     assert m.device_error() == 0
 
 
+def small_codes(case, top=1.0):
+    """Codes of magnitudes up to `top`, so that values under the largest scale stay finite."""
+    mags = np.arange(0x7F, dtype=np.uint8)
+    mags = mags[ref.e4m3_decode(mags) <= top]
+    for c in case.cache:
+        c[:] = case.rng.choice(mags, c.shape) | (case.rng.integers(0, 2, c.shape).astype(np.uint8) << 7)
+
+
 def close(case, got, got_lse, out, lse, mag, size, low, weight=2.0 ** -25):
     """As test_gpu_kv_cache.compare, without a floor for the smallest outputs.
     A score and the value scale's exponent meet in one FP32 number, and references of both are subtracted
@@ -46,6 +54,27 @@ def attend(bsq, case, heads, q_scale=1.0, **kw):
     q, qn = case.rows(heads, q_scale)
     got = bsq.kv_attention(q, *case.device(), int(np.max(np.diff(case.offsets))), return_lse=True)
     close(case, *got, *ref.attention(qn, *case.cache, *case.scales, case.table, case.offsets, case.lens, case.dim ** -0.5, True, 0), **kw)
+
+
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("q_scale", [0.0, 1.0])
+@pytest.mark.parametrize("value_bytes", [(1,), (254,), (1, 254), (1, 127, 254), (95, 247), (20, 100, 127)])
+def test_value_scales_from_end_to_end(bsq, group, new, q_scale, value_bytes):
+    """The lse does not depend on the values' scales, and the output is their weighted mean, however far apart they are."""
+    case = Case([777, 130, new], [new] * 3, 2, 128, 16, seed=len(value_bytes) + new)
+    small_codes(case)
+    case.scales = [case.rng.integers(124, 130, case.scales[0].shape).astype(np.uint8),
+                   case.rng.choice(np.array(value_bytes, np.uint8), case.scales[1].shape)]
+    attend(bsq, case, 2 * group, q_scale)
+
+
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("byte", [1, 12])
+def test_small_value_scales_over_many_tokens(bsq, group, new, byte):
+    case = Case([40000], [new], 1, 64, 64, seed=byte)
+    small_codes(case)
+    case.scales[1][:] = byte
+    attend(bsq, case, group, 0.1)
 
 
 def test_append_under_the_largest_scale(bsq):
