@@ -4,18 +4,19 @@
 // Per query row of a head, over the allowed keys j of its sequence:
 //   s_j = sm_scale log2(e) q.k_j,  out = sum_j 2^s_j v_j / sum_j 2^s_j.
 // A page holds codes under power-of-two scales, k = c 2^ek and v = c 2^ev.  The
-// value scale goes into the exponent: with t_j = s_j + ev_j, and m at or above
-// most t_j (it follows the running maximum once that is 8 above it) and a reference z of the scores,
+// value scale goes into the exponent: with t_j = s_j + ev_j, a reference m of those (the running maximum less
+// kKvAbove, once that is kKvLag above it) and a reference z of the scores,
 //   out = 2^(m - z) sum_j 2^(t_j - m) c_j / sum_j 2^(s_j - z),
 // so the weights of the codes stay within FP16 whatever the pages' scales are, and
 // nothing is multiplied into the values.  While the pages' |ev| are at most kKvTameExp, z is m and the sum below
-// takes 2^(t_j - m) 2^-ev, an exponential per key for both: it stays below 2^(48 + 30), and what 2^(t_j - m) loses
-// below 2^-126 is less than 2^-46 of the largest.  From the first page past that on, an item's share
+// takes 2^(t_j - m) 2^-ev, an exponential per key for both: it stays below 2^(55 + 30), and what 2^(t_j - m) loses
+// below 2^-126 is less than 2^-53 of the largest.  From the first page past that on, an item's share
 // has a z of its own, the scores' running maximum, and exponentials of its own for the sum.
 // The key scale is one factor of a tile's scores.  E4M3 codes and scaled query rows (a power of two per row) are exact in FP16
 // (elements below 2^-28 of a row's largest: to 2^-37 of that);
 // weights are rounded to FP16 (a relative 2^-11 each, against 2^-9 of a BF16
-// output), and all sums are FP32.
+// output; the row's largest is between 2^kKvAbove and 2^kKvLag, so that subnormal ones are off by 2^-32 of
+// it at most), and all sums are FP32.
 //
 // What bounds it: the cache is read once, about 2 x heads-per-kv-head operations
 // per byte, so DRAM.  Persistent blocks (one to three per SM) of four consumer warps and a
@@ -307,6 +308,7 @@ __device__ __forceinline__ bool kv_start(const KvAttnArgs& a, int blocks_per_sm,
 struct KvPageScale {
   float kfac, ev, inv;
 };
+constexpr float kKvAbove = 7.f, kKvLag = 15.f;  // 2^15 leaves FP16 a factor of 2
 constexpr float kKvTameExp = 40.f;
 // No such page, or |ev| above kKvTameExp, as one comparison of 2^-ev.
 __device__ __forceinline__ bool kv_special(const KvPageScale& ps) {
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
                 x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
                 x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
                 top[t][h] = x;
-                raise |= x > m[t][h] + 8.f;
+                raise |= x > m[t][h] + kKvLag;
               }
             }
             if constexpr (kWild) {
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
               for (int t = 0; t < NT; ++t) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const float mn = fmaxf(m[t][h], top[t][h]);
+                  const float mn = fmaxf(m[t][h], top[t][h] - kKvAbove);
                   const float f = m[t][h] == -INFINITY ? 0.f : fast_exp2(m[t][h] - mn);
                   m[t][h] = mn;
                   if constexpr (!kWild) l[t][h] *= f;

@@ -16,7 +16,7 @@
 // A second issuing warp: 529 against 511.  Products on a scheduler without a converter, its work spread over the
 // other three: 484 us, no gain.)
 //  * warps 0-3 and 4-7: the halves' softmax, a thread per row, 64 scores in registers.
-//    O is rescaled only where a row's maximum grew by more than 2^8.  They also bring the
+//    O is rescaled only where a row's maximum grew past 2^kKvLag of its reference.  They also bring the
 //    query rows (a power of two per row, so that they are exact in FP16) and write the output.
 //  * warps 8-11: E4M3 tiles to FP16 in the 128-byte-swizzled layout that both
 //    products read (K as rows of the dimension, V as rows of keys, the same bytes); keys outside the
@@ -459,8 +459,8 @@ __global__ void __launch_bounds__(kKpThreads, 1)
             const float top = masked ? kp_scores<true>(a, row, tile, slot, shift, first, key0, lo, hi, x)
                                      : kp_scores<false>(a, row, tile, slot, shift, first, key0, lo, hi, x);
             if constexpr (kWild) row.l = kp_wild_sum(row.l, row_z, slot, shift, first, x);
-            if (__any_sync(~0u, top > row.m + 8.f)) {
-              const float mn = fmaxf(row.m, top), f = row.m == -INFINITY ? 0.f : fast_exp2(row.m - mn);
+            if (__any_sync(~0u, top > row.m + kKvLag)) {
+              const float mn = fmaxf(row.m, top - kKvAbove), f = row.m == -INFINITY ? 0.f : fast_exp2(row.m - mn);
               row.m = mn;
               if constexpr (!kWild) row.l *= f;
               // O holds the keys before: wait for the last product (the one before it is done: these

@@ -101,3 +101,22 @@ def test_zero_keys_under_any_scale(bsq, group, new):
     case.cache[0][:] = case.rng.choice(np.array([0x00, 0x80], np.uint8), case.cache[0].shape)
     case.scales[0][:] = 254
     attend(bsq, case, 2 * group, 2.0 ** 100)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("group,new", ROWS)
+def test_one_heavy_key_and_a_flat_tail(bsq, group, new, dtype):
+    """A first key 26 ln 2 above all others, with values of 0: what is left comes from 4000 weights of 2^-26, of
+    which no more than 2^-32 of the first key's weight may be lost each.  Enough heads that a block meets many keys of one."""
+    heads = 152
+    case = Case([4000], [new], heads, 64, 64, seed=new, dtype=dtype)
+    case.cache[0][:] = 0
+    case.cache[0][case.table[0, 0], :, 0] = 0x38         # the first key: ones, all others zeros
+    case.cache[1][:] = 0x38
+    case.cache[1][case.table[0, 0], :, 0] = 0
+    for s in case.scales:
+        s[:] = 127
+    q = torch.full((new, heads * group, 64), 26 * np.log(2) / 8).to(torch.bfloat16 if dtype == "bf16" else torch.float16)
+    got = bsq.kv_attention(q.cuda(), *case.device(), new, return_lse=True)
+    expect = ref.attention(q.double().numpy(), *case.cache, *case.scales, case.table, case.offsets, case.lens, 1 / 8, True, 0)
+    close(case, *got, *expect, weight=2.0 ** -32)
