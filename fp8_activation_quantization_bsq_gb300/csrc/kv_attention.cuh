@@ -374,7 +374,8 @@ struct KvSum {
     wild = true;
   }
   __device__ __forceinline__ float stored() const { return wild ? -l : l; }
-  __device__ __forceinline__ float lse(float m) const { return l > 0.f ? ((wild ? z : m) + log2f(l)) * 0.6931471805599453f : -INFINITY; }
+  // 0: no key; NaN stays NaN.
+  __device__ __forceinline__ float lse(float m) const { return l == 0.f ? -INFINITY : ((wild ? z : m) + log2f(l)) * 0.6931471805599453f; }
 };
 
 // The codes of 4 consecutive dimensions of two keys -> for each dimension
@@ -841,7 +842,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
           for (int k = 0; k < 4; ++k) {
             const float wm = warp_m[k][r], wl = warp_l[k][r];
             below.wild |= wl < 0.f;
-            below.l += wm == -INFINITY ? 0.f : wl * fast_exp2(wm - am);
+            below.l += wl * (wm == -INFINITY ? 0.f : fast_exp2(wm - am));  // a NaN stays
           }
 #pragma unroll(16 / kOwn)
           for (int p = 0; p < near + far; ++p) {

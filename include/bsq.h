@@ -482,7 +482,7 @@ BSQ_API int32_t bsq_kv_append(int32_t dtype, const void* k_dev, const void* v_de
  *                     leaves its counters zeroed again (after a reported BSQ_ERR_TIMEOUT
  *                     it has to be zeroed anew).  Calls sharing it must not overlap.
  *   total             total * heads / kv_heads <= 2^30.
- * A row without an allowed key gets zeros and -inf.  What the cache holds
+ * A row without an allowed key gets zeros and -inf, a row with NaN in q gets NaN in both.  What the cache holds
  * beyond a sequence's length, or outside the allowed keys, does not matter.
  * Rows of q that belong to no sequence are left as they are.  A softmax
  * weight enters its product with the values as FP16; scores, sums and

@@ -120,3 +120,20 @@ def test_one_heavy_key_and_a_flat_tail(bsq, group, new, dtype):
     got = bsq.kv_attention(q.cuda(), *case.device(), new, return_lse=True)
     expect = ref.attention(q.double().numpy(), *case.cache, *case.scales, case.table, case.offsets, case.lens, 1 / 8, True, 0)
     close(case, *got, *expect, weight=2.0 ** -32)
+
+
+@pytest.mark.parametrize("group,new", ROWS)
+@pytest.mark.parametrize("length", [90, 5000])
+def test_nan_query_rows_stay_nan(bsq, group, new, length):
+    """The output and the lse of such a row are NaN (an lse of -inf marks a row without keys); other rows do not change."""
+    case = Case([length, 40], [new, new], 1, 128, 64, seed=new)
+    q, _ = case.rows(group)
+    expect, lse = bsq.kv_attention(q, *case.device(), new, return_lse=True)
+    bad = q.clone()
+    bad[0, 0] = float("nan")
+    bad[-1, -1, 5] = float("nan")
+    got, got_lse = bsq.kv_attention(bad, *case.device(), new, return_lse=True)
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    hit[0, 0] = hit[-1, -1] = True
+    assert got[hit].isnan().all() and got_lse[hit].isnan().all()
+    assert torch.equal(got[~hit], expect[~hit]) and torch.equal(got_lse[~hit], lse[~hit])
