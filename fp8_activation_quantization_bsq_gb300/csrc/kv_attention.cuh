@@ -34,12 +34,9 @@
 // per kv head 100 us, 6.1 TB/s or 90 % of a plain copy; 16 rows 116 us and 32 rows 237 us, where
 // the conversions and mma.sync products bound it.  One context of 777: 10.3 us, a chain of
 // latencies (lengths, table, codes, the join); two of 131072, 4 kv heads: 53 us.
-// An item cut by the runs is finished by the block that began it, which adds the other blocks' parts
-// in block order (first in groups where there are many): those blocks hold them at the start of
-// their runs, it at the end of its own.  A block waits only for blocks after it, and for the first
-// thing they do: of those on the GPU at most the last one, its group's first and its item's first
-// wait for one that is not there yet, and all others leave and make room.  So the launch needs
-// not be cooperative (the grid fits an idle GPU at once; other work on it only delays).
+// An item cut by the runs is joined from its blocks' parts, in block order, by whichever block stores its part last
+// (first in groups where there are many).  So no block waits for another, whether it is on the GPU yet or not, and
+// the sums' order does not depend on which one is last.
 #pragma once
 
 #include <type_traits>
@@ -49,14 +46,17 @@
 namespace bsq {
 
 constexpr int kKvTile = 64;       // keys per unit
-constexpr int kKvMaxBlocks = 1024;
+constexpr int kKvMaxBlocks = 512;
 constexpr int kKvMinRun = 3;      // units of a run, at least, once every SM has one
-// Parts of an item that one block joins by itself, and the size of the groups
+// Parts of an item that are joined at once, and the size of the groups
 // that are joined first where there are more: about their number's square root.  (104 parts, one
 // context of 20000 with one kv head: 16.3 us, 25.6 when one block joins them all; 57 parts of
 // contexts of 131072: 53.3 / 53.9, and 53.2 to 54.7 for groups of 5 to 20.)
 __device__ __forceinline__ int kv_join_group(int parts) { return parts <= 20 ? parts : parts <= 72 ? 8 : 16; }
-constexpr int kKvCounterBytes = 4 * kKvMaxBlocks;
+// Parts stored so far, zero between calls: of a group (by its first block, which can be the first of one item and of
+// a later group of the item before), of an item's groups (by the item's first block).
+constexpr int kKvGroupCounters = 0, kKvLaterCounters = kKvMaxBlocks, kKvItemCounters = 2 * kKvMaxBlocks;
+constexpr int kKvCounterBytes = 4 * 3 * kKvMaxBlocks;
 
 struct KvAttnArgs {
   const uint16_t* q;              // (total, heads, D)
@@ -74,8 +74,8 @@ struct KvAttnArgs {
   // takes the one, a page's the other, so that neither product loses bits below FP32's normal numbers
   float scale_pow, scale_sig;
   uint64_t group_inv;             // ceil(2^64 / group), for kv_token
-  uint32_t* ready;                // [block] part stored, zero between calls
-  float* part;                    // [block][rows * D + 3 * rows]: sums, m, sums below, z
+  uint32_t* arrived;              // counters
+  float* part;                    // [block][first of the item, later][rows * D + 3 * rows]: sums, m, sums below, z
   unsigned int* err;
 };
 
@@ -396,13 +396,38 @@ __device__ __forceinline__ uint32_t kv_chunk(int r, int c) {
   return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Wait for a block's part, for about a second, and take the flag down.
-__device__ __forceinline__ bool kv_take_part(uint32_t* flag, const volatile uint32_t* abort_flag) {
-  const long long t0 = clock64();
-  while (ld_acquire(flag) == 0u)
-    if (*abort_flag != 0u || clock64() - t0 > kWaitLimitCycles) return false;
-  *flag = 0u;
-  return true;
+// Where an item's blocks meet: block own0 + i is its i-th of `count`, in groups of `join`.
+struct KvJoin {
+  int own0, me, count, join;
+  __device__ __forceinline__ KvJoin(const KvStart& start, int64_t first, int64_t units) {
+    own0 = start.owner(first);
+    me = static_cast<int>(blockIdx.x) - own0;
+    count = start.owner(first + units - 1) - own0 + 1;
+    join = kv_join_group(count);
+  }
+  __device__ __forceinline__ int head() const { return me / join * join; }
+  __device__ __forceinline__ int members() const { return min(join, count - head()); }
+  __device__ __forceinline__ int groups() const { return (count - 1) / join + 1; }
+  __device__ __forceinline__ float* part(const KvAttnArgs& a, int i, int floats) const {
+    return a.part + (2 * static_cast<int64_t>(own0 + i) + (i > 0 ? 1 : 0)) * floats;
+  }
+  __device__ __forceinline__ uint32_t* group_counter(const KvAttnArgs& a) const {
+    return a.arrived + (head() > 0 ? kKvLaterCounters : kKvGroupCounters) + own0 + head();
+  }
+  __device__ __forceinline__ uint32_t* item_counter(const KvAttnArgs& a) const { return a.arrived + kKvItemCounters + own0; }
+};
+
+// `threads` threads of a block, whose parts are stored, meet at barrier `id`; true if theirs is the last of n
+// (then all n can be read and the counter is 0 again).
+__device__ __forceinline__ bool kv_arrive(uint32_t* counter, int n, int id, int threads, bool first, volatile uint32_t* last) {
+  named_sync(id, threads);
+  if (first) {
+    const bool is_last = atomic_add_acq_rel(counter, 1u) == static_cast<uint32_t>(n) - 1u;
+    if (is_last) *counter = 0u;
+    *last = is_last ? 1u : 0u;
+  }
+  named_sync(id, threads);
+  return *last != 0u;
 }
 
 // An 8 x 8 matrix of 16-bit elements over the warp, transposed.
@@ -429,7 +454,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
   __shared__ KvWalk<RT, kKvTile> walks[S::kWarps + 1];
   __shared__ KvStart start;
   __shared__ int64_t warp_sum[S::kWarps + 1];
-  __shared__ volatile uint32_t abort_flag, fills, used_tiles, go_on, joined;
+  __shared__ volatile uint32_t abort_flag, fills, used_tiles, go_on, last;
 
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   if (tid == 0) {
@@ -773,12 +798,38 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
       named_sync(1, kT);
       if (tid == 0) go_on = abort_flag == 0u ? 1u : 0u;  // one answer for all warps
       const int live = min(RT, rows - g.rt * RT);  // rows of the tile
-      const int own0 = start.owner(g.first), own1 = start.owner(g.first + g.count - 1);
-      const int me = static_cast<int>(blockIdx.x) - own0, count = own1 - own0 + 1;
-      // parts of the group's other blocks, then (the item's first block) of the other groups' first blocks
-      const int join = kv_join_group(count);
-      const int near = me % join == 0 ? min(join, count - me) - 1 : 0, far = me == 0 ? (count - 1) / join : 0;
-      float* mine = a.part + static_cast<int64_t>(blockIdx.x) * S::kPartFloats;
+      const KvJoin team(start, g.first, g.count);
+      // kTpr threads per row, float4s kTpr i + tid % kTpr of it
+      constexpr int kTpr = kT / S::kPassRows, kOwn = D / 4 / kTpr;
+      const int rl = tid / kTpr, d4 = tid % kTpr;
+      // Row r of the tile to a part, or where there is none to the output.
+      const auto put = [&](int r, float4 (&acc)[kOwn], float am, const KvSum& below, float* part) {
+        if (part != nullptr) {
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i) __stcg(reinterpret_cast<float4*>(part + r * D) + kTpr * i + d4, acc[i]);
+          if (d4 == 0) {
+            __stcg(part + RT * D + r, am);
+            __stcg(part + RT * D + RT + r, below.stored());
+            if (below.wild) __stcg(part + RT * D + 2 * RT + r, below.z);
+          }
+          return;
+        }
+        const int rr = g.rt * RT + r;
+        const int tok = kv_token(a, rr);
+        const int64_t row = static_cast<int64_t>(g.s.t0 + tok) * a.heads + g.head * a.group + rr - tok * a.group;
+        float f = below.l > 0.f ? 1.f / below.l : 0.f;
+        if (below.wild) {  // 2^(m - z) in two steps: the whole may pass FP32 where the output does not
+          const float half = fast_exp2(0.5f * (am - below.z));
+          f *= half;
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i) acc[i] = make_float4(acc[i].x * half, acc[i].y * half, acc[i].z * half, acc[i].w * half);
+        }
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i)
+          *reinterpret_cast<uint2*>(a.out + row * D + 4 * (kTpr * i + d4)) =
+              make_uint2(f32x2_to_elem2<F16>(acc[i].x * f, acc[i].y * f), f32x2_to_elem2<F16>(acc[i].z * f, acc[i].w * f));
+        if (d4 == 0 && a.lse != nullptr) a.lse[row] = below.lse(am);
+      };
 #pragma unroll
       for (int pass = 0; pass < RT / S::kPassRows; ++pass) {
         if (pass > 0) named_sync(1, kT);  // the buffer has been read
@@ -802,27 +853,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
         }
         named_sync(1, kT);
         ok = go_on != 0u;
-        if (ok && pass == 0 && near + far > 0) {
-          if (warp == 0) {
-            bool got = true;
-            for (int p = lane; p < near + far && got; p += 32)
-              got = kv_take_part(a.ready + blockIdx.x + (p < near ? 1 + p : join * (p - near + 1)), &abort_flag);
-            got = __all_sync(~0u, got);
-            if (lane == 0) {
-              if (!got) {
-                if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
-                abort_flag = 1u;
-              }
-              joined = got ? 1u : 0u;
-            }
-          }
-          named_sync(1, kT);
-          if (joined == 0u) go_on = 0u;  // every thread, the same
-          ok = joined != 0u;
-        }
-        // kTpr threads per row, float4s kTpr i + tid % kTpr of it
-        constexpr int kTpr = kT / S::kPassRows, kOwn = D / 4 / kTpr;
-        const int rl = tid / kTpr, r = pass * S::kPassRows + rl, d4 = tid % kTpr;
+        const int r = pass * S::kPassRows + rl;
         if (ok && r < live) {
           float4 acc[kOwn];
 #pragma unroll
@@ -844,63 +875,60 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
             below.wild |= wl < 0.f;
             below.l += wl * (wm == -INFINITY ? 0.f : fast_exp2(wm - am));  // a NaN stays
           }
-#pragma unroll(16 / kOwn)
-          for (int p = 0; p < near + far; ++p) {
-            const float* part = mine + static_cast<int64_t>(p < near ? 1 + p : join * (p - near + 1)) * S::kPartFloats;
-            float4 v[kOwn];
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(part + r * D) + kTpr * i + d4);
-            const float pm = __ldcg(part + RT * D + r), pl = __ldcg(part + RT * D + RT + r);
-            const float mm = fmaxf(am, pm);
-            const float f0 = am == -INFINITY ? 0.f : fast_exp2(am - mm), f1 = pm == -INFINITY ? 0.f : fast_exp2(pm - mm);
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i)
-              acc[i] = make_float4(acc[i].x * f0 + v[i].x * f1, acc[i].y * f0 + v[i].y * f1, acc[i].z * f0 + v[i].z * f1,
-                                   acc[i].w * f0 + v[i].w * f1);
-            below.wild |= pl < 0.f;
-            below.l = below.l * f0 + pl * f1;
-            am = mm;
-          }
           if (below.wild) {  // the sum again, with every z
             below = KvSum{};
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) below.add_wild(warp_m[k][r], warp_l[k][r], warp_z[k][r]);
-#pragma unroll 1
-            for (int p = 0; p < near + far; ++p) {
-              const float* part = mine + static_cast<int64_t>(p < near ? 1 + p : join * (p - near + 1)) * S::kPartFloats + RT * D + r;
-              below.add_wild(__ldcg(part), __ldcg(part + RT), __ldcg(part + 2 * RT));
-            }
           }
-          if (me != 0) {
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i) __stcg(reinterpret_cast<float4*>(mine + r * D) + kTpr * i + d4, acc[i]);
-            if (d4 == 0) {
-              __stcg(mine + RT * D + r, am);
-              __stcg(mine + RT * D + RT + r, below.stored());
-              if (below.wild) __stcg(mine + RT * D + 2 * RT + r, below.z);
-            }
-          } else {
-            const int rr = g.rt * RT + r;
-            const int tok = kv_token(a, rr);
-            const int64_t row = static_cast<int64_t>(g.s.t0 + tok) * a.heads + g.head * a.group + rr - tok * a.group;
-            float f = below.l > 0.f ? 1.f / below.l : 0.f;
-            if (below.wild) {  // 2^(m - z) in two steps: the whole may pass FP32 where the output does not
-              const float half = fast_exp2(0.5f * (am - below.z));
-              f *= half;
-#pragma unroll
-              for (int i = 0; i < kOwn; ++i) acc[i] = make_float4(acc[i].x * half, acc[i].y * half, acc[i].z * half, acc[i].w * half);
-            }
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i)
-              *reinterpret_cast<uint2*>(a.out + row * D + 4 * (kTpr * i + d4)) =
-                  make_uint2(f32x2_to_elem2<F16>(acc[i].x * f, acc[i].y * f), f32x2_to_elem2<F16>(acc[i].z * f, acc[i].w * f));
-            if (d4 == 0 && a.lse != nullptr) a.lse[row] = below.lse(am);
-          }
+          put(r, acc, am, below, team.count > 1 ? team.part(a, team.me, S::kPartFloats) : nullptr);
         }
       }
-      if (ok && me != 0) {
-        named_sync(1, kT);
-        if (tid == 0) st_release(a.ready + blockIdx.x, 1u);
+      if (ok && team.count > 1) {
+        // n parts, from part i0 on every step-th, into one or the output
+        const auto join_parts = [&](int i0, int step, int n, float* to) {
+#pragma unroll 1
+          for (int r = rl; r < RT; r += S::kPassRows) {
+            const uint32_t mask = __ballot_sync(~0u, r < live);
+            if (r >= live) continue;
+            float4 acc[kOwn];
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            KvSum below;
+            float am = -INFINITY;
+#pragma unroll(16 / kOwn)
+            for (int p = 0; p < n; ++p) {
+              const float* part = team.part(a, i0 + p * step, S::kPartFloats);
+              float4 v[kOwn];
+#pragma unroll
+              for (int i = 0; i < kOwn; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(part + r * D) + kTpr * i + d4);
+              const float pm = __ldcg(part + RT * D + r), pl = __ldcg(part + RT * D + RT + r);
+              const float mm = fmaxf(am, pm);
+              const float f0 = am == -INFINITY ? 0.f : fast_exp2(am - mm), f1 = pm == -INFINITY ? 0.f : fast_exp2(pm - mm);
+#pragma unroll
+              for (int i = 0; i < kOwn; ++i)
+                acc[i] = make_float4(acc[i].x * f0 + v[i].x * f1, acc[i].y * f0 + v[i].y * f1, acc[i].z * f0 + v[i].z * f1,
+                                     acc[i].w * f0 + v[i].w * f1);
+              below.wild |= pl < 0.f;
+              below.l = below.l * f0 + pl * f1;
+              am = mm;
+            }
+            if (below.wild) {
+              below = KvSum{};
+#pragma unroll 1
+              for (int p = 0; p < n; ++p) {
+                const float* part = team.part(a, i0 + p * step, S::kPartFloats) + RT * D + r;
+                below.add_wild(__ldcg(part), __ldcg(part + RT), __ldcg(part + 2 * RT));
+              }
+            }
+            __syncwarp(mask);  // the row's threads, all in this warp, have read what put may replace
+            put(r, acc, am, below, to);
+          }
+        };
+        const int head = team.head(), groups = team.groups();
+        if (kv_arrive(team.group_counter(a), team.members(), 1, kT, tid == 0, &last)) {
+          join_parts(head, 1, team.members(), groups > 1 ? team.part(a, head, S::kPartFloats) : nullptr);
+          if (groups > 1 && kv_arrive(team.item_counter(a), groups, 1, kT, tid == 0, &last)) join_parts(0, team.join, groups, nullptr);
+        }
       }
       // the merge buffer and the flags are written again only after the first
       // barrier of the next item's end, which all threads reach after this

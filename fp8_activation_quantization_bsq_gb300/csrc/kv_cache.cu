@@ -152,9 +152,9 @@ int64_t bsq_kv_attention_workspace_bytes(int64_t total, int32_t heads, int32_t k
   if (total < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || (dim != 64 && dim != 128) || batch < 0 || max_q < 0)
     return 0;
   if (static_cast<int64_t>(max_q) * (heads / kv_heads) > kKvFewRows)
-    return kKvCounterBytes + int64_t(kKpMaxBlocks) * (dim == 64 ? KpShape<64>::kPartFloats : KpShape<128>::kPartFloats) * 4;
-  // a part of 16 rows for each of the blocks, or of 32 for half as many
-  return kKvCounterBytes + int64_t(kKvMaxBlocks) * KvShape<128, 2>::kPartFloats * 4;
+    return kKvCounterBytes + 2 * int64_t(kKpMaxBlocks) * (dim == 64 ? KpShape<64>::kPartFloats : KpShape<128>::kPartFloats) * 4;
+  // two parts of 16 rows for each of the blocks, or of 32 for half as many
+  return kKvCounterBytes + 2 * int64_t(kKvMaxBlocks) * KvShape<128, 2>::kPartFloats * 4;
 }
 
 int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t heads, int32_t kv_heads, int32_t dim,
@@ -208,7 +208,7 @@ int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t he
   const float significand = std::frexp(scale, &exponent);  // 0, or in [1/2, 1)
   a.scale_sig = 2.f * significand;
   a.scale_pow = std::copysign(std::ldexp(1.f, exponent - 1), sm_scale);
-  a.ready = static_cast<uint32_t*>(workspace);
+  a.arrived = static_cast<uint32_t*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKvCounterBytes);
   a.err = d.error_word;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

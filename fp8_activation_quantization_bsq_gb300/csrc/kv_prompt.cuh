@@ -32,7 +32,7 @@ constexpr int kKpKeys = 128, kKpRows = 256, kKpThreads = 448;
 constexpr int kKpSub = 64;              // keys of an S tile
 constexpr int kKpRaw = 4, kKpWide = 3;  // rings of E4M3 and FP16 tiles: K, V, K, V, ...
 constexpr int kKpSlots = 8;             // units whose page scales are kept
-constexpr int kKpMaxBlocks = 256;
+constexpr int kKpMaxBlocks = 160;
 
 template <int D>
 struct KpShape {
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
   __shared__ volatile uint32_t more[2];
   __shared__ int64_t warp_sum[kKpThreads / 32];
   __shared__ uint32_t tmem_slot;
-  __shared__ volatile uint32_t abort_flag, fills, used_tiles, joined;
+  __shared__ volatile uint32_t abort_flag, fills, used_tiles, go_on, last;
 
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   if (tid == 0) {
@@ -390,8 +390,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const uint32_t ts = lanes + 128 * half, to = lanes + 256 + 128 * half;
     const int shift = min(a.page_shift, 7);
-    float* const mine = a.part + static_cast<int64_t>(blockIdx.x) * S::kPartFloats;
-    float* const row_z = mine + kKpRows * D + 3 * kKpRows + r_tile;
+    float* const row_z = a.part + 2 * static_cast<int64_t>(blockIdx.x) * S::kPartFloats + kKpRows * D + 3 * kKpRows + r_tile;
     uint32_t unit = 0, k = 0, finished = 0;
     bool ok = true;
     while (walk.step_together(a, 1, 256, tid == 0, &more[0], &abort_flag)) {
@@ -504,86 +503,90 @@ __global__ void __launch_bounds__(kKpThreads, 1)
       }
       if (!ok && lane == 0) fail();
       // ---- the item's share
-      const int own0 = start.owner(g.first), own1 = start.owner(g.first + g.count - 1);
-      const int me = static_cast<int>(blockIdx.x) - own0, count = own1 - own0 + 1;
-      const int join = kv_join_group(count);
-      const int near = me % join == 0 ? min(join, count - me) - 1 : 0, far = me == 0 ? (count - 1) / join : 0;
+      const KvJoin team(start, g.first, g.count);
       named_sync(1, 256);
-      if (warp == 0) {
-        bool got = abort_flag == 0u;
-        got = __shfl_sync(~0u, got ? 1 : 0, 0) != 0;
-        for (int p = lane; p < near + far && got; p += 32)
-          got = kv_take_part(a.ready + blockIdx.x + (p < near ? 1 + p : join * (p - near + 1)), &abort_flag);
-        got = __all_sync(~0u, got);
-        if (lane == 0) {
-          if (!got) fail();
-          joined = got ? 1u : 0u;
-        }
+      if (tid == 0) {
+        // the group's first block is its last to arrive as a rule: it then need not store its own part
+        const bool direct = team.count > 1 && team.me == team.head() &&
+                            ld_acquire(team.group_counter(a)) == static_cast<uint32_t>(team.members()) - 1u;
+        go_on = abort_flag != 0u ? 0u : direct ? 2u : 1u;
+        if (go_on == 2u) *team.group_counter(a) = 0u;
       }
       named_sync(1, 256);
-      ok = joined != 0u;  // one answer for all warps
-      if (ok && half_rows > 0) {  // uniform per warp
-        const auto part_of = [&](int p) { return mine + static_cast<int64_t>(p < near ? 1 + p : join * (p - near + 1)) * S::kPartFloats; };
-        KvSum below{fabsf(row.l), row.l < 0.f ? *row_z : row.m, row.l < 0.f};
-        float am = row.m;
-        for (int p = 0; p < near + far; ++p) {
-          const float pm = row.live ? __ldcg(part_of(p) + kKpRows * D + r_tile) : -INFINITY;
-          const float pl = row.live ? __ldcg(part_of(p) + kKpRows * D + kKpRows + r_tile) : 0.f;
+      ok = go_on != 0u;  // one answer for all warps
+      const bool direct = go_on == 2u;
+      // 32 dimensions of this thread's row, and its sum, to a part, or where there is none to the output
+      const auto put = [&](int c, const float (&x)[32], float am, const KvSum& below, float* part) {
+        if (part != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) __stcg(part + (c + i) * kKpRows + r_tile, x[i]);
+          if (c == 0) {
+            __stcg(part + kKpRows * D + r_tile, am);
+            __stcg(part + kKpRows * D + kKpRows + r_tile, below.stored());
+            if (below.wild) __stcg(part + kKpRows * D + 2 * kKpRows + r_tile, below.z);
+          }
+          return;
+        }
+        // a wild sum's 2^(m - z) in two steps: the whole may pass FP32 where the output does not
+        const float half = below.wild ? fast_exp2(0.5f * (am - below.z)) : 1.f, inv = below.l > 0.f ? half / below.l : 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+          *reinterpret_cast<uint4*>(a.out + out_row * D + c + i) =
+              make_uint4(f32x2_to_elem2<F16>(x[i] * inv * half, x[i + 1] * inv * half),
+                         f32x2_to_elem2<F16>(x[i + 2] * inv * half, x[i + 3] * inv * half),
+                         f32x2_to_elem2<F16>(x[i + 4] * inv * half, x[i + 5] * inv * half),
+                         f32x2_to_elem2<F16>(x[i + 6] * inv * half, x[i + 7] * inv * half));
+        if (c == 0 && a.lse != nullptr) a.lse[out_row] = below.lse(am);
+      };
+      const int head = team.head(), groups = team.groups();
+      const bool whole = team.count == 1 || direct;
+      // Three steps, as far as they are this block's: its own rows (with the group's other parts, where they are there),
+      // the group's parts, the groups' parts.  Each takes n of them, from part i0 on every step-th, to a part or
+      // the output; a row's thread reads and writes it alone.  Own rows come from tensor memory and are the
+      // first of their group: the same operations on the same numbers as from a part.
+#pragma unroll 1
+      for (int level = whole ? 0 : -1; ok && level < (groups > 1 ? 2 : 1); ++level) {
+        const bool own = level < 0 || (level == 0 && whole), top = level == 1;
+        const int i0 = top ? 0 : head, step = top ? team.join : 1, n = level < 0 ? 1 : top ? groups : team.members();
+        float* const to_part = level < 0 ? team.part(a, team.me, S::kPartFloats) : !top && groups > 1 ? team.part(a, head, S::kPartFloats) : nullptr;
+        if (!own && !kv_arrive(top ? team.item_counter(a) : team.group_counter(a), n, 1, 256, tid == 0, &last)) break;
+        if (half_rows <= 0) continue;  // uniform per warp
+        const int p0 = own ? 1 : 0, p1 = row.live ? n : 0;
+        const auto part_of = [&](int p) { return team.part(a, i0 + p * step, S::kPartFloats) + r_tile; };
+        KvSum below;
+        float am = -INFINITY;
+        if (own) {
+          below = KvSum{fabsf(row.l), row.l < 0.f ? *row_z : row.m, row.l < 0.f};
+          am = row.m;
+        }
+        for (int p = p0; p < p1; ++p) {
+          const float pm = __ldcg(part_of(p) + kKpRows * D), pl = __ldcg(part_of(p) + kKpRows * D + kKpRows);
           const float mm = fmaxf(am, pm);
           if (below.wild || pl < 0.f) {
             if (!below.wild) below.z = am;
-            below.add_wild(pm, pl, __ldcg(part_of(p) + kKpRows * D + 2 * kKpRows + r_tile));
+            below.add_wild(pm, pl, __ldcg(part_of(p) + kKpRows * D + 2 * kKpRows));
           } else {
             below.l = below.l * (am == -INFINITY ? 0.f : fast_exp2(am - mm)) + pl * (pm == -INFINITY ? 0.f : fast_exp2(pm - mm));
           }
           am = mm;
         }
         const float f0 = row.m == -INFINITY ? 0.f : fast_exp2(row.m - am);
-        // a wild sum's 2^(m - z) in two steps: the whole may pass FP32 where the output does not
-        const float half = below.wild ? fast_exp2(0.5f * (am - below.z)) : 1.f, inv = below.l > 0.f ? half / below.l : 0.f;
+        __syncwarp();  // tensor-memory loads want the whole warp
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = D - 32; c >= 0; c -= 32) {  // the maxima are read in every round and replaced in the last
           float x[32];
-          if (busy) t5_ld32(to + c, x);
+          if (own && busy) t5_ld32(to + c, x);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = busy ? x[i] * f0 : 0.f;
-          for (int p = 0; p < near + far; ++p) {
-            const float pm = row.live ? __ldcg(part_of(p) + kKpRows * D + r_tile) : -INFINITY;
-            const float f1 = pm == -INFINITY ? 0.f : fast_exp2(pm - am);
-            if (row.live) {
+          for (int i = 0; i < 32; ++i) x[i] = own && busy ? x[i] * f0 : 0.f;
+          for (int p = p0; p < p1; ++p) {
+            const float pm = __ldcg(part_of(p) + kKpRows * D), f = pm == -INFINITY ? 0.f : fast_exp2(pm - am);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = fmaf(f1, __ldcg(part_of(p) + (c + i) * kKpRows + r_tile), x[i]);
-            }
+            for (int i = 0; i < 32; ++i) x[i] = fmaf(f, __ldcg(part_of(p) + (c + i) * kKpRows), x[i]);
           }
-          if (row.live) {
-            if (me != 0) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) __stcg(mine + (c + i) * kKpRows + r_tile, x[i]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                *reinterpret_cast<uint4*>(a.out + out_row * D + c + i) =
-                    make_uint4(f32x2_to_elem2<F16>(x[i] * inv * half, x[i + 1] * inv * half),
-                               f32x2_to_elem2<F16>(x[i + 2] * inv * half, x[i + 3] * inv * half),
-                               f32x2_to_elem2<F16>(x[i + 4] * inv * half, x[i + 5] * inv * half),
-                               f32x2_to_elem2<F16>(x[i + 6] * inv * half, x[i + 7] * inv * half));
-            }
-          }
-        }
-        if (row.live) {
-          if (me != 0) {
-            __stcg(mine + kKpRows * D + r_tile, am);
-            __stcg(mine + kKpRows * D + kKpRows + r_tile, below.stored());
-            if (below.wild) __stcg(mine + kKpRows * D + 2 * kKpRows + r_tile, below.z);
-          } else if (a.lse != nullptr) {
-            a.lse[out_row] = below.lse(am);
-          }
+          if (row.live) put(c, x, am, below, to_part);
+          __syncwarp();
         }
         t5_fence_before();
-      }
-      if (ok && me != 0) {
-        named_sync(1, 256);
-        if (tid == 0) st_release(a.ready + blockIdx.x, 1u);
       }
     }
   }
