@@ -56,7 +56,9 @@ __device__ __forceinline__ int kv_join_group(int parts) { return parts <= 20 ? p
 // Parts stored so far, zero between calls: of a group (by its first block, which can be the first of one item and of
 // a later group of the item before), of an item's groups (by the item's first block).
 constexpr int kKvGroupCounters = 0, kKvLaterCounters = kKvMaxBlocks, kKvItemCounters = 2 * kKvMaxBlocks;
-constexpr int kKvCounterBytes = 4 * 3 * kKvMaxBlocks;
+// Not 0 once a call has given up in a wait: what else the workspace holds is then not to be trusted.
+constexpr int kKvSpoiled = 3 * kKvMaxBlocks;
+constexpr int kKvCounterBytes = 4 * (3 * kKvMaxBlocks + 4);
 
 struct KvAttnArgs {
   const uint16_t* q;              // (total, heads, D)
@@ -74,7 +76,7 @@ struct KvAttnArgs {
   // takes the one, a page's the other, so that neither product loses bits below FP32's normal numbers
   float scale_pow, scale_sig;
   uint64_t group_inv;             // ceil(2^64 / group), for kv_token
-  uint32_t* arrived;              // counters
+  uint32_t* arrived;              // counters, and whether they hold
   float* part;                    // [block][first of the item, later][rows * D + 3 * rows]: sums, m, sums below, z
   unsigned int* err;
 };
@@ -263,11 +265,13 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
 }
 
 // Sum every sequence's units and find this block's run (by all THREADS of the
-// block, a thread taking consecutive sequences); false for a block without one.
+// block, a thread taking consecutive sequences); false for a block without one, or in a
+// workspace that an earlier call spoiled.
 template <int RT, int TILE, int THREADS>
-__device__ __forceinline__ bool kv_start(const KvAttnArgs& a, int blocks_per_sm, int64_t* warp_sum, KvStart* start) {
+__device__ __forceinline__ bool kv_start(const KvAttnArgs& a, int blocks_per_sm, int64_t* warp_sum, uint32_t* spoiled, KvStart* start) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.batch + THREADS - 1) / THREADS, b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
+  const uint32_t word = tid == 0 ? __ldcg(a.arrived + kKvSpoiled) : 0u;  // under way beside the lengths
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) mine += kv_seq_units<RT, TILE>(a, kv_seq<RT>(a, b, blockIdx.x == 0)) * a.kv_heads;
   int64_t sum = mine;
@@ -277,7 +281,12 @@ __device__ __forceinline__ bool kv_start(const KvAttnArgs& a, int blocks_per_sm,
     if (lane >= d) sum += o;
   }
   if (lane == 31) warp_sum[warp] = sum;
+  if (tid == 0) *spoiled = word;
   __syncthreads();
+  if (*spoiled != 0u) {
+    if (tid == 0) record_error_at(a.err, kErrTimeout);
+    return false;
+  }
   KvStart s;
   s.total = 0;
 #pragma unroll 1
@@ -454,6 +463,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
   __shared__ KvWalk<RT, kKvTile> walks[S::kWarps + 1];
   __shared__ KvStart start;
   __shared__ int64_t warp_sum[S::kWarps + 1];
+  __shared__ uint32_t spoiled;
   __shared__ volatile uint32_t abort_flag, fills, used_tiles, go_on, last;
 
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
@@ -472,7 +482,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
   pdl_wait();
   KvWalk<RT, kKvTile>& walk = walks[warp];
   const KvSegment& g = walk.seg;
-  if (!kv_start<RT, kKvTile, S::kThreads>(a, S::kBlocksPerSm, warp_sum, &start)) return;  // the whole block
+  if (!kv_start<RT, kKvTile, S::kThreads>(a, S::kBlocksPerSm, warp_sum, &spoiled, &start)) return;  // the whole block
   walk.begin(a, start, lane == 0);
 
   if (warp == S::kWarps) {
@@ -937,6 +947,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
   }
   __syncthreads();
   // after an expired wait: loads that nothing consumed land before the block ends
+  if (tid == 0 && abort_flag != 0u) a.arrived[kKvSpoiled] = 1u;
   if (tid == 0)
     for (uint32_t f = used_tiles; f < fills; ++f)
       if (!mbar_wait_clocked(&full_bar[f % S::kStages], (f / S::kStages) & 1u)) record_error_at(a.err, kErrTimeout);

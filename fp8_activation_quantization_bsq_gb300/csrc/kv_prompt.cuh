@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
   __shared__ KvWalk<kKpRows, kKpKeys> walks[4];
   __shared__ volatile uint32_t more[2];
   __shared__ int64_t warp_sum[kKpThreads / 32];
-  __shared__ uint32_t tmem_slot;
+  __shared__ uint32_t tmem_slot, spoiled;
   __shared__ volatile uint32_t abort_flag, fills, used_tiles, go_on, last;
 
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
     prefetch_tensormap(&map_v);
   }
   pdl_wait();
-  if (!kv_start<kKpRows, kKpKeys, kKpThreads>(a, 1, warp_sum, &start)) return;  // the whole block
+  if (!kv_start<kKpRows, kKpKeys, kKpThreads>(a, 1, warp_sum, &spoiled, &start)) return;  // the whole block
   if (warp == 13) t5_alloc(&tmem_slot, 512);
   t5_fence_before();
   __syncthreads();
@@ -592,6 +592,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
   }
   __syncthreads();
   // after an expired wait: loads that nothing consumed land before the block ends
+  if (tid == 0 && abort_flag != 0u) a.arrived[kKvSpoiled] = 1u;
   if (tid == 0)
     for (uint32_t f = used_tiles; f < fills; ++f)
       if (!mbar_wait_clocked(&raw_full[f % kKpRaw], f / kKpRaw & 1u)) record_error_at(a.err, kErrTimeout);

@@ -48,7 +48,8 @@ constexpr int kMoeQuantThreads = 256;      // warps 4-11 quantize the tokens and
 constexpr int kMoeHalfBytes = 128 * 128;  // a stage's 128 rows x 128 bytes of one tile half
 constexpr int kMoeMaxBlocks = 512;
 // counters at the start of the workspace, zero between calls
-constexpr int kMoeBarQuant = 0, kMoeBarDone = 32, kMoeBarExit = 64, kMoePartReady = 96,
+// (kMoeSpoiled: not 0 once a call has given up in a wait; what else the workspace holds is then not to be trusted)
+constexpr int kMoeBarQuant = 0, kMoeBarDone = 32, kMoeBarExit = 64, kMoeSpoiled = 80, kMoePartReady = 96,
               kMoeExpertDone = kMoePartReady + 2 * kMoeMaxBlocks;
 constexpr int kMoeCounterBytes = 4 * (kMoeExpertDone + 1024);
 
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full_bar[8], empty_bar[8], acc_full[2], acc_empty[2], drain_bar;
-  __shared__ uint32_t tmem_slot, last_flag;
+  __shared__ uint32_t tmem_slot, last_flag, spoiled;
   __shared__ volatile uint32_t abort_flag, fills_a, fills_b, consumed;
   __shared__ int active_count;
   __shared__ uint32_t warp_sum[kMoeThreads / 32];
@@ -383,12 +384,19 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   if (warp >= 4) moe_load_x(a, quant_at, quant_total, per_row, xv);
   // as many logits a lane as the experts need, in two sizes (256 experts: 649 / 668 us for 64 tokens and 51 / 52
   // for one with the smaller / larger form)
+  const uint32_t spoiled_word = tid == 0 ? __ldcg(a.counters + kMoeSpoiled) : 0u;
   if (a.experts <= 256) {
     for (int t = warp; t < a.tokens; t += kMoeThreads / 32) moe_route<8>(a, tb, t, lane);
   } else {
     for (int t = warp; t < a.tokens; t += kMoeThreads / 32) moe_route<32>(a, tb, t, lane);
   }
+  if (tid == 0) spoiled = spoiled_word;
   __syncthreads();
+  if (spoiled != 0u) {  // the whole block, before anything is in flight
+    if (tid == 0) record_error_at(a.err, kErrTimeout);
+    if (warp == 1) t5_dealloc(tmem_slot, 512);
+    return;
+  }
   // active experts in increasing order and their first rows: a thread per expert, (rows << 16 | 1) summed
   {
     uint32_t base = 0;
@@ -745,6 +753,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 
   __syncthreads();
   // after an expired wait: loads that nothing consumed land before the block ends
+  if (tid == 0 && abort_flag != 0u) a.counters[kMoeSpoiled] = 1u;
   if (tid == 0) {
     const uint32_t most = max(fills_a, fills_b);
     for (uint32_t f = consumed; f < most; ++f) {

@@ -116,7 +116,8 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     ``window`` > 0: only the last ``window`` of those.  ``sm_scale``: 1 /
     sqrt(dim) when None.  A row without keys gives zeros and an lse of -inf.
     ``workspace``: uint8, zeroed once (``torch.zeros``), left ready for the
-    next call; allocated when None.  Returns ``out`` (contiguous, q's type),
+    next call (but for one after which :func:`device_error` reports
+    BSQ_ERR_TIMEOUT: then zeroed again); allocated when None.  Returns ``out`` (contiguous, q's type),
     or (out, float32 lse (tokens, heads)) with ``return_lse``."""
     dt, shape, stride, index = _rows(q, "q")
     total, heads, dim = shape
@@ -160,7 +161,9 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w13_scal
     weighted by their probabilities (divided by their sum with
     ``renormalize``).  Activations are quantized to ``fmt`` as by
     :func:`quantize`, x before the first product and bf16(silu(g) * u) before the second.
-    ``workspace``: uint8, zeroed once, left ready for the next call; allocated when None."""
+    ``workspace``: uint8, zeroed once, left ready for the next call (but for one
+    after which :func:`device_error` reports BSQ_ERR_TIMEOUT: then zeroed
+    again); allocated when None."""
     shape = x.shape
     if x.dtype is not _BF16 or len(shape) != 2 or not x.is_cuda or (xs := x.stride())[1] != 1:
         raise ValueError("x must be a 2-D bfloat16 CUDA tensor with unit inner stride")

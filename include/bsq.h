@@ -479,8 +479,9 @@ BSQ_API int32_t bsq_kv_append(int32_t dtype, const void* k_dev, const void* v_de
  *                     of exp(score) over the allowed keys.
  *   workspace_dev     bsq_kv_attention_workspace_bytes() bytes, 16-byte
  *                     aligned, zeroed by the caller once before its first use; every call
- *                     leaves its counters zeroed again (after a reported BSQ_ERR_TIMEOUT
- *                     it has to be zeroed anew).  Calls sharing it must not overlap.
+ *                     leaves its counters zeroed again.  After a reported BSQ_ERR_TIMEOUT
+ *                     it has to be zeroed anew: until then calls with it write nothing
+ *                     else and report BSQ_ERR_TIMEOUT again.  Calls sharing it must not overlap.
  *   total             total * heads / kv_heads <= 2^30.
  * A row without an allowed key gets zeros and -inf, a row with NaN in q gets NaN in both.  What the cache holds
  * beyond a sequence's length, or outside the allowed keys, does not matter.
@@ -525,8 +526,11 @@ BSQ_API int32_t bsq_kv_attention(int32_t dtype, const void* q_dev, int64_t total
  * gives zeros.  NaN logits count as -inf and record BSQ_ERR_VALUE.
  *   workspace_dev     bsq_moe_layer_workspace_bytes() bytes, 256-byte aligned,
  *                     zeroed by the caller once before its first use; every call leaves
- *                     its counters zeroed again (after a reported BSQ_ERR_TIMEOUT it has
- *                     to be zeroed anew).  Calls sharing it must not overlap.
+ *                     its counters zeroed again.  After a reported BSQ_ERR_TIMEOUT it has
+ *                     to be zeroed anew: until then calls with it write nothing else and report
+ *                     BSQ_ERR_TIMEOUT again.  Calls sharing it must not overlap.  The kernel's
+ *                     blocks wait for one another, each wait for about a second at most: work
+ *                     of other streams that keeps some of them off the GPU for longer ends the call with BSQ_ERR_TIMEOUT.
  */
 BSQ_API int64_t bsq_moe_layer_workspace_bytes(int32_t fmt, int32_t tokens, int64_t hidden, int64_t inter, int32_t experts,
                                               int32_t top_k);

@@ -2,6 +2,7 @@
 import pytest
 
 from test_gpu_kv_cache import Case
+from test_gpu_moe_layer import Layer
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +42,36 @@ def test_parts_meet_in_any_order(bsq, group, new, lens):
         torch.cuda.synchronize()
         assert torch.equal(got, expect) and torch.equal(got_lse, lse)
         assert not ws[:4096].any()
+
+
+@pytest.mark.parametrize("group,new", [(4, 1), (8, 4), (4, 40)])
+def test_spoiled_attention_workspace_is_reported(bsq, group, new):
+    """Counters that do not hold (as after a wait that gave up): nothing is written, each call says so, zeros mend it."""
+    case = Case([3000, 100], [new, new], 1, 64, 16, seed=new)
+    q, _ = case.rows(group)
+    args = case.device()
+    ws = torch.zeros(bsq.kv_attention_workspace_bytes(q.shape[0], group, 1, 64, 2, new), dtype=torch.uint8, device="cuda")
+    expect = bsq.kv_attention(q, *args, new, workspace=ws)
+    ws.fill_(255)
+    out = torch.full_like(expect, 7.0)
+    for _ in range(2):
+        bsq.kv_attention(q, *args, new, out=out, workspace=ws)
+        assert bsq.device_error() == 6 and (out == 7.0).all()
+    ws.zero_()
+    assert torch.equal(bsq.kv_attention(q, *args, new, workspace=ws), expect) and bsq.device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4", "mxfp8"])
+def test_spoiled_expert_workspace_is_reported(bsq, fmt):
+    layer = Layer(bsq, fmt, 128, 128, 6, seed=1)
+    x, _, z = layer.inputs(5, 2)
+    zl = torch.from_numpy(z).cuda()
+    ws = torch.zeros(bsq.moe_layer_workspace_bytes(fmt, 5, 128, 128, 6, 2), dtype=torch.uint8, device="cuda")
+    expect = bsq.moe_layer(x, zl, *layer.args, fmt, 2, workspace=ws, **layer.kw)
+    ws.fill_(255)
+    out = torch.full_like(expect, 7.0)
+    for _ in range(2):
+        bsq.moe_layer(x, zl, *layer.args, fmt, 2, out=out, workspace=ws, **layer.kw)
+        assert bsq.device_error() == 6 and (out == 7.0).all()
+    ws.zero_()
+    assert torch.equal(bsq.moe_layer(x, zl, *layer.args, fmt, 2, workspace=ws, **layer.kw), expect) and bsq.device_error() == 0
