@@ -80,6 +80,9 @@ _SIGNATURES = {
 _SIGNATURES |= {
     "bsq_kv_append": (_c_i32, [_c_i32, _c_p, _c_p, _c_i64, _c_i32, _c_i32, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64,
                                _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i32, _c_p, _c_p, _c_i32, _c_p]),
+    "bsq_kv_append_strided": (_c_i32, [_c_i32, _c_p, _c_p, _c_i64, _c_i32, _c_i32, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p,
+                                       _c_p, _c_i64, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i32, _c_p, _c_p, _c_i32,
+                                       _c_p]),
     "bsq_kv_attention_workspace_bytes": (_c_i64, [_c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32]),
     "bsq_kv_attention": (_c_i32, [_c_i32, _c_p, _c_i64, _c_i32, _c_i32, _c_i32, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p,
                                   _c_i64, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i32, _c_p, _c_p, _c_i32,

@@ -26,7 +26,7 @@ constexpr int kKvAppendThreads = 128;
 
 struct KvAppendArgs {
   const uint16_t* src[2];        // new keys, values: (total, kv_heads, D)
-  int64_t src_tok, src_head;     // strides in elements
+  int64_t src_tok[2], src_head[2];  // strides in elements
   uint8_t* cache[2];             // codes, page p head h token t at p*cs_page + h*cs_head + t*cs_tok
   int64_t cs_page, cs_head, cs_tok;
   uint8_t* scales[2];            // (num_pages, kv_heads) E8M0 bytes
@@ -82,14 +82,15 @@ __global__ void __launch_bounds__(kKvAppendThreads) kv_append_kernel(const KvApp
   const int64_t base = pg * a.page;
   const int lo = static_cast<int>(max(start, base) - base), hi = static_cast<int>(min(len, base + a.page) - base);
   const int row0 = tid / kRowThreads, col = tid % kRowThreads * 8;
-  const uint16_t* src = a.src[kv] + (t0 + base - start) * a.src_tok + head * a.src_head + col;
+  const int64_t src_tok = a.src_tok[kv];
+  const uint16_t* src = a.src[kv] + (t0 + base - start) * src_tok + head * a.src_head[kv] + col;
 
   uint4 v[ITERS];
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < ITERS; ++i) {
     const int r = lo + row0 + i * kRowsPerIter;
-    v[i] = r < hi ? ld_global_nc_v4(src + r * a.src_tok) : make_uint4(0, 0, 0, 0);
+    v[i] = r < hi ? ld_global_nc_v4(src + r * src_tok) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < ITERS; ++i)

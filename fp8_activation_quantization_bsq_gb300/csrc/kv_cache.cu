@@ -106,20 +106,32 @@ int32_t bsq_kv_append(int32_t dtype, const void* k, const void* v, int64_t total
                       int64_t num_pages, int32_t page, int64_t cs_page, int64_t cs_head, int64_t cs_tok,
                       const int32_t* table, int64_t table_ld, int32_t table_width, const int32_t* offsets,
                       const int32_t* lens, int32_t batch, void* stream) {
-  if (bsq_status s = check_cache(dtype, total, kv_heads, dim, src_tok, src_head, k_cache, v_cache, k_scales, v_scales,
+  return bsq_kv_append_strided(dtype, k, v, total, kv_heads, dim, src_tok, src_head, src_tok, src_head, k_cache, v_cache, k_scales,
+                               v_scales, num_pages, page, cs_page, cs_head, cs_tok, table, table_ld, table_width, offsets, lens,
+                               batch, stream);
+}
+
+int32_t bsq_kv_append_strided(int32_t dtype, const void* k, const void* v, int64_t total, int32_t kv_heads, int32_t dim,
+                              int64_t k_tok, int64_t k_head, int64_t v_tok, int64_t v_head, void* k_cache, void* v_cache,
+                              void* k_scales, void* v_scales, int64_t num_pages, int32_t page, int64_t cs_page, int64_t cs_head,
+                              int64_t cs_tok, const int32_t* table, int64_t table_ld, int32_t table_width,
+                              const int32_t* offsets, const int32_t* lens, int32_t batch, void* stream) {
+  if (bsq_status s = check_cache(dtype, total, kv_heads, dim, k_tok, k_head, k_cache, v_cache, k_scales, v_scales,
                                  num_pages, page, cs_page, cs_head, cs_tok, table, table_ld, table_width, offsets, lens, batch);
       s != BSQ_OK)
     return s;
   if (total == 0 || batch == 0) return BSQ_OK;
   if (!k || !v) return BSQ_ERR_NULL;
-  if (!aligned(k, 16) || !aligned(v, 16)) return BSQ_ERR_ALIGN;
+  if (!aligned(k, 16) || !aligned(v, 16) || v_tok % 8 != 0 || v_head % 8 != 0) return BSQ_ERR_ALIGN;
   HostDevice d;
   if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
   KvAppendArgs a{};
   a.src[0] = static_cast<const uint16_t*>(k);
   a.src[1] = static_cast<const uint16_t*>(v);
-  a.src_tok = src_tok;
-  a.src_head = src_head;
+  a.src_tok[0] = k_tok;
+  a.src_tok[1] = v_tok;
+  a.src_head[0] = k_head;
+  a.src_head[1] = v_head;
   a.cache[0] = static_cast<uint8_t*>(k_cache);
   a.cache[1] = static_cast<uint8_t*>(v_cache);
   a.cs_page = cs_page;

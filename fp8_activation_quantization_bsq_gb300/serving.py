@@ -80,7 +80,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
               stream=None) -> None:
     """Write new keys and values into the 8-bit paged cache, in place.
 
-    ``k``, ``v``: (tokens, kv_heads, dim) BF16 or FP16 of equal strides, the
+    ``k``, ``v``: (tokens, kv_heads, dim) BF16 or FP16, each with strides of its own, the
     rows of sequence b at ``offsets[b]:offsets[b+1]`` (int32, batch + 1).
     ``k_cache``, ``v_cache``: uint8 (pages, kv_heads, page, dim) E4M3 codes in
     any order of equal strides (e.g. a transposed view of (pages, page,
@@ -90,13 +90,14 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     with the new tokens.  A page that earlier tokens share keeps the larger
     of its scale and the new tokens', and its codes are rewritten when it grows."""
     dt, shape, stride, index = _rows(k, "k")
-    if v.dtype != k.dtype or v.shape != shape or v.stride() != stride or v.get_device() != index:
-        raise ValueError("k and v must have equal shapes, types and strides")
+    vs = v.stride()
+    if v.dtype != k.dtype or v.shape != shape or vs[2] != 1 or v.get_device() != index:
+        raise ValueError("k and v must have equal shapes and types, unit inner strides and one device")
     heads, cache = _cache(shape[2], index, k_cache, v_cache, k_scales, v_scales, block_table, offsets, seq_lens)
     if shape[1] != heads:
         raise ValueError("k must have the cache's kv_heads")
-    _call("bsq_kv_append", index, stream,
-          (dt, k.data_ptr(), v.data_ptr(), shape[0], heads, shape[2], stride[0], stride[1], *cache))
+    _call("bsq_kv_append_strided", index, stream,
+          (dt, k.data_ptr(), v.data_ptr(), shape[0], heads, shape[2], stride[0], stride[1], vs[0], vs[1], *cache))
 
 
 def kv_attention_workspace_bytes(total: int, heads: int, kv_heads: int, dim: int, batch: int, max_q: int) -> int:

@@ -463,6 +463,15 @@ BSQ_API int32_t bsq_kv_append(int32_t dtype, const void* k_dev, const void* v_de
                               int64_t page_stride, int64_t head_stride, int64_t token_stride,
                               const int32_t* block_table_dev, int64_t table_stride, int32_t table_width,
                               const int32_t* offsets_dev, const int32_t* seq_lens_dev, int32_t batch, void* stream);
+/* The same with strides of their own for keys and values (keys that a rotary embedding left contiguous beside values
+ * that are a view of the projection's output). */
+BSQ_API int32_t bsq_kv_append_strided(int32_t dtype, const void* k_dev, const void* v_dev, int64_t total, int32_t kv_heads,
+                                      int32_t dim, int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                                      int64_t v_head_stride, void* k_cache_dev, void* v_cache_dev, void* k_scales_dev,
+                                      void* v_scales_dev, int64_t num_pages, int32_t page, int64_t page_stride,
+                                      int64_t head_stride, int64_t token_stride, const int32_t* block_table_dev,
+                                      int64_t table_stride, int32_t table_width, const int32_t* offsets_dev,
+                                      const int32_t* seq_lens_dev, int32_t batch, void* stream);
 
 /*
  * Attention of query rows over their sequences' cached keys and values.

@@ -137,3 +137,20 @@ def test_nan_query_rows_stay_nan(bsq, group, new, length):
     hit[0, 0] = hit[-1, -1] = True
     assert got[hit].isnan().all() and got_lse[hit].isnan().all()
     assert torch.equal(got[~hit], expect[~hit]) and torch.equal(got_lse[~hit], lse[~hit])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("new", [1, 40])
+def test_append_keys_and_values_of_different_strides(bsq, new, dtype):
+    """Keys contiguous (as after a rotary embedding), values a view of the fused projection, and the other way round."""
+    for turn in (False, True):
+        case = Case([70, new + 3], [new, new], 3, 64, 32, seed=8, dtype=dtype)
+        args = case.device()
+        (k, kn), (v, vn) = case.rows(3), case.rows(3)
+        fused = torch.cat([k, v, k], 1)
+        bsq.kv_append(*((fused[:, :3], v) if turn else (k, fused[:, 3:6])), *args)
+        for x, cache, scales, got_c, got_s in ((kn, case.cache[0], case.scales[0], args[0], args[2]),
+                                               (vn, case.cache[1], case.scales[1], args[1], args[3])):
+            ref.append(x, cache, scales, case.table, case.offsets, case.lens)
+            np.testing.assert_array_equal(got_s.cpu().numpy(), scales)
+            np.testing.assert_array_equal(got_c.cpu().numpy(), cache)
