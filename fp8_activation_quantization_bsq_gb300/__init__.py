@@ -84,6 +84,9 @@ _SIGNATURES |= {
                                        _c_p, _c_i64, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i32, _c_p, _c_p, _c_i32,
                                        _c_p]),
     "bsq_kv_attention_workspace_bytes": (_c_i64, [_c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32]),
+    "bsq_workspace_zero": (_c_i32, [_c_p, _c_i64, _c_p]),
+    "bsq_kv_attention_counter_bytes": (_c_i64, []),
+    "bsq_moe_layer_counter_bytes": (_c_i64, []),
     "bsq_kv_attention": (_c_i32, [_c_i32, _c_p, _c_i64, _c_i32, _c_i32, _c_i32, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p,
                                   _c_i64, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i32, _c_p, _c_p, _c_i32,
                                   _c_i32, _c_f32, _c_i32, _c_i32, _c_p, _c_p, _c_p, _c_i64, _c_p]),

@@ -169,6 +169,15 @@ int64_t bsq_kv_attention_workspace_bytes(int64_t total, int32_t heads, int32_t k
   return kKvCounterBytes + 2 * int64_t(kKvMaxBlocks) * KvShape<128, 2>::kPartFloats * 4;
 }
 
+int64_t bsq_kv_attention_counter_bytes(void) { return kKvCounterBytes; }
+
+int32_t bsq_workspace_zero(void* workspace, int64_t bytes, void* stream) {
+  if (bytes < 0) return BSQ_ERR_SHAPE;
+  if (bytes == 0) return BSQ_OK;
+  if (!workspace) return BSQ_ERR_NULL;
+  return cudaMemsetAsync(workspace, 0, static_cast<size_t>(bytes), static_cast<cudaStream_t>(stream)) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
+}
+
 int32_t bsq_kv_attention(int32_t dtype, const void* q, int64_t total, int32_t heads, int32_t kv_heads, int32_t dim,
                          int64_t q_tok, int64_t q_head, const void* k_cache, const void* v_cache, const void* k_scales,
                          const void* v_scales, int64_t num_pages, int32_t page, int64_t cs_page, int64_t cs_head,

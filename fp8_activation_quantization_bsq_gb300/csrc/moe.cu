@@ -96,6 +96,8 @@ int64_t bsq_moe_layer_workspace_bytes(int32_t fmt, int32_t tokens, int64_t hidde
   return moe_workspace(fmt, tokens, hidden, inter, experts, top_k).bytes;
 }
 
+int64_t bsq_moe_layer_counter_bytes(void) { return kMoeCounterBytes; }
+
 int32_t bsq_moe_layer(int32_t fmt, const void* x, int64_t ld_x, const float* logits, int64_t ld_logits, const void* w13,
                       const void* w13_s, const void* w2, const void* w2_s, const float* x_sf, const float* w13_sf,
                       const float* h_sf, const float* w2_sf, void* y, int64_t ld_y, int32_t tokens, int64_t hidden,

@@ -46,7 +46,7 @@ constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 1024;
 constexpr int kMoeThreads = 384;          // weights, products, tokens, (idle), 4 epilogue and 4 helper warps
 constexpr int kMoeQuantThreads = 256;      // warps 4-11 quantize the tokens and sum y
 constexpr int kMoeHalfBytes = 128 * 128;  // a stage's 128 rows x 128 bytes of one tile half
-constexpr int kMoeMaxBlocks = 512;
+constexpr int kMoeMaxBlocks = 160;  // one per SM
 // counters at the start of the workspace, zero between calls
 // (kMoeSpoiled: not 0 once a call has given up in a wait; what else the workspace holds is then not to be trusted)
 constexpr int kMoeBarQuant = 0, kMoeBarDone = 32, kMoeBarExit = 64, kMoeSpoiled = 80, kMoePartReady = 96,

@@ -41,6 +41,13 @@ def _new(stream, make, shape, dtype, device):
         return make(shape, dtype=dtype, device=device)
 
 
+def _own_workspace(stream, index, nbytes, counter_bytes, device):
+    """A workspace for one call: its counters have to be zero, the rest may hold anything."""
+    ws = _new(stream, torch.empty, nbytes, _U8, device)
+    _call("bsq_workspace_zero", index, stream, (ws.data_ptr(), min(nbytes, counter_bytes)))
+    return ws
+
+
 def _rows(x, what):
     """(dtype code, shape, strides, device index) of a (tokens, heads, dim) 16-bit CUDA tensor."""
     code, shape = _DTYPES.get(x.dtype), x.shape
@@ -133,7 +140,8 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     elif lse.dtype is not _F32 or lse.shape != (total, heads) or not lse.is_contiguous() or lse.get_device() != index:
         raise ValueError("lse must be a contiguous float32 (tokens, heads) tensor on q's device")
     if workspace is None:
-        workspace = _new(stream, torch.zeros, kv_attention_workspace_bytes(total, heads, kv_heads, dim, cache[-1], max_q), _U8, q.device)
+        workspace = _own_workspace(stream, index, kv_attention_workspace_bytes(total, heads, kv_heads, dim, cache[-1], max_q),
+                                   lib().bsq_kv_attention_counter_bytes(), q.device)
     elif workspace.dtype is not _U8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
     _call("bsq_kv_attention", index, stream,
@@ -203,7 +211,8 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w13_scal
     elif out.dtype is not _BF16 or out.shape != shape or out.stride(1) != 1 or out.get_device() != index:
         raise ValueError("out must be a (tokens, hidden) bfloat16 tensor with unit inner stride on x's device")
     if workspace is None:
-        workspace = _new(stream, torch.zeros, moe_layer_workspace_bytes(f, tokens, hidden, inter, experts, top_k), _U8, x.device)
+        workspace = _own_workspace(stream, index, moe_layer_workspace_bytes(f, tokens, hidden, inter, experts, top_k),
+                                   lib().bsq_moe_layer_counter_bytes(), x.device)
     elif workspace.dtype is not _U8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on x's device")
     _call("bsq_moe_layer", index, stream,

@@ -416,6 +416,10 @@ BSQ_API int32_t bsq_gemm_quantize(int32_t fmt, const void* a_dev, const void* b_
 
 typedef enum { BSQ_BF16 = 0, BSQ_F16 = 1 } bsq_dtype;
 
+/* Enqueue the zeroing of the first `bytes` bytes of a workspace (bsq_kv_attention_counter_bytes(),
+ * bsq_moe_layer_counter_bytes()). */
+BSQ_API int32_t bsq_workspace_zero(void* workspace_dev, int64_t bytes, void* stream);
+
 /*
  * The cache.  Keys and values are held in pages of `page` tokens (16, 32, 64
  * or 128) of each kv head: E4M3 codes, and one E8M0 scale byte e + 127 per
@@ -500,6 +504,8 @@ BSQ_API int32_t bsq_kv_append_strided(int32_t dtype, const void* k_dev, const vo
  */
 BSQ_API int64_t bsq_kv_attention_workspace_bytes(int64_t total, int32_t heads, int32_t kv_heads, int32_t dim, int32_t batch,
                                                  int32_t max_q);
+/* The counters: the workspace's first bytes, for all sizes; zeroing these is enough. */
+BSQ_API int64_t bsq_kv_attention_counter_bytes(void);
 BSQ_API int32_t bsq_kv_attention(int32_t dtype, const void* q_dev, int64_t total, int32_t heads, int32_t kv_heads,
                                  int32_t dim, int64_t q_token_stride, int64_t q_head_stride, const void* k_cache_dev,
                                  const void* v_cache_dev, const void* k_scales_dev, const void* v_scales_dev,
@@ -543,6 +549,8 @@ BSQ_API int32_t bsq_kv_attention(int32_t dtype, const void* q_dev, int64_t total
  */
 BSQ_API int64_t bsq_moe_layer_workspace_bytes(int32_t fmt, int32_t tokens, int64_t hidden, int64_t inter, int32_t experts,
                                               int32_t top_k);
+/* The counters: the workspace's first bytes, for all sizes; zeroing these is enough. */
+BSQ_API int64_t bsq_moe_layer_counter_bytes(void);
 BSQ_API int32_t bsq_moe_layer(int32_t fmt, const void* x_dev, int64_t ld_x, const float* logits_dev, int64_t ld_logits,
                               const void* w13_dev, const void* w13_scales_dev, const void* w2_dev,
                               const void* w2_scales_dev, const float* x_sf_dev, const float* w13_sf_dev,

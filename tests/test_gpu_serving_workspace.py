@@ -75,3 +75,36 @@ def test_spoiled_expert_workspace_is_reported(bsq, fmt):
         assert bsq.device_error() == 6 and (out == 7.0).all()
     ws.zero_()
     assert torch.equal(bsq.moe_layer(x, zl, *layer.args, fmt, 2, workspace=ws, **layer.kw), expect) and bsq.device_error() == 0
+
+
+@pytest.mark.parametrize("group,new", [(4, 1), (8, 4), (4, 40)])
+def test_only_attention_counters_have_to_be_zero(bsq, group, new):
+    """A workspace of anything but for its counters, passed in or (from memory of that kind) the call's own."""
+    case = Case([5000, 100], [new, new], 1, 64, 16, seed=new)
+    q, _ = case.rows(group)
+    args = case.device()
+    nbytes, counters = bsq.kv_attention_workspace_bytes(q.shape[0], group, 1, 64, 2, new), bsq.lib().bsq_kv_attention_counter_bytes()
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+    expect = bsq.kv_attention(q, *args, new, workspace=ws)
+    ws.fill_(255)[:counters].zero_()
+    assert torch.equal(bsq.kv_attention(q, *args, new, workspace=ws), expect)
+    assert not ws[:counters].any()
+    ws.fill_(255)
+    del ws
+    assert torch.equal(bsq.kv_attention(q, *args, new), expect) and bsq.device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4", "mxfp8"])
+def test_only_expert_counters_have_to_be_zero(bsq, fmt):
+    layer = Layer(bsq, fmt, 288, 256, 6, seed=1)
+    x, _, z = layer.inputs(5, 2)
+    zl = torch.from_numpy(z).cuda()
+    nbytes, counters = bsq.moe_layer_workspace_bytes(fmt, 5, 288, 256, 6, 2), bsq.lib().bsq_moe_layer_counter_bytes()
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+    expect = bsq.moe_layer(x, zl, *layer.args, fmt, 2, workspace=ws, **layer.kw)
+    ws.fill_(255)[:counters].zero_()
+    assert torch.equal(bsq.moe_layer(x, zl, *layer.args, fmt, 2, workspace=ws, **layer.kw), expect)
+    assert not ws[:counters].any()
+    ws.fill_(255)
+    del ws
+    assert torch.equal(bsq.moe_layer(x, zl, *layer.args, fmt, 2, **layer.kw), expect) and bsq.device_error() == 0

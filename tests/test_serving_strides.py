@@ -1,4 +1,4 @@
-"""Refusals of the append with strides of their own for keys and values, on the CPU."""
+"""Refusals of the append with strides of its own for keys and values, and of the workspace calls, on the CPU."""
 import pytest
 
 from test_serving_args import ALIGN, APPEND, CACHE_BAD, NULL, P, bsq  # noqa: F401
@@ -15,3 +15,13 @@ for key, value in APPEND.items():
     (dict(v_head=68), ALIGN)])
 def test_strided_append_refusals(bsq, change, code):  # noqa: F811
     assert bsq.lib().bsq_kv_append_strided(*{**STRIDED, **change}.values()) == code
+
+
+def test_workspace_zero_refusals(bsq):  # noqa: F811
+    lib = bsq.lib()
+    assert lib.bsq_workspace_zero(None, 16, None) == NULL
+    assert lib.bsq_workspace_zero(P, -1, None) == 2
+    assert lib.bsq_workspace_zero(None, 0, None) == 0
+    assert lib.bsq_kv_attention_counter_bytes() > 0 and lib.bsq_moe_layer_counter_bytes() > 0
+    assert bsq.moe_layer_workspace_bytes("mxfp8", 1, 64, 128, 1, 1) > lib.bsq_moe_layer_counter_bytes()
+    assert bsq.kv_attention_workspace_bytes(1, 1, 1, 64, 1, 1) > lib.bsq_kv_attention_counter_bytes()
