@@ -26,6 +26,7 @@ bsq_status check_cache(int32_t dtype, int64_t total, int32_t kv_heads, int32_t d
   if (total < 0 || total >= (int64_t(1) << 31) || batch < 0 || kv_heads < 1 || kv_heads > 1024 || (dim != 64 && dim != 128) ||
       num_pages < 1 || num_pages >= (int64_t(1) << 31) || (page != 16 && page != 32 && page != 64 && page != 128) ||
       table_width < 0 || static_cast<int64_t>(table_width) * page > kKvMaxLen || (batch > 1 && table_ld < table_width) || cs_tok < dim || cs_page < 0 || cs_head < 0 ||
+      total / page + 2 * static_cast<int64_t>(batch) >= (int64_t(1) << 31) ||  // blocks of an append
       cs_tok >= (int64_t(1) << 32) || cs_head >= (int64_t(1) << 38) || cs_page >= (int64_t(1) << 38))
     return BSQ_ERR_SHAPE;
   if (total == 0 || batch == 0) return BSQ_OK;

@@ -438,6 +438,7 @@ BSQ_API int32_t bsq_workspace_zero(void* workspace_dev, int64_t bytes, void* str
  *                     head_stride and token_stride are multiples of 16,
  *                     token_stride >= dim.
  *   block_table_dev   int32, `batch` rows of table_width entries, table_width * page <= 2^30.
+ *   batch             total / page + 2 * batch < 2^31.
  *   offsets_dev       int32[batch + 1], non-decreasing from 0: sequence b owns the
  *                     rows [offsets[b], offsets[b+1]) of the 16-bit tensors.
  *   seq_lens_dev      int32[batch]: cached tokens of the sequence, the rows
