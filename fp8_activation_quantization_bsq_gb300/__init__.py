@@ -71,6 +71,7 @@ _SIGNATURES = {
                                        _c_i64, _c_p, _c_i32, _c_p, _c_i64, _c_p]),
     "bsq_device_error": (_c_i32, [_c_p, ctypes.POINTER(_c_i32)]),
     "bsq_selftest_wait_timeout": (_c_i32, [_c_p]),
+    "bsq_selftest_serving_waits": (_c_i32, [_c_p]),
     "bsq_block_scaled_dot": (_c_i32, [_c_i32, _c_p, _c_p, ctypes.c_float, _c_p, _c_p, ctypes.c_float,
                                       _c_i64, _c_i64, _c_i64, _c_p, _c_p]),
     "bsq_gemm_quantize": (_c_i32, [_c_i32, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_f32,

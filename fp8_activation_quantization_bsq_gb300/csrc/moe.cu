@@ -86,9 +86,43 @@ bsq_status launch_moe(MoeArgs& a, const void* w13, const void* w2, const HostDev
   return cudaLaunchKernelEx(&cfg, moe_layer_kernel<FMT>, m13, m2, mx, mh, a) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
 }
 
+__device__ uint32_t g_selftest_count;  // stays 0
+
+// The serving kernels' waits, each on something that nothing completes, with limits of about a millisecond; then
+// once more where another role has given up, and on what is complete.
+__global__ void serving_waits_selftest_kernel(unsigned int* err) {
+  __shared__ uint64_t never, done;
+  __shared__ volatile uint32_t abort_flag;
+  pdl_wait();
+  if (threadIdx.x != 0) return;
+  constexpr long long kLimit = 2000000;
+  mbar_init(&never, 1);
+  mbar_init(&done, 1);
+  abort_flag = 0u;
+  fence_mbar_init();
+  mbar_arrive(&done);
+  const long long t0 = clock64();
+  bool right = !mbar_wait_clocked(&never, 0, &abort_flag, kLimit) && !mbar_wait_clocked(&never, 0, kLimit) &&
+               !moe_wait_count(&g_selftest_count, 1u, &abort_flag, kLimit) && clock64() - t0 >= 3 * kLimit;
+  right = right && mbar_wait_clocked(&done, 0, &abort_flag) && mbar_wait_clocked(&done, 0) && moe_wait_count(&g_selftest_count, 0u, &abort_flag);
+  abort_flag = 1u;
+  const long long t1 = clock64();
+  right = right && !mbar_wait_clocked(&never, 0, &abort_flag) && !moe_wait_count(&g_selftest_count, 1u, &abort_flag) &&
+          clock64() - t1 < kWaitLimitCycles;
+  record_error_at(err, right ? kErrTimeout : kErrValue);
+}
+
 }  // namespace
 
 extern "C" {
+
+int32_t bsq_selftest_serving_waits(void* stream) {
+  HostDevice d;
+  if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
+  return launch_pdl(serving_waits_selftest_kernel, dim3(1), dim3(32), 0, static_cast<cudaStream_t>(stream), d.error_word) == cudaSuccess
+             ? BSQ_OK
+             : BSQ_ERR_CUDA;
+}
 
 int64_t bsq_moe_layer_workspace_bytes(int32_t fmt, int32_t tokens, int64_t hidden, int64_t inter, int32_t experts,
                                       int32_t top_k) {

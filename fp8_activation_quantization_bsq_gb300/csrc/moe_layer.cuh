@@ -312,11 +312,12 @@ __device__ __forceinline__ void moe_products(uint32_t d, uint64_t da, uint64_t d
 __device__ __forceinline__ int moe_token_scale(int r, int s) { return (s >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (s & 3); }
 
 // Wait until a counter in global memory reaches `value`, for about a second.
-__device__ __forceinline__ bool moe_wait_count(const uint32_t* p, uint32_t value, const volatile uint32_t* abort_flag) {
+__device__ __forceinline__ bool moe_wait_count(const uint32_t* p, uint32_t value, const volatile uint32_t* abort_flag,
+                                               long long limit = kWaitLimitCycles) {
   if (ld_acquire(p) >= value) return true;
   const long long t0 = clock64();
   while (ld_acquire(p) < value)
-    if (*abort_flag != 0u || clock64() - t0 > kWaitLimitCycles) return false;
+    if (*abort_flag != 0u || clock64() - t0 > limit) return false;
   return true;
 }
 

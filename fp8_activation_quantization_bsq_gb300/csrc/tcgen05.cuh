@@ -14,19 +14,20 @@ constexpr long long kWaitLimitCycles = 2000000000ll;
 
 // Wait until the phase with the given parity has completed; false when the
 // limit expired or another role of the block has given up.
-__device__ __forceinline__ bool mbar_wait_clocked(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort_flag) {
+__device__ __forceinline__ bool mbar_wait_clocked(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort_flag,
+                                                  long long limit = kWaitLimitCycles) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity))
-    if (*abort_flag != 0u || clock64() - t0 > kWaitLimitCycles) return false;
+    if (*abort_flag != 0u || clock64() - t0 > limit) return false;
   return true;
 }
 
 // The same for copies and products that have to land whatever happened.
-__device__ __forceinline__ bool mbar_wait_clocked(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_clocked(uint64_t* bar, uint32_t parity, long long limit = kWaitLimitCycles) {
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity))
-    if (clock64() - t0 > kWaitLimitCycles) return false;
+    if (clock64() - t0 > limit) return false;
   return true;
 }
 

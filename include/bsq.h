@@ -569,6 +569,13 @@ BSQ_API int32_t bsq_moe_layer(int32_t fmt, const void* x_dev, int64_t ld_x, cons
 BSQ_API int32_t bsq_selftest_wait_timeout(void* stream);
 
 /*
+ * The same for the waits of the serving kernels (on barriers and counters), with limits of
+ * about a millisecond: records BSQ_ERR_TIMEOUT when each ended as it should,
+ * BSQ_ERR_VALUE otherwise.
+ */
+BSQ_API int32_t bsq_selftest_serving_waits(void* stream);
+
+/*
  * Synchronize `stream`, then read and clear the current device's error word.
  * *code_out receives BSQ_OK or the first device-side error recorded since the
  * last call (BSQ_ERR_VALUE, BSQ_ERR_TIMEOUT).  Returns BSQ_ERR_CUDA if the

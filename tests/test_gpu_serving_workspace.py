@@ -108,3 +108,12 @@ def test_only_expert_counters_have_to_be_zero(bsq, fmt):
     ws.fill_(255)
     del ws
     assert torch.equal(bsq.moe_layer(x, zl, *layer.args, fmt, 2, **layer.kw), expect) and bsq.device_error() == 0
+
+
+def test_waits_end_and_the_context_stays_usable(bsq):
+    """The kernels' waits on barriers and counters that nothing completes give up at their limit."""
+    assert bsq.lib().bsq_selftest_serving_waits(torch.cuda.current_stream().cuda_stream) == 0
+    assert bsq.device_error() == 6 and bsq.device_error() == 0
+    case = Case([100], [1], 1, 64, 16, seed=1)
+    q, _ = case.rows(2)
+    assert torch.isfinite(bsq.kv_attention(q, *case.device(), 1)).all() and bsq.device_error() == 0
