@@ -13,7 +13,7 @@
 // below 2^-126 is less than 2^-53 of the largest.  From the first page past that on, an item's share
 // has a z of its own, the scores' running maximum, and exponentials of its own for the sum.
 // The key scale is one factor of a tile's scores.  E4M3 codes and scaled query rows (a power of two per row) are exact in FP16
-// (elements below 2^-28 of a row's largest: to 2^-37 of that);
+// (but for elements below 2^-29 of a row's largest in BF16, 2^-26 in FP16: off by 2^-37 of it at most);
 // weights are rounded to FP16 (a relative 2^-11 each, against 2^-9 of a BF16
 // output; the row's largest is between 2^kKvAbove and 2^kKvLag, so that subnormal ones are off by 2^-32 of
 // it at most), and all sums are FP32.
