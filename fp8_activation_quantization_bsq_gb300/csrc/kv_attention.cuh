@@ -423,8 +423,18 @@ struct KvJoin {
   __device__ __forceinline__ uint32_t* group_counter(const KvAttnArgs& a) const {
     return a.arrived + (head() > 0 ? kKvLaterCounters : kKvGroupCounters) + own0 + head();
   }
+  // Whether this is the group's first block and the last to arrive, as it is as a rule (a block meets its last item's
+  // beginning at the end of its run): it then need not store its own part.  The counter is 0 again.  One thread calls.
+  __device__ __forceinline__ bool arrived_but_one(const KvAttnArgs& a) const {
+    if (count == 1 || me != head() || ld_acquire(group_counter(a)) != static_cast<uint32_t>(members()) - 1u) return false;
+    *group_counter(a) = 0u;
+    return true;
+  }
   __device__ __forceinline__ uint32_t* item_counter(const KvAttnArgs& a) const { return a.arrived + kKvItemCounters + own0; }
 };
+
+// The sums of a part onto others, both taken to the larger m; written out, so that it is the same wherever it is done.
+__device__ __forceinline__ float kv_add(float x, float f0, float v, float f1) { return __fmaf_rn(v, f1, __fmul_rn(x, f0)); }
 
 // `threads` threads of a block, whose parts are stored, meet at barrier `id`; true if theirs is the last of n
 // (then all n can be read and the counter is 0 again).
@@ -806,12 +816,45 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
         }
       }
       named_sync(1, kT);
-      if (tid == 0) go_on = abort_flag == 0u ? 1u : 0u;  // one answer for all warps
       const int live = min(RT, rows - g.rt * RT);  // rows of the tile
       const KvJoin team(start, g.first, g.count);
+      if (tid == 0) go_on = abort_flag != 0u ? 0u : team.arrived_but_one(a) ? 2u : 1u;  // one answer for all warps
       // kTpr threads per row, float4s kTpr i + tid % kTpr of it
       constexpr int kTpr = kT / S::kPassRows, kOwn = D / 4 / kTpr;
       const int rl = tid / kTpr, d4 = tid % kTpr;
+      const int head = team.head(), groups = team.groups();
+      float* const to_group = groups > 1 ? team.part(a, head, S::kPartFloats) : nullptr;
+      // Parts p0 to n - 1, of part i0 and every step-th after it, onto row r's sums.
+      const auto add_parts = [&](int r, int i0, int step, int p0, int n, float4 (&acc)[kOwn], float& am, KvSum& below) {
+        const float m0 = am;
+        const KvSum before = below;
+#pragma unroll(16 / kOwn)
+        for (int p = p0; p < n; ++p) {
+          const float* part = team.part(a, i0 + p * step, S::kPartFloats);
+          float4 v[kOwn];
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(part + r * D) + kTpr * i + d4);
+          const float pm = __ldcg(part + RT * D + r), pl = __ldcg(part + RT * D + RT + r);
+          const float mm = fmaxf(am, pm);
+          const float f0 = am == -INFINITY ? 0.f : fast_exp2(am - mm), f1 = pm == -INFINITY ? 0.f : fast_exp2(pm - mm);
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i)
+            acc[i] = make_float4(kv_add(acc[i].x, f0, v[i].x, f1), kv_add(acc[i].y, f0, v[i].y, f1),
+                                 kv_add(acc[i].z, f0, v[i].z, f1), kv_add(acc[i].w, f0, v[i].w, f1));
+          below.wild |= pl < 0.f;
+          below.l = kv_add(below.l, f0, pl, f1);
+          am = mm;
+        }
+        if (below.wild) {  // the sum again, with every z
+          below = KvSum{};
+          if (p0 > 0) below.add_wild(m0, before.stored(), before.z);
+#pragma unroll 1
+          for (int p = p0; p < n; ++p) {
+            const float* part = team.part(a, i0 + p * step, S::kPartFloats) + RT * D + r;
+            below.add_wild(__ldcg(part), __ldcg(part + RT), __ldcg(part + 2 * RT));
+          }
+        }
+      };
       // Row r of the tile to a part, or where there is none to the output.
       const auto put = [&](int r, float4 (&acc)[kOwn], float am, const KvSum& below, float* part) {
         if (part != nullptr) {
@@ -863,6 +906,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
         }
         named_sync(1, kT);
         ok = go_on != 0u;
+        const bool direct = go_on == 2u;
         const int r = pass * S::kPassRows + rl;
         if (ok && r < live) {
           float4 acc[kOwn];
@@ -890,12 +934,16 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) below.add_wild(warp_m[k][r], warp_l[k][r], warp_z[k][r]);
           }
-          put(r, acc, am, below, team.count > 1 ? team.part(a, team.me, S::kPartFloats) : nullptr);
+          if (direct) add_parts(r, head, 1, 1, team.members(), acc, am, below);
+          put(r, acc, am, below, direct ? to_group : team.count > 1 ? team.part(a, team.me, S::kPartFloats) : nullptr);
         }
       }
       if (ok && team.count > 1) {
-        // n parts, from part i0 on every step-th, into one or the output
-        const auto join_parts = [&](int i0, int step, int n, float* to) {
+#pragma unroll 1
+        for (int level = go_on == 2u ? 1 : 0; level < (groups > 1 ? 2 : 1); ++level) {  // the group's parts, then the groups'
+          const bool top = level == 1;
+          const int n = top ? groups : team.members();
+          if (!kv_arrive(top ? team.item_counter(a) : team.group_counter(a), n, 1, kT, tid == 0, &last)) break;
 #pragma unroll 1
           for (int r = rl; r < RT; r += S::kPassRows) {
             const uint32_t mask = __ballot_sync(~0u, r < live);
@@ -905,39 +953,10 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
             for (int i = 0; i < kOwn; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             KvSum below;
             float am = -INFINITY;
-#pragma unroll(16 / kOwn)
-            for (int p = 0; p < n; ++p) {
-              const float* part = team.part(a, i0 + p * step, S::kPartFloats);
-              float4 v[kOwn];
-#pragma unroll
-              for (int i = 0; i < kOwn; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(part + r * D) + kTpr * i + d4);
-              const float pm = __ldcg(part + RT * D + r), pl = __ldcg(part + RT * D + RT + r);
-              const float mm = fmaxf(am, pm);
-              const float f0 = am == -INFINITY ? 0.f : fast_exp2(am - mm), f1 = pm == -INFINITY ? 0.f : fast_exp2(pm - mm);
-#pragma unroll
-              for (int i = 0; i < kOwn; ++i)
-                acc[i] = make_float4(acc[i].x * f0 + v[i].x * f1, acc[i].y * f0 + v[i].y * f1, acc[i].z * f0 + v[i].z * f1,
-                                     acc[i].w * f0 + v[i].w * f1);
-              below.wild |= pl < 0.f;
-              below.l = below.l * f0 + pl * f1;
-              am = mm;
-            }
-            if (below.wild) {
-              below = KvSum{};
-#pragma unroll 1
-              for (int p = 0; p < n; ++p) {
-                const float* part = team.part(a, i0 + p * step, S::kPartFloats) + RT * D + r;
-                below.add_wild(__ldcg(part), __ldcg(part + RT), __ldcg(part + 2 * RT));
-              }
-            }
+            add_parts(r, top ? 0 : head, top ? team.join : 1, 0, n, acc, am, below);
             __syncwarp(mask);  // the row's threads, all in this warp, have read what put may replace
-            put(r, acc, am, below, to);
+            put(r, acc, am, below, top ? nullptr : to_group);
           }
-        };
-        const int head = team.head(), groups = team.groups();
-        if (kv_arrive(team.group_counter(a), team.members(), 1, kT, tid == 0, &last)) {
-          join_parts(head, 1, team.members(), groups > 1 ? team.part(a, head, S::kPartFloats) : nullptr);
-          if (groups > 1 && kv_arrive(team.item_counter(a), groups, 1, kT, tid == 0, &last)) join_parts(0, team.join, groups, nullptr);
         }
       }
       // the merge buffer and the flags are written again only after the first

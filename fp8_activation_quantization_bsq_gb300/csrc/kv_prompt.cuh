@@ -505,13 +505,7 @@ __global__ void __launch_bounds__(kKpThreads, 1)
       // ---- the item's share
       const KvJoin team(start, g.first, g.count);
       named_sync(1, 256);
-      if (tid == 0) {
-        // the group's first block is its last to arrive as a rule: it then need not store its own part
-        const bool direct = team.count > 1 && team.me == team.head() &&
-                            ld_acquire(team.group_counter(a)) == static_cast<uint32_t>(team.members()) - 1u;
-        go_on = abort_flag != 0u ? 0u : direct ? 2u : 1u;
-        if (go_on == 2u) *team.group_counter(a) = 0u;
-      }
+      if (tid == 0) go_on = abort_flag != 0u ? 0u : team.arrived_but_one(a) ? 2u : 1u;
       named_sync(1, 256);
       ok = go_on != 0u;  // one answer for all warps
       const bool direct = go_on == 2u;
