@@ -55,10 +55,12 @@ class Layer:
         self.workspaces = {}
 
     def workspace(self, name, nbytes):
-        """Zeroed once, kept between calls (each leaves it ready for the next)."""
-        if name not in self.workspaces or self.workspaces[name].numel() < nbytes:
-            self.workspaces[name] = torch.zeros(nbytes, dtype=torch.uint8, device=self.w_out.device)
-        return self.workspaces[name]
+        """Zeroed once, kept between calls (each leaves it ready for the next); a smaller one that a larger
+        replaces is kept too, for a captured step goes on using it."""
+        kept = self.workspaces.setdefault(name, [])
+        if not kept or kept[-1].numel() < nbytes:
+            kept.append(torch.zeros(nbytes, dtype=torch.uint8, device=self.w_out.device))
+        return kept[-1]
 
     def attend(self, x, cache, offsets, max_q):
         """x: (tokens, hidden), rows offsets[b]:offsets[b+1] new in sequence b, which cache.lens already counts."""
