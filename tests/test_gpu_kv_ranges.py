@@ -58,7 +58,7 @@ def attend(bsq, case, heads, q_scale=1.0, **kw):
 
 @pytest.mark.parametrize("group,new", ROWS)
 @pytest.mark.parametrize("q_scale", [0.0, 1.0])
-@pytest.mark.parametrize("value_bytes", [(1,), (254,), (1, 254), (1, 127, 254), (95, 247), (20, 100, 127)])
+@pytest.mark.parametrize("value_bytes", [(1,), (254,), (1, 254), (1, 127, 254), (95, 247), (20, 100, 127), (87, 167), (86, 127, 168)])
 def test_value_scales_from_end_to_end(bsq, group, new, q_scale, value_bytes):
     """The lse does not depend on the values' scales, and the output is their weighted mean, however far apart they are."""
     case = Case([777, 130, new], [new] * 3, 2, 128, 16, seed=len(value_bytes) + new)
