@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(KvShape<D, NT>::kThreads, KvShape<D, NT>::kBlo
       const auto add_parts = [&](int r, int i0, int step, int p0, int n, float4 (&acc)[kOwn], float& am, KvSum& below) {
         const float m0 = am;
         const KvSum before = below;
-#pragma unroll(16 / kOwn)
+#pragma unroll(8 / kOwn)  // more in flight is more code to fetch: one short context 10.0 us, 11.0 with 16
         for (int p = p0; p < n; ++p) {
           const float* part = team.part(a, i0 + p * step, S::kPartFloats);
           float4 v[kOwn];
