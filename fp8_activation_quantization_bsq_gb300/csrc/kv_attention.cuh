@@ -31,9 +31,9 @@
 // dimension in q.k and of the output rows is free, so a thread takes 16 consecutive bytes of a
 // key, and pairs of keys are interleaved bytewise before conversion.
 // Measured (64 contexts of 1000 to 8192 tokens, 64 heads of 128 over 8, a graph of calls): 8 rows
-// per kv head 100 us, 6.1 TB/s or 90 % of a plain copy; 16 rows 116 us and 32 rows 237 us, where
-// the conversions and mma.sync products bound it.  One context of 777: 10.3 us, a chain of
-// latencies (lengths, table, codes, the join); two of 131072, 4 kv heads: 53 us.
+// per kv head 101 us, 6.0 TB/s or 89 % of a plain copy; 16 rows 118 us and 32 rows 248 us, where
+// the conversions and mma.sync products bound it.  One context of 777: 10.0 us, a chain of
+// latencies (lengths, table, codes, the join: 4 of them); two of 131072, 4 kv heads: 53 us.
 // An item cut by the runs is joined from its blocks' parts, in block order, by whichever block stores its part last
 // (first in groups where there are many).  So no block waits for another, whether it is on the GPU yet or not, and
 // the sums' order does not depend on which one is last.
@@ -50,8 +50,8 @@ constexpr int kKvMaxBlocks = 512;
 constexpr int kKvMinRun = 3;      // units of a run, at least, once every SM has one
 // Parts of an item that are joined at once, and the size of the groups
 // that are joined first where there are more: about their number's square root.  (104 parts, one
-// context of 20000 with one kv head: 16.3 us, 25.6 when one block joins them all; 57 parts of
-// contexts of 131072: 53.3 / 53.9, and 53.2 to 54.7 for groups of 5 to 20.)
+// context of 20000 with one kv head: 14.1 us, 27.9 when one block joins them all; 57 parts of
+// contexts of 131072: 52.7 / 59.3, and 51.7 for groups of 5, 54.8 for groups of 20.)
 __device__ __forceinline__ int kv_join_group(int parts) { return parts <= 20 ? parts : parts <= 72 ? 8 : 16; }
 // Parts stored so far, zero between calls: of a group (by its first block, which can be the first of one item and of
 // a later group of the item before), of an item's groups (by the item's first block).
@@ -295,9 +295,8 @@ __device__ __forceinline__ bool kv_start(const KvAttnArgs& a, int blocks_per_sm,
     s.total += warp_sum[w];
   }
   // Joining a part costs about as much as a few units: at most one run per SM
-  // until they have kKvMinRun units (contexts of 777 / 3000 tokens with 8 kv heads and 20000 with one:
-  // 10.3 / 12.5 / 16.3 us, and 10.3 / 16.5 / 18.1 with a run for every unit; with at least four
-  // 12.4 / 13.8 where three took 10.1 / 13.1)
+  // until they have kKvMinRun units (contexts of 3000 tokens with 8 kv heads / 20000 with one / 8 of up to 2000:
+  // 12.7 / 14.1 / 15.1 us, 12.6 / 15.5 / 15.1 with a run for every unit, 12.7 / 14.1 / 14.7 with at least four)
   s.parts = static_cast<int>(min(static_cast<int64_t>(gridDim.x),
                                  max(s.total / kKvMinRun, min(s.total, static_cast<int64_t>(gridDim.x / blocks_per_sm)))));
   if (static_cast<int>(blockIdx.x) >= s.parts) return false;
@@ -340,7 +339,8 @@ struct KvShape {
   static constexpr int kRows = 8 * NT;
   static constexpr int kPassRows = NT == 1 ? 8 : 16;       // rows merged at a time
   // registers allow 15 warps per SM at 128, 10 at 168, 5 at 255 (five warps spread unevenly over four
-  // schedulers); 64 contexts to 8192 with 8 rows: 101 us with three blocks, 106 to 108 with two of longer rings
+  // schedulers); 64 contexts to 8192 with 8 rows: 101 us with three blocks, 104 with two of longer rings; with 16
+  // rows 118 with two, 156 with three.  For dimensions of 64 the same numbers, not measured apart
   static constexpr int kBlocksPerSm = NT == 1 ? 3 : NT == 2 ? 2 : 1;
   static constexpr int kTileBytes = kKvTile * D;           // of keys, and of values
   static constexpr int kStages = NT == 1 ? 3 : NT == 2 ? 4 : 6;
@@ -349,8 +349,8 @@ struct KvShape {
   static constexpr int kEighth = D / 8 + 4, kRow = 8 * kEighth + 4;
   static constexpr int kMergeBytes = kWarps * kPassRows * kRow * 4;
   // query rows in shared memory, in the merge buffer that an item uses after them, where registers are short: with
-  // 16 rows of 128 (64 contexts to 8192 / 16 to 800) 116 / 14.8 us against 125 / 15.1 in registers, with 16 of 64
-  // (guessed tokens) 26.7 against 24.6.  Three blocks per SM for 16 rows: 111, but 17.3 for the short contexts
+  // 16 rows of 128 (64 contexts to 8192 / 16 to 800) 118 / 16.1 us against 126 / 16.4 in registers, with 16 of 64
+  // (guessed tokens) 28.8 against 26.5
   static constexpr bool kSharedQuery = NT == 4 || (NT == 2 && D == 128);
   static constexpr int kSmem = 1024 + kStages * 2 * kTileBytes + kMergeBytes;
   static constexpr int kPartFloats = kRows * D + 3 * kRows;

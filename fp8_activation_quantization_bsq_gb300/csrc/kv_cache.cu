@@ -50,8 +50,8 @@ cudaError_t launch_append(const KvAppendArgs& a, cudaStream_t st) {
 }
 
 // Rows (query tokens x heads of a kv head) up to which the kernel for few rows runs: its
-// largest tile.  64 contexts of 1000 to 8192, 64 heads over 8: 32 rows 237 us there and 297 in the kernel for many,
-// 64 rows 461 and 299.  Eight contexts to 2000, 32 rows: 24 and 34.
+// largest tile.  64 contexts of 1000 to 8192, 64 heads over 8: 32 rows 248 us there and 305 in the kernel for many,
+// 64 rows 480 and 307.  Eight contexts to 2000, 32 rows: 26 and 37.
 constexpr int kKvFewRows = 32;
 
 // The cache as a 4D tensor of bytes (dimension, token, head, page), in boxes
@@ -86,8 +86,8 @@ bsq_status launch_attention(const KvAttnArgs& a, const CUtensorMap& mk, const CU
 template <int D, bool F16>
 bsq_status launch_attention_rows(const KvAttnArgs& a, int64_t max_rows, const CUtensorMap& mk, const CUtensorMap& mv,
                                  const HostDevice& d, cudaStream_t st) {
-  // the narrowest tile that holds all rows (those 64 contexts: 8 rows 100 / 119 / 225 us in tiles of 8 / 16 / 32,
-  // 16 rows 116 / 228 in tiles of 16 / 32): unused rows are products, registers and warps per SM lost
+  // the narrowest tile that holds all rows (those 64 contexts: 8 rows 101 / 115 / 236 us in tiles of 8 / 16 / 32,
+  // 16 rows 118 / 240 in tiles of 16 / 32): unused rows are products, registers and warps per SM lost
   if (max_rows <= 8) return launch_attention<D, 1, F16>(a, mk, mv, d, st);
   if (max_rows <= 16) return launch_attention<D, 2, F16>(a, mk, mv, d, st);
   if (max_rows <= kKvFewRows) return launch_attention<D, 4, F16>(a, mk, mv, d, st);

@@ -11,10 +11,10 @@
 // What bounds it: 4 x 256 x 128 x D operations a unit, 2048 cycles of the tensor cores at D = 128; and
 // shared memory, 3072 cycles at 128 bytes each: a 128 x 64 x 16 product reads 6 KB in its 32 cycles (1536 a unit), the
 // values 512, the conversions below and the codes' arrival 1024.  Measured: a 2048-token chunk over 16384, 32 heads of 128
-// over 8: 485 us, 1.06 PFLOP/s or 55 % of a library product's rate, 4500 cycles a unit; P then waits for the issuing warp, which the
+// over 8: 497 us, 1.04 PFLOP/s or 53 % of a library product's rate, 4600 cycles a unit; P then waits for the issuing warp, which the
 // products hold up.  (Scores 128 wide would read a third less, but leave no room for a second S tile: 560 us where this form took 515.
 // A second issuing warp: 529 against 511.  Products on a scheduler without a converter, its work spread over the
-// other three: 484 us, no gain.)
+// other three: 484 us against 485.)
 //  * warps 0-3 and 4-7: the halves' softmax, a thread per row, 64 scores in registers.
 //    O is rescaled only where a row's maximum grew past 2^kKvLag of its reference.  They also bring the
 //    query rows (a power of two per row, so that they are exact in FP16) and write the output.
