@@ -20,7 +20,10 @@ quantize), gemm_quantize (a matmul with the quantize in its epilogue).
 
 Serving a decoder layer from block-scaled storage (serving.py): kv_append and
 kv_attention (an 8-bit paged key/value cache), moe_layer (a
-mixture-of-experts layer for a few tokens over packed weights).
+mixture-of-experts layer for a few tokens over packed weights), and what
+stands between them (layer.py): packed_linear (projections over packed
+weights), qk_norm_rope (norm and rotation of query and key heads), moe_route
+and moe_rows (routing to experts, and the rows' order for grouped calls).
 """
 from __future__ import annotations
 
@@ -36,7 +39,8 @@ __all__ = ["FORMATS", "GROUPED_KERNELS", "lib", "BsqError", "block_size", "packe
            "grouped_quantize_dynamic",
            "grouped_quantize", "grouped_quantize_workspace_bytes", "scales_interleave", "block_scaled_dot", "gemm_quantize", "device_error",
            "status_string", "kv_append", "kv_attention", "kv_attention_workspace_bytes", "moe_layer",
-           "moe_layer_workspace_bytes"]
+           "moe_layer_workspace_bytes", "packed_linear", "qk_norm_rope", "moe_route", "moe_rows",
+           "moe_rows_scale_rows"]
 
 FORMATS = {"nvfp4": 0, "mxfp4": 1, "mxfp8": 2}
 GROUPED_KERNELS = {"auto": 0, "stream": 1, "latency": 2, "token": 3}
@@ -94,6 +98,13 @@ _SIGNATURES |= {
     "bsq_moe_layer_workspace_bytes": (_c_i64, [_c_i32, _c_i32, _c_i64, _c_i64, _c_i32, _c_i32]),
     "bsq_moe_layer": (_c_i32, [_c_i32, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
                                _c_i64, _c_i32, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_p, _c_i64, _c_p]),
+    "bsq_packed_linear": (_c_i32, [_c_i32, _c_i32, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i32, _c_p,
+                                   _c_i64, _c_p]),
+    "bsq_qk_norm_rope": (_c_i32, [_c_i32, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_p, _c_p, _c_i32,
+                                  _c_i32, _c_p, _c_p, _c_i32, _c_f32, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p]),
+    "bsq_moe_route": (_c_i32, [_c_i32, _c_p, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_f32, _c_p,
+                               _c_p, _c_p]),
+    "bsq_moe_rows": (_c_i32, [_c_p, _c_i64, _c_i32, _c_i32, _c_p, _c_p, _c_p, _c_p, _c_p]),
 }
 
 _lib = None
@@ -399,3 +410,4 @@ def device_error(device=None, stream=None) -> int:
 
 from .serving import (kv_append, kv_attention, kv_attention_workspace_bytes, moe_layer,  # noqa: E402
                       moe_layer_workspace_bytes)
+from .layer import moe_route, moe_rows, moe_rows_scale_rows, packed_linear, qk_norm_rope  # noqa: E402

@@ -1,0 +1,94 @@
+// Host side of the products with packed weights (bsq_packed_linear).
+#include <algorithm>
+
+#include "host_common.h"
+#include "packed_linear.cuh"
+
+namespace {
+
+using namespace bsq;
+
+constexpr int kPlSmem = 113 * 1024;  // a block's dynamic shared memory at most: two per SM
+
+template <int FMT, bool F16, int NT>
+bsq_status launch_linear(PlArgs& a, const HostDevice& d, cudaStream_t st) {
+  auto kernel = packed_linear_kernel<FMT, F16, NT>;
+  constexpr int kCols = PlFmt<FMT>::kCols;
+  const int tile_tokens = std::min(a.tokens, NT * 8);
+  // blocks of a cluster: enough for two per SM, as long as every warp has a piece or two
+  const int64_t tiles = ceil_div(a.rows, 128) * 4 * ceil_div(a.tokens, NT * 8);
+  int ranks = 1;
+  while (ranks < 8 && tiles * ranks < 2 * d.sm_count && a.pieces >= 2 * ranks * kPlWarps) ranks *= 2;
+  a.per_rank = static_cast<int>(ceil_div(ceil_div(a.pieces, ranks), kPlWarps) * kPlWarps);
+  ranks = static_cast<int>(ceil_div(a.pieces, a.per_rank));
+  a.segment = kPlWarps;  // as many rounds of pieces as fit beside the rings
+  while (a.segment < a.per_rank && tile_tokens * ((a.segment + kPlWarps) * kCols * 2 + 64) <= kPlSmem - kPlRing) a.segment += kPlWarps;
+  const int smem = std::max(kPlRing + tile_tokens * (a.segment * kCols * 2 + 64), kPlWarps * NT * 8 * 32 * 4);
+  if (bsq_status s = allow_smem(reinterpret_cast<const void*>(kernel), 227 * 1024 - 2048, d.index); s != BSQ_OK) return s;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ranks, static_cast<unsigned>(ceil_div(a.rows, 128) * 4), static_cast<unsigned>(ceil_div(a.tokens, NT * 8)));
+  cfg.blockDim = dim3(kPlThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
+}
+
+template <int FMT, bool F16>
+bsq_status launch_linear_tokens(PlArgs& a, const HostDevice& d, cudaStream_t st) {
+  if (a.tokens <= 8) return launch_linear<FMT, F16, 1>(a, d, st);
+  if (a.tokens <= 16) return launch_linear<FMT, F16, 2>(a, d, st);
+  return launch_linear<FMT, F16, 4>(a, d, st);
+}
+
+}  // namespace
+
+extern "C" int32_t bsq_packed_linear(int32_t fmt, int32_t dtype, const void* x, int64_t tokens, int64_t cols, int64_t ld_x, const void* w,
+                                     const void* w_scales5d, int64_t rows, const float* w_sf, const void* add, int64_t ld_add,
+                                     int32_t out_dtype, void* out, int64_t ld_out, void* stream) {
+  if (!fmt_ok(fmt) || (dtype != BSQ_BF16 && dtype != BSQ_F16) || (out_dtype != dtype && out_dtype != BSQ_F32)) return BSQ_ERR_VALUE;
+  if (tokens < 0 || rows < 0 || tokens > (1 << 20) || rows > (1 << 20) || cols < 32 || cols % 32 != 0 || cols > (1 << 20) ||
+      (tokens > 1 && (ld_x < cols || ld_out < rows)) || ld_x < 0 || ld_out < 0 || ld_add < 0 || ld_x >= (int64_t(1) << 31) ||
+      ld_out >= (int64_t(1) << 31) || ld_add >= (int64_t(1) << 31) || (add && ld_add != 0 && tokens > 1 && ld_add < rows))
+    return BSQ_ERR_SHAPE;
+  if (tokens == 0 || rows == 0) return BSQ_OK;
+  if (!x || !w || !w_scales5d || !out || (fmt == BSQ_NVFP4 && !w_sf)) return BSQ_ERR_NULL;
+  const int elem = out_dtype == BSQ_F32 ? 4 : 2;
+  if (!aligned(x, 16) || ld_x % 8 != 0 || !aligned(w, 16) || !aligned(w_scales5d, 16) || !aligned(w_sf, 4) || !aligned(add, elem) ||
+      !aligned(out, elem))
+    return BSQ_ERR_ALIGN;
+  HostDevice d;
+  if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
+  PlArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.ld_x = ld_x;
+  a.w = static_cast<const uint8_t*>(w);
+  a.scales = static_cast<const uint8_t*>(w_scales5d);
+  a.sf = w_sf;
+  a.add = add;
+  a.ld_add = ld_add;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.rows = rows;
+  a.tokens = static_cast<int>(tokens);
+  a.cols = static_cast<int>(cols);
+  a.row_bytes = row_bytes_of(fmt, cols);
+  a.pieces = static_cast<int>(ceil_div(a.row_bytes, 64));
+  a.k_atoms = static_cast<int>(ceil_div(cols, atom_cols_of(fmt)));
+  a.out_f32 = out_dtype == BSQ_F32;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f16 = dtype == BSQ_F16;
+  switch (fmt) {
+    case BSQ_NVFP4: return f16 ? launch_linear_tokens<kNVFP4, true>(a, d, st) : launch_linear_tokens<kNVFP4, false>(a, d, st);
+    case BSQ_MXFP4: return f16 ? launch_linear_tokens<kMXFP4, true>(a, d, st) : launch_linear_tokens<kMXFP4, false>(a, d, st);
+    default: return f16 ? launch_linear_tokens<kMXFP8, true>(a, d, st) : launch_linear_tokens<kMXFP8, false>(a, d, st);
+  }
+}

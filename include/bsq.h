@@ -414,7 +414,7 @@ BSQ_API int32_t bsq_gemm_quantize(int32_t fmt, const void* a_dev, const void* b_
  * few tokens over packed weights.
  * ------------------------------------------------------------------------ */
 
-typedef enum { BSQ_BF16 = 0, BSQ_F16 = 1 } bsq_dtype;
+typedef enum { BSQ_BF16 = 0, BSQ_F16 = 1, BSQ_F32 = 2 } bsq_dtype; /* BSQ_F32 only where a call says so */
 
 /* Enqueue the zeroing of the first `bytes` bytes of a workspace (bsq_kv_attention_counter_bytes(),
  * bsq_moe_layer_counter_bytes()). */
@@ -558,6 +558,93 @@ BSQ_API int32_t bsq_moe_layer(int32_t fmt, const void* x_dev, int64_t ld_x, cons
                               const float* h_sf_dev, const float* w2_sf_dev, void* y_dev, int64_t ld_y, int32_t tokens,
                               int64_t hidden, int64_t inter, int32_t experts, int32_t top_k, int32_t renormalize,
                               void* workspace_dev, int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Between those calls: projections over packed weights, norm and rotation of
+ * query and key heads, routing to experts.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Products with packed weights: out[t][n] = sum_k x[t][k] w[n][k] (+ add[t][n]), w the values that bsq_quantize's codes
+ * and scales stand for; x is not quantized.
+ *   fmt               bsq_format of the weights.
+ *   dtype             bsq_dtype of x: BSQ_BF16 or BSQ_F16.
+ *   x_dev             (tokens, cols), row stride ld_x (>= cols, % 8 == 0), 16-byte aligned.
+ *   cols              a multiple of 32, 32 to 2^20.
+ *   w_dev             packed codes of `rows` rows, bsq_packed_row_bytes(fmt, cols) bytes each, 16-byte aligned.
+ *   w_scales5d_dev    bsq_scales5d_bytes(fmt, rows, cols) bytes, 16-byte aligned.  Scale bytes are as bsq_quantize writes
+ *                     them (no NaN codes).
+ *   w_sf_dev          NVFP4: one float (> 0), the weights' tensor scale; ignored for MX.
+ *   add_dev           NULL, or values of the output's type: (tokens, rows) with row stride ld_add (>= rows), or, with
+ *                     ld_add == 0, one row for every token.  May be out_dev itself.
+ *   out_dtype         dtype, or BSQ_F32.
+ *   out_dev           (tokens, rows), row stride ld_out (>= rows).
+ *   tokens, rows      0 to 2^20 (0 = no-op).
+ * Sums are FP32 (of a token's values relative to its largest, for MX weights), rounded once to the output's type.  BF16 values of x are held in FP16 times a power of two of their
+ * token: exact but for values below 2^-31 of the token's largest, which are off by at most 2^-39 of that.
+ */
+BSQ_API int32_t bsq_packed_linear(int32_t fmt, int32_t dtype, const void* x_dev, int64_t tokens, int64_t cols, int64_t ld_x,
+                                  const void* w_dev, const void* w_scales5d_dev, int64_t rows, const float* w_sf_dev,
+                                  const void* add_dev, int64_t ld_add, int32_t out_dtype, void* out_dev, int64_t ld_out,
+                                  void* stream);
+
+/*
+ * Norm and rotation of query and key heads, in one pass.  Per token and head, with a weight given:
+ * u = x / sqrt(mean(x^2) + eps) * weight (without: u = x); then, for the first `pairs` pairs of u,
+ *   (u_a, u_b) -> (u_a cos t - u_b sin t, u_b cos t + u_a sin t),  t = position * inv_freq[i],
+ * pairs (i, i + pairs), or (2i, 2i + 1) with `interleaved`; elements from 2 * pairs on pass.
+ *   dtype             bsq_dtype of queries and keys: BSQ_BF16 or BSQ_F16.
+ *   q_dev, k_dev      (tokens, heads, dim) and (tokens, kv_heads, dim), strides in elements (multiples of 8), 16-byte
+ *                     aligned.  heads or kv_heads may be 0 (at most 4096 each).
+ *   dim               8 to 256, a multiple of 8; 0 <= 2 * pairs <= dim.
+ *   positions_dev     int32[tokens]; a token at a negative position is left out (its rows of the outputs stay as they are).
+ *   inv_freq_dev      float[pairs].
+ *   q_weight_dev, k_weight_dev   NULL (no norm), or dim values of weight_dtype: dtype or BSQ_F32.
+ *   eps               >= 0.
+ *   q_out_dev, k_out_dev   outputs, strided like the inputs; each may be its input itself, and must not overlap it otherwise.
+ * Angles are exact up to their rounding to FP32 as a fraction of a turn, at any position; arithmetic is FP32, rounded once.
+ */
+BSQ_API int32_t bsq_qk_norm_rope(int32_t dtype, const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, const void* k_dev,
+                                 int64_t k_token_stride, int64_t k_head_stride, int64_t tokens, int32_t heads, int32_t kv_heads,
+                                 int32_t dim, const int32_t* positions_dev, const float* inv_freq_dev, int32_t pairs,
+                                 int32_t interleaved, const void* q_weight_dev, const void* k_weight_dev, int32_t weight_dtype,
+                                 float eps, void* q_out_dev, int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out_dev,
+                                 int64_t k_out_token_stride, int64_t k_out_head_stride, void* stream);
+
+/*
+ * Routing: the experts of each token and their weights.
+ *   dtype             bsq_dtype of the logits (BSQ_F32 too).
+ *   logits_dev        (tokens, experts), row stride ld_logits (>= experts).
+ *   experts           1 to 1024; 1 <= top_k <= 16.
+ *   sigmoid           0: scores p = softmax(logits); else p = 1 / (1 + exp(-logit)).
+ *   bias_dev          NULL, or float[experts]: an expert's value is p + bias, without a bias its logit.
+ *   groups            1 to 32, a divisor of experts: consecutive experts form groups, of which the top_groups with the largest
+ *                     scores stay (equal ones: the first).  A group's score is its largest value (group_top 1) or the sum of its
+ *                     two largest (group_top 2; without a bias the two largest p).  top_k experts fit into top_groups groups.
+ * Chosen are the top_k largest values among the groups that stay, in falling order, equal ones lowest expert first; weights are
+ * their p, divided by their sum where renormalize != 0 (0 where that is 0), times `scale`.
+ * Where p enters a comparison it is held to about 2^-45, so the choice is that of exact arithmetic but for values
+ * closer than that.  Logits (and biases) of -inf exclude an expert: p counts as 0 (with a logit of -inf), its value as -inf; experts
+ * outside the groups that stay count as -inf too.  Logits or biases of NaN or +inf count as -inf and record BSQ_ERR_VALUE.
+ *   ids_dev, weights_dev   int32 and float (tokens, top_k).
+ */
+BSQ_API int32_t bsq_moe_route(int32_t dtype, const void* logits_dev, int64_t ld_logits, int64_t tokens, int32_t experts, int32_t top_k,
+                              int32_t sigmoid, const float* bias_dev, int32_t groups, int32_t top_groups, int32_t group_top,
+                              int32_t renormalize, float scale, int32_t* ids_dev, float* weights_dev, void* stream);
+
+/*
+ * The rows of routed pairs, for the grouped calls with one group per expert (G = experts, expert_ids 0 to experts - 1):
+ * pairs sorted by expert, equal experts in the order of ids.
+ *   ids_dev           int32 (tokens, top_k), contiguous.  Negative: the pair has no row.  Ids past the last expert record
+ *                     BSQ_ERR_VALUE and count as negative.  An expert may come twice for a token.
+ *   experts           1 to 1024; top_k 1 to 1024; tokens * top_k <= 2^30.
+ *   row_offsets_dev   uint32[experts + 1]: expert e owns the rows [row_offsets[e], row_offsets[e + 1]).
+ *   scales_offsets_dev   uint32[experts + 1]: prefix sums of the experts' row counts, each rounded up to 128.
+ *   row_indices_dev   int32[tokens * top_k]: each row's token; 0 behind the last row.
+ *   positions_dev     int32 (tokens, top_k): each pair's row, -1 without one.
+ */
+BSQ_API int32_t bsq_moe_rows(const int32_t* ids_dev, int64_t tokens, int32_t top_k, int32_t experts, uint32_t* row_offsets_dev,
+                             uint32_t* scales_offsets_dev, int32_t* row_indices_dev, int32_t* positions_dev, void* stream);
 
 /*
  * Self-test of the device-side failure path: enqueues a one-warp kernel that
