@@ -3,6 +3,7 @@
 
 #include "host_common.h"
 #include "packed_linear.cuh"
+#include "packed_many.cuh"
 
 namespace {
 
@@ -42,11 +43,80 @@ bsq_status launch_linear(PlArgs& a, const HostDevice& d, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
 }
 
+bool linear_map(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, int64_t inner, int64_t rows, int64_t stride_bytes,
+                uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  auto enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(stride_bytes)};
+  const cuuint32_t box[2] = {box_inner, box_rows}, ones[2] = {1, 1};
+  return enc(map, type, 2, const_cast<void*>(ptr), dim, stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kPmSmem = 227 * 1024 - 2048;  // dynamic shared memory at most: one block per SM
+
+template <int FMT, bool F16, int MT>
+bsq_status launch_many(const PlArgs& p, const HostDevice& d, cudaStream_t st) {
+  using F = PmFmt<FMT>;
+  auto kernel = packed_many_kernel<FMT, F16, MT>;
+  PmArgs a{};
+  a.p = p;
+  a.err = d.error_word;
+  constexpr int kMost = 256 / MT;
+  a.token_tiles = static_cast<int>(ceil_div(p.tokens, kMost));
+  a.tokens_tile = static_cast<int>(ceil_div(ceil_div(p.tokens, a.token_tiles), 16) * 16);
+  a.row_tiles = static_cast<int>(ceil_div(p.rows, 128 * MT));
+  a.steps = static_cast<int>(ceil_div(p.cols, kPmCols));
+  const int64_t tiles = static_cast<int64_t>(a.row_tiles) * a.token_tiles;
+  if (tiles >= (int64_t(1) << 31)) return BSQ_ERR_SHAPE;
+  // blocks of a cluster, which share K: the number that ends first, where a block costs its steps and about eight more
+  int ranks = 1;
+  int64_t best = INT64_MAX;
+  for (int r = 1; r <= 8 && tiles <= d.sm_count; ++r) {
+    const int64_t share = ceil_div(a.steps, r), cost = ceil_div(tiles * r, d.sm_count) * (share + 8);
+    if (ceil_div(a.steps, share) == r && cost < best) {
+      best = cost;
+      ranks = r;
+    }
+  }
+  a.x_bytes = a.tokens_tile * 128;
+  a.w_bytes = static_cast<int>(ceil_div(MT * (F::kTileBytes + F::kAtoms * 512), 1024) * 1024);
+  // a step of weights and two of tokens at a time, as often as they fit
+  a.w_stages = std::min({kPmMaxStages / 2, (kPmSmem - 1024) / (a.w_bytes + 2 * a.x_bytes)});
+  a.x_stages = std::min(kPmMaxStages, (kPmSmem - 1024 - a.w_stages * a.w_bytes) / a.x_bytes);
+  // more than half of the SM's memory, and the sums of a cluster's block
+  const int smem = std::max({1024 + a.w_stages * a.w_bytes + a.x_stages * a.x_bytes, 120 * 1024,
+                             ranks > 1 ? 1024 + a.tokens_tile * 128 * MT * 4 : 0});
+  CUtensorMap mw, mx;
+  if (!linear_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, p.row_bytes, p.rows, p.row_bytes, F::kRowBytes, 128,
+                  FMT == kMXFP8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !linear_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT16, p.x, p.cols, p.tokens, p.ld_x * 2, 64, a.tokens_tile, CU_TENSOR_MAP_SWIZZLE_128B))
+    return BSQ_ERR_CUDA;
+  if (bsq_status s = allow_smem(reinterpret_cast<const void*>(kernel), kPmSmem, d.index); s != BSQ_OK) return s;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ranks > 1 ? tiles : std::min<int64_t>(tiles, d.sm_count)), ranks);
+  cfg.blockDim = dim3(kPmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = ranks;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, mw, mx, a) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
+}
+
 template <int FMT, bool F16>
 bsq_status launch_linear_tokens(PlArgs& a, const HostDevice& d, cudaStream_t st) {
   if (a.tokens <= 8) return launch_linear<FMT, F16, 1>(a, d, st);
   if (a.tokens <= 16) return launch_linear<FMT, F16, 2>(a, d, st);
-  return launch_linear<FMT, F16, 4>(a, d, st);
+  if (a.tokens <= 128) return launch_many<FMT, F16, 2>(a, d, st);
+  return launch_many<FMT, F16, 1>(a, d, st);
 }
 
 }  // namespace
