@@ -67,30 +67,31 @@ bsq_status launch_many(const PlArgs& p, const HostDevice& d, cudaStream_t st) {
   a.token_tiles = static_cast<int>(ceil_div(p.tokens, kMost));
   a.tokens_tile = static_cast<int>(ceil_div(ceil_div(p.tokens, a.token_tiles), 16) * 16);
   a.row_tiles = static_cast<int>(ceil_div(p.rows, 128 * MT));
-  a.steps = static_cast<int>(ceil_div(p.cols, kPmCols));
+  a.stages = static_cast<int>(ceil_div(p.cols, F::kCols));
   const int64_t tiles = static_cast<int64_t>(a.row_tiles) * a.token_tiles;
   if (tiles >= (int64_t(1) << 31)) return BSQ_ERR_SHAPE;
-  // blocks of a cluster, which share K: the number that ends first, where a block costs its steps and about eight more
+  // blocks of a cluster, which share K: the number that ends first, where a block costs its stages and about four more, and
+  // clusters are held by as many SMs as have room for whole ones
+  static constexpr int kResident[9] = {0, 152, 152, 138, 144, 140, 138, 105, 120};  // blocks of clusters of 1 to 8, of 152 SMs
   int ranks = 1;
   int64_t best = INT64_MAX;
-  for (int r = 1; r <= 8 && tiles <= d.sm_count; ++r) {
-    const int64_t share = ceil_div(a.steps, r), cost = ceil_div(tiles * r, d.sm_count) * (share + 8);
-    if (ceil_div(a.steps, share) == r && cost < best) {
+  for (int r = 1; r <= 8 && tiles < d.sm_count; ++r) {
+    const int64_t share = ceil_div(a.stages, r), cost = ceil_div(tiles * r, kResident[r]) * (share + 4);
+    if (ceil_div(a.stages, share) == r && cost < best) {
       best = cost;
       ranks = r;
     }
   }
   a.x_bytes = a.tokens_tile * 128;
   a.w_bytes = static_cast<int>(ceil_div(MT * (F::kTileBytes + F::kAtoms * 512), 1024) * 1024);
-  // a step of weights and two of tokens at a time, as often as they fit
-  a.w_stages = std::min({kPmMaxStages / 2, (kPmSmem - 1024) / (a.w_bytes + 2 * a.x_bytes)});
+  // halves of a step of tokens: four at least; stages of weights: what is left, at most as many as those four need twice over
+  a.w_stages = std::min(5, (kPmSmem - 1024 - 4 * a.x_bytes) / a.w_bytes);
   a.x_stages = std::min(kPmMaxStages, (kPmSmem - 1024 - a.w_stages * a.w_bytes) / a.x_bytes);
   // more than half of the SM's memory, and the sums of a cluster's block
   const int smem = std::max({1024 + a.w_stages * a.w_bytes + a.x_stages * a.x_bytes, 120 * 1024,
                              ranks > 1 ? 1024 + a.tokens_tile * 128 * MT * 4 : 0});
   CUtensorMap mw, mx;
-  if (!linear_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, p.row_bytes, p.rows, p.row_bytes, F::kRowBytes, 128,
-                  FMT == kMXFP8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+  if (!linear_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, p.row_bytes, p.rows, p.row_bytes, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !linear_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT16, p.x, p.cols, p.tokens, p.ld_x * 2, 64, a.tokens_tile, CU_TENSOR_MAP_SWIZZLE_128B))
     return BSQ_ERR_CUDA;
   if (bsq_status s = allow_smem(reinterpret_cast<const void*>(kernel), kPmSmem, d.index); s != BSQ_OK) return s;

@@ -9,8 +9,8 @@
 // relative to their row's largest scale, exact down to 2^-36 (E2M1) and 2^-21 (E4M3) of it, and off by at most 2^-35 (2^-23) of it below.
 //
 // Form.  A block takes MT (1, 2) tiles of 128 rows and up to 256 / MT tokens, K in steps of 128 columns: warp 0 streams codes and scales
-// (one ring) and the tokens' columns (another) by TMA, warps 4-11 convert (with one tile the two groups of four take turns, with
-// two each has its own), warp 1 issues the products, FP32 in tensor memory; the converters then store the tile.  One
+// (one ring) and the tokens' columns (another) by TMA, warps 4-19 convert (groups of four that take turns, all with one tile, two per tile with
+// two), warp 1 issues the products, FP32 in tensor memory; the converters then store the tile.  One
 // tile of 256 tokens asks shared memory for 64 bytes per clock and converts 16 weights per clock; two tiles of 128 would ask for as
 // much and convert twice as many; for fewer tokens two tiles halve how often those are read.  Where rows are few, the blocks of a
 // cluster share K and add their sums through distributed shared memory, in their order.
@@ -24,23 +24,25 @@
 
 namespace bsq {
 
-constexpr int kPmThreads = 384, kPmCols = 128;  // columns of a step
+constexpr int kPmConverters = 16;  // warps
+constexpr int kPmThreads = 32 * (4 + kPmConverters);
 constexpr int kPmMaxStages = 12;
 
 struct PmArgs {
   PlArgs p;
   int tokens_tile;        // of a block, a multiple of 16
   int row_tiles, token_tiles;
-  int steps;              // of a row, in all
+  int stages;             // of weights in a row, in all
   int x_stages, w_stages, x_bytes, w_bytes;
   unsigned int* err;
 };
 
-// Rows of codes and scale atoms of a step and tile.
+// A stage of weights: 128 bytes of each row of a tile, and their scale atoms.  It is converted in steps of 128 columns and
+// multiplied in halves of a step, 64 columns, a stage of the tokens each.
 template <int FMT> struct PmFmt {
-  static constexpr int kRowBytes = FMT == kMXFP8 ? 128 : 64;
-  static constexpr int kTileBytes = 128 * kRowBytes;
-  static constexpr int kAtoms = FMT == kNVFP4 ? 2 : 1;
+  static constexpr int kCols = FMT == kMXFP8 ? 128 : 256, kSteps = kCols / 128;
+  static constexpr int kTileBytes = 128 * 128;
+  static constexpr int kAtoms = kCols / Fmt<FMT>::ATOM_COLS;
 };
 
 // D (128 x N, FP32) (+)= A B^T, K = 64: A from tensor memory (packed pairs, 8 columns per 16), B K-major with the 128-byte swizzle.
@@ -96,16 +98,76 @@ __device__ __forceinline__ void pm_factors(const uint32_t (&word)[2], int top, u
   }
 }
 
+// The codes of 32 columns of a row of 128 bytes, as FP16: one 16-byte piece of E2M1 (piece c), two of E4M3 (2 c and 2 c + 1).
+// The pieces lie where the 128-byte swizzle puts them (swz: row mod 8).
+template <int FMT>
+__device__ __forceinline__ void pm_codes(const uint8_t* row, int c, int swz, uint32_t (&v)[16]) {
+  if constexpr (FMT == kMXFP8) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const uint4 x = *reinterpret_cast<const uint4*>(row + (((2 * c + p) ^ swz) << 4));
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[8 * p + 2 * i] = e4m3x2_to_f16x2(u[i] & 0xFFFFu);
+        v[8 * p + 2 * i + 1] = e4m3x2_to_f16x2(u[i] >> 16);
+      }
+    }
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4*>(row + ((c ^ swz) << 4));
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t p[4];
+      e2m1x8_to_f16(u[i], p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * i + j] = p[j];
+    }
+  }
+}
+
+// One row's values of up to 32 tokens: times f, plus add where there is one, to rows `ld` apart.
+template <bool F16, typename T>
+__device__ __forceinline__ void pm_store(const float (&y)[32], float f, int n, T* out, int64_t ld, const T* add, int64_t ld_add) {
+#pragma unroll
+  for (int i0 = 0; i0 < 32; i0 += 8) {
+    T x[8];
+    if (add != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i0 + i < n) {
+          x[i] = *add;
+          add += ld_add;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i0 + i >= n) return;
+      float s = y[i0 + i] * f;
+      if constexpr (sizeof(T) == 4) {
+        if (add != nullptr) s += x[i];
+        *out = s;
+      } else {
+        if (add != nullptr) s += elem2_to_f32x2<F16>(x[i]).x;
+        *out = static_cast<uint16_t>(f32x2_to_elem2<F16>(s, 0.f));
+      }
+      out += ld;
+    }
+  }
+}
+
 // MT: tiles of 128 rows that a block takes.
 template <int FMT, bool F16, int MT>
 __global__ void __launch_bounds__(kPmThreads, 1)
     packed_many_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const PmArgs a) {
   using F = PmFmt<FMT>;
-  constexpr int kABufs = MT == 1 ? 4 : 2, kACol = 256, kABufCols = 64 * MT, kDCol = 128;  // tensor memory: D, second D, A
+  // tensor memory: the tiles' sums, then the weights in buffers of half a step, 32 columns per tile
+  constexpr int kMaxBufs = 8, kBufCols = 32 * MT;
+  const uint32_t d_col = a.tokens_tile <= 64 ? 64 : 128, a_col = MT == 1 ? 256 : 2 * d_col, a_bufs = (512 - a_col) / kBufCols;  // 8; 6 or 4
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t x_full[kPmMaxStages], x_empty[kPmMaxStages], w_full[kPmMaxStages], w_empty[kPmMaxStages];
-  __shared__ uint64_t a_full[kABufs], a_empty[kABufs], d_full, d_empty, drain_bar;
+  __shared__ uint64_t a_full[kMaxBufs], a_empty[kMaxBufs], d_full, d_empty, drain_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag, x_fills, w_fills;
 
@@ -113,8 +175,9 @@ __global__ void __launch_bounds__(kPmThreads, 1)
   const int ranks = gridDim.y;  // of the cluster
   uint8_t* const xs = smem;
   uint8_t* const ws = smem + a.x_stages * a.x_bytes;
-  const int share = static_cast<int>((a.steps + ranks - 1) / ranks);
-  const int k_lo = blockIdx.y * share, k_hi = min(k_lo + share, a.steps);
+  const int share = (a.stages + ranks - 1) / ranks;
+  const int k_lo = blockIdx.y * share, k_hi = min(k_lo + share, a.stages);  // of the block's share of K
+  const int col0 = k_lo * F::kCols, halves = (min(k_hi * F::kCols, a.p.cols) - col0 + 63) / 64, steps = (halves + 1) / 2;
   const int n_tok = a.tokens_tile;
   if (tid == 0) {
     for (int i = 0; i < a.x_stages; ++i) {
@@ -123,14 +186,14 @@ __global__ void __launch_bounds__(kPmThreads, 1)
     }
     for (int i = 0; i < a.w_stages; ++i) {
       mbar_init(&w_full[i], 1);
-      mbar_init(&w_empty[i], 4 * MT);
+      mbar_init(&w_empty[i], kPmConverters);
     }
-    for (int i = 0; i < kABufs; ++i) {
+    for (int i = 0; i < kMaxBufs; ++i) {
       mbar_init(&a_full[i], 4 * MT);
       mbar_init(&a_empty[i], 1);
     }
     mbar_init(&d_full, 1);
-    mbar_init(&d_empty, 8);
+    mbar_init(&d_empty, kPmConverters);
     mbar_init(&drain_bar, 1);
     abort_flag = 0u;
     x_fills = w_fills = 0u;
@@ -150,35 +213,45 @@ __global__ void __launch_bounds__(kPmThreads, 1)
     abort_flag = 1u;
   };
 
-  if (warp == 0) {
-    // ---- copies
+  if (warp == 2) {
+    // ---- copies of weights
     if (lane == 0) {
-      uint32_t xn = 0, wn = 0;
+      uint32_t n = 0;
       bool ok = true;
       for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const int rt = tile % a.row_tiles, tt = tile / a.row_tiles;
-        for (int k = k_lo; k < k_hi && ok; ++k) {
-          const uint32_t s = wn % a.w_stages;
-          ok = mbar_wait_clocked(&w_empty[s], (wn / a.w_stages & 1u) ^ 1u, &abort_flag);
+        const int band0 = tile / a.token_tiles * MT;
+        const int bands = min(MT, static_cast<int>((a.p.rows - static_cast<int64_t>(band0) * 128 + 127) / 128));
+        for (int k = k_lo; k < k_hi; ++k) {
+          const uint32_t s = n % a.w_stages;
+          ok = mbar_wait_clocked(&w_empty[s], (n / a.w_stages & 1u) ^ 1u, &abort_flag);
           if (!ok) break;
           uint8_t* w = ws + s * a.w_bytes;
           const int atoms = min(F::kAtoms, a.p.k_atoms - k * F::kAtoms);
-          const int bands = min(MT, static_cast<int>((a.p.rows - static_cast<int64_t>(rt) * MT * 128 + 127) / 128));
           mbar_arrive_expect_tx(&w_full[s], bands * (F::kTileBytes + atoms * 512));
           for (int m = 0; m < bands; ++m) {
-            tma_load_2d(w + m * F::kTileBytes, &map_w, k * F::kRowBytes, (rt * MT + m) * 128, &w_full[s]);
+            tma_load_2d(w + m * F::kTileBytes, &map_w, k * 128, (band0 + m) * 128, &w_full[s]);
             bulk_load(w + MT * F::kTileBytes + m * F::kAtoms * 512,
-                      a.p.scales + (static_cast<int64_t>(rt * MT + m) * a.p.k_atoms + k * F::kAtoms) * 512, atoms * 512, &w_full[s]);
+                      a.p.scales + (static_cast<int64_t>(band0 + m) * a.p.k_atoms + k * F::kAtoms) * 512, atoms * 512, &w_full[s]);
           }
-          w_fills = ++wn;
-          for (int h = 0; h < 2 && 2 * k * 64 + h * 64 < a.p.cols; ++h) {
-            const uint32_t t = xn % a.x_stages;
-            ok = mbar_wait_clocked(&x_empty[t], (xn / a.x_stages & 1u) ^ 1u, &abort_flag);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&x_full[t], a.x_bytes);
-            tma_load_2d(xs + t * a.x_bytes, &map_x, (2 * k + h) * 64, tt * n_tok, &x_full[t]);
-            x_fills = ++xn;
-          }
+          w_fills = ++n;
+        }
+      }
+      if (!ok) fail();
+    }
+  } else if (warp == 0) {
+    // ---- copies of tokens
+    if (lane == 0) {
+      uint32_t n = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        const int y = tile % a.token_tiles * n_tok;
+        for (int h = 0; h < halves; ++h) {
+          const uint32_t s = n % a.x_stages;
+          ok = mbar_wait_clocked(&x_empty[s], (n / a.x_stages & 1u) ^ 1u, &abort_flag);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&x_full[s], a.x_bytes);
+          tma_load_2d(xs + s * a.x_bytes, &map_x, col0 + h * 64, y, &x_full[s]);
+          x_fills = ++n;
         }
       }
       if (!ok) fail();
@@ -188,27 +261,22 @@ __global__ void __launch_bounds__(kPmThreads, 1)
     const uint32_t lead = t5_elect();
     const uint32_t idesc = t5_idesc_f16(n_tok, false) | (F16 ? 0u : (1u << 7) | (1u << 10));
     const auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(~0u, mbar_wait_clocked(bar, parity, &abort_flag)); };
-    uint32_t xn = 0, an = 0, done = 0;
+    uint32_t n = 0, done = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++done) {
-      const int rt = tile % a.row_tiles;
-      const bool two = MT == 2 && static_cast<int64_t>(rt * MT + 1) * 128 < a.p.rows;
+      const bool two = MT == 2 && static_cast<int64_t>(tile / a.token_tiles * MT + 1) * 128 < a.p.rows;
       ok = wait(&d_empty, (done & 1u) ^ 1u);
-      for (int k = k_lo; k < k_hi && ok; ++k, ++an) {
-        const uint32_t b = an % kABufs;
-        ok = wait(&a_full[b], an / kABufs & 1u);
-        for (int h = 0; h < 2 && ok && (2 * k + h) * 64 < a.p.cols; ++h, ++xn) {
-          const uint32_t t = xn % a.x_stages;
-          ok = wait(&x_full[t], xn / a.x_stages & 1u);
-          if (!ok) break;
-          t5_fence_after();
-          const uint64_t db = t5_desc_sw128(smem_addr(xs + t * a.x_bytes));
-          const uint32_t acc = k > k_lo || h > 0;
-          pm_mma64(tmem, tmem + kACol + b * kABufCols + 32 * h, db, idesc, acc, lead);
-          if (two) pm_mma64(tmem + kDCol, tmem + kACol + b * kABufCols + 64 + 32 * h, db, idesc, acc, lead);
-          t5_commit(smem_addr(&x_empty[t]), lead);
-        }
-        if (ok) t5_commit(smem_addr(&a_empty[b]), lead);
+      for (int h = 0; h < halves && ok; ++h, ++n) {
+        const uint32_t b = n % a_bufs, s = n % a.x_stages;
+        ok = wait(&a_full[b], n / a_bufs & 1u) && wait(&x_full[s], n / a.x_stages & 1u);
+        if (!ok) break;
+        t5_fence_after();
+        const uint64_t db = t5_desc_sw128(smem_addr(xs + s * a.x_bytes));
+        const uint32_t ta = tmem + a_col + b * kBufCols;
+        pm_mma64(tmem, ta, db, idesc, h > 0, lead);
+        if (two) pm_mma64(tmem + d_col, ta + 32, db, idesc, h > 0, lead);
+        t5_commit(smem_addr(&x_empty[s]), lead);
+        t5_commit(smem_addr(&a_empty[b]), lead);
       }
       if (ok) t5_commit(smem_addr(&d_full), lead);
     }
@@ -217,127 +285,111 @@ __global__ void __launch_bounds__(kPmThreads, 1)
     if (!mbar_wait_clocked(&drain_bar, 0) && lane == 0) record_error_at(a.err, kErrTimeout);
   } else if (warp >= 4) {
     // ---- conversion, then the tile's output; a thread per row
-    const int group = (warp - 4) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
+    // the groups of four warps of a tile take turns with its steps
+    constexpr int kTurns = kPmConverters / 4 / MT;
+    const int group = (warp - 4) >> 2, m = group / kTurns, turn = group % kTurns, quarter = warp & 3, r = 32 * quarter + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-    const float sf = FMT == kNVFP4 ? __ldg(a.p.sf) : 1.f;
-    uint32_t n = 0, done = 0;
+    const float inv = FMT == kNVFP4 ? __fdiv_rn(1.f, __ldg(a.p.sf)) : 1.f;
+    uint32_t wn = 0, done = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++done) {
-      const int rt = tile % a.row_tiles, tt = tile / a.row_tiles;
-      const int m = MT == 2 ? group : 0;
+      const int rt = tile / a.token_tiles, tt = tile % a.token_tiles;
       const int64_t band = static_cast<int64_t>(rt) * MT + m, row = band * 128 + r;
       const bool idle = band * 128 >= a.p.rows;  // the second tile lies behind the last row
       int top = 0;  // with FP16 tokens and MX: the row's largest scale byte
       if constexpr (F16 && FMT != kNVFP4) {
         if (!idle) {
           const uint8_t* s = a.p.scales + band * a.p.k_atoms * 512 + lane * 16 + quarter * 4;
-          for (int k = k_lo; k < k_hi; ++k) {
-            const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(s + static_cast<int64_t>(k) * 512));
+          for (int c = col0; c < col0 + halves * 64; c += 128) {
+            const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(s + static_cast<int64_t>(c / 128) * 512));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (k * 128 + 32 * i < a.p.cols) top = max(top, static_cast<int>(w >> (8 * i) & 255u));
+              if (c + 32 * i < a.p.cols) top = max(top, static_cast<int>(w >> (8 * i) & 255u));
           }
         }
       }
-      for (int k = k_lo; k < k_hi && ok; ++k, ++n) {
-        if (MT == 1 && (n & 1u) != static_cast<uint32_t>(group)) continue;
-        const uint32_t s = n % a.w_stages, b = n % kABufs;
-        ok = __all_sync(~0u, mbar_wait_clocked(&w_full[s], n / a.w_stages & 1u, &abort_flag) &&
-                                 mbar_wait_clocked(&a_empty[b], (n / kABufs & 1u) ^ 1u, &abort_flag));
-        if (!ok) break;
-        t5_fence_after();
-        if (!idle) {
-          const uint8_t* w = ws + s * a.w_bytes + m * F::kTileBytes + r * F::kRowBytes;
-          const uint8_t* sc = ws + s * a.w_bytes + MT * F::kTileBytes + m * F::kAtoms * 512 + lane * 16 + quarter * 4;
-          uint32_t word[2] = {*reinterpret_cast<const uint32_t*>(sc), 0u};
-          if (FMT == kNVFP4 && k * 128 + 64 < a.p.cols) word[1] = *reinterpret_cast<const uint32_t*>(sc + 512);
-          uint32_t f[8];
+      for (int k = 0; k < k_hi - k_lo && ok; ++k, ++wn) {
+        const uint32_t s = wn % a.w_stages;
+        // every group waits for and gives back every stage, converted by it or not: a barrier's parity tells only neighbouring
+        // phases apart, so none may pass unseen
+        ok = __all_sync(~0u, mbar_wait_clocked(&w_full[s], wn / a.w_stages & 1u, &abort_flag));
+#pragma unroll 1
+        for (int j = 0; j < F::kSteps && ok; ++j) {
+          const uint32_t step = k * F::kSteps + j;  // of the tile
+          if (step >= static_cast<uint32_t>(steps) || (done * steps + step) % kTurns != static_cast<uint32_t>(turn)) continue;
+          const uint8_t* w = ws + s * a.w_bytes + m * F::kTileBytes + r * 128;
+          uint32_t word[2] = {0u, 0u}, f[8];
+          bool wide = false;  // past BF16's range (2^127 more than 2^-112): a second factor
+          if (!idle) {
+            constexpr int kStepAtoms = F::kAtoms / F::kSteps;
+            const uint8_t* sc = ws + s * a.w_bytes + MT * F::kTileBytes + (m * F::kAtoms + j * kStepAtoms) * 512 + lane * 16 + quarter * 4;
+            word[0] = *reinterpret_cast<const uint32_t*>(sc);
+            if (FMT == kNVFP4 && 2 * static_cast<int>(step) + 1 < halves) word[1] = *reinterpret_cast<const uint32_t*>(sc + 512);
+            if constexpr (!F16 && FMT != kNVFP4) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) wide |= (word[0] >> (8 * i) & 255u) > 142u;
+              wide = __any_sync(~0u, wide);
+            }
+          }
           pm_factors<FMT, F16>(word, top, f);
-          const uint32_t to = lanes + kACol + b * kABufCols + 64 * m;
-          // past BF16's range (2^127 more than 2^-112): a second factor
-          bool wide = false;
-          if constexpr (!F16 && FMT != kNVFP4) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) wide |= (word[0] >> (8 * i) & 255u) > 142u;
-            wide = __any_sync(~0u, wide);
-          }
+          for (int h = 0; h < 2; ++h) {
+            if (2 * static_cast<int>(step) + h >= halves) break;
+            const uint32_t n = done * halves + 2 * step + h, b = n % a_bufs;
+            // unambiguous: there are at least 2 kTurns buffers, so this group's last step knew the phase before
+            ok = __all_sync(~0u, mbar_wait_clocked(&a_empty[b], (n / a_bufs & 1u) ^ 1u, &abort_flag));
+            if (!ok) break;
+            t5_fence_after();
+            if (!idle) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {  // 32 columns each
-            uint32_t v[16];
-            if constexpr (FMT == kMXFP8) {
+              for (int q = 2 * h; q < 2 * h + 2; ++q) {  // 32 columns each
+                uint32_t v[16];
+                pm_codes<FMT>(w, 4 * j + q, r & 7, v);
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const uint4 x = *reinterpret_cast<const uint4*>(w + (((2 * q + c) ^ (r & 7)) << 4));
-                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  v[8 * c + 2 * i] = e4m3x2_to_f16x2(u[i] & 0xFFFFu);
-                  v[8 * c + 2 * i + 1] = e4m3x2_to_f16x2(u[i] >> 16);
+                for (int i = 0; i < 16; ++i) {
+                  const uint32_t g = FMT == kNVFP4 ? f[2 * q + i / 8] : f[q];
+                  v[i] = F16 ? mul_f16x2(v[i], g) : mul_bf16x2(pm_f16_to_bf16(v[i]), g);
                 }
+                if (!F16 && FMT != kNVFP4 && wide) {
+                  const int byte = word[0] >> (8 * q) & 255u;
+                  const uint32_t e = static_cast<uint32_t>(127 + max(byte + 112 - 254, 0)) << 7;
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) v[i] = mul_bf16x2(v[i], e | e << 16);
+                }
+                t5_st16(lanes + a_col + b * kBufCols + 32 * m + 16 * (q & 1), v);
               }
-            } else {
-              const uint4 x = *reinterpret_cast<const uint4*>(w + ((q ^ ((r >> 1) & 3)) << 4));
-              const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t p[4];
-                e2m1x8_to_f16(u[i], p);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[4 * i + j] = p[j];
-              }
+              t5_st_wait();
             }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint32_t g = FMT == kNVFP4 ? f[2 * q + i / 8] : f[q];
-              v[i] = F16 ? mul_f16x2(v[i], g) : mul_bf16x2(pm_f16_to_bf16(v[i]), g);
-            }
-            if (!F16 && FMT != kNVFP4 && wide) {
-              const int byte = word[0] >> (8 * q) & 255u;
-              const uint32_t e = static_cast<uint32_t>(127 + max(byte + 112 - 254, 0)) << 7;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = mul_bf16x2(v[i], e | e << 16);
-            }
-            t5_st16(to + 16 * q, v);
+            t5_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&a_full[b]);
           }
-          t5_st_wait();
         }
-        t5_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&w_empty[s]);
-          mbar_arrive(&a_full[b]);
-        }
+        if (ok && lane == 0) mbar_arrive(&w_empty[s]);
       }
       // ---- output
       if (ok) ok = __all_sync(~0u, mbar_wait_clocked(&d_full, done & 1u, &abort_flag));
       if (!ok) break;
       t5_fence_after();
       const int tok0 = tt * n_tok, toks = min(n_tok, a.p.tokens - tok0);
-      const float f = F16 && FMT != kNVFP4 ? pow2f(max(top, 1) - 127 - (FMT == kMXFP8 ? 7 : 13)) : 1.f;
+      const float f = F16 && FMT != kNVFP4 ? pow2f(max(top, 1) - 127 - (FMT == kMXFP8 ? 7 : 13)) : inv;
       if (!idle) {
-        for (int c0 = MT == 1 ? 32 * group : 0; c0 < n_tok; c0 += MT == 1 ? 64 : 32) {
+        for (int c0 = 32 * turn; c0 < toks; c0 += 32 * kTurns) {
           float y[32];
-          t5_ld32(lanes + kDCol * m + c0, y);
+          t5_ld32(lanes + d_col * m + c0, y);
+          const int n_out = min(32, toks - c0);
           if (ranks > 1) {
-            float* red = reinterpret_cast<float*>(smem);
+            float* red = reinterpret_cast<float*>(smem) + c0 * (128 * MT) + 128 * m + r;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (c0 + i < toks) red[(c0 + i) * (128 * MT) + 128 * m + r] = y[i] * f;
+              if (i < n_out) red[i * (128 * MT)] = y[i] * f;
           } else if (row < a.p.rows) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (c0 + i >= toks) break;
-              const int64_t tok = tok0 + c0 + i;
-              float s = y[i] * f;
-              if (FMT == kNVFP4) s = __fdiv_rn(s, sf);
-              if (a.p.out_f32) {
-                if (a.p.add) s += static_cast<const float*>(a.p.add)[tok * a.p.ld_add + row];
-                static_cast<float*>(a.p.out)[tok * a.p.ld_out + row] = s;
-              } else {
-                if (a.p.add) s += elem2_to_f32x2<F16>(static_cast<const uint16_t*>(a.p.add)[tok * a.p.ld_add + row]).x;
-                static_cast<uint16_t*>(a.p.out)[tok * a.p.ld_out + row] = static_cast<uint16_t>(f32x2_to_elem2<F16>(s, 0.f));
-              }
-            }
+            const int64_t at = (tok0 + c0) * a.p.ld_out + row, add_at = (tok0 + c0) * a.p.ld_add + row;
+            if (a.p.out_f32)
+              pm_store<F16>(y, f, n_out, static_cast<float*>(a.p.out) + at, a.p.ld_out, a.p.add ? static_cast<const float*>(a.p.add) + add_at : nullptr, a.p.ld_add);
+            else
+              pm_store<F16>(y, f, n_out, static_cast<uint16_t*>(a.p.out) + at, a.p.ld_out,
+                            a.p.add ? static_cast<const uint16_t*>(a.p.add) + add_at : nullptr, a.p.ld_add);
           }
           __syncwarp();
         }
@@ -366,24 +418,32 @@ __global__ void __launch_bounds__(kPmThreads, 1)
   }
   if (ranks > 1) {  // one tile per cluster: every block's sums are in its shared memory
     cluster_sync_all();
-    const int rt = blockIdx.x % a.row_tiles, tt = blockIdx.x / a.row_tiles;
+    const int rt = blockIdx.x / a.token_tiles, tt = blockIdx.x % a.token_tiles;
     const int tok0 = tt * n_tok, toks = min(n_tok, a.p.tokens - tok0);
+    // tokens me, me + ranks, ...: four rows a thread, their parts from all blocks at once
     const float* red = reinterpret_cast<const float*>(smem);
-    const float sf = FMT == kNVFP4 ? __ldg(a.p.sf) : 1.f;
-    const int me = blockIdx.y;
-    for (int e = tid; e < 128 * MT * ((toks - me + ranks - 1) / ranks); e += kPmThreads) {
-      const int t = me + e / (128 * MT) * ranks, r = e % (128 * MT);
+    constexpr int kQuads = 32 * MT;
+    const int me = blockIdx.y, n_out = toks > me ? (toks - me + ranks - 1) / ranks : 0;
+    for (int e = tid; e < kQuads * n_out; e += kPmThreads) {
+      const int t = me + e / kQuads * ranks, r = e % kQuads * 4;
       const int64_t row = static_cast<int64_t>(rt) * MT * 128 + r, tok = tok0 + t;
-      if (row >= a.p.rows) continue;
-      float s = 0.f;
-      for (int q = 0; q < ranks; ++q) s += __uint_as_float(cluster_ld_u32(cluster_map(red + t * 128 * MT + r, q)));
-      if (FMT == kNVFP4) s = __fdiv_rn(s, sf);
-      if (a.p.out_f32) {
-        if (a.p.add) s += static_cast<const float*>(a.p.add)[tok * a.p.ld_add + row];
-        static_cast<float*>(a.p.out)[tok * a.p.ld_out + row] = s;
-      } else {
-        if (a.p.add) s += elem2_to_f32x2<F16>(static_cast<const uint16_t*>(a.p.add)[tok * a.p.ld_add + row]).x;
-        static_cast<uint16_t*>(a.p.out)[tok * a.p.ld_out + row] = static_cast<uint16_t>(f32x2_to_elem2<F16>(s, 0.f));
+      float4 v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < ranks) v[q] = cluster_ld_f4(cluster_map(red + t * 128 * MT + r, q));
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < ranks) s[0] += v[q].x, s[1] += v[q].y, s[2] += v[q].z, s[3] += v[q].w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (row + i >= a.p.rows) break;
+        const int64_t at = tok * a.p.ld_out + row + i, add_at = tok * a.p.ld_add + row + i;
+        if (a.p.out_f32)
+          static_cast<float*>(a.p.out)[at] = a.p.add ? s[i] + static_cast<const float*>(a.p.add)[add_at] : s[i];
+        else
+          static_cast<uint16_t*>(a.p.out)[at] = static_cast<uint16_t>(f32x2_to_elem2<F16>(
+              a.p.add ? s[i] + elem2_to_f32x2<F16>(static_cast<const uint16_t*>(a.p.add)[add_at]).x : s[i], 0.f));
       }
     }
     cluster_sync_all();  // no block leaves while another reads its sums
