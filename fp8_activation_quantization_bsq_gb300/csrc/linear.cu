@@ -9,25 +9,35 @@ namespace {
 
 using namespace bsq;
 
-constexpr int kPlSmem = 113 * 1024;  // a block's dynamic shared memory at most: two per SM
-
-template <int FMT, bool F16, int NT>
+template <int FMT, bool F16, int NT, int RT>
 bsq_status launch_linear(PlArgs& a, const HostDevice& d, cudaStream_t st) {
-  auto kernel = packed_linear_kernel<FMT, F16, NT>;
-  constexpr int kCols = PlFmt<FMT>::kCols;
+  auto kernel = packed_linear_kernel<FMT, F16, NT, RT>;
+  constexpr int kCols = PlFmt<FMT>::kCols, kSplit = kPlWarps / RT;
   const int tile_tokens = std::min(a.tokens, NT * 8);
-  // blocks of a cluster: enough for two per SM, as long as every warp has a piece or two
-  const int64_t tiles = ceil_div(a.rows, 128) * 4 * ceil_div(a.tokens, NT * 8);
-  int ranks = 1;
-  while (ranks < 8 && tiles * ranks < 2 * d.sm_count && a.pieces >= 2 * ranks * kPlWarps) ranks *= 2;
-  a.per_rank = static_cast<int>(ceil_div(ceil_div(a.pieces, ranks), kPlWarps) * kPlWarps);
-  ranks = static_cast<int>(ceil_div(a.pieces, a.per_rank));
-  a.segment = kPlWarps;  // as many rounds of pieces as fit beside the rings
-  while (a.segment < a.per_rank && tile_tokens * ((a.segment + kPlWarps) * kCols * 2 + 64) <= kPlSmem - kPlRing) a.segment += kPlWarps;
+  constexpr int kStep = kSplit * kCols % 256 == 0 ? kSplit : 2 * kSplit;  // a segment is a multiple of 256 columns
+  static_assert(kStep * kCols % 256 == 0);
+  // blocks per SM, and what tokens each may hold beside its rings
+  const int per_sm = tile_tokens == 1 ? 3 : 2, room = (227 / per_sm - 2) * 1024 - kPlRing;
+  const int most = std::max(kStep, static_cast<int>((room / tile_tokens - 64) / (kStep * kCols * 2) * kStep));
+  // blocks of a cluster, which share K: the number that leaves the fullest SM the least to do, a block costing its pieces and about
+  // eight more for each segment of its tokens
+  const int64_t row_tiles = ceil_div(a.rows, 128) * 4 / RT, tiles = row_tiles * ceil_div(a.tokens, NT * 8);
+  a.per_rank = static_cast<int>(ceil_div(a.pieces, kSplit) * kSplit);
+  int64_t best = INT64_MAX;
+  for (int r = 1; r <= 8; ++r) {
+    const int64_t share = ceil_div(ceil_div(a.pieces, r), kSplit) * kSplit, blocks = ceil_div(a.pieces, share) * tiles;
+    const int64_t cost = ceil_div(blocks, d.sm_count) * (share + 8 * ceil_div(share, most));
+    if (cost < best) {
+      best = cost;
+      a.per_rank = static_cast<int>(share);
+    }
+  }
+  const int ranks = static_cast<int>(ceil_div(a.pieces, a.per_rank));
+  a.segment = std::min(most, static_cast<int>(ceil_div(a.per_rank, kStep) * kStep));
   const int smem = std::max(kPlRing + tile_tokens * (a.segment * kCols * 2 + 64), kPlWarps * NT * 8 * 32 * 4);
   if (bsq_status s = allow_smem(reinterpret_cast<const void*>(kernel), 227 * 1024 - 2048, d.index); s != BSQ_OK) return s;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ranks, static_cast<unsigned>(ceil_div(a.rows, 128) * 4), static_cast<unsigned>(ceil_div(a.tokens, NT * 8)));
+  cfg.gridDim = dim3(ranks, static_cast<unsigned>(row_tiles), static_cast<unsigned>(ceil_div(a.tokens, NT * 8)));
   cfg.blockDim = dim3(kPlThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -114,8 +124,10 @@ bsq_status launch_many(const PlArgs& p, const HostDevice& d, cudaStream_t st) {
 
 template <int FMT, bool F16>
 bsq_status launch_linear_tokens(PlArgs& a, const HostDevice& d, cudaStream_t st) {
-  if (a.tokens <= 8) return launch_linear<FMT, F16, 1>(a, d, st);
-  if (a.tokens <= 16) return launch_linear<FMT, F16, 2>(a, d, st);
+  if (a.tokens <= 2) return launch_linear<FMT, F16, 1, 1>(a, d, st);
+  if (a.tokens <= 8) return launch_linear<FMT, F16, 1, 2>(a, d, st);
+  if (a.tokens <= 16) return launch_linear<FMT, F16, 2, 4>(a, d, st);
+  if (a.tokens <= 32) return launch_linear<FMT, F16, 4, 4>(a, d, st);
   if (a.tokens <= 128) return launch_many<FMT, F16, 2>(a, d, st);
   return launch_many<FMT, F16, 1>(a, d, st);
 }

@@ -56,17 +56,18 @@ __device__ __forceinline__ void pm_mma64(uint32_t d, uint32_t a, uint64_t b, uin
 }
 #undef BSQ_PM_TS
 
-// FP16 pairs that hold E2M1 or E4M3 values -> BF16 pairs of 2^-112 of them: the exponent's and the top mantissa bits move down by
-// three (FP16's low mantissa bits are zero), the sign stays.
-__device__ __forceinline__ uint32_t pm_f16_to_bf16(uint32_t h) { return (h & 0x80008000u) | ((h >> 3) & 0x0FFF0FFFu); }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+// An FP16 pair times f -> a BF16 pair, by way of FP32 (exact for codes times scales).  Conversions and packed products use pipes of
+// their own: 38 codes a clock and SM; the same by shifts and masks of the FP16 bits 28, of the codes' bits 32.
+__device__ __forceinline__ uint32_t pm_scaled_bf16(uint32_t h, float f) {
+  float2 v = f16x2_to_f32x2(h);
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(v.x), "+f"(v.y)
+      : "f"(f));
+  return f32x2_to_elem2<false>(v.x, v.y);
 }
 
-// The factors of a row's step: NVFP4 eight, MX four, as pairs of the tokens' type; for BF16 2^112 times the scale (at most 2^127:
-// what lies past that is a second factor).  `top`: with FP16 tokens and MX, the byte that stands for 2^13 (E2M1) or 2^7 (E4M3).
+// The factors of a row's step: NVFP4 eight, MX four, as FP16 pairs or FP32 numbers.  `top`: with FP16 tokens and MX, the byte
+// that stands for 2^13 (E2M1) or 2^7 (E4M3).
 template <int FMT, bool F16>
 __device__ __forceinline__ void pm_factors(const uint32_t (&word)[2], int top, uint32_t (&f)[8]) {
   if constexpr (FMT == kNVFP4) {
@@ -78,22 +79,21 @@ __device__ __forceinline__ void pm_factors(const uint32_t (&word)[2], int top, u
         f[2 * i + 1] = __byte_perm(pair, 0, 0x3232);
       } else {
         const float2 s = f16x2_to_f32x2(pair);
-        f[2 * i] = f32x2_to_elem2<false>(s.x * 0x1p112f, s.x * 0x1p112f);
-        f[2 * i + 1] = f32x2_to_elem2<false>(s.y * 0x1p112f, s.y * 0x1p112f);
+        f[2 * i] = __float_as_uint(s.x);
+        f[2 * i + 1] = __float_as_uint(s.y);
       }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int byte = word[0] >> (8 * i) & 255u;
-      uint32_t one;
+      const uint32_t byte = word[0] >> (8 * i) & 255u;
       if constexpr (F16) {
-        const int e = byte - top + (FMT == kMXFP8 ? 7 : 13);  // at most 13
-        one = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
+        const int e = static_cast<int>(byte) - top + (FMT == kMXFP8 ? 7 : 13);  // at most 13
+        const uint32_t one = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
+        f[i] = one | one << 16;
       } else {
-        one = static_cast<uint32_t>(min(byte + 112, 254)) << 7;
+        f[i] = max(byte << 23, 0x00400000u);  // byte 0 is 2^-127
       }
-      f[i] = one | one << 16;
     }
   }
 }
@@ -319,17 +319,11 @@ __global__ void __launch_bounds__(kPmThreads, 1)
           if (step >= static_cast<uint32_t>(steps) || (done * steps + step) % kTurns != static_cast<uint32_t>(turn)) continue;
           const uint8_t* w = ws + s * a.w_bytes + m * F::kTileBytes + r * 128;
           uint32_t word[2] = {0u, 0u}, f[8];
-          bool wide = false;  // past BF16's range (2^127 more than 2^-112): a second factor
           if (!idle) {
             constexpr int kStepAtoms = F::kAtoms / F::kSteps;
             const uint8_t* sc = ws + s * a.w_bytes + MT * F::kTileBytes + (m * F::kAtoms + j * kStepAtoms) * 512 + lane * 16 + quarter * 4;
             word[0] = *reinterpret_cast<const uint32_t*>(sc);
             if (FMT == kNVFP4 && 2 * static_cast<int>(step) + 1 < halves) word[1] = *reinterpret_cast<const uint32_t*>(sc + 512);
-            if constexpr (!F16 && FMT != kNVFP4) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) wide |= (word[0] >> (8 * i) & 255u) > 142u;
-              wide = __any_sync(~0u, wide);
-            }
           }
           pm_factors<FMT, F16>(word, top, f);
 #pragma unroll
@@ -348,13 +342,7 @@ __global__ void __launch_bounds__(kPmThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                   const uint32_t g = FMT == kNVFP4 ? f[2 * q + i / 8] : f[q];
-                  v[i] = F16 ? mul_f16x2(v[i], g) : mul_bf16x2(pm_f16_to_bf16(v[i]), g);
-                }
-                if (!F16 && FMT != kNVFP4 && wide) {
-                  const int byte = word[0] >> (8 * q) & 255u;
-                  const uint32_t e = static_cast<uint32_t>(127 + max(byte + 112 - 254, 0)) << 7;
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) v[i] = mul_bf16x2(v[i], e | e << 16);
+                  v[i] = F16 ? mul_f16x2(v[i], g) : pm_scaled_bf16(v[i], __uint_as_float(g));
                 }
                 t5_st16(lanes + a_col + b * kBufCols + 32 * m + 16 * (q & 1), v);
               }
