@@ -1,4 +1,5 @@
-"""Compile libbsq (the CUDA kernels + C ABI) in-tree for sm_103a with nvcc."""
+"""Compile libbsq (the CUDA kernels + C ABI) in-tree for sm_103a with nvcc, and
+the compiled part of its Python binding with the host compiler."""
 from __future__ import annotations
 
 import os
@@ -11,6 +12,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_DIR = os.path.join(PKG_DIR, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libbsq.so")
+BINDING_PATH = os.path.join(LIB_DIR, "_bsq_binding.so")
 
 SOURCES = ["bsq.cu", "kv_cache.cu", "moe.cu", "linear.cu", "rope.cu", "route.cu"]
 HEADERS = ["host_common.h", "tcgen05.cuh", "serving_common.cuh", "kv_append.cuh", "kv_attention.cuh", "kv_prompt.cuh", "moe_layer.cuh",
@@ -26,20 +28,39 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build libbsq")
 
 
+BINDING = "binding.cpp"
+
+
 def _inputs():
-    return ([os.path.join(CSRC, s) for s in SOURCES + HEADERS]
+    return ([os.path.join(CSRC, s) for s in SOURCES + HEADERS + [BINDING]]
             + [os.path.join(INCLUDE, "bsq.h"), os.path.abspath(__file__)])
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
+def _binding_commands():
+    """Compile and link commands of the binding: torch's headers and libraries, libbsq beside it."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    obj = os.path.join(LIB_DIR, BINDING + ".o")
+    cxx = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-isystem", os.path.join(base, "include"), "-isystem",
+           os.path.join(base, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"), "-isystem",
+           sysconfig.get_paths()["include"], "-c", "-o", obj, os.path.join(CSRC, BINDING)]
+    link = ["g++", "-shared", "-o", BINDING_PATH + ".tmp", obj, "-L" + LIB_DIR, "-lbsq", "-L" + os.path.join(base, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    return cxx, link
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build ``_lib/libbsq.so`` (skipped when up to date); returns its path."""
+    """Build ``_lib/libbsq.so`` and the binding beside it (skipped when up to date); returns the library's path."""
     if not force and not is_stale():
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
@@ -49,13 +70,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             "-I", INCLUDE]
     # one compiler process per translation unit, all at once, then the link
     objects = [os.path.join(LIB_DIR, s + ".o") for s in SOURCES]
-    jobs = [base + ["-c", "-o", o, os.path.join(CSRC, s)] for s, o in zip(SOURCES, objects)]
+    binding, binding_link = _binding_commands()
+    jobs = [base + ["-c", "-o", o, os.path.join(CSRC, s)] for s, o in zip(SOURCES, objects)] + [binding]
     running = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in jobs]
     results = [(c, p.communicate()[0], p.returncode) for c, p in zip(jobs, running)]
+    def then(command):
+        res = subprocess.run(command, capture_output=True, text=True)
+        results.append((command, res.stdout + res.stderr, res.returncode))
+
     if all(rc == 0 for _, _, rc in results):
-        link = base + ["-shared", "-Xlinker", "-rpath,/usr/local/cuda/lib64", "-o", tmp] + objects
-        res = subprocess.run(link, capture_output=True, text=True)
-        results.append((link, res.stdout + res.stderr, res.returncode))
+        then(base + ["-shared", "-Xlinker", "-rpath,/usr/local/cuda/lib64", "-Xlinker", "-soname,libbsq.so", "-o", tmp] + objects)
+    if all(rc == 0 for _, _, rc in results):
+        os.replace(tmp, LIB_PATH)
+        then(binding_link)
     for cmd, text, rc in results:
         if verbose or rc != 0:
             print(" ".join(cmd))
@@ -63,7 +90,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     failed = [text for _, text, rc in results if rc != 0]
     if failed:
         raise RuntimeError("libbsq build failed:\n" + "\n".join(failed)[-4000:])
-    os.replace(tmp, LIB_PATH)
+    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
     return LIB_PATH
 
 
