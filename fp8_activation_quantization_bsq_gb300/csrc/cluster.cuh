@@ -14,6 +14,10 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Its two halves: what a thread does in between overlaps with the other blocks' arrival.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // The address of *p (this block's shared memory) in block `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_map(const void* p, int rank) {
   const uint32_t local = static_cast<uint32_t>(__cvta_generic_to_shared(p));

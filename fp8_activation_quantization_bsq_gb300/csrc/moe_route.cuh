@@ -4,7 +4,7 @@
 // (p grows with it); of equal groups of experts those with the largest sums of their one or two largest
 // values stay; then the top_k largest values, equal ones lowest expert first; weights p (/ their sum) * scale.
 // One warp per token, the logits in registers.  Which experts are chosen must not hang on how p was rounded: two
-// values may lie closer than FP32 tells apart.  Where p enters the comparison it is therefore held as a
+// values may lie closer than FP32 tells apart.  Where p enters such a comparison it is held as a
 // sum of two FP32 numbers (about 2^-45 of 1; RouteFF), whose order as (high, low) is the values' order; where logits are compared
 // they are exact as they are.  FP64 has no units to speak of on this GPU.
 //
@@ -52,12 +52,12 @@ __device__ __forceinline__ RouteFF ff_mul(RouteFF a, RouteFF b) {
   const float p = __fmul_rn(a.h, b.h);
   return ff_fast(p, __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.h, -p))));
 }
-__device__ __forceinline__ RouteFF ff_div(RouteFF a, RouteFF b) {
-  const float q = __fdiv_rn(a.h, b.h);
-  // a - q b, its leading part exact
-  const float p = __fmul_rn(q, b.h), e = __fmaf_rn(q, b.h, -p);
-  const float r = __fadd_rn(__fsub_rn(__fsub_rn(a.h, p), e), __fmaf_rn(-q, b.l, a.l));
-  return ff_fast(q, __fdiv_rn(r, b.h));
+// 1 / b for b between 1 and 2^20: an approximate reciprocal r and one Newton step, r (1 + e) with e = 1 - b r (its square is lost).
+__device__ __forceinline__ RouteFF ff_inverse(RouteFF b) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b.h));
+  const float e = __fmaf_rn(-b.l, r, __fmaf_rn(-b.h, r, 1.f));
+  return ff_fast(r, __fmul_rn(r, e));
 }
 __device__ __forceinline__ bool ff_greater(RouteFF a, RouteFF b) { return a.h > b.h || (a.h == b.h && a.l > b.l); }
 
@@ -99,6 +99,33 @@ __device__ __forceinline__ uint32_t route_key(float z) {
 }
 __device__ __forceinline__ float route_unkey(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k); }
 
+// What the choice of groups does with values: one FP32 number, or two.
+template <typename V> struct RouteNum;
+template <> struct RouteNum<float> {
+  static __device__ __forceinline__ float least() { return -INFINITY; }
+  static __device__ __forceinline__ float leading(float a) { return a; }
+  static __device__ __forceinline__ bool greater(float a, float b) { return a > b; }
+  static __device__ __forceinline__ bool equal(float a, float b) { return a == b; }
+  static __device__ __forceinline__ float sum(float a, float b) { return a + b; }
+  static __device__ __forceinline__ float shuffle(float a, int lane) { return __shfl_sync(~0u, a, lane); }
+  static __device__ __forceinline__ float shuffle_xor(float a, int d) { return __shfl_xor_sync(~0u, a, d); }
+};
+template <> struct RouteNum<RouteFF> {
+  static __device__ __forceinline__ RouteFF least() { return {-INFINITY, 0.f}; }
+  static __device__ __forceinline__ float leading(RouteFF a) { return a.h; }
+  static __device__ __forceinline__ bool greater(RouteFF a, RouteFF b) { return ff_greater(a, b); }
+  static __device__ __forceinline__ bool equal(RouteFF a, RouteFF b) { return a.h == b.h && a.l == b.l; }
+  static __device__ __forceinline__ RouteFF sum(RouteFF a, RouteFF b) {
+    return a.h > -INFINITY && b.h > -INFINITY ? ff_add(a, b) : least();
+  }
+  static __device__ __forceinline__ RouteFF shuffle(RouteFF a, int lane) {
+    return {__shfl_sync(~0u, a.h, lane), __shfl_sync(~0u, a.l, lane)};
+  }
+  static __device__ __forceinline__ RouteFF shuffle_xor(RouteFF a, int d) {
+    return {__shfl_xor_sync(~0u, a.h, d), __shfl_xor_sync(~0u, a.l, d)};
+  }
+};
+
 // One logit as FP32; DTYPE is a bsq_dtype.
 template <int DTYPE>
 __device__ __forceinline__ float route_load(const void* row, int e) {
@@ -106,200 +133,300 @@ __device__ __forceinline__ float route_load(const void* row, int e) {
   return elem2_to_f32x2<DTYPE == 1>(__ldg(static_cast<const uint16_t*>(row) + e)).x;
 }
 
-// The largest key of the warp and its lowest expert, taken out of the lane's keys.  Returns the expert.
+// The top_k largest keys, in order, equal ones lowest expert (32 slot + lane) first: lane k gets the k-th's expert, and the keys
+// become 0.  `margin`: the least distance of neighbours among them and the next one, of their leading 32 bits' numbers;
+// `least`: those of the last one.  Every lane does the same work in every round: a branch for the lane that holds the winner costs more.
 template <int NL, typename K>
-__device__ __forceinline__ int route_take(K (&key)[NL], int lane, K& top) {
-  K best = 0;
+__device__ __forceinline__ int route_select(K (&key)[NL], int top_k, int lane, float& margin, float& least) {
+  int my_id = 0;
+  margin = INFINITY;
+  least = INFINITY;
+#pragma unroll 1
+  for (int k = 0; k <= top_k; ++k) {
+    K best = key[0], top;
 #pragma unroll
-  for (int i = 0; i < NL; ++i) best = max(best, key[i]);
-  if constexpr (sizeof(K) == 8) {
-    const uint32_t hi = __reduce_max_sync(~0u, static_cast<uint32_t>(best >> 32));
-    const uint32_t lo = __reduce_max_sync(~0u, static_cast<uint32_t>(best >> 32) == hi ? static_cast<uint32_t>(best) : 0u);
-    top = static_cast<K>(hi) << 32 | lo;
-  } else {
-    top = __reduce_max_sync(~0u, best);
+    for (int i = 1; i < NL; ++i) best = max(best, key[i]);
+    if constexpr (sizeof(K) == 8) {
+      const uint32_t hi = __reduce_max_sync(~0u, static_cast<uint32_t>(best >> 32));
+      const uint32_t lo = __reduce_max_sync(~0u, static_cast<uint32_t>(best >> 32) == hi ? static_cast<uint32_t>(best) : 0u);
+      top = static_cast<K>(hi) << 32 | lo;
+    } else {
+      top = __reduce_max_sync(~0u, best);
+    }
+    uint32_t leading;
+    if constexpr (sizeof(K) == 8) leading = static_cast<uint32_t>(top >> 32); else leading = top;
+    const float value = leading != 0u ? route_unkey(leading) : -INFINITY;
+    if (value > -INFINITY) margin = fminf(margin, least - value);
+    if (k == top_k) break;
+    least = value;
+    uint32_t at = ~0u;
+#pragma unroll
+    for (int i = NL - 1; i >= 0; --i)
+      if (key[i] == top) at = 32 * i + lane;
+    const uint32_t id = __reduce_min_sync(~0u, at);
+    if (lane == k) my_id = static_cast<int>(id);
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      if (32 * i + lane == static_cast<int>(id)) key[i] = 0;
   }
-  int at = 0x7FFFFFFF;
-#pragma unroll
-  for (int i = NL - 1; i >= 0; --i)
-    if (key[i] == top) at = 32 * i + lane;
-  const int id = static_cast<int>(__reduce_min_sync(~0u, static_cast<uint32_t>(at)));
-#pragma unroll
-  for (int i = 0; i < NL; ++i)
-    if (32 * i + lane == id) key[i] = 0;
-  return id;
+  return my_id;
 }
 
-// The groups that stay, a bit per group: the lanes share the groups out, `v` holds the experts' values in shared memory.
-__device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const RouteFF* v, int lane) {
+// The groups that stay, a bit per group: the lanes share the groups out, `v` holds the experts' values in shared memory.  `margin`:
+// how far the least score that stays lies above the largest that does not.
+template <typename V>
+__device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const V* v, int lane, float& margin) {
   int span = 32;  // lanes per group
   while (span * a.groups > 32) span >>= 1;
   const int g = lane / span, part = lane % span, per = a.experts / a.groups;
-  const RouteFF none = {-INFINITY, 0.f};
-  RouteFF first = none, second = none;
+  V first = RouteNum<V>::least(), second = first;
   if (g < a.groups)
     for (int j = part; j < per; j += span) {
-      const RouteFF x = v[g * per + j];
-      if (ff_greater(x, first)) {
+      const V x = v[g * per + j];
+      if (RouteNum<V>::greater(x, first)) {
         second = first;
         first = x;
-      } else if (ff_greater(x, second)) {
+      } else if (RouteNum<V>::greater(x, second)) {
         second = x;
       }
     }
   for (int d = 1; d < span; d <<= 1) {
-    const RouteFF f = {__shfl_xor_sync(~0u, first.h, d), __shfl_xor_sync(~0u, first.l, d)};
-    const RouteFF s = {__shfl_xor_sync(~0u, second.h, d), __shfl_xor_sync(~0u, second.l, d)};
-    if (ff_greater(f, first)) {
-      second = ff_greater(first, s) ? first : s;
+    const V f = RouteNum<V>::shuffle_xor(first, d), s = RouteNum<V>::shuffle_xor(second, d);
+    if (RouteNum<V>::greater(f, first)) {
+      second = RouteNum<V>::greater(first, s) ? first : s;
       first = f;
-    } else if (ff_greater(f, second)) {
+    } else if (RouteNum<V>::greater(f, second)) {
       second = f;
     }
   }
-  RouteFF score = first;
-  if (a.group_top == 2 && per > 1) score = first.h > -INFINITY && second.h > -INFINITY ? ff_add(first, second) : none;
+  V score = first;
+  if (a.group_top == 2 && per > 1) score = RouteNum<V>::sum(first, second);
   int before = 0;
   for (int o = 0; o < a.groups; ++o) {
-    const RouteFF s = {__shfl_sync(~0u, score.h, o * span), __shfl_sync(~0u, score.l, o * span)};
-    before += ff_greater(s, score) || (o < g && s.h == score.h && s.l == score.l);
+    const V s = RouteNum<V>::shuffle(score, o * span);
+    before += RouteNum<V>::greater(s, score) || (o < g && RouteNum<V>::equal(s, score));
   }
-  const uint32_t votes = __ballot_sync(~0u, g < a.groups && part == 0 && before < a.top_groups);
+  const bool there = g < a.groups && part == 0, stays = there && before < a.top_groups;
+  const uint32_t votes = __ballot_sync(~0u, stays);
+  const uint32_t low = __reduce_min_sync(~0u, stays ? route_key(RouteNum<V>::leading(score)) : ~0u);
+  const uint32_t high = __reduce_max_sync(~0u, there && !stays ? route_key(RouteNum<V>::leading(score)) : 0u);
+  margin = high == 0u || route_unkey(high) == -INFINITY ? INFINITY : route_unkey(low) - route_unkey(high);
   uint32_t kept = 0;
   for (int o = 0; o < a.groups; ++o) kept |= (votes >> (o * span) & 1u) << o;
   return kept;
 }
 
+// Whether expert e's group stays; inv: 2^20 / experts per group, rounded up (e * inv >> 20 is the group for e up to 1024).
+__device__ __forceinline__ bool route_kept(uint32_t kept, uint32_t e, uint32_t inv) { return kept >> ((e * inv) >> 20) & 1u; }
+
+// A logit or bias that takes part: NaN and +inf count as -inf.
+__device__ __forceinline__ float route_clean(float x) { return x < INFINITY ? x : -INFINITY; }
+
+// exp of a logit less `top` (softmax), or 1 / (1 + exp(-z)) (sigmoid: exp(min(z, 0)) / (1 + exp(-|z|))).  Every lane calls.
+__device__ __forceinline__ RouteFF route_score(float z, float top, int sigmoid, RouteFF tab) {
+  const bool off = !(z > -INFINITY);
+  RouteFF v = ff_exp(off ? RouteFF{0.f, 0.f} : sigmoid ? RouteFF{-fabsf(z), 0.f} : ff_two_sum(z, -top), tab);
+  if (sigmoid) {
+    const RouteFF s = ff_fast(1.f, v.h), r = ff_inverse(ff_fast(s.h, __fadd_rn(s.l, v.l)));
+    v = z >= 0.f ? r : ff_mul(v, r);
+  }
+  return off ? RouteFF{0.f, 0.f} : v;
+}
+// 1 for the sigmoid, 1 / the sum of all experts' exponentials (at least 1 where a logit is there) for the softmax.
+template <int DTYPE>
+__device__ __forceinline__ RouteFF route_factor(const RouteArgs& a, const void* row, float top, RouteFF tab, int lane) {
+  if (a.sigmoid) return {1.f, 0.f};
+  RouteFF sum = {0.f, 0.f};
+#pragma unroll 2
+  for (int e0 = 0; e0 < a.experts; e0 += 32)
+    sum = ff_add(sum, route_score(e0 + lane < a.experts ? route_clean(route_load<DTYPE>(row, e0 + lane)) : -INFINITY, top, 0, tab));
+#pragma unroll 1
+  for (int d = 16; d > 0; d >>= 1) sum = ff_add(sum, RouteFF{__shfl_xor_sync(~0u, sum.h, d), __shfl_xor_sync(~0u, sum.l, d)});
+  return sum.h > 0.f ? ff_inverse(sum) : RouteFF{0.f, 0.f};
+}
+// The value of an expert: its score times the factor, plus its bias.
+__device__ __forceinline__ RouteFF route_value(RouteFF score, RouteFF factor, float z, const float* bias, int e) {
+  RouteFF v = ff_mul(score, factor);
+  if (bias) {
+    const float b = route_clean(__ldg(bias + e));
+    const RouteFF s = ff_two_sum(v.h, b);
+    v = ff_fast(s.h, __fadd_rn(s.l, v.l));
+    if (!(b > -INFINITY) || !(z > -INFINITY)) v = {-INFINITY, 0.f};
+  }
+  return v;
+}
+
+// The choice among the experts that FP32 leaves open (`count` of them, at most 32, lane j's in `mine`): their values in two numbers, and each
+// one's place by counting those in front.  `out`: shared memory for the top_k.
+template <int DTYPE>
+__device__ __noinline__ int route_near(const RouteArgs& a, const void* row, int32_t* out, float top, int lane, int mine, int count) {
+  const RouteFF tab = {kRouteExp2[2 * lane], kRouteExp2[2 * lane + 1]};
+  const RouteFF factor = route_factor<DTYPE>(a, row, top, tab, lane);
+  const bool in = lane < count;
+  const float z = in ? route_clean(route_load<DTYPE>(row, mine)) : -INFINITY;
+  const RouteFF score = route_score(z, top, a.sigmoid, tab);
+  const RouteFF v = in ? route_value(score, factor, z, a.bias, mine) : RouteFF{-INFINITY, 0.f};
+  int before = 0;
+#pragma unroll 4
+  for (int o = 0; o < count; ++o) {
+    const RouteFF x = {__shfl_sync(~0u, v.h, o), __shfl_sync(~0u, v.l, o)};
+    const int id = __shfl_sync(~0u, mine, o);
+    before += ff_greater(x, v) || (x.h == v.h && x.l == v.l && id < mine);
+  }
+  __syncwarp();
+  if (in && before < a.top_k) out[before] = mine;
+  __syncwarp();
+  return lane < a.top_k ? out[lane] : 0;
+}
+
+// The choice with all values in two numbers, where the groups' order or more than 32 experts are open: once in many thousand
+// tokens, so small rather than fast.
+template <int DTYPE, int NL>
+__device__ __noinline__ int route_exact(const RouteArgs& a, const void* row, RouteFF* values, float top, int lane) {
+  const RouteFF tab = {kRouteExp2[2 * lane], kRouteExp2[2 * lane + 1]};
+  const RouteFF factor = route_factor<DTYPE>(a, row, top, tab, lane);
+#pragma unroll 1
+  for (int e0 = 0; e0 < a.experts; e0 += 32) {
+    const int e = e0 + lane;
+    const float z = e < a.experts ? route_clean(route_load<DTYPE>(row, e)) : -INFINITY;
+    const RouteFF score = route_score(z, top, a.sigmoid, tab);
+    if (e < a.experts) values[e] = route_value(score, factor, z, a.bias, e);
+  }
+  __syncwarp();
+  float margin, least;
+  const uint32_t kept = a.groups > 1 ? route_groups(a, values, lane, margin) : 1u;
+  const uint32_t per = a.experts / a.groups, inv = ((1u << 20) + per - 1) / per;
+  uint64_t key[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int e = 32 * i + lane;
+    key[i] = 0;
+    if (e < a.experts) {
+      RouteFF v = a.bias ? values[e] : RouteFF{route_clean(route_load<DTYPE>(row, e)), 0.f};
+      if (!route_kept(kept, e, inv)) v = {-INFINITY, 0.f};
+      key[i] = static_cast<uint64_t>(route_key(v.h)) << 32 | route_key(v.l);
+    }
+  }
+  return route_select<NL>(key, a.top_k, lane, margin, least);
+}
+
 // NL: logits per lane (expert 32 i + lane in slot i).  PAIR: p enters the comparison (a bias, or sums of two in groups).
+//
+// p is then computed in FP32 first, off by at most some 2^-20 of the largest score; where no two values whose order
+// matters lie closer than that allows, the choice is the exact one, and otherwise (about one token in a hundred, at random) it is made again
+// with two numbers per value, among the few experts that are open.
 template <int DTYPE, int NL, bool PAIR>
 __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteArgs a) {
-  extern __shared__ RouteFF route_values[];  // [warps][experts] with groups
-  __shared__ float chosen[kRouteWarps][kRouteMaxTopK];
-  using Key = std::conditional_t<PAIR, uint64_t, uint32_t>;
+  extern __shared__ RouteFF route_smem[];  // [warps][experts], with groups or PAIR
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
-  RouteFF tab = {0.f, 0.f};
-  if constexpr (PAIR) tab = {kRouteExp2[2 * lane], kRouteExp2[2 * lane + 1]};
+  RouteFF* const values = route_smem + warp * a.experts;
+  float* const plain = reinterpret_cast<float*>(values);
   pdl_wait();
   if (token >= a.tokens) return;
   const void* row = static_cast<const char*>(a.logits) + token * a.ld * (DTYPE == 2 ? 4 : 2);
 
-  float z[NL];
+  float z[NL], v[NL];
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
     const int e = 32 * i + lane;
-    z[i] = e < a.experts ? route_load<DTYPE>(row, e) : -INFINITY;
-    if (!(z[i] < INFINITY)) {  // NaN, +inf
-      bad = true;
-      z[i] = -INFINITY;
-    }
+    const float x = e < a.experts ? route_load<DTYPE>(row, e) : -INFINITY;
+    z[i] = route_clean(x);
+    bad |= !(x < INFINITY);
   }
-  float bias[PAIR ? NL : 1];
   if constexpr (PAIR) {
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       const int e = 32 * i + lane;
-      bias[i] = a.bias && e < a.experts ? __ldg(a.bias + e) : 0.f;
-      if (!(bias[i] < INFINITY)) {
-        bad = true;
-        bias[i] = -INFINITY;
-      }
+      const float x = a.bias && e < a.experts ? __ldg(a.bias + e) : 0.f;
+      v[i] = route_clean(x);
+      bad |= !(x < INFINITY);
     }
   }
   if (__any_sync(~0u, bad) && lane == 0) record_error_at(a.err, kErrValue);
-  float top = -INFINITY;
+  float top = -INFINITY, total = 1.f;  // of the softmax
   if (!a.sigmoid) {
 #pragma unroll
     for (int i = 0; i < NL; ++i) top = fmaxf(top, z[i]);
     top = route_unkey(__reduce_max_sync(~0u, route_key(top)));
   }
-
-  Key key[NL];
-  float total = 0.f;  // of the softmax
-  if constexpr (PAIR) {
-    RouteFF e[NL], sum = {0.f, 0.f};
+  float tol = 0x1p-19f;  // twice what two values may be off
+  if (PAIR || (!a.sigmoid && !a.renorm)) {
+    float p[NL], sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const bool off = !(z[i] > -INFINITY);
-      if (a.sigmoid) {
-        const RouteFF u = ff_exp(RouteFF{off ? 0.f : -fabsf(z[i]), 0.f}, tab);
-        const RouteFF d = ff_add(RouteFF{1.f, 0.f}, u);
-        e[i] = ff_div(z[i] >= 0.f ? RouteFF{1.f, 0.f} : u, d);
-      } else {
-        e[i] = ff_exp(off ? RouteFF{0.f, 0.f} : ff_two_sum(z[i], -top), tab);
-      }
-      if (off) e[i] = {0.f, 0.f};
-      sum = ff_add(sum, e[i]);
+      const float e = expf(a.sigmoid ? -z[i] : z[i] - top);
+      p[i] = !(z[i] > -INFINITY) ? 0.f : a.sigmoid ? __fdividef(1.f, 1.f + fminf(e, 0x1p100f)) : e;
+      sum += p[i];
     }
+    float factor = 1.f;
     if (!a.sigmoid) {
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum = ff_add(sum, RouteFF{__shfl_xor_sync(~0u, sum.h, d), __shfl_xor_sync(~0u, sum.l, d)});
-#pragma unroll
-      for (int i = 0; i < NL; ++i)
-        if (sum.h > 0.f) e[i] = ff_div(e[i], sum);
-      total = sum.h;
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+      total = sum;
+      factor = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
+      tol = 0x1p-17f * factor;  // scores are at most this factor
     }
+    if constexpr (PAIR) {
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      RouteFF v = e[i];
-      if (a.bias) {
-        const RouteFF s = ff_two_sum(v.h, bias[i]);
-        v = ff_fast(s.h, __fadd_rn(s.l, v.l));
-        if (!(z[i] > -INFINITY) || !(bias[i] > -INFINITY)) v = {-INFINITY, 0.f};
+      for (int i = 0; i < NL; ++i) {
+        const int e = 32 * i + lane;
+        const float s = p[i] * factor;
+        v[i] = z[i] > -INFINITY || !a.bias ? s + v[i] : -INFINITY;
+        if (a.groups > 1 && e < a.experts) plain[e] = v[i];
+        if (!a.bias) v[i] = z[i];
       }
-      if (a.groups > 1 && 32 * i + lane < a.experts) route_values[warp * a.experts + 32 * i + lane] = v;
-      if (!a.bias) v = {z[i], 0.f};
-      key[i] = 32 * i + lane < a.experts ? static_cast<uint64_t>(route_key(v.h)) << 32 | route_key(v.l) : 0;
     }
-  } else {
+  }
+  if constexpr (!PAIR) {
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      key[i] = 32 * i + lane < a.experts ? route_key(z[i]) : 0u;
-      if (a.groups > 1 && 32 * i + lane < a.experts) route_values[warp * a.experts + 32 * i + lane] = {z[i], 0.f};
+      v[i] = z[i];
+      if (a.groups > 1 && 32 * i + lane < a.experts) plain[32 * i + lane] = z[i];
     }
   }
 
+  float group_margin = INFINITY, margin, least;
+  uint32_t kept = 1u;
   if (a.groups > 1) {
     __syncwarp();
-    const uint32_t kept = route_groups(a, route_values + warp * a.experts, lane);
-    const int per = a.experts / a.groups;
-    const uint32_t inv = ((1u << 20) + per - 1) / per;  // e * inv >> 20 is e / per for e, per <= 1024
-    const Key least = PAIR ? static_cast<Key>(static_cast<uint64_t>(route_key(-INFINITY)) << 32 | route_key(0.f))
-                           : static_cast<Key>(route_key(-INFINITY));
+    kept = route_groups(a, plain, lane, group_margin);
+  }
+  const uint32_t per = a.experts / a.groups, inv = ((1u << 20) + per - 1) / per;
+  uint32_t key[NL];
+  float size = 0.f;  // of the values, whose rounding counts too
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const uint32_t e = 32 * i + lane;
-      if (e < static_cast<uint32_t>(a.experts) && !(kept >> ((e * inv) >> 20) & 1u)) key[i] = least;
+  for (int i = 0; i < NL; ++i) {
+    const uint32_t e = 32 * i + lane;
+    if (PAIR && v[i] > -INFINITY && e < static_cast<uint32_t>(a.experts)) size = fmaxf(size, fabsf(v[i]));
+    key[i] = e < static_cast<uint32_t>(a.experts) ? route_key(route_kept(kept, e, inv) ? v[i] : -INFINITY) : 0u;
+  }
+  int my_id = route_select<NL>(key, a.top_k, lane, margin, least);
+  if constexpr (PAIR) {
+    tol += 0x1p-21f * __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(size)));
+    // without a bias the logits themselves are compared, and only the groups' scores are rounded
+    const bool groups_open = !(group_margin > 2.f * tol), open = a.bias && !(margin > tol);
+    if (groups_open || open) {
+      // the chosen experts, and those that may belong in their place
+      int mine = my_id, count = a.top_k;
+      const float from = least - tol;
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const uint32_t near = __ballot_sync(~0u, key[i] != 0u && route_unkey(key[i]) >= from);
+        for (uint32_t rest = near; rest != 0u; rest &= rest - 1u, ++count)
+          if (lane == count) mine = 32 * i + __ffs(rest) - 1;
+      }
+      my_id = groups_open || count > 32 || !(least > -INFINITY) ? route_exact<DTYPE, NL>(a, row, values, top, lane)
+                                                                : route_near<DTYPE>(a, row, reinterpret_cast<int32_t*>(values), top, lane, mine, count);
     }
   }
-
-  if (!PAIR && !a.sigmoid && !a.renorm) {
-#pragma unroll
-    for (int i = 0; i < NL; ++i)
-      if (z[i] > -INFINITY) total += expf(z[i] - top);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(~0u, total, d);
-  }
-
-  int my_id = 0;
-  for (int k = 0; k < a.top_k; ++k) {
-    Key best;
-    const int id = route_take<NL>(key, lane, best);
-    if (lane == k) my_id = id;
-    if ((id & 31) == lane) {
-#pragma unroll
-      for (int i = 0; i < NL; ++i)
-        if (32 * i + lane == id) chosen[warp][k] = z[i];
-    }
-  }
-  __syncwarp();
   // weights: from the logits, and relative to the largest chosen one where they are divided by their sum, so that small
   // scores keep their ratios: 1 / (1 + exp(-z)) = exp(min(z, 0)) / (1 + exp(-|z|))
-  const float zc = lane < a.top_k ? chosen[warp][lane] : -INFINITY;
+  const float zc = lane < a.top_k ? route_clean(route_load<DTYPE>(row, my_id)) : -INFINITY;
   float from = a.sigmoid ? 0.f : top;
   if (a.renorm) from = fminf(from, route_unkey(__reduce_max_sync(~0u, route_key(zc))));
-  float w = 0.f, sum = a.sigmoid ? 1.f : total;
+  float w = 0.f, sum = total;
   if (zc > -INFINITY) w = a.sigmoid ? __fdiv_rn(expf(fminf(zc, 0.f) - from), 1.f + expf(-fabsf(zc))) : expf(zc - from);
   if (a.renorm) {
     sum = w;
@@ -320,7 +447,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
 // sums over warps, blocks (through distributed shared memory) and experts, and the warp goes over its run again:
 // a pair's row is its counter plus the number of lower lanes with its expert.  No atomics, so the order
 // is the pairs' own.  Bound by latency: a few dependent passes of one to eight blocks.
-constexpr int kRowsThreads = 1024, kRowsWarps = kRowsThreads / 32, kRowsMaxBlocks = 8;
+// Measured figures are beside the launch.
+constexpr int kRowsThreads = 1024, kRowsWarps = kRowsThreads / 32, kRowsMaxBlocks = 8, kRowsHeld = 8;
 
 struct RowsArgs {
   const int32_t* ids;
@@ -334,53 +462,90 @@ struct RowsArgs {
 
 inline int rows_smem_bytes(int experts) { return 4 * (kRowsWarps * experts + 2 * experts); }
 
+// HELD: a run has at most 32 kRowsHeld pairs, whose experts and places among their warp's stay in registers.
+template <bool HELD>
 __global__ void __launch_bounds__(kRowsThreads, 1) moe_rows_kernel(const RowsArgs a) {
   extern __shared__ uint32_t rows_smem[];
   __shared__ uint32_t part[2][kRowsWarps];
+  __shared__ uint32_t used;
   uint32_t* count = rows_smem;                             // [warps][experts]
   uint32_t* total = rows_smem + kRowsWarps * a.experts;    // [experts] of this block
   uint32_t* base = total + a.experts;                      // [experts] first row of this block's pairs
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = blockIdx.x, blocks = gridDim.x, experts = a.experts;
   for (int i = tid; i < kRowsWarps * experts; i += kRowsThreads) count[i] = 0u;
   pdl_wait();
-  __syncthreads();
   const int64_t begin = (static_cast<int64_t>(rank) * kRowsWarps + warp) * a.run;
   const int64_t end = min(begin + a.run, a.pairs);
   uint32_t* mine = count + warp * experts;
   bool bad = false;
-  for (int64_t at = begin; at < end; at += 32) {
-    int id = at + lane < end ? __ldg(a.ids + at + lane) : -1;
+  // one round: the pair's expert (-1: none) and its place among those of its expert that the warp has counted, itself left out
+  const auto place = [&](int& id, uint32_t& before) {
     if (id >= experts) {
       bad = true;
       id = -1;
     }
     const uint32_t same = __match_any_sync(~0u, id);
-    if (id >= 0 && lane == __ffs(same) - 1) mine[id] += __popc(same);
+    uint32_t first = 0;
+    if (id >= 0) first = mine[id];
     __syncwarp();
+    if (id >= 0 && lane == __ffs(same) - 1) mine[id] = first + __popc(same);
+    __syncwarp();
+    before = first + __popc(same & ((1u << lane) - 1u));
+  };
+  int ids[HELD ? kRowsHeld : 1];
+  uint32_t offs[HELD ? kRowsHeld : 1];
+  if constexpr (HELD) {
+#pragma unroll
+    for (int i = 0; i < kRowsHeld; ++i) ids[i] = begin + 32 * i + lane < end ? __ldg(a.ids + begin + 32 * i + lane) : -1;
+  }
+  __syncthreads();
+  if constexpr (HELD) {
+#pragma unroll
+    for (int i = 0; i < kRowsHeld; ++i)
+      if (begin + 32 * i < end) place(ids[i], offs[i]);
+  } else {
+    for (int64_t at = begin; at < end; at += 32) {
+      int id = at + lane < end ? __ldg(a.ids + at + lane) : -1;
+      uint32_t before;
+      place(id, before);
+    }
   }
   if (__any_sync(~0u, bad) && lane == 0) record_error_at(a.err, kErrValue);
   __syncthreads();
   // per expert: prefix over the block's warps
   for (int e = tid; e < experts; e += kRowsThreads) {
     uint32_t run = 0;
-#pragma unroll 8
-    for (int w = 0; w < kRowsWarps; ++w) {
-      const uint32_t c = count[w * experts + e];
-      count[w * experts + e] = run;
-      run += c;
+#pragma unroll
+    for (int w0 = 0; w0 < kRowsWarps; w0 += 16) {
+      uint32_t c[16];
+#pragma unroll
+      for (int w = 0; w < 16; ++w) c[w] = count[(w0 + w) * experts + e];
+#pragma unroll
+      for (int w = 0; w < 16; ++w) {
+        count[(w0 + w) * experts + e] = run;
+        run += c[w];
+      }
     }
     total[e] = run;
   }
-  cluster_sync_all();
+  if (blocks > 1) cluster_sync_all(); else __syncthreads();
   // over blocks and experts (at most 1024: a thread each)
   uint32_t all = 0, before = 0;
-  if (tid < experts)
-    for (int r = 0; r < blocks; ++r) {
-      const uint32_t c = cluster_ld_u32(cluster_map(total + tid, r));
-      before += r < rank ? c : 0u;
-      all += c;
+  if (tid < experts) {
+    if (blocks > 1) {
+      uint32_t c[kRowsMaxBlocks];
+#pragma unroll
+      for (int r = 0; r < kRowsMaxBlocks; ++r) c[r] = r < blocks ? cluster_ld_u32(cluster_map(total + tid, r)) : 0u;
+#pragma unroll
+      for (int r = 0; r < kRowsMaxBlocks; ++r) {
+        before += r < rank ? c[r] : 0u;
+        all += c[r];
+      }
+    } else {
+      all = total[tid];
     }
-  cluster_sync_all();  // the other blocks' memory is no longer read
+  }
+  if (blocks > 1) cluster_arrive();  // this block no longer reads the others' memory
   uint32_t rows = all, padded = (all + 127u) & ~127u;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -395,9 +560,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1) moe_rows_kernel(const RowsArg
     part[1][warp] = padded;
   }
   __syncthreads();
-  for (int w = 0; w < warp; ++w) {
-    rows += part[0][w];
-    padded += part[1][w];
+  {
+    const uint32_t r = __reduce_add_sync(~0u, lane < warp ? part[0][lane] : 0u), q = __reduce_add_sync(~0u, lane < warp ? part[1][lane] : 0u);
+    rows += r;
+    padded += q;
   }
   if (tid < experts) {
     base[tid] = rows - all + before;
@@ -406,32 +572,36 @@ __global__ void __launch_bounds__(kRowsThreads, 1) moe_rows_kernel(const RowsArg
       a.scales_offsets[tid + 1] = padded;
       if (tid == 0) a.row_offsets[0] = a.scales_offsets[0] = 0u;
     }
+    if (tid == experts - 1) used = rows;
   }
-  __shared__ uint32_t used;
-  if (tid == experts - 1) used = rows;
   __syncthreads();
-  for (int64_t at = begin; at < end; at += 32) {
-    const int64_t pair = at + lane;
-    int id = pair < end ? __ldg(a.ids + pair) : -1;
-    if (id >= experts) id = -1;
-    const uint32_t same = __match_any_sync(~0u, id);
-    uint32_t first = 0;
-    if (id >= 0) first = mine[id];
-    __syncwarp();
-    if (id >= 0 && lane == __ffs(same) - 1) mine[id] = first + __popc(same);
-    __syncwarp();
-    if (pair < end) {
-      int32_t row = -1;
-      if (id >= 0) {
-        row = static_cast<int32_t>(base[id] + first + __popc(same & ((1u << lane) - 1u)));
-        a.row_indices[row] = static_cast<int32_t>(pair / a.top_k);
-      }
-      a.positions[pair] = row;
+  const auto put = [&](int64_t pair, int id, uint32_t before) {  // before: in the block, of this expert
+    int32_t row = -1;
+    if (id >= 0) {
+      row = static_cast<int32_t>(base[id] + before);
+      a.row_indices[row] = static_cast<int32_t>(static_cast<uint32_t>(pair) / static_cast<uint32_t>(a.top_k));
+    }
+    a.positions[pair] = row;
+  };
+  if constexpr (HELD) {
+#pragma unroll
+    for (int i = 0; i < kRowsHeld; ++i) {
+      const int64_t pair = begin + 32 * i + lane;
+      // the counters now hold what the warps in front have
+      if (pair < end) put(pair, ids[i], ids[i] >= 0 ? mine[ids[i]] + offs[i] : 0u);
+    }
+  } else {
+    for (int64_t at = begin; at < end; at += 32) {
+      int id = at + lane < end ? __ldg(a.ids + at + lane) : -1;
+      uint32_t before;
+      place(id, before);
+      if (at + lane < end) put(at + lane, id, before);
     }
   }
   // rows that no pair took (dropped pairs leave them at the end) point at token 0
   for (int64_t r = used + static_cast<int64_t>(rank) * kRowsThreads + tid; r < a.pairs; r += static_cast<int64_t>(blocks) * kRowsThreads)
     a.row_indices[r] = 0;
+  if (blocks > 1) cluster_wait();
 }
 
 }  // namespace bsq

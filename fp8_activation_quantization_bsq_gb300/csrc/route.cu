@@ -13,7 +13,7 @@ using namespace bsq;
 template <int DTYPE, int NL>
 cudaError_t launch_route(const RouteArgs& a, bool pair, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(ceil_div(a.tokens, kRouteWarps))), block(kRouteWarps * 32);
-  const size_t smem = a.groups > 1 ? sizeof(RouteFF) * kRouteWarps * a.experts : 0;
+  const size_t smem = a.groups > 1 || pair ? sizeof(RouteFF) * kRouteWarps * a.experts : 0;
   return pair ? launch_pdl(moe_route_kernel<DTYPE, NL, true>, grid, block, smem, st, a)
               : launch_pdl(moe_route_kernel<DTYPE, NL, false>, grid, block, smem, st, a);
 }
@@ -95,8 +95,8 @@ int32_t bsq_moe_rows(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t 
   a.positions = positions;
   a.err = d.error_word;
   const int smem = rows_smem_bytes(experts);
-  if (bsq_status s = allow_smem(reinterpret_cast<const void*>(moe_rows_kernel), rows_smem_bytes(kRouteMaxExperts), d.index); s != BSQ_OK)
-    return s;
+  const auto kernel = a.run <= 32 * kRowsHeld ? moe_rows_kernel<true> : moe_rows_kernel<false>;
+  if (bsq_status s = allow_smem(reinterpret_cast<const void*>(kernel), rows_smem_bytes(kRouteMaxExperts), d.index); s != BSQ_OK) return s;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kRowsThreads);
@@ -111,7 +111,7 @@ int32_t bsq_moe_rows(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, moe_rows_kernel, a) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
 }
 
 }  // extern "C"
