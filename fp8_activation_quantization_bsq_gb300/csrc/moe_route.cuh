@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
 // a pair's row is its counter plus the number of lower lanes with its expert.  No atomics, so the order
 // is the pairs' own.  Bound by latency: a few dependent passes of one to eight blocks.
 // Measured figures are beside the launch.
-constexpr int kRowsThreads = 1024, kRowsWarps = kRowsThreads / 32, kRowsMaxBlocks = 8, kRowsHeld = 8;
+constexpr int kRowsThreads = 1024, kRowsWarps = kRowsThreads / 32, kRowsMaxBlocks = 16, kRowsHeld = 8;
 
 struct RowsArgs {
   const int32_t* ids;

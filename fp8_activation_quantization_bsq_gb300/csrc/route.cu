@@ -97,6 +97,7 @@ int32_t bsq_moe_rows(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t 
   const int smem = rows_smem_bytes(experts);
   const auto kernel = a.run <= 32 * kRowsHeld ? moe_rows_kernel<true> : moe_rows_kernel<false>;
   if (bsq_status s = allow_smem(reinterpret_cast<const void*>(kernel), rows_smem_bytes(kRouteMaxExperts), d.index); s != BSQ_OK) return s;
+  if (blocks > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return BSQ_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kRowsThreads);
