@@ -12,11 +12,11 @@
 // at most position * inv_freq * 2^-64 turns before the last 32 bits are cut off, at any position.
 #pragma once
 
-#include "serving_common.cuh"
+#include "tcgen05.cuh"  // fma_f32x2
 
 namespace bsq {
 
-constexpr int kRopeWarps = 4;
+constexpr int kRopeWarps = 4, kRopeDepth = 6;  // steps of a warp in flight
 
 struct RopeArgs {
   const uint16_t* src[2];  // queries, keys
@@ -29,7 +29,7 @@ struct RopeArgs {
   int heads, rows;  // query heads, query and key heads
   int dim, pairs;
   int weight_f32;
-  float eps;
+  float eps, inv_dim;
   int chunks, per_chunk;  // tasks per token, rows per task
 };
 
@@ -58,13 +58,21 @@ __device__ __forceinline__ float2 rope_turn(float f, int position) {
   return r;
 }
 
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
 // Rows whose elements a lane reads: MODE 0 pairs (i, i + pairs) with pairs a multiple of 4, 1 neighbouring pairs,
-// 2 pairs (i, i + pairs) of any number, whose other sides come through shared memory.  L lanes per row.
+// 2 pairs (i, i + pairs) of any number, whose other sides come through shared memory.  L lanes per row.  Arithmetic goes two
+// elements at a time.
 template <bool F16, int L, int MODE>
-__global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const RopeArgs a) {
-  constexpr int kPer = 32 / L;   // rows at a time
-  constexpr int kUnroll = 4;     // row loads in flight per lane
+__global__ void __launch_bounds__(kRopeWarps * 32, MODE == 2 ? 5 : 8) qk_norm_rope_kernel(const RopeArgs a) {
+  constexpr int kPer = 32 / L;  // rows at a time
   __shared__ float other[MODE == 2 ? kRopeWarps * 256 : 1];
+  __shared__ uint4 ring[kRopeWarps][kRopeDepth][32];  // a lane's elements of a step, which it copies and reads itself
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / L, p = lane % L;
   const int64_t task = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp;
@@ -80,130 +88,125 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const Rop
 
   constexpr int kAngles = MODE == 2 ? 8 : 4;
   float cs[kAngles], sn[kAngles];
-  bool turns[kAngles];
+  uint32_t turns = 0;  // a bit per angle
 #pragma unroll
   for (int j = 0; j < kAngles; ++j) {
     int i = MODE == 2 ? 8 * p + j : 4 * p + j;
-    turns[j] = active && (MODE == 0 ? apart : MODE == 1 ? i < a.pairs : i < 2 * a.pairs);
+    const bool turn = active && (MODE == 0 ? apart : MODE == 1 ? i < a.pairs : i < 2 * a.pairs);
     const bool second = MODE == 2 && i >= a.pairs;
     if (second) i -= a.pairs;
     cs[j] = 1.f;
     sn[j] = 0.f;
-    if (turns[j]) {
+    if (turn) {
+      turns |= 1u << j;
       const float2 t = rope_turn(__ldg(a.inv_freq + i), position);
       cs[j] = t.x;
       sn[j] = second ? -t.y : t.y;
     }
   }
 
-  float w[8];
-  int kind = -1;
-  for (int r0 = first; r0 < last; r0 += kPer * kUnroll) {
-    uint2 va[kUnroll], vb[kUnroll];
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {  // the task's queries, then its keys
+    const int r0 = max(first, k ? a.heads : 0), r1 = min(last, k ? a.rows : a.heads);
+    if (r0 >= r1) continue;
+    const bool norm = a.weight[k] != nullptr;
+    float2 w[4];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int r = r0 + u * kPer + sub;
-      va[u] = vb[u] = make_uint2(0, 0);
-      if (r < last && active) {
-        const int k = r >= a.heads;
-        const uint16_t* s = a.src[k] + token * a.src_tok[k] + (r - (k ? a.heads : 0)) * a.src_head[k];
-        if (apart) {
-          va[u] = *reinterpret_cast<const uint2*>(s + ea);
-          vb[u] = *reinterpret_cast<const uint2*>(s + eb);
+    for (int j = 0; j < 4; ++j) {
+      const int e = j < 2 ? ea + 2 * j : eb + 2 * j - 4;
+      w[j] = make_float2(1.f, 1.f);
+      if (norm && active) {
+        if (a.weight_f32) {
+          const float* src = static_cast<const float*>(a.weight[k]) + e;
+          w[j] = make_float2(__ldg(src), __ldg(src + 1));
         } else {
-          const uint4 v = *reinterpret_cast<const uint4*>(s + ea);
-          va[u] = make_uint2(v.x, v.y);
-          vb[u] = make_uint2(v.z, v.w);
+          const uint16_t* src = static_cast<const uint16_t*>(a.weight[k]) + e;
+          w[j] = elem2_to_f32x2<F16>(__ldg(src) | static_cast<uint32_t>(__ldg(src + 1)) << 16);
         }
       }
     }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (r0 + u * kPer >= last) break;  // the whole warp
-      const int r = r0 + u * kPer + sub;
-      const int k = r >= a.heads;
-      const bool has_norm = a.weight[k] != nullptr;
-      if (k != kind) {
-        kind = k;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = j < 4 ? ea + j : eb + j - 4;
-          w[j] = 1.f;
-          if (has_norm && active) {
-            if (a.weight_f32) {
-              w[j] = __ldg(static_cast<const float*>(a.weight[k]) + e);
-            } else {
-              w[j] = elem2_to_f32x2<F16>(__ldg(static_cast<const uint16_t*>(a.weight[k]) + e)).x;
-            }
-          }
+    const int h = r0 + sub - (k ? a.heads : 0), n = r1 - r0;
+    const uint16_t* s = a.src[k] + token * a.src_tok[k] + h * a.src_head[k];
+    uint16_t* d = a.dst[k] + token * a.dst_tok[k] + h * a.dst_head[k];
+    const int64_t s_step = kPer * a.src_head[k], d_step = kPer * a.dst_head[k];
+    uint4* const mine_in = &ring[warp][0][lane];
+    int left = active ? n - sub : 0;  // rows not yet asked for, this lane's at every kPer-th
+    const auto ask = [&](int slot) {
+      if (left > 0) {
+        const uint32_t to = smem_addr(mine_in + slot * 32);
+        if (apart) {
+          cp_async8(to, s + ea);
+          cp_async8(to + 8, s + eb);
+        } else {
+          cp_async16(to, s + ea);
         }
       }
-      float x[8];
-      {
-        const float2 x0 = elem2_to_f32x2<F16>(va[u].x), x1 = elem2_to_f32x2<F16>(va[u].y);
-        const float2 x2 = elem2_to_f32x2<F16>(vb[u].x), x3 = elem2_to_f32x2<F16>(vb[u].y);
-        x[0] = x0.x, x[1] = x0.y, x[2] = x1.x, x[3] = x1.y, x[4] = x2.x, x[5] = x2.y, x[6] = x3.x, x[7] = x3.y;
-      }
-      if (a.weight[0] != nullptr || a.weight[1] != nullptr) {
-        float sum = 0.f;
+      cp_async_commit();
+      left -= kPer;
+      s += s_step;
+    };
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
+    for (int i = 0; i < kRopeDepth - 1; ++i) ask(i);
+    int slot = 0;
+#pragma unroll 1
+    for (int i = sub; i - sub < n; i += kPer, d += d_step) {
+      const bool in = i < n && active;
+      cp_async_wait<kRopeDepth - 2>();
+      const uint4 v = in ? mine_in[slot * 32] : make_uint4(0, 0, 0, 0);
+      ask(slot == 0 ? kRopeDepth - 1 : slot - 1);
+      slot = slot == kRopeDepth - 1 ? 0 : slot + 1;
+      const uint2 va = make_uint2(v.x, v.y), vb = make_uint2(v.z, v.w);
+      float2 x[4] = {elem2_to_f32x2<F16>(va.x), elem2_to_f32x2<F16>(va.y), elem2_to_f32x2<F16>(vb.x), elem2_to_f32x2<F16>(vb.y)};
+      if (norm) {
+        const auto squares = [&]() {
+          float2 q = mul_f32x2(x[0], x[0]);
 #pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-        float eps = a.eps;
+          for (int j = 1; j < 4; ++j) q = fma_f32x2(x[j], x[j], q);
+          float sum = q.x + q.y;
+#pragma unroll
+          for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+          return sum;
+        };
+        float sum = squares(), eps = a.eps;
         if (!F16 && __any_sync(~0u, sum > 3.0e38f)) {  // squares past FP32 (rows beyond 2^63): once more, 2^-96 smaller
-          const bool again = sum > 3.0e38f;
-          float small = 0.f;
+          const float less = sum > 3.0e38f ? 0x1p-96f : 1.f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (again && has_norm) x[j] *= 0x1p-96f;
-            small = fmaf(x[j], x[j], small);
-          }
-#pragma unroll
-          for (int d = L / 2; d > 0; d >>= 1) small += __shfl_xor_sync(~0u, small, d);
-          if (again) {
-            sum = small;
-            eps = 0.f;  // far below the mean
-          }
+          for (int j = 0; j < 4; ++j) x[j] = mul_f32x2(x[j], make_float2(less, less));
+          sum = squares();
+          if (less != 1.f) eps = 0.f;  // far below the mean
         }
-        if (has_norm) {
-          const float f = rsqrtf(sum / static_cast<float>(a.dim) + eps);
+        const float f = rsqrtf(sum * a.inv_dim + eps);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] *= f * w[j];
-        }
+        for (int j = 0; j < 4; ++j) x[j] = mul_f32x2(x[j], mul_f32x2(w[j], make_float2(f, f)));
       }
-      float y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = x[j];
+      float2 y[4] = {x[0], x[1], x[2], x[3]};
       if constexpr (MODE == 0) {
+        if (turns != 0u) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (turns[j]) {
-            y[j] = x[j] * cs[j] - x[j + 4] * sn[j];
-            y[j + 4] = x[j + 4] * cs[j] + x[j] * sn[j];
+          for (int j = 0; j < 2; ++j) {
+            const float2 c = make_float2(cs[2 * j], cs[2 * j + 1]), t = make_float2(sn[2 * j], sn[2 * j + 1]);
+            y[j] = fma_f32x2(x[j], c, mul_f32x2(x[j + 2], make_float2(-t.x, -t.y)));
+            y[j + 2] = fma_f32x2(x[j + 2], c, mul_f32x2(x[j], t));
           }
+        }
       } else if constexpr (MODE == 1) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (turns[j]) {
-            y[2 * j] = x[2 * j] * cs[j] - x[2 * j + 1] * sn[j];
-            y[2 * j + 1] = x[2 * j + 1] * cs[j] + x[2 * j] * sn[j];
-          }
-      }
-      if constexpr (MODE == 2) {
+          if (turns >> j & 1u) y[j] = make_float2(x[j].x * cs[j] - x[j].y * sn[j], x[j].y * cs[j] + x[j].x * sn[j]);
+      } else {
         float* mine = other + (warp * kPer + sub) * 8 * L;  // the row's other lanes
+        float* out = reinterpret_cast<float*>(y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mine[8 * p + j] = x[j];
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(mine + 8 * p + 2 * j) = x[j];
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (turns[j]) y[j] = x[j] * cs[j] - mine[8 * p + j < a.pairs ? 8 * p + j + a.pairs : 8 * p + j - a.pairs] * sn[j];
+          if (turns >> j & 1u) out[j] = out[j] * cs[j] - mine[8 * p + j < a.pairs ? 8 * p + j + a.pairs : 8 * p + j - a.pairs] * sn[j];
         __syncwarp();
       }
-      if (r < last && active) {
-        uint16_t* d = a.dst[k] + token * a.dst_tok[k] + (r - (k ? a.heads : 0)) * a.dst_head[k];
-        const uint2 oa = make_uint2(f32x2_to_elem2<F16>(y[0], y[1]), f32x2_to_elem2<F16>(y[2], y[3]));
-        const uint2 ob = make_uint2(f32x2_to_elem2<F16>(y[4], y[5]), f32x2_to_elem2<F16>(y[6], y[7]));
+      if (in) {
+        const uint2 oa = make_uint2(f32x2_to_elem2<F16>(y[0].x, y[0].y), f32x2_to_elem2<F16>(y[1].x, y[1].y));
+        const uint2 ob = make_uint2(f32x2_to_elem2<F16>(y[2].x, y[2].y), f32x2_to_elem2<F16>(y[3].x, y[3].y));
         if (apart) {
           *reinterpret_cast<uint2*>(d + ea) = oa;
           *reinterpret_cast<uint2*>(d + eb) = ob;
@@ -212,6 +215,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const Rop
         }
       }
     }
+    cp_async_wait<0>();
   }
 }
 

@@ -74,6 +74,7 @@ extern "C" int32_t bsq_qk_norm_rope(int32_t dtype, const void* q, int64_t q_tok,
   a.pairs = pairs;
   a.weight_f32 = weight_dtype == BSQ_F32;
   a.eps = eps;
+  a.inv_dim = 1.f / static_cast<float>(dim);
   // a warp takes a token's rows, or, where there are too few tokens to fill the GPU, an equal share of them
   const int at_once = dim <= 64 ? 4 : dim <= 128 ? 2 : 1;
   const int steps = static_cast<int>(ceil_div(rows, at_once));
