@@ -98,6 +98,8 @@ _SIGNATURES |= {
     "bsq_moe_layer_workspace_bytes": (_c_i64, [_c_i32, _c_i32, _c_i64, _c_i64, _c_i32, _c_i32]),
     "bsq_moe_layer": (_c_i32, [_c_i32, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
                                _c_i64, _c_i32, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_p, _c_i64, _c_p]),
+    "bsq_moe_layer_routed": (_c_i32, [_c_i32, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i32,
+                                      _c_i64, _c_i64, _c_i32, _c_i32, _c_p, _c_i64, _c_p]),
     "bsq_packed_linear": (_c_i32, [_c_i32, _c_i32, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i32, _c_p,
                                    _c_i64, _c_p]),
     "bsq_qk_norm_rope": (_c_i32, [_c_i32, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_p, _c_p, _c_i32,

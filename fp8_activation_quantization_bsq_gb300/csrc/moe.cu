@@ -57,9 +57,9 @@ bool moe_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t row_bytes,
 // Dynamic shared memory of the layer's block: what the SM allows less the kernel's static tables.
 constexpr int kMoeDynamicSmem = 227 * 1024 - 1024;
 
-template <int FMT>
+template <int FMT, bool ROUTED>
 bsq_status launch_moe(MoeArgs& a, const void* w13, const void* w2, const HostDevice& d, cudaStream_t st) {
-  if (bsq_status s = allow_smem(reinterpret_cast<const void*>(moe_layer_kernel<FMT>), kMoeDynamicSmem, d.index); s != BSQ_OK)
+  if (bsq_status s = allow_smem(reinterpret_cast<const void*>(moe_layer_kernel<FMT, ROUTED>), kMoeDynamicSmem, d.index); s != BSQ_OK)
     return s;
   const int64_t pairs = static_cast<int64_t>(a.tokens) * a.top_k;
   CUtensorMap m13, m2, mx, mh;
@@ -83,7 +83,58 @@ bsq_status launch_moe(MoeArgs& a, const void* w13, const void* w2, const HostDev
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, moe_layer_kernel<FMT>, m13, m2, mx, mh, a) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, moe_layer_kernel<FMT, ROUTED>, m13, m2, mx, mh, a) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
+}
+
+// The checks and the launch that both forms of the layer share; `a` holds its routing.
+template <bool ROUTED>
+bsq_status run_moe(int32_t fmt, MoeArgs& a, const void* x, int64_t ld_x, const void* w13, const void* w13_s, const void* w2, const void* w2_s,
+                   const float* x_sf, const float* w13_sf, const float* h_sf, const float* w2_sf, void* y, int64_t ld_y, int32_t tokens,
+                   int64_t hidden, int64_t inter, int32_t experts, int32_t top_k, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!fmt_ok(fmt)) return BSQ_ERR_VALUE;
+  if (!moe_sizes_ok(tokens, hidden, inter, experts, top_k)) return BSQ_ERR_SHAPE;
+  if (tokens == 0) return BSQ_OK;
+  if (tokens > 1 && (ld_x < hidden || ld_y < hidden || (!ROUTED && a.ld_logits < experts))) return BSQ_ERR_SHAPE;
+  if (!x || !w13 || !w13_s || !w2 || !w2_s || !y || !workspace || (ROUTED ? !a.ids || !a.weights : !a.logits)) return BSQ_ERR_NULL;
+  if (fmt == BSQ_NVFP4 && (!x_sf || !w13_sf || !h_sf || !w2_sf)) return BSQ_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(a.logits, 4) || !aligned(a.ids, 4) || !aligned(a.weights, 4) || !aligned(w13, 16) || !aligned(w13_s, 16) ||
+      !aligned(w2, 16) || !aligned(w2_s, 16) || !aligned(y, 16) || !aligned(workspace, 256) || ld_x % 8 != 0 || ld_y % 8 != 0 ||
+      !aligned(x_sf, 4) || !aligned(w13_sf, 4) || !aligned(h_sf, 4) || !aligned(w2_sf, 4))
+    return BSQ_ERR_ALIGN;
+  const MoeWorkspace w = moe_workspace(fmt, tokens, hidden, inter, experts, top_k);
+  if (workspace_bytes < w.bytes) return BSQ_ERR_SHAPE;
+  HostDevice d;
+  if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.x = static_cast<const uint16_t*>(x);
+  a.ld_x = ld_x;
+  a.w13_s = static_cast<const uint8_t*>(w13_s);
+  a.w2_s = static_cast<const uint8_t*>(w2_s);
+  a.x_sf = x_sf;
+  a.w13_sf = w13_sf;
+  a.h_sf = h_sf;
+  a.w2_sf = w2_sf;
+  a.y = static_cast<uint16_t*>(y);
+  a.ld_y = ld_y;
+  a.tokens = tokens;
+  a.hidden = static_cast<int>(hidden);
+  a.inter = static_cast<int>(inter);
+  a.experts = experts;
+  a.top_k = top_k;
+  a.counters = reinterpret_cast<uint32_t*>(ws);
+  a.xq = ws + w.xq;
+  a.xq_s = ws + w.xq_s;
+  a.hq = ws + w.hq;
+  a.hq_s = ws + w.hq_s;
+  a.part = reinterpret_cast<float*>(ws + w.part);
+  a.yp = reinterpret_cast<float*>(ws + w.yp);
+  a.err = d.error_word;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (fmt) {
+    case BSQ_NVFP4: return launch_moe<kNVFP4, ROUTED>(a, w13, w2, d, st);
+    case BSQ_MXFP4: return launch_moe<kMXFP4, ROUTED>(a, w13, w2, d, st);
+    default: return launch_moe<kMXFP8, ROUTED>(a, w13, w2, d, st);
+  }
 }
 
 __device__ uint32_t g_selftest_count;  // stays 0
@@ -137,54 +188,23 @@ int32_t bsq_moe_layer(int32_t fmt, const void* x, int64_t ld_x, const float* log
                       const float* h_sf, const float* w2_sf, void* y, int64_t ld_y, int32_t tokens, int64_t hidden,
                       int64_t inter, int32_t experts, int32_t top_k, int32_t renormalize, void* workspace,
                       int64_t workspace_bytes, void* stream) {
-  if (!fmt_ok(fmt)) return BSQ_ERR_VALUE;
-  if (!moe_sizes_ok(tokens, hidden, inter, experts, top_k)) return BSQ_ERR_SHAPE;
-  if (tokens == 0) return BSQ_OK;
-  if (tokens > 1 && (ld_x < hidden || ld_y < hidden || ld_logits < experts)) return BSQ_ERR_SHAPE;
-  if (!x || !logits || !w13 || !w13_s || !w2 || !w2_s || !y || !workspace) return BSQ_ERR_NULL;
-  if (fmt == BSQ_NVFP4 && (!x_sf || !w13_sf || !h_sf || !w2_sf)) return BSQ_ERR_NULL;
-  if (!aligned(x, 16) || !aligned(logits, 4) || !aligned(w13, 16) || !aligned(w13_s, 16) || !aligned(w2, 16) ||
-      !aligned(w2_s, 16) || !aligned(y, 16) || !aligned(workspace, 256) || ld_x % 8 != 0 || ld_y % 8 != 0 ||
-      !aligned(x_sf, 4) || !aligned(w13_sf, 4) || !aligned(h_sf, 4) || !aligned(w2_sf, 4))
-    return BSQ_ERR_ALIGN;
-  const MoeWorkspace w = moe_workspace(fmt, tokens, hidden, inter, experts, top_k);
-  if (workspace_bytes < w.bytes) return BSQ_ERR_SHAPE;
-  HostDevice d;
-  if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
   MoeArgs a{};
-  a.x = static_cast<const uint16_t*>(x);
-  a.ld_x = ld_x;
   a.logits = logits;
   a.ld_logits = ld_logits;
-  a.w13_s = static_cast<const uint8_t*>(w13_s);
-  a.w2_s = static_cast<const uint8_t*>(w2_s);
-  a.x_sf = x_sf;
-  a.w13_sf = w13_sf;
-  a.h_sf = h_sf;
-  a.w2_sf = w2_sf;
-  a.y = static_cast<uint16_t*>(y);
-  a.ld_y = ld_y;
-  a.tokens = tokens;
-  a.hidden = static_cast<int>(hidden);
-  a.inter = static_cast<int>(inter);
-  a.experts = experts;
-  a.top_k = top_k;
   a.renorm = renormalize;
-  a.counters = reinterpret_cast<uint32_t*>(ws);
-  a.xq = ws + w.xq;
-  a.xq_s = ws + w.xq_s;
-  a.hq = ws + w.hq;
-  a.hq_s = ws + w.hq_s;
-  a.part = reinterpret_cast<float*>(ws + w.part);
-  a.yp = reinterpret_cast<float*>(ws + w.yp);
-  a.err = d.error_word;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  switch (fmt) {
-    case BSQ_NVFP4: return launch_moe<kNVFP4>(a, w13, w2, d, st);
-    case BSQ_MXFP4: return launch_moe<kMXFP4>(a, w13, w2, d, st);
-    default: return launch_moe<kMXFP8>(a, w13, w2, d, st);
-  }
+  return run_moe<false>(fmt, a, x, ld_x, w13, w13_s, w2, w2_s, x_sf, w13_sf, h_sf, w2_sf, y, ld_y, tokens, hidden, inter, experts, top_k,
+                        workspace, workspace_bytes, stream);
+}
+
+int32_t bsq_moe_layer_routed(int32_t fmt, const void* x, int64_t ld_x, const int32_t* ids, const float* weights, const void* w13,
+                             const void* w13_s, const void* w2, const void* w2_s, const float* x_sf, const float* w13_sf,
+                             const float* h_sf, const float* w2_sf, void* y, int64_t ld_y, int32_t tokens, int64_t hidden,
+                             int64_t inter, int32_t experts, int32_t top_k, void* workspace, int64_t workspace_bytes, void* stream) {
+  MoeArgs a{};
+  a.ids = ids;
+  a.weights = weights;
+  return run_moe<true>(fmt, a, x, ld_x, w13, w13_s, w2, w2_s, x_sf, w13_sf, h_sf, w2_sf, y, ld_y, tokens, hidden, inter, experts, top_k,
+                       workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

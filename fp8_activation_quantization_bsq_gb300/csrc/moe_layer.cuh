@@ -64,6 +64,8 @@ struct MoeArgs {
   int64_t ld_x;
   const float* logits;
   int64_t ld_logits;
+  const int32_t* ids;    // a finished routing in place of the logits: (tokens, top_k)
+  const float* weights;
   const uint8_t *w13_s, *w2_s;
   const float *x_sf, *w13_sf, *h_sf, *w2_sf;  // NVFP4
   uint16_t* y;
@@ -191,6 +193,28 @@ __device__ __forceinline__ void moe_route(const MoeArgs& a, const MoeTables& tb,
     tb.prob[t * a.top_k + lane] = top > -INFINITY ? p / sum : 0.f;
     tb.id[t * a.top_k + lane] = my_id;
     atomicOr(&tb.mask[2 * my_id + (t >> 5)], 1u << (t & 31));
+  }
+}
+
+// The choices of token t from a finished routing, with one warp, a lane per choice.  One without an expert gets id -1 and
+// has no row; an expert that comes again for a token takes the later weights too.
+__device__ __forceinline__ void moe_take_route(const MoeArgs& a, const MoeTables& tb, int t, int lane) {
+  const bool in = lane < a.top_k;
+  int id = in ? __ldg(a.ids + t * a.top_k + lane) : -1;
+  const float w = in ? __ldg(a.weights + t * a.top_k + lane) : 0.f;
+  if (__any_sync(~0u, id >= a.experts) && lane == 0 && blockIdx.x == 0) record_error_at(a.err, kErrValue);
+  if (id >= a.experts) id = -1;
+  const uint32_t same = __match_any_sync(~0u, id >= 0 ? id : -1 - lane);
+  float sum = 0.f;
+  for (int k = 0; k < a.top_k; ++k) {
+    const float wk = __shfl_sync(~0u, w, k);
+    if (same >> k & 1u) sum += wk;
+  }
+  if (__ffs(same) - 1 != lane) id = -1;
+  if (in) {
+    tb.id[t * a.top_k + lane] = id < 0 ? -1 : id;
+    tb.prob[t * a.top_k + lane] = sum;
+    if (id >= 0) atomicOr(&tb.mask[2 * id + (t >> 5)], 1u << (t & 31));
   }
 }
 
@@ -322,7 +346,8 @@ __device__ __forceinline__ bool moe_wait_count(const uint32_t* p, uint32_t value
   return true;
 }
 
-template <int FMT>
+// ROUTED: the routing is given (moe_take_route), and may leave choices without an expert.
+template <int FMT, bool ROUTED>
 __global__ void __launch_bounds__(kMoeThreads, 1)
     moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_constant__ CUtensorMap map_w2,
                      const __grid_constant__ CUtensorMap map_xq, const __grid_constant__ CUtensorMap map_hq, const MoeArgs a) {
@@ -387,7 +412,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   // as many logits a lane as the experts need, in two sizes (256 experts: 649 / 668 us for 64 tokens and 51 / 52
   // for one with the smaller / larger form)
   const uint32_t spoiled_word = tid == 0 ? __ldcg(a.counters + kMoeSpoiled) : 0u;
-  if (a.experts <= 256) {
+  if constexpr (ROUTED) {
+    for (int t = warp; t < a.tokens; t += kMoeThreads / 32) moe_take_route(a, tb, t, lane);
+  } else if (a.experts <= 256) {
     for (int t = warp; t < a.tokens; t += kMoeThreads / 32) moe_route<8>(a, tb, t, lane);
   } else {
     for (int t = warp; t < a.tokens; t += kMoeThreads / 32) moe_route<32>(a, tb, t, lane);
@@ -440,6 +467,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   t5_fence_after();
   for (int p = tid; p < pairs; p += kMoeThreads) {  // rows of an expert in token order
     const int t = p / a.top_k, e = tb.id[p];
+    if (ROUTED && e < 0) continue;
     tb.pair_of[tb.row0[tb.index_of[e]] + moe_rank(tb, e, t)] = p;
   }
   __syncthreads();
@@ -588,14 +616,17 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         uint4 next[4];
         moe_load_x(a, quant_at + quant_step, quant_total, per_row, next);
         const int pair = quant_at / per_row, c = quant_at - pair * per_row, t = pair / a.top_k;
-        const int e = tb.id[pair], i = tb.index_of[e], r = moe_rank(tb, e, t);
-        const int s0 = 32 * c / kSF;  // first scale column
-        uint8_t* sc = a.xq_s + static_cast<int64_t>(i) * kt * 512;
-        uint8_t* word = sc + moe_token_scale(r, s0);
-        moe_quant_block<FMT>(xv, FMT == kNVFP4 ? __ldg(a.x_sf + e) : 1.f,
-                             a.xq + static_cast<int64_t>(tb.row0[i] + r) * row_bytes + (FMT == kMXFP8 ? 32 * c : 16 * c), word);
-        if (c == per_row - 1)  // the last atom's columns past the row: zero
-          for (int s = s0 + 32 / kSF; s < 4 * kt; ++s) sc[moe_token_scale(r, s)] = 0;
+        const int e = tb.id[pair];
+        if (!ROUTED || e >= 0) {
+          const int i = tb.index_of[e], r = moe_rank(tb, e, t);
+          const int s0 = 32 * c / kSF;  // first scale column
+          uint8_t* sc = a.xq_s + static_cast<int64_t>(i) * kt * 512;
+          uint8_t* word = sc + moe_token_scale(r, s0);
+          moe_quant_block<FMT>(xv, FMT == kNVFP4 ? __ldg(a.x_sf + e) : 1.f,
+                               a.xq + static_cast<int64_t>(tb.row0[i] + r) * row_bytes + (FMT == kMXFP8 ? 32 * c : 16 * c), word);
+          if (c == per_row - 1)  // the last atom's columns past the row: zero
+            for (int s = s0 + 32 / kSF; s < 4 * kt; ++s) sc[moe_token_scale(r, s)] = 0;
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) xv[q] = next[q];
         quant_at += quant_step;
@@ -732,7 +763,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           float4 v[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            if (k0 + k < a.top_k) v[k] = __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(k0 + k) * a.hidden));
+            if (k0 + k < a.top_k) {
+              if (ROUTED && tb.id[t * a.top_k + k0 + k] < 0)
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              else
+                v[k] = __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(k0 + k) * a.hidden));
+            }
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             if (k0 + k < a.top_k) {

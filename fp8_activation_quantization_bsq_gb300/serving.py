@@ -158,11 +158,13 @@ def moe_layer_workspace_bytes(fmt, tokens: int, hidden: int, inter: int, experts
 
 def moe_layer(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w13_scales: torch.Tensor, w2: torch.Tensor,
               w2_scales: torch.Tensor, fmt, top_k: int, x_sf=None, w13_sf=None, h_sf=None, w2_sf=None,
-              renormalize: bool = True, out=None, workspace=None, stream=None) -> torch.Tensor:
+              renormalize: bool = True, out=None, workspace=None, stream=None, routing=None) -> torch.Tensor:
     """A mixture-of-experts layer for at most 64 tokens.
 
     ``x``: BF16 (tokens, hidden); ``logits``: float32 (tokens, experts) of the
-    router.  ``w13``: packed codes (experts, 2*inter, row bytes), gate rows
+    router, or None with ``routing``: (ids, weights) as :func:`moe_route`
+    gives them, int32 and float32 (tokens, top_k), which are then taken as
+    they are (a negative id is no choice).  ``w13``: packed codes (experts, 2*inter, row bytes), gate rows
     first, and ``w2`` (experts, hidden, row bytes), as :func:`quantize` gives
     them for each expert's BF16 rows, with their 5D scales (experts, bytes).
     NVFP4 also takes the float32 (experts) tensor scales of x, w13, the inner
@@ -178,12 +180,25 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w13_scal
         raise ValueError("x must be a 2-D bfloat16 CUDA tensor with unit inner stride")
     tokens, hidden = shape
     index = x.get_device()
-    lshape = logits.shape
-    if logits.dtype is not _F32 or len(lshape) != 2 or lshape[0] != tokens or (ls := logits.stride())[1] != 1:
-        raise ValueError("logits must be a float32 (tokens, experts) tensor with unit inner stride")
-    experts = lshape[1]
-    f = _fmt(fmt)
     s13, s2 = w13.shape, w2.shape
+    if routing is not None:
+        ids, weights = routing
+        if logits is not None:
+            raise ValueError("logits must be None when a routing is given")
+        if ids.dtype is not _I32 or ids.shape != (tokens, top_k) or not ids.is_contiguous() or ids.get_device() != index or \
+                weights.dtype is not _F32 or weights.shape != (tokens, top_k) or not weights.is_contiguous() or weights.get_device() != index:
+            raise ValueError("routing must be contiguous int32 and float32 (tokens, top_k) tensors on x's device")
+        if len(s13) != 3:
+            raise ValueError("w13 must be a contiguous uint8 (experts, rows, row bytes) tensor")
+        experts = s13[0]
+    else:
+        lshape = logits.shape
+        if logits.dtype is not _F32 or len(lshape) != 2 or lshape[0] != tokens or (ls := logits.stride())[1] != 1:
+            raise ValueError("logits must be a float32 (tokens, experts) tensor with unit inner stride")
+        if logits.get_device() != index:
+            raise ValueError("all tensors must be on one CUDA device")
+        experts = lshape[1]
+    f = _fmt(fmt)
     if w13.dtype is not _U8 or len(s13) != 3 or w2.dtype is not _U8 or len(s2) != 3 or not w13.is_contiguous() or \
             not w2.is_contiguous():
         raise ValueError("w13 and w2 must be contiguous uint8 (experts, rows, row bytes) tensors")
@@ -197,7 +212,7 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w13_scal
     if w13_scales.dtype is not _U8 or w13_scales.numel() != n13 or not w13_scales.is_contiguous() or \
             w2_scales.dtype is not _U8 or w2_scales.numel() != n2 or not w2_scales.is_contiguous():
         raise ValueError("w13_scales and w2_scales must be contiguous uint8 tensors of each expert's 5D scales")
-    if not (logits.get_device() == w13.get_device() == w2.get_device() == w13_scales.get_device() == w2_scales.get_device() == index):
+    if not (w13.get_device() == w2.get_device() == w13_scales.get_device() == w2_scales.get_device() == index):
         raise ValueError("all tensors must be on one CUDA device")
     if f == _NVFP4:
         for t in (x_sf, w13_sf, h_sf, w2_sf):
@@ -215,8 +230,12 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor, w13_scal
                                    lib().bsq_moe_layer_counter_bytes(), x.device)
     elif workspace.dtype is not _U8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on x's device")
-    _call("bsq_moe_layer", index, stream,
-          (f, x.data_ptr(), xs[0], logits.data_ptr(), ls[0], w13.data_ptr(), w13_scales.data_ptr(), w2.data_ptr(),
-           w2_scales.data_ptr(), *sfs, out.data_ptr(), out.stride(0), tokens, hidden, inter, experts, top_k,
-           1 if renormalize else 0, workspace.data_ptr(), workspace.numel()))
+    weights_and_scales = (w13.data_ptr(), w13_scales.data_ptr(), w2.data_ptr(), w2_scales.data_ptr(), *sfs, out.data_ptr(), out.stride(0),
+                          tokens, hidden, inter, experts, top_k)
+    if routing is not None:
+        _call("bsq_moe_layer_routed", index, stream, (f, x.data_ptr(), xs[0], ids.data_ptr(), weights.data_ptr(), *weights_and_scales,
+                                                      workspace.data_ptr(), workspace.numel()))
+    else:
+        _call("bsq_moe_layer", index, stream, (f, x.data_ptr(), xs[0], logits.data_ptr(), ls[0], *weights_and_scales,
+                                               1 if renormalize else 0, workspace.data_ptr(), workspace.numel()))
     return out

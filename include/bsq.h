@@ -559,6 +559,19 @@ BSQ_API int32_t bsq_moe_layer(int32_t fmt, const void* x_dev, int64_t ld_x, cons
                               int64_t hidden, int64_t inter, int32_t experts, int32_t top_k, int32_t renormalize,
                               void* workspace_dev, int64_t workspace_bytes, void* stream);
 
+/*
+ * The same layer with a finished routing in place of the logits (bsq_moe_route's, or any other): token t's choices are the experts
+ * ids[t*top_k ..] with the weights weights[t*top_k ..], taken as they are.
+ *   ids_dev, weights_dev   int32 and float (tokens, top_k), contiguous.  A negative id is no choice (its weight does not matter); an
+ *                     id past the last expert counts as negative and records BSQ_ERR_VALUE.  An expert that comes again for a token adds
+ *                     its weight to the first time.  A choice of weight 0 adds nothing.
+ */
+BSQ_API int32_t bsq_moe_layer_routed(int32_t fmt, const void* x_dev, int64_t ld_x, const int32_t* ids_dev, const float* weights_dev,
+                                     const void* w13_dev, const void* w13_scales_dev, const void* w2_dev, const void* w2_scales_dev,
+                                     const float* x_sf_dev, const float* w13_sf_dev, const float* h_sf_dev, const float* w2_sf_dev,
+                                     void* y_dev, int64_t ld_y, int32_t tokens, int64_t hidden, int64_t inter, int32_t experts,
+                                     int32_t top_k, void* workspace_dev, int64_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------------
  * Between those calls: projections over packed weights, norm and rotation of
  * query and key heads, routing to experts.

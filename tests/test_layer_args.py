@@ -93,3 +93,15 @@ def test_binding_rejects_host_and_mistyped_tensors(bsq):
         bsq.moe_route(f32(1, 8), 2)
     with pytest.raises(ValueError, match="CUDA"):
         bsq.moe_rows(i32(1, 2), 8)
+
+
+ROUTED = dict(fmt=2, x=P, ld_x=64, ids=P, weights=P, w13=P, w13_s=P, w2=P, w2_s=P, x_sf=None, w13_sf=None, h_sf=None, w2_sf=None, y=P, ld_y=64,
+              tokens=2, hidden=64, inter=128, experts=4, top_k=2, ws=P, ws_bytes=1 << 40, stream=None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(fmt=3), VALUE), (dict(tokens=65), SHAPE), (dict(top_k=5), SHAPE), (dict(ld_x=56), SHAPE), (dict(ids=None), NULL), (dict(weights=None), NULL),
+    (dict(x=None), NULL), (dict(fmt=0), NULL), (dict(ids=P + 2), ALIGN), (dict(weights=P + 1), ALIGN), (dict(ws=P + 16), ALIGN),
+    (dict(ws_bytes=100), SHAPE), (dict(tokens=0), OK)])
+def test_routed_moe_refusals(bsq, change, code):
+    assert bsq.lib().bsq_moe_layer_routed(*{**ROUTED, **change}.values()) == code
