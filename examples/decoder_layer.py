@@ -3,11 +3,14 @@
 paged key/value cache in chunks, then tokens are generated one per sequence,
 with attention over the cache and a mixture of experts over packed weights.
 
-    python examples/decoder_layer.py [--fmt nvfp4] [--batch 4] [--prompt 300] [--steps 8]
+    python examples/decoder_layer.py [--fmt nvfp4] [--batch 4] [--prompt 300] [--steps 8] [--packed]
 
-Weights are random; the layer's projections are plain matmuls.  A whole
-decoding step can be captured in a CUDA graph: every call is asynchronous on
-the current stream and keeps its workspace."""
+Weights are random.  The layer's projections are plain matmuls and its router
+a softmax inside the expert layer; with --packed the projections and the
+router run over packed weights, queries and keys are normed and rotated by
+their positions, and experts are chosen by biased sigmoid scores among
+groups.  A whole decoding step can be captured in a CUDA graph: every call is
+asynchronous on the current stream and keeps its workspace."""
 from __future__ import annotations
 
 import argparse
@@ -85,9 +88,50 @@ class Layer:
         return torch.cat([self.experts(part) for part in x.split(64)])  # the expert layer takes a few tokens at a time
 
 
-def serve(fmt="nvfp4", batch=4, prompt=300, steps=8, chunk=128, seed=0):
+class PackedLayer(Layer):
+    """The same layer with its projections and router in packed weights, norm and rotation of queries and keys, and
+    experts chosen in groups."""
+
+    def __init__(self, fmt, *, groups=4, top_groups=2, base=10000.0, seed=0, device="cuda", **sizes):
+        super().__init__(fmt, seed=seed, device=device, **sizes)
+        self.groups, self.top_groups = groups, top_groups
+        self.projections = {}
+        for name in ("w_qkv", "w_out", "w_router"):
+            w = getattr(self, name)
+            sf = bsq.tensor_sf(w)[1:] if fmt == "nvfp4" else None
+            self.projections[name] = (*bsq.quantize_dynamic(w, fmt, sf), fmt, sf)
+        g = torch.Generator(device=device).manual_seed(seed + 2)
+        self.q_weight, self.k_weight = (1 + 0.1 * torch.randn((2, self.dim), generator=g, device=device)).bfloat16().unbind()
+        self.bias = 0.05 * torch.randn(self.w_router.shape[0], generator=g, device=device)
+        self.inv_freq = base ** (-torch.arange(0, self.dim, 2, device=device) / self.dim)
+
+    def attend(self, x, cache, offsets, max_q):
+        tokens = x.shape[0]
+        h = torch.nn.functional.rms_norm(x, (self.hidden,))
+        qkv = bsq.packed_linear(h, *self.projections["w_qkv"]).view(tokens, -1, self.dim)
+        q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)
+        positions = (cache.lens[:, None] - max_q + torch.arange(max_q, dtype=torch.int32, device=x.device)).flatten()
+        bsq.qk_norm_rope(q, k, positions, self.inv_freq, self.q_weight, self.k_weight, q_out=q, k_out=k)  # in place, v beside them stays
+        bsq.kv_append(k, v, *cache.tensors(), offsets, cache.lens)
+        ws = self.workspace("attention", bsq.kv_attention_workspace_bytes(tokens, self.heads, self.kv_heads, self.dim, cache.lens.numel(), max_q))
+        out = bsq.kv_attention(q, *cache.tensors(), offsets, cache.lens, max_q, workspace=ws)
+        return bsq.packed_linear(out.view(tokens, -1), *self.projections["w_out"], add=x)
+
+    def route(self, y):
+        logits = bsq.packed_linear(y, *self.projections["w_router"], out_dtype=torch.float32)
+        return bsq.moe_route(logits, self.top_k, "sigmoid", self.bias, self.groups, self.top_groups)
+
+    def experts(self, x):
+        y = torch.nn.functional.rms_norm(x.contiguous(), (self.hidden,))
+        routing = self.route(y)
+        ws = self.workspace("moe", bsq.moe_layer_workspace_bytes(self.fmt, x.shape[0], self.hidden, self.moe[2].shape[2] * (1 if self.fmt == "mxfp8" else 2),
+                                                                 self.bias.numel(), self.top_k))
+        return x + bsq.moe_layer(y, None, *self.moe, self.fmt, self.top_k, workspace=ws, routing=routing, **self.kw)
+
+
+def serve(fmt="nvfp4", batch=4, prompt=300, steps=8, chunk=128, seed=0, packed=False):
     """(outputs of the prompts' last tokens and of each step, the cache)."""
-    layer = Layer(fmt, seed=seed)
+    layer = (PackedLayer if packed else Layer)(fmt, seed=seed)
     cache = Cache(batch, prompt + steps, layer.kv_heads, layer.dim)
     g = torch.Generator(device="cuda").manual_seed(seed + 1)
     prompts = torch.randn((batch, prompt, layer.hidden), generator=g, device="cuda").bfloat16()
@@ -112,8 +156,9 @@ def main(argv=None):
     ap.add_argument("--batch", type=int, default=4)
     ap.add_argument("--prompt", type=int, default=300)
     ap.add_argument("--steps", type=int, default=8)
+    ap.add_argument("--packed", action="store_true")
     a = ap.parse_args(argv)
-    outs, cache = serve(a.fmt, a.batch, a.prompt, a.steps)
+    outs, cache = serve(a.fmt, a.batch, a.prompt, a.steps, packed=a.packed)
     torch.cuda.synchronize()
     assert bsq.device_error() == 0
     print(f"{a.fmt}: {a.batch} prompts of {a.prompt} tokens and {a.steps} steps; cache lengths {cache.lens.tolist()}, "
