@@ -94,11 +94,12 @@ bsq_status launch_many(const PlArgs& p, const HostDevice& d, cudaStream_t st) {
   }
   a.x_bytes = a.tokens_tile * 128;
   a.w_bytes = static_cast<int>(ceil_div(MT * (F::kTileBytes + F::kAtoms * 512), 1024) * 1024);
-  // halves of a step of tokens: four at least; stages of weights: what is left, at most as many as those four need twice over
-  a.w_stages = std::min(5, (kPmSmem - 1024 - 4 * a.x_bytes) / a.w_bytes);
-  a.x_stages = std::min(kPmMaxStages, (kPmSmem - 1024 - a.w_stages * a.w_bytes) / a.x_bytes);
+  // as many steps as tensor memory holds weights of, four at least, if their tokens leave room for three stages of weights
+  const int room = kPmSmem - 1024, d_cols = MT == 1 ? 256 : a.tokens_tile <= 64 ? 128 : 256;
+  a.depth = std::min((512 - d_cols) / (32 * MT), std::max(4, (room - 3 * a.w_bytes) / a.x_bytes));
+  a.w_stages = std::min(6, (room - a.depth * a.x_bytes) / a.w_bytes);
   // more than half of the SM's memory, and the sums of a cluster's block
-  const int smem = std::max({1024 + a.w_stages * a.w_bytes + a.x_stages * a.x_bytes, 120 * 1024,
+  const int smem = std::max({1024 + a.w_stages * a.w_bytes + a.depth * a.x_bytes, 120 * 1024,
                              ranks > 1 ? 1024 + a.tokens_tile * 128 * MT * 4 : 0});
   CUtensorMap mw, mx;
   if (!linear_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, p.row_bytes, p.rows, p.row_bytes, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||

@@ -26,21 +26,21 @@ namespace bsq {
 
 constexpr int kPmConverters = 16;  // warps
 constexpr int kPmThreads = 32 * (4 + kPmConverters);
-constexpr int kPmMaxStages = 12;
+constexpr int kPmMaxStages = 8;
 
 struct PmArgs {
   PlArgs p;
   int tokens_tile;        // of a block, a multiple of 16
   int row_tiles, token_tiles;
   int stages;             // of weights in a row, in all
-  int x_stages, w_stages, x_bytes, w_bytes;
+  int depth, w_stages, x_bytes, w_bytes;  // steps (tokens in shared, weights in tensor memory) and stages of weights in flight
   unsigned int* err;
 };
 
-// A stage of weights: 128 bytes of each row of a tile, and their scale atoms.  It is converted in steps of 128 columns and
-// multiplied in halves of a step, 64 columns, a stage of the tokens each.
+// A stage of weights: 128 bytes of each row of a tile, and their scale atoms.  It is converted and multiplied in steps of 64
+// columns.
 template <int FMT> struct PmFmt {
-  static constexpr int kCols = FMT == kMXFP8 ? 128 : 256, kSteps = kCols / 128;
+  static constexpr int kCols = FMT == kMXFP8 ? 128 : 256, kSteps = kCols / 64;
   static constexpr int kTileBytes = 128 * 128;
   static constexpr int kAtoms = kCols / Fmt<FMT>::ATOM_COLS;
 };
@@ -66,14 +66,14 @@ __device__ __forceinline__ uint32_t pm_scaled_bf16(uint32_t h, float f) {
   return f32x2_to_elem2<false>(v.x, v.y);
 }
 
-// The factors of a row's step: NVFP4 eight, MX four, as FP16 pairs or FP32 numbers.  `top`: with FP16 tokens and MX, the byte
-// that stands for 2^13 (E2M1) or 2^7 (E4M3).
+// The factors of a row's step: NVFP4 four, from `word`'s bytes, MX two, from its bytes at `at` and behind, as FP16 pairs or FP32
+// numbers.  `top`: with FP16 tokens and MX, the byte that stands for 2^13 (E2M1) or 2^7 (E4M3).
 template <int FMT, bool F16>
-__device__ __forceinline__ void pm_factors(const uint32_t (&word)[2], int top, uint32_t (&f)[8]) {
+__device__ __forceinline__ void pm_factors(uint32_t word, int at, int top, uint32_t (&f)[4]) {
   if constexpr (FMT == kNVFP4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t pair = e4m3x2_to_f16x2(word[i / 2] >> (16 * (i & 1)) & 0xFFFFu);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t pair = e4m3x2_to_f16x2(word >> (16 * i) & 0xFFFFu);
       if constexpr (F16) {
         f[2 * i] = __byte_perm(pair, 0, 0x1010);
         f[2 * i + 1] = __byte_perm(pair, 0, 0x3232);
@@ -85,8 +85,8 @@ __device__ __forceinline__ void pm_factors(const uint32_t (&word)[2], int top, u
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t byte = word[0] >> (8 * i) & 255u;
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t byte = word >> (8 * (at + i)) & 255u;
       if constexpr (F16) {
         const int e = static_cast<int>(byte) - top + (FMT == kMXFP8 ? 7 : 13);  // at most 13
         const uint32_t one = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
@@ -161,42 +161,40 @@ template <int FMT, bool F16, int MT>
 __global__ void __launch_bounds__(kPmThreads, 1)
     packed_many_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const PmArgs a) {
   using F = PmFmt<FMT>;
-  // tensor memory: the tiles' sums, then the weights in buffers of half a step, 32 columns per tile
-  constexpr int kMaxBufs = 8, kBufCols = 32 * MT;
-  const uint32_t d_col = a.tokens_tile <= 64 ? 64 : 128, a_col = MT == 1 ? 256 : 2 * d_col, a_bufs = (512 - a_col) / kBufCols;  // 8; 6 or 4
+  // tensor memory: the tiles' sums, then the weights of `depth` steps, 32 columns per tile
+  constexpr uint32_t kBufCols = 32 * MT;
+  const uint32_t d_col = a.tokens_tile <= 64 ? 64 : 128, a_col = MT == 1 ? 256 : 2 * d_col, depth = a.depth;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  __shared__ uint64_t x_full[kPmMaxStages], x_empty[kPmMaxStages], w_full[kPmMaxStages], w_empty[kPmMaxStages];
-  __shared__ uint64_t a_full[kMaxBufs], a_empty[kMaxBufs], d_full, d_empty, drain_bar;
+  // a step is full when its tokens have landed and its weights are converted: one wait and one commit of the products' warp, whose
+  // own instructions would otherwise take longer than the products (two waits and commits a step: 236 us for 2048 tokens)
+  __shared__ uint64_t full[kPmMaxStages], empty[kPmMaxStages], w_full[kPmMaxStages], w_empty[kPmMaxStages], d_full, d_empty, drain_bar;
   __shared__ uint32_t tmem_slot;
-  __shared__ volatile uint32_t abort_flag, x_fills, w_fills;
+  __shared__ volatile uint32_t abort_flag, x_fills, w_fills, converted[kPmConverters];  // steps of each warp
 
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int ranks = gridDim.y;  // of the cluster
   uint8_t* const xs = smem;
-  uint8_t* const ws = smem + a.x_stages * a.x_bytes;
+  uint8_t* const ws = smem + depth * a.x_bytes;
   const int share = (a.stages + ranks - 1) / ranks;
   const int k_lo = blockIdx.y * share, k_hi = min(k_lo + share, a.stages);  // of the block's share of K
-  const int col0 = k_lo * F::kCols, halves = (min(k_hi * F::kCols, a.p.cols) - col0 + 63) / 64, steps = (halves + 1) / 2;
+  const int col0 = k_lo * F::kCols, steps = (min(k_hi * F::kCols, a.p.cols) - col0 + 63) / 64;
   const int n_tok = a.tokens_tile;
   if (tid == 0) {
-    for (int i = 0; i < a.x_stages; ++i) {
-      mbar_init(&x_full[i], 1);
-      mbar_init(&x_empty[i], 1);
+    for (uint32_t i = 0; i < depth; ++i) {
+      mbar_init(&full[i], 4 * MT + 1);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < a.w_stages; ++i) {
       mbar_init(&w_full[i], 1);
       mbar_init(&w_empty[i], kPmConverters);
-    }
-    for (int i = 0; i < kMaxBufs; ++i) {
-      mbar_init(&a_full[i], 4 * MT);
-      mbar_init(&a_empty[i], 1);
     }
     mbar_init(&d_full, 1);
     mbar_init(&d_empty, kPmConverters);
     mbar_init(&drain_bar, 1);
     abort_flag = 0u;
     x_fills = w_fills = 0u;
+    for (int i = 0; i < kPmConverters; ++i) converted[i] = 0u;
     fence_mbar_init();
     prefetch_tensormap(&map_w);
     prefetch_tensormap(&map_x);
@@ -241,17 +239,17 @@ __global__ void __launch_bounds__(kPmThreads, 1)
   } else if (warp == 0) {
     // ---- copies of tokens
     if (lane == 0) {
-      uint32_t n = 0;
+      uint32_t n = 0, b = 0, parity = 1;
       bool ok = true;
       for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
         const int y = tile % a.token_tiles * n_tok;
-        for (int h = 0; h < halves; ++h) {
-          const uint32_t s = n % a.x_stages;
-          ok = mbar_wait_clocked(&x_empty[s], (n / a.x_stages & 1u) ^ 1u, &abort_flag);
+        for (int h = 0; h < steps; ++h) {
+          ok = mbar_wait_clocked(&empty[b], parity, &abort_flag);
           if (!ok) break;
-          mbar_arrive_expect_tx(&x_full[s], a.x_bytes);
-          tma_load_2d(xs + s * a.x_bytes, &map_x, col0 + h * 64, y, &x_full[s]);
+          mbar_arrive_expect_tx(&full[b], a.x_bytes);
+          tma_load_2d(xs + b * a.x_bytes, &map_x, col0 + h * 64, y, &full[b]);
           x_fills = ++n;
+          if (++b == depth) { b = 0; parity ^= 1u; }
         }
       }
       if (!ok) fail();
@@ -261,22 +259,23 @@ __global__ void __launch_bounds__(kPmThreads, 1)
     const uint32_t lead = t5_elect();
     const uint32_t idesc = t5_idesc_f16(n_tok, false) | (F16 ? 0u : (1u << 7) | (1u << 10));
     const auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(~0u, mbar_wait_clocked(bar, parity, &abort_flag)); };
-    uint32_t n = 0, done = 0;
+    const uint64_t x_desc = t5_desc_sw128(smem_addr(xs));
+    const uint32_t x_step = a.x_bytes >> 4;
+    uint32_t b = 0, parity = 0, done = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++done) {
       const bool two = MT == 2 && static_cast<int64_t>(tile / a.token_tiles * MT + 1) * 128 < a.p.rows;
       ok = wait(&d_empty, (done & 1u) ^ 1u);
-      for (int h = 0; h < halves && ok; ++h, ++n) {
-        const uint32_t b = n % a_bufs, s = n % a.x_stages;
-        ok = wait(&a_full[b], n / a_bufs & 1u) && wait(&x_full[s], n / a.x_stages & 1u);
+      for (int h = 0; h < steps; ++h) {
+        ok = ok && wait(&full[b], parity);
         if (!ok) break;
         t5_fence_after();
-        const uint64_t db = t5_desc_sw128(smem_addr(xs + s * a.x_bytes));
+        const uint64_t db = x_desc + b * x_step;
         const uint32_t ta = tmem + a_col + b * kBufCols;
         pm_mma64(tmem, ta, db, idesc, h > 0, lead);
         if (two) pm_mma64(tmem + d_col, ta + 32, db, idesc, h > 0, lead);
-        t5_commit(smem_addr(&x_empty[s]), lead);
-        t5_commit(smem_addr(&a_empty[b]), lead);
+        t5_commit(smem_addr(&empty[b]), lead);
+        if (++b == depth) { b = 0; parity ^= 1u; }
       }
       if (ok) t5_commit(smem_addr(&d_full), lead);
     }
@@ -290,7 +289,7 @@ __global__ void __launch_bounds__(kPmThreads, 1)
     const int group = (warp - 4) >> 2, m = group / kTurns, turn = group % kTurns, quarter = warp & 3, r = 32 * quarter + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const float inv = FMT == kNVFP4 ? __fdiv_rn(1.f, __ldg(a.p.sf)) : 1.f;
-    uint32_t wn = 0, done = 0;
+    uint32_t wn = 0, done = 0, b = turn, parity = 1, next = turn;  // next: this group's next step, counted over all tiles
     bool ok = true;
     for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++done) {
       const int rt = tile / a.token_tiles, tt = tile % a.token_tiles;
@@ -300,7 +299,7 @@ __global__ void __launch_bounds__(kPmThreads, 1)
       if constexpr (F16 && FMT != kNVFP4) {
         if (!idle) {
           const uint8_t* s = a.p.scales + band * a.p.k_atoms * 512 + lane * 16 + quarter * 4;
-          for (int c = col0; c < col0 + halves * 64; c += 128) {
+          for (int c = col0; c < col0 + steps * 64; c += 128) {
             const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(s + static_cast<int64_t>(c / 128) * 512));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -313,45 +312,43 @@ __global__ void __launch_bounds__(kPmThreads, 1)
         // every group waits for and gives back every stage, converted by it or not: a barrier's parity tells only neighbouring
         // phases apart, so none may pass unseen
         ok = __all_sync(~0u, mbar_wait_clocked(&w_full[s], wn / a.w_stages & 1u, &abort_flag));
-#pragma unroll 1
-        for (int j = 0; j < F::kSteps && ok; ++j) {
-          const uint32_t step = k * F::kSteps + j;  // of the tile
-          if (step >= static_cast<uint32_t>(steps) || (done * steps + step) % kTurns != static_cast<uint32_t>(turn)) continue;
-          const uint8_t* w = ws + s * a.w_bytes + m * F::kTileBytes + r * 128;
-          uint32_t word[2] = {0u, 0u}, f[8];
+        const uint32_t base = done * steps, stop = base + min((k + 1) * F::kSteps, steps);
+        while (ok && next < stop) {
+          const int j = static_cast<int>(next - base) - k * F::kSteps;  // of the stage
+          // unambiguous: `depth` is at least kTurns, so this group's last step knew the phase before
+          ok = __all_sync(~0u, mbar_wait_clocked(&empty[b], parity, &abort_flag));
+          if (!ok) break;
+          t5_fence_after();
           if (!idle) {
-            constexpr int kStepAtoms = F::kAtoms / F::kSteps;
-            const uint8_t* sc = ws + s * a.w_bytes + MT * F::kTileBytes + (m * F::kAtoms + j * kStepAtoms) * 512 + lane * 16 + quarter * 4;
-            word[0] = *reinterpret_cast<const uint32_t*>(sc);
-            if (FMT == kNVFP4 && 2 * static_cast<int>(step) + 1 < halves) word[1] = *reinterpret_cast<const uint32_t*>(sc + 512);
-          }
-          pm_factors<FMT, F16>(word, top, f);
+            // 64 columns: NVFP4 a scale atom, MX half of one
+            const int atom = FMT == kNVFP4 ? j : j / 2;
+            const uint32_t word = *reinterpret_cast<const uint32_t*>(ws + s * a.w_bytes + MT * F::kTileBytes + (m * F::kAtoms + atom) * 512 +
+                                                                     lane * 16 + quarter * 4);
+            const uint8_t* w = ws + s * a.w_bytes + m * F::kTileBytes + r * 128;
+            uint32_t f[4];
+            pm_factors<FMT, F16>(word, 2 * (j & 1), top, f);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (2 * static_cast<int>(step) + h >= halves) break;
-            const uint32_t n = done * halves + 2 * step + h, b = n % a_bufs;
-            // unambiguous: there are at least 2 kTurns buffers, so this group's last step knew the phase before
-            ok = __all_sync(~0u, mbar_wait_clocked(&a_empty[b], (n / a_bufs & 1u) ^ 1u, &abort_flag));
-            if (!ok) break;
-            t5_fence_after();
-            if (!idle) {
+            for (int q = 0; q < 2; ++q) {  // 32 columns each
+              uint32_t v[16];
+              pm_codes<FMT>(w, 2 * j + q, r & 7, v);
 #pragma unroll
-              for (int q = 2 * h; q < 2 * h + 2; ++q) {  // 32 columns each
-                uint32_t v[16];
-                pm_codes<FMT>(w, 4 * j + q, r & 7, v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const uint32_t g = FMT == kNVFP4 ? f[2 * q + i / 8] : f[q];
-                  v[i] = F16 ? mul_f16x2(v[i], g) : pm_scaled_bf16(v[i], __uint_as_float(g));
-                }
-                t5_st16(lanes + a_col + b * kBufCols + 32 * m + 16 * (q & 1), v);
+              for (int i = 0; i < 16; ++i) {
+                const uint32_t g = FMT == kNVFP4 ? f[2 * q + i / 8] : f[q];
+                v[i] = F16 ? mul_f16x2(v[i], g) : pm_scaled_bf16(v[i], __uint_as_float(g));
               }
-              t5_st_wait();
+              t5_st16(lanes + a_col + b * kBufCols + 32 * m + 16 * q, v);
             }
-            t5_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&a_full[b]);
+            t5_st_wait();
           }
+          t5_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&full[b]);
+            converted[warp - 4] = next / kTurns + 1u;
+          }
+          next += kTurns;
+          b += kTurns;
+          if (b >= depth) { b -= depth; parity ^= 1u; }
         }
         if (ok && lane == 0) mbar_arrive(&w_empty[s]);
       }
@@ -392,8 +389,12 @@ __global__ void __launch_bounds__(kPmThreads, 1)
   // after an expired wait: loads that nothing consumed land before the block ends (the last fill of each stage)
   if (tid == 0 && abort_flag != 0u) {
     const uint32_t xf = x_fills, wf = w_fills;
-    for (uint32_t i = xf > static_cast<uint32_t>(a.x_stages) ? xf - a.x_stages : 0u; i < xf; ++i)
-      if (!mbar_wait_clocked(&x_full[i % a.x_stages], i / a.x_stages & 1u)) record_error_at(a.err, kErrTimeout);
+    constexpr uint32_t kTurns = kPmConverters / 4 / MT;
+    for (uint32_t i = xf > depth ? xf - depth : 0u; i < xf; ++i) {
+      for (uint32_t w = 0; w < kPmConverters; ++w)  // in place of the converters that have not come to this step
+        if (w / 4 % kTurns == i % kTurns && converted[w] <= i / kTurns) mbar_arrive(&full[i % depth]);
+      if (!mbar_wait_clocked(&full[i % depth], i / depth & 1u)) record_error_at(a.err, kErrTimeout);
+    }
     for (uint32_t i = wf > static_cast<uint32_t>(a.w_stages) ? wf - a.w_stages : 0u; i < wf; ++i)
       if (!mbar_wait_clocked(&w_full[i % a.w_stages], i / a.w_stages & 1u)) record_error_at(a.err, kErrTimeout);
   }
