@@ -32,12 +32,6 @@ __device__ __forceinline__ uint32_t cluster_ld_u32(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ float4 cluster_ld_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-
 __device__ __forceinline__ void cluster_st_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }

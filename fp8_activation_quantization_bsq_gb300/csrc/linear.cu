@@ -77,19 +77,20 @@ bsq_status launch_many(const PlArgs& p, const HostDevice& d, cudaStream_t st) {
   a.token_tiles = static_cast<int>(ceil_div(p.tokens, kMost));
   a.tokens_tile = static_cast<int>(ceil_div(ceil_div(p.tokens, a.token_tiles), 16) * 16);
   a.row_tiles = static_cast<int>(ceil_div(p.rows, 128 * MT));
-  a.stages = static_cast<int>(ceil_div(p.cols, F::kCols));
+  const int64_t units = ceil_div(p.cols, 128);
   const int64_t tiles = static_cast<int64_t>(a.row_tiles) * a.token_tiles;
   if (tiles >= (int64_t(1) << 31)) return BSQ_ERR_SHAPE;
-  // blocks of a cluster, which share K: the number that ends first, where a block costs its stages and about four more, and
+  // blocks of a cluster, which share K: the number that ends first, where a block costs its 128 columns' worth and about eight more, and
   // clusters are held by as many SMs as have room for whole ones
   static constexpr int kResident[9] = {0, 152, 152, 138, 144, 140, 138, 105, 120};  // blocks of clusters of 1 to 8, of 152 SMs
   int ranks = 1;
   int64_t best = INT64_MAX;
-  for (int r = 1; r <= 8 && tiles < d.sm_count; ++r) {
-    const int64_t share = ceil_div(a.stages, r), cost = ceil_div(tiles * r, kResident[r]) * (share + 4);
-    if (ceil_div(a.stages, share) == r && cost < best) {
+  for (int r = 1; r <= 8 && (r == 1 || tiles < d.sm_count); ++r) {
+    const int64_t share = ceil_div(units, r), cost = ceil_div(tiles * r, kResident[r]) * (share + 8);
+    if (ceil_div(units, share) == r && cost < best) {
       best = cost;
       ranks = r;
+      a.share = static_cast<int>(share);
     }
   }
   a.x_bytes = a.tokens_tile * 128;
@@ -100,7 +101,7 @@ bsq_status launch_many(const PlArgs& p, const HostDevice& d, cudaStream_t st) {
   a.w_stages = std::min(6, (room - a.depth * a.x_bytes) / a.w_bytes);
   // more than half of the SM's memory, and the sums of a cluster's block
   const int smem = std::max({1024 + a.w_stages * a.w_bytes + a.depth * a.x_bytes, 120 * 1024,
-                             ranks > 1 ? 1024 + a.tokens_tile * 128 * MT * 4 : 0});
+                             ranks > 1 ? 1024 + (a.tokens_tile + ranks) * 128 * MT * 4 : 0});
   CUtensorMap mw, mx;
   if (!linear_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, p.row_bytes, p.rows, p.row_bytes, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !linear_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT16, p.x, p.cols, p.tokens, p.ld_x * 2, 64, a.tokens_tile, CU_TENSOR_MAP_SWIZZLE_128B))

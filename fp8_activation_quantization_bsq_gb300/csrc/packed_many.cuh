@@ -32,7 +32,7 @@ struct PmArgs {
   PlArgs p;
   int tokens_tile;        // of a block, a multiple of 16
   int row_tiles, token_tiles;
-  int stages;             // of weights in a row, in all
+  int share;              // of a block's part of K, in 128 columns
   int depth, w_stages, x_bytes, w_bytes;  // steps (tokens in shared, weights in tensor memory) and stages of weights in flight
   unsigned int* err;
 };
@@ -156,6 +156,57 @@ __device__ __forceinline__ void pm_store(const float (&y)[32], float f, int n, T
   }
 }
 
+// Four neighbouring values of the output's type, as far as `left` of them are there, at once where they are aligned.
+template <bool F16>
+__device__ __forceinline__ void pm_load4(const void* base, int f32, int64_t at, int64_t left, float4& v) {
+  float* x = &v.x;
+  if (f32) {
+    const float* p = static_cast<const float*>(base) + at;
+    if (left >= 4 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+      v = *reinterpret_cast<const float4*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) x[i] = p[i];
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    if (left >= 4 && (reinterpret_cast<uintptr_t>(p) & 7u) == 0) {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      const float2 lo = elem2_to_f32x2<F16>(w.x), hi = elem2_to_f32x2<F16>(w.y);
+      v = make_float4(lo.x, lo.y, hi.x, hi.y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) x[i] = elem2_to_f32x2<F16>(p[i]).x;
+    }
+  }
+}
+template <bool F16>
+__device__ __forceinline__ void pm_store4(void* base, int f32, int64_t at, int64_t left, float4 v) {
+  const float* x = &v.x;
+  if (f32) {
+    float* p = static_cast<float*>(base) + at;
+    if (left >= 4 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+      *reinterpret_cast<float4*>(p) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) p[i] = x[i];
+    }
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(base) + at;
+    const uint2 w = make_uint2(f32x2_to_elem2<F16>(v.x, v.y), f32x2_to_elem2<F16>(v.z, v.w));
+    if (left >= 4 && (reinterpret_cast<uintptr_t>(p) & 7u) == 0) {
+      *reinterpret_cast<uint2*>(p) = w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) p[i] = static_cast<uint16_t>((i < 2 ? w.x : w.y) >> (16 * (i & 1)));
+    }
+  }
+}
+
 // MT: tiles of 128 rows that a block takes.
 template <int FMT, bool F16, int MT>
 __global__ void __launch_bounds__(kPmThreads, 1)
@@ -176,9 +227,8 @@ __global__ void __launch_bounds__(kPmThreads, 1)
   const int ranks = gridDim.y;  // of the cluster
   uint8_t* const xs = smem;
   uint8_t* const ws = smem + depth * a.x_bytes;
-  const int share = (a.stages + ranks - 1) / ranks;
-  const int k_lo = blockIdx.y * share, k_hi = min(k_lo + share, a.stages);  // of the block's share of K
-  const int col0 = k_lo * F::kCols, steps = (min(k_hi * F::kCols, a.p.cols) - col0 + 63) / 64;
+  const int col0 = blockIdx.y * a.share * 128, cols = min(a.share * 128, a.p.cols - col0);  // of the block's part of K
+  const int steps = (cols + 63) / 64, stages = (cols + F::kCols - 1) / F::kCols;
   const int n_tok = a.tokens_tile;
   if (tid == 0) {
     for (uint32_t i = 0; i < depth; ++i) {
@@ -206,6 +256,7 @@ __global__ void __launch_bounds__(kPmThreads, 1)
   t5_fence_after();
   const uint32_t tmem = warp_uniform(static_cast<int>(tmem_slot));
   const int tiles = a.row_tiles * a.token_tiles;
+  float row_factor = 1.f;  // a converter's row, in the end
   const auto fail = [&]() {
     if (abort_flag == 0u) record_error_at(a.err, kErrTimeout);
     abort_flag = 1u;
@@ -219,17 +270,17 @@ __global__ void __launch_bounds__(kPmThreads, 1)
       for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
         const int band0 = tile / a.token_tiles * MT;
         const int bands = min(MT, static_cast<int>((a.p.rows - static_cast<int64_t>(band0) * 128 + 127) / 128));
-        for (int k = k_lo; k < k_hi; ++k) {
+        for (int k = 0; k < stages; ++k) {
           const uint32_t s = n % a.w_stages;
           ok = mbar_wait_clocked(&w_empty[s], (n / a.w_stages & 1u) ^ 1u, &abort_flag);
           if (!ok) break;
           uint8_t* w = ws + s * a.w_bytes;
-          const int atoms = min(F::kAtoms, a.p.k_atoms - k * F::kAtoms);
+          const int atom0 = col0 / Fmt<FMT>::ATOM_COLS + k * F::kAtoms, atoms = min(F::kAtoms, a.p.k_atoms - atom0);
           mbar_arrive_expect_tx(&w_full[s], bands * (F::kTileBytes + atoms * 512));
           for (int m = 0; m < bands; ++m) {
-            tma_load_2d(w + m * F::kTileBytes, &map_w, k * 128, (band0 + m) * 128, &w_full[s]);
+            tma_load_2d(w + m * F::kTileBytes, &map_w, col0 / (F::kCols / 128) + k * 128, (band0 + m) * 128, &w_full[s]);
             bulk_load(w + MT * F::kTileBytes + m * F::kAtoms * 512,
-                      a.p.scales + (static_cast<int64_t>(band0 + m) * a.p.k_atoms + k * F::kAtoms) * 512, atoms * 512, &w_full[s]);
+                      a.p.scales + (static_cast<int64_t>(band0 + m) * a.p.k_atoms + atom0) * 512, atoms * 512, &w_full[s]);
           }
           w_fills = ++n;
         }
@@ -307,7 +358,7 @@ __global__ void __launch_bounds__(kPmThreads, 1)
           }
         }
       }
-      for (int k = 0; k < k_hi - k_lo && ok; ++k, ++wn) {
+      for (int k = 0; k < stages && ok; ++k, ++wn) {
         const uint32_t s = wn % a.w_stages;
         // every group waits for and gives back every stage, converted by it or not: a barrier's parity tells only neighbouring
         // phases apart, so none may pass unseen
@@ -358,17 +409,13 @@ __global__ void __launch_bounds__(kPmThreads, 1)
       t5_fence_after();
       const int tok0 = tt * n_tok, toks = min(n_tok, a.p.tokens - tok0);
       const float f = F16 && FMT != kNVFP4 ? pow2f(max(top, 1) - 127 - (FMT == kMXFP8 ? 7 : 13)) : inv;
-      if (!idle) {
+      row_factor = f;
+      if (!idle && ranks == 1) {
         for (int c0 = 32 * turn; c0 < toks; c0 += 32 * kTurns) {
           float y[32];
           t5_ld32(lanes + d_col * m + c0, y);
           const int n_out = min(32, toks - c0);
-          if (ranks > 1) {
-            float* red = reinterpret_cast<float*>(smem) + c0 * (128 * MT) + 128 * m + r;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < n_out) red[i * (128 * MT)] = y[i] * f;
-          } else if (row < a.p.rows) {
+          if (row < a.p.rows) {
             const int64_t at = (tok0 + c0) * a.p.ld_out + row, add_at = (tok0 + c0) * a.p.ld_add + row;
             if (a.p.out_f32)
               pm_store<F16>(y, f, n_out, static_cast<float*>(a.p.out) + at, a.p.ld_out, a.p.add ? static_cast<const float*>(a.p.add) + add_at : nullptr, a.p.ld_add);
@@ -401,41 +448,62 @@ __global__ void __launch_bounds__(kPmThreads, 1)
   t5_fence_before();
   __syncthreads();
   t5_fence_after();
+  if (ranks > 1) {
+    // One tile per cluster.  Block q gets tokens q n .. of all blocks' sums, written from tensor memory straight into its shared
+    // memory, [block][token][row], once every block is done with its rings; then it adds them in the blocks' order.
+    const int rt = blockIdx.x / a.token_tiles, tt = blockIdx.x % a.token_tiles, me = blockIdx.y;
+    const int toks = min(n_tok, a.p.tokens - tt * n_tok), per = (toks + ranks - 1) / ranks, mine = max(0, min(per, toks - me * per));
+    constexpr int kRows = 128 * MT, kQuads = kRows / 4, kTurns = kPmConverters / 4 / MT;
+    cluster_sync_all();
+    const int m = (warp - 4) / 4 / kTurns, turn = (warp - 4) / 4 % kTurns, quarter = warp & 3;
+    if (warp >= 4 && abort_flag == 0u && (static_cast<int64_t>(rt) * MT + m) * 128 < a.p.rows) {
+      for (int c0 = 32 * turn; c0 < toks; c0 += 32 * kTurns) {
+        float y[32];
+        t5_ld32(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + d_col * m + c0, y);
+        int owner = c0 / per, t = c0 - owner * per;
+        const float* to = reinterpret_cast<const float*>(smem) + me * per * kRows + 128 * m + 32 * quarter + lane;
+        uint32_t base = cluster_map(to, owner);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (c0 + i >= toks) break;
+          cluster_st_u32(base + t * (kRows * 4), __float_as_uint(y[i] * row_factor));
+          if (++t == per && c0 + i + 1 < toks) {
+            t = 0;
+            base = cluster_map(to, ++owner);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // the residuals of the first two items are on their way meanwhile: four rows of a token each
+    const int items = kQuads * mine;
+    const int64_t tok0 = static_cast<int64_t>(tt) * n_tok + me * per, row0 = static_cast<int64_t>(rt) * kRows;
+    const auto residual = [&](int e) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.p.add && e < items) pm_load4<F16>(a.p.add, a.p.out_f32, (tok0 + e / kQuads) * a.p.ld_add + row0 + e % kQuads * 4, a.p.rows - row0 - e % kQuads * 4, x);
+      return x;
+    };
+    float4 next[2] = {residual(tid), residual(tid + kPmThreads)};
+    cluster_sync_all();
+    const float4* sums = reinterpret_cast<const float4*>(smem);
+    for (int e = tid; e < items; e += kPmThreads) {
+      float4 v = sums[e];
+      for (int q = 1; q < ranks; ++q) {
+        const float4 x = sums[q * per * kQuads + e];
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+      }
+      if (a.p.add) v.x += next[0].x, v.y += next[0].y, v.z += next[0].z, v.w += next[0].w;
+      pm_store4<F16>(a.p.out, a.p.out_f32, (tok0 + e / kQuads) * a.p.ld_out + row0 + e % kQuads * 4, a.p.rows - row0 - e % kQuads * 4, v);
+      next[0] = next[1];
+      next[1] = residual(e + 2 * kPmThreads);
+    }
+    t5_fence_before();
+    __syncthreads();
+    t5_fence_after();
+  }
   if (warp == 1) {
     __syncwarp();
     t5_dealloc(tmem, 512);
-  }
-  if (ranks > 1) {  // one tile per cluster: every block's sums are in its shared memory
-    cluster_sync_all();
-    const int rt = blockIdx.x / a.token_tiles, tt = blockIdx.x % a.token_tiles;
-    const int tok0 = tt * n_tok, toks = min(n_tok, a.p.tokens - tok0);
-    // tokens me, me + ranks, ...: four rows a thread, their parts from all blocks at once
-    const float* red = reinterpret_cast<const float*>(smem);
-    constexpr int kQuads = 32 * MT;
-    const int me = blockIdx.y, n_out = toks > me ? (toks - me + ranks - 1) / ranks : 0;
-    for (int e = tid; e < kQuads * n_out; e += kPmThreads) {
-      const int t = me + e / kQuads * ranks, r = e % kQuads * 4;
-      const int64_t row = static_cast<int64_t>(rt) * MT * 128 + r, tok = tok0 + t;
-      float4 v[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q < ranks) v[q] = cluster_ld_f4(cluster_map(red + t * 128 * MT + r, q));
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q < ranks) s[0] += v[q].x, s[1] += v[q].y, s[2] += v[q].z, s[3] += v[q].w;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (row + i >= a.p.rows) break;
-        const int64_t at = tok * a.p.ld_out + row + i, add_at = tok * a.p.ld_add + row + i;
-        if (a.p.out_f32)
-          static_cast<float*>(a.p.out)[at] = a.p.add ? s[i] + static_cast<const float*>(a.p.add)[add_at] : s[i];
-        else
-          static_cast<uint16_t*>(a.p.out)[at] = static_cast<uint16_t>(f32x2_to_elem2<F16>(
-              a.p.add ? s[i] + elem2_to_f32x2<F16>(static_cast<const uint16_t*>(a.p.add)[add_at]).x : s[i], 0.f));
-      }
-    }
-    cluster_sync_all();  // no block leaves while another reads its sums
   }
 }
 
