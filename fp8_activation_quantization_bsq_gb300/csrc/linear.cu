@@ -129,7 +129,6 @@ bsq_status launch_linear_tokens(PlArgs& a, const HostDevice& d, cudaStream_t st)
   if (a.tokens <= 2) return launch_linear<FMT, F16, 1, 1>(a, d, st);
   if (a.tokens <= 8) return launch_linear<FMT, F16, 1, 2>(a, d, st);
   if (a.tokens <= 16) return launch_linear<FMT, F16, 2, 4>(a, d, st);
-  if (a.tokens <= 32) return launch_linear<FMT, F16, 4, 4>(a, d, st);
   if (a.tokens <= 128) return launch_many<FMT, F16, 2>(a, d, st);
   return launch_many<FMT, F16, 1>(a, d, st);
 }
