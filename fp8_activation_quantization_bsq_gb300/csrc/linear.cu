@@ -74,9 +74,19 @@ bsq_status launch_many(const PlArgs& p, const HostDevice& d, cudaStream_t st) {
   a.p = p;
   a.err = d.error_word;
   constexpr int kMost = 256 / MT;
-  a.token_tiles = static_cast<int>(ceil_div(p.tokens, kMost));
-  a.tokens_tile = static_cast<int>(ceil_div(ceil_div(p.tokens, a.token_tiles), 16) * 16);
   a.row_tiles = static_cast<int>(ceil_div(p.rows, 128 * MT));
+  // tokens of a tile: those with which the last wave of tiles ends first, a tile costing its tokens and about 128 more
+  a.token_tiles = static_cast<int>(ceil_div(p.tokens, kMost));
+  int64_t least = INT64_MAX;
+  for (int64_t t = a.token_tiles, n = 0; t <= 2 * ceil_div(p.tokens, kMost); ++t) {
+    n = ceil_div(ceil_div(p.tokens, t), 16) * 16;
+    const int64_t tiles = a.row_tiles * ceil_div(p.tokens, n), cost = ceil_div(tiles, d.sm_count) * (n + 128);
+    if (tiles >= d.sm_count ? cost < least : least == INT64_MAX) {
+      least = cost;
+      a.tokens_tile = static_cast<int>(n);
+      a.token_tiles = static_cast<int>(ceil_div(p.tokens, n));
+    }
+  }
   const int64_t units = ceil_div(p.cols, 128);
   const int64_t tiles = static_cast<int64_t>(a.row_tiles) * a.token_tiles;
   if (tiles >= (int64_t(1) << 31)) return BSQ_ERR_SHAPE;
@@ -85,7 +95,7 @@ bsq_status launch_many(const PlArgs& p, const HostDevice& d, cudaStream_t st) {
   static constexpr int kResident[9] = {0, 152, 152, 138, 144, 140, 138, 105, 120};  // blocks of clusters of 1 to 8, of 152 SMs
   int ranks = 1;
   int64_t best = INT64_MAX;
-  for (int r = 1; r <= 8 && (r == 1 || tiles < d.sm_count); ++r) {
+  for (int r = 1; r <= 8 && (r == 1 || tiles < 2 * d.sm_count); ++r) {
     const int64_t share = ceil_div(units, r), cost = ceil_div(tiles * r, kResident[r]) * (share + 8);
     if (ceil_div(units, share) == r && cost < best) {
       best = cost;
