@@ -9,32 +9,50 @@ namespace {
 
 using namespace bsq;
 
-template <int FMT, bool F16, int NT, int RT>
-bsq_status launch_linear(PlArgs& a, const HostDevice& d, cudaStream_t st) {
-  auto kernel = packed_linear_kernel<FMT, F16, NT, RT>;
-  constexpr int kCols = PlFmt<FMT>::kCols, kSplit = kPlWarps / RT;
-  const int tile_tokens = std::min(a.tokens, NT * 8);
-  constexpr int kStep = kSplit * kCols % 256 == 0 ? kSplit : 2 * kSplit;  // a segment is a multiple of 256 columns
-  static_assert(kStep * kCols % 256 == 0);
-  // blocks per SM, and what tokens each may hold beside its rings
-  const int per_sm = tile_tokens == 1 ? 3 : 2, room = (227 / per_sm - 2) * 1024 - kPlRing;
-  const int most = std::max(kStep, static_cast<int>((room / tile_tokens - 64) / (kStep * kCols * 2) * kStep));
-  // blocks of a cluster, which share K: the number that leaves the fullest SM the least to do, a block costing its pieces and about
-  // eight more for each segment of its tokens
-  const int64_t row_tiles = ceil_div(a.rows, 128) * 4 / RT, tiles = row_tiles * ceil_div(a.tokens, NT * 8);
-  a.per_rank = static_cast<int>(ceil_div(a.pieces, kSplit) * kSplit);
-  int64_t best = INT64_MAX;
-  for (int r = 1; r <= 8; ++r) {
-    const int64_t share = ceil_div(ceil_div(a.pieces, r), kSplit) * kSplit, blocks = ceil_div(a.pieces, share) * tiles;
-    const int64_t cost = ceil_div(blocks, d.sm_count) * (share + 8 * ceil_div(share, most));
-    if (cost < best) {
-      best = cost;
-      a.per_rank = static_cast<int>(share);
+// How the kernel for few tokens is laid out: sets of 32 rows per block (1 or 4), pieces of K per block and of its tokens at a time.
+//
+// Measured for 1, 4, 8 and 16 tokens with 1, 2 and 4 sets and 1 to 8 blocks along K (10240 x 7168 and 4096 x 4096 NVFP4, 256 x 7168 MXFP8,
+// 1000 x 2912 MXFP4): a call takes about 5 us and 0.043 us for each unit that the fullest SM has, where a unit is a piece of 32 rows; a piece's
+// tokens count 0.23 each, a further segment of tokens 60, a block for which the SM has no room at first 85, a sum over a cluster 12.  One token,
+// 10240 rows: 4 sets and 5 blocks along K 11.8 us, 1 set and one block 12.6, 1 set and two 14.  8 tokens: 4 sets and 3 blocks 15.2, 7 blocks 18.2,
+// 1 set 35.  16 tokens, 256 rows: 1 set and 8 blocks 6.2, 4 sets 8.4.  One token, 4096 x 4096: 1 set and one block 4.3, 4 sets and 4 blocks 5.1.
+struct PlPlan {
+  int sets, per_rank, segment, ranks, smem;
+};
+PlPlan plan_linear(const PlArgs& a, int cols_of_piece, int token_tile, int sm_count) {
+  const int toks = std::min(a.tokens, token_tile);
+  constexpr int kBlockMost = 227 * 1024, kOverhead = 2 * 1024;  // static shared memory and what the system takes, per block
+  PlPlan best{};
+  double least = 0;
+  for (int sets = 1; sets <= 4; sets += 3) {
+    const int split = kPlWarps / sets, step = split * cols_of_piece % 256 == 0 ? split : 2 * split;  // a segment: a multiple of 256 columns
+    const int room = 113 * 1024 - kOverhead - kPlRing;  // for tokens, with two blocks per SM
+    const int most = std::max(step, (room / toks - 64) / (step * cols_of_piece * 2) * step);
+    const int64_t tiles = ceil_div(a.rows, 128) * 4 / sets * ceil_div(a.tokens, token_tile);
+    for (int r = 1; r <= 8; ++r) {
+      const int share = static_cast<int>(ceil_div(ceil_div(a.pieces, r), split) * split), ranks = static_cast<int>(ceil_div(a.pieces, share));
+      const int segment = std::min(most, static_cast<int>(ceil_div(share, step) * step));
+      const int smem = std::max(kPlRing + toks * (segment * cols_of_piece * 2 + 64), kPlWarps * token_tile * 32 * 4);
+      const int resident = std::min(token_tile == 8 ? 3 : 2, kBlockMost / (smem + kOverhead));
+      const double n = static_cast<double>(ceil_div(tiles * ranks, sm_count));
+      const double cost = n * (sets * share + 0.23 * share * toks * cols_of_piece / 128 + 60.0 * (ceil_div(share, segment) - 1)) +
+                          85.0 * std::max(0.0, n - resident) + (ranks > 1 ? 12.0 : 0.0);
+      if (best.sets == 0 || cost < least) {
+        least = cost;
+        best = {sets, share, segment, ranks, smem};
+      }
     }
   }
-  const int ranks = static_cast<int>(ceil_div(a.pieces, a.per_rank));
-  a.segment = std::min(most, static_cast<int>(ceil_div(a.per_rank, kStep) * kStep));
-  const int smem = std::max(kPlRing + tile_tokens * (a.segment * kCols * 2 + 64), kPlWarps * NT * 8 * 32 * 4);
+  return best;
+}
+
+template <int FMT, bool F16, int NT, int RT>
+bsq_status launch_linear(PlArgs& a, const PlPlan& plan, const HostDevice& d, cudaStream_t st) {
+  auto kernel = packed_linear_kernel<FMT, F16, NT, RT>;
+  a.per_rank = plan.per_rank;
+  a.segment = plan.segment;
+  const int64_t row_tiles = ceil_div(a.rows, 128) * 4 / RT;
+  const int ranks = plan.ranks, smem = plan.smem;
   if (bsq_status s = allow_smem(reinterpret_cast<const void*>(kernel), 227 * 1024 - 2048, d.index); s != BSQ_OK) return s;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks, static_cast<unsigned>(row_tiles), static_cast<unsigned>(ceil_div(a.tokens, NT * 8)));
@@ -136,9 +154,14 @@ bsq_status launch_many(const PlArgs& p, const HostDevice& d, cudaStream_t st) {
 
 template <int FMT, bool F16>
 bsq_status launch_linear_tokens(PlArgs& a, const HostDevice& d, cudaStream_t st) {
-  if (a.tokens <= 2) return launch_linear<FMT, F16, 1, 1>(a, d, st);
-  if (a.tokens <= 8) return launch_linear<FMT, F16, 1, 2>(a, d, st);
-  if (a.tokens <= 16) return launch_linear<FMT, F16, 2, 4>(a, d, st);
+  if (a.tokens <= 8) {
+    const PlPlan p = plan_linear(a, PlFmt<FMT>::kCols, 8, d.sm_count);
+    return p.sets == 1 ? launch_linear<FMT, F16, 1, 1>(a, p, d, st) : launch_linear<FMT, F16, 1, 4>(a, p, d, st);
+  }
+  if (a.tokens <= 16) {
+    const PlPlan p = plan_linear(a, PlFmt<FMT>::kCols, 16, d.sm_count);
+    return p.sets == 1 ? launch_linear<FMT, F16, 2, 1>(a, p, d, st) : launch_linear<FMT, F16, 2, 4>(a, p, d, st);
+  }
   if (a.tokens <= 128) return launch_many<FMT, F16, 2>(a, d, st);
   return launch_many<FMT, F16, 1>(a, d, st);
 }
