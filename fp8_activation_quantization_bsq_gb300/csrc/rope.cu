@@ -48,6 +48,16 @@ extern "C" int32_t bsq_qk_norm_rope(int32_t dtype, const void* q, int64_t q_tok,
       (q_tok | q_head | k_tok | k_head | qo_tok | qo_head | ko_tok | ko_head) % 8 != 0 ||
       !aligned(q_weight, weight_dtype == BSQ_F32 ? 4 : 2) || !aligned(k_weight, weight_dtype == BSQ_F32 ? 4 : 2))
     return BSQ_ERR_ALIGN;
+  // outputs whose rows lie in one another, and inputs overwritten in another order than they are read in
+  if ((heads > 1 && qo_head < dim) || (kv_heads > 1 && ko_head < dim) || (tokens > 1 && ((heads && qo_tok < dim) || (kv_heads && ko_tok < dim))))
+    return BSQ_ERR_SHAPE;
+  const auto moved = [&](int64_t tok, int64_t head, int64_t to_tok, int64_t to_head, int n) {
+    return (tokens > 1 && tok != to_tok) || (n > 1 && head != to_head);
+  };
+  if ((heads && q_out == q && moved(q_tok, q_head, qo_tok, qo_head, heads)) ||
+      (kv_heads && k_out == k && moved(k_tok, k_head, ko_tok, ko_head, kv_heads)) ||
+      (heads && kv_heads && (q_out == k || k_out == q || q_out == k_out)))
+    return BSQ_ERR_VALUE;
   HostDevice d;
   if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
   RopeArgs a{};

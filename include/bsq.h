@@ -589,12 +589,16 @@ BSQ_API int32_t bsq_moe_layer_routed(int32_t fmt, const void* x_dev, int64_t ld_
  *                     them (no NaN codes).
  *   w_sf_dev          NVFP4: one float (> 0), the weights' tensor scale; ignored for MX.
  *   add_dev           NULL, or values of the output's type: (tokens, rows) with row stride ld_add (>= rows), or, with
- *                     ld_add == 0, one row for every token.  May be out_dev itself.
+ *                     ld_add == 0, one row for every token.  May be out_dev itself (with its row stride).
  *   out_dtype         dtype, or BSQ_F32.
- *   out_dev           (tokens, rows), row stride ld_out (>= rows).
+ *   out_dev           (tokens, rows), row stride ld_out (>= rows); shares no bytes with x or, otherwise, add: BSQ_ERR_VALUE (so do
+ *                     interleaved rows with different strides).
  *   tokens, rows      0 to 2^20 (0 = no-op).
- * Sums are FP32 (of a token's values relative to its largest, for MX weights), rounded once to the output's type.  BF16 values of x are held in FP16 times a power of two of their
- * token: exact but for values below 2^-31 of the token's largest, which are off by at most 2^-39 of that.
+ * Sums are FP32 (of a token's values relative to its largest, for MX weights), rounded once to the output's type.  Products are of exact
+ * values, with three exceptions.  BF16 x, at most 16 tokens: values of x below 2^-31 of their token's largest are off by at most 2^-39 of that
+ * (x is held in FP16 times a power of two of its token).  BF16 x, more tokens: values of MX weights below 2^-126 are off by at most 2^-134
+ * (w is held in BF16).  FP16 x, MX weights, more than 16 tokens: values of w below 2^-36 (E2M1) or 2^-21 (E4M3) of their row's largest
+ * scale are off by at most 2^-35 or 2^-23 of it (w is held in FP16 relative to that).
  */
 BSQ_API int32_t bsq_packed_linear(int32_t fmt, int32_t dtype, const void* x_dev, int64_t tokens, int64_t cols, int64_t ld_x,
                                   const void* w_dev, const void* w_scales5d_dev, int64_t rows, const float* w_sf_dev,
@@ -614,7 +618,9 @@ BSQ_API int32_t bsq_packed_linear(int32_t fmt, int32_t dtype, const void* x_dev,
  *   inv_freq_dev      float[pairs].
  *   q_weight_dev, k_weight_dev   NULL (no norm), or dim values of weight_dtype: dtype or BSQ_F32.
  *   eps               >= 0.
- *   q_out_dev, k_out_dev   outputs, strided like the inputs; each may be its input itself, and must not overlap it otherwise.
+ *   q_out_dev, k_out_dev   outputs, strided like the inputs, but with strides of at least dim; each may be its input itself, with
+ *                     its strides.  No output overlaps anything else (one that is another input, the other output or its input with other
+ *                     strides is refused with BSQ_ERR_VALUE).
  * Angles are exact up to their rounding to FP32 as a fraction of a turn, at any position; arithmetic is FP32, rounded once.
  */
 BSQ_API int32_t bsq_qk_norm_rope(int32_t dtype, const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, const void* k_dev,

@@ -105,3 +105,28 @@ ROUTED = dict(fmt=2, x=P, ld_x=64, ids=P, weights=P, w13=P, w13_s=P, w2=P, w2_s=
     (dict(ws_bytes=100), SHAPE), (dict(tokens=0), OK)])
 def test_routed_moe_refusals(bsq, change, code):
     assert bsq.lib().bsq_moe_layer_routed(*{**ROUTED, **change}.values()) == code
+
+
+BIG = 0x100000
+
+
+@pytest.mark.parametrize("change,refused", [
+    (dict(out=P), True), (dict(out=P + 64), True), (dict(out=P, tokens=1), True), (dict(out=P + 128, ld_out=128, ld_x=256), True),
+    (dict(out=P + 128, ld_out=256, ld_x=256), False), (dict(out=P + 126, ld_out=256, ld_x=256), True),
+    (dict(out=P + 312, ld_out=256, ld_x=256), False), (dict(out=P + 314, ld_out=256, ld_x=256), True), (dict(out=P - 200, ld_out=256, ld_x=256), False),
+    (dict(out=P - 198, ld_out=256, ld_x=256), True), (dict(out=P + 192, tokens=2), True), (dict(out=P + 256, tokens=2), False),
+    (dict(out=BIG, add=BIG, ld_add=100), False), (dict(out=BIG, add=BIG, ld_add=0), True), (dict(out=BIG, add=BIG, ld_add=108), True),
+    (dict(out=BIG, add=BIG + 2, ld_add=100), True), (dict(out=BIG, add=BIG + 200, ld_add=100), True), (dict(out=BIG, add=BIG + 400, ld_add=0), False),
+    (dict(out=BIG, add=BIG, ld_add=0, tokens=1), False)])
+def test_linear_refuses_overlaps(bsq, change, refused):
+    if not refused and torch.cuda.is_available():
+        pytest.skip("would run")  # without a device such a call ends where that is looked for
+    got = bsq.lib().bsq_packed_linear(*{**LINEAR, **change}.values())
+    assert got == VALUE if refused else got not in (OK, NULL, SHAPE, ALIGN, VALUE)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(qo=P, ko=3 * BIG, qo_tok=520), VALUE), (dict(qo=P, ko=3 * BIG, qo_head=72), VALUE), (dict(ko=BIG, ko_tok=136), VALUE), (dict(qo=BIG), VALUE),
+    (dict(ko=P), VALUE), (dict(qo=2 * BIG, ko=2 * BIG), VALUE), (dict(qo_head=56), SHAPE), (dict(ko_tok=0), SHAPE), (dict(qo_tok=0), SHAPE)])
+def test_rope_refuses_overlaps(bsq, change, code):
+    assert bsq.lib().bsq_qk_norm_rope(*{**ROPE, "k": BIG, "qo": 2 * BIG, "ko": 3 * BIG, **change}.values()) == code
