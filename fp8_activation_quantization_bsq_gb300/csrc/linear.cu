@@ -84,43 +84,63 @@ bool linear_map(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, int
 
 constexpr int kPmSmem = 227 * 1024 - 2048;  // dynamic shared memory at most: one block per SM
 
-template <int FMT, bool F16, int MT>
-bsq_status launch_many(const PlArgs& p, const HostDevice& d, cudaStream_t st) {
-  using F = PmFmt<FMT>;
-  auto kernel = packed_many_kernel<FMT, F16, MT>;
-  PmArgs a{};
-  a.p = p;
-  a.err = d.error_word;
-  constexpr int kMost = 256 / MT;
-  a.row_tiles = static_cast<int>(ceil_div(p.rows, 128 * MT));
-  // tokens of a tile: those with which the last wave of tiles ends first, a tile costing its tokens and about 128 more
-  a.token_tiles = static_cast<int>(ceil_div(p.tokens, kMost));
+// How the work of the kernel for many tokens is split: tokens of a tile, tiles, blocks along K and their share of it.
+struct PmPlan {
+  int tokens_tile, token_tiles, row_tiles, ranks, share;
+  int64_t tiles;
+  double cost;
+};
+PmPlan plan_many(const PlArgs& p, int mt, int sm_count) {
+  PmPlan a{};
+  const int most = 256 / mt;
+  a.row_tiles = static_cast<int>(ceil_div(p.rows, 128 * mt));
+  // tokens of a tile: those with which the last wave of tiles ends first, a tile costing its tokens and about 128 more (2048 tokens, 10240 rows
+  // 168 us, with tiles of 256 177; 300 tokens 56 and 64)
+  a.token_tiles = static_cast<int>(ceil_div(p.tokens, most));
   int64_t least = INT64_MAX;
-  for (int64_t t = a.token_tiles, n = 0; t <= 2 * ceil_div(p.tokens, kMost); ++t) {
+  for (int64_t t = a.token_tiles, n = 0; t <= 2 * ceil_div(p.tokens, most); ++t) {
     n = ceil_div(ceil_div(p.tokens, t), 16) * 16;
-    const int64_t tiles = a.row_tiles * ceil_div(p.tokens, n), cost = ceil_div(tiles, d.sm_count) * (n + 128);
-    if (tiles >= d.sm_count ? cost < least : least == INT64_MAX) {
+    const int64_t tiles = a.row_tiles * ceil_div(p.tokens, n), cost = ceil_div(tiles, sm_count) * (n + 128);
+    if (tiles >= sm_count ? cost < least : least == INT64_MAX) {
       least = cost;
       a.tokens_tile = static_cast<int>(n);
       a.token_tiles = static_cast<int>(ceil_div(p.tokens, n));
     }
   }
   const int64_t units = ceil_div(p.cols, 128);
-  const int64_t tiles = static_cast<int64_t>(a.row_tiles) * a.token_tiles;
-  if (tiles >= (int64_t(1) << 31)) return BSQ_ERR_SHAPE;
+  a.tiles = static_cast<int64_t>(a.row_tiles) * a.token_tiles;
   // blocks of a cluster, which share K: the number that ends first, where a block costs its 128 columns' worth and about eight more, and
-  // clusters are held by as many SMs as have room for whole ones
+  // clusters are held by as many SMs as have room for whole ones.  64 tokens, 7168 x 8192, two tiles: 1 to 8 blocks 56, 34, 26, 22, 20,
+  // 34, 33, 31 us (5 are taken); 300 tokens 39, 49, 58, 64, 63, 71, 102, 97 (1)
   static constexpr int kResident[9] = {0, 152, 152, 138, 144, 140, 138, 105, 120};  // blocks of clusters of 1 to 8, of 152 SMs
-  int ranks = 1;
   int64_t best = INT64_MAX;
-  for (int r = 1; r <= 8 && (r == 1 || tiles < 2 * d.sm_count); ++r) {
-    const int64_t share = ceil_div(units, r), cost = ceil_div(tiles * r, kResident[r]) * (share + 8);
-    if (ceil_div(units, share) == r && cost < best) {
-      best = cost;
-      ranks = r;
+  for (int r = 1; r <= 8 && (r == 1 || a.tiles < 2 * sm_count); ++r) {
+    const int64_t share = ceil_div(units, r), waves = ceil_div(a.tiles * r, kResident[r]);
+    if (ceil_div(units, share) == r && waves * (share + 8) < best) {
+      best = waves * (share + 8);
+      a.ranks = r;
       a.share = static_cast<int>(share);
+      // with up to 128 tokens, in us: as measured for 17 to 128 tokens of 7168 x 8192, 16384 x 7168 and 1024 x 8192 NVFP4
+      a.cost = waves * (mt == 2 ? 5.0 + 0.055 * p.tokens + 0.9 * share : 5.2 + 0.015 * p.tokens + 0.47 * share);
     }
   }
+  return a;
+}
+
+template <int FMT, bool F16, int MT>
+bsq_status launch_many(const PlArgs& p, const PmPlan& plan, const HostDevice& d, cudaStream_t st) {
+  using F = PmFmt<FMT>;
+  auto kernel = packed_many_kernel<FMT, F16, MT>;
+  const int64_t tiles = plan.tiles;
+  if (tiles >= (int64_t(1) << 31)) return BSQ_ERR_SHAPE;
+  PmArgs a{};
+  a.p = p;
+  a.err = d.error_word;
+  a.tokens_tile = plan.tokens_tile;
+  a.row_tiles = plan.row_tiles;
+  a.token_tiles = plan.token_tiles;
+  a.share = plan.share;
+  const int ranks = plan.ranks;
   a.x_bytes = a.tokens_tile * 128;
   a.w_bytes = static_cast<int>(ceil_div(MT * (F::kTileBytes + F::kAtoms * 512), 1024) * 1024);
   // as many steps as tensor memory holds weights of, four at least, if their tokens leave room for three stages of weights
@@ -162,8 +182,15 @@ bsq_status launch_linear_tokens(PlArgs& a, const HostDevice& d, cudaStream_t st)
     const PlPlan p = plan_linear(a, PlFmt<FMT>::kCols, 16, d.sm_count);
     return p.sets == 1 ? launch_linear<FMT, F16, 2, 1>(a, p, d, st) : launch_linear<FMT, F16, 2, 4>(a, p, d, st);
   }
-  if (a.tokens <= 128) return launch_many<FMT, F16, 2>(a, d, st);
-  return launch_many<FMT, F16, 1>(a, d, st);
+  // one or two tiles of rows per block.  Two halve the blocks, and so the sums that blocks along K exchange, and share the tokens' columns:
+  // 64 tokens, 7168 x 8192 20.0 us against 22.4, 24 tokens 17.3 and 21.0; with too few rows to fill the GPU one is better: 64 tokens,
+  // 1024 x 8192 10.2 us against 13.9.  Beyond 128 tokens one tile takes twice as many of them: 192 tokens 26.8 and 36.5.
+  const PmPlan one = plan_many(a, 1, d.sm_count);
+  if (a.tokens <= 128) {
+    const PmPlan two = plan_many(a, 2, d.sm_count);
+    if (two.cost < one.cost) return launch_many<FMT, F16, 2>(a, two, d, st);
+  }
+  return launch_many<FMT, F16, 1>(a, one, d, st);
 }
 
 // Whether n rows of a_width bytes, a_step apart, and n of b_width, b_step apart, share bytes; of interleaved ones only those with equal steps
