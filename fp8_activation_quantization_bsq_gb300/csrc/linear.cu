@@ -9,17 +9,23 @@ namespace {
 
 using namespace bsq;
 
+// Blocks that the GPU's 152 SMs hold at a time in clusters of 1 to 8, with one and with two per SM (as reported for these kernels: clusters
+// lie within a GPU processing cluster, whose SMs they may not divide).
+constexpr int kResident[9] = {0, 152, 152, 138, 144, 140, 138, 105, 120}, kResidentTwo[9] = {0, 304, 304, 291, 296, 290, 276, 266, 288};
+
 // How the kernel for few tokens is laid out: sets of 32 rows per block (1 or 4), pieces of K per block and of its tokens at a time.
 //
-// Measured for 1, 4, 8 and 16 tokens with 1, 2 and 4 sets and 1 to 8 blocks along K (10240 x 7168 and 4096 x 4096 NVFP4, 256 x 7168 MXFP8,
-// 1000 x 2912 MXFP4): a call takes about 5 us and 0.043 us for each unit that the fullest SM has, where a unit is a piece of 32 rows; a piece's
-// tokens count 0.23 each, a further segment of tokens 60, a block for which the SM has no room at first 85, a sum over a cluster 12.  One token,
-// 10240 rows: 4 sets and 5 blocks along K 11.8 us, 1 set and one block 12.6, 1 set and two 14.  8 tokens: 4 sets and 3 blocks 15.2, 7 blocks 18.2,
-// 1 set 35.  16 tokens, 256 rows: 1 set and 8 blocks 6.2, 4 sets 8.4.  One token, 4096 x 4096: 1 set and one block 4.3, 4 sets and 4 blocks 5.1.
+// The cost is fitted to 1, 2, 4, 8 and 16 tokens with 1 and 4 sets and 1 to 8 blocks along K (10240 x 7168, 7168 x 8192, 4096 x 4096
+// NVFP4, 4096 x 8192, 2048 x 16384 and 256 x 7168 MXFP8, 1000 x 2912 MXFP4): a call takes about 5 us and 0.043 us for each unit that the
+// fullest SM has, where a unit is a piece of 32 rows, its tokens count 0.23 each, a further segment of tokens 60, a block for which the SM has
+// no room at first 85, a sum over a cluster 12, and a block that is alone on its SM a tenth more.  Both sides, in us:
+//   1 token, 10240 x 7168: 4 sets and 5 blocks along K 11.8, 1 set and one block 12.6, two 14.0; 4096 x 4096: 1 set and one block 4.3, 4 and 4 5.1
+//   8 tokens, 10240 x 7168: 4 sets and 3 blocks 15.2, 7 blocks 18.2, 1 set 35; 2048 x 16384 MXFP8: 4 sets and 6 blocks 14.4, 8 14.9, 4 22.0
+//   16 tokens, 7168 x 8192: 4 sets and 5 blocks 15.7, 8 20.9, 1 set 34.9; 256 x 7168 MXFP8: 1 set and 8 blocks 6.2, 4 sets 8.4
 struct PlPlan {
   int sets, per_rank, segment, ranks, smem;
 };
-PlPlan plan_linear(const PlArgs& a, int cols_of_piece, int token_tile, int sm_count) {
+PlPlan plan_linear(const PlArgs& a, int cols_of_piece, int token_tile) {
   const int toks = std::min(a.tokens, token_tile);
   constexpr int kBlockMost = 227 * 1024, kOverhead = 2 * 1024;  // static shared memory and what the system takes, per block
   PlPlan best{};
@@ -34,7 +40,8 @@ PlPlan plan_linear(const PlArgs& a, int cols_of_piece, int token_tile, int sm_co
       const int segment = std::min(most, static_cast<int>(ceil_div(share, step) * step));
       const int smem = std::max(kPlRing + toks * (segment * cols_of_piece * 2 + 64), kPlWarps * token_tile * 32 * 4);
       const int resident = std::min(token_tile == 8 ? 3 : 2, kBlockMost / (smem + kOverhead));
-      const double n = static_cast<double>(ceil_div(tiles * ranks, sm_count));
+      const int64_t blocks = tiles * ranks;
+      const double n = blocks <= kResident[ranks] ? 1.1 : blocks <= kResidentTwo[ranks] ? 2.0 : static_cast<double>(ceil_div(2 * blocks, kResidentTwo[ranks]));
       const double cost = n * (sets * share + 0.23 * share * toks * cols_of_piece / 128 + 60.0 * (ceil_div(share, segment) - 1)) +
                           85.0 * std::max(0.0, n - resident) + (ranks > 1 ? 12.0 : 0.0);
       if (best.sets == 0 || cost < least) {
@@ -112,7 +119,6 @@ PmPlan plan_many(const PlArgs& p, int mt, int sm_count) {
   // blocks of a cluster, which share K: the number that ends first, where a block costs its 128 columns' worth and about eight more, and
   // clusters are held by as many SMs as have room for whole ones.  64 tokens, 7168 x 8192, two tiles: 1 to 8 blocks 56, 34, 26, 22, 20,
   // 34, 33, 31 us (5 are taken); 300 tokens 39, 49, 58, 64, 63, 71, 102, 97 (1)
-  static constexpr int kResident[9] = {0, 152, 152, 138, 144, 140, 138, 105, 120};  // blocks of clusters of 1 to 8, of 152 SMs
   int64_t best = INT64_MAX;
   for (int r = 1; r <= 8 && (r == 1 || a.tiles < 2 * sm_count); ++r) {
     const int64_t share = ceil_div(units, r), waves = ceil_div(a.tiles * r, kResident[r]);
@@ -175,11 +181,11 @@ bsq_status launch_many(const PlArgs& p, const PmPlan& plan, const HostDevice& d,
 template <int FMT, bool F16>
 bsq_status launch_linear_tokens(PlArgs& a, const HostDevice& d, cudaStream_t st) {
   if (a.tokens <= 8) {
-    const PlPlan p = plan_linear(a, PlFmt<FMT>::kCols, 8, d.sm_count);
+    const PlPlan p = plan_linear(a, PlFmt<FMT>::kCols, 8);
     return p.sets == 1 ? launch_linear<FMT, F16, 1, 1>(a, p, d, st) : launch_linear<FMT, F16, 1, 4>(a, p, d, st);
   }
   if (a.tokens <= 16) {
-    const PlPlan p = plan_linear(a, PlFmt<FMT>::kCols, 16, d.sm_count);
+    const PlPlan p = plan_linear(a, PlFmt<FMT>::kCols, 16);
     return p.sets == 1 ? launch_linear<FMT, F16, 2, 1>(a, p, d, st) : launch_linear<FMT, F16, 2, 4>(a, p, d, st);
   }
   // one or two tiles of rows per block.  Two halve the blocks, and so the sums that blocks along K exchange, and share the tokens' columns:
