@@ -84,7 +84,7 @@ int32_t bsq_moe_rows(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t 
   a.pairs = pairs;
   a.top_k = top_k;
   a.experts = experts;
-  // one block up to a round of 32 pairs per warp, then as many as give each warp such a round, at most a cluster
+  // one block up to a round of 32 pairs per warp, then as many as give each warp such a round, at most a cluster (figures: moe_route.cuh)
   const int64_t rounds = std::max<int64_t>(1, ceil_div(pairs, 32 * kRowsWarps));
   int blocks = 1;
   while (blocks < kRowsMaxBlocks && blocks < rounds) blocks *= 2;
