@@ -645,7 +645,7 @@ BSQ_API int32_t bsq_qk_norm_rope(int32_t dtype, const void* q_dev, int64_t q_tok
  * Where p enters a comparison it is held to about 2^-45, so the choice is that of exact arithmetic but for values
  * closer than that.  Logits (and biases) of -inf exclude an expert: p counts as 0 (with a logit of -inf), its value as -inf; experts
  * outside the groups that stay count as -inf too.  Logits or biases of NaN or +inf count as -inf and record BSQ_ERR_VALUE.
- *   ids_dev, weights_dev   int32 and float (tokens, top_k).
+ *   ids_dev, weights_dev   int32 and float (tokens, top_k), overlapping nothing else.
  */
 BSQ_API int32_t bsq_moe_route(int32_t dtype, const void* logits_dev, int64_t ld_logits, int64_t tokens, int32_t experts, int32_t top_k,
                               int32_t sigmoid, const float* bias_dev, int32_t groups, int32_t top_groups, int32_t group_top,
@@ -661,6 +661,7 @@ BSQ_API int32_t bsq_moe_route(int32_t dtype, const void* logits_dev, int64_t ld_
  *   scales_offsets_dev   uint32[experts + 1]: prefix sums of the experts' row counts, each rounded up to 128.
  *   row_indices_dev   int32[tokens * top_k]: each row's token; 0 behind the last row.
  *   positions_dev     int32 (tokens, top_k): each pair's row, -1 without one.
+ * The outputs overlap nothing else.
  */
 BSQ_API int32_t bsq_moe_rows(const int32_t* ids_dev, int64_t tokens, int32_t top_k, int32_t experts, uint32_t* row_offsets_dev,
                              uint32_t* scales_offsets_dev, int32_t* row_indices_dev, int32_t* positions_dev, void* stream);

@@ -217,3 +217,36 @@ def test_graph_streams_and_repeats(bsq, tokens):
     ys = [w.call(bsq, x, stream=s) for s in (stream, other) * 4]
     torch.cuda.synchronize()
     assert all(torch.equal(y, expect) for y in ys)
+
+
+@pytest.mark.parametrize("fmt,dtype", [("nvfp4", "bf16"), ("mxfp4", "f16"), ("mxfp8", "bf16"), ("mxfp8", "f16")])
+@pytest.mark.parametrize("tokens,rows,cols", [
+    (1, 10000, 1024),    # more blocks than SMs, none along K
+    (2, 5000, 4096),     # four sets of rows per block, eight blocks along K, more of them than fit at once
+    (5, 20000, 256),
+    (16, 100, 16384),    # tokens in more than one segment, one set of rows per block
+    (16, 1000, 16384),   # the same with four
+    (17, 9750, 1024),    # two tiles of rows per block, three blocks along K, the last tile behind the last row
+    (100, 19580, 512),   # two tiles, one block along K
+    (33, 60000, 96),     # the same, several tiles one after the other
+    (300, 20000, 96),    # one tile of rows, several one after the other
+])
+def test_splits(bsq, fmt, dtype, tokens, rows, cols):
+    """The ways in which rows, K and tokens are shared out, with a residual; the rows at both ends and some between are checked."""
+    w = Weights(bsq, fmt, 1, 32, seed=0)  # for its call
+    rng = np.random.default_rng(rows)
+    full = torch.from_numpy(rng.standard_normal((rows, cols), np.float32) / np.float32(np.sqrt(cols))).bfloat16().cuda()
+    w.sf = bsq.tensor_sf(full)[1:] if fmt == "nvfp4" else None
+    w.packed, w.scales = bsq.quantize_dynamic(full, fmt, w.sf)
+    bands = sorted({0, 128 * int(rng.integers(0, -(-rows // 128))), (rows - 1) // 256 * 256, (rows - 1) // 128 * 128})
+    x = inputs(tokens, cols, dtype)
+    add = torch.from_numpy(rng.standard_normal((tokens, rows), np.float32)).to(DT[dtype]).cuda()
+    y = w.call(bsq, x, add=add).double().cpu().numpy()
+    atom_row = w.scales.numel() // -(-rows // 128)  # bytes of a band's scales
+    for r0 in bands:
+        r1 = min(r0 + 128, rows)
+        values = ref.weights(fmt, w.packed[r0:r1].cpu().numpy(), w.scales.reshape(-1)[r0 // 128 * atom_row:][:atom_row].cpu().numpy(), r1 - r0, cols,
+                             1.0 if w.sf is None else float(w.sf))
+        expect, tol = ref.linear(x.double().cpu().numpy(), values, add[:, r0:r1].double().cpu().numpy(), dtype)
+        err = np.abs(y[:, r0:r1] - expect)
+        assert (err <= tol).all(), f"rows from {r0}: {(err / tol).max():.3f} of the tolerance"
