@@ -24,6 +24,8 @@ struct RouteArgs {
   int64_t tokens;
   const float* bias;  // may be null
   int experts, top_k, groups, top_groups, group_top;
+  int per, span_log;  // experts per group, and lanes that share its values (a power of two)
+  uint32_t inv;       // 2^20 / per, rounded up: e * inv >> 20 is the group of expert e, for e up to 1024
   int sigmoid, renorm;
   float scale;
   int32_t* ids;
@@ -172,15 +174,15 @@ __device__ __forceinline__ int route_select(K (&key)[NL], int top_k, int lane, f
   return my_id;
 }
 
-// The groups that stay, a bit per group: the lanes share the groups out, `v` holds the experts' values in shared memory.  `margin`:
+// The groups that stay, group g's bit at g times the power of two span_log: the lanes share the groups out, `v` holds the experts' values in shared memory.  `margin`:
 // how far the least score that stays lies above the largest that does not.
 template <typename V>
 __device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const V* v, int lane, float& margin) {
-  int span = 32;  // lanes per group
-  while (span * a.groups > 32) span >>= 1;
-  const int g = lane / span, part = lane % span, per = a.experts / a.groups;
+  const int span = 1 << a.span_log;  // lanes per group
+  const int g = lane >> a.span_log, part = lane & (span - 1), per = a.per;
   V first = RouteNum<V>::least(), second = first;
   if (g < a.groups)
+#pragma unroll 4
     for (int j = part; j < per; j += span) {
       const V x = v[g * per + j];
       if (RouteNum<V>::greater(x, first)) {
@@ -202,6 +204,7 @@ __device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const V* v,
   V score = first;
   if (a.group_top == 2 && per > 1) score = RouteNum<V>::sum(first, second);
   int before = 0;
+#pragma unroll 4
   for (int o = 0; o < a.groups; ++o) {
     const V s = RouteNum<V>::shuffle(score, o * span);
     before += RouteNum<V>::greater(s, score) || (o < g && RouteNum<V>::equal(s, score));
@@ -211,13 +214,11 @@ __device__ __forceinline__ uint32_t route_groups(const RouteArgs& a, const V* v,
   const uint32_t low = __reduce_min_sync(~0u, stays ? route_key(RouteNum<V>::leading(score)) : ~0u);
   const uint32_t high = __reduce_max_sync(~0u, there && !stays ? route_key(RouteNum<V>::leading(score)) : 0u);
   margin = high == 0u || route_unkey(high) == -INFINITY ? INFINITY : route_unkey(low) - route_unkey(high);
-  uint32_t kept = 0;
-  for (int o = 0; o < a.groups; ++o) kept |= (votes >> (o * span) & 1u) << o;
-  return kept;
+  return votes;
 }
 
-// Whether expert e's group stays; inv: 2^20 / experts per group, rounded up (e * inv >> 20 is the group for e up to 1024).
-__device__ __forceinline__ bool route_kept(uint32_t kept, uint32_t e, uint32_t inv) { return kept >> ((e * inv) >> 20) & 1u; }
+// Whether expert e's group stays.
+__device__ __forceinline__ bool route_kept(const RouteArgs& a, uint32_t kept, uint32_t e) { return kept >> (((e * a.inv) >> 20) << a.span_log) & 1u; }
 
 // A logit or bias that takes part: NaN and +inf count as -inf.
 __device__ __forceinline__ float route_clean(float x) { return x < INFINITY ? x : -INFINITY; }
@@ -295,7 +296,6 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, const void* row, Rou
   __syncwarp();
   float margin, least;
   const uint32_t kept = a.groups > 1 ? route_groups(a, values, lane, margin) : 1u;
-  const uint32_t per = a.experts / a.groups, inv = ((1u << 20) + per - 1) / per;
   uint64_t key[NL];
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
@@ -303,7 +303,7 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, const void* row, Rou
     key[i] = 0;
     if (e < a.experts) {
       RouteFF v = a.bias ? values[e] : RouteFF{route_clean(route_load<DTYPE>(row, e)), 0.f};
-      if (!route_kept(kept, e, inv)) v = {-INFINITY, 0.f};
+      if (!route_kept(a, kept, e)) v = {-INFINITY, 0.f};
       key[i] = static_cast<uint64_t>(route_key(v.h)) << 32 | route_key(v.l);
     }
   }
@@ -397,14 +397,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
     __syncwarp();
     kept = route_groups(a, plain, lane, group_margin);
   }
-  const uint32_t per = a.experts / a.groups, inv = ((1u << 20) + per - 1) / per;
   uint32_t key[NL];
   float size = 0.f;  // of the values, whose rounding counts too
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
     const uint32_t e = 32 * i + lane;
     if (PAIR && v[i] > -INFINITY && e < static_cast<uint32_t>(a.experts)) size = fmaxf(size, fabsf(v[i]));
-    key[i] = e < static_cast<uint32_t>(a.experts) ? route_key(route_kept(kept, e, inv) ? v[i] : -INFINITY) : 0u;
+    key[i] = e < static_cast<uint32_t>(a.experts) ? route_key(route_kept(a, kept, e) ? v[i] : -INFINITY) : 0u;
   }
   int my_id = route_select<NL>(key, a.top_k, lane, margin, least);
   if constexpr (PAIR) {

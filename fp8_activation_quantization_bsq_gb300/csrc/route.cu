@@ -21,7 +21,9 @@ cudaError_t launch_route(const RouteArgs& a, bool pair, cudaStream_t st) {
 template <int DTYPE>
 cudaError_t launch_route_experts(const RouteArgs& a, bool pair, cudaStream_t st) {
   if (a.experts <= 64) return launch_route<DTYPE, 2>(a, pair, st);
+  if (a.experts <= 128) return launch_route<DTYPE, 4>(a, pair, st);
   if (a.experts <= 256) return launch_route<DTYPE, 8>(a, pair, st);
+  if (a.experts <= 512) return launch_route<DTYPE, 16>(a, pair, st);
   return launch_route<DTYPE, 32>(a, pair, st);
 }
 
@@ -54,6 +56,10 @@ int32_t bsq_moe_route(int32_t dtype, const void* logits, int64_t ld_logits, int6
   a.groups = groups;
   a.top_groups = top_groups;
   a.group_top = group_top;
+  a.per = experts / groups;
+  a.inv = ((1u << 20) + a.per - 1) / a.per;
+  a.span_log = 5;
+  while (groups << a.span_log > 32) --a.span_log;
   a.sigmoid = sigmoid != 0;
   a.renorm = renormalize != 0;
   a.scale = scale;
