@@ -310,9 +310,10 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, const void* row, Rou
   return route_select<NL>(key, a.top_k, lane, margin, least);
 }
 
-// Measured, 8 of 256 experts: 64 tokens by softmax 2.5 us, one token by sigmoid with bias and groups 4.3 us; 4096 tokens of those 11 us, of
-// plain softmax 5.3.  Of the 11 the nine rounds of the choice take 2.7, the groups 1.8, tokens that are chosen again 0.9, a launch 2, DRAM
-// 0.7: about 1600 instructions a token.  All values in two numbers from the start, in place of FP32 first: 18.8 us, one token 7.9.
+// Measured, 8 of 256 experts: 64 tokens by softmax 2.5 us, one token by sigmoid with bias and groups 4.0 us; 4096 tokens of those 9.6 us, of
+// plain softmax 5.3.  Bound by instructions, some 1400 a token: the nine rounds of the choice (2.7 us of 10.9 before the kept groups' experts
+// were put side by side, which takes 10.4 to 9.6), the groups (1.8), tokens that are chosen again (0.9), a launch (2); DRAM's part is 0.7 us.
+// All values in two numbers from the start, in place of FP32 first: 18.8 us, one token 7.9.  Slots for 128 and 512 experts: 9.2 -> 7.2 and 26.6 -> 18.1.
 //
 // NL: logits per lane (expert 32 i + lane in slot i).  PAIR: p enters the comparison (a bias, or sums of two in groups).
 //
@@ -397,32 +398,68 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
     __syncwarp();
     kept = route_groups(a, plain, lane, group_margin);
   }
-  uint32_t key[NL];
-  float size = 0.f;  // of the values, whose rounding counts too
-#pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    const uint32_t e = 32 * i + lane;
-    if (PAIR && v[i] > -INFINITY && e < static_cast<uint32_t>(a.experts)) size = fmaxf(size, fabsf(v[i]));
-    key[i] = e < static_cast<uint32_t>(a.experts) ? route_key(route_kept(a, kept, e) ? v[i] : -INFINITY) : 0u;
-  }
-  int my_id = route_select<NL>(key, a.top_k, lane, margin, least);
   if constexpr (PAIR) {
-    tol += 0x1p-21f * __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(size)));
-    // without a bias the logits themselves are compared, and only the groups' scores are rounded
-    const bool groups_open = !(group_margin > 2.f * tol), open = a.bias && !(margin > tol);
-    if (groups_open || open) {
-      // the chosen experts, and those that may belong in their place
-      int mine = my_id, count = a.top_k;
-      const float from = least - tol;
+    float size = 0.f;  // of the values, whose rounding counts too
 #pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const uint32_t near = __ballot_sync(~0u, key[i] != 0u && route_unkey(key[i]) >= from);
-        for (uint32_t rest = near; rest != 0u; rest &= rest - 1u, ++count)
-          if (lane == count) mine = 32 * i + __ffs(rest) - 1;
+    for (int i = 0; i < NL; ++i)
+      if (v[i] > -INFINITY && 32 * i + lane < a.experts) size = fmaxf(size, fabsf(v[i]));
+    tol += 0x1p-21f * __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(size)));
+  }
+  int my_id = 0;
+  // the choice by the keys of 32 slots a lane; expert_of: a slot's expert
+  const auto choose = [&](auto& key, auto expert_of) {
+    constexpr int N = sizeof(key) / sizeof(key[0]);
+    my_id = expert_of(route_select<N>(key, a.top_k, lane, margin, least));
+    if constexpr (PAIR) {
+      // without a bias the logits themselves are compared, and only the groups' scores are rounded
+      const bool groups_open = !(group_margin > 2.f * tol), open = a.bias && !(margin > tol);
+      if (groups_open || open) {
+        // the chosen experts, and those that may belong in their place
+        int mine = my_id, count = a.top_k;
+        const float from = least - tol;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const uint32_t near = __ballot_sync(~0u, key[i] != 0u && route_unkey(key[i]) >= from);
+          for (uint32_t rest = near; rest != 0u; rest &= rest - 1u, ++count) {
+            const int id = expert_of(32 * i + __ffs(rest) - 1);
+            if (lane == count) mine = id;
+          }
+        }
+        my_id = groups_open || count > 32 || !(least > -INFINITY) ? route_exact<DTYPE, NL>(a, row, values, top, lane)
+                                                                  : route_near<DTYPE>(a, row, reinterpret_cast<int32_t*>(values), top, lane, mine, count);
       }
-      my_id = groups_open || count > 32 || !(least > -INFINITY) ? route_exact<DTYPE, NL>(a, row, values, top, lane)
-                                                                : route_near<DTYPE>(a, row, reinterpret_cast<int32_t*>(values), top, lane, mine, count);
     }
+  };
+  bool chosen = false;
+  if constexpr (NL >= 4) {
+    // where the groups that stay fill at most half of the slots, their experts alone, side by side (in the same order)
+    if (a.groups > 1 && a.top_groups * a.per <= 16 * NL && (!PAIR || a.bias)) {
+      int* const list = reinterpret_cast<int*>(plain + a.experts);  // the groups that stay
+      if (kept >> lane & 1u) list[__popc(kept & ((1u << lane) - 1u))] = lane >> a.span_log;
+      __syncwarp();
+      const auto expert_of = [&](uint32_t slot) {
+        const uint32_t g = (slot * a.inv) >> 20;
+        return g < static_cast<uint32_t>(a.top_groups) ? static_cast<int>(slot + (list[g] - g) * a.per) : -1;
+      };
+      uint32_t key[NL / 2];
+#pragma unroll
+      for (int i = 0; i < NL / 2; ++i) {
+        const int e = expert_of(32 * i + lane);
+        key[i] = e >= 0 ? route_key(plain[e]) : 0u;
+      }
+      // (with fewer than top_k values the rest goes to the lowest experts of any group)
+      choose(key, expert_of);
+      chosen = least > -INFINITY;
+    }
+  }
+  if (!chosen) {
+    uint32_t key[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const uint32_t e = 32 * i + lane;
+      key[i] = e < static_cast<uint32_t>(a.experts) ? route_key(route_kept(a, kept, e) ? v[i] : -INFINITY) : 0u;
+    }
+    choose(key, [](int slot) { return slot; });
   }
   // weights: from the logits, and relative to the largest chosen one where they are divided by their sum, so that small
   // scores keep their ratios: 1 / (1 + exp(-z)) = exp(min(z, 0)) / (1 + exp(-|z|))
@@ -450,8 +487,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
 // sums over warps, blocks (through distributed shared memory) and experts, and the warp goes over its run again:
 // a pair's row is its counter plus the number of lower lanes with its expert.  No atomics, so the order
 // is the pairs' own.  Bound by latency: a few dependent passes.  Measured, 8 of 256 experts (graph replay, with the
-// routing in front, which alone takes 11 us for 4096 tokens): 4096 tokens 17.9 us in a cluster of 16 blocks, 20.3 with 8, 25.5 with 4, 70 with one;
+// routing in front, which then took 11 us for 4096 tokens): 4096 tokens 17.9 us in a cluster of 16 blocks, 20.3 with 8, 25.5 with 4, 70 with one;
 // 512 tokens 11.2, with one block 14.7.  Runs of up to 8 rounds keep experts and places in registers: 17.9 against 18.9, 128 tokens 8.3 and 9.0.
+// Now 16.0 us with the routing's 9.6.  Of 12 thousand cycles reading the ids takes 0.8, two rounds of places 2, the sums over warps 1, the cluster's
+// 2.6, the scan 1.2, and the scattered stores 2.6.
 constexpr int kRowsThreads = 1024, kRowsWarps = kRowsThreads / 32, kRowsMaxBlocks = 16, kRowsHeld = 8;
 
 struct RowsArgs {

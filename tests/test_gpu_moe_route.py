@@ -209,3 +209,27 @@ def test_graph_and_streams(bsq):
     got = bsq.moe_route(z, 8, "sigmoid", bias, 8, 4, stream=stream)
     torch.cuda.synchronize()
     assert torch.equal(got[0], expect)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups,top_groups", [(128, 8, 3), (96, 6, 2), (250, 10, 5), (512, 4, 2), (1000, 20, 3)])
+def test_few_groups_of_many(bsq, scoring, experts, groups, top_groups):
+    """Groups that fill at most half of the experts: values left in all, some and none of them, equal ones, and ones closer than FP32 tells apart."""
+    rng = np.random.default_rng(experts)
+    z = logits(9, experts, "f32", seed=experts)
+    per = experts // groups
+    z[1, 5:] = -np.inf                        # five left, all in the first groups
+    z[2, :experts - 3] = -np.inf              # three left in the last group: the others are the first experts of all
+    z[3] = -np.inf
+    z[4, ::2] = -np.inf
+    z[5] = 0.5                                # all equal
+    z[6] = torch.from_numpy(np.repeat(rng.standard_normal(groups), per).astype(np.float32)).cuda()  # equal within a group
+    z[7, per:] = -np.inf
+    for bias in (None, biases(experts, 0.2)):
+        for group_top in (1, 2):
+            check(bsq, z, 8, scoring, bias, groups, top_groups, group_top)
+    one = rng.standard_normal(experts).astype(np.float32)
+    p = 1 / (1 + np.exp(-one.astype(np.float64))) if scoring == "sigmoid" else np.exp(one.astype(np.float64)) / np.exp(one.astype(np.float64)).sum()
+    bias = (1.0 - p).astype(np.float32)
+    bias[per * top_groups:] -= np.float32(0.25)  # the first groups stay, their values one apart by the bias's rounding
+    check(bsq, torch.from_numpy(np.tile(one, (5, 1))).cuda(), 8, scoring, torch.from_numpy(bias).cuda(), groups, top_groups, 1)
