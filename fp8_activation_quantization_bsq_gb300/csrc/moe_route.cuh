@@ -311,7 +311,7 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, const void* row, Rou
 }
 
 // Measured, 8 of 256 experts: 64 tokens by softmax 2.5 us, one token by sigmoid with bias and groups 4.0 us; 4096 tokens of those 9.6 us, of
-// plain softmax 5.3.  Bound by instructions, some 1400 a token: the nine rounds of the choice (2.7 us of 10.9 before the kept groups' experts
+// plain softmax 5.3.  Bound by instructions, about 1350 a token: the nine rounds of the choice (2.7 us of 10.9 before the kept groups' experts
 // were put side by side, which takes 10.4 to 9.6), the groups (1.8), tokens that are chosen again (0.9), a launch (2); DRAM's part is 0.7 us.
 // All values in two numbers from the start, in place of FP32 first: 18.8 us, one token 7.9.  Slots for 128 and 512 experts: 9.2 -> 7.2 and 26.6 -> 18.1.
 //

@@ -230,6 +230,8 @@ def test_graph_streams_and_repeats(bsq, tokens):
     (100, 19580, 512),   # two tiles, one block along K
     (33, 60000, 96),     # the same, several tiles one after the other
     (300, 20000, 96),    # one tile of rows, several one after the other
+    (250, 129, 8192),    # eight blocks along K and the largest tile of tokens, one tile of rows
+    (112, 7000, 16384),  # five, and two
 ])
 def test_splits(bsq, fmt, dtype, tokens, rows, cols):
     """The ways in which rows, K and tokens are shared out, with a residual; the rows at both ends and some between are checked."""
