@@ -55,7 +55,7 @@ def _binding_commands():
            os.path.join(base, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"), "-isystem",
            sysconfig.get_paths()["include"], "-c", "-o", obj, os.path.join(CSRC, BINDING)]
     link = ["g++", "-shared", "-o", BINDING_PATH + ".tmp", obj, "-L" + LIB_DIR, "-lbsq", "-L" + os.path.join(base, "lib"), "-ltorch_python",
-            "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+            "-ltorch_cpu", "-ltorch", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
     return cxx, link
 
 

@@ -6,7 +6,8 @@
 // BsqError; work goes to the given or current stream, and outputs are allocated under it.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -89,7 +90,7 @@ struct Call {
     }
   }
   at::Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(c10::Device(c10::DeviceType::CUDA, static_cast<c10::DeviceIndex>(index))));
+    return at::Tensor(at::detail::empty_cuda(shape, type, c10::Device(c10::DeviceType::CUDA, static_cast<c10::DeviceIndex>(index)), std::nullopt));
   }
   void check(int32_t rc, const char* name) const {
     if (rc == BSQ_OK) return;
