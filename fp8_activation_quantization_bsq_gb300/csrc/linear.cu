@@ -28,22 +28,26 @@ struct PlPlan {
 PlPlan plan_linear(const PlArgs& a, int cols_of_piece, int token_tile) {
   const int toks = std::min(a.tokens, token_tile);
   constexpr int kBlockMost = 227 * 1024, kOverhead = 2 * 1024;  // static shared memory and what the system takes, per block
+  const int bands = static_cast<int>(ceil_div(a.rows, 128)) * static_cast<int>(ceil_div(a.tokens, token_tile));
+  const int token_bytes = cols_of_piece * 2;  // of a piece
   PlPlan best{};
   double least = 0;
   for (int sets = 1; sets <= 4; sets += 3) {
     const int split = kPlWarps / sets, step = split * cols_of_piece % 256 == 0 ? split : 2 * split;  // a segment: a multiple of 256 columns
     const int room = 113 * 1024 - kOverhead - kPlRing;  // for tokens, with two blocks per SM
-    const int most = std::max(step, (room / toks - 64) / (step * cols_of_piece * 2) * step);
-    const int64_t tiles = ceil_div(a.rows, 128) * 4 / sets * ceil_div(a.tokens, token_tile);
+    const int most = std::max(step, (room / toks - 64) / (step * token_bytes) * step);
+    int last = 0;
     for (int r = 1; r <= 8; ++r) {
-      const int share = static_cast<int>(ceil_div(ceil_div(a.pieces, r), split) * split), ranks = static_cast<int>(ceil_div(a.pieces, share));
-      const int segment = std::min(most, static_cast<int>(ceil_div(share, step) * step));
-      const int smem = std::max(kPlRing + toks * (segment * cols_of_piece * 2 + 64), kPlWarps * token_tile * 32 * 4);
+      const int share = ((a.pieces + r - 1) / r + split - 1) & -split;  // split and step are powers of two
+      if (share == last) continue;
+      last = share;
+      const int ranks = (a.pieces + share - 1) / share, blocks = bands * (4 / sets) * ranks;
+      const int segment = std::min(most, (share + step - 1) & -step), more = segment < share ? (share - 1) / segment : 0;
+      const int smem = std::max(kPlRing + toks * (segment * token_bytes + 64), kPlWarps * token_tile * 32 * 4);
       const int resident = std::min(token_tile == 8 ? 3 : 2, kBlockMost / (smem + kOverhead));
-      const int64_t blocks = tiles * ranks;
-      const double n = blocks <= kResident[ranks] ? 1.1 : blocks <= kResidentTwo[ranks] ? 2.0 : static_cast<double>(ceil_div(2 * blocks, kResidentTwo[ranks]));
-      const double cost = n * (sets * share + 0.23 * share * toks * cols_of_piece / 128 + 60.0 * (ceil_div(share, segment) - 1)) +
-                          85.0 * std::max(0.0, n - resident) + (ranks > 1 ? 12.0 : 0.0);
+      const double n = blocks <= kResident[ranks] ? 1.1 : blocks <= kResidentTwo[ranks] ? 2.0 : static_cast<double>((2 * blocks - 1) / kResidentTwo[ranks] + 1);
+      const double cost = n * (sets * share + 0.23 / 128 * (share * toks * cols_of_piece) + 60.0 * more) + 85.0 * std::max(0.0, n - resident) +
+                          (ranks > 1 ? 12.0 : 0.0);
       if (best.sets == 0 || cost < least) {
         least = cost;
         best = {sets, share, segment, ranks, smem};
