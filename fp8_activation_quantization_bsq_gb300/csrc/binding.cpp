@@ -1,9 +1,10 @@
 // Python module _bsq_binding: the calls of layer.py from torch tensors to the C ABI (bsq.h).
 //
 // A call for a single token keeps the GPU busy for two to four microseconds; reading the tensors' attributes, allocating and
-// converting the arguments from Python took four times that (routing 13.5 us a call of the host, the rows' order 24).
-// The checks, the allocation of missing outputs and the call are therefore compiled.  Refused arguments raise ValueError, statuses
-// BsqError; work goes to the given or current stream, and outputs are allocated under it.
+// converting the arguments from Python took the host 13.5 us for routing and 24 for the rows' order.  The checks, the allocation of missing outputs
+// and the call are therefore compiled: 3.7 us a projection, 4.5 a rotation or routing, routing and rows 10.2 (through the dispatcher's allocation
+// 4.3, 5.3 and 13.1).  Refused arguments raise ValueError, statuses BsqError; work goes to the given or current stream, and outputs are
+// allocated under it.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
