@@ -3,11 +3,12 @@
 //   (u_a, u_b) -> (u_a cos t - u_b sin t, u_b cos t + u_a sin t),  t = position * inv_freq[i]
 // for the first `pairs` pairs of a row, (i, i + pairs) or (2i, 2i + 1); what lies behind passes.
 //
-// Bound by DRAM: 2 bytes read and 2 written per element.  Measured: 4096 tokens of 64 + 8 heads of 128 29.4 us (5.1 TB/s; of 6.8 copied), 16384
-// tokens 6.3 TB/s; one token of 32 + 8 heads 2.7 us, a launch.  A warp keeps 6 steps of its rows in flight through a ring in shared memory
-// (two in registers: 48.7 us, they are too many).  A row's 8 elements per lane are two
-// groups of 4 that hold both sides of a lane's pairs, so that no element crosses lanes and the lane's 4
-// angles serve every head of the token that the warp takes; 8, 16 or 32 lanes per row (dim to 64, 128, 256).
+// Bound by DRAM: 2 bytes read and 2 written per element.  Measured: 4096 tokens of 64 + 8 heads of 128 26.5 us (5.7 TB/s; of 6.8 copied), 16384
+// tokens 6.2 TB/s; one token of 32 + 8 heads 2.6 us, a launch.  A row's 8 elements per lane are two
+// groups of 4 that hold both sides of a lane's pairs, so that no element crosses lanes in registers and the lane's 4
+// angles serve every head of the token that the warp takes; 8, 16 or 32 lanes per row (dim to 64, 128, 256).  A warp keeps 4 steps of its rows in
+// flight through a ring in shared memory, 16 bytes a lane: with 3, 5, 6 and 8 steps 28.1, 26.8, 27.5 and 28.5 us (heads of 256 51.9, 59.4, 60.4, 61.0, with
+// 4 56.3; 16384 tokens of 128 100.6, 95.8, 95.1, 95.7, with 4 97.1); each lane copying its own two groups of 8 bytes 29.4; two steps in registers 48.7.
 //
 // Angles: t / 2 pi in fixed point.  inv_freq is a 24-bit integer times a power of two, 1 / (2 pi) a 64-bit
 // fraction, and the position multiplies their product modulo 2^64, which drops whole turns exactly: off by
@@ -18,7 +19,7 @@
 
 namespace bsq {
 
-constexpr int kRopeWarps = 4, kRopeDepth = 6;  // steps of a warp in flight
+constexpr int kRopeWarps = 4, kRopeDepth = 4;  // steps of a warp in flight
 
 struct RopeArgs {
   const uint16_t* src[2];  // queries, keys
@@ -74,7 +75,7 @@ template <bool F16, int L, int MODE>
 __global__ void __launch_bounds__(kRopeWarps * 32, MODE == 2 ? 5 : 8) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int kPer = 32 / L;  // rows at a time
   __shared__ float other[MODE == 2 ? kRopeWarps * 256 : 1];
-  __shared__ uint4 ring[kRopeWarps][kRopeDepth][32];  // a lane's elements of a step, which it copies and reads itself
+  __shared__ uint4 ring[kRopeWarps][kRopeDepth][32];  // the rows of a step, 16 bytes a lane
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / L, p = lane % L;
   const int64_t task = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp;
@@ -132,17 +133,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32, MODE == 2 ? 5 : 8) qk_norm_ro
     uint16_t* d = a.dst[k] + token * a.dst_tok[k] + h * a.dst_head[k];
     const int64_t s_step = kPer * a.src_head[k], d_step = kPer * a.dst_head[k];
     uint4* const mine_in = &ring[warp][0][lane];
+    const uint8_t* const row_in = reinterpret_cast<const uint8_t*>(&ring[warp][0][sub * L]);
     int left = active ? n - sub : 0;  // rows not yet asked for, this lane's at every kPer-th
     const auto ask = [&](int slot) {
-      if (left > 0) {
-        const uint32_t to = smem_addr(mine_in + slot * 32);
-        if (apart) {
-          cp_async8(to, s + ea);
-          cp_async8(to + 8, s + eb);
-        } else {
-          cp_async16(to, s + ea);
-        }
-      }
+      if (left > 0) cp_async16(smem_addr(mine_in + slot * 32), s + 8 * p);
       cp_async_commit();
       left -= kPer;
       s += s_step;
@@ -154,10 +148,20 @@ __global__ void __launch_bounds__(kRopeWarps * 32, MODE == 2 ? 5 : 8) qk_norm_ro
     for (int i = sub; i - sub < n; i += kPer, d += d_step) {
       const bool in = i < n && active;
       cp_async_wait<kRopeDepth - 2>();
-      const uint4 v = in ? mine_in[slot * 32] : make_uint4(0, 0, 0, 0);
+      uint2 va = make_uint2(0, 0), vb = va;
+      if constexpr (MODE == 0) {
+        __syncwarp();  // a lane reads what others copied
+        if (in) {
+          va = *reinterpret_cast<const uint2*>(row_in + slot * 512 + ea * 2);
+          vb = *reinterpret_cast<const uint2*>(row_in + slot * 512 + eb * 2);
+        }
+      } else if (in) {
+        const uint4 v = mine_in[slot * 32];
+        va = make_uint2(v.x, v.y);
+        vb = make_uint2(v.z, v.w);
+      }
       ask(slot == 0 ? kRopeDepth - 1 : slot - 1);
       slot = slot == kRopeDepth - 1 ? 0 : slot + 1;
-      const uint2 va = make_uint2(v.x, v.y), vb = make_uint2(v.z, v.w);
       float2 x[4] = {elem2_to_f32x2<F16>(va.x), elem2_to_f32x2<F16>(va.y), elem2_to_f32x2<F16>(vb.x), elem2_to_f32x2<F16>(vb.y)};
       if (norm) {
         const auto squares = [&]() {

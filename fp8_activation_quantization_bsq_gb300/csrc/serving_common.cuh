@@ -72,7 +72,7 @@ __device__ __forceinline__ float elem_absmax_final(uint32_t acc) {
 // 2^e for -127 <= e <= 127 (2^-127 is subnormal).
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(e > -127 ? static_cast<uint32_t>(e + 127) << 23 : 0x00400000u); }
 
-// Asynchronous copies into shared memory, 16 bytes (zeros where not valid, nothing is read then) or 8, and their groups.
+// Asynchronous copies of 16 bytes into shared memory (zeros where not valid, nothing is read then), and their groups.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
@@ -80,9 +80,6 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
