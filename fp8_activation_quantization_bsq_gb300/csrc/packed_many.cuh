@@ -70,8 +70,11 @@ __device__ __forceinline__ uint32_t pm_scaled_bf16(uint32_t h, float f) {
   return f32x2_to_elem2<false>(v.x, v.y);
 }
 
+// With FP16 tokens and MX, weights are held relative to their row's largest scale, which becomes 2^this: the largest codes then fit FP16.
+template <int FMT> constexpr int kPmTop = FMT == kMXFP8 ? 7 : 13;
+
 // The factors of a row's step: NVFP4 four, from `word`'s bytes, MX two, from its bytes at `at` and behind, as FP16 pairs or FP32
-// numbers.  `top`: with FP16 tokens and MX, the byte that stands for 2^13 (E2M1) or 2^7 (E4M3).
+// numbers.  `top`: with FP16 tokens and MX, the byte that stands for 2^kPmTop.
 template <int FMT, bool F16>
 __device__ __forceinline__ void pm_factors(uint32_t word, int at, int top, uint32_t (&f)[4]) {
   if constexpr (FMT == kNVFP4) {
@@ -92,7 +95,7 @@ __device__ __forceinline__ void pm_factors(uint32_t word, int at, int top, uint3
     for (int i = 0; i < 2; ++i) {
       const uint32_t byte = word >> (8 * (at + i)) & 255u;
       if constexpr (F16) {
-        const int e = static_cast<int>(byte) - top + (FMT == kMXFP8 ? 7 : 13);  // at most 13
+        const int e = static_cast<int>(byte) - top + kPmTop<FMT>;  // at most 13
         const uint32_t one = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
         f[i] = one | one << 16;
       } else {
@@ -350,7 +353,9 @@ __global__ void __launch_bounds__(kPmThreads, 1)
       const int rt = tile / a.token_tiles, tt = tile % a.token_tiles;
       const int64_t band = static_cast<int64_t>(rt) * MT + m, row = band * 128 + r;
       const bool idle = band * 128 >= a.p.rows;  // the second tile lies behind the last row
-      int top = 0;  // with FP16 tokens and MX: the row's largest scale byte
+      // with FP16 tokens and MX: the row's largest scale byte, and no less than what lets the factor at the end be a number (2^-127); smaller
+      // scales are then held below 2^13 (E2M1) or 2^7 (E4M3), exactly
+      int top = kPmTop<FMT>;
       if constexpr (F16 && FMT != kNVFP4) {
         if (!idle) {
           const uint8_t* s = a.p.scales + band * a.p.k_atoms * 512 + lane * 16 + quarter * 4;
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(kPmThreads, 1)
       if (!ok) break;
       t5_fence_after();
       const int tok0 = tt * n_tok, toks = min(n_tok, a.p.tokens - tok0);
-      const float f = F16 && FMT != kNVFP4 ? pow2f(max(top, 1) - 127 - (FMT == kMXFP8 ? 7 : 13)) : inv;
+      const float f = F16 && FMT != kNVFP4 ? pow2f(top - 127 - kPmTop<FMT>) : inv;
       row_factor = f;
       if (!idle && ranks == 1) {
         for (int c0 = 32 * turn; c0 < toks; c0 += 32 * kTurns) {
