@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, MODE == 2 ? 5 : 8) qk_norm_ro
       }
     }
     cp_async_wait<0>();
+    __syncwarp();  // the keys' first rows go where a lane may still read the queries' last ones
   }
 }
 

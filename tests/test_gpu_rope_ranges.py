@@ -1,0 +1,28 @@
+"""qk_norm_rope where its parts meet and at the ends of its ranges, against the
+64-bit statement."""
+import pytest
+
+from test_gpu_qk_norm_rope import bsq, check, make  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("norm", [None, "q", "k"])
+def test_queries_and_keys_of_every_number_of_steps(bsq, dim, norm):  # noqa: F811
+    """A warp takes a token's queries, then its keys, through one ring of shared memory, without anything between but what the passes
+    themselves wait for: every number of steps that leaves the ring at another place, each way of pairing."""
+    at_once = 256 // dim if dim < 256 else 1
+    for steps in range(1, 10):
+        for pairs, interleaved in ((dim // 2, False), (dim // 2, True), (dim // 2 - 1, False)):
+            # so many tokens that a warp takes all rows of one
+            q, k, pos, freq, qw, kw = make(2600, steps * at_once, 2 * at_once, dim, pairs, "bf16", seed=steps)
+            a, b = qw if norm == "q" else None, kw if norm == "k" else None
+            got = bsq.qk_norm_rope(q, k, pos, freq, a, b, interleaved=interleaved)
+            part = slice(None, None, 97)
+            check(q[part], k[part], pos[part], freq, a, b, (got[0][part], got[1][part]), "bf16", interleaved)
+            # the same rows one pass at a time
+            assert torch.equal(got[0], bsq.qk_norm_rope(q, k[:, :0], pos, freq, a, b, interleaved=interleaved)[0])
+            assert torch.equal(got[1], bsq.qk_norm_rope(q[:, :0], k, pos, freq, a, b, interleaved=interleaved)[1])
