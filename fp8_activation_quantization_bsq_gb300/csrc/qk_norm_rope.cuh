@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, MODE == 2 ? 5 : 8) qk_norm_ro
         }
         const float f = rsqrtf(sum * a.inv_dim + eps);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = mul_f32x2(x[j], mul_f32x2(w[j], make_float2(f, f)));
+        for (int j = 0; j < 4; ++j) x[j] = mul_f32x2(mul_f32x2(x[j], make_float2(f, f)), w[j]);  // f w alone may pass FP32
       }
       float2 y[4] = {x[0], x[1], x[2], x[3]};
       if constexpr (MODE == 0) {

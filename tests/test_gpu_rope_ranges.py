@@ -1,5 +1,6 @@
 """qk_norm_rope where its parts meet and at the ends of its ranges, against the
 64-bit statement."""
+import numpy as np
 import pytest
 
 from test_gpu_qk_norm_rope import bsq, check, make  # noqa: F401
@@ -26,3 +27,12 @@ def test_queries_and_keys_of_every_number_of_steps(bsq, dim, norm):  # noqa: F81
             # the same rows one pass at a time
             assert torch.equal(got[0], bsq.qk_norm_rope(q, k[:, :0], pos, freq, a, b, interleaved=interleaved)[0])
             assert torch.equal(got[1], bsq.qk_norm_rope(q[:, :0], k, pos, freq, a, b, interleaved=interleaved)[1])
+
+
+@pytest.mark.parametrize("size,weight,eps", [(1e18, 1e-25, 1e-6), (1e-12, 1e30, 0.0), (1e10, 1e-36, 1e-6), (1e-10, 1e28, 1e-30)])
+def test_weights_far_from_one(bsq, size, weight, eps):  # noqa: F811
+    """The norm's factor times the weight may lie outside FP32 where the result does not."""
+    q, k, pos, freq, qw, kw = make(20, 3, 2, 128, 64, "bf16", seed=8)
+    q, k, qw, kw = q.float().mul(size).bfloat16(), k.float().mul(size).bfloat16(), qw.float() * weight, kw.float() * weight
+    got = bsq.qk_norm_rope(q, k, pos, freq, qw, kw, eps=eps)
+    check(q, k, pos, freq, qw, kw, got, "bf16", False, float(np.float32(eps)))
