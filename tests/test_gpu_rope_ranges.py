@@ -3,7 +3,7 @@
 import numpy as np
 import pytest
 
-from test_gpu_qk_norm_rope import bsq, check, make  # noqa: F401
+from test_gpu_qk_norm_rope import DT, bsq, check, make  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +36,18 @@ def test_weights_far_from_one(bsq, size, weight, eps):  # noqa: F811
     q, k, qw, kw = q.float().mul(size).bfloat16(), k.float().mul(size).bfloat16(), qw.float() * weight, kw.float() * weight
     got = bsq.qk_norm_rope(q, k, pos, freq, qw, kw, eps=eps)
     check(q, k, pos, freq, qw, kw, got, "bf16", False, float(np.float32(eps)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-40, 1e-36, 1e-30, 1e-24, 1e-21, 1e-20, 1e-12, 1e-6, 1.0, 1e20, 3.4e38])
+def test_every_size_of_rows_with_every_eps(bsq, dtype, eps):  # noqa: F811
+    """Rows whose squares leave FP32 at either end, with an eps that matters beside them, far above or not at all; elements of very different
+    sizes in one row."""
+    q, k, pos, freq, qw, kw = make(60, 3, 1, 128, 64, dtype, seed=9)
+    low, high = (-130, 126) if dtype == "bf16" else (-20, 14)
+    size = torch.exp2(torch.linspace(low, high, 60, device="cuda").round()).double()[:, None, None]
+    q, k = ((x.double().clamp(-1.9, 1.9) * size).to(DT[dtype]) for x in (q, k))
+    q[:, 1, ::5] = (q[:, 1, ::5].double() * 2.0 ** -60).to(DT[dtype])
+    q[:, 2, 1:] = 0  # one element alone
+    got = bsq.qk_norm_rope(q, k, pos, freq, qw, kw, eps=eps)
+    check(q, k, pos, freq, qw, kw, got, dtype, False, float(np.float32(eps)))
