@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(LIB_DIR, "libbsq.so")
 BINDING_PATH = os.path.join(LIB_DIR, "_bsq_binding.so")
 
 SOURCES = ["bsq.cu", "kv_cache.cu", "moe.cu", "linear.cu", "rope.cu", "route.cu"]
-HEADERS = ["host_common.h", "tcgen05.cuh", "serving_common.cuh", "kv_append.cuh", "kv_attention.cuh", "kv_prompt.cuh", "moe_layer.cuh",
+HEADERS = ["host_common.h", "host_regions.h", "tcgen05.cuh", "serving_common.cuh", "kv_append.cuh", "kv_attention.cuh", "kv_prompt.cuh", "moe_layer.cuh",
            "packed_linear.cuh", "packed_many.cuh", "qk_norm_rope.cuh", "moe_route.cuh",
            "device_common.cuh", "box_quant.cuh", "dense_quant.cuh", "grouped_quant.cuh", "interleave.cuh",
            "tensor_scale.cuh", "block_scaled_dot.cuh", "cluster.cuh", "gemm_quant.cuh", "grouped_token.cuh"]

@@ -3,6 +3,7 @@
 #include <cmath>
 
 #include "host_common.h"
+#include "host_regions.h"
 #include "qk_norm_rope.cuh"
 
 namespace {
@@ -48,16 +49,26 @@ extern "C" int32_t bsq_qk_norm_rope(int32_t dtype, const void* q, int64_t q_tok,
       (q_tok | q_head | k_tok | k_head | qo_tok | qo_head | ko_tok | ko_head) % 8 != 0 ||
       !aligned(q_weight, weight_dtype == BSQ_F32 ? 4 : 2) || !aligned(k_weight, weight_dtype == BSQ_F32 ? 4 : 2))
     return BSQ_ERR_ALIGN;
-  // outputs whose rows lie in one another, and inputs overwritten in another order than they are read in
   if ((heads > 1 && qo_head < dim) || (kv_heads > 1 && ko_head < dim) || (tokens > 1 && ((heads && qo_tok < dim) || (kv_heads && ko_tok < dim))))
     return BSQ_ERR_SHAPE;
-  const auto moved = [&](int64_t tok, int64_t head, int64_t to_tok, int64_t to_head, int n) {
-    return (tokens > 1 && tok != to_tok) || (n > 1 && head != to_head);
+  // [input, output][queries, keys]
+  const auto rows_of = [&](const void* at, int64_t tok, int64_t head, int n) {
+    return HostRegion{n ? at : nullptr, dim * int64_t(2), {tokens, n}, {tok * 2, head * 2}};
   };
-  if ((heads && q_out == q && moved(q_tok, q_head, qo_tok, qo_head, heads)) ||
-      (kv_heads && k_out == k && moved(k_tok, k_head, ko_tok, ko_head, kv_heads)) ||
-      (heads && kv_heads && (q_out == k || k_out == q || q_out == k_out)))
-    return BSQ_ERR_VALUE;
+  const HostRegion io[2][2] = {{rows_of(q, q_tok, q_head, heads), rows_of(k, k_tok, k_head, kv_heads)},
+                               {rows_of(q_out, qo_tok, qo_head, heads), rows_of(k_out, ko_tok, ko_head, kv_heads)}};
+  const int64_t weight_bytes = dim * int64_t(weight_dtype == BSQ_F32 ? 4 : 2);
+  const HostRegion also[4] = {host_region(positions, tokens * 4), host_region(inv_freq, pairs * int64_t(4)), host_region(q_weight, weight_bytes),
+                              host_region(k_weight, weight_bytes)};
+  for (int i = 0; i < 2; ++i) {
+    const HostRegion &in = io[0][i], &out = io[1][i];
+    const bool itself = in.at == out.at && (tokens == 1 || in.step[0] == out.step[0]) && (in.n[1] == 1 || in.step[1] == out.step[1]);
+    if ((!itself && regions_overlap(out, in)) || regions_overlap(out, io[0][1 - i])) return BSQ_ERR_VALUE;
+    for (const HostRegion& r : also)
+      if (regions_overlap(out, r)) return BSQ_ERR_VALUE;
+  }
+  if (regions_overlap(io[1][0], io[1][1])) return BSQ_ERR_VALUE;
+  if (region_overlaps_itself(io[1][0]) || region_overlaps_itself(io[1][1])) return BSQ_ERR_SHAPE;
   HostDevice d;
   if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
   RopeArgs a{};

@@ -618,9 +618,10 @@ BSQ_API int32_t bsq_packed_linear(int32_t fmt, int32_t dtype, const void* x_dev,
  *   inv_freq_dev      float[pairs].
  *   q_weight_dev, k_weight_dev   NULL (no norm), or dim values of weight_dtype: dtype or BSQ_F32.
  *   eps               >= 0.
- *   q_out_dev, k_out_dev   outputs, strided like the inputs, but with strides of at least dim; each may be its input itself, with
- *                     its strides.  No output overlaps anything else (one that is another input, the other output or its input with other
- *                     strides is refused with BSQ_ERR_VALUE).
+ *   q_out_dev, k_out_dev   outputs, strided like the inputs, but no row in another (BSQ_ERR_SHAPE); each may be its input itself, with
+ *                     its strides.  An output that otherwise shares bytes with an input or the other output is refused with BSQ_ERR_VALUE.
+ *                     Tensors whose rows lie between one another's, as views of one projection, share none; with different strides they count
+ *                     as sharing.
  * Angles are exact up to their rounding to FP32 as a fraction of a turn, at any position; arithmetic is FP32, rounded once.
  */
 BSQ_API int32_t bsq_qk_norm_rope(int32_t dtype, const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, const void* k_dev,
