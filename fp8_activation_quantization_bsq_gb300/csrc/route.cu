@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "host_common.h"
+#include "host_regions.h"
 #include "moe_route.cuh"
 
 namespace {
@@ -44,6 +45,12 @@ int32_t bsq_moe_route(int32_t dtype, const void* logits, int64_t ld_logits, int6
   if (tokens == 0) return BSQ_OK;
   if (!logits || !ids || !weights) return BSQ_ERR_NULL;
   if (!aligned(logits, dtype == BSQ_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4)) return BSQ_ERR_ALIGN;
+  const int64_t wide = dtype == BSQ_F32 ? 4 : 2, out_bytes = tokens * top_k * 4;
+  const HostRegion in = {logits, experts * wide, {tokens, 1}, {ld_logits * wide, 0}}, of_bias = host_region(bias, experts * int64_t(4)),
+                   out[2] = {host_region(ids, out_bytes), host_region(weights, out_bytes)};
+  if (regions_overlap(out[0], out[1])) return BSQ_ERR_VALUE;
+  for (const HostRegion& o : out)
+    if (regions_overlap(o, in) || regions_overlap(o, of_bias)) return BSQ_ERR_VALUE;
   HostDevice d;
   if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
   RouteArgs a{};

@@ -646,7 +646,7 @@ BSQ_API int32_t bsq_qk_norm_rope(int32_t dtype, const void* q_dev, int64_t q_tok
  * Where p enters a comparison it is held to about 2^-45, so the choice is that of exact arithmetic but for values
  * closer than that.  Logits (and biases) of -inf exclude an expert: p counts as 0 (with a logit of -inf), its value as -inf; experts
  * outside the groups that stay count as -inf too.  Logits or biases of NaN or +inf count as -inf and record BSQ_ERR_VALUE.
- *   ids_dev, weights_dev   int32 and float (tokens, top_k), overlapping nothing else.
+ *   ids_dev, weights_dev   int32 and float (tokens, top_k), sharing bytes with nothing else (BSQ_ERR_VALUE).
  */
 BSQ_API int32_t bsq_moe_route(int32_t dtype, const void* logits_dev, int64_t ld_logits, int64_t tokens, int32_t experts, int32_t top_k,
                               int32_t sigmoid, const float* bias_dev, int32_t groups, int32_t top_groups, int32_t group_top,

@@ -91,3 +91,17 @@ def test_rope_overlaps_by_counting_bytes(bsq):
             assert passed(got) or got == VALUE
         counts[clash] += 1
     assert min(counts.values()) > 300
+
+
+ROUTE = dict(dtype=2, z=P, ld=64, tokens=3, experts=64, top_k=4, sigmoid=0, bias=2 * P, groups=8, top_groups=2, group_top=2, renorm=1, scale=1.0,
+             ids=3 * P, weights=4 * P, stream=None)
+
+
+@pytest.mark.parametrize("change,refused", [
+    (dict(), False), (dict(ids=P), True), (dict(weights=P + 3 * 256 - 4), True), (dict(weights=P + 3 * 256), False), (dict(ids=P - 48), False),
+    (dict(ids=P - 44), True), (dict(ids=2 * P + 252), True), (dict(ids=2 * P + 256), False), (dict(weights=3 * P), True), (dict(weights=3 * P + 44), True),
+    (dict(weights=3 * P + 48), False), (dict(ids=4 * P + 4), True), (dict(bias=None, ids=2 * P), False), (dict(dtype=0, ids=P + 384), False),
+    (dict(dtype=0, ids=P + 380), True), (dict(ld=128, ids=P + 256), False), (dict(ld=128, ids=P + 468), True), (dict(tokens=1, ld=0, ids=P + 256), False)])
+def test_route_overlaps(bsq, change, refused):
+    got = bsq.lib().bsq_moe_route(*{**ROUTE, **change}.values())
+    assert got == VALUE if refused else passed(got)
