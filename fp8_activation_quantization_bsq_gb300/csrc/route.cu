@@ -90,6 +90,11 @@ int32_t bsq_moe_rows(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t 
   if (!row_offsets || !scales_offsets || (pairs && (!ids || !row_indices || !positions))) return BSQ_ERR_NULL;
   if (!aligned(ids, 4) || !aligned(row_offsets, 4) || !aligned(scales_offsets, 4) || !aligned(row_indices, 4) || !aligned(positions, 4))
     return BSQ_ERR_ALIGN;
+  const HostRegion all[5] = {host_region(ids, pairs * 4), host_region(row_offsets, (experts + 1) * int64_t(4)),
+                             host_region(scales_offsets, (experts + 1) * int64_t(4)), host_region(row_indices, pairs * 4), host_region(positions, pairs * 4)};
+  for (int i = 1; i < 5; ++i)
+    for (int j = 0; j < i; ++j)
+      if (regions_overlap(all[i], all[j])) return BSQ_ERR_VALUE;
   HostDevice d;
   if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
   RowsArgs a{};

@@ -662,7 +662,7 @@ BSQ_API int32_t bsq_moe_route(int32_t dtype, const void* logits_dev, int64_t ld_
  *   scales_offsets_dev   uint32[experts + 1]: prefix sums of the experts' row counts, each rounded up to 128.
  *   row_indices_dev   int32[tokens * top_k]: each row's token; 0 behind the last row.
  *   positions_dev     int32 (tokens, top_k): each pair's row, -1 without one.
- * The outputs overlap nothing else.
+ * The outputs share bytes with nothing else (BSQ_ERR_VALUE).
  */
 BSQ_API int32_t bsq_moe_rows(const int32_t* ids_dev, int64_t tokens, int32_t top_k, int32_t experts, uint32_t* row_offsets_dev,
                              uint32_t* scales_offsets_dev, int32_t* row_indices_dev, int32_t* positions_dev, void* stream);

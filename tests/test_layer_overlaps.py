@@ -105,3 +105,16 @@ ROUTE = dict(dtype=2, z=P, ld=64, tokens=3, experts=64, top_k=4, sigmoid=0, bias
 def test_route_overlaps(bsq, change, refused):
     got = bsq.lib().bsq_moe_route(*{**ROUTE, **change}.values())
     assert got == VALUE if refused else passed(got)
+
+
+ROWS = dict(ids=P, tokens=3, top_k=2, experts=5, ro=2 * P, so=3 * P, idx=4 * P, pos=5 * P, stream=None)
+
+
+@pytest.mark.parametrize("change,refused", [
+    (dict(), False), (dict(ro=P), True), (dict(ro=P + 20), True), (dict(ro=P + 24), False), (dict(so=P - 20), True), (dict(so=P - 24), False),
+    (dict(idx=P), True), (dict(pos=P), True), (dict(so=2 * P + 20), True), (dict(so=2 * P + 24), False), (dict(idx=2 * P + 4), True),
+    (dict(pos=3 * P - 4), True), (dict(pos=4 * P + 20), True), (dict(pos=4 * P + 24), False), (dict(tokens=0, ids=2 * P), False),
+    (dict(tokens=0, so=2 * P), True)])
+def test_rows_overlaps(bsq, change, refused):
+    got = bsq.lib().bsq_moe_rows(*{**ROWS, **change}.values())
+    assert got == VALUE if refused else passed(got)
