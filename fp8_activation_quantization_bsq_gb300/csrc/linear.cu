@@ -2,6 +2,7 @@
 #include <algorithm>
 
 #include "host_common.h"
+#include "host_regions.h"
 #include "packed_linear.cuh"
 #include "packed_many.cuh"
 
@@ -205,16 +206,6 @@ bsq_status launch_linear_tokens(PlArgs& a, const HostDevice& d, cudaStream_t st)
   return launch_many<FMT, F16, 1>(a, one, d, st);
 }
 
-// Whether n rows of a_width bytes, a_step apart, and n of b_width, b_step apart, share bytes; of interleaved ones only those with equal steps
-// count as apart.
-bool rows_overlap(const void* a, int64_t a_step, int64_t a_width, const void* b, int64_t b_step, int64_t b_width, int64_t n) {
-  const uint64_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-  if (pa + (n - 1) * a_step + a_width <= pb || pb + (n - 1) * b_step + b_width <= pa) return false;
-  if (n == 1 || a_step != b_step) return true;
-  const int64_t d = (static_cast<int64_t>(pb - pa)) % a_step, behind = d < 0 ? d + a_step : d;  // b's rows behind a's
-  return behind < a_width || a_step - behind < b_width;
-}
-
 }  // namespace
 
 extern "C" int32_t bsq_packed_linear(int32_t fmt, int32_t dtype, const void* x, int64_t tokens, int64_t cols, int64_t ld_x, const void* w,
@@ -231,10 +222,10 @@ extern "C" int32_t bsq_packed_linear(int32_t fmt, int32_t dtype, const void* x, 
   if (!aligned(x, 16) || ld_x % 8 != 0 || !aligned(w, 16) || !aligned(w_scales5d, 16) || !aligned(w_sf, 4) || !aligned(add, elem) ||
       !aligned(out, elem))
     return BSQ_ERR_ALIGN;
-  if (rows_overlap(x, ld_x * 2, cols * 2, out, ld_out * elem, rows * elem, tokens)) return BSQ_ERR_VALUE;
-  if (add && !(add == out && (tokens == 1 || ld_add == ld_out)) &&
-      rows_overlap(add, ld_add * elem, rows * elem, out, ld_out * elem, rows * elem, tokens))
-    return BSQ_ERR_VALUE;
+  const auto rows_of = [&](const void* at, int64_t width, int64_t step) { return HostRegion{at, width, {step ? tokens : 1, 1}, {step, 0}}; };
+  const HostRegion of_out = rows_of(out, rows * elem, ld_out * elem);
+  if (regions_overlap(rows_of(x, cols * 2, ld_x * 2), of_out)) return BSQ_ERR_VALUE;
+  if (!(add == out && (tokens == 1 || ld_add == ld_out)) && regions_overlap(rows_of(add, rows * elem, ld_add * elem), of_out)) return BSQ_ERR_VALUE;
   HostDevice d;
   if (bsq_status s = host_device(&d); s != BSQ_OK) return s;
   PlArgs a{};

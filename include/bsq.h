@@ -591,8 +591,9 @@ BSQ_API int32_t bsq_moe_layer_routed(int32_t fmt, const void* x_dev, int64_t ld_
  *   add_dev           NULL, or values of the output's type: (tokens, rows) with row stride ld_add (>= rows), or, with
  *                     ld_add == 0, one row for every token.  May be out_dev itself (with its row stride).
  *   out_dtype         dtype, or BSQ_F32.
- *   out_dev           (tokens, rows), row stride ld_out (>= rows); shares no bytes with x or, otherwise, add: BSQ_ERR_VALUE (so do
- *                     interleaved rows with different strides).
+ *   out_dev           (tokens, rows), row stride ld_out (>= rows); shares no bytes with x or, otherwise, add: BSQ_ERR_VALUE
+ *                     (interleaved rows with different strides count as sharing).  It may not lie in the weights or their scales
+ *                     either; that is not looked at.
  *   tokens, rows      0 to 2^20 (0 = no-op).
  * Sums are FP32 (of a token's values relative to its largest, for MX weights), rounded once to the output's type.  Products are of exact
  * values, with three exceptions.  BF16 x, at most 16 tokens: values of x below 2^-31 of their token's largest are off by at most 2^-39 of that

@@ -118,3 +118,18 @@ ROWS = dict(ids=P, tokens=3, top_k=2, experts=5, ro=2 * P, so=3 * P, idx=4 * P, 
 def test_rows_overlaps(bsq, change, refused):
     got = bsq.lib().bsq_moe_rows(*{**ROWS, **change}.values())
     assert got == VALUE if refused else passed(got)
+
+
+LINEAR = dict(fmt=0, dtype=0, x=P, tokens=3, cols=64, ld_x=64, w=2 * P, ws=3 * P, rows=100, sf=4 * P, add=None, ld_add=0, out_dtype=0, out=8 * P,
+              ld_out=256, stream=None)
+
+
+@pytest.mark.parametrize("change,refused", [
+    (dict(add=8 * P + 512 - 200), False),                       # a bias between the rows of an output
+    (dict(add=8 * P + 200), False), (dict(add=8 * P + 512 - 198), True), (dict(add=8 * P + 198), True), (dict(add=8 * P + 512), True),
+    (dict(add=8 * P + 1024 + 200), False), (dict(add=8 * P + 200, ld_add=256), False), (dict(add=8 * P + 198, ld_add=256), True),
+    (dict(add=8 * P + 200, ld_add=200), True), (dict(add=8 * P, ld_add=256), False), (dict(tokens=1, add=8 * P + 200, ld_add=7), False),
+    (dict(x=8 * P + 208, ld_x=256), False), (dict(x=8 * P + 192, ld_x=256), True)])
+def test_linear_overlaps(bsq, change, refused):
+    got = bsq.lib().bsq_packed_linear(*{**LINEAR, **change}.values())
+    assert got == VALUE if refused else passed(got)
