@@ -1,7 +1,10 @@
 """Compile libbsq (the CUDA kernels + C ABI) in-tree for sm_103a with nvcc, and
-the compiled part of its Python binding with the host compiler."""
+the compiled part of its Python binding with the host compiler.  The library
+needs nothing but the CUDA toolkit (``python fp8_activation_quantization_bsq_gb300/_build.py``);
+the binding is built where torch is installed."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -36,19 +39,24 @@ def _inputs():
             + [os.path.join(INCLUDE, "bsq.h"), os.path.abspath(__file__)])
 
 
+def _torch_dir():
+    """Where torch is installed (not imported for that), or None."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
+    outputs = [LIB_PATH] + ([BINDING_PATH] if _torch_dir() else [])
+    if not all(os.path.exists(p) for p in outputs):
         return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
+    t = min(os.path.getmtime(p) for p in outputs)
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
-def _binding_commands():
-    """Compile and link commands of the binding: torch's headers and libraries, libbsq beside it."""
+def _binding_commands(base: str):
+    """Compile and link commands of the binding: headers and libraries of the torch in `base`, libbsq beside it."""
     import sysconfig
 
-    import torch
-    base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     obj = os.path.join(LIB_DIR, BINDING + ".o")
     cxx = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-isystem", os.path.join(base, "include"), "-isystem",
@@ -60,7 +68,7 @@ def _binding_commands():
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build ``_lib/libbsq.so`` and the binding beside it (skipped when up to date); returns the library's path."""
+    """Build ``_lib/libbsq.so`` and, with torch, the binding beside it (skipped when up to date); returns the library's path."""
     if not force and not is_stale():
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
@@ -70,8 +78,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             "-I", INCLUDE]
     # one compiler process per translation unit, all at once, then the link
     objects = [os.path.join(LIB_DIR, s + ".o") for s in SOURCES]
-    binding, binding_link = _binding_commands()
-    jobs = [base + ["-c", "-o", o, os.path.join(CSRC, s)] for s, o in zip(SOURCES, objects)] + [binding]
+    jobs = [base + ["-c", "-o", o, os.path.join(CSRC, s)] for s, o in zip(SOURCES, objects)]
+    torch_dir = _torch_dir()
+    if torch_dir:
+        binding, binding_link = _binding_commands(torch_dir)
+        jobs.append(binding)
     running = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in jobs]
     results = [(c, p.communicate()[0], p.returncode) for c, p in zip(jobs, running)]
     def then(command):
@@ -82,7 +93,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         then(base + ["-shared", "-Xlinker", "-rpath,/usr/local/cuda/lib64", "-Xlinker", "-soname,libbsq.so", "-o", tmp] + objects)
     if all(rc == 0 for _, _, rc in results):
         os.replace(tmp, LIB_PATH)
-        then(binding_link)
+        if torch_dir:
+            then(binding_link)
     for cmd, text, rc in results:
         if verbose or rc != 0:
             print(" ".join(cmd))
@@ -90,7 +102,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     failed = [text for _, text, rc in results if rc != 0]
     if failed:
         raise RuntimeError("libbsq build failed:\n" + "\n".join(failed)[-4000:])
-    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+    if torch_dir:
+        os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
     return LIB_PATH
 
 
