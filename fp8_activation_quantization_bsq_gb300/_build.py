@@ -6,8 +6,10 @@ from __future__ import annotations
 
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
@@ -15,7 +17,6 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_DIR = os.path.join(PKG_DIR, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libbsq.so")
-BINDING_PATH = os.path.join(LIB_DIR, "_bsq_binding.so")
 
 SOURCES = ["bsq.cu", "kv_cache.cu", "moe.cu", "linear.cu", "rope.cu", "route.cu"]
 HEADERS = ["host_common.h", "host_regions.h", "tcgen05.cuh", "serving_common.cuh", "kv_append.cuh", "kv_attention.cuh", "kv_prompt.cuh", "moe_layer.cuh",
@@ -31,7 +32,24 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build libbsq")
 
 
+def _torch_dir():
+    """Where torch is installed (not imported for that), or None."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _binding_path():
+    """The binding's file, named by the torch and the Python that it is compiled against, whose classes it holds by layout; None without torch."""
+    base = _torch_dir()
+    if base is None:
+        return None
+    with open(os.path.join(base, "version.py")) as f:
+        version = re.search(r"^__version__ = ['\"]([^'\"]+)", f.read(), re.M).group(1)
+    return os.path.join(LIB_DIR, f"_bsq_binding-{version}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 BINDING = "binding.cpp"
+BINDING_PATH = _binding_path()
 
 
 def _inputs():
@@ -39,24 +57,17 @@ def _inputs():
             + [os.path.join(INCLUDE, "bsq.h"), os.path.abspath(__file__)])
 
 
-def _torch_dir():
-    """Where torch is installed (not imported for that), or None."""
-    spec = importlib.util.find_spec("torch")
-    return os.path.dirname(spec.origin) if spec and spec.origin else None
-
-
 def is_stale() -> bool:
-    outputs = [LIB_PATH] + ([BINDING_PATH] if _torch_dir() else [])
+    outputs = [LIB_PATH] + ([BINDING_PATH] if BINDING_PATH else [])
     if not all(os.path.exists(p) for p in outputs):
         return True
     t = min(os.path.getmtime(p) for p in outputs)
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
-def _binding_commands(base: str):
-    """Compile and link commands of the binding: headers and libraries of the torch in `base`, libbsq beside it."""
-    import sysconfig
-
+def _binding_commands():
+    """Compile and link commands of the binding: torch's headers and libraries, libbsq beside it."""
+    base = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     obj = os.path.join(LIB_DIR, BINDING + ".o")
     cxx = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-isystem", os.path.join(base, "include"), "-isystem",
@@ -79,9 +90,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     # one compiler process per translation unit, all at once, then the link
     objects = [os.path.join(LIB_DIR, s + ".o") for s in SOURCES]
     jobs = [base + ["-c", "-o", o, os.path.join(CSRC, s)] for s, o in zip(SOURCES, objects)]
-    torch_dir = _torch_dir()
-    if torch_dir:
-        binding, binding_link = _binding_commands(torch_dir)
+    if BINDING_PATH:
+        binding, binding_link = _binding_commands()
         jobs.append(binding)
     running = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in jobs]
     results = [(c, p.communicate()[0], p.returncode) for c, p in zip(jobs, running)]
@@ -93,7 +103,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         then(base + ["-shared", "-Xlinker", "-rpath,/usr/local/cuda/lib64", "-Xlinker", "-soname,libbsq.so", "-o", tmp] + objects)
     if all(rc == 0 for _, _, rc in results):
         os.replace(tmp, LIB_PATH)
-        if torch_dir:
+        if BINDING_PATH:
             then(binding_link)
     for cmd, text, rc in results:
         if verbose or rc != 0:
@@ -102,7 +112,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     failed = [text for _, text, rc in results if rc != 0]
     if failed:
         raise RuntimeError("libbsq build failed:\n" + "\n".join(failed)[-4000:])
-    if torch_dir:
+    if BINDING_PATH:
         os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
     return LIB_PATH
 
