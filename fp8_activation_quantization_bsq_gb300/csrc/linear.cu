@@ -27,9 +27,9 @@ struct PlPlan {
   int sets, per_rank, segment, ranks, smem;
 };
 PlPlan plan_linear(const PlArgs& a, int cols_of_piece, int token_tile) {
-  const int toks = std::min(a.tokens, token_tile);
+  const int toks = a.tokens;  // at most token_tile
   constexpr int kBlockMost = 227 * 1024, kOverhead = 2 * 1024;  // static shared memory and what the system takes, per block
-  const int bands = static_cast<int>(ceil_div(a.rows, 128)) * static_cast<int>(ceil_div(a.tokens, token_tile));
+  const int bands = static_cast<int>(ceil_div(a.rows, 128));
   const int token_bytes = cols_of_piece * 2;  // of a piece
   PlPlan best{};
   double least = 0;
@@ -67,7 +67,7 @@ bsq_status launch_linear(PlArgs& a, const PlPlan& plan, const HostDevice& d, cud
   const int ranks = plan.ranks, smem = plan.smem;
   if (bsq_status s = allow_smem(reinterpret_cast<const void*>(kernel), 227 * 1024 - 2048, d.index); s != BSQ_OK) return s;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ranks, static_cast<unsigned>(row_tiles), static_cast<unsigned>(ceil_div(a.tokens, NT * 8)));
+  cfg.gridDim = dim3(ranks, static_cast<unsigned>(row_tiles));
   cfg.blockDim = dim3(kPlThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

@@ -96,7 +96,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 2^k that takes a largest magnitude (FP32 bits) to below 2^15; k from -113 to 127.
+// 2^k that takes a largest magnitude (FP32 bits) to below 2^15; k from -113 to 127, or -114 for an infinity.
 __device__ __forceinline__ int pl_exponent(uint32_t amax) {
   const int e = static_cast<int>(amax >> 23) - 127;  // of an FP32 number, -127 below the normal ones
   return min(127, 14 - max(e, -127));
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kPlThreads, NT == 1 ? 3 : 2) packed_linear_ker
   const int part = warp % kSplit;                  // of K
   const int64_t tile = static_cast<int64_t>(blockIdx.y) * RT + warp / kSplit;  // 32 rows
   const int64_t row0 = (tile >> 2) * 128 + (tile & 3) * 8;
-  const int tok0 = blockIdx.z * kTile, toks = min(kTile, a.tokens - tok0);
+  const int toks = a.tokens;  // at most kTile
   const int p_lo = rank * a.per_rank, p_hi = min(p_lo + a.per_rank, a.pieces);
   const int x_stride = a.segment * kCols * 2 + 64;  // bytes of a token: 64 past a multiple of 128, for the banks
 
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kPlThreads, NT == 1 ? 3 : 2) packed_linear_ker
   const auto copy_tokens = [&](int seg) {
     const int col0 = seg * kCols, live = min(min(seg + a.segment, p_hi) * kCols, a.cols) - col0;
     const uint32_t dst = smem_addr(xs);
-    const uint16_t* src = a.x + tok0 * a.ld_x + col0;
+    const uint16_t* src = a.x + col0;
     each_item([&](int tok, int c) { cp_async16(dst + tok * x_stride + c * 2, src + (c < live ? tok * a.ld_x + c : 0), c < live); });
     cp_async_commit();
   };
@@ -412,11 +412,10 @@ __global__ void __launch_bounds__(kPlThreads, NT == 1 ? 3 : 2) packed_linear_ker
     const int64_t row = (static_cast<int64_t>(blockIdx.y) * RT + (e >> 5) / kTile) / 4 * 128 +
                         ((static_cast<int64_t>(blockIdx.y) * RT + (e >> 5) / kTile) & 3) * 8 + 32 * ((e >> 3) & 3) + (e & 7);
     if (t_in >= toks || row >= a.rows) continue;
-    const int tok = tok0 + t_in;
-    const int64_t at = tok * a.ld_out + row;
+    const int64_t at = t_in * a.ld_out + row;
     float extra = 0.f;
-    if (a.add) extra = a.out_f32 ? static_cast<const float*>(a.add)[tok * a.ld_add + row]
-                                 : elem2_to_f32x2<F16>(static_cast<const uint16_t*>(a.add)[tok * a.ld_add + row]).x;
+    if (a.add) extra = a.out_f32 ? static_cast<const float*>(a.add)[t_in * a.ld_add + row]
+                                 : elem2_to_f32x2<F16>(static_cast<const uint16_t*>(a.add)[t_in * a.ld_add + row]).x;
     float s = 0.f;
     if (ranks > 1) {
       float v[8];
