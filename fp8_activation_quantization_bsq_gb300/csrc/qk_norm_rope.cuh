@@ -33,7 +33,6 @@ struct RopeArgs {
   int dim, pairs;
   int weight_f32;
   float eps, inv_dim;
-  uint32_t least, span;  // sums of squares that are not among the span + 1 numbers from this one on are taken again (0: eps is far above small ones)
   int chunks, per_chunk;  // tasks per token, rows per task
 };
 
@@ -165,30 +164,28 @@ __global__ void __launch_bounds__(kRopeWarps * 32, MODE == 2 ? 5 : 8) qk_norm_ro
       slot = slot == kRopeDepth - 1 ? 0 : slot + 1;
       float2 x[4] = {elem2_to_f32x2<F16>(va.x), elem2_to_f32x2<F16>(va.y), elem2_to_f32x2<F16>(vb.x), elem2_to_f32x2<F16>(vb.y)};
       if (norm) {
-        const auto squares = [&](const float2 (&v)[4]) {
-          float2 q = mul_f32x2(v[0], v[0]);
+        const auto squares = [&]() {
+          float2 q = mul_f32x2(x[0], x[0]);
 #pragma unroll
-          for (int j = 1; j < 4; ++j) q = fma_f32x2(v[j], v[j], q);
+          for (int j = 1; j < 4; ++j) q = fma_f32x2(x[j], x[j], q);
           float sum = q.x + q.y;
 #pragma unroll
           for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
           return sum;
         };
-        const float sum = squares(x);
-        float f = rsqrtf(sum * a.inv_dim + a.eps);
-        // Squares that near FP32's ends (BF16 rows beyond 2^50 / sqrt(dim), or, beside an eps as small, below 2^-45): once more of the row times
-        // 2^-96 or 2^96.  The elements take the power of two where it does not cost them bits: small ones before the factor, large ones after it.
-        if (!F16 && __any_sync(~0u, __float_as_uint(sum) - a.least > a.span)) {
-          const float by = sum > 0x1p100f ? 0x1p-96f : sum < __uint_as_float(a.least) ? 0x1p96f : 1.f;
-          const float before = fmaxf(by, 1.f), after = fminf(by, 1.f);
-          float2 v[4];
+        float sum = squares(), eps = a.eps;
+        // Squares that near FP32's ends (BF16 rows only): once more, of 2^-72 or 2^96 times the row, where sums below 2^-90 (FP32 may have lost some)
+        // matter beside an eps as small, above 2^124, and above 2^100 beside an eps that with their mean passes FP32.  That is exact: what 2^-72
+        // takes below FP32's subnormal numbers lies below BF16's once it is divided by its row's root.  (Limits from the arguments in place of these
+        // constants cost 3 % of a prompt's time.)
+        if (!F16 && __any_sync(~0u, sum > 0x1p100f || sum < 0x1p-90f)) {
+          const float by = sum > (eps > 0x1p126f ? 0x1p100f : 0x1p124f) ? 0x1p-72f : sum < 0x1p-90f && eps < 0x1p-70f ? 0x1p96f : 1.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = mul_f32x2(x[j], make_float2(by, by));
-          f = rsqrtf(squares(v) * a.inv_dim + a.eps * by * by);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = mul_f32x2(mul_f32x2(mul_f32x2(x[j], make_float2(before, before)), make_float2(f, f)), make_float2(after, after));
-          f = 1.f;
+          for (int j = 0; j < 4; ++j) x[j] = mul_f32x2(x[j], make_float2(by, by));
+          sum = squares();
+          eps = eps * by * by;
         }
+        const float f = rsqrtf(sum * a.inv_dim + eps);
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = mul_f32x2(mul_f32x2(x[j], make_float2(f, f)), w[j]);  // f w alone may pass FP32
       }

@@ -96,8 +96,6 @@ extern "C" int32_t bsq_qk_norm_rope(int32_t dtype, const void* q, int64_t q_tok,
   a.weight_f32 = weight_dtype == BSQ_F32;
   a.eps = eps;
   a.inv_dim = 1.f / static_cast<float>(dim);
-  a.least = eps < 0x1p-70f ? (127u - 90u) << 23 : 0u;  // 2^-90
-  a.span = ((127u + 100u) << 23) - a.least;            // to 2^100
   // a warp takes a token's rows, or, where there are too few tokens for 16 warps per SM, an equal share of them (512 tokens of 72 heads then 6.7 us,
   // with 4 warps per SM 8.1, with 64 9.3; 257 tokens of 32 heads 3.6, with 32 or 64 4.7: each warp works out the token's angles)
   const int at_once = dim <= 64 ? 4 : dim <= 128 ? 2 : 1;
