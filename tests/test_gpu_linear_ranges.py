@@ -65,3 +65,21 @@ def test_rows_of_small_and_ordinary_scales(bsq, fmt, tokens, rows, cols):
     tol = tol + np.abs(xn).sum(1)[:, None] * largest[None] * 2.0 ** (-35 if fmt == "mxfp4" else -23) + 8 * 2.0 ** -149
     err = np.abs(y - expect)
     assert (err <= tol).all(), f"{(err / tol).max():.3f} of the tolerance"
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4", "mxfp8"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("tokens,rows", [(1, 1), (16, 129), (17, 1), (17, 128), (33, 129), (300, 2), (257, 257)])
+def test_one_block_of_columns(bsq, fmt, dtype, tokens, rows):
+    """32 columns, less than any kernel's step: whole numbers, so the sums are exact."""
+    rng = np.random.default_rng(tokens + rows)
+    packed = rng.choice(np.array([0x00, 0x30, 0x38, 0x40, 0xB8, 0xC4], np.uint8), (rows, 32)) if fmt == "mxfp8" else rng.integers(0, 256, (rows, 16), dtype=np.uint8)
+    scales = np.zeros(-(-rows // 128) * 512, np.uint8)  # what lies past the last row and column
+    r = np.arange(rows)
+    for c in range(2 if fmt == "nvfp4" else 1):
+        scales[r // 128 * 512 + (r % 32) * 16 + (r % 128) // 32 * 4 + c] = rng.choice([0x38, 0x40] if fmt == "nvfp4" else [127, 128], rows)
+    x = torch.from_numpy(rng.integers(-4, 5, (tokens, 32))).to(DT[dtype]).cuda()
+    sf = torch.tensor([0.5], device="cuda") if fmt == "nvfp4" else None
+    w = ref.weights(fmt, packed, scales, rows, 32, 0.5 if fmt == "nvfp4" else 1.0)
+    y = bsq.packed_linear(x, torch.from_numpy(packed).cuda(), torch.from_numpy(scales).cuda(), fmt, w_sf=sf, out_dtype=torch.float32)
+    np.testing.assert_array_equal(y.double().cpu().numpy(), x.double().cpu().numpy() @ w.T)

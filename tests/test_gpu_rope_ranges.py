@@ -51,3 +51,9 @@ def test_every_size_of_rows_with_every_eps(bsq, dtype, eps):  # noqa: F811
     q[:, 2, 1:] = 0  # one element alone
     got = bsq.qk_norm_rope(q, k, pos, freq, qw, kw, eps=eps)
     check(q, k, pos, freq, qw, kw, got, dtype, False, float(np.float32(eps)))
+
+
+@pytest.mark.parametrize("tokens,heads,kv_heads,dim", [(1, 4096, 4096, 8), (2, 300, 37, 64), (3, 1, 500, 128), (1, 2, 1, 256)])
+def test_many_heads(bsq, tokens, heads, kv_heads, dim):  # noqa: F811
+    q, k, pos, freq, qw, kw = make(tokens, heads, kv_heads, dim, dim // 2, "f16", seed=10)
+    check(q, k, pos, freq, qw, kw, bsq.qk_norm_rope(q, k, pos, freq, qw, kw), "f16", False)
