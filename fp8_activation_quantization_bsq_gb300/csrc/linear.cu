@@ -14,6 +14,8 @@ using namespace bsq;
 // lie within a GPU processing cluster, whose SMs they may not divide).
 constexpr int kResident[9] = {0, 152, 152, 138, 144, 140, 138, 105, 120}, kResidentTwo[9] = {0, 304, 304, 291, 296, 290, 276, 266, 288};
 
+// The figures of both sides beside the rules here are of three sets of inputs in turn, part of which stays in L2 with the smaller sizes.
+//
 // How the kernel for few tokens is laid out: sets of 32 rows per block (1 or 4), pieces of K per block and of its tokens at a time.
 //
 // The cost is fitted to 1, 2, 4, 8 and 16 tokens with 1 and 4 sets and 1 to 8 blocks along K (10240 x 7168, 7168 x 8192, 4096 x 4096
@@ -186,7 +188,8 @@ bsq_status launch_many(const PlArgs& p, const PmPlan& plan, const HostDevice& d,
 template <int FMT, bool F16>
 bsq_status launch_linear_tokens(PlArgs& a, const HostDevice& d, cudaStream_t st) {
   // The weights' stream up to 16 tokens, tensor memory beyond.  10240 x 7168 NVFP4: 16 tokens 23.4 us against 22.5, 24 tokens 38.8 against
-  // 22.8; 16384 x 7168: 16 tokens 28.5, 17 tokens with the other kernel 30.3; 1024 x 2048 5.1 and 6.4; 256 x 7168 6.2 and 8.6.
+  // 22.8; 16384 x 7168: 16 tokens 28.5, 17 tokens with the other kernel 30.3; 1024 x 2048 5.1 and 6.4; 256 x 7168 6.2 and 8.6; 7168 x 8192, from
+  // DRAM, 16.7 and 19.3.
   if (a.tokens <= 8) {
     const PlPlan p = plan_linear(a, PlFmt<FMT>::kCols, 8);
     return p.sets == 1 ? launch_linear<FMT, F16, 1, 1>(a, p, d, st) : launch_linear<FMT, F16, 1, 4>(a, p, d, st);
@@ -197,7 +200,9 @@ bsq_status launch_linear_tokens(PlArgs& a, const HostDevice& d, cudaStream_t st)
   }
   // one or two tiles of rows per block.  Two halve the blocks, and so the sums that blocks along K exchange, and share the tokens' columns:
   // 64 tokens, 7168 x 8192 20.0 us against 22.4, 24 tokens 17.3 and 21.0; with too few rows to fill the GPU one is better: 64 tokens,
-  // 1024 x 8192 10.2 us against 13.9.  Beyond 128 tokens one tile takes twice as many of them: 192 tokens 26.8 and 36.5.
+  // 1024 x 8192 10.2 us against 13.9.  Beyond 128 tokens one tile takes twice as many of them: 192 tokens 26.8 and 36.5.  The cost's constants are
+  // of NVFP4; with MX weights (20, 32, 64 and 128 tokens of seven sizes) it names the slower one for 128 tokens of 7168 x 8192, by 5 and 6 %
+  // (MXFP4 22.7 and 21.6 us, MXFP8 26.2 and 24.7), for 64 of 16384 x 7168 MXFP8 by 2 %, and the faster one elsewhere.
   const PmPlan one = plan_many(a, 1, d.sm_count);
   if (a.tokens <= 128) {
     const PmPlan two = plan_many(a, 2, d.sm_count);

@@ -310,9 +310,11 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, const void* row, Rou
   return route_select<NL>(key, a.top_k, lane, margin, least);
 }
 
-// Measured, 8 of 256 experts: 64 tokens by softmax 2.5 us, one token by sigmoid with bias and groups 4.0 us; 4096 tokens of those 9.6 us, of
-// plain softmax 5.3.  Bound by instructions, about 1350 a token: the nine rounds of the choice (2.7 us of 10.9 before the kept groups' experts
-// were put side by side, which takes 10.4 to 9.6), the groups (1.8), tokens that are chosen again (0.9), a launch (2); DRAM's part is 0.7 us.
+// Measured, 8 of 256 experts: 64 tokens by softmax 2.6 us, one token by sigmoid with bias and groups 3.9 us; 4096 tokens of those 9.6 us (10.9 with
+// logits from DRAM), of plain softmax 5.3 (6.5); 16384 tokens 28.1.  4096 tokens are bound by a warp's own chain, since all of their warps are on the GPU at
+// once: issuing their instructions (about 1350 a token) alone would take 4.4 us, and the counters show fixed latency and 35 % of the SMs' throughput; 16384
+// tokens are nearer the issue rate (18 us).  The chain: the nine rounds of the choice (2.7 us of 10.9 before the kept groups' experts were put side by
+// side, which takes 10.4 to 9.6), the groups (1.8), tokens that are chosen again (0.9), a launch (2); DRAM's part is 0.7 us.
 // All values in two numbers from the start, in place of FP32 first: 18.8 us, one token 7.9.  Slots for 128 and 512 experts: 9.2 -> 7.2 and 26.6 -> 18.1.
 //
 // NL: logits per lane (expert 32 i + lane in slot i).  PAIR: p enters the comparison (a bias, or sums of two in groups).
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
 // is the pairs' own.  Bound by latency: a few dependent passes.  Measured, 8 of 256 experts (graph replay, with the
 // routing in front, which then took 11 us for 4096 tokens): 4096 tokens 17.9 us in a cluster of 16 blocks, 20.3 with 8, 25.5 with 4, 70 with one;
 // 512 tokens 11.2, with one block 14.7.  Runs of up to 8 rounds keep experts and places in registers: 17.9 against 18.9, 128 tokens 8.3 and 9.0.
-// Now 16.0 us with the routing's 9.6.  Of 12 thousand cycles reading the ids takes 0.8, two rounds of places 2, the sums over warps 1, the cluster's
+// Now 16.0 us with the routing's 9.6 (17.4 from DRAM; 131072 pairs 14 us).  Of 12 thousand cycles reading the ids takes 0.8, two rounds of places 2, the sums over warps 1, the cluster's
 // 2.6, the scan 1.2, and the scattered stores 2.6.
 constexpr int kRowsThreads = 1024, kRowsWarps = kRowsThreads / 32, kRowsMaxBlocks = 16, kRowsHeld = 8;
 

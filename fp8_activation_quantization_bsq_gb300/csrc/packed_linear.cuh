@@ -17,11 +17,14 @@
 // columns, which lie in shared memory as FP16) and share out K otherwise.  Blocks of a cluster share K too; the warps' sums
 // are added in shared memory, the blocks' through the cluster's, in a fixed order.
 //
-// Measured (graph replay, inputs larger than L2, of 6787 GB/s measured): one token of BF16, 10240 x 7168 NVFP4 11.8 us (3.5 TB/s), MXFP8 16.4
-// (4.6), 16000 x 8192 NVFP4 16.5 (4.5); 5 tokens, 1000 x 2912 MXFP4 3.3 us; 16 tokens, 256 x 7168 MXFP8 6.0.  About 5 us of a call are
-// its start, the tokens' way into shared memory and the sums; without its products the first takes 10.95 us, so the stream bounds the rest:
-// SMs get equal shares of DRAM's rate, and those with a block more end later.  A ring of 4 or 5 pieces takes the room of a third
-// block or of the next call's first ones: 9728 x 7168 12.3 and 12.7 us against 8.8.  A copy into L2 ahead of the launch's wait: 14.4 against 13.3.
+// Measured (graph replay, inputs rotated through twice L2, of 6787 GB/s measured): one token of BF16, 10240 x 7168 NVFP4 11.9 us (3.5 TB/s), MXFP8
+// 17.4 (4.4), 16000 x 8192 NVFP4 16.6 to 17.9 (4.1 to 4.5); 5 tokens, 1000 x 2912 MXFP4 3.9 us (3.3 from L2); 16 tokens, 256 x 7168 MXFP8 6.2.
+// About 5 us of a call are its start, the tokens' way into shared memory and the sums.  The rest is not DRAM's rate but how the blocks divide over
+// the SMs: each SM gets an equal share of that rate, and those with a block more end later (9728 x 7168, two blocks for each SM, takes 9.4 to 9.6 us,
+// 5 % more rows 11.9; without its products that takes 10.95).  Every block copies, scans and converts its tokens' columns for at most 128 rows, so
+// tokens cost as much as weights from about 16 on: 2, 4, 8, 12 and 16 tokens, 10240 x 7168, 12.5, 13.3, 15.4, 21.9 and 24.3 us.  A ring of 4 or 5
+// pieces takes the room of a third block or of the next call's first ones: 9728 x 7168 12.3 and 12.7 us against 8.8.  A copy into L2 ahead of the
+// launch's wait: 14.4 against 13.3.
 #pragma once
 
 #include "cluster.cuh"

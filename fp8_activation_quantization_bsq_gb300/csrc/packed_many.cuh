@@ -16,7 +16,10 @@
 // records BSQ_ERR_TIMEOUT, stops the block's roles, waits for the copies and products in flight, frees the tensor memory and returns.
 //
 // Measured (graph replay, BF16 tokens, NVFP4): 2048 tokens, 10240 x 7168 168 to 171 us (1.76 to 1.79 PFLOP/s; 1.91 measured of the library's plain
-// BF16 product), tensor pipe 81 % active; 64 tokens, 7168 x 8192 19.5 us, of which products start after 2.7 us, 26 steps take 10, and the sums 4.
+// BF16 product), tensor pipe 81 % active; 64 tokens, 7168 x 8192 21.3 us with inputs rotated through twice L2, and 19.5 through three sets, part of which
+// stays there; of the latter, as the figures below, products start after 2.7 us, 26 steps take 10, and the sums 4.  From 129 to about 1000 tokens whole
+// tiles in whole waves leave SMs idle: 300 tokens of 10240 x 7168 (240 tiles of 112 tokens on 152 SMs) take 56 us where their operations need 23, 512
+// tokens 60 (39), 1000 tokens 93 (77).
 // A product of 128 x N x 16 takes 64 cycles up to N = 128 and 133 at 256, for its 128-row operand's sake.  With FP16 tokens the 64 take
 // 16.9 us, with codes that are not converted 15.7.  The cluster's sums go at about 10 bytes a clock and SM, read (20.6 us) or written (19.6), one or
 // four values at a time (21.5).

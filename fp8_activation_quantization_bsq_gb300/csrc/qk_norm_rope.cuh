@@ -3,16 +3,18 @@
 //   (u_a, u_b) -> (u_a cos t - u_b sin t, u_b cos t + u_a sin t),  t = position * inv_freq[i]
 // for the first `pairs` pairs of a row, (i, i + pairs) or (2i, 2i + 1); what lies behind passes.
 //
-// Bound by DRAM: 2 bytes read and 2 written per element.  Measured: 4096 tokens of 64 + 8 heads of 128 26.5 us (5.7 TB/s; of 6.8 copied), 16384
-// tokens 6.2 TB/s; one token of 32 + 8 heads 2.6 us, a launch.  A row's 8 elements per lane are two
+// Bound by DRAM: 2 bytes read and 2 written per element.  Measured: 4096 tokens of 64 + 8 heads of 128 26.5 to 26.8 us (5.6 TB/s; of 6.8 copied), neighbouring
+// pairs 26.1 to 28.1, without norm 25.1, 16384 tokens 6.2 TB/s; one token of 32 + 8 heads 2.6 us, a launch.  Pairs (i, i + n) of a number that no 4
+// divides (MODE 2) take 50 us: their other sides go through shared memory, whose banks and latency bound it (half of
+// the cycles between a warp's instructions are waits for it).  A row's 8 elements per lane are two
 // groups of 4 that hold both sides of a lane's pairs, so that no element crosses lanes in registers and the lane's 4
 // angles serve every head of the token that the warp takes; 8, 16 or 32 lanes per row (dim to 64, 128, 256).  A warp keeps 4 steps of its rows in
 // flight through a ring in shared memory, 16 bytes a lane: with 3, 5, 6 and 8 steps 28.1, 26.8, 27.5 and 28.5 us (heads of 256 51.9, 59.4, 60.4, 61.0, with
 // 4 56.3; 16384 tokens of 128 100.6, 95.8, 95.1, 95.7, with 4 97.1); each lane copying its own two groups of 8 bytes 29.4; two steps in registers 48.7.
 //
 // Angles: t / 2 pi in fixed point.  inv_freq is a 24-bit integer times a power of two, 1 / (2 pi) a 64-bit
-// fraction, and the position multiplies their product modulo 2^64, which drops whole turns exactly: off by
-// at most position * inv_freq * 2^-64 turns before the last 32 bits are cut off, at any position.
+// fraction, and the position multiplies their product, cut off at 2^-64 turns, modulo 2^64, which drops whole turns exactly: off by
+// at most position (1 + |inv_freq|) 2^-64 turns before the last 32 bits are cut off.
 #pragma once
 
 #include "tcgen05.cuh"  // fma_f32x2

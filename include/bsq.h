@@ -595,7 +595,8 @@ BSQ_API int32_t bsq_moe_layer_routed(int32_t fmt, const void* x_dev, int64_t ld_
  *                     (interleaved rows with different strides count as sharing).  It may not lie in the weights or their scales
  *                     either; that is not looked at.
  *   tokens, rows      0 to 2^20 (0 = no-op).
- * Sums are FP32 (of a token's values relative to its largest, for MX weights), rounded once to the output's type.  Products are of exact
+ * Sums are FP32 (for MX weights of a token's values relative to its largest, for NVFP4 before they are divided by the tensor scale), rounded once to the
+ * output's type; values of w that FP32 does not hold may count as infinite.  Products are of exact
  * values, with three exceptions.  BF16 x, at most 16 tokens: values of x below 2^-31 of their token's largest are off by at most 2^-39 of that
  * (x is held in FP16 times a power of two of its token).  BF16 x, more tokens: values of MX weights below 2^-126 are off by at most 2^-134
  * (w is held in BF16).  FP16 x, MX weights, more than 16 tokens: values of w below 2^-36 (E2M1) or 2^-21 (E4M3) of their row's largest
@@ -623,7 +624,8 @@ BSQ_API int32_t bsq_packed_linear(int32_t fmt, int32_t dtype, const void* x_dev,
  *                     its strides.  An output that otherwise shares bytes with an input or the other output is refused with BSQ_ERR_VALUE.
  *                     Tensors whose rows lie between one another's, as views of one projection, share none; with different strides they count
  *                     as sharing.
- * Angles are exact up to their rounding to FP32 as a fraction of a turn, at any position; arithmetic is FP32, rounded once.
+ * Angles are off by at most position (1 + |inv_freq|) 2^-64 of a turn (2^-32 at the last position with frequencies up to 1) before they are rounded to
+ * FP32 as a fraction of a turn; arithmetic is FP32, rounded once.
  */
 BSQ_API int32_t bsq_qk_norm_rope(int32_t dtype, const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, const void* k_dev,
                                  int64_t k_token_stride, int64_t k_head_stride, int64_t tokens, int32_t heads, int32_t kv_heads,
